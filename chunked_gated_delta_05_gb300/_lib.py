@@ -10,6 +10,7 @@ from . import build as _build
 GDN_OK, GDN_EINVAL, GDN_EUNSUPPORTED, GDN_ECUDA, GDN_ETIMEOUT, GDN_ERANGE = 0, 1, 2, 3, 4, 5
 
 c_int, c_float, c_size_t, c_void_p = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
+c_ll = ctypes.c_longlong
 
 
 class Desc(ctypes.Structure):
@@ -54,6 +55,75 @@ class ConvBwdArgs(ctypes.Structure):
                 ("dhalo", c_void_p), ("workspace", c_void_p), ("workspace_bytes", c_size_t)]
 
 
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", c_ll), ("width", c_int), ("eps", c_float), ("residual_scale", c_float),
+                ("stream_kind", c_int), ("activation", c_int)]
+
+
+class NormFwdArgs(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("residual", c_void_p), ("weight", c_void_p), ("y", c_void_p), ("stream", c_void_p)]
+
+
+class NormBwdArgs(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("gate", c_void_p), ("weight", c_void_p), ("dy", c_void_p), ("dstream", c_void_p),
+                ("dx", c_void_p), ("dgate", c_void_p), ("dresidual", c_void_p), ("dweight", c_void_p),
+                ("workspace", c_void_p), ("workspace_bytes", c_size_t)]
+
+
+class ConvStepDesc(ctypes.Structure):
+    _fields_ = [("B", c_int), ("C", c_int), ("W", c_int), ("dilation", c_int), ("activation", c_int),
+                ("num_slots", c_int), ("x_stride", c_ll)]
+
+
+class ConvStepArgs(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("weight", c_void_p), ("bias", c_void_p), ("state", c_void_p),
+                ("state_indices", c_void_p), ("y", c_void_p), ("status", c_void_p)]
+
+
+class StepDesc(ctypes.Structure):
+    _fields_ = [("B", c_int), ("H", c_int), ("num_k_heads", c_int), ("num_slots", c_int), ("scale", c_float),
+                ("use_qk_l2norm", c_int), ("use_beta_sigmoid", c_int), ("use_gate_in_kernel", c_int),
+                ("lower_bound", c_float), ("q_stride", c_ll), ("k_stride", c_ll), ("v_stride", c_ll)]
+
+
+class StepArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("g", c_void_p), ("beta", c_void_p),
+                ("state", c_void_p), ("state_indices", c_void_p), ("o", c_void_p), ("A_log", c_void_p),
+                ("dt_bias", c_void_p), ("status", c_void_p)]
+
+
+class SscanDesc(ctypes.Structure):
+    _fields_ = [("B", c_int), ("T", c_int), ("D", c_int), ("N", c_int), ("G", c_int),
+                ("cu_seqlens", ctypes.POINTER(ctypes.c_int32)), ("num_seqs", c_int), ("delta_softplus", c_int),
+                ("u_stride", c_ll), ("delta_stride", c_ll), ("z_stride", c_ll), ("B_stride", c_ll), ("C_stride", c_ll)]
+
+
+class SscanFwdArgs(ctypes.Structure):
+    _fields_ = [("u", c_void_p), ("delta", c_void_p), ("A", c_void_p), ("Bm", c_void_p), ("Cm", c_void_p),
+                ("D", c_void_p), ("delta_bias", c_void_p), ("z", c_void_p), ("initial_state", c_void_p),
+                ("y", c_void_p), ("final_state", c_void_p), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+                ("saved", c_void_p), ("saved_bytes", c_size_t)]
+
+
+class SscanBwdArgs(ctypes.Structure):
+    _fields_ = [("u", c_void_p), ("delta", c_void_p), ("A", c_void_p), ("Bm", c_void_p), ("Cm", c_void_p),
+                ("D", c_void_p), ("delta_bias", c_void_p), ("z", c_void_p), ("initial_state", c_void_p),
+                ("dy", c_void_p), ("dfinal", c_void_p), ("du", c_void_p), ("ddelta", c_void_p), ("dA", c_void_p),
+                ("dB", c_void_p), ("dC", c_void_p), ("dD", c_void_p), ("ddelta_bias", c_void_p), ("dz", c_void_p),
+                ("dh0", c_void_p), ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("saved", c_void_p),
+                ("saved_bytes", c_size_t)]
+
+
+class SscanStepArgs(ctypes.Structure):
+    _fields_ = [("u", c_void_p), ("delta", c_void_p), ("A", c_void_p), ("Bm", c_void_p), ("Cm", c_void_p),
+                ("D", c_void_p), ("delta_bias", c_void_p), ("z", c_void_p), ("state", c_void_p),
+                ("state_indices", c_void_p), ("num_slots", c_int), ("y", c_void_p), ("status", c_void_p)]
+
+
+def _call(desc, args):
+    return ([ctypes.POINTER(desc), ctypes.POINTER(args), c_void_p], c_int)
+
+
 # Every symbol include/gdn.h declares, with its ctypes signature.
 SIGNATURES = {
     "gdn_strerror": ([c_int], ctypes.c_char_p),
@@ -78,6 +148,21 @@ SIGNATURES = {
     "gdn_conv_bwd_workspace_size": ([ctypes.POINTER(ConvDesc)], c_size_t),
     "gdn_conv_fwd": ([ctypes.POINTER(ConvDesc), ctypes.POINTER(ConvFwdArgs), c_void_p], c_int),
     "gdn_conv_bwd": ([ctypes.POINTER(ConvDesc), ctypes.POINTER(ConvBwdArgs), c_void_p], c_int),
+    "gdn_conv_state": _call(ConvDesc, ConvFwdArgs),
+    "gdn_conv_step": _call(ConvStepDesc, ConvStepArgs),
+    "gdn_norm_bwd_workspace_size": ([ctypes.POINTER(NormDesc)], c_size_t),
+    "gdn_add_norm_fwd": _call(NormDesc, NormFwdArgs),
+    "gdn_add_norm_bwd": _call(NormDesc, NormBwdArgs),
+    "gdn_gated_norm_fwd": _call(NormDesc, NormFwdArgs),
+    "gdn_gated_norm_bwd": _call(NormDesc, NormBwdArgs),
+    "gdn_step": _call(StepDesc, StepArgs),
+    "kda_step": _call(StepDesc, StepArgs),
+    "gdn_sscan_fwd_workspace_size": ([ctypes.POINTER(SscanDesc)], c_size_t),
+    "gdn_sscan_bwd_workspace_size": ([ctypes.POINTER(SscanDesc)], c_size_t),
+    "gdn_sscan_saved_size": ([ctypes.POINTER(SscanDesc)], c_size_t),
+    "gdn_sscan_fwd": _call(SscanDesc, SscanFwdArgs),
+    "gdn_sscan_bwd": _call(SscanDesc, SscanBwdArgs),
+    "gdn_sscan_step": _call(SscanDesc, SscanStepArgs),
     "gdn_timing_enable": ([c_int], c_int),
     "gdn_timing_kinds": ([], c_int),
     "gdn_timing_name": ([c_int], ctypes.c_char_p),

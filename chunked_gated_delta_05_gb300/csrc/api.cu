@@ -296,7 +296,9 @@ int check_cuda(cudaError_t e, const char* what) {
 // Optional per-kernel timing (CUDA events recorded on the launching stream around every
 // launch while enabled). Process-global and not thread-safe: a profiling aid.
 const char* const kKindNames[kKinds] = {"tables", "prepare", "chain_fwd", "chain_bwd", "bwd_feat", "bwd_tok",
-                                        "compose", "group_sum", "conv_fwd", "conv_bwd", "gate_grad"};
+                                        "compose", "group_sum", "conv_fwd", "conv_bwd", "gate_grad",
+                                        "norm_fwd", "norm_bwd", "conv_step", "delta_step", "sscan_fwd", "sscan_bwd",
+                                        "sscan_step"};
 struct Timing {
   bool on = false;
   std::vector<std::pair<cudaEvent_t, cudaEvent_t>> ev[kKinds];

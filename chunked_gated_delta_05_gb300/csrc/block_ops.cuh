@@ -1,0 +1,193 @@
+// Parameters and device helpers of the operators around the recurrence: the block norms (k_norm.cu),
+// the single-token steps (k_step.cu) and the selective scan (k_sscan*.cu).
+#pragma once
+#include "common.cuh"
+
+namespace gdn {
+
+// ------------------------------------------------------------------ device arithmetic
+
+__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_approx(1.f + exp2_approx(-kLog2e * x)); }
+
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], with log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
+// by the Taylor series of atanh through s^13 (the next term is below 2e-8 of the sum). Unlike log(1 + e) it keeps
+// its relative precision for the small step sizes that softplus gives here. *slope = d softplus / dx = sigmoid(x).
+__device__ __forceinline__ float softplus(float x, float* slope) {
+  const float e = exp2_approx(-kLog2e * fabsf(x));
+  const float s = e * rcp_approx(2.f + e), s2 = s * s;
+  float p = 1.f / 13.f;
+  p = fmaf(p, s2, 1.f / 11.f);
+  p = fmaf(p, s2, 1.f / 9.f);
+  p = fmaf(p, s2, 1.f / 7.f);
+  p = fmaf(p, s2, 1.f / 5.f);
+  p = fmaf(p, s2, 1.f / 3.f);
+  p = fmaf(p, s2, 1.f);
+  const float r = rcp_approx(1.f + e);
+  *slope = x >= 0.f ? r : e * r;
+  return fmaxf(x, 0.f) + 2.f * s * p;
+}
+
+// Pairs of fp32 in one 64-bit register pair: one instruction per two multiply-adds.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unf2(F2 a, float* lo, float* hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(a.v)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 exp2_approx2(F2 a) {
+  float lo, hi;
+  unf2(a, &lo, &hi);
+  return f2(exp2_approx(lo), exp2_approx(hi));
+}
+__device__ __forceinline__ float sum2(F2 a) {
+  float lo, hi;
+  unf2(a, &lo, &hi);
+  return lo + hi;
+}
+
+// ------------------------------------------------------------------ parameter blocks
+
+// Residual add and RMS norm before a block; gated RMS norm after it (k_norm.cu). `stream` is the
+// residual stream: 0 none (x itself is normalised), 1 bf16, 2 fp32.
+struct NormParams {
+  long long rows;
+  int width;
+  float eps, scale;
+  int stream_kind;
+  int act;                     // gated: 1 SiLU, 2 sigmoid
+  const __nv_bfloat16* x;      // [rows,width]
+  const void* residual;        // [rows,width] of the stream's type, or null
+  const __nv_bfloat16* gate;   // gated: [rows,width]
+  const float* weight;         // [width]
+  __nv_bfloat16* y;
+  void* stream;                // forward: written; backward: read (the forward's, or x without a residual)
+  const __nv_bfloat16* dy;
+  const void* dstream;         // gradient w.r.t. the stream, its type (bf16 without a residual), or null
+  __nv_bfloat16 *dx, *dgate;
+  void* dresidual;             // or null
+  float* part;                 // [norm_partial_rows()][width] partial weight gradients
+  float* dweight;
+  int sms;
+};
+cudaError_t launch_add_norm_fwd(const NormParams& p, cudaStream_t s);
+cudaError_t launch_add_norm_bwd(const NormParams& p, cudaStream_t s);
+cudaError_t launch_gated_norm_fwd(const NormParams& p, cudaStream_t s);
+cudaError_t launch_gated_norm_bwd(const NormParams& p, cudaStream_t s);
+constexpr int kNormMaxWidth = 16384;
+// The most rows of partial weight gradients a backward writes.
+int norm_partial_rows();
+
+// Single-token steps (k_step.cu). Row b of the batch uses state slot index[b] (or b): a negative index marks a
+// padding row (zero output, no state touched), one >= slots is recorded in the status word as GDN_ERANGE
+// and treated the same.
+struct ConvStepParams {
+  int B, C, W, dil, HW, slots, silu;
+  long long x_stride;          // elements between batch rows
+  const int* index;
+  const __nv_bfloat16* x;
+  const float *w, *bias;
+  __nv_bfloat16 *state, *y;    // [slots,HW,C], [B,C]
+  int* status;
+  int sms;
+};
+cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t s);
+
+struct ConvStateParams {
+  int N, T, C, HW;
+  const int* cu;               // device offsets [N+1], or null (dense: N rows of T tokens)
+  const __nv_bfloat16 *x, *halo;
+  __nv_bfloat16* state;        // [N,HW,C]
+};
+cudaError_t launch_conv_state(const ConvStateParams& p, cudaStream_t s);
+
+struct DeltaStepParams {
+  int B, H, group, slots;      // group: value heads per q/k head
+  int kda, l2norm, beta_sigmoid, gate_act;
+  float scale, lower_bound;
+  long long q_stride, k_stride, v_stride;
+  const int* index;
+  const __nv_bfloat16 *q, *k, *v, *beta;
+  const float *g, *A_log, *dt_bias;
+  float* state;                // [slots,H,128,128]
+  __nv_bfloat16* o;            // [B,H,128]
+  int* status;
+};
+cudaError_t launch_delta_step(const DeltaStepParams& p, cudaStream_t s);
+
+// Selective scan (k_sscan_fwd.cu, k_sscan_bwd.cu, k_step.cu).
+constexpr int kSscanMaxN = 16;     // states per channel
+constexpr int kSscanBlock = 32;    // tokens between the states a training forward keeps; segments are multiples of it
+constexpr int kSscanThreads = 128; // channels per CTA
+
+struct SscanParams {
+  int T, D, N, G, Dg, seqs;    // Dg = D / G channels per group
+  int nseg_dense, nck_dense;   // segments and kept states per sequence of a dense batch
+  int L;                       // tokens per segment
+  int segs;                    // segments of all sequences
+  const int *cu, *seg_base, *ck_base;  // packed: device arrays [seqs+1] (tokens, segments, kept states), else null
+  int softplus;
+  long long u_s, dt_s, z_s, b_s, c_s;  // elements between tokens
+  const __nv_bfloat16 *u, *delta, *z, *Bm, *Cm;
+  const float *A, *Dskip, *bias, *h0;
+  __nv_bfloat16* y;            // [rows,D]
+  float* final_state;          // [seqs,D,N] or null
+  float* ck;                   // [kept states][N][D]: state before every kSscanBlock-th token, or null
+  float* seg_state;            // [segs][N][D]: the segments' end states, then their entry states
+  float* seg_dt;               // [segs][D]: sum of the step sizes
+  // backward
+  const __nv_bfloat16* dy;
+  const float* dfinal;
+  __nv_bfloat16 *du, *ddelta, *dz, *dB, *dC;
+  float *dA, *dD, *dbias, *dh0;
+  float* part_bc;              // [channel blocks][rows][2][N] partial dB, dC
+  float* part_par;             // [segs][N+2][D] partial dA, dD, ddelta_bias
+  long long rows;
+};
+// Channel blocks of all groups.
+inline int sscan_blocks(int G, int Dg) { return G * ((Dg + kSscanThreads - 1) / kSscanThreads); }
+cudaError_t launch_sscan_fwd(const SscanParams& p, cudaStream_t s);
+cudaError_t launch_sscan_bwd(const SscanParams& p, cudaStream_t s);
+
+struct SscanStepParams {
+  int B, D, N, G, Dg, slots, softplus;
+  long long u_s, dt_s, z_s, b_s, c_s;  // elements between batch rows
+  const int* index;
+  const __nv_bfloat16 *u, *delta, *z, *Bm, *Cm;
+  const float *A, *Dskip, *bias;
+  float* state;                // [slots,D,N]
+  __nv_bfloat16* y;            // [B,D]
+  int* status;
+};
+cudaError_t launch_sscan_step(const SscanStepParams& p, cudaStream_t s);
+
+}  // namespace gdn

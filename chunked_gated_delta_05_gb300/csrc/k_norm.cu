@@ -1,0 +1,355 @@
+// RMS norms before and after a block.
+//
+// Before:  r = residual + scale x (kept in the stream's type),  y = r rstd(r) w,  rstd(r) = (mean(r^2) + eps)^(-1/2).
+//   dr = dstream + rstd (dy w - xh mean(dy w xh)),  xh = r rstd;   dx = scale dr,  dresidual = dr,  dw = sum_rows dy xh.
+// After:   y = x rstd(x) w act(gate), act = SiLU or sigmoid.
+//   dn = dy act;  dx = rstd (dn w - xh mean(dn w xh));  dgate = dy xh w act';  dw = sum_rows dn xh.
+// The backward kernels recompute rstd: sum r^2 and sum dy w r come out of the same pass over the row, so nothing but
+// the stream is kept by the forward.
+//
+// A row is held in registers by G threads (a power of two) of NV vectors of VEC elements each: one read and one write
+// of every tensor. All sums are fp32. Rows of widths that are no multiple of 8, or unaligned tensors, take the element
+// path (VEC = 1). Bound: HBM.
+#include <algorithm>
+#include <initializer_list>
+
+#include "block_ops.cuh"
+
+namespace gdn {
+namespace {
+
+enum { kAdd = 0, kGated = 1 };
+
+template <int VEC>
+__device__ __forceinline__ void load_row(float* v, const __nv_bfloat16* src) {
+  if constexpr (VEC == 8) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+    v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
+    v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+  } else {
+    v[0] = __bfloat162float(src[0]);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void load_row(float* v, const float* src) {
+  if constexpr (VEC == 8) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    v[0] = src[0];
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float* v) {
+  if constexpr (VEC == 8)
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  else
+    dst[0] = __float2bfloat16_rn(v[0]);
+}
+template <int VEC>
+__device__ __forceinline__ void store_row(float* dst, const float* v) {
+  if constexpr (VEC == 8) {
+    reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    dst[0] = v[0];
+  }
+}
+__device__ __forceinline__ float round_to(float v, const float*) { return v; }
+__device__ __forceinline__ float round_to(float v, const __nv_bfloat16*) { return __bfloat162float(__float2bfloat16_rn(v)); }
+
+// Sums of NS values over the G threads of a row; every thread of the block takes part. `red` holds NS x 32 floats.
+template <int NS>
+__device__ __forceinline__ void row_sum(float* s, int G, float* red) {
+  const int lanes = min(G, 32);
+  for (int o = lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < NS; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+  if (G <= 32) return;
+  const int warp = threadIdx.x >> 5, per = G >> 5, first = warp / per * per;
+  __syncthreads();  // the previous row's sums have been read
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int i = 0; i < NS; ++i) red[i * 32 + warp] = s[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    float t = 0.f;
+    for (int w = 0; w < per; ++w) t += red[i * 32 + first + w];
+    s[i] = t;
+  }
+}
+
+// act(gate) and its derivative.
+__device__ __forceinline__ float gate_act(float g, int act, float* d) {
+  const float sg = sigmoid_fast(g);
+  if (act == 1) {
+    *d = sg * (1.f + g * (1.f - sg));
+    return g * sg;
+  }
+  *d = sg * (1.f - sg);
+  return sg;
+}
+
+template <int KIND, int VEC, int NV, int THREADS, typename ST>
+__global__ void __launch_bounds__(THREADS) k_norm_fwd(NormParams p, int G) {
+  __shared__ float red[32];
+  const int per_block = blockDim.x / G, lane = threadIdx.x & (G - 1);
+  const int units = p.width / VEC;
+  const float inv = 1.f / float(p.width);
+  for (long long r0 = (long long)blockIdx.x * per_block; r0 < p.rows; r0 += (long long)gridDim.x * per_block) {
+    const long long r = r0 + threadIdx.x / G;
+    const bool live = r < p.rows;
+    const long long base = r * p.width;
+    float v[NV][VEC], ss[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int u = lane + j * G;
+      if (live && u < units) {
+        const long long at = base + (long long)u * VEC;
+        load_row<VEC>(v[j], p.x + at);
+        if (KIND == kAdd && p.residual) {
+          float t[VEC];
+          load_row<VEC>(t, static_cast<const ST*>(p.residual) + at);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[j][e] = round_to(fmaf(p.scale, v[j][e], t[e]), (const ST*)nullptr);
+          store_row<VEC>(static_cast<ST*>(p.stream) + at, v[j]);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) ss[0] = fmaf(v[j][e], v[j][e], ss[0]);
+      }
+    }
+    row_sum<1>(ss, G, red);
+    const float rstd = rsqrtf(fmaf(ss[0], inv, p.eps));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int u = lane + j * G;
+      if (live && u < units) {
+        const long long at = base + (long long)u * VEC;
+        float w[VEC];
+        load_row<VEC>(w, p.weight + u * VEC);
+        if (KIND == kGated) {
+          float t[VEC], d;
+          load_row<VEC>(t, p.gate + at);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) w[e] *= gate_act(t[e], p.act, &d);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[j][e] = v[j][e] * rstd * w[e];
+        store_row<VEC>(p.y + at, v[j]);
+      }
+    }
+  }
+}
+
+// One pass per row; each thread keeps its columns' weight gradients in registers over all rows of its group, the groups of
+// the block add theirs in shared memory in a fixed order, and the block writes one row of partial sums.
+template <int KIND, int VEC, int NV, int THREADS, typename ST>
+__global__ void __launch_bounds__(THREADS) k_norm_bwd(NormParams p, int G) {
+  extern __shared__ float acc_s[];
+  __shared__ float red[64];
+  const int per_block = blockDim.x / G, lane = threadIdx.x & (G - 1), grp = threadIdx.x / G;
+  const int units = p.width / VEC;
+  const float inv = 1.f / float(p.width);
+  float dw[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) dw[j][e] = 0.f;
+  for (long long r0 = (long long)blockIdx.x * per_block; r0 < p.rows; r0 += (long long)gridDim.x * per_block) {
+    const long long r = r0 + grp;
+    const bool live = r < p.rows;
+    const long long base = r * p.width;
+    float v[NV][VEC], d[NV][VEC], s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int u = lane + j * G;
+      if (live && u < units) {
+        const long long at = base + (long long)u * VEC;
+        load_row<VEC>(v[j], KIND == kAdd ? static_cast<const ST*>(p.stream) + at : reinterpret_cast<const ST*>(p.x) + at);
+        load_row<VEC>(d[j], p.dy + at);
+        float w[VEC];
+        load_row<VEC>(w, p.weight + u * VEC);
+        if (KIND == kGated) {
+          float t[VEC], da;
+          load_row<VEC>(t, p.gate + at);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) d[j][e] *= gate_act(t[e], p.act, &da);  // dn
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          s[0] = fmaf(v[j][e], v[j][e], s[0]);
+          s[1] = fmaf(d[j][e] * w[e], v[j][e], s[1]);
+        }
+      }
+    }
+    row_sum<2>(s, G, red);
+    const float rstd = rsqrtf(fmaf(s[0], inv, p.eps));
+    const float c = s[1] * inv * rstd * rstd;  // mean(dn w xh) / (rstd r) per element: xh mean(...) = r rstd^2 mean(dn w r)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int u = lane + j * G;
+      if (live && u < units) {
+        const long long at = base + (long long)u * VEC;
+        float w[VEC], o[VEC];
+        load_row<VEC>(w, p.weight + u * VEC);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          o[e] = rstd * fmaf(d[j][e], w[e], -v[j][e] * c);
+          dw[j][e] = fmaf(d[j][e], v[j][e] * rstd, dw[j][e]);
+        }
+        if (KIND == kAdd) {
+          if (p.dstream) {
+            float t[VEC];
+            load_row<VEC>(t, static_cast<const ST*>(p.dstream) + at);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) o[e] += t[e];
+          }
+          if (p.dresidual) store_row<VEC>(static_cast<ST*>(p.dresidual) + at, o);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) o[e] *= p.scale;
+        } else {
+          float t[VEC], q[VEC], da;
+          load_row<VEC>(t, p.gate + at);
+          load_row<VEC>(q, p.dy + at);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            gate_act(t[e], p.act, &da);
+            q[e] *= v[j][e] * rstd * w[e] * da;
+          }
+          store_row<VEC>(p.dgate + at, q);
+        }
+        store_row<VEC>(p.dx + at, o);
+      }
+    }
+  }
+  for (int g = 0; g < per_block; ++g) {
+    if (grp == g) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const int u = lane + j * G;
+          if (u >= units) continue;
+          const int at = u * VEC + e;
+          const float t = g == 0 ? dw[j][e] : acc_s[at] + dw[j][e];
+          if (g == per_block - 1)
+            p.part[(long long)blockIdx.x * p.width + at] = t;
+          else
+            acc_s[at] = t;
+        }
+    }
+    if (per_block > 1) __syncthreads();
+  }
+}
+
+// dweight[c] = sum over the blocks' partial rows, in a fixed order: 32 columns x 32 row lanes per block.
+__global__ void __launch_bounds__(1024) k_norm_reduce(const float* part, float* dw, int rows, int width) {
+  __shared__ float s[32][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float t = 0.f;
+  if (c < width)
+#pragma unroll 4
+    for (int r = threadIdx.y; r < rows; r += 32) t += part[(long long)r * width + c];
+  s[threadIdx.y][threadIdx.x] = t;
+  __syncthreads();
+  float v = s[threadIdx.x][threadIdx.y];  // lane: row group, warp: column
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int cc = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && cc < width) dw[cc] = v;
+}
+
+struct Plan {
+  int vec, nv, G, threads;
+};
+
+// Threads and vectors of a row: as few threads as hold it in two vectors each (16 elements; 8 on the element path), so that
+// the sums cross few threads and each has several loads in flight; four (32) where that takes over 256 threads.
+Plan plan_rows(int width, bool vec8) {
+  Plan p;
+  p.vec = vec8 ? 8 : 1;
+  const int units = width / p.vec, few = vec8 ? 2 : 8, most = vec8 ? 4 : 32;
+  int G = 8;
+  while (G < 256 && G * few < units) G *= 2;
+  if (G * most < units) G = 512;
+  const int nv = (units + G - 1) / G;
+  p.nv = vec8 && nv <= 1 ? 1 : nv <= few ? few : most;
+  p.G = G;
+  p.threads = G > 256 ? G : 256;
+  return p;
+}
+
+constexpr int kBwdBlocksPerSm = 4;
+constexpr int kMaxPartialRows = 160 * kBwdBlocksPerSm;
+
+// Calls f<VEC, NV, THREADS>() of the plan.
+#define GDN_NORM_DISPATCH(q, CALL)                                   \
+  if (q.vec == 8) {                                                  \
+    if (q.threads == 512) { CALL(8, 4, 512); }                       \
+    else if (q.nv == 1) { CALL(8, 1, 256); }                         \
+    else if (q.nv == 2) { CALL(8, 2, 256); }                         \
+    else { CALL(8, 4, 256); }                                        \
+  } else {                                                           \
+    if (q.threads == 512) { CALL(1, 32, 512); }                      \
+    else if (q.nv == 8) { CALL(1, 8, 256); }                         \
+    else { CALL(1, 32, 256); }                                       \
+  }
+
+template <int KIND, typename ST>
+cudaError_t run_fwd(const NormParams& p, bool vec8, cudaStream_t s) {
+  const Plan q = plan_rows(p.width, vec8);
+  const int per_block = q.threads / q.G;
+  const long long blocks = (p.rows + per_block - 1) / per_block;
+  const int grid = int(blocks < (1ll << 30) ? blocks : (1ll << 30));
+#define GDN_CALL(VEC, NV, T) k_norm_fwd<KIND, VEC, NV, T, ST><<<grid, T, 0, s>>>(p, q.G)
+  GDN_NORM_DISPATCH(q, GDN_CALL)
+#undef GDN_CALL
+  return cudaGetLastError();
+}
+
+template <int KIND, typename ST>
+cudaError_t run_bwd(const NormParams& p, bool vec8, cudaStream_t s) {
+  const Plan q = plan_rows(p.width, vec8);
+  const int per_block = q.threads / q.G;
+  const long long blocks = (p.rows + per_block - 1) / per_block;
+  const long long most = std::min((long long)p.sms * kBwdBlocksPerSm, (long long)kMaxPartialRows);
+  const int grid = int(std::min(blocks, most));
+  const size_t smem = per_block > 1 ? size_t(p.width) * 4 : 0;
+#define GDN_CALL(VEC, NV, T) k_norm_bwd<KIND, VEC, NV, T, ST><<<grid, T, smem, s>>>(p, q.G)
+  GDN_NORM_DISPATCH(q, GDN_CALL)
+#undef GDN_CALL
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  k_norm_reduce<<<(p.width + 31) / 32, dim3(32, 32), 0, s>>>(p.part, p.dweight, grid, p.width);
+  return cudaGetLastError();
+}
+
+bool all16(std::initializer_list<const void*> ps) {
+  uintptr_t m = 0;
+  for (const void* q : ps) m |= reinterpret_cast<uintptr_t>(q);
+  return (m & 15) == 0;
+}
+
+}  // namespace
+
+int norm_partial_rows() { return kMaxPartialRows; }
+
+cudaError_t launch_add_norm_fwd(const NormParams& p, cudaStream_t s) {
+  const bool v = p.width % 8 == 0 && all16({p.x, p.residual, p.weight, p.y, p.stream});
+  return p.stream_kind == 2 ? run_fwd<kAdd, float>(p, v, s) : run_fwd<kAdd, __nv_bfloat16>(p, v, s);
+}
+cudaError_t launch_add_norm_bwd(const NormParams& p, cudaStream_t s) {
+  const bool v = p.width % 8 == 0 && all16({p.dy, p.dstream, p.stream, p.weight, p.dx, p.dresidual});
+  return p.stream_kind == 2 ? run_bwd<kAdd, float>(p, v, s) : run_bwd<kAdd, __nv_bfloat16>(p, v, s);
+}
+cudaError_t launch_gated_norm_fwd(const NormParams& p, cudaStream_t s) {
+  const bool v = p.width % 8 == 0 && all16({p.x, p.gate, p.weight, p.y});
+  return run_fwd<kGated, __nv_bfloat16>(p, v, s);
+}
+cudaError_t launch_gated_norm_bwd(const NormParams& p, cudaStream_t s) {
+  const bool v = p.width % 8 == 0 && all16({p.x, p.gate, p.weight, p.dy, p.dx, p.dgate});
+  return run_bwd<kGated, __nv_bfloat16>(p, v, s);
+}
+
+}  // namespace gdn

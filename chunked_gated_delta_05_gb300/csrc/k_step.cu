@@ -1,0 +1,318 @@
+// Single-token forms: one new token per batch row, states updated in place. All of them read and write a state that
+// is far larger than the token's vectors and do a few operations per value of it, so HBM bounds a large batch and the
+// launch a small one; every state element is read once and written once, in 16-byte pieces where its layout allows.
+//
+//   convolution  z = b + sum_i w_i x[t - (W-1-i) d],  y = silu(z);  the state holds the last (W-1) d inputs.
+//   delta rule   S' = exp(g) S,  d = b (v - S'^T k),  S = S' + k d^T,  o = scale S^T q = scale (S'^T q + (q.k) d):
+//                both products with S' come out of one pass, so the state is read before one barrier and written after it.
+//   scan         h = exp(dt A) h + dt u B,  y = (C.h + D u) silu(z).
+#include <algorithm>
+
+#include "block_ops.cuh"
+#include "gdn.h"
+
+namespace gdn {
+namespace {
+
+// State slot of batch row b, or -1 for a padding row (or an index outside the pool, which is recorded).
+__device__ __forceinline__ int slot_of(const int* index, int b, int slots, int* status) {
+  if (!index) return b;
+  const int i = __ldg(index + b);
+  if (i >= slots) {
+    if (status && threadIdx.x == 0) atomicCAS(status, 0, GDN_ERANGE);
+    return -1;
+  }
+  return i;
+}
+
+// ------------------------------------------------------------------ short convolution
+
+// Eight channels per thread: the weights stay in registers while the block walks its batch rows.
+template <int W>
+__global__ void __launch_bounds__(128) k_conv_step(ConvStepParams p) {
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  const bool live = c < p.C;
+  float w[8][W], bias[8];
+  if (live) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[e][i] = __ldg(p.w + (size_t)(c + e) * W + i);
+      bias[e] = p.bias ? __ldg(p.bias + c + e) : 0.f;
+    }
+  }
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
+    const int slot = slot_of(p.index, b, p.slots, p.status);
+    if (!live) continue;
+    __nv_bfloat16* y = p.y + (size_t)b * p.C + c;
+    if (slot < 0) {
+      *reinterpret_cast<uint4*>(y) = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 xu = __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)b * p.x_stride + c));
+    uint4* st = reinterpret_cast<uint4*>(p.state + (size_t)slot * p.HW * p.C + c);
+    const size_t row = size_t(p.C) / 8;
+    float z[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = bias[e];
+    auto tap = [&](const uint4& u, int i) {
+      const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        z[2 * e] = fmaf(bf16_lo(q[e]), w[2 * e][i], z[2 * e]);
+        z[2 * e + 1] = fmaf(bf16_hi(q[e]), w[2 * e + 1][i], z[2 * e + 1]);
+      }
+    };
+    if (p.dil == 1) {
+      uint4 h[W];
+#pragma unroll
+      for (int i = 0; i < W - 1; ++i) h[i] = st[i * row];
+      h[W - 1] = xu;
+#pragma unroll
+      for (int i = 0; i < W; ++i) tap(h[i], i);
+#pragma unroll
+      for (int i = 0; i < W - 1; ++i) st[i * row] = h[i + 1];
+    } else {
+      // oldest row first: row j moves to j - 1; rows that are multiples of the dilation are taps
+#pragma unroll
+      for (int i = 0; i < W - 1; ++i) tap(st[(size_t)i * p.dil * row], i);
+      tap(xu, W - 1);
+      for (int j = 0; j + 1 < p.HW; ++j) st[j * row] = st[(j + 1) * row];
+      if (p.HW > 0) st[(size_t)(p.HW - 1) * row] = xu;
+    }
+    if (p.silu)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] *= sigmoid_fast(z[e]);
+    *reinterpret_cast<uint4*>(y) = make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
+  }
+}
+
+// The last HW inputs of every sequence (its halo's, or zeros, where it is shorter): what a prompt leaves for the step.
+__global__ void __launch_bounds__(128) k_conv_state(ConvStateParams p) {
+  const int cblocks = (p.C / 8 + 127) / 128;
+  const int c = (blockIdx.x % cblocks * 128 + threadIdx.x) * 8;
+  const int nj = blockIdx.x / cblocks, n = nj / p.HW, j = nj % p.HW;
+  if (c >= p.C) return;
+  const long long t0 = p.cu ? p.cu[n] : (long long)n * p.T, t1 = p.cu ? p.cu[n + 1] : t0 + p.T;
+  const long long t = t1 - p.HW + j;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (t >= t0)
+    v = __ldg(reinterpret_cast<const uint4*>(p.x + t * p.C + c));
+  else if (p.halo)
+    v = __ldg(reinterpret_cast<const uint4*>(p.halo + ((long long)n * p.HW + (p.HW + (t - t0))) * p.C + c));
+  *reinterpret_cast<uint4*>(p.state + ((long long)n * p.HW + j) * p.C + c) = v;
+}
+
+// ------------------------------------------------------------------ delta rule
+
+// One CTA per (row, head, 32 of the 128 value columns): thread = 4 columns x 4 key rows, the state's 64 bytes in
+// registers from their load to their store. Warps hold key rows 4 w + 32 i, so every load instruction covers four
+// 128-byte lines.
+constexpr int kVSplit = 4;
+
+__global__ void __launch_bounds__(256) k_delta_step(DeltaStepParams p) {
+  __shared__ float qs[kD], ks[kD], dec[kD], qk_s;
+  __shared__ float4 red[2][8][8];
+  const int vt = blockIdx.x % kVSplit, h = (blockIdx.x / kVSplit) % p.H;
+  const int b = blockIdx.x / (kVSplit * p.H);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slot = slot_of(p.index, b, p.slots, p.status);
+  __nv_bfloat16* o = p.o + ((size_t)b * p.H + h) * kD + vt * 32;
+  if (slot < 0) {
+    if (tid < 16) reinterpret_cast<uint32_t*>(o)[tid] = 0;
+    return;
+  }
+  const int cg = lane & 7, rg = warp * 4 + (lane >> 3);  // column group, key row modulo 32
+  float4* S = reinterpret_cast<float4*>(p.state + (((size_t)slot * p.H + h) * kD) * kD + vt * 32) + cg;
+  float4 st[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) st[i] = S[(size_t)(rg + 32 * i) * (kD / 4)];
+
+  const int hk = h / p.group;
+  if (warp == 0) {
+    const uint2 qu = *reinterpret_cast<const uint2*>(p.q + (size_t)b * p.q_stride + hk * kD + lane * 4);
+    const uint2 ku = *reinterpret_cast<const uint2*>(p.k + (size_t)b * p.k_stride + hk * kD + lane * 4);
+    float q[4] = {bf16_lo(qu.x), bf16_hi(qu.x), bf16_lo(qu.y), bf16_hi(qu.y)};
+    float k[4] = {bf16_lo(ku.x), bf16_hi(ku.x), bf16_lo(ku.y), bf16_hi(ku.y)};
+    float qq = 0.f, kk = 0.f, qk = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      qq = fmaf(q[e], q[e], qq);
+      kk = fmaf(k[e], k[e], kk);
+      qk = fmaf(q[e], k[e], qk);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+      qq += __shfl_xor_sync(0xffffffffu, qq, m);
+      kk += __shfl_xor_sync(0xffffffffu, kk, m);
+      qk += __shfl_xor_sync(0xffffffffu, qk, m);
+    }
+    const float rq = p.l2norm ? rsqrtf(qq + 1e-6f) : 1.f, rk = p.l2norm ? rsqrtf(kk + 1e-6f) : 1.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      qs[lane * 4 + e] = q[e] * rq;
+      ks[lane * 4 + e] = k[e] * rk;
+    }
+    if (lane == 0) qk_s = qk * rq * rk;
+  } else if (warp >= 4) {
+    const int i = tid - 128;
+    float g;
+    if (!p.kda) {
+      g = __ldg(p.g + (size_t)b * p.H + h);
+    } else {
+      g = __ldg(p.g + ((size_t)b * p.H + h) * kD + i);
+      if (p.gate_act) g = p.lower_bound * sigmoid_fast(expf(__ldg(p.A_log + h)) * (g + __ldg(p.dt_bias + h * kD + i)));
+    }
+    dec[i] = exp2_approx(g * kLog2e);
+  }
+  __syncthreads();
+  float4 pk = make_float4(0.f, 0.f, 0.f, 0.f), pq = pk;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = rg + 32 * i;
+    const float d = dec[r], kr = ks[r], qr = qs[r];
+    st[i].x *= d, st[i].y *= d, st[i].z *= d, st[i].w *= d;
+    pk.x = fmaf(kr, st[i].x, pk.x), pk.y = fmaf(kr, st[i].y, pk.y), pk.z = fmaf(kr, st[i].z, pk.z), pk.w = fmaf(kr, st[i].w, pk.w);
+    pq.x = fmaf(qr, st[i].x, pq.x), pq.y = fmaf(qr, st[i].y, pq.y), pq.z = fmaf(qr, st[i].z, pq.z), pq.w = fmaf(qr, st[i].w, pq.w);
+  }
+#pragma unroll
+  for (int m = 8; m <= 16; m <<= 1) {
+    pk.x += __shfl_xor_sync(0xffffffffu, pk.x, m), pk.y += __shfl_xor_sync(0xffffffffu, pk.y, m);
+    pk.z += __shfl_xor_sync(0xffffffffu, pk.z, m), pk.w += __shfl_xor_sync(0xffffffffu, pk.w, m);
+    pq.x += __shfl_xor_sync(0xffffffffu, pq.x, m), pq.y += __shfl_xor_sync(0xffffffffu, pq.y, m);
+    pq.z += __shfl_xor_sync(0xffffffffu, pq.z, m), pq.w += __shfl_xor_sync(0xffffffffu, pq.w, m);
+  }
+  if (lane < 8) {
+    red[0][warp][cg] = pk;
+    red[1][warp][cg] = pq;
+  }
+  __syncthreads();
+  float4 a = red[0][0][cg];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) {
+    const float4 t = red[0][w][cg];
+    a.x += t.x, a.y += t.y, a.z += t.z, a.w += t.w;
+  }
+  float beta = __bfloat162float(p.beta[(size_t)b * p.H + h]);
+  if (p.beta_sigmoid) beta = sigmoid_fast(beta);
+  const uint2 vu = *reinterpret_cast<const uint2*>(p.v + (size_t)b * p.v_stride + h * kD + vt * 32 + cg * 4);
+  const float4 dl = make_float4(beta * (bf16_lo(vu.x) - a.x), beta * (bf16_hi(vu.x) - a.y), beta * (bf16_lo(vu.y) - a.z), beta * (bf16_hi(vu.y) - a.w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float kr = ks[rg + 32 * i];
+    st[i].x = fmaf(kr, dl.x, st[i].x), st[i].y = fmaf(kr, dl.y, st[i].y), st[i].z = fmaf(kr, dl.z, st[i].z), st[i].w = fmaf(kr, dl.w, st[i].w);
+    S[(size_t)(rg + 32 * i) * (kD / 4)] = st[i];
+  }
+  if (tid < 8) {
+    float4 c = red[1][0][cg];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+      const float4 t = red[1][w][cg];
+      c.x += t.x, c.y += t.y, c.z += t.z, c.w += t.w;
+    }
+    const float qk = qk_s, sc = p.scale;
+    reinterpret_cast<uint2*>(o)[cg] = make_uint2(pack_bf16(sc * fmaf(qk, dl.x, c.x), sc * fmaf(qk, dl.y, c.y)),
+                                                 pack_bf16(sc * fmaf(qk, dl.z, c.z), sc * fmaf(qk, dl.w, c.w)));
+  }
+}
+
+// ------------------------------------------------------------------ selective scan
+
+// LPC lanes per channel, four states each (16-byte pieces when N is a multiple of 4).
+template <int LPC>
+__global__ void __launch_bounds__(256) k_sscan_step(SscanStepParams p) {
+  const int cblocks = (p.D * LPC + 255) / 256;
+  const int b = blockIdx.x / cblocks, i = blockIdx.x % cblocks * 256 + threadIdx.x;
+  const int d = i / LPC, n0 = (i % LPC) * 4;
+  const int slot = slot_of(p.index, b, p.slots, p.status);
+  const bool live = d < p.D;
+  float y = 0.f;
+  if (live && slot >= 0) {
+    float* hp = p.state + ((size_t)slot * p.D + d) * p.N + n0;
+    const float* ap = p.A + (size_t)d * p.N + n0;
+    const __nv_bfloat16* bp = p.Bm + (size_t)b * p.b_s + (d / p.Dg) * p.N + n0;
+    const __nv_bfloat16* cp = p.Cm + (size_t)b * p.c_s + (d / p.Dg) * p.N + n0;
+    const int ns = min(4, p.N - n0);
+    const bool vec = p.N % 4 == 0;
+    float h[4] = {0.f, 0.f, 0.f, 0.f}, a[4] = {0.f, 0.f, 0.f, 0.f};
+    if (vec) {
+      const float4 hv = *reinterpret_cast<const float4*>(hp), av = __ldg(reinterpret_cast<const float4*>(ap));
+      h[0] = hv.x, h[1] = hv.y, h[2] = hv.z, h[3] = hv.w;
+      a[0] = av.x, a[1] = av.y, a[2] = av.z, a[3] = av.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < ns) h[e] = hp[e], a[e] = __ldg(ap + e);
+    }
+    const float u = __bfloat162float(p.u[(size_t)b * p.u_s + d]);
+    float dt = __bfloat162float(p.delta[(size_t)b * p.dt_s + d]), slope;
+    if (p.bias) dt += __ldg(p.bias + d);
+    if (p.softplus) dt = softplus(dt, &slope);
+    const float dtu = dt * u, dtl = dt * kLog2e;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e < ns) {
+        h[e] = fmaf(exp2_approx(dtl * a[e]), h[e], dtu * __bfloat162float(bp[e]));
+        y = fmaf(h[e], __bfloat162float(cp[e]), y);
+      }
+    }
+    if (vec) {
+      *reinterpret_cast<float4*>(hp) = make_float4(h[0], h[1], h[2], h[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < ns) hp[e] = h[e];
+    }
+    if (n0 == 0 && p.Dskip) y = fmaf(__ldg(p.Dskip + d), u, y);
+  }
+#pragma unroll
+  for (int m = LPC / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+  if (live && n0 == 0) {
+    if (p.z && slot >= 0) {
+      const float z = __bfloat162float(p.z[(size_t)b * p.z_s + d]);
+      y *= z * sigmoid_fast(z);
+    }
+    p.y[(size_t)b * p.D + d] = __float2bfloat16_rn(y);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t s) {
+  const int bx = (p.C / 8 + 127) / 128;
+  // up to eight CTAs of four warps per SM; beyond that a block walks several rows on one load of its weights
+  const int by = std::max(1, std::min(p.B, (p.sms * 8 + bx - 1) / bx));
+  const dim3 grid(bx, std::min(by, 65535));
+  switch (p.W) {
+    case 1: k_conv_step<1><<<grid, 128, 0, s>>>(p); break;
+    case 2: k_conv_step<2><<<grid, 128, 0, s>>>(p); break;
+    case 3: k_conv_step<3><<<grid, 128, 0, s>>>(p); break;
+    case 4: k_conv_step<4><<<grid, 128, 0, s>>>(p); break;
+    case 5: k_conv_step<5><<<grid, 128, 0, s>>>(p); break;
+    case 6: k_conv_step<6><<<grid, 128, 0, s>>>(p); break;
+    case 7: k_conv_step<7><<<grid, 128, 0, s>>>(p); break;
+    default: k_conv_step<8><<<grid, 128, 0, s>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_conv_state(const ConvStateParams& p, cudaStream_t s) {
+  k_conv_state<<<(p.C / 8 + 127) / 128 * p.N * p.HW, 128, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_delta_step(const DeltaStepParams& p, cudaStream_t s) {
+  k_delta_step<<<p.B * p.H * kVSplit, 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_sscan_step(const SscanStepParams& p, cudaStream_t s) {
+  const int lpc = p.N <= 4 ? 1 : p.N <= 8 ? 2 : 4;
+  const int grid = (p.D * lpc + 255) / 256 * p.B;
+  if (lpc == 1) k_sscan_step<1><<<grid, 256, 0, s>>>(p);
+  else if (lpc == 2) k_sscan_step<2><<<grid, 256, 0, s>>>(p);
+  else k_sscan_step<4><<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace gdn

@@ -3,6 +3,8 @@
  * Operations (forward and backward of one layer's recurrence):
  *   gdn_fwd / gdn_bwd : Gated DeltaNet, one scalar log-decay g per token and head.
  *   kda_fwd / kda_bwd : Kimi Delta Attention, one log-decay per token, head and key channel.
+ * Around them: the short convolution, the block norms, the selective scan, and single-token steps
+ * (each described with its declarations below).
  *
  * What is computed. For every independent sequence (a dense batch row, or one document of a
  * packed row) and head, starting from S = initial_state (or 0), with K x V state S:
@@ -260,6 +262,181 @@ size_t gdn_conv_fwd_workspace_size(const gdn_conv_desc_t* desc);
 size_t gdn_conv_bwd_workspace_size(const gdn_conv_desc_t* desc);
 int gdn_conv_fwd(const gdn_conv_desc_t* desc, const gdn_conv_fwd_args_t* args, void* stream);
 int gdn_conv_bwd(const gdn_conv_desc_t* desc, const gdn_conv_bwd_args_t* args, void* stream);
+
+/* The state a prompt leaves for gdn_conv_step: the last (W-1) dilation inputs of every sequence (its
+ * halo's, or zeros, where the sequence is shorter), bf16 [N,(W-1)*dilation,C], the halo's layout.
+ * `args` uses x, halo, y (the state, written), workspace; the workspace is the forward's. */
+int gdn_conv_state(const gdn_conv_desc_t* desc, const gdn_conv_fwd_args_t* args, void* stream);
+
+/* ---- Norms before and after a block (the layers around the recurrence; no counterpart in the pages).
+ * Before: r = residual + residual_scale x, kept in the residual stream's type (stream_kind 1: bf16, 2: fp32),
+ *   y = r rsqrt(mean(r^2) + eps) weight; the norm reads the stream as it is kept. stream_kind 0: no residual, r = x
+ *   (residual, stream NULL, residual_scale 1).
+ * After: y = x rsqrt(mean(x^2) + eps) weight act(gate), act: 1 SiLU, 2 sigmoid.
+ * Rows are contiguous; width 1 .. 16384. Sums are fp32. Rows of a width that is a multiple of 8, in tensors aligned to
+ * 16 bytes, move in 16-byte pieces; others are slower, not refused. */
+typedef struct {
+  long long rows;
+  int width;
+  float eps;                 /* >= 0 */
+  float residual_scale;
+  int stream_kind;           /* gdn_add_norm_*: 0, 1, 2 (above) */
+  int activation;            /* gdn_gated_norm_*: 1 SiLU, 2 sigmoid */
+} gdn_norm_desc_t;
+
+typedef struct {
+  const void* x;             /* bf16 [rows,width] */
+  const void* residual;      /* add: [rows,width] of the stream's type; gated: the gate, bf16 */
+  const float* weight;       /* fp32 [width] */
+  void* y;                   /* bf16 [rows,width], written */
+  void* stream;              /* add with a residual: [rows,width] of the stream's type, written; may be `residual` */
+} gdn_norm_fwd_args_t;
+
+typedef struct {
+  const void* x;             /* add: the forward's stream (x itself for stream_kind 0); gated: x */
+  const void* gate;          /* gated: bf16 */
+  const float* weight;
+  const void* dy;            /* bf16 [rows,width] */
+  const void* dstream;       /* add: gradient w.r.t. the stream, its type (bf16 for stream_kind 0), or NULL */
+  void* dx;                  /* bf16, written (add: residual_scale times the stream's total gradient) */
+  void* dgate;               /* gated: bf16, written */
+  void* dresidual;           /* add with a residual: the stream's type, written, or NULL */
+  float* dweight;            /* fp32 [width], written: summed over the rows in a fixed order */
+  void* workspace;           /* >= gdn_norm_bwd_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+} gdn_norm_bwd_args_t;
+
+size_t gdn_norm_bwd_workspace_size(const gdn_norm_desc_t* desc);
+int gdn_add_norm_fwd(const gdn_norm_desc_t* desc, const gdn_norm_fwd_args_t* args, void* stream);
+int gdn_add_norm_bwd(const gdn_norm_desc_t* desc, const gdn_norm_bwd_args_t* args, void* stream);
+int gdn_gated_norm_fwd(const gdn_norm_desc_t* desc, const gdn_norm_fwd_args_t* args, void* stream);
+int gdn_gated_norm_bwd(const gdn_norm_desc_t* desc, const gdn_norm_bwd_args_t* args, void* stream);
+
+/* ---- Single-token steps: one new token per batch row, the rows' states updated in place.
+ * State slot of row b: state_indices[b] (device int32), or b when state_indices is NULL. A negative index marks a
+ * padding row: its output is zero and no state is touched; so does an index >= num_slots, which also records GDN_ERANGE
+ * in the status word. The steps do not reset that word. No slot may appear twice. They need no workspace and allocate nothing. */
+typedef struct {
+  int B, C;                  /* C % 8 == 0 */
+  int W, dilation;           /* as gdn_conv_desc_t */
+  int activation;
+  int num_slots;             /* rows of the state (>= B without state_indices) */
+  long long x_stride;        /* elements between batch rows of x (0: C); a multiple of 8 */
+} gdn_conv_step_desc_t;
+
+typedef struct {
+  const void* x;             /* bf16 [B,C], 16-byte aligned */
+  const float* weight;       /* fp32 [C,W] */
+  const float* bias;         /* fp32 [C] or NULL */
+  void* state;               /* bf16 [num_slots,(W-1)*dilation,C], the last inputs, oldest first; 16-byte aligned, updated */
+  const int32_t* state_indices; /* [B] or NULL */
+  void* y;                   /* bf16 [B,C], 16-byte aligned, written */
+  int* status;               /* or NULL */
+} gdn_conv_step_args_t;
+
+int gdn_conv_step(const gdn_conv_step_desc_t* desc, const gdn_conv_step_args_t* args, void* stream);
+
+/* One token of the recurrence of gdn_fwd / kda_fwd (same formulas and flags). */
+typedef struct {
+  int B, H;
+  int num_k_heads;           /* 0 means H */
+  int num_slots;
+  float scale;               /* <= 0 selects 1/sqrt(128) */
+  int use_qk_l2norm, use_beta_sigmoid;
+  int use_gate_in_kernel;    /* KDA only, with lower_bound in [-5, 0) */
+  float lower_bound;
+  long long q_stride, k_stride, v_stride; /* elements between batch rows (0: contiguous); multiples of 4 */
+} gdn_step_desc_t;
+
+typedef struct {
+  const void *q, *k, *v;     /* bf16 [B,Hk,128], [B,Hk,128], [B,H,128], heads contiguous, 8-byte aligned */
+  const float* g;            /* GDN [B,H], KDA [B,H,128] */
+  const void* beta;          /* bf16 [B,H] */
+  float* state;              /* fp32 [num_slots,H,128,128], 16-byte aligned, updated */
+  const int32_t* state_indices;
+  void* o;                   /* bf16 [B,H,128], 8-byte aligned, written */
+  const float *A_log, *dt_bias;
+  int* status;
+} gdn_step_args_t;
+
+int gdn_step(const gdn_step_desc_t* desc, const gdn_step_args_t* args, void* stream);
+int kda_step(const gdn_step_desc_t* desc, const gdn_step_args_t* args, void* stream);
+
+/* ---- Selective state space scan (a sibling of the gated delta rule with a diagonal transition; no counterpart in the
+ * pages). For every sequence, channel d of group d / (D/G), and its N states:
+ *   dt = softplus(delta + delta_bias) when delta_softplus, else delta + delta_bias
+ *   h  = exp(dt A[d]) h + dt u B_t,   y = (C_t . h + D u) silu(z)     (D, z: optional)
+ * State arithmetic is fp32. A is expected negative (dt A <= 0). Layout: u, delta, z, y [B,T,D] and B, C [B,T,G,N] bf16,
+ * token rows `*_stride` elements apart (0: contiguous; batches follow each other at T rows), everything else contiguous.
+ * A [D,N], D, delta_bias [D], states [N_seq,D,N] fp32. Packed documents as for gdn_fwd. N is 1 .. 16. Nothing needs more
+ * than its type's own alignment. */
+typedef struct {
+  int B, T, D, N, G;
+  const int32_t* cu_seqlens; /* HOST, num_seqs + 1 offsets, or NULL for dense */
+  int num_seqs;
+  int delta_softplus;
+  long long u_stride, delta_stride, z_stride, B_stride, C_stride;
+} gdn_sscan_desc_t;
+
+typedef struct {
+  const void *u, *delta;
+  const float* A;
+  const void *Bm, *Cm;
+  const float *D, *delta_bias; /* or NULL */
+  const void* z;             /* or NULL */
+  const float* initial_state;/* or NULL (zeros) */
+  void* y;                   /* bf16 [B,T,D], written */
+  float* final_state;        /* written, or NULL */
+  void* workspace;           /* >= gdn_sscan_fwd_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  void* saved;               /* training: >= gdn_sscan_saved_size() bytes (256-byte aligned) for the states the backward
+                                starts from; or NULL */
+  size_t saved_bytes;
+} gdn_sscan_fwd_args_t;
+
+typedef struct {
+  const void *u, *delta;     /* the forward's inputs */
+  const float* A;
+  const void *Bm, *Cm;
+  const float *D, *delta_bias;
+  const void* z;
+  const float* initial_state;
+  const void* dy;            /* bf16 [B,T,D] contiguous */
+  const float* dfinal;       /* gradient of the final state, or NULL */
+  void *du, *ddelta;         /* bf16 [B,T,D] contiguous, written */
+  float* dA;                 /* [D,N], written */
+  void *dB, *dC;             /* bf16 [B,T,G,N] contiguous, written: summed over the group's channels */
+  float *dD, *ddelta_bias;   /* [D], written when not NULL (each needs its input) */
+  void* dz;                  /* bf16, written; needed with z */
+  float* dh0;                /* or NULL */
+  void* workspace;           /* >= gdn_sscan_bwd_workspace_size() bytes; with `saved`, >= that minus gdn_sscan_saved_size() */
+  size_t workspace_bytes;
+  const void* saved;         /* the forward's, or NULL (recomputed) */
+  size_t saved_bytes;
+} gdn_sscan_bwd_args_t;
+
+size_t gdn_sscan_fwd_workspace_size(const gdn_sscan_desc_t* desc);
+size_t gdn_sscan_bwd_workspace_size(const gdn_sscan_desc_t* desc);
+size_t gdn_sscan_saved_size(const gdn_sscan_desc_t* desc);
+int gdn_sscan_fwd(const gdn_sscan_desc_t* desc, const gdn_sscan_fwd_args_t* args, void* stream);
+int gdn_sscan_bwd(const gdn_sscan_desc_t* desc, const gdn_sscan_bwd_args_t* args, void* stream);
+
+/* One token per batch row: u, delta, z, y [B,D], B, C [B,G,N] (row strides as above, T ignored, cu_seqlens NULL),
+ * state fp32 [num_slots,D,N] updated (16-byte aligned when N % 4 == 0, like A). */
+typedef struct {
+  const void *u, *delta;
+  const float* A;
+  const void *Bm, *Cm;
+  const float *D, *delta_bias;
+  const void* z;
+  float* state;
+  const int32_t* state_indices;
+  int num_slots;
+  void* y;
+  int* status;
+} gdn_sscan_step_args_t;
+
+int gdn_sscan_step(const gdn_sscan_desc_t* desc, const gdn_sscan_step_args_t* args, void* stream);
 
 /* Profiling hooks (not part of the computation). While enabled, every kernel launch of the
  * calls above is bracketed by CUDA events on its stream. gdn_timing_read() synchronizes the
