@@ -166,7 +166,7 @@ int validate_sscan(const gdn_sscan_desc_t* d, SscanProblem* P, bool step) {
   P->c_s = d->C_stride ? d->C_stride : gn;
   if (P->u_s < d->D || P->dt_s < d->D || P->z_s < d->D || P->b_s < gn || P->c_s < gn) return bad("a token stride is shorter than a token");
   for (long long st : {P->u_s, P->dt_s, P->z_s, P->b_s, P->c_s})
-    if (st > (1ll << 31)) return bad("a token stride is too large");
+    if (st > (1ll << 26)) return bad("a token stride is too large");
   P->cu = d->cu_seqlens;
   P->seqs = d->B;
   if (P->cu) {
@@ -191,7 +191,7 @@ struct SscanPlan {
   long long segs, cks;   // segments and kept states of all sequences
 };
 constexpr int kSms = 152;
-constexpr int kFwdCtasPerSm = 4, kBwdCtasPerSm = 2;
+constexpr int kFwdCtasPerSm = 5, kBwdCtasPerSm = 2;
 constexpr int kMinSegment = 64;
 
 SscanPlan plan_sscan(const SscanProblem& P, bool backward) {
@@ -203,7 +203,7 @@ SscanPlan plan_sscan(const SscanProblem& P, bool backward) {
     for (int i = 0; i < P.seqs; ++i) longest = std::max(longest, sequence_length(P, i));
   }
   const long long whole = ((long long)longest + kSscanBlock - 1) / kSscanBlock * kSscanBlock;
-  long long L = P.rows * blocks / want / kSscanBlock * kSscanBlock;
+  long long L = (P.rows * blocks + want * kSscanBlock - 1) / (want * kSscanBlock) * kSscanBlock;
   L = std::max<long long>(L, kMinSegment);
   if (blocks * P.rows >= want * longest || L >= whole) L = whole;
   SscanPlan q{};
@@ -306,6 +306,14 @@ void fill(const SscanProblem& P, const SscanPlan& q, const SscanLayout& l, char*
     p->seg_state = reinterpret_cast<float*>(ws + l.seg_state);
     p->seg_dt = reinterpret_cast<float*>(ws + l.seg_dt);
   }
+}
+
+// Whether all channel blocks' rows start on 16-byte boundaries: the tensors, their strides and the groups.
+void set_vectors(const SscanProblem& P, SscanParams* p) {
+  const bool groups = P.G == 1 || (P.D / P.G) % 8 == 0;
+  p->vec = groups && aligned(p->u, 16) && aligned(p->delta, 16) && aligned(p->z, 16) && aligned(p->dy, 16) && P.u_s % 8 == 0 &&
+           P.dt_s % 8 == 0 && (!p->z || P.z_s % 8 == 0) && (!p->dy || P.D % 8 == 0);
+  p->vec_out = groups && P.D % 8 == 0 && aligned(p->y, 16) && aligned(p->du, 16) && aligned(p->ddelta, 16) && aligned(p->dz, 16);
 }
 
 using bf = __nv_bfloat16;
@@ -517,6 +525,7 @@ int gdn_sscan_fwd(const gdn_sscan_desc_t* d, const gdn_sscan_fwd_args_t* a, void
   p.final_state = a->final_state;
   p.ck = static_cast<float*>(a->saved);
   if (P.cu && (rc = upload_tables(P, q, const_cast<int*>(p.cu), s))) return rc;
+  set_vectors(P, &p);
   TimedScope t(kKSscanFwd, s);
   return cuda_rc(launch_sscan_fwd(p, s), "selective scan kernels");
 }
@@ -562,6 +571,7 @@ int gdn_sscan_bwd(const gdn_sscan_desc_t* d, const gdn_sscan_bwd_args_t* a, void
   if (!a->saved) {  // the forward's states again, without its output
     fill(P, f, lf, ws, &p);
     if (P.cu && (rc = upload_tables(P, f, const_cast<int*>(p.cu), s))) return rc;
+    set_vectors(P, &p);
     TimedScope t(kKSscanFwd, s);
     if ((rc = cuda_rc(launch_sscan_fwd(p, s), "selective scan kernels"))) return rc;
   }
@@ -580,6 +590,7 @@ int gdn_sscan_bwd(const gdn_sscan_desc_t* d, const gdn_sscan_bwd_args_t* a, void
   p.part_bc = reinterpret_cast<float*>(ws + l.part_bc);
   p.part_par = reinterpret_cast<float*>(ws + l.part_par);
   if (P.cu && (rc = upload_tables(P, q, const_cast<int*>(p.cu), s))) return rc;
+  set_vectors(P, &p);
   TimedScope t(kKSscanBwd, s);
   return cuda_rc(launch_sscan_bwd(p, s), "selective scan backward kernels");
 }

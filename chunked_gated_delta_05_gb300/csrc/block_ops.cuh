@@ -156,6 +156,7 @@ struct SscanParams {
   int segs;                    // segments of all sequences
   const int *cu, *seg_base, *ck_base;  // packed: device arrays [seqs+1] (tokens, segments, kept states), else null
   int softplus;
+  bool vec, vec_out;           // u, delta, z (dy): every 8 channels of a block 16-byte aligned; the same of the outputs
   long long u_s, dt_s, z_s, b_s, c_s;  // elements between tokens
   const __nv_bfloat16 *u, *delta, *z, *Bm, *Cm;
   const float *A, *Dskip, *bias, *h0;

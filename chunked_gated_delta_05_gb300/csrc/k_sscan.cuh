@@ -42,6 +42,7 @@ __device__ __forceinline__ SscanSeg sscan_seg(const SscanParams& p, int s) {
 // Channel block of the call: group, channel and whether this thread has one (the others run along on zeros).
 struct SscanChan {
   int g, d;
+  int d0, chans;  // the block's first channel and how many it has
   bool live;
 };
 __device__ __forceinline__ SscanChan sscan_chan(const SscanParams& p, int cb) {
@@ -49,20 +50,22 @@ __device__ __forceinline__ SscanChan sscan_chan(const SscanParams& p, int cb) {
   SscanChan c;
   c.g = cb / bpg;
   const int i = (cb - c.g * bpg) * kSscanThreads + threadIdx.x;
+  c.d0 = c.g * p.Dg + (cb - c.g * bpg) * kSscanThreads;
+  c.chans = min(kSscanThreads, p.Dg - (cb - c.g * bpg) * kSscanThreads);
   c.live = i < p.Dg;
   c.d = c.g * p.Dg + min(i, p.Dg - 1);
   return c;
 }
 
-// A block of kSscanBlock tokens of B and C as fp32 in shared memory, [token][NP], zero past the segment's end and
-// past N: every thread of the CTA reads the same token's vectors (broadcasts).
-template <int NP>
+// TT tokens of B and C as fp32 in shared memory, [token][NP], zero past the segment's end and past N: every thread of
+// the CTA reads the same token's vectors (broadcasts).
+template <int NP, int TT>
 struct BcTile {
-  float B[kSscanBlock][NP], C[kSscanBlock][NP];
+  float B[TT][NP], C[TT][NP];
 };
-template <int NP>
+template <int NP, int TT>
 struct BcRegs {
-  static constexpr int kPer = kSscanBlock * NP / kSscanThreads;
+  static constexpr int kPer = TT * NP / kSscanThreads;
   uint16_t b[kPer], c[kPer];
   __device__ __forceinline__ void load(const SscanParams& p, int g, long long row, int len, bool want_b, bool want_c) {
 #pragma unroll
@@ -73,7 +76,7 @@ struct BcRegs {
       c[j] = in && want_c ? __ldg(reinterpret_cast<const uint16_t*>(p.Cm + (row + t) * p.c_s + g * p.N + n)) : 0;
     }
   }
-  __device__ __forceinline__ void store(BcTile<NP>& s) const {
+  __device__ __forceinline__ void store(BcTile<NP, TT>& s) const {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int e = threadIdx.x + j * kSscanThreads;
@@ -83,6 +86,51 @@ struct BcRegs {
   }
 };
 
+// TT tokens x kSscanThreads channels of a bf16 tensor in shared memory, as they are in memory, zero past the segment's
+// end and the group's channels. Copied in 16-byte pieces where every piece is aligned (`vec`), else by elements.
+template <int TT>
+struct ChTile {
+  uint16_t v[TT][kSscanThreads];
+  // src: element (first token, first channel); row: elements between tokens; len tokens and chans channels exist.
+  __device__ __forceinline__ void load(const __nv_bfloat16* src, long long row, int len, int chans, bool vec) {
+    if (vec) {
+      constexpr int kPieces = kSscanThreads / 8;
+#pragma unroll
+      for (int j = 0; j < TT * kPieces / kSscanThreads; ++j) {
+        const int e = threadIdx.x + j * kSscanThreads, t = e / kPieces, c = e % kPieces * 8;
+        const int bytes = t < len ? max(0, min(8, chans - c)) * 2 : 0;
+        const __nv_bfloat16* from = bytes ? src + t * row + c : src;
+        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&v[t][c]));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+      }
+    } else {
+      const int c = threadIdx.x;
+#pragma unroll 8
+      for (int t = 0; t < TT; ++t)
+        v[t][c] = t < len && c < chans ? __ldg(reinterpret_cast<const uint16_t*>(src + t * row + c)) : uint16_t(0);
+    }
+  }
+  // Writes the tile's valid part to dst; every element must have been written to the tile before a barrier.
+  __device__ __forceinline__ void store(__nv_bfloat16* dst, long long row, int len, int chans, bool vec) const {
+    if (vec) {
+      constexpr int kPieces = kSscanThreads / 8;
+#pragma unroll
+      for (int j = 0; j < TT * kPieces / kSscanThreads; ++j) {
+        const int e = threadIdx.x + j * kSscanThreads, t = e / kPieces, c = e % kPieces * 8;
+        if (t < len && c < chans) *reinterpret_cast<uint4*>(dst + t * row + c) = *reinterpret_cast<const uint4*>(&v[t][c]);
+      }
+    } else {
+      const int c = threadIdx.x;
+      for (int t = 0; t < TT; ++t)
+        if (t < len && c < chans) reinterpret_cast<uint16_t*>(dst)[t * row + c] = v[t][c];
+    }
+  }
+  __device__ __forceinline__ float at(int t) const { return __uint_as_float(uint32_t(v[t][threadIdx.x]) << 16); }
+  __device__ __forceinline__ void set(int t, float x) { v[t][threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+};
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
 // Pair j of a token's vector.
 __device__ __forceinline__ void load_pairs(F2* out, const float* src, int np) {
 #pragma unroll
@@ -91,10 +139,6 @@ __device__ __forceinline__ void load_pairs(F2* out, const float* src, int np) {
     out[2 * i] = f2(v.x, v.y);
     out[2 * i + 1] = f2(v.z, v.w);
   }
-}
-
-__device__ __forceinline__ float bf16_at(const __nv_bfloat16* p) {
-  return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p))) << 16);
 }
 
 // log2(e) A of the thread's channel, zero past N (a padded state then stays 0).

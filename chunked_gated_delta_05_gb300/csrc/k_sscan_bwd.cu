@@ -19,64 +19,71 @@ constexpr int kTile = 8;
 constexpr int kTiles = kSscanBlock / kTile;
 constexpr int kWarps = kSscanThreads / 32;
 
+constexpr int kRt = 16;  // tokens the adjoint map stages together, double-buffered
+
+template <int NP>
+struct RmapSmem {
+  BcTile<NP, kRt> bc[2];
+  ChTile<kRt> delta[2], dy[2], z[2];
+};
+
 // The adjoint map of a segment: from a zero exit gradient to the gradient of the state before its first token.
 template <int NP>
-__global__ void __launch_bounds__(kSscanThreads) k_sscan_rmap(SscanParams p, int blocks) {
-  __shared__ BcTile<NP> bc[2];
-  const SscanSeg sg = sscan_seg(p, blockIdx.x / blocks);
+__global__ void __launch_bounds__(kSscanThreads, 5) k_sscan_rmap(SscanParams p, int blocks) {
+  extern __shared__ __align__(16) char smem_raw[];
+  RmapSmem<NP>& sm = *reinterpret_cast<RmapSmem<NP>*>(smem_raw);
+  const int seg = blockIdx.x / blocks;
+  const SscanSeg sg = sscan_seg(p, seg);
   if (sg.j == 0) return;
   const SscanChan ch = sscan_chan(p, blockIdx.x % blocks);
-  const int d = ch.d, seg = blockIdx.x / blocks;
+  const int d = ch.d;
   F2 A2[NP / 2], g[NP / 2];
   load_A2<NP>(A2, p, d);
 #pragma unroll
   for (int i = 0; i < NP / 2; ++i) g[i] = f2(0.f, 0.f);
   const float bias = p.bias ? __ldg(p.bias + d) : 0.f;
-  const bool gate = p.z != nullptr;
-  const __nv_bfloat16 *dp = p.delta + sg.row0 * p.dt_s + d, *yp = p.dy + sg.row0 * p.D + d;
-  const __nv_bfloat16* zp = gate ? p.z + sg.row0 * p.z_s + d : nullptr;
+  const bool gate = p.z != nullptr, softplus_on = p.softplus;
   float dt_sum = 0.f;
-  const int nb = (sg.len + kSscanBlock - 1) / kSscanBlock;
-  BcRegs<NP> raw;
-  raw.load(p, ch.g, sg.row0 + (nb - 1) * kSscanBlock, sg.len - (nb - 1) * kSscanBlock, false, true);
-  raw.store(bc[0]);
-  float yn[kTile], dn[kTile], zn[kTile];
-  auto fetch = [&](int t0) {
-#pragma unroll
-    for (int i = 0; i < kTile; ++i) {
-      const bool in = t0 >= 0 && t0 + i < sg.len;
-      yn[i] = in ? bf16_at(yp + (long long)(t0 + i) * p.D) : 0.f;
-      dn[i] = in ? bf16_at(dp + (t0 + i) * p.dt_s) : 0.f;
-      zn[i] = in && gate ? bf16_at(zp + (t0 + i) * p.z_s) : 0.f;
-    }
+  BcRegs<NP, kRt> raw;
+  auto request = [&](int tb, int buf) {
+    const long long row = sg.row0 + tb;
+    const int len = sg.len - tb;
+    sm.delta[buf].load(p.delta + row * p.dt_s + ch.d0, p.dt_s, len, ch.chans, p.vec);
+    sm.dy[buf].load(p.dy + row * p.D + ch.d0, p.D, len, ch.chans, p.vec);
+    if (gate) sm.z[buf].load(p.z + row * p.z_s + ch.d0, p.z_s, len, ch.chans, p.vec);
+    copies_commit();
+    raw.load(p, ch.g, row, len, false, true);
   };
-  fetch((sg.len - 1) / kTile * kTile);
-  __syncthreads();
-  for (int b = nb - 1, buf = 0; b >= 0; --b, buf ^= 1) {
-    const int tb = b * kSscanBlock, n = min(kSscanBlock, sg.len - tb);
-    if (b > 0) raw.load(p, ch.g, sg.row0 + tb - kSscanBlock, kSscanBlock, false, true);
-    for (int q = (n - 1) / kTile * kTile; q >= 0; q -= kTile) {
-      float yc[kTile], dc[kTile], zc[kTile];
-#pragma unroll
-      for (int i = 0; i < kTile; ++i) yc[i] = yn[i], dc[i] = dn[i], zc[i] = zn[i];
-      fetch(tb + q - kTile);
-#pragma unroll
-      for (int i = kTile - 1; i >= 0; --i) {
-        if (q + i < n) {
-          float dt = dc[i] + bias, slope;
-          if (p.softplus) dt = softplus(dt, &slope);
-          dt_sum += dt;
-          const float dy0 = gate ? yc[i] * zc[i] * sigmoid_fast(zc[i]) : yc[i];
-          const F2 dt2 = f2(dt, dt), dy2 = f2(dy0, dy0);
-          F2 v[NP / 2];
-          load_pairs(v, bc[buf].C[q + i], NP);
-#pragma unroll
-          for (int s = 0; s < NP / 2; ++s) g[s] = mul2(exp2_approx2(mul2(dt2, A2[s])), fma2(v[s], dy2, g[s]));
-        }
-      }
-    }
-    if (b > 0) raw.store(bc[buf ^ 1]);
+  const int last = (sg.len - 1) / kRt * kRt;
+  request(last, 0);
+  raw.store(sm.bc[0]);
+  for (int tb = last, buf = 0; tb >= 0; tb -= kRt, buf ^= 1) {
+    copies_wait();
     __syncthreads();
+    if (tb > 0) request(tb - kRt, buf ^ 1);
+    const int n = min(kRt, sg.len - tb);
+    auto token = [&](int t) {
+      float dt = sm.delta[buf].at(t) + bias, slope, dy0 = sm.dy[buf].at(t);
+      if (softplus_on) dt = softplus(dt, &slope);
+      dt_sum += dt;
+      if (gate) {
+        const float z = sm.z[buf].at(t);
+        dy0 *= z * sigmoid_fast(z);
+      }
+      const F2 dt2 = f2(dt, dt), dy2 = f2(dy0, dy0);
+      F2 v[NP / 2];
+      load_pairs(v, sm.bc[buf].C[t], NP);
+#pragma unroll
+      for (int s = 0; s < NP / 2; ++s) g[s] = mul2(exp2_approx2(mul2(dt2, A2[s])), fma2(v[s], dy2, g[s]));
+    };
+    if (n == kRt) {
+#pragma unroll 4
+      for (int t = kRt - 1; t >= 0; --t) token(t);
+    } else {
+#pragma unroll 1
+      for (int t = n - 1; t >= 0; --t) token(t);
+    }
+    if (tb > 0) raw.store(sm.bc[buf ^ 1]);
   }
   if (!ch.live) return;
   store_state<NP>(g, p.seg_state + (size_t)seg * p.N * p.D, p, d);
@@ -131,20 +138,22 @@ __device__ __forceinline__ void channel_sum(float* c, const F2* v, const float* 
 
 template <int NP>
 struct BwdSmem {
-  BcTile<NP> bc;
+  BcTile<NP, kSscanBlock> bc;
+  ChTile<kSscanBlock> u, delta, z, dy;                 // du, ddelta and dz replace u, delta and z token by token
   float entry[kTiles][NP / 2][kSscanThreads][2];       // states before each tile
+  float2 dts[kTile][kSscanThreads];                    // the tile's dt and d dt / d delta
   float red[kWarps][kSscanBlock][2][16];               // the warps' sums over their channels: dC, dB
 };
 
 template <int NP>
-__global__ void __launch_bounds__(kSscanThreads) k_sscan_bwd(SscanParams p, int blocks) {
+__global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   BwdSmem<NP>& sm = *reinterpret_cast<BwdSmem<NP>*>(smem_raw);
   const int seg = blockIdx.x / blocks, cb = blockIdx.x % blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   const SscanChan ch = sscan_chan(p, cb);
   const int d = ch.d, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool gate = p.z != nullptr;
+  const bool gate = p.z != nullptr, softplus_on = p.softplus;
   float even[4], odd[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -160,114 +169,104 @@ __global__ void __launch_bounds__(kSscanThreads) k_sscan_bwd(SscanParams p, int 
     else if (p.dfinal) load_user_state<NP>(g, p.dfinal + (size_t)sg.seq * p.D * p.N, p, d);
   }
   const float bias = p.bias ? __ldg(p.bias + d) : 0.f, skip = p.Dskip ? __ldg(p.Dskip + d) : 0.f;
-  const __nv_bfloat16 *up = p.u + sg.row0 * p.u_s + d, *dp = p.delta + sg.row0 * p.dt_s + d, *yp = p.dy + sg.row0 * p.D + d;
-  const __nv_bfloat16* zp = gate ? p.z + sg.row0 * p.z_s + d : nullptr;
-  const long long out0 = sg.row0 * p.D + d;
   float dD = 0.f, dbias = 0.f;
   const int nb = (sg.len + kSscanBlock - 1) / kSscanBlock;
   for (int b = nb - 1; b >= 0; --b) {
-    const int tb = b * kSscanBlock, n = min(kSscanBlock, sg.len - tb);
-    {
-      BcRegs<NP> raw;
-      raw.load(p, ch.g, sg.row0 + tb, n, true, true);
-      __syncthreads();  // the previous block's tile and sums have been read
-      raw.store(sm.bc);
-    }
-    __syncthreads();
+    const int tb = b * kSscanBlock, n = min(kSscanBlock, sg.len - tb), tiles = (n + kTile - 1) / kTile;
+    const long long row = sg.row0 + tb;
+    __syncthreads();  // the previous block's tiles and sums have been read
+    sm.u.load(p.u + row * p.u_s + ch.d0, p.u_s, n, ch.chans, p.vec);
+    sm.delta.load(p.delta + row * p.dt_s + ch.d0, p.dt_s, n, ch.chans, p.vec);
+    sm.dy.load(p.dy + row * p.D + ch.d0, p.D, n, ch.chans, p.vec);
+    if (gate) sm.z.load(p.z + row * p.z_s + ch.d0, p.z_s, n, ch.chans, p.vec);
+    copies_commit();
     F2 h[NP / 2];
     load_state<NP>(h, p.ck + (size_t)(sg.ck0 + b) * p.N * p.D, p, d);
-    const int tiles = (n + kTile - 1) / kTile;
+    {
+      BcRegs<NP, kSscanBlock> raw;
+      raw.load(p, ch.g, row, n, true, true);
+      raw.store(sm.bc);
+    }
+    copies_wait();
+    __syncthreads();
+    // forward over the block, leaving the states before each tile
     for (int q = 0; q < tiles; ++q) {
 #pragma unroll
       for (int s = 0; s < NP / 2; ++s) *reinterpret_cast<unsigned long long*>(sm.entry[q][s][tid]) = h[s].v;
       if (q == tiles - 1) break;
-      float uc[kTile], dc[kTile];
-#pragma unroll
+#pragma unroll 4
       for (int i = 0; i < kTile; ++i) {
-        uc[i] = bf16_at(up + (tb + q * kTile + i) * p.u_s);
-        dc[i] = bf16_at(dp + (tb + q * kTile + i) * p.dt_s);
-      }
-#pragma unroll
-      for (int i = 0; i < kTile; ++i) {
-        float dt = dc[i] + bias, slope;
-        if (p.softplus) dt = softplus(dt, &slope);
-        const float dtu = dt * uc[i];
+        const int t = q * kTile + i;
+        float dt = sm.delta.at(t) + bias, slope;
+        if (softplus_on) dt = softplus(dt, &slope);
+        const float dtu = dt * sm.u.at(t);
         const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
         F2 v[NP / 2];
-        load_pairs(v, sm.bc.B[q * kTile + i], NP);
+        load_pairs(v, sm.bc.B[t], NP);
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) h[s] = fma2(exp2_approx2(mul2(dt2, A2[s])), h[s], mul2(dtu2, v[s]));
       }
     }
     for (int q = tiles - 1; q >= 0; --q) {
-      const int t0 = tb + q * kTile, m = min(kTile, sg.len - t0);
-      float uc[kTile], dt[kTile], slope[kTile], yc[kTile], zc[kTile];
-#pragma unroll
-      for (int i = 0; i < kTile; ++i) {
-        const bool in = i < m && ch.live;
-        uc[i] = in ? bf16_at(up + (t0 + i) * p.u_s) : 0.f;
-        dt[i] = in ? bf16_at(dp + (t0 + i) * p.dt_s) : 0.f;
-        yc[i] = in ? bf16_at(yp + (long long)(t0 + i) * p.D) : 0.f;
-        zc[i] = in && gate ? bf16_at(zp + (t0 + i) * p.z_s) : 0.f;
-      }
+      const int m = n - q * kTile;  // tokens of the tile, if fewer than kTile
       F2 H[kTile][NP / 2];
 #pragma unroll
       for (int s = 0; s < NP / 2; ++s) h[s].v = *reinterpret_cast<const unsigned long long*>(sm.entry[q][s][tid]);
 #pragma unroll
       for (int i = 0; i < kTile; ++i) {
-        dt[i] += bias;
-        slope[i] = 1.f;
-        if (p.softplus) dt[i] = softplus(dt[i], &slope[i]);
-        const float dtu = dt[i] * uc[i];
-        const F2 dt2 = f2(dt[i], dt[i]), dtu2 = f2(dtu, dtu);
+        const int t = q * kTile + i;
+        float dt = sm.delta.at(t) + bias, slope = 1.f;
+        if (softplus_on) dt = softplus(dt, &slope);
+        sm.dts[i][tid] = make_float2(dt, slope);
+        const float dtu = dt * sm.u.at(t);
+        const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
         F2 v[NP / 2];
-        load_pairs(v, sm.bc.B[q * kTile + i], NP);
+        load_pairs(v, sm.bc.B[t], NP);
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) H[i][s] = fma2(exp2_approx2(mul2(dt2, A2[s])), i ? H[i ? i - 1 : 0][s] : h[s], mul2(dtu2, v[s]));
       }
 #pragma unroll
       for (int i = kTile - 1; i >= 0; --i) {
         if (i < m) {
-          float dy0 = yc[i], sig = 0.f;
+          const int t = q * kTile + i;
+          const float u = sm.u.at(t), dy = sm.dy.at(t), dt = sm.dts[i][tid].x, dtu = dt * u;
+          float dy0 = dy, sig = 0.f, z = 0.f;
           if (gate) {
-            sig = sigmoid_fast(zc[i]);
-            dy0 *= zc[i] * sig;
+            z = sm.z.at(t);
+            sig = sigmoid_fast(z);
+            dy0 *= z * sig;
           }
-          const float dtu = dt[i] * uc[i];
-          const F2 dt2 = f2(dt[i], dt[i]), dtu2 = f2(dtu, dtu), dy2 = f2(dy0, dy0);
+          const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu), dy2 = f2(dy0, dy0);
           float cC[4] = {0.f, 0.f, 0.f, 0.f}, cB[4] = {0.f, 0.f, 0.f, 0.f};
-          F2 v[NP / 2], t[NP / 2];
-          load_pairs(v, sm.bc.C[q * kTile + i], NP);
-          F2 y2 = f2(skip * uc[i], 0.f), sB = f2(0.f, 0.f), sA = f2(0.f, 0.f);
+          F2 v[NP / 2], w[NP / 2];
+          load_pairs(v, sm.bc.C[t], NP);
+          F2 y2 = f2(skip * u, 0.f), sB = f2(0.f, 0.f), sA = f2(0.f, 0.f);
 #pragma unroll
           for (int s = 0; s < NP / 2; ++s) {
             y2 = fma2(H[i][s], v[s], y2);
             g[s] = fma2(v[s], dy2, g[s]);
-            t[s] = mul2(H[i][s], dy2);
+            w[s] = mul2(H[i][s], dy2);
           }
-          channel_sum<NP>(cC, t, even, odd);
+          channel_sum<NP>(cC, w, even, odd);
 #pragma unroll
-          for (int s = 0; s < NP / 2; ++s) t[s] = mul2(g[s], dtu2);
-          channel_sum<NP>(cB, t, even, odd);
-          load_pairs(v, sm.bc.B[q * kTile + i], NP);
+          for (int s = 0; s < NP / 2; ++s) w[s] = mul2(g[s], dtu2);
+          channel_sum<NP>(cB, w, even, odd);
+          load_pairs(v, sm.bc.B[t], NP);
 #pragma unroll
           for (int s = 0; s < NP / 2; ++s) {
             sB = fma2(g[s], v[s], sB);
             g[s] = mul2(g[s], exp2_approx2(mul2(dt2, A2[s])));
-            const F2 w = mul2(g[s], i ? H[i ? i - 1 : 0][s] : h[s]);
-            sA = fma2(w, A2[s], sA);
-            dA[s] = fma2(w, dt2, dA[s]);
+            const F2 x = mul2(g[s], i ? H[i ? i - 1 : 0][s] : h[s]);
+            sA = fma2(x, A2[s], sA);
+            dA[s] = fma2(x, dt2, dA[s]);
           }
           const float dhB = sum2(sB);
-          const float ddt = fmaf(uc[i], dhB, 0.6931471805599453f * sum2(sA)), dd = ddt * slope[i];
-          dD = fmaf(dy0, uc[i], dD);
+          const float ddt = fmaf(u, dhB, 0.6931471805599453f * sum2(sA)), dd = ddt * sm.dts[i][tid].y;
+          dD = fmaf(dy0, u, dD);
           dbias += dd;
-          if (ch.live) {
-            const long long at = out0 + (long long)(t0 + i) * p.D;
-            p.du[at] = __float2bfloat16_rn(fmaf(dt[i], dhB, skip * dy0));
-            p.ddelta[at] = __float2bfloat16_rn(dd);
-            if (gate) p.dz[at] = __float2bfloat16_rn(yc[i] * sum2(y2) * sig * (1.f + zc[i] * (1.f - sig)));
-          }
+          sm.u.set(t, fmaf(dt, dhB, skip * dy0));
+          sm.delta.set(t, dd);
+          if (gate) sm.z.set(t, dy * sum2(y2) * sig * (1.f + z * (1.f - sig)));
           // rows of the accumulators = states, the four lanes of a row hold two column groups each: of the four sums
           // (dC, dB of states < 8 and >= 8) each lane ends with one
           const bool o1 = lane & 1, o2 = lane & 2;
@@ -275,15 +274,18 @@ __global__ void __launch_bounds__(kSscanThreads) k_sscan_bwd(SscanParams p, int 
           const float k0 = (o1 ? b0 : c0) + __shfl_xor_sync(0xffffffffu, o1 ? c0 : b0, 1);
           const float k1 = (o1 ? b1 : c1) + __shfl_xor_sync(0xffffffffu, o1 ? c1 : b1, 1);
           const float r = (o2 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, o2 ? k0 : k1, 2);
-          sm.red[warp][q * kTile + i][o1][(lane >> 2) + (o2 ? 8 : 0)] = r;
+          sm.red[warp][t][o1][(lane >> 2) + (o2 ? 8 : 0)] = r;
         }
       }
     }
     __syncthreads();
+    sm.u.store(p.du + row * p.D + ch.d0, p.D, n, ch.chans, p.vec_out);
+    sm.delta.store(p.ddelta + row * p.D + ch.d0, p.D, n, ch.chans, p.vec_out);
+    if (gate) sm.z.store(p.dz + row * p.D + ch.d0, p.D, n, ch.chans, p.vec_out);
     const int per = 2 * p.N;
-    float* part = p.part_bc + ((size_t)cb * p.rows + sg.row0 + tb) * per;
+    float* part = p.part_bc + ((size_t)cb * p.rows + row) * per;
     for (int e = tid; e < n * per; e += kSscanThreads) {
-      const int t = e / per, w = e % per, which = w / p.N, st = w - which * p.N;
+      const int t = e / per, x = e % per, which = x / p.N, st = x - which * p.N;
       float r = 0.f;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) r += sm.red[k][t][which][st];
@@ -332,7 +334,7 @@ template <int NP>
 cudaError_t run(const SscanParams& p, cudaStream_t s) {
   const int blocks = sscan_blocks(p.G, p.Dg), grid = blocks * p.segs;
   if (p.seg_state) {
-    k_sscan_rmap<NP><<<grid, kSscanThreads, 0, s>>>(p, blocks);
+    k_sscan_rmap<NP><<<grid, kSscanThreads, sizeof(RmapSmem<NP>), s>>>(p, blocks);
     const long long n = (long long)p.seqs * p.N * p.D;
     k_sscan_rcompose<<<int((n + 255) / 256), 256, 0, s>>>(p);
   }

@@ -15,15 +15,23 @@
 namespace gdn {
 namespace {
 
-constexpr int kGroup = 8;  // tokens whose inputs are loaded together, one group ahead
+constexpr int kTt = 16;  // tokens staged together, double-buffered; kSscanBlock is a multiple of it
 
 template <int NP, bool MAP>
-__global__ void __launch_bounds__(kSscanThreads) k_sscan_pass(SscanParams p, int blocks) {
-  __shared__ BcTile<NP> bc[2];
-  const SscanSeg sg = sscan_seg(p, blockIdx.x / blocks);
+struct PassSmem {
+  BcTile<NP, kTt> bc[2];
+  ChTile<kTt> delta[2], u[2], z[MAP ? 1 : 2];  // y replaces u token by token
+};
+
+template <int NP, bool MAP>
+__global__ void __launch_bounds__(kSscanThreads, 5) k_sscan_pass(SscanParams p, int blocks) {
+  extern __shared__ __align__(16) char smem_raw[];
+  PassSmem<NP, MAP>& sm = *reinterpret_cast<PassSmem<NP, MAP>*>(smem_raw);
+  const int seg = blockIdx.x / blocks;
+  const SscanSeg sg = sscan_seg(p, seg);
   if (MAP && sg.j == sg.nseg - 1) return;
   const SscanChan ch = sscan_chan(p, blockIdx.x % blocks);
-  const int d = ch.d, seg = blockIdx.x / blocks;
+  const int d = ch.d;
 
   F2 A2[NP / 2], h[NP / 2];
   load_A2<NP>(A2, p, d);
@@ -34,64 +42,66 @@ __global__ void __launch_bounds__(kSscanThreads) k_sscan_pass(SscanParams p, int
     else if (p.h0) load_user_state<NP>(h, p.h0 + (size_t)sg.seq * p.D * p.N, p, d);
   }
   const float bias = p.bias ? __ldg(p.bias + d) : 0.f, skip = !MAP && p.Dskip ? __ldg(p.Dskip + d) : 0.f;
-  const bool gate = !MAP && p.z != nullptr;
-  const __nv_bfloat16 *up = p.u + sg.row0 * p.u_s + d, *dp = p.delta + sg.row0 * p.dt_s + d;
-  const __nv_bfloat16* zp = gate ? p.z + sg.row0 * p.z_s + d : nullptr;
-  __nv_bfloat16* yp = p.y ? p.y + sg.row0 * p.D + d : nullptr;
+  const bool out = !MAP && p.y, gate = out && p.z, softplus_on = p.softplus;
   float dt_sum = 0.f;
 
-  BcRegs<NP> raw;
-  raw.load(p, ch.g, sg.row0, sg.len, true, !MAP);
-  raw.store(bc[0]);
-  float un[kGroup], dn[kGroup], zn[kGroup];
-  auto fetch = [&](int t0) {
-#pragma unroll
-    for (int i = 0; i < kGroup; ++i) {
-      const bool in = t0 + i < sg.len;
-      un[i] = in ? bf16_at(up + (t0 + i) * p.u_s) : 0.f;
-      dn[i] = in ? bf16_at(dp + (t0 + i) * p.dt_s) : 0.f;
-      zn[i] = in && gate ? bf16_at(zp + (t0 + i) * p.z_s) : 0.f;
-    }
+  BcRegs<NP, kTt> raw;
+  auto request = [&](int tb, int buf) {
+    const long long row = sg.row0 + tb;
+    const int len = sg.len - tb;
+    sm.delta[buf].load(p.delta + row * p.dt_s + ch.d0, p.dt_s, len, ch.chans, p.vec);
+    sm.u[buf].load(p.u + row * p.u_s + ch.d0, p.u_s, len, ch.chans, p.vec);
+    if (!MAP && gate) sm.z[buf].load(p.z + row * p.z_s + ch.d0, p.z_s, len, ch.chans, p.vec);
+    copies_commit();
+    raw.load(p, ch.g, row, len, true, out);
   };
-  fetch(0);
-  __syncthreads();
-  for (int tb = 0, buf = 0; tb < sg.len; tb += kSscanBlock, buf ^= 1) {
-    const bool more = tb + kSscanBlock < sg.len;
-    if (more) raw.load(p, ch.g, sg.row0 + tb + kSscanBlock, sg.len - tb - kSscanBlock, true, !MAP);
-    if (!MAP && p.ck && ch.live) store_state<NP>(h, p.ck + (size_t)(sg.ck0 + tb / kSscanBlock) * p.N * p.D, p, d);
-    const int n = min(kSscanBlock, sg.len - tb);
-    for (int q = 0; q < n; q += kGroup) {
-      float uc[kGroup], dc[kGroup], zc[kGroup];
-#pragma unroll
-      for (int i = 0; i < kGroup; ++i) uc[i] = un[i], dc[i] = dn[i], zc[i] = zn[i];
-      fetch(tb + q + kGroup);
-#pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
-        if (q + i < n) {
-          float dt = dc[i] + bias, slope;
-          if (p.softplus) dt = softplus(dt, &slope);
-          const float dtu = dt * uc[i];
-          const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
-          F2 v[NP / 2];
-          load_pairs(v, bc[buf].B[q + i], NP);
-#pragma unroll
-          for (int s = 0; s < NP / 2; ++s) h[s] = fma2(exp2_approx2(mul2(dt2, A2[s])), h[s], mul2(dtu2, v[s]));
-          if (MAP) {
-            dt_sum += dt;
-          } else if (yp) {
-            load_pairs(v, bc[buf].C[q + i], NP);
-            F2 y2 = f2(skip * uc[i], 0.f);
-#pragma unroll
-            for (int s = 0; s < NP / 2; ++s) y2 = fma2(h[s], v[s], y2);
-            float y = sum2(y2);
-            if (gate) y *= zc[i] * sigmoid_fast(zc[i]);
-            if (ch.live) yp[(long long)(tb + q + i) * p.D] = __float2bfloat16_rn(y);
-          }
-        }
-      }
-    }
-    if (more) raw.store(bc[buf ^ 1]);
+  request(0, 0);
+  raw.store(sm.bc[0]);
+  for (int tb = 0, buf = 0; tb < sg.len; tb += kTt, buf ^= 1) {
+    copies_wait();
     __syncthreads();
+    const bool more = tb + kTt < sg.len;
+    if (more) request(tb + kTt, buf ^ 1);
+    if (!MAP && p.ck && tb % kSscanBlock == 0 && ch.live)
+      store_state<NP>(h, p.ck + (size_t)(sg.ck0 + tb / kSscanBlock) * p.N * p.D, p, d);
+    const int n = min(kTt, sg.len - tb);
+    auto token = [&](int t) {
+      float dt = sm.delta[buf].at(t) + bias, slope;
+      const float u = sm.u[buf].at(t);
+      if (softplus_on) dt = softplus(dt, &slope);
+      const float dtu = dt * u;
+      const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
+      F2 v[NP / 2];
+      load_pairs(v, sm.bc[buf].B[t], NP);
+#pragma unroll
+      for (int s = 0; s < NP / 2; ++s) h[s] = fma2(exp2_approx2(mul2(dt2, A2[s])), h[s], mul2(dtu2, v[s]));
+      if (MAP) {
+        dt_sum += dt;
+      } else if (out) {
+        load_pairs(v, sm.bc[buf].C[t], NP);
+        F2 y2 = f2(skip * u, 0.f);
+#pragma unroll
+        for (int s = 0; s < NP / 2; ++s) y2 = fma2(h[s], v[s], y2);
+        float y = sum2(y2);
+        if (gate) {
+          const float z = sm.z[MAP ? 0 : buf].at(t);
+          y *= z * sigmoid_fast(z);
+        }
+        sm.u[buf].set(t, y);
+      }
+    };
+    if (n == kTt) {
+#pragma unroll 4
+      for (int t = 0; t < kTt; ++t) token(t);
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < n; ++t) token(t);
+    }
+    if (more) raw.store(sm.bc[buf ^ 1]);
+    if (out) {
+      __syncthreads();
+      sm.u[buf].store(p.y + (sg.row0 + tb) * p.D + ch.d0, p.D, n, ch.chans, p.vec_out);
+    }
   }
   if (!ch.live) return;
   if (MAP) {
@@ -132,15 +142,17 @@ template <int NP>
 cudaError_t run(const SscanParams& p, cudaStream_t s) {
   const int blocks = sscan_blocks(p.G, p.Dg), grid = blocks * p.segs;
   if (p.seg_state) {
-    k_sscan_pass<NP, true><<<grid, kSscanThreads, 0, s>>>(p, blocks);
+    k_sscan_pass<NP, true><<<grid, kSscanThreads, sizeof(PassSmem<NP, true>), s>>>(p, blocks);
     const long long n = (long long)p.seqs * p.N * p.D;
     k_sscan_compose<<<int((n + 255) / 256), 256, 0, s>>>(p);
   }
-  k_sscan_pass<NP, false><<<grid, kSscanThreads, 0, s>>>(p, blocks);
+  k_sscan_pass<NP, false><<<grid, kSscanThreads, sizeof(PassSmem<NP, false>), s>>>(p, blocks);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+static_assert(sizeof(PassSmem<kSscanMaxN, false>) <= 48 * 1024, "fits the default shared memory limit");
 
 cudaError_t launch_sscan_fwd(const SscanParams& p, cudaStream_t s) { return p.N <= 8 ? run<8>(p, s) : run<16>(p, s); }
 
