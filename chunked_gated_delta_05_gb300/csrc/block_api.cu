@@ -183,8 +183,9 @@ int validate_sscan(const gdn_sscan_desc_t* d, SscanProblem* P, bool step) {
 }
 
 // Segments. One CTA walks kSscanThreads channels of one segment token by token, so a call needs CTAs enough for
-// every SM; a second segment costs the map pass over all tokens but the last segments'. Without a cut the time is the
-// longest sequence's walk, so a call is left whole only when its sequences alone give each SM its CTAs.
+// every SM; a second segment costs the map pass, which walks all segments but the last ones again. The plan takes, of the
+// lengths that fill one, two or more rounds of resident CTAs, the one whose rounds x length (plus a CTA's fixed cost, in
+// tokens) is least, and leaves the sequences whole when that is no longer than both passes.
 struct SscanPlan {
   int L;                 // tokens per segment, a multiple of kSscanBlock
   int most;              // most segments of a sequence
@@ -192,34 +193,42 @@ struct SscanPlan {
 };
 constexpr int kSms = 152;
 constexpr int kFwdCtasPerSm = 5, kBwdCtasPerSm = 2;
-constexpr int kMinSegment = 64;
+constexpr int kMinSegment = 64, kCtaTokens = 16;
+constexpr double kMapCost = 0.6;  // a token of the map pass against one of the pass that writes the outputs
+
+long long count_segments(const SscanProblem& P, long long L) {
+  if (!P.cu) return (P.T + L - 1) / L * P.seqs;
+  long long n = 0;
+  for (int i = 0; i < P.seqs; ++i) n += (sequence_length(P, i) + L - 1) / L;
+  return n;
+}
 
 SscanPlan plan_sscan(const SscanProblem& P, bool backward) {
-  const long long blocks = sscan_blocks(P.G, P.D / P.G);
-  const long long want = (long long)kSms * (backward ? kBwdCtasPerSm : kFwdCtasPerSm);
+  const long long blocks = sscan_blocks(P.G, P.D / P.G), slots = (long long)kSms * (backward ? kBwdCtasPerSm : kFwdCtasPerSm);
   int longest = P.T;
   if (P.cu) {
     longest = 0;
     for (int i = 0; i < P.seqs; ++i) longest = std::max(longest, sequence_length(P, i));
   }
   const long long whole = ((long long)longest + kSscanBlock - 1) / kSscanBlock * kSscanBlock;
-  long long L = (P.rows * blocks + want * kSscanBlock - 1) / (want * kSscanBlock) * kSscanBlock;
-  L = std::max<long long>(L, kMinSegment);
-  if (blocks * P.rows >= want * longest || L >= whole) L = whole;
-  SscanPlan q{};
-  q.L = int(L);
-  for (int i = 0; i < P.seqs; ++i) {
-    const int len = sequence_length(P, i), n = int((len + L - 1) / L), c = (len + kSscanBlock - 1) / kSscanBlock;
-    if (!P.cu) {
-      q.most = n;
-      q.segs = (long long)n * P.seqs;
-      q.cks = (long long)c * P.seqs;
-      break;
-    }
-    q.most = std::max(q.most, n);
-    q.segs += n;
-    q.cks += c;
+  auto rounds = [&](long long segs) { return (segs * blocks + slots - 1) / slots; };
+  long long best = whole;
+  double cost = double(rounds(P.seqs)) * (whole + kCtaTokens);
+  const int most_rounds = P.seqs > 64 ? 2 : 4;  // counting the segments of many documents takes host time
+  for (int r = 1; r <= most_rounds; ++r) {
+    long long L = (P.rows * blocks + slots * r * kSscanBlock - 1) / (slots * r * kSscanBlock) * kSscanBlock;
+    L = std::max<long long>(L, kMinSegment);
+    long long n = count_segments(P, L);
+    for (int k = 0; k < 4 && rounds(n) > r; ++k) n = count_segments(P, L += kSscanBlock);
+    if (L >= whole) continue;
+    const double c = double(rounds(n)) * (L + kCtaTokens) * (1.0 + kMapCost);
+    if (c < cost) cost = c, best = L;
   }
+  SscanPlan q{};
+  q.L = int(best);
+  q.segs = count_segments(P, best);
+  q.most = int((longest + best - 1) / best);
+  q.cks = count_segments(P, kSscanBlock);
   return q;
 }
 

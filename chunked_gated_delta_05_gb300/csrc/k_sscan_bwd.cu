@@ -7,9 +7,9 @@
 // One thread walks one channel. The states it needs in reverse come from the states a training forward keeps before every
 // 32nd token: a block of 32 is run forward once to leave the entry states of its 8-token tiles in shared memory, and each
 // tile, last to first, is run forward again into registers and then walked back. The adjoint chain is cut into segments
-// like the forward's. The sums over channels in dB and dC are matrix products with ones: a lane's pair of states is a
-// column of the B operand of m16n8k8, selector rows of A put state n into row n of the accumulator, and four lanes' channels
-// add up in each product (tf32 operands; the results are bf16). All other sums are fp32.
+// like the forward's. The sums over channels in dB and dC begin as matrix products with ones: a
+// lane's four states are its share of the A operand of m16n8k8, whose products add up four lanes' channels (tf32 operands;
+// the results are bf16), and seven exchanges add up the eight groups of lanes. All other sums are fp32.
 #include "k_sscan.cuh"
 
 namespace gdn {
@@ -62,26 +62,19 @@ __global__ void __launch_bounds__(kSscanThreads, 5) k_sscan_rmap(SscanParams p, 
     __syncthreads();
     if (tb > 0) request(tb - kRt, buf ^ 1);
     const int n = min(kRt, sg.len - tb);
-    auto token = [&](int t) {
-      float dt = sm.delta[buf].at(t) + bias, slope, dy0 = sm.dy[buf].at(t);
-      if (softplus_on) dt = softplus(dt, &slope);
+    // as in the forward: no branch in a token's work; past the segment's end dt and dy are 0
+#pragma unroll 4
+    for (int t = kRt - 1; t >= 0; --t) {
+      const float x = sm.delta[buf].at(t) + bias, dy = sm.dy[buf].at(t), z = sm.z[buf].at(t);
+      float slope, dt = softplus(x, &slope);
+      dt = t < n ? (softplus_on ? dt : x) : 0.f;
       dt_sum += dt;
-      if (gate) {
-        const float z = sm.z[buf].at(t);
-        dy0 *= z * sigmoid_fast(z);
-      }
+      const float dy0 = gate ? dy * (z * sigmoid_fast(z)) : dy;
       const F2 dt2 = f2(dt, dt), dy2 = f2(dy0, dy0);
       F2 v[NP / 2];
       load_pairs(v, sm.bc[buf].C[t], NP);
 #pragma unroll
       for (int s = 0; s < NP / 2; ++s) g[s] = mul2(exp2_approx2(mul2(dt2, A2[s])), fma2(v[s], dy2, g[s]));
-    };
-    if (n == kRt) {
-#pragma unroll 4
-      for (int t = kRt - 1; t >= 0; --t) token(t);
-    } else {
-#pragma unroll 1
-      for (int t = n - 1; t >= 0; --t) token(t);
     }
     if (tb > 0) raw.store(sm.bc[buf ^ 1]);
   }
@@ -116,24 +109,32 @@ __global__ void __launch_bounds__(256) k_sscan_rcompose(SscanParams p) {
   }
 }
 
-// C[r][c] += sum_k A[r][k] B[k][c] with this lane's b0 (k = lane % 4) and b1 (k = lane % 4 + 4) of column lane / 4.
-__device__ __forceinline__ void mma_sel(float* c, float a0, float a1, float a2, float a3, float b0, float b1) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+// D = A B + C for one m16n8k8 product: this lane holds A's rows lane / 4 and lane / 4 + 8 at k = lane % 4 (a0, a1) and
+// k = lane % 4 + 4 (a2, a3), and B's column lane / 4 at the same two k.
+__device__ __forceinline__ void mma_tf32(float* d, float a0, float a1, float a2, float a3, float b0, float b1, const float* c) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
-        "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+        "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// Adds this lane's NP values (pairs over states) into accumulator rows = states, columns = groups of four lanes.
+// Sums over the four channels of lanes 4 r .. 4 r + 3 of NP values a lane (pairs over states): states 4 j .. 4 j + 3 enter
+// product j as A, whose B has ones in column 2 j for k < 4 and in column 2 j + 1 for k >= 4 (sel). Lane 4 r + j then holds the
+// sums of states 4 j + {0, 2, 1, 3} of the four lanes.
 template <int NP>
-__device__ __forceinline__ void channel_sum(float* c, const F2* v, const float* even, const float* odd) {
+__device__ __forceinline__ void channel_sum(float* c, const F2* v, const float (*sel)[2]) {
+  const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < NP / 2; ++j) {
-    float lo, hi;
-    unf2(v[j], &lo, &hi);
-    if (j < 4) mma_sel(c, even[j], 0.f, odd[j], 0.f, lo, hi);
-    else mma_sel(c, 0.f, even[j - 4], 0.f, odd[j - 4], lo, hi);
+  for (int j = 0; j < NP / 4; ++j) {
+    float a0, a1, a2, a3;
+    unf2(v[2 * j], &a0, &a1);
+    unf2(v[2 * j + 1], &a2, &a3);
+    mma_tf32(c, a0, a1, a2, a3, sel[j][0], sel[j][1], j ? c : zero);
   }
+}
+// One value for two lanes: the lane with `up` keeps b, the other a, each plus the other lane's.
+__device__ __forceinline__ float exchange(float a, float b, bool up, int mask) {
+  return (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, mask);
 }
 
 template <int NP>
@@ -154,11 +155,11 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
   const SscanChan ch = sscan_chan(p, cb);
   const int d = ch.d, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool gate = p.z != nullptr, softplus_on = p.softplus;
-  float even[4], odd[4];
+  float sel[NP / 4][2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    even[j] = (lane >> 2) == 2 * j ? 1.f : 0.f;
-    odd[j] = (lane >> 2) == 2 * j + 1 ? 1.f : 0.f;
+  for (int j = 0; j < NP / 4; ++j) {
+    sel[j][0] = (lane >> 2) == 2 * j ? 1.f : 0.f;
+    sel[j][1] = (lane >> 2) == 2 * j + 1 ? 1.f : 0.f;
   }
   F2 A2[NP / 2], g[NP / 2], dA[NP / 2];
   load_A2<NP>(A2, p, d);
@@ -197,8 +198,9 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
 #pragma unroll 4
       for (int i = 0; i < kTile; ++i) {
         const int t = q * kTile + i;
-        float dt = sm.delta.at(t) + bias, slope;
-        if (softplus_on) dt = softplus(dt, &slope);
+        const float x = sm.delta.at(t) + bias;
+        float slope, dt = softplus(x, &slope);
+        dt = softplus_on ? dt : x;
         const float dtu = dt * sm.u.at(t);
         const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
         F2 v[NP / 2];
@@ -208,15 +210,17 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
       }
     }
     for (int q = tiles - 1; q >= 0; --q) {
-      const int m = n - q * kTile;  // tokens of the tile, if fewer than kTile
+      // no branch in a token's work; past the segment's end dt and d dt / d delta are 0
       F2 H[kTile][NP / 2];
 #pragma unroll
       for (int s = 0; s < NP / 2; ++s) h[s].v = *reinterpret_cast<const unsigned long long*>(sm.entry[q][s][tid]);
 #pragma unroll
       for (int i = 0; i < kTile; ++i) {
         const int t = q * kTile + i;
-        float dt = sm.delta.at(t) + bias, slope = 1.f;
-        if (softplus_on) dt = softplus(dt, &slope);
+        const float x = sm.delta.at(t) + bias;
+        float slope, dt = softplus(x, &slope);
+        dt = t < n ? (softplus_on ? dt : x) : 0.f;
+        slope = t < n ? (softplus_on ? slope : 1.f) : 0.f;
         sm.dts[i][tid] = make_float2(dt, slope);
         const float dtu = dt * sm.u.at(t);
         const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
@@ -227,55 +231,49 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
       }
 #pragma unroll
       for (int i = kTile - 1; i >= 0; --i) {
-        if (i < m) {
-          const int t = q * kTile + i;
-          const float u = sm.u.at(t), dy = sm.dy.at(t), dt = sm.dts[i][tid].x, dtu = dt * u;
-          float dy0 = dy, sig = 0.f, z = 0.f;
-          if (gate) {
-            z = sm.z.at(t);
-            sig = sigmoid_fast(z);
-            dy0 *= z * sig;
-          }
-          const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu), dy2 = f2(dy0, dy0);
-          float cC[4] = {0.f, 0.f, 0.f, 0.f}, cB[4] = {0.f, 0.f, 0.f, 0.f};
-          F2 v[NP / 2], w[NP / 2];
-          load_pairs(v, sm.bc.C[t], NP);
-          F2 y2 = f2(skip * u, 0.f), sB = f2(0.f, 0.f), sA = f2(0.f, 0.f);
+        const int t = q * kTile + i;
+        const float u = sm.u.at(t), dy = sm.dy.at(t), z = sm.z.at(t);
+        const float2 ds = sm.dts[i][tid];
+        const float dt = ds.x, dtu = dt * u, sig = sigmoid_fast(z);
+        const float dy0 = gate ? dy * (z * sig) : dy;
+        const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu), dy2 = f2(dy0, dy0);
+        float cC[4], cB[4];
+        F2 v[NP / 2], w[NP / 2];
+        load_pairs(v, sm.bc.C[t], NP);
+        F2 y2 = f2(skip * u, 0.f), sB = f2(0.f, 0.f), sA = f2(0.f, 0.f);
 #pragma unroll
-          for (int s = 0; s < NP / 2; ++s) {
-            y2 = fma2(H[i][s], v[s], y2);
-            g[s] = fma2(v[s], dy2, g[s]);
-            w[s] = mul2(H[i][s], dy2);
-          }
-          channel_sum<NP>(cC, w, even, odd);
-#pragma unroll
-          for (int s = 0; s < NP / 2; ++s) w[s] = mul2(g[s], dtu2);
-          channel_sum<NP>(cB, w, even, odd);
-          load_pairs(v, sm.bc.B[t], NP);
-#pragma unroll
-          for (int s = 0; s < NP / 2; ++s) {
-            sB = fma2(g[s], v[s], sB);
-            g[s] = mul2(g[s], exp2_approx2(mul2(dt2, A2[s])));
-            const F2 x = mul2(g[s], i ? H[i ? i - 1 : 0][s] : h[s]);
-            sA = fma2(x, A2[s], sA);
-            dA[s] = fma2(x, dt2, dA[s]);
-          }
-          const float dhB = sum2(sB);
-          const float ddt = fmaf(u, dhB, 0.6931471805599453f * sum2(sA)), dd = ddt * sm.dts[i][tid].y;
-          dD = fmaf(dy0, u, dD);
-          dbias += dd;
-          sm.u.set(t, fmaf(dt, dhB, skip * dy0));
-          sm.delta.set(t, dd);
-          if (gate) sm.z.set(t, dy * sum2(y2) * sig * (1.f + z * (1.f - sig)));
-          // rows of the accumulators = states, the four lanes of a row hold two column groups each: of the four sums
-          // (dC, dB of states < 8 and >= 8) each lane ends with one
-          const bool o1 = lane & 1, o2 = lane & 2;
-          const float c0 = cC[0] + cC[1], c1 = cC[2] + cC[3], b0 = cB[0] + cB[1], b1 = cB[2] + cB[3];
-          const float k0 = (o1 ? b0 : c0) + __shfl_xor_sync(0xffffffffu, o1 ? c0 : b0, 1);
-          const float k1 = (o1 ? b1 : c1) + __shfl_xor_sync(0xffffffffu, o1 ? c1 : b1, 1);
-          const float r = (o2 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, o2 ? k0 : k1, 2);
-          sm.red[warp][t][o1][(lane >> 2) + (o2 ? 8 : 0)] = r;
+        for (int s = 0; s < NP / 2; ++s) {
+          y2 = fma2(H[i][s], v[s], y2);
+          g[s] = fma2(v[s], dy2, g[s]);
+          w[s] = mul2(H[i][s], dy2);
         }
+        channel_sum<NP>(cC, w, sel);
+#pragma unroll
+        for (int s = 0; s < NP / 2; ++s) w[s] = mul2(g[s], dtu2);
+        channel_sum<NP>(cB, w, sel);
+        load_pairs(v, sm.bc.B[t], NP);
+#pragma unroll
+        for (int s = 0; s < NP / 2; ++s) {
+          sB = fma2(g[s], v[s], sB);
+          g[s] = mul2(g[s], exp2_approx2(mul2(dt2, A2[s])));
+          const F2 x = mul2(g[s], i ? H[i ? i - 1 : 0][s] : h[s]);
+          sA = fma2(x, A2[s], sA);
+          dA[s] = fma2(x, dt2, dA[s]);
+        }
+        const float dhB = sum2(sB);
+        const float ddt = fmaf(u, dhB, 0.6931471805599453f * sum2(sA)), dd = ddt * ds.y;
+        dD = fmaf(dy0, u, dD);
+        dbias += dd;
+        sm.u.set(t, fmaf(dt, dhB, skip * dy0));
+        sm.delta.set(t, dd);
+        sm.z.set(t, dy * sum2(y2) * (sig * fmaf(z, 1.f - sig, 1.f)));
+        // the eight sums of lane 4 r + j over its four lanes, added up over r, of which each lane ends with one
+        const bool r0 = lane & 4, r1 = lane & 8, r2 = lane & 16;
+        const float k0 = exchange(cC[0], cB[0], r0, 4), k1 = exchange(cC[1], cB[1], r0, 4);
+        const float k2 = exchange(cC[2], cB[2], r0, 4), k3 = exchange(cC[3], cB[3], r0, 4);
+        const float l0 = exchange(k0, k1, r1, 8), l1 = exchange(k2, k3, r1, 8);
+        // accumulator 0, 1, 2, 3 = states 4 j + 0, 2, 1, 3
+        sm.red[warp][t][r0][(lane & 3) * 4 + (r1 ? 2 : 0) + (r2 ? 1 : 0)] = exchange(l0, l1, r2, 16);
       }
     }
     __syncthreads();

@@ -65,10 +65,13 @@ __global__ void __launch_bounds__(kSscanThreads, 5) k_sscan_pass(SscanParams p, 
     if (!MAP && p.ck && tb % kSscanBlock == 0 && ch.live)
       store_state<NP>(h, p.ck + (size_t)(sg.ck0 + tb / kSscanBlock) * p.N * p.D, p, d);
     const int n = min(kTt, sg.len - tb);
-    auto token = [&](int t) {
-      float dt = sm.delta[buf].at(t) + bias, slope;
-      const float u = sm.u[buf].at(t);
-      if (softplus_on) dt = softplus(dt, &slope);
+    // no branch in a token's work, so that the compiler can overlap several tokens: past the segment's end dt = 0, which
+    // leaves the state as it is, and without softplus or gate their results are not selected
+#pragma unroll 4
+    for (int t = 0; t < kTt; ++t) {
+      const float x = sm.delta[buf].at(t) + bias, u = sm.u[buf].at(t);
+      float slope, dt = softplus(x, &slope);
+      dt = t < n ? (softplus_on ? dt : x) : 0.f;
       const float dtu = dt * u;
       const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
       F2 v[NP / 2];
@@ -77,25 +80,14 @@ __global__ void __launch_bounds__(kSscanThreads, 5) k_sscan_pass(SscanParams p, 
       for (int s = 0; s < NP / 2; ++s) h[s] = fma2(exp2_approx2(mul2(dt2, A2[s])), h[s], mul2(dtu2, v[s]));
       if (MAP) {
         dt_sum += dt;
-      } else if (out) {
+      } else {
         load_pairs(v, sm.bc[buf].C[t], NP);
         F2 y2 = f2(skip * u, 0.f);
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) y2 = fma2(h[s], v[s], y2);
-        float y = sum2(y2);
-        if (gate) {
-          const float z = sm.z[MAP ? 0 : buf].at(t);
-          y *= z * sigmoid_fast(z);
-        }
-        sm.u[buf].set(t, y);
+        const float z = sm.z[MAP ? 0 : buf].at(t), y = sum2(y2);
+        sm.u[buf].set(t, gate ? y * (z * sigmoid_fast(z)) : y);
       }
-    };
-    if (n == kTt) {
-#pragma unroll 4
-      for (int t = 0; t < kTt; ++t) token(t);
-    } else {
-#pragma unroll 1
-      for (int t = 0; t < n; ++t) token(t);
     }
     if (more) raw.store(sm.bc[buf ^ 1]);
     if (out) {
