@@ -182,7 +182,7 @@ int validate_sscan(const gdn_sscan_desc_t* d, SscanProblem* P, bool step) {
   return GDN_OK;
 }
 
-// Segments. One CTA walks kSscanThreads channels of one segment token by token, so a call needs CTAs enough for
+// Segments. One CTA walks kSscanChans channels of one segment token by token, so a call needs CTAs enough for
 // every SM; a second segment costs the map pass, which walks all segments but the last ones again. The plan takes, of the
 // lengths that fill one, two or more rounds of resident CTAs, the one whose rounds x length (plus a CTA's fixed cost, in
 // tokens) is least, and leaves the sequences whole when that is no longer than both passes.
@@ -192,7 +192,7 @@ struct SscanPlan {
   long long segs, cks;   // segments and kept states of all sequences
 };
 constexpr int kSms = 152;
-constexpr int kFwdCtasPerSm = 5, kBwdCtasPerSm = 2;
+constexpr int kFwdCtasPerSm = 6, kBwdCtasPerSm = 2;
 constexpr int kMinSegment = 64, kCtaTokens = 16;
 constexpr double kMapCost = 0.6;  // a token of the map pass against one of the pass that writes the outputs
 

@@ -59,6 +59,11 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   F2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
@@ -147,7 +152,8 @@ cudaError_t launch_delta_step(const DeltaStepParams& p, cudaStream_t s);
 // Selective scan (k_sscan_fwd.cu, k_sscan_bwd.cu, k_step.cu).
 constexpr int kSscanMaxN = 16;     // states per channel
 constexpr int kSscanBlock = 32;    // tokens between the states a training forward keeps; segments are multiples of it
-constexpr int kSscanThreads = 128; // channels per CTA
+constexpr int kSscanChans = 128;   // channels per CTA
+constexpr int kSscanThreads = kSscanChans / 2;
 
 struct SscanParams {
   int T, D, N, G, Dg, seqs;    // Dg = D / G channels per group
@@ -175,7 +181,7 @@ struct SscanParams {
   long long rows;
 };
 // Channel blocks of all groups.
-inline int sscan_blocks(int G, int Dg) { return G * ((Dg + kSscanThreads - 1) / kSscanThreads); }
+inline int sscan_blocks(int G, int Dg) { return G * ((Dg + kSscanChans - 1) / kSscanChans); }
 cudaError_t launch_sscan_fwd(const SscanParams& p, cudaStream_t s);
 cudaError_t launch_sscan_bwd(const SscanParams& p, cudaStream_t s);
 

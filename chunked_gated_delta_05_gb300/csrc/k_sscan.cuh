@@ -1,4 +1,5 @@
-// Device pieces shared by the selective scan's forward and backward kernels.
+// Device pieces shared by the selective scan's forward and backward kernels. A thread walks two neighbouring channels, packed
+// in pairs of fp32: every multiply-add of the recurrence, of softplus and of the gate is one instruction for both.
 #pragma once
 #include "block_ops.cuh"
 
@@ -39,150 +40,192 @@ __device__ __forceinline__ SscanSeg sscan_seg(const SscanParams& p, int s) {
   return r;
 }
 
-// Channel block of the call: group, channel and whether this thread has one (the others run along on zeros).
+// Channel block of the call: its group, first channel and channels, and this thread's pair (channels the block lacks are
+// clamped: they run along on zeros and store nothing).
 struct SscanChan {
-  int g, d;
-  int d0, chans;  // the block's first channel and how many it has
-  bool live;
+  int g, d0, chans;
+  int d[2];
+  bool live[2];
 };
 __device__ __forceinline__ SscanChan sscan_chan(const SscanParams& p, int cb) {
-  const int bpg = (p.Dg + kSscanThreads - 1) / kSscanThreads;
+  const int bpg = (p.Dg + kSscanChans - 1) / kSscanChans;
   SscanChan c;
   c.g = cb / bpg;
-  const int i = (cb - c.g * bpg) * kSscanThreads + threadIdx.x;
-  c.d0 = c.g * p.Dg + (cb - c.g * bpg) * kSscanThreads;
-  c.chans = min(kSscanThreads, p.Dg - (cb - c.g * bpg) * kSscanThreads);
-  c.live = i < p.Dg;
-  c.d = c.g * p.Dg + min(i, p.Dg - 1);
+  const int first = (cb - c.g * bpg) * kSscanChans;
+  c.d0 = c.g * p.Dg + first;
+  c.chans = min(kSscanChans, p.Dg - first);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = 2 * threadIdx.x + e;
+    c.live[e] = i < c.chans;
+    c.d[e] = c.d0 + min(i, c.chans - 1);
+  }
   return c;
 }
 
-// TT tokens of B and C as fp32 in shared memory, [token][NP], zero past the segment's end and past N: every thread of
-// the CTA reads the same token's vectors (broadcasts).
+// TT tokens of B or C in shared memory, fp32 and each value twice (for both channels of a thread): [token][NP], zero past the
+// segment's end and past N. Every thread of the CTA reads the same token's vector (broadcasts).
 template <int NP, int TT>
 struct BcTile {
-  float B[TT][NP], C[TT][NP];
+  float2 v[TT][NP];
 };
 template <int NP, int TT>
 struct BcRegs {
   static constexpr int kPer = TT * NP / kSscanThreads;
-  uint16_t b[kPer], c[kPer];
-  __device__ __forceinline__ void load(const SscanParams& p, int g, long long row, int len, bool want_b, bool want_c) {
+  uint16_t r[kPer];
+  __device__ __forceinline__ void load(const __nv_bfloat16* src, long long row, int len, int N) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int e = threadIdx.x + j * kSscanThreads, t = e / NP, n = e % NP;
-      const bool in = t < len && n < p.N;
-      b[j] = in && want_b ? __ldg(reinterpret_cast<const uint16_t*>(p.Bm + (row + t) * p.b_s + g * p.N + n)) : 0;
-      c[j] = in && want_c ? __ldg(reinterpret_cast<const uint16_t*>(p.Cm + (row + t) * p.c_s + g * p.N + n)) : 0;
+      r[j] = t < len && n < N ? __ldg(reinterpret_cast<const uint16_t*>(src + t * row + n)) : uint16_t(0);
     }
   }
   __device__ __forceinline__ void store(BcTile<NP, TT>& s) const {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int e = threadIdx.x + j * kSscanThreads;
-      (&s.B[0][0])[e] = __uint_as_float(uint32_t(b[j]) << 16);
-      (&s.C[0][0])[e] = __uint_as_float(uint32_t(c[j]) << 16);
+      const float x = __uint_as_float(uint32_t(r[j]) << 16);
+      (&s.v[0][0])[threadIdx.x + j * kSscanThreads] = make_float2(x, x);
     }
   }
 };
+// States 2 i and 2 i + 1 of a token's vector.
+__device__ __forceinline__ void load_two(F2* out, const float2* src) {
+  const float4 q = *reinterpret_cast<const float4*>(src);
+  out[0] = f2(q.x, q.y);
+  out[1] = f2(q.z, q.w);
+}
 
-// TT tokens x kSscanThreads channels of a bf16 tensor in shared memory, as they are in memory, zero past the segment's
+// TT tokens x kSscanChans channels of a bf16 tensor in shared memory, as they are in memory, zero past the segment's
 // end and the group's channels. Copied in 16-byte pieces where every piece is aligned (`vec`), else by elements.
-template <int TT>
+template <int TT, int THREADS = kSscanThreads>
 struct ChTile {
-  uint16_t v[TT][kSscanThreads];
+  uint16_t v[TT][kSscanChans];
+  static constexpr int kPieces = kSscanChans / 8;
   // src: element (first token, first channel); row: elements between tokens; len tokens and chans channels exist.
   __device__ __forceinline__ void load(const __nv_bfloat16* src, long long row, int len, int chans, bool vec) {
     if (vec) {
-      constexpr int kPieces = kSscanThreads / 8;
 #pragma unroll
-      for (int j = 0; j < TT * kPieces / kSscanThreads; ++j) {
-        const int e = threadIdx.x + j * kSscanThreads, t = e / kPieces, c = e % kPieces * 8;
+      for (int j = 0; j < TT * kPieces / THREADS; ++j) {
+        const int e = threadIdx.x + j * THREADS, t = e / kPieces, c = e % kPieces * 8;
         const int bytes = t < len ? max(0, min(8, chans - c)) * 2 : 0;
         const __nv_bfloat16* from = bytes ? src + t * row + c : src;
         const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&v[t][c]));
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
       }
     } else {
-      const int c = threadIdx.x;
+      for (int c = threadIdx.x; c < kSscanChans; c += THREADS)
 #pragma unroll 8
-      for (int t = 0; t < TT; ++t)
-        v[t][c] = t < len && c < chans ? __ldg(reinterpret_cast<const uint16_t*>(src + t * row + c)) : uint16_t(0);
+        for (int t = 0; t < TT; ++t)
+          v[t][c] = t < len && c < chans ? __ldg(reinterpret_cast<const uint16_t*>(src + t * row + c)) : uint16_t(0);
     }
   }
   // Writes the tile's valid part to dst; every element must have been written to the tile before a barrier.
   __device__ __forceinline__ void store(__nv_bfloat16* dst, long long row, int len, int chans, bool vec) const {
     if (vec) {
-      constexpr int kPieces = kSscanThreads / 8;
 #pragma unroll
-      for (int j = 0; j < TT * kPieces / kSscanThreads; ++j) {
-        const int e = threadIdx.x + j * kSscanThreads, t = e / kPieces, c = e % kPieces * 8;
+      for (int j = 0; j < TT * kPieces / THREADS; ++j) {
+        const int e = threadIdx.x + j * THREADS, t = e / kPieces, c = e % kPieces * 8;
         if (t < len && c < chans) *reinterpret_cast<uint4*>(dst + t * row + c) = *reinterpret_cast<const uint4*>(&v[t][c]);
       }
     } else {
-      const int c = threadIdx.x;
-      for (int t = 0; t < TT; ++t)
-        if (t < len && c < chans) reinterpret_cast<uint16_t*>(dst)[t * row + c] = v[t][c];
+      for (int c = threadIdx.x; c < kSscanChans; c += THREADS)
+        for (int t = 0; t < TT; ++t)
+          if (t < len && c < chans) reinterpret_cast<uint16_t*>(dst)[t * row + c] = v[t][c];
     }
   }
-  __device__ __forceinline__ float at(int t) const { return __uint_as_float(uint32_t(v[t][threadIdx.x]) << 16); }
-  __device__ __forceinline__ void set(int t, float x) { v[t][threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+  // One channel of token t, and the thread's pair.
+  __device__ __forceinline__ float one(int t, int c) const { return __uint_as_float(uint32_t(v[t][c]) << 16); }
+  __device__ __forceinline__ void set_one(int t, int c, float x) { v[t][c] = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+  __device__ __forceinline__ F2 at(int t) const {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&v[t][2 * threadIdx.x]);
+    return f2(bf16_lo(u), bf16_hi(u));
+  }
+  __device__ __forceinline__ void set(int t, F2 x) {
+    float lo, hi;
+    unf2(x, &lo, &hi);
+    *reinterpret_cast<uint32_t*>(&v[t][2 * threadIdx.x]) = pack_bf16(lo, hi);
+  }
 };
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// Pair j of a token's vector.
-__device__ __forceinline__ void load_pairs(F2* out, const float* src, int np) {
-#pragma unroll
-  for (int i = 0; i < np / 4; ++i) {
-    const float4 v = reinterpret_cast<const float4*>(src)[i];
-    out[2 * i] = f2(v.x, v.y);
-    out[2 * i + 1] = f2(v.z, v.w);
+__device__ __forceinline__ F2 dup2(float x) { return f2(x, x); }
+__device__ __forceinline__ F2 select2(bool c, F2 a, F2 b) { return F2{c ? a.v : b.v}; }
+__device__ __forceinline__ F2 rcp2(F2 a) {
+  float lo, hi;
+  unf2(a, &lo, &hi);
+  return f2(rcp_approx(lo), rcp_approx(hi));
+}
+__device__ __forceinline__ F2 sigmoid2(F2 x) { return rcp2(add2(dup2(1.f), exp2_approx2(mul2(dup2(-kLog2e), x)))); }
+
+// softplus() of two values; see there.
+template <bool SLOPE>
+__device__ __forceinline__ F2 softplus2(F2 x, F2* slope) {
+  float a, b;
+  unf2(x, &a, &b);
+  const F2 e = f2(exp2_approx(-kLog2e * fabsf(a)), exp2_approx(-kLog2e * fabsf(b)));
+  const F2 s = mul2(e, rcp2(add2(e, dup2(2.f)))), s2 = mul2(s, s);
+  F2 p = fma2(s2, dup2(2.f / 13.f), dup2(2.f / 11.f));
+  p = fma2(p, s2, dup2(2.f / 9.f));
+  p = fma2(p, s2, dup2(2.f / 7.f));
+  p = fma2(p, s2, dup2(2.f / 5.f));
+  p = fma2(p, s2, dup2(2.f / 3.f));
+  p = fma2(p, s2, dup2(2.f));
+  if (SLOPE) {
+    const F2 r = rcp2(add2(e, dup2(1.f))), q = mul2(e, r);
+    float r0, r1, q0, q1;
+    unf2(r, &r0, &r1);
+    unf2(q, &q0, &q1);
+    *slope = f2(a >= 0.f ? r0 : q0, b >= 0.f ? r1 : q1);
   }
+  return fma2(s, p, f2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
 }
 
-// log2(e) A of the thread's channel, zero past N (a padded state then stays 0).
+// log2(e) A of the thread's channels, zero past N (a padded state then stays 0).
 template <int NP>
-__device__ __forceinline__ void load_A2(F2* A2, const SscanParams& p, int d) {
-  const float* a = p.A + (size_t)d * p.N;
+__device__ __forceinline__ void load_A2(F2* A2, const SscanParams& p, const SscanChan& c) {
 #pragma unroll
-  for (int i = 0; i < NP / 2; ++i)
-    A2[i] = f2(2 * i < p.N ? kLog2e * __ldg(a + 2 * i) : 0.f, 2 * i + 1 < p.N ? kLog2e * __ldg(a + 2 * i + 1) : 0.f);
+  for (int n = 0; n < NP; ++n)
+    A2[n] = n < p.N ? f2(kLog2e * __ldg(p.A + (size_t)c.d[0] * p.N + n), kLog2e * __ldg(p.A + (size_t)c.d[1] * p.N + n)) : f2(0.f, 0.f);
+}
+__device__ __forceinline__ F2 load_param(const float* v, const SscanChan& c) {
+  return v ? f2(__ldg(v + c.d[0]), __ldg(v + c.d[1])) : f2(0.f, 0.f);
+}
+__device__ __forceinline__ void store_pair(float* v, F2 x, const SscanChan& c) {
+  float lo, hi;
+  unf2(x, &lo, &hi);
+  if (c.live[0]) v[c.d[0]] = lo;
+  if (c.live[1]) v[c.d[1]] = hi;
 }
 
 // A [..][N][D] fp32 state (segment states, kept states): consecutive channels are contiguous.
 template <int NP>
-__device__ __forceinline__ void load_state(F2* h, const float* s, const SscanParams& p, int d) {
+__device__ __forceinline__ void load_state(F2* h, const float* s, const SscanParams& p, const SscanChan& c) {
 #pragma unroll
-  for (int i = 0; i < NP / 2; ++i)
-    h[i] = f2(2 * i < p.N ? s[(size_t)(2 * i) * p.D + d] : 0.f, 2 * i + 1 < p.N ? s[(size_t)(2 * i + 1) * p.D + d] : 0.f);
+  for (int n = 0; n < NP; ++n)
+    h[n] = n < p.N ? f2(s[(size_t)n * p.D + c.d[0]], s[(size_t)n * p.D + c.d[1]]) : f2(0.f, 0.f);
 }
 template <int NP>
-__device__ __forceinline__ void store_state(const F2* h, float* s, const SscanParams& p, int d) {
+__device__ __forceinline__ void store_state(const F2* h, float* s, const SscanParams& p, const SscanChan& c) {
 #pragma unroll
-  for (int i = 0; i < NP / 2; ++i) {
-    float lo, hi;
-    unf2(h[i], &lo, &hi);
-    if (2 * i < p.N) s[(size_t)(2 * i) * p.D + d] = lo;
-    if (2 * i + 1 < p.N) s[(size_t)(2 * i + 1) * p.D + d] = hi;
-  }
+  for (int n = 0; n < NP; ++n)
+    if (n < p.N) store_pair(s + (size_t)n * p.D, h[n], c);
 }
 // A caller's [..][D][N] state.
 template <int NP>
-__device__ __forceinline__ void load_user_state(F2* h, const float* s, const SscanParams& p, int d) {
-  const float* q = s + (size_t)d * p.N;
+__device__ __forceinline__ void load_user_state(F2* h, const float* s, const SscanParams& p, const SscanChan& c) {
 #pragma unroll
-  for (int i = 0; i < NP / 2; ++i) h[i] = f2(2 * i < p.N ? q[2 * i] : 0.f, 2 * i + 1 < p.N ? q[2 * i + 1] : 0.f);
+  for (int n = 0; n < NP; ++n)
+    h[n] = n < p.N ? f2(s[(size_t)c.d[0] * p.N + n], s[(size_t)c.d[1] * p.N + n]) : f2(0.f, 0.f);
 }
 template <int NP>
-__device__ __forceinline__ void store_user_state(const F2* h, float* s, const SscanParams& p, int d) {
-  float* q = s + (size_t)d * p.N;
+__device__ __forceinline__ void store_user_state(const F2* h, float* s, const SscanParams& p, const SscanChan& c) {
 #pragma unroll
-  for (int i = 0; i < NP / 2; ++i) {
+  for (int n = 0; n < NP; ++n) {
     float lo, hi;
-    unf2(h[i], &lo, &hi);
-    if (2 * i < p.N) q[2 * i] = lo;
-    if (2 * i + 1 < p.N) q[2 * i + 1] = hi;
+    unf2(h[n], &lo, &hi);
+    if (n < p.N && c.live[0]) s[(size_t)c.d[0] * p.N + n] = lo;
+    if (n < p.N && c.live[1]) s[(size_t)c.d[1] * p.N + n] = hi;
   }
 }
 

@@ -17,34 +17,33 @@ namespace {
 
 constexpr int kTile = 8;
 constexpr int kTiles = kSscanBlock / kTile;
-constexpr int kWarps = kSscanThreads / 32;
 
 constexpr int kRt = 16;  // tokens the adjoint map stages together, double-buffered
 
 template <int NP>
 struct RmapSmem {
-  BcTile<NP, kRt> bc[2];
+  BcTile<NP, kRt> C[2];
   ChTile<kRt> delta[2], dy[2], z[2];
 };
 
-// The adjoint map of a segment: from a zero exit gradient to the gradient of the state before its first token.
+// The adjoint map of a segment: from a zero exit gradient to the gradient of the state before its first token. Two channels
+// a thread, as in the forward.
 template <int NP>
-__global__ void __launch_bounds__(kSscanThreads, 5) k_sscan_rmap(SscanParams p, int blocks) {
+__global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_rmap(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   RmapSmem<NP>& sm = *reinterpret_cast<RmapSmem<NP>*>(smem_raw);
   const int seg = blockIdx.x / blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   if (sg.j == 0) return;
   const SscanChan ch = sscan_chan(p, blockIdx.x % blocks);
-  const int d = ch.d;
-  F2 A2[NP / 2], g[NP / 2];
-  load_A2<NP>(A2, p, d);
+  F2 A2[NP], g[NP];
+  load_A2<NP>(A2, p, ch);
 #pragma unroll
-  for (int i = 0; i < NP / 2; ++i) g[i] = f2(0.f, 0.f);
-  const float bias = p.bias ? __ldg(p.bias + d) : 0.f;
+  for (int n = 0; n < NP; ++n) g[n] = f2(0.f, 0.f);
+  const F2 bias = load_param(p.bias, ch);
   const bool gate = p.z != nullptr, softplus_on = p.softplus;
-  float dt_sum = 0.f;
-  BcRegs<NP, kRt> raw;
+  F2 dt_sum = f2(0.f, 0.f);
+  BcRegs<NP, kRt> rc;
   auto request = [&](int tb, int buf) {
     const long long row = sg.row0 + tb;
     const int len = sg.len - tb;
@@ -52,35 +51,36 @@ __global__ void __launch_bounds__(kSscanThreads, 5) k_sscan_rmap(SscanParams p, 
     sm.dy[buf].load(p.dy + row * p.D + ch.d0, p.D, len, ch.chans, p.vec);
     if (gate) sm.z[buf].load(p.z + row * p.z_s + ch.d0, p.z_s, len, ch.chans, p.vec);
     copies_commit();
-    raw.load(p, ch.g, row, len, false, true);
+    rc.load(p.Cm + row * p.c_s + ch.g * p.N, p.c_s, len, p.N);
   };
   const int last = (sg.len - 1) / kRt * kRt;
   request(last, 0);
-  raw.store(sm.bc[0]);
+  rc.store(sm.C[0]);
   for (int tb = last, buf = 0; tb >= 0; tb -= kRt, buf ^= 1) {
     copies_wait();
     __syncthreads();
     if (tb > 0) request(tb - kRt, buf ^ 1);
-    const int n = min(kRt, sg.len - tb);
+    const int len = min(kRt, sg.len - tb);
     // as in the forward: no branch in a token's work; past the segment's end dt and dy are 0
-#pragma unroll 4
+#pragma unroll 2
     for (int t = kRt - 1; t >= 0; --t) {
-      const float x = sm.delta[buf].at(t) + bias, dy = sm.dy[buf].at(t), z = sm.z[buf].at(t);
-      float slope, dt = softplus(x, &slope);
-      dt = t < n ? (softplus_on ? dt : x) : 0.f;
-      dt_sum += dt;
-      const float dy0 = gate ? dy * (z * sigmoid_fast(z)) : dy;
-      const F2 dt2 = f2(dt, dt), dy2 = f2(dy0, dy0);
-      F2 v[NP / 2];
-      load_pairs(v, sm.bc[buf].C[t], NP);
+      const F2 x = add2(sm.delta[buf].at(t), bias), dy = sm.dy[buf].at(t), z = sm.z[buf].at(t);
+      F2 dt = softplus2<false>(x, nullptr);
+      dt = select2(t < len, select2(softplus_on, dt, x), f2(0.f, 0.f));
+      dt_sum = add2(dt_sum, dt);
+      const F2 dy0 = select2(gate, mul2(dy, mul2(z, sigmoid2(z))), dy);
 #pragma unroll
-      for (int s = 0; s < NP / 2; ++s) g[s] = mul2(exp2_approx2(mul2(dt2, A2[s])), fma2(v[s], dy2, g[s]));
+      for (int n = 0; n < NP; n += 2) {
+        F2 c[2];
+        load_two(c, &sm.C[buf].v[t][n]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) g[n + e] = mul2(exp2_approx2(mul2(dt, A2[n + e])), fma2(c[e], dy0, g[n + e]));
+      }
     }
-    if (tb > 0) raw.store(sm.bc[buf ^ 1]);
+    if (tb > 0) rc.store(sm.C[buf ^ 1]);
   }
-  if (!ch.live) return;
-  store_state<NP>(g, p.seg_state + (size_t)seg * p.N * p.D, p, d);
-  p.seg_dt[(size_t)seg * p.D + d] = dt_sum;
+  store_state<NP>(g, p.seg_state + (size_t)seg * p.N * p.D, p, ch);
+  store_pair(p.seg_dt + (size_t)seg * p.D, dt_sum, ch);
 }
 
 // One thread per (sequence, state, channel): from the sequence's end, each segment's exit gradient.
@@ -137,24 +137,71 @@ __device__ __forceinline__ float exchange(float a, float b, bool up, int mask) {
   return (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, mask);
 }
 
+// ------------------------------------------------------------------ one channel a thread, states in pairs
+
+constexpr int kBwdThreads = kSscanChans;
+constexpr int kWarps = kBwdThreads / 32;
+
+// A block of tokens of B or C as fp32, [token][NP].
+template <int NP>
+struct VecTile {
+  float v[kSscanBlock][NP];
+  __device__ __forceinline__ void load(const __nv_bfloat16* src, long long row, int len, int N) {
+    constexpr int kPer = kSscanBlock * NP / kBwdThreads;
+    uint16_t r[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int e = threadIdx.x + j * kBwdThreads, t = e / NP, n = e % NP;
+      r[j] = t < len && n < N ? __ldg(reinterpret_cast<const uint16_t*>(src + t * row + n)) : uint16_t(0);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) (&v[0][0])[threadIdx.x + j * kBwdThreads] = __uint_as_float(uint32_t(r[j]) << 16);
+  }
+  __device__ __forceinline__ void pairs(F2* out, int t) const {
+#pragma unroll
+    for (int i = 0; i < NP / 4; ++i) {
+      const float4 q = reinterpret_cast<const float4*>(v[t])[i];
+      out[2 * i] = f2(q.x, q.y);
+      out[2 * i + 1] = f2(q.z, q.w);
+    }
+  }
+};
+
+// States of one channel, D apart (kept and segment states) or 1 apart (a caller's).
+template <int NP>
+__device__ __forceinline__ void load_states(F2* h, const float* s, size_t apart, int N) {
+#pragma unroll
+  for (int i = 0; i < NP / 2; ++i) h[i] = f2(2 * i < N ? s[2 * i * apart] : 0.f, 2 * i + 1 < N ? s[(2 * i + 1) * apart] : 0.f);
+}
+template <int NP>
+__device__ __forceinline__ void store_states(const F2* h, float* s, size_t apart, int N) {
+#pragma unroll
+  for (int i = 0; i < NP / 2; ++i) {
+    float lo, hi;
+    unf2(h[i], &lo, &hi);
+    if (2 * i < N) s[2 * i * apart] = lo;
+    if (2 * i + 1 < N) s[(2 * i + 1) * apart] = hi;
+  }
+}
+
 template <int NP>
 struct BwdSmem {
-  BcTile<NP, kSscanBlock> bc;
-  ChTile<kSscanBlock> u, delta, z, dy;                 // du, ddelta and dz replace u, delta and z token by token
-  float entry[kTiles][NP / 2][kSscanThreads][2];       // states before each tile
-  float2 dts[kTile][kSscanThreads];                    // the tile's dt and d dt / d delta
+  VecTile<NP> B, C;
+  ChTile<kSscanBlock, kBwdThreads> u, delta, z, dy;                 // du, ddelta and dz replace u, delta and z token by token
+  float entry[kTiles][NP / 2][kBwdThreads][2];       // states before each tile
+  float2 dts[kTile][kBwdThreads];                    // the tile's dt and d dt / d delta
   float red[kWarps][kSscanBlock][2][16];               // the warps' sums over their channels: dC, dB
 };
 
 template <int NP>
-__global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, int blocks) {
+__global__ void __launch_bounds__(kBwdThreads, 2) k_sscan_bwd(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   BwdSmem<NP>& sm = *reinterpret_cast<BwdSmem<NP>*>(smem_raw);
   const int seg = blockIdx.x / blocks, cb = blockIdx.x % blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   const SscanChan ch = sscan_chan(p, cb);
-  const int d = ch.d, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool gate = p.z != nullptr, softplus_on = p.softplus;
+  const int tid = threadIdx.x, d = ch.d0 + min(tid, ch.chans - 1), lane = tid & 31, warp = tid >> 5;
+  const bool gate = p.z != nullptr, softplus_on = p.softplus, live = tid < ch.chans;
   float sel[NP / 4][2];
 #pragma unroll
   for (int j = 0; j < NP / 4; ++j) {
@@ -162,12 +209,15 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
     sel[j][1] = (lane >> 2) == 2 * j + 1 ? 1.f : 0.f;
   }
   F2 A2[NP / 2], g[NP / 2], dA[NP / 2];
-  load_A2<NP>(A2, p, d);
+  load_states<NP>(A2, p.A + (size_t)d * p.N, 1, p.N);
 #pragma unroll
-  for (int i = 0; i < NP / 2; ++i) g[i] = dA[i] = f2(0.f, 0.f);
-  if (ch.live) {
-    if (p.seg_state) load_state<NP>(g, p.seg_state + (size_t)seg * p.N * p.D, p, d);
-    else if (p.dfinal) load_user_state<NP>(g, p.dfinal + (size_t)sg.seq * p.D * p.N, p, d);
+  for (int i = 0; i < NP / 2; ++i) {
+    A2[i] = mul2(A2[i], dup2(kLog2e));
+    g[i] = dA[i] = f2(0.f, 0.f);
+  }
+  if (live) {
+    if (p.seg_state) load_states<NP>(g, p.seg_state + (size_t)seg * p.N * p.D + d, p.D, p.N);
+    else if (p.dfinal) load_states<NP>(g, p.dfinal + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);
   }
   const float bias = p.bias ? __ldg(p.bias + d) : 0.f, skip = p.Dskip ? __ldg(p.Dskip + d) : 0.f;
   float dD = 0.f, dbias = 0.f;
@@ -182,12 +232,9 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
     if (gate) sm.z.load(p.z + row * p.z_s + ch.d0, p.z_s, n, ch.chans, p.vec);
     copies_commit();
     F2 h[NP / 2];
-    load_state<NP>(h, p.ck + (size_t)(sg.ck0 + b) * p.N * p.D, p, d);
-    {
-      BcRegs<NP, kSscanBlock> raw;
-      raw.load(p, ch.g, row, n, true, true);
-      raw.store(sm.bc);
-    }
+    load_states<NP>(h, p.ck + (size_t)(sg.ck0 + b) * p.N * p.D + d, p.D, p.N);
+    sm.B.load(p.Bm + row * p.b_s + ch.g * p.N, p.b_s, n, p.N);
+    sm.C.load(p.Cm + row * p.c_s + ch.g * p.N, p.c_s, n, p.N);
     copies_wait();
     __syncthreads();
     // forward over the block, leaving the states before each tile
@@ -198,13 +245,13 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
 #pragma unroll 4
       for (int i = 0; i < kTile; ++i) {
         const int t = q * kTile + i;
-        const float x = sm.delta.at(t) + bias;
+        const float x = sm.delta.one(t, tid) + bias;
         float slope, dt = softplus(x, &slope);
         dt = softplus_on ? dt : x;
-        const float dtu = dt * sm.u.at(t);
+        const float dtu = dt * sm.u.one(t, tid);
         const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
         F2 v[NP / 2];
-        load_pairs(v, sm.bc.B[t], NP);
+        sm.B.pairs(v, t);
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) h[s] = fma2(exp2_approx2(mul2(dt2, A2[s])), h[s], mul2(dtu2, v[s]));
       }
@@ -217,29 +264,29 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
 #pragma unroll
       for (int i = 0; i < kTile; ++i) {
         const int t = q * kTile + i;
-        const float x = sm.delta.at(t) + bias;
+        const float x = sm.delta.one(t, tid) + bias;
         float slope, dt = softplus(x, &slope);
         dt = t < n ? (softplus_on ? dt : x) : 0.f;
         slope = t < n ? (softplus_on ? slope : 1.f) : 0.f;
         sm.dts[i][tid] = make_float2(dt, slope);
-        const float dtu = dt * sm.u.at(t);
+        const float dtu = dt * sm.u.one(t, tid);
         const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
         F2 v[NP / 2];
-        load_pairs(v, sm.bc.B[t], NP);
+        sm.B.pairs(v, t);
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) H[i][s] = fma2(exp2_approx2(mul2(dt2, A2[s])), i ? H[i ? i - 1 : 0][s] : h[s], mul2(dtu2, v[s]));
       }
 #pragma unroll
       for (int i = kTile - 1; i >= 0; --i) {
         const int t = q * kTile + i;
-        const float u = sm.u.at(t), dy = sm.dy.at(t), z = sm.z.at(t);
+        const float u = sm.u.one(t, tid), dy = sm.dy.one(t, tid), z = sm.z.one(t, tid);
         const float2 ds = sm.dts[i][tid];
         const float dt = ds.x, dtu = dt * u, sig = sigmoid_fast(z);
         const float dy0 = gate ? dy * (z * sig) : dy;
         const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu), dy2 = f2(dy0, dy0);
         float cC[4], cB[4];
         F2 v[NP / 2], w[NP / 2];
-        load_pairs(v, sm.bc.C[t], NP);
+        sm.C.pairs(v, t);
         F2 y2 = f2(skip * u, 0.f), sB = f2(0.f, 0.f), sA = f2(0.f, 0.f);
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) {
@@ -251,7 +298,7 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) w[s] = mul2(g[s], dtu2);
         channel_sum<NP>(cB, w, sel);
-        load_pairs(v, sm.bc.B[t], NP);
+        sm.B.pairs(v, t);
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) {
           sB = fma2(g[s], v[s], sB);
@@ -264,9 +311,9 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
         const float ddt = fmaf(u, dhB, 0.6931471805599453f * sum2(sA)), dd = ddt * ds.y;
         dD = fmaf(dy0, u, dD);
         dbias += dd;
-        sm.u.set(t, fmaf(dt, dhB, skip * dy0));
-        sm.delta.set(t, dd);
-        sm.z.set(t, dy * sum2(y2) * (sig * fmaf(z, 1.f - sig, 1.f)));
+        sm.u.set_one(t, tid, fmaf(dt, dhB, skip * dy0));
+        sm.delta.set_one(t, tid, dd);
+        sm.z.set_one(t, tid, dy * sum2(y2) * (sig * fmaf(z, 1.f - sig, 1.f)));
         // the eight sums of lane 4 r + j over its four lanes, added up over r, of which each lane ends with one
         const bool r0 = lane & 4, r1 = lane & 8, r2 = lane & 16;
         const float k0 = exchange(cC[0], cB[0], r0, 4), k1 = exchange(cC[1], cB[1], r0, 4);
@@ -282,7 +329,7 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
     if (gate) sm.z.store(p.dz + row * p.D + ch.d0, p.D, n, ch.chans, p.vec_out);
     const int per = 2 * p.N;
     float* part = p.part_bc + ((size_t)cb * p.rows + row) * per;
-    for (int e = tid; e < n * per; e += kSscanThreads) {
+    for (int e = tid; e < n * per; e += kBwdThreads) {
       const int t = e / per, x = e % per, which = x / p.N, st = x - which * p.N;
       float r = 0.f;
 #pragma unroll
@@ -290,12 +337,12 @@ __global__ void __launch_bounds__(kSscanThreads, 2) k_sscan_bwd(SscanParams p, i
       part[e] = r;
     }
   }
-  if (!ch.live) return;
-  if (p.dh0 && sg.j == 0) store_user_state<NP>(g, p.dh0 + (size_t)sg.seq * p.D * p.N, p, d);
-  float* par = p.part_par + (size_t)seg * (p.N + 2) * p.D;
-  store_state<NP>(dA, par, p, d);
-  par[(size_t)p.N * p.D + d] = dD;
-  par[(size_t)(p.N + 1) * p.D + d] = dbias;
+  if (!live) return;
+  if (p.dh0 && sg.j == 0) store_states<NP>(g, p.dh0 + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);
+  float* par = p.part_par + (size_t)seg * (p.N + 2) * p.D + d;
+  store_states<NP>(dA, par, p.D, p.N);
+  par[(size_t)p.N * p.D] = dD;
+  par[(size_t)(p.N + 1) * p.D] = dbias;
 }
 
 // dC and dB of one (row, group, state): the sum over the group's channel blocks, in order.
@@ -339,7 +386,7 @@ cudaError_t run(const SscanParams& p, cudaStream_t s) {
   const int smem = int(sizeof(BwdSmem<NP>));
   cudaError_t e = cudaFuncSetAttribute(k_sscan_bwd<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k_sscan_bwd<NP><<<grid, kSscanThreads, smem, s>>>(p, blocks);
+  k_sscan_bwd<NP><<<grid, kBwdThreads, smem, s>>>(p, blocks);
   const long long n = p.rows * p.G * 2 * p.N;
   k_sscan_sum_bc<<<int((n + 255) / 256), 256, 0, s>>>(p, blocks / p.G);
   k_sscan_sum_par<<<dim3((p.D + 31) / 32, p.N + 2), dim3(32, 8), 0, s>>>(p);

@@ -1,10 +1,10 @@
 // Selective scan, forward. For every channel d with N states and every token t of a sequence,
 //   h_t = exp(dt_t A) h_{t-1} + dt_t u_t B_t,   y_t = (C_t . h_t + D u_t) silu(z_t),   dt = softplus(delta + bias).
 //
-// One thread walks one channel with its N states in registers: the sums over states stay in the thread, B and C are
+// One thread walks two channels with their N states in registers: the sums over states stay in the thread, B and C are
 // broadcast from shared memory, and u, delta, z and y are read and written once. The work per state and token is one
-// exponential and four multiply-adds (packed in pairs), which the exponential unit and the fp32 pipe bound alike:
-// about 4 cycles per warp and state on each.
+// exponential and four multiply-adds (packed for both channels), which the exponential unit and the fp32 pipe bound
+// alike: about 4 cycles per warp and state on each.
 //
 // Few channels leave the GPU empty, so the tokens are cut into segments of L. The map of a segment,
 // h_out = exp(A sum dt) h_in + F, is diagonal: a first pass runs every segment but the last from zero for F and sum dt,
@@ -19,33 +19,32 @@ constexpr int kTt = 16;  // tokens staged together, double-buffered; kSscanBlock
 
 template <int NP, bool MAP>
 struct PassSmem {
-  BcTile<NP, kTt> bc[2];
+  BcTile<NP, kTt> B[2], C[MAP ? 1 : 2];
   ChTile<kTt> delta[2], u[2], z[MAP ? 1 : 2];  // y replaces u token by token
 };
 
 template <int NP, bool MAP>
-__global__ void __launch_bounds__(kSscanThreads, 5) k_sscan_pass(SscanParams p, int blocks) {
+__global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   PassSmem<NP, MAP>& sm = *reinterpret_cast<PassSmem<NP, MAP>*>(smem_raw);
   const int seg = blockIdx.x / blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   if (MAP && sg.j == sg.nseg - 1) return;
   const SscanChan ch = sscan_chan(p, blockIdx.x % blocks);
-  const int d = ch.d;
 
-  F2 A2[NP / 2], h[NP / 2];
-  load_A2<NP>(A2, p, d);
+  F2 A2[NP], h[NP];
+  load_A2<NP>(A2, p, ch);
 #pragma unroll
-  for (int i = 0; i < NP / 2; ++i) h[i] = f2(0.f, 0.f);
+  for (int n = 0; n < NP; ++n) h[n] = f2(0.f, 0.f);
   if (!MAP) {
-    if (p.seg_state) load_state<NP>(h, p.seg_state + (size_t)seg * p.N * p.D, p, d);
-    else if (p.h0) load_user_state<NP>(h, p.h0 + (size_t)sg.seq * p.D * p.N, p, d);
+    if (p.seg_state) load_state<NP>(h, p.seg_state + (size_t)seg * p.N * p.D, p, ch);
+    else if (p.h0) load_user_state<NP>(h, p.h0 + (size_t)sg.seq * p.D * p.N, p, ch);
   }
-  const float bias = p.bias ? __ldg(p.bias + d) : 0.f, skip = !MAP && p.Dskip ? __ldg(p.Dskip + d) : 0.f;
+  const F2 bias = load_param(p.bias, ch), skip = load_param(MAP ? nullptr : p.Dskip, ch);
   const bool out = !MAP && p.y, gate = out && p.z, softplus_on = p.softplus;
-  float dt_sum = 0.f;
+  F2 dt_sum = f2(0.f, 0.f);
 
-  BcRegs<NP, kTt> raw;
+  BcRegs<NP, kTt> rb, rc;
   auto request = [&](int tb, int buf) {
     const long long row = sg.row0 + tb;
     const int len = sg.len - tb;
@@ -53,54 +52,60 @@ __global__ void __launch_bounds__(kSscanThreads, 5) k_sscan_pass(SscanParams p, 
     sm.u[buf].load(p.u + row * p.u_s + ch.d0, p.u_s, len, ch.chans, p.vec);
     if (!MAP && gate) sm.z[buf].load(p.z + row * p.z_s + ch.d0, p.z_s, len, ch.chans, p.vec);
     copies_commit();
-    raw.load(p, ch.g, row, len, true, out);
+    rb.load(p.Bm + row * p.b_s + ch.g * p.N, p.b_s, len, p.N);
+    if (!MAP) rc.load(p.Cm + row * p.c_s + ch.g * p.N, p.c_s, len, p.N);
+  };
+  auto arrive = [&](int buf) {
+    rb.store(sm.B[buf]);
+    if (!MAP) rc.store(sm.C[buf]);
   };
   request(0, 0);
-  raw.store(sm.bc[0]);
+  arrive(0);
   for (int tb = 0, buf = 0; tb < sg.len; tb += kTt, buf ^= 1) {
     copies_wait();
     __syncthreads();
     const bool more = tb + kTt < sg.len;
     if (more) request(tb + kTt, buf ^ 1);
-    if (!MAP && p.ck && tb % kSscanBlock == 0 && ch.live)
-      store_state<NP>(h, p.ck + (size_t)(sg.ck0 + tb / kSscanBlock) * p.N * p.D, p, d);
-    const int n = min(kTt, sg.len - tb);
+    if (!MAP && p.ck && tb % kSscanBlock == 0) store_state<NP>(h, p.ck + (size_t)(sg.ck0 + tb / kSscanBlock) * p.N * p.D, p, ch);
+    const int len = min(kTt, sg.len - tb);
     // no branch in a token's work, so that the compiler can overlap several tokens: past the segment's end dt = 0, which
     // leaves the state as it is, and without softplus or gate their results are not selected
-#pragma unroll 4
+#pragma unroll 2
     for (int t = 0; t < kTt; ++t) {
-      const float x = sm.delta[buf].at(t) + bias, u = sm.u[buf].at(t);
-      float slope, dt = softplus(x, &slope);
-      dt = t < n ? (softplus_on ? dt : x) : 0.f;
-      const float dtu = dt * u;
-      const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
-      F2 v[NP / 2];
-      load_pairs(v, sm.bc[buf].B[t], NP);
+      const F2 x = add2(sm.delta[buf].at(t), bias), u = sm.u[buf].at(t);
+      F2 dt = softplus2<false>(x, nullptr);
+      dt = select2(t < len, select2(softplus_on, dt, x), f2(0.f, 0.f));
+      const F2 dtu = mul2(dt, u);
+      F2 y = mul2(skip, u);
 #pragma unroll
-      for (int s = 0; s < NP / 2; ++s) h[s] = fma2(exp2_approx2(mul2(dt2, A2[s])), h[s], mul2(dtu2, v[s]));
+      for (int n = 0; n < NP; n += 2) {
+        F2 b[2], c[2];
+        load_two(b, &sm.B[buf].v[t][n]);
+        if (!MAP) load_two(c, &sm.C[buf].v[t][n]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          h[n + e] = fma2(exp2_approx2(mul2(dt, A2[n + e])), h[n + e], mul2(dtu, b[e]));
+          if (!MAP) y = fma2(h[n + e], c[e], y);
+        }
+      }
       if (MAP) {
-        dt_sum += dt;
+        dt_sum = add2(dt_sum, dt);
       } else {
-        load_pairs(v, sm.bc[buf].C[t], NP);
-        F2 y2 = f2(skip * u, 0.f);
-#pragma unroll
-        for (int s = 0; s < NP / 2; ++s) y2 = fma2(h[s], v[s], y2);
-        const float z = sm.z[MAP ? 0 : buf].at(t), y = sum2(y2);
-        sm.u[buf].set(t, gate ? y * (z * sigmoid_fast(z)) : y);
+        const F2 z = sm.z[MAP ? 0 : buf].at(t);
+        sm.u[buf].set(t, select2(gate, mul2(y, mul2(z, sigmoid2(z))), y));
       }
     }
-    if (more) raw.store(sm.bc[buf ^ 1]);
+    if (more) arrive(buf ^ 1);
     if (out) {
       __syncthreads();
-      sm.u[buf].store(p.y + (sg.row0 + tb) * p.D + ch.d0, p.D, n, ch.chans, p.vec_out);
+      sm.u[buf].store(p.y + (sg.row0 + tb) * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
     }
   }
-  if (!ch.live) return;
   if (MAP) {
-    store_state<NP>(h, p.seg_state + (size_t)seg * p.N * p.D, p, d);
-    p.seg_dt[(size_t)seg * p.D + d] = dt_sum;
+    store_state<NP>(h, p.seg_state + (size_t)seg * p.N * p.D, p, ch);
+    store_pair(p.seg_dt + (size_t)seg * p.D, dt_sum, ch);
   } else if (p.final_state && sg.j == sg.nseg - 1) {
-    store_user_state<NP>(h, p.final_state + (size_t)sg.seq * p.D * p.N, p, d);
+    store_user_state<NP>(h, p.final_state + (size_t)sg.seq * p.D * p.N, p, ch);
   }
 }
 
