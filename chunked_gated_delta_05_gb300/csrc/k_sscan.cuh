@@ -1,5 +1,6 @@
-// Device pieces shared by the selective scan's forward and backward kernels. A thread walks two neighbouring channels, packed
-// in pairs of fp32: every multiply-add of the recurrence, of softplus and of the gate is one instruction for both.
+// Device pieces shared by the selective scan's forward and backward kernels. A thread walks two neighbouring channels, each
+// state pair packed in one 64-bit register pair: a token's B and C come out of shared memory once for both channels, four
+// bytes a state, which matters because shared memory returns 128 bytes a cycle to an SM whether lanes share them or not.
 #pragma once
 #include "block_ops.cuh"
 
@@ -63,11 +64,17 @@ __device__ __forceinline__ SscanChan sscan_chan(const SscanParams& p, int cb) {
   return c;
 }
 
-// TT tokens of B or C in shared memory, fp32 and each value twice (for both channels of a thread): [token][NP], zero past the
-// segment's end and past N. Every thread of the CTA reads the same token's vector (broadcasts).
+// TT tokens of B or C as fp32 in shared memory, [token][NP], zero past the segment's end and past N. Every thread of the CTA
+// reads the same token's vector.
 template <int NP, int TT>
 struct BcTile {
-  float2 v[TT][NP];
+  float v[TT][NP];
+  // States 4 i .. 4 i + 3 of token t as two pairs.
+  __device__ __forceinline__ void quad(F2* out, int t, int i) const {
+    const float4 q = reinterpret_cast<const float4*>(v[t])[i];
+    out[0] = f2(q.x, q.y);
+    out[1] = f2(q.z, q.w);
+  }
 };
 template <int NP, int TT>
 struct BcRegs {
@@ -83,18 +90,10 @@ struct BcRegs {
   __device__ __forceinline__ void store(BcTile<NP, TT>& s) const {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const float x = __uint_as_float(uint32_t(r[j]) << 16);
-      (&s.v[0][0])[threadIdx.x + j * kSscanThreads] = make_float2(x, x);
+      (&s.v[0][0])[threadIdx.x + j * kSscanThreads] = __uint_as_float(uint32_t(r[j]) << 16);
     }
   }
 };
-// States 2 i and 2 i + 1 of a token's vector.
-__device__ __forceinline__ void load_two(F2* out, const float2* src) {
-  const float4 q = *reinterpret_cast<const float4*>(src);
-  out[0] = f2(q.x, q.y);
-  out[1] = f2(q.z, q.w);
-}
-
 // TT tokens x kSscanChans channels of a bf16 tensor in shared memory, as they are in memory, zero past the segment's
 // end and the group's channels. Copied in 16-byte pieces where every piece is aligned (`vec`), else by elements.
 template <int TT, int THREADS = kSscanThreads>
@@ -136,97 +135,41 @@ struct ChTile {
   // One channel of token t, and the thread's pair.
   __device__ __forceinline__ float one(int t, int c) const { return __uint_as_float(uint32_t(v[t][c]) << 16); }
   __device__ __forceinline__ void set_one(int t, int c, float x) { v[t][c] = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
-  __device__ __forceinline__ F2 at(int t) const {
+  __device__ __forceinline__ float2 at(int t) const {
     const uint32_t u = *reinterpret_cast<const uint32_t*>(&v[t][2 * threadIdx.x]);
-    return f2(bf16_lo(u), bf16_hi(u));
+    return make_float2(bf16_lo(u), bf16_hi(u));
   }
-  __device__ __forceinline__ void set(int t, F2 x) {
-    float lo, hi;
-    unf2(x, &lo, &hi);
-    *reinterpret_cast<uint32_t*>(&v[t][2 * threadIdx.x]) = pack_bf16(lo, hi);
-  }
+  __device__ __forceinline__ void set(int t, float a, float b) { *reinterpret_cast<uint32_t*>(&v[t][2 * threadIdx.x]) = pack_bf16(a, b); }
 };
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ F2 dup2(float x) { return f2(x, x); }
-__device__ __forceinline__ F2 select2(bool c, F2 a, F2 b) { return F2{c ? a.v : b.v}; }
-__device__ __forceinline__ F2 rcp2(F2 a) {
-  float lo, hi;
-  unf2(a, &lo, &hi);
-  return f2(rcp_approx(lo), rcp_approx(hi));
-}
-__device__ __forceinline__ F2 sigmoid2(F2 x) { return rcp2(add2(dup2(1.f), exp2_approx2(mul2(dup2(-kLog2e), x)))); }
 
-// softplus() of two values; see there.
-template <bool SLOPE>
-__device__ __forceinline__ F2 softplus2(F2 x, F2* slope) {
-  float a, b;
-  unf2(x, &a, &b);
-  const F2 e = f2(exp2_approx(-kLog2e * fabsf(a)), exp2_approx(-kLog2e * fabsf(b)));
-  const F2 s = mul2(e, rcp2(add2(e, dup2(2.f)))), s2 = mul2(s, s);
-  F2 p = fma2(s2, dup2(2.f / 13.f), dup2(2.f / 11.f));
-  p = fma2(p, s2, dup2(2.f / 9.f));
-  p = fma2(p, s2, dup2(2.f / 7.f));
-  p = fma2(p, s2, dup2(2.f / 5.f));
-  p = fma2(p, s2, dup2(2.f / 3.f));
-  p = fma2(p, s2, dup2(2.f));
-  if (SLOPE) {
-    const F2 r = rcp2(add2(e, dup2(1.f))), q = mul2(e, r);
-    float r0, r1, q0, q1;
-    unf2(r, &r0, &r1);
-    unf2(q, &q0, &q1);
-    *slope = f2(a >= 0.f ? r0 : q0, b >= 0.f ? r1 : q1);
-  }
-  return fma2(s, p, f2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
-}
-
-// log2(e) A of the thread's channels, zero past N (a padded state then stays 0).
+// The state pairs of one channel, `apart` elements between states: the channels' own layout ([..][N][D], segment and kept
+// states) or a caller's ([..][D][N]). Zero past N.
 template <int NP>
-__device__ __forceinline__ void load_A2(F2* A2, const SscanParams& p, const SscanChan& c) {
+__device__ __forceinline__ void load_states(F2* h, const float* s, size_t apart, int N) {
 #pragma unroll
-  for (int n = 0; n < NP; ++n)
-    A2[n] = n < p.N ? f2(kLog2e * __ldg(p.A + (size_t)c.d[0] * p.N + n), kLog2e * __ldg(p.A + (size_t)c.d[1] * p.N + n)) : f2(0.f, 0.f);
-}
-__device__ __forceinline__ F2 load_param(const float* v, const SscanChan& c) {
-  return v ? f2(__ldg(v + c.d[0]), __ldg(v + c.d[1])) : f2(0.f, 0.f);
-}
-__device__ __forceinline__ void store_pair(float* v, F2 x, const SscanChan& c) {
-  float lo, hi;
-  unf2(x, &lo, &hi);
-  if (c.live[0]) v[c.d[0]] = lo;
-  if (c.live[1]) v[c.d[1]] = hi;
-}
-
-// A [..][N][D] fp32 state (segment states, kept states): consecutive channels are contiguous.
-template <int NP>
-__device__ __forceinline__ void load_state(F2* h, const float* s, const SscanParams& p, const SscanChan& c) {
-#pragma unroll
-  for (int n = 0; n < NP; ++n)
-    h[n] = n < p.N ? f2(s[(size_t)n * p.D + c.d[0]], s[(size_t)n * p.D + c.d[1]]) : f2(0.f, 0.f);
+  for (int i = 0; i < NP / 2; ++i) h[i] = f2(2 * i < N ? s[2 * i * apart] : 0.f, 2 * i + 1 < N ? s[(2 * i + 1) * apart] : 0.f);
 }
 template <int NP>
-__device__ __forceinline__ void store_state(const F2* h, float* s, const SscanParams& p, const SscanChan& c) {
+__device__ __forceinline__ void store_states(const F2* h, float* s, size_t apart, int N) {
 #pragma unroll
-  for (int n = 0; n < NP; ++n)
-    if (n < p.N) store_pair(s + (size_t)n * p.D, h[n], c);
-}
-// A caller's [..][D][N] state.
-template <int NP>
-__device__ __forceinline__ void load_user_state(F2* h, const float* s, const SscanParams& p, const SscanChan& c) {
-#pragma unroll
-  for (int n = 0; n < NP; ++n)
-    h[n] = n < p.N ? f2(s[(size_t)c.d[0] * p.N + n], s[(size_t)c.d[1] * p.N + n]) : f2(0.f, 0.f);
-}
-template <int NP>
-__device__ __forceinline__ void store_user_state(const F2* h, float* s, const SscanParams& p, const SscanChan& c) {
-#pragma unroll
-  for (int n = 0; n < NP; ++n) {
+  for (int i = 0; i < NP / 2; ++i) {
     float lo, hi;
-    unf2(h[n], &lo, &hi);
-    if (n < p.N && c.live[0]) s[(size_t)c.d[0] * p.N + n] = lo;
-    if (n < p.N && c.live[1]) s[(size_t)c.d[1] * p.N + n] = hi;
+    unf2(h[i], &lo, &hi);
+    if (2 * i < N) s[2 * i * apart] = lo;
+    if (2 * i + 1 < N) s[(2 * i + 1) * apart] = hi;
   }
 }
+// log2(e) A of one channel (a padded state then stays 0).
+template <int NP>
+__device__ __forceinline__ void load_A2(F2* A2, const SscanParams& p, int d) {
+  load_states<NP>(A2, p.A + (size_t)d * p.N, 1, p.N);
+#pragma unroll
+  for (int i = 0; i < NP / 2; ++i) A2[i] = mul2(A2[i], dup2(kLog2e));
+}
+__device__ __forceinline__ float param(const float* v, int d) { return v ? __ldg(v + d) : 0.f; }
 
 }  // namespace gdn

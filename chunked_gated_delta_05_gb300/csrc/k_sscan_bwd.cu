@@ -18,6 +18,7 @@ namespace {
 constexpr int kTile = 8;
 constexpr int kTiles = kSscanBlock / kTile;
 
+constexpr int kRGroup = 4;
 constexpr int kRt = 16;  // tokens the adjoint map stages together, double-buffered
 
 template <int NP>
@@ -29,20 +30,23 @@ struct RmapSmem {
 // The adjoint map of a segment: from a zero exit gradient to the gradient of the state before its first token. Two channels
 // a thread, as in the forward.
 template <int NP>
-__global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_rmap(SscanParams p, int blocks) {
+__global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   RmapSmem<NP>& sm = *reinterpret_cast<RmapSmem<NP>*>(smem_raw);
   const int seg = blockIdx.x / blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   if (sg.j == 0) return;
   const SscanChan ch = sscan_chan(p, blockIdx.x % blocks);
-  F2 A2[NP], g[NP];
-  load_A2<NP>(A2, p, ch);
+  F2 A2[2][NP / 2], g[2][NP / 2];
+  float bias[2], dt_sum[2] = {0.f, 0.f};
 #pragma unroll
-  for (int n = 0; n < NP; ++n) g[n] = f2(0.f, 0.f);
-  const F2 bias = load_param(p.bias, ch);
+  for (int e = 0; e < 2; ++e) {
+    load_A2<NP>(A2[e], p, ch.d[e]);
+#pragma unroll
+    for (int i = 0; i < NP / 2; ++i) g[e][i] = f2(0.f, 0.f);
+    bias[e] = param(p.bias, ch.d[e]);
+  }
   const bool gate = p.z != nullptr, softplus_on = p.softplus;
-  F2 dt_sum = f2(0.f, 0.f);
   BcRegs<NP, kRt> rc;
   auto request = [&](int tb, int buf) {
     const long long row = sg.row0 + tb;
@@ -61,26 +65,45 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_rmap(SscanParams p, 
     __syncthreads();
     if (tb > 0) request(tb - kRt, buf ^ 1);
     const int len = min(kRt, sg.len - tb);
-    // as in the forward: no branch in a token's work; past the segment's end dt and dy are 0
-#pragma unroll 2
-    for (int t = kRt - 1; t >= 0; --t) {
-      const F2 x = add2(sm.delta[buf].at(t), bias), dy = sm.dy[buf].at(t), z = sm.z[buf].at(t);
-      F2 dt = softplus2<false>(x, nullptr);
-      dt = select2(t < len, select2(softplus_on, dt, x), f2(0.f, 0.f));
-      dt_sum = add2(dt_sum, dt);
-      const F2 dy0 = select2(gate, mul2(dy, mul2(z, sigmoid2(z))), dy);
+    // as in the forward: tokens in groups, no branch in a token's work; past the segment's end dt and dy are 0
+#pragma unroll 1
+    for (int t0 = kRt - kRGroup; t0 >= 0; t0 -= kRGroup) {
+      float dt[kRGroup][2], dy0[kRGroup][2];
 #pragma unroll
-      for (int n = 0; n < NP; n += 2) {
-        F2 c[2];
-        load_two(c, &sm.C[buf].v[t][n]);
+      for (int i = 0; i < kRGroup; ++i) {
+        const float2 dr = sm.delta[buf].at(t0 + i), yr = sm.dy[buf].at(t0 + i), zr = sm.z[buf].at(t0 + i);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) g[n + e] = mul2(exp2_approx2(mul2(dt, A2[n + e])), fma2(c[e], dy0, g[n + e]));
+        for (int e = 0; e < 2; ++e) {
+          const float x = (e ? dr.y : dr.x) + bias[e], dy = e ? yr.y : yr.x, z = e ? zr.y : zr.x;
+          float slope;
+          const float sp = softplus(x, &slope);
+          dt[i][e] = t0 + i < len ? (softplus_on ? sp : x) : 0.f;
+          dt_sum[e] += dt[i][e];
+          dy0[i][e] = gate ? dy * (z * sigmoid_fast(z)) : dy;
+        }
+      }
+#pragma unroll
+      for (int i = kRGroup - 1; i >= 0; --i) {
+        const F2 dt2[2] = {dup2(dt[i][0]), dup2(dt[i][1])}, dy2[2] = {dup2(dy0[i][0]), dup2(dy0[i][1])};
+#pragma unroll
+        for (int s = 0; s < NP / 2; s += 2) {
+          F2 c[2];
+          sm.C[buf].quad(c, t0 + i, s / 2);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) g[e][s + k] = mul2(exp2_approx2(mul2(dt2[e], A2[e][s + k])), fma2(c[k], dy2[e], g[e][s + k]));
+        }
       }
     }
     if (tb > 0) rc.store(sm.C[buf ^ 1]);
   }
-  store_state<NP>(g, p.seg_state + (size_t)seg * p.N * p.D, p, ch);
-  store_pair(p.seg_dt + (size_t)seg * p.D, dt_sum, ch);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (!ch.live[e]) continue;
+    store_states<NP>(g[e], p.seg_state + (size_t)seg * p.N * p.D + ch.d[e], p.D, p.N);
+    p.seg_dt[(size_t)seg * p.D + ch.d[e]] = dt_sum[e];
+  }
 }
 
 // One thread per (sequence, state, channel): from the sequence's end, each segment's exit gradient.
@@ -167,23 +190,6 @@ struct VecTile {
   }
 };
 
-// States of one channel, D apart (kept and segment states) or 1 apart (a caller's).
-template <int NP>
-__device__ __forceinline__ void load_states(F2* h, const float* s, size_t apart, int N) {
-#pragma unroll
-  for (int i = 0; i < NP / 2; ++i) h[i] = f2(2 * i < N ? s[2 * i * apart] : 0.f, 2 * i + 1 < N ? s[(2 * i + 1) * apart] : 0.f);
-}
-template <int NP>
-__device__ __forceinline__ void store_states(const F2* h, float* s, size_t apart, int N) {
-#pragma unroll
-  for (int i = 0; i < NP / 2; ++i) {
-    float lo, hi;
-    unf2(h[i], &lo, &hi);
-    if (2 * i < N) s[2 * i * apart] = lo;
-    if (2 * i + 1 < N) s[(2 * i + 1) * apart] = hi;
-  }
-}
-
 template <int NP>
 struct BwdSmem {
   VecTile<NP> B, C;
@@ -209,12 +215,9 @@ __global__ void __launch_bounds__(kBwdThreads, 2) k_sscan_bwd(SscanParams p, int
     sel[j][1] = (lane >> 2) == 2 * j + 1 ? 1.f : 0.f;
   }
   F2 A2[NP / 2], g[NP / 2], dA[NP / 2];
-  load_states<NP>(A2, p.A + (size_t)d * p.N, 1, p.N);
+  load_A2<NP>(A2, p, d);
 #pragma unroll
-  for (int i = 0; i < NP / 2; ++i) {
-    A2[i] = mul2(A2[i], dup2(kLog2e));
-    g[i] = dA[i] = f2(0.f, 0.f);
-  }
+  for (int i = 0; i < NP / 2; ++i) g[i] = dA[i] = f2(0.f, 0.f);
   if (live) {
     if (p.seg_state) load_states<NP>(g, p.seg_state + (size_t)seg * p.N * p.D + d, p.D, p.N);
     else if (p.dfinal) load_states<NP>(g, p.dfinal + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);

@@ -3,7 +3,7 @@
 //
 // One thread walks two channels with their N states in registers: the sums over states stay in the thread, B and C are
 // broadcast from shared memory, and u, delta, z and y are read and written once. The work per state and token is one
-// exponential and four multiply-adds (packed for both channels), which the exponential unit and the fp32 pipe bound
+// exponential and four multiply-adds (packed in state pairs), which the exponential unit and the fp32 pipe bound
 // alike: about 4 cycles per warp and state on each.
 //
 // Few channels leave the GPU empty, so the tokens are cut into segments of L. The map of a segment,
@@ -15,6 +15,7 @@
 namespace gdn {
 namespace {
 
+constexpr int kGroup = 4;
 constexpr int kTt = 16;  // tokens staged together, double-buffered; kSscanBlock is a multiple of it
 
 template <int NP, bool MAP>
@@ -24,7 +25,7 @@ struct PassSmem {
 };
 
 template <int NP, bool MAP>
-__global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, int blocks) {
+__global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_pass(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   PassSmem<NP, MAP>& sm = *reinterpret_cast<PassSmem<NP, MAP>*>(smem_raw);
   const int seg = blockIdx.x / blocks;
@@ -32,17 +33,22 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
   if (MAP && sg.j == sg.nseg - 1) return;
   const SscanChan ch = sscan_chan(p, blockIdx.x % blocks);
 
-  F2 A2[NP], h[NP];
-  load_A2<NP>(A2, p, ch);
+  F2 A2[2][NP / 2], h[2][NP / 2];
+  float bias[2], skip[2], dt_sum[2] = {0.f, 0.f};
 #pragma unroll
-  for (int n = 0; n < NP; ++n) h[n] = f2(0.f, 0.f);
-  if (!MAP) {
-    if (p.seg_state) load_state<NP>(h, p.seg_state + (size_t)seg * p.N * p.D, p, ch);
-    else if (p.h0) load_user_state<NP>(h, p.h0 + (size_t)sg.seq * p.D * p.N, p, ch);
+  for (int e = 0; e < 2; ++e) {
+    const int d = ch.d[e];
+    load_A2<NP>(A2[e], p, d);
+#pragma unroll
+    for (int i = 0; i < NP / 2; ++i) h[e][i] = f2(0.f, 0.f);
+    if (!MAP) {
+      if (p.seg_state) load_states<NP>(h[e], p.seg_state + (size_t)seg * p.N * p.D + d, p.D, p.N);
+      else if (p.h0) load_states<NP>(h[e], p.h0 + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);
+    }
+    bias[e] = param(p.bias, d);
+    skip[e] = param(MAP ? nullptr : p.Dskip, d);
   }
-  const F2 bias = load_param(p.bias, ch), skip = load_param(MAP ? nullptr : p.Dskip, ch);
   const bool out = !MAP && p.y, gate = out && p.z, softplus_on = p.softplus;
-  F2 dt_sum = f2(0.f, 0.f);
 
   BcRegs<NP, kTt> rb, rc;
   auto request = [&](int tb, int buf) {
@@ -66,33 +72,59 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
     __syncthreads();
     const bool more = tb + kTt < sg.len;
     if (more) request(tb + kTt, buf ^ 1);
-    if (!MAP && p.ck && tb % kSscanBlock == 0) store_state<NP>(h, p.ck + (size_t)(sg.ck0 + tb / kSscanBlock) * p.N * p.D, p, ch);
-    const int len = min(kTt, sg.len - tb);
-    // no branch in a token's work, so that the compiler can overlap several tokens: past the segment's end dt = 0, which
-    // leaves the state as it is, and without softplus or gate their results are not selected
-#pragma unroll 2
-    for (int t = 0; t < kTt; ++t) {
-      const F2 x = add2(sm.delta[buf].at(t), bias), u = sm.u[buf].at(t);
-      F2 dt = softplus2<false>(x, nullptr);
-      dt = select2(t < len, select2(softplus_on, dt, x), f2(0.f, 0.f));
-      const F2 dtu = mul2(dt, u);
-      F2 y = mul2(skip, u);
+    if (!MAP && p.ck && tb % kSscanBlock == 0) {
 #pragma unroll
-      for (int n = 0; n < NP; n += 2) {
-        F2 b[2], c[2];
-        load_two(b, &sm.B[buf].v[t][n]);
-        if (!MAP) load_two(c, &sm.C[buf].v[t][n]);
+      for (int e = 0; e < 2; ++e)
+        if (ch.live[e]) store_states<NP>(h[e], p.ck + (size_t)(sg.ck0 + tb / kSscanBlock) * p.N * p.D + ch.d[e], p.D, p.N);
+    }
+    const int len = min(kTt, sg.len - tb);
+    // Tokens go in groups, whose step sizes and gates (long dependent chains) are computed side by side before and after the
+    // states. No branch in a token's work: past the segment's end dt = 0, which leaves the state as it is, and without
+    // softplus or gate their results are not selected.
+#pragma unroll 1
+    for (int t0 = 0; t0 < kTt; t0 += kGroup) {
+      float dt[kGroup][2], dtu[kGroup][2], y[kGroup][2];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        const float2 dr = sm.delta[buf].at(t0 + i), ur = sm.u[buf].at(t0 + i);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          h[n + e] = fma2(exp2_approx2(mul2(dt, A2[n + e])), h[n + e], mul2(dtu, b[e]));
-          if (!MAP) y = fma2(h[n + e], c[e], y);
+          const float x = (e ? dr.y : dr.x) + bias[e], u = e ? ur.y : ur.x;
+          float slope;
+          const float sp = softplus(x, &slope);
+          dt[i][e] = t0 + i < len ? (softplus_on ? sp : x) : 0.f;
+          dtu[i][e] = dt[i][e] * u;
+          if (MAP) dt_sum[e] += dt[i][e];
+          else y[i][e] = skip[e] * u;
         }
       }
-      if (MAP) {
-        dt_sum = add2(dt_sum, dt);
-      } else {
-        const F2 z = sm.z[MAP ? 0 : buf].at(t);
-        sm.u[buf].set(t, select2(gate, mul2(y, mul2(z, sigmoid2(z))), y));
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        F2 y2[2] = {f2(y[i][0], 0.f), f2(y[i][1], 0.f)};
+        const F2 dt2[2] = {dup2(dt[i][0]), dup2(dt[i][1])}, dtu2[2] = {dup2(dtu[i][0]), dup2(dtu[i][1])};
+#pragma unroll
+        for (int s = 0; s < NP / 2; s += 2) {
+          F2 b[2], c[2];
+          sm.B[buf].quad(b, t0 + i, s / 2);
+          if (!MAP) sm.C[buf].quad(c, t0 + i, s / 2);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              h[e][s + k] = fma2(exp2_approx2(mul2(dt2[e], A2[e][s + k])), h[e][s + k], mul2(dtu2[e], b[k]));
+              if (!MAP) y2[e] = fma2(h[e][s + k], c[k], y2[e]);
+            }
+        }
+        y[i][0] = sum2(y2[0]);
+        y[i][1] = sum2(y2[1]);
+      }
+      if (!MAP) {
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          const float2 z = sm.z[MAP ? 0 : buf].at(t0 + i);
+          const float a = y[i][0] * (z.x * sigmoid_fast(z.x)), b = y[i][1] * (z.y * sigmoid_fast(z.y));
+          sm.u[buf].set(t0 + i, gate ? a : y[i][0], gate ? b : y[i][1]);
+        }
       }
     }
     if (more) arrive(buf ^ 1);
@@ -101,11 +133,16 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
       sm.u[buf].store(p.y + (sg.row0 + tb) * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
     }
   }
-  if (MAP) {
-    store_state<NP>(h, p.seg_state + (size_t)seg * p.N * p.D, p, ch);
-    store_pair(p.seg_dt + (size_t)seg * p.D, dt_sum, ch);
-  } else if (p.final_state && sg.j == sg.nseg - 1) {
-    store_user_state<NP>(h, p.final_state + (size_t)sg.seq * p.D * p.N, p, ch);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (!ch.live[e]) continue;
+    const int d = ch.d[e];
+    if (MAP) {
+      store_states<NP>(h[e], p.seg_state + (size_t)seg * p.N * p.D + d, p.D, p.N);
+      p.seg_dt[(size_t)seg * p.D + d] = dt_sum[e];
+    } else if (p.final_state && sg.j == sg.nseg - 1) {
+      store_states<NP>(h[e], p.final_state + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);
+    }
   }
 }
 
