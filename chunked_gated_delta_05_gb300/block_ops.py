@@ -443,7 +443,7 @@ def selective_scan_step(state, u, delta, A, B, C, *, D=None, z=None, delta_bias=
 
 
 class SelectiveScan(torch.autograd.Function):
-    """Autograd wrapper of the selective scan: the forward keeps a state every 32 tokens, the backward starts from them."""
+    """Autograd wrapper of the selective scan: the forward keeps a state every 8 tokens, the backward starts from them."""
 
     @staticmethod
     def forward(ctx, u, delta, A, B, C, D, z, delta_bias, initial_state, delta_softplus, output_final_state, cu_seqlens):

@@ -182,19 +182,24 @@ int validate_sscan(const gdn_sscan_desc_t* d, SscanProblem* P, bool step) {
   return GDN_OK;
 }
 
-// Segments. One CTA walks kSscanChans channels of one segment token by token, so a call needs CTAs enough for
-// every SM; a second segment costs the map pass, which walks all segments but the last ones again. The plan takes, of the
-// lengths that fill one, two or more rounds of resident CTAs, the one whose rounds x length (plus a CTA's fixed cost, in
-// tokens) is least, and leaves the sequences whole when that is no longer than both passes.
+// Segments. One CTA walks kSscanChans channels of one segment token by token, so a call needs CTAs enough for every SM;
+// cutting the sequences costs the map pass, which walks all segments but the last ones again. The times compared are in
+// steps of one CTA among others on its SM: whole sequences take the longest one's steps, at `alone` each while the SM has
+// few CTAs, or one CTA after the other when there are more; cut ones take all steps and the map's, evenly spread. Measured
+// at 8192 tokens x 4096 channels (forward): segments of 96, 128, 224, 320 tokens 294, 289, 296, 299 us; backward at 4093
+// packed tokens x 2048 channels, segments of 64, 128, 256: 252, 255, 266 us.
 struct SscanPlan {
-  int L;                 // tokens per segment, a multiple of kSscanBlock
+  int L;                 // tokens per segment, a multiple of kSscanCut
   int most;              // most segments of a sequence
   long long segs, cks;   // segments and kept states of all sequences
 };
 constexpr int kSms = 152;
-constexpr int kFwdCtasPerSm = 6, kBwdCtasPerSm = 2;
-constexpr int kMinSegment = 64, kCtaTokens = 16;
-constexpr double kMapCost = 0.6;  // a token of the map pass against one of the pass that writes the outputs
+constexpr int kMinSegment = 64;
+struct SscanCost {
+  int ctas;              // CTAs of all rounds per SM that the segments are cut for
+  double alone, map;     // a step of a CTA alone on its SM, and of the map pass
+};
+constexpr SscanCost kFwdCost = {14, 2.4, 0.7}, kBwdCost = {8, 1.5, 0.3};
 
 long long count_segments(const SscanProblem& P, long long L) {
   if (!P.cu) return (P.T + L - 1) / L * P.seqs;
@@ -204,30 +209,24 @@ long long count_segments(const SscanProblem& P, long long L) {
 }
 
 SscanPlan plan_sscan(const SscanProblem& P, bool backward) {
-  const long long blocks = sscan_blocks(P.G, P.D / P.G), slots = (long long)kSms * (backward ? kBwdCtasPerSm : kFwdCtasPerSm);
+  const SscanCost& c = backward ? kBwdCost : kFwdCost;
+  const long long blocks = sscan_blocks(P.G, P.D / P.G);
   int longest = P.T;
   if (P.cu) {
     longest = 0;
     for (int i = 0; i < P.seqs; ++i) longest = std::max(longest, sequence_length(P, i));
   }
-  const long long whole = ((long long)longest + kSscanBlock - 1) / kSscanBlock * kSscanBlock;
-  auto rounds = [&](long long segs) { return (segs * blocks + slots - 1) / slots; };
-  long long best = whole;
-  double cost = double(rounds(P.seqs)) * (whole + kCtaTokens);
-  const int most_rounds = P.seqs > 64 ? 2 : 4;  // counting the segments of many documents takes host time
-  for (int r = 1; r <= most_rounds; ++r) {
-    long long L = (P.rows * blocks + slots * r * kSscanBlock - 1) / (slots * r * kSscanBlock) * kSscanBlock;
-    L = std::max<long long>(L, kMinSegment);
-    long long n = count_segments(P, L);
-    for (int k = 0; k < 4 && rounds(n) > r; ++k) n = count_segments(P, L += kSscanBlock);
-    if (L >= whole) continue;
-    const double c = double(rounds(n)) * (L + kCtaTokens) * (1.0 + kMapCost);
-    if (c < cost) cost = c, best = L;
+  const double whole = longest * std::max(c.alone, double((P.seqs * blocks + kSms - 1) / kSms));
+  const double cut = (1.0 + c.map) * double(P.rows) * blocks / kSms;
+  long long L = ((long long)longest + kSscanCut - 1) / kSscanCut * kSscanCut;
+  if (cut < whole) {
+    const long long unit = (long long)kSms * c.ctas * kSscanCut;
+    L = std::min(L, std::max<long long>(kMinSegment, (P.rows * blocks + unit - 1) / unit * kSscanCut));
   }
   SscanPlan q{};
-  q.L = int(best);
-  q.segs = count_segments(P, best);
-  q.most = int((longest + best - 1) / best);
+  q.L = int(L);
+  q.segs = count_segments(P, L);
+  q.most = int((longest + L - 1) / L);
   q.cks = count_segments(P, kSscanBlock);
   return q;
 }
@@ -319,6 +318,7 @@ void fill(const SscanProblem& P, const SscanPlan& q, const SscanLayout& l, char*
 
 // Whether all channel blocks' rows start on 16-byte boundaries: the tensors, their strides and the groups.
 void set_vectors(const SscanProblem& P, SscanParams* p) {
+  p->pair = P.D % 2 == 0 && (P.D / P.G) % 2 == 0;
   const bool groups = P.G == 1 || (P.D / P.G) % 8 == 0;
   p->vec = groups && aligned(p->u, 16) && aligned(p->delta, 16) && aligned(p->z, 16) && aligned(p->dy, 16) && P.u_s % 8 == 0 &&
            P.dt_s % 8 == 0 && (!p->z || P.z_s % 8 == 0) && (!p->dy || P.D % 8 == 0);

@@ -149,7 +149,8 @@ cudaError_t launch_delta_step(const DeltaStepParams& p, cudaStream_t s);
 
 // Selective scan (k_sscan_fwd.cu, k_sscan_bwd.cu, k_step.cu).
 constexpr int kSscanMaxN = 16;     // states per channel
-constexpr int kSscanBlock = 32;    // tokens between the states a training forward keeps; segments are multiples of it
+constexpr int kSscanBlock = 8;     // tokens between the states a training forward keeps
+constexpr int kSscanCut = 32;      // segments are multiples of this
 constexpr int kSscanChans = 128;   // channels per CTA
 constexpr int kSscanThreads = kSscanChans / 2;
 
@@ -160,6 +161,7 @@ struct SscanParams {
   int segs;                    // segments of all sequences
   const int *cu, *seg_base, *ck_base;  // packed: device arrays [seqs+1] (tokens, segments, kept states), else null
   int softplus;
+  bool pair;                   // neighbouring channels of a state row 8-byte aligned
   bool vec, vec_out;           // u, delta, z (dy): every 8 channels of a block 16-byte aligned; the same of the outputs
   long long u_s, dt_s, z_s, b_s, c_s;  // elements between tokens
   const __nv_bfloat16 *u, *delta, *z, *Bm, *Cm;

@@ -163,6 +163,27 @@ __device__ __forceinline__ void store_states(const F2* h, float* s, size_t apart
     if (2 * i + 1 < N) s[(2 * i + 1) * apart] = hi;
   }
 }
+// Both channels' states into a kept or segment state (`row`: its first channel's place), in 8-byte pieces where the pairs are
+// aligned.
+template <int NP>
+__device__ __forceinline__ void store_rows(const F2 (*h)[NP / 2], float* row, const SscanParams& p, const SscanChan& c) {
+  if (!p.pair) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (c.live[e]) store_states<NP>(h[e], row + c.d[e], p.D, p.N);
+    return;
+  }
+  if (!c.live[0]) return;
+#pragma unroll
+  for (int i = 0; i < NP / 2; ++i) {
+    float a0, a1, b0, b1;
+    unf2(h[0][i], &a0, &a1);
+    unf2(h[1][i], &b0, &b1);
+    if (2 * i < p.N) *reinterpret_cast<float2*>(row + (size_t)(2 * i) * p.D + c.d[0]) = make_float2(a0, b0);
+    if (2 * i + 1 < p.N) *reinterpret_cast<float2*>(row + (size_t)(2 * i + 1) * p.D + c.d[0]) = make_float2(a1, b1);
+  }
+}
+
 // log2(e) A of one channel (a padded state then stays 0).
 template <int NP>
 __device__ __forceinline__ void load_A2(F2* A2, const SscanParams& p, int d) {

@@ -4,19 +4,16 @@
 //   w = dh_t a_t h_{t-1},  dA = sum_t w dt,  ddt = u (B . dh) + A . w,  ddelta = ddt sigmoid(delta + bias),
 //   dz = dy (C . h + D u) silu'(z),  dD = sum_t dy0 u,  dh0 = a_1 dh_1.
 //
-// One thread walks one channel. The states it needs in reverse come from the states a training forward keeps before every
-// 32nd token: a block of 32 is run forward once to leave the entry states of its 8-token tiles in shared memory, and each
-// tile, last to first, is run forward again into registers and then walked back. The adjoint chain is cut into segments
-// like the forward's. The sums over channels in dB and dC begin as matrix products with ones: a
+// One thread walks one channel. The states it needs in reverse come from those a training forward keeps before every 8th
+// token (8 bytes a token and channel): each tile of 8, last to first, is run forward again and then walked back. Keeping
+// fewer costs another forward walk, which this kernel, bound by its instructions at 7% of HBM's rate, cannot hide as it
+// does the reads. The adjoint chain is cut into segments like the forward's. The sums over channels in dB and dC begin as matrix products with ones: a
 // lane's four states are its share of the A operand of m16n8k8, whose products add up four lanes' channels (tf32 operands;
 // the results are bf16), and seven exchanges add up the eight groups of lanes. All other sums are fp32.
 #include "k_sscan.cuh"
 
 namespace gdn {
 namespace {
-
-constexpr int kTile = 8;
-constexpr int kTiles = kSscanBlock / kTile;
 
 constexpr int kRGroup = 4;
 constexpr int kRt = 16;  // tokens the adjoint map stages together, double-buffered
@@ -98,10 +95,10 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, 
     }
     if (tb > 0) rc.store(sm.C[buf ^ 1]);
   }
+  store_rows<NP>(g, p.seg_state + (size_t)seg * p.N * p.D, p, ch);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     if (!ch.live[e]) continue;
-    store_states<NP>(g[e], p.seg_state + (size_t)seg * p.N * p.D + ch.d[e], p.D, p.N);
     p.seg_dt[(size_t)seg * p.D + ch.d[e]] = dt_sum[e];
   }
 }
@@ -164,21 +161,19 @@ __device__ __forceinline__ float exchange(float a, float b, bool up, int mask) {
 
 constexpr int kBwdThreads = kSscanChans;
 constexpr int kWarps = kBwdThreads / 32;
+constexpr int kTile = kSscanBlock, kHalf = kTile / 2;
 
-// A block of tokens of B or C as fp32, [token][NP].
+// A tile of tokens of B or C as fp32, [token][NP]: one element a thread.
 template <int NP>
 struct VecTile {
-  float v[kSscanBlock][NP];
-  __device__ __forceinline__ void load(const __nv_bfloat16* src, long long row, int len, int N) {
-    constexpr int kPer = kSscanBlock * NP / kBwdThreads;
-    uint16_t r[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = threadIdx.x + j * kBwdThreads, t = e / NP, n = e % NP;
-      r[j] = t < len && n < N ? __ldg(reinterpret_cast<const uint16_t*>(src + t * row + n)) : uint16_t(0);
-    }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) (&v[0][0])[threadIdx.x + j * kBwdThreads] = __uint_as_float(uint32_t(r[j]) << 16);
+  float v[kTile][NP];
+  static_assert(kTile * NP <= kBwdThreads, "one element a thread");
+  __device__ __forceinline__ static uint16_t fetch(const __nv_bfloat16* src, long long row, int len, int N) {
+    const int t = threadIdx.x / NP, n = threadIdx.x % NP;
+    return t < len && t < kTile && n < N ? __ldg(reinterpret_cast<const uint16_t*>(src + t * row + n)) : uint16_t(0);
+  }
+  __device__ __forceinline__ void put(uint16_t r) {
+    if (threadIdx.x < kTile * NP) (&v[0][0])[threadIdx.x] = __uint_as_float(uint32_t(r) << 16);
   }
   __device__ __forceinline__ void pairs(F2* out, int t) const {
 #pragma unroll
@@ -192,13 +187,16 @@ struct VecTile {
 
 template <int NP>
 struct BwdSmem {
-  VecTile<NP> B, C;
-  ChTile<kSscanBlock, kBwdThreads> u, delta, z, dy;                 // du, ddelta and dz replace u, delta and z token by token
-  float entry[kTiles][NP / 2][kBwdThreads][2];       // states before each tile
-  float2 dts[kTile][kBwdThreads];                    // the tile's dt and d dt / d delta
-  float red[kWarps][kSscanBlock][2][16];               // the warps' sums over their channels: dC, dB
+  VecTile<NP> B[2], C[2];
+  ChTile<kTile, kBwdThreads> u[2], delta[2], z[2], dy[2];  // du, ddelta and dz replace u, delta and z token by token
+  float ck[2][NP][kBwdThreads];                            // states before the tile
+  float4 H[kHalf][NP / 4][kBwdThreads];                    // states after the tokens of the tile's first half
+  float2 dts[kTile][kBwdThreads];                          // dt and d dt / d delta
+  float red[kWarps][kTile][2][16];                         // the warps' sums over their channels: dC, dB
 };
 
+// Tile by tile, the last first: forward over the tile's tokens, whose states stay in shared memory (first half) and
+// registers (second half), then back over them.
 template <int NP>
 __global__ void __launch_bounds__(kBwdThreads, 2) k_sscan_bwd(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
@@ -222,74 +220,90 @@ __global__ void __launch_bounds__(kBwdThreads, 2) k_sscan_bwd(SscanParams p, int
     if (p.seg_state) load_states<NP>(g, p.seg_state + (size_t)seg * p.N * p.D + d, p.D, p.N);
     else if (p.dfinal) load_states<NP>(g, p.dfinal + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);
   }
-  const float bias = p.bias ? __ldg(p.bias + d) : 0.f, skip = p.Dskip ? __ldg(p.Dskip + d) : 0.f;
+  const float bias = param(p.bias, d), skip = param(p.Dskip, d);
   float dD = 0.f, dbias = 0.f;
-  const int nb = (sg.len + kSscanBlock - 1) / kSscanBlock;
-  for (int b = nb - 1; b >= 0; --b) {
-    const int tb = b * kSscanBlock, n = min(kSscanBlock, sg.len - tb), tiles = (n + kTile - 1) / kTile;
+  uint16_t rb, rc;
+  auto request = [&](int tb, int buf) {
     const long long row = sg.row0 + tb;
-    __syncthreads();  // the previous block's tiles and sums have been read
-    sm.u.load(p.u + row * p.u_s + ch.d0, p.u_s, n, ch.chans, p.vec);
-    sm.delta.load(p.delta + row * p.dt_s + ch.d0, p.dt_s, n, ch.chans, p.vec);
-    sm.dy.load(p.dy + row * p.D + ch.d0, p.D, n, ch.chans, p.vec);
-    if (gate) sm.z.load(p.z + row * p.z_s + ch.d0, p.z_s, n, ch.chans, p.vec);
+    const int len = sg.len - tb;
+    sm.u[buf].load(p.u + row * p.u_s + ch.d0, p.u_s, len, ch.chans, p.vec);
+    sm.delta[buf].load(p.delta + row * p.dt_s + ch.d0, p.dt_s, len, ch.chans, p.vec);
+    sm.dy[buf].load(p.dy + row * p.D + ch.d0, p.D, len, ch.chans, p.vec);
+    if (gate) sm.z[buf].load(p.z + row * p.z_s + ch.d0, p.z_s, len, ch.chans, p.vec);
+    const float* ck = p.ck + (size_t)(sg.ck0 + tb / kTile) * p.N * p.D + d;
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&sm.ck[buf][0][tid]));
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + n * kBwdThreads * 4), "l"(ck + (size_t)min(n, p.N - 1) * p.D),
+                   "r"(n < p.N ? 4 : 0)
+                   : "memory");
     copies_commit();
-    F2 h[NP / 2];
-    load_states<NP>(h, p.ck + (size_t)(sg.ck0 + b) * p.N * p.D + d, p.D, p.N);
-    sm.B.load(p.Bm + row * p.b_s + ch.g * p.N, p.b_s, n, p.N);
-    sm.C.load(p.Cm + row * p.c_s + ch.g * p.N, p.c_s, n, p.N);
+    rb = VecTile<NP>::fetch(p.Bm + row * p.b_s + ch.g * p.N, p.b_s, len, p.N);
+    rc = VecTile<NP>::fetch(p.Cm + row * p.c_s + ch.g * p.N, p.c_s, len, p.N);
+  };
+  const int last = (sg.len - 1) / kTile * kTile;
+  request(last, 0);
+  sm.B[0].put(rb);
+  sm.C[0].put(rc);
+  for (int tb = last, buf = 0; tb >= 0; tb -= kTile, buf ^= 1) {
+    const int len = min(kTile, sg.len - tb);
+    const long long row = sg.row0 + tb;
     copies_wait();
     __syncthreads();
-    // forward over the block, leaving the states before each tile
-    for (int q = 0; q < tiles; ++q) {
+    if (tb > 0) request(tb - kTile, buf ^ 1);
+    // No branch in a token's work: past the segment's end dt and d dt / d delta are 0, dy is 0, and the state stays.
+    F2 h[NP / 2], H[kHalf][NP / 2];
 #pragma unroll
-      for (int s = 0; s < NP / 2; ++s) *reinterpret_cast<unsigned long long*>(sm.entry[q][s][tid]) = h[s].v;
-      if (q == tiles - 1) break;
-#pragma unroll 4
-      for (int i = 0; i < kTile; ++i) {
-        const int t = q * kTile + i;
-        const float x = sm.delta.one(t, tid) + bias;
-        float slope, dt = softplus(x, &slope);
-        dt = softplus_on ? dt : x;
-        const float dtu = dt * sm.u.one(t, tid);
-        const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
-        F2 v[NP / 2];
-        sm.B.pairs(v, t);
+    for (int i = 0; i < NP / 2; ++i) h[i] = f2(sm.ck[buf][2 * i][tid], sm.ck[buf][2 * i + 1][tid]);
+    auto forward = [&](int t, const F2* from, F2* to) {
+      const float x = sm.delta[buf].one(t, tid) + bias, u = sm.u[buf].one(t, tid);
+      float slope, dt = softplus(x, &slope);
+      dt = t < len ? (softplus_on ? dt : x) : 0.f;
+      slope = t < len ? (softplus_on ? slope : 1.f) : 0.f;
+      sm.dts[t][tid] = make_float2(dt, slope);
+      const F2 dt2 = dup2(dt), dtu2 = dup2(dt * u);
+      F2 v[NP / 2];
+      sm.B[buf].pairs(v, t);
 #pragma unroll
-        for (int s = 0; s < NP / 2; ++s) h[s] = fma2(exp2_approx2(mul2(dt2, A2[s])), h[s], mul2(dtu2, v[s]));
+      for (int s = 0; s < NP / 2; ++s) to[s] = fma2(exp2_approx2(mul2(dt2, A2[s])), from[s], mul2(dtu2, v[s]));
+    };
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      forward(i, h, h);
+#pragma unroll
+      for (int s = 0; s < NP / 4; ++s) {
+        float4 q;
+        unf2(h[2 * s], &q.x, &q.y);
+        unf2(h[2 * s + 1], &q.z, &q.w);
+        sm.H[i][s][tid] = q;
       }
     }
-    for (int q = tiles - 1; q >= 0; --q) {
-      // no branch in a token's work; past the segment's end dt and d dt / d delta are 0
-      F2 H[kTile][NP / 2];
 #pragma unroll
-      for (int s = 0; s < NP / 2; ++s) h[s].v = *reinterpret_cast<const unsigned long long*>(sm.entry[q][s][tid]);
+    for (int i = 0; i < kHalf; ++i) forward(kHalf + i, i ? H[i ? i - 1 : 0] : h, H[i]);
+#pragma unroll 1
+    for (int half = 1; half >= 0; --half) {
+      if (half == 0) {
 #pragma unroll
-      for (int i = 0; i < kTile; ++i) {
-        const int t = q * kTile + i;
-        const float x = sm.delta.one(t, tid) + bias;
-        float slope, dt = softplus(x, &slope);
-        dt = t < n ? (softplus_on ? dt : x) : 0.f;
-        slope = t < n ? (softplus_on ? slope : 1.f) : 0.f;
-        sm.dts[i][tid] = make_float2(dt, slope);
-        const float dtu = dt * sm.u.one(t, tid);
-        const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu);
-        F2 v[NP / 2];
-        sm.B.pairs(v, t);
+        for (int i = 0; i < kHalf; ++i)
 #pragma unroll
-        for (int s = 0; s < NP / 2; ++s) H[i][s] = fma2(exp2_approx2(mul2(dt2, A2[s])), i ? H[i ? i - 1 : 0][s] : h[s], mul2(dtu2, v[s]));
+          for (int s = 0; s < NP / 4; ++s) {
+            const float4 q = sm.H[i][s][tid];
+            H[i][2 * s] = f2(q.x, q.y);
+            H[i][2 * s + 1] = f2(q.z, q.w);
+          }
+#pragma unroll
+        for (int i = 0; i < NP / 2; ++i) h[i] = f2(sm.ck[buf][2 * i][tid], sm.ck[buf][2 * i + 1][tid]);
       }
 #pragma unroll
-      for (int i = kTile - 1; i >= 0; --i) {
-        const int t = q * kTile + i;
-        const float u = sm.u.one(t, tid), dy = sm.dy.one(t, tid), z = sm.z.one(t, tid);
-        const float2 ds = sm.dts[i][tid];
-        const float dt = ds.x, dtu = dt * u, sig = sigmoid_fast(z);
-        const float dy0 = gate ? dy * (z * sig) : dy;
-        const F2 dt2 = f2(dt, dt), dtu2 = f2(dtu, dtu), dy2 = f2(dy0, dy0);
+      for (int i = kHalf - 1; i >= 0; --i) {
+        const int t = half * kHalf + i;
+        const float u = sm.u[buf].one(t, tid), dy = sm.dy[buf].one(t, tid), z = sm.z[buf].one(t, tid);
+        const float2 ds = sm.dts[t][tid];
+        const float dt = ds.x, sig = sigmoid_fast(z), dy0 = gate ? dy * (z * sig) : dy;
+        const F2 dt2 = dup2(dt), dtu2 = dup2(dt * u), dy2 = dup2(dy0);
         float cC[4], cB[4];
         F2 v[NP / 2], w[NP / 2];
-        sm.C.pairs(v, t);
+        sm.C[buf].pairs(v, t);
         F2 y2 = f2(skip * u, 0.f), sB = f2(0.f, 0.f), sA = f2(0.f, 0.f);
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) {
@@ -301,7 +315,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) k_sscan_bwd(SscanParams p, int
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) w[s] = mul2(g[s], dtu2);
         channel_sum<NP>(cB, w, sel);
-        sm.B.pairs(v, t);
+        sm.B[buf].pairs(v, t);
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) {
           sB = fma2(g[s], v[s], sB);
@@ -314,9 +328,9 @@ __global__ void __launch_bounds__(kBwdThreads, 2) k_sscan_bwd(SscanParams p, int
         const float ddt = fmaf(u, dhB, 0.6931471805599453f * sum2(sA)), dd = ddt * ds.y;
         dD = fmaf(dy0, u, dD);
         dbias += dd;
-        sm.u.set_one(t, tid, fmaf(dt, dhB, skip * dy0));
-        sm.delta.set_one(t, tid, dd);
-        sm.z.set_one(t, tid, dy * sum2(y2) * (sig * fmaf(z, 1.f - sig, 1.f)));
+        sm.u[buf].set_one(t, tid, fmaf(dt, dhB, skip * dy0));
+        sm.delta[buf].set_one(t, tid, dd);
+        sm.z[buf].set_one(t, tid, dy * sum2(y2) * (sig * fmaf(z, 1.f - sig, 1.f)));
         // the eight sums of lane 4 r + j over its four lanes, added up over r, of which each lane ends with one
         const bool r0 = lane & 4, r1 = lane & 8, r2 = lane & 16;
         const float k0 = exchange(cC[0], cB[0], r0, 4), k1 = exchange(cC[1], cB[1], r0, 4);
@@ -326,18 +340,23 @@ __global__ void __launch_bounds__(kBwdThreads, 2) k_sscan_bwd(SscanParams p, int
         sm.red[warp][t][r0][(lane & 3) * 4 + (r1 ? 2 : 0) + (r2 ? 1 : 0)] = exchange(l0, l1, r2, 16);
       }
     }
+    if (tb > 0) {
+      sm.B[buf ^ 1].put(rb);
+      sm.C[buf ^ 1].put(rc);
+    }
     __syncthreads();
-    sm.u.store(p.du + row * p.D + ch.d0, p.D, n, ch.chans, p.vec_out);
-    sm.delta.store(p.ddelta + row * p.D + ch.d0, p.D, n, ch.chans, p.vec_out);
-    if (gate) sm.z.store(p.dz + row * p.D + ch.d0, p.D, n, ch.chans, p.vec_out);
-    const int per = 2 * p.N;
-    float* part = p.part_bc + ((size_t)cb * p.rows + row) * per;
-    for (int e = tid; e < n * per; e += kBwdThreads) {
-      const int t = e / per, x = e % per, which = x / p.N, st = x - which * p.N;
+    sm.u[buf].store(p.du + row * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
+    sm.delta[buf].store(p.ddelta + row * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
+    if (gate) sm.z[buf].store(p.dz + row * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
+    // partial dC and dB of the tile: [token][dC, dB][N]
+    float* part = p.part_bc + ((size_t)cb * p.rows + row) * 2 * p.N;
+#pragma unroll
+    for (int j = 0; j < kTile * 32 / kBwdThreads; ++j) {
+      const int e = tid + j * kBwdThreads, t = e / 32, which = e / 16 % 2, n = e % 16;
       float r = 0.f;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) r += sm.red[k][t][which][st];
-      part[e] = r;
+      for (int k = 0; k < kWarps; ++k) r += sm.red[k][t][which][n];
+      if (t < len && n < p.N) part[(t * 2 + which) * p.N + n] = r;
     }
   }
   if (!live) return;

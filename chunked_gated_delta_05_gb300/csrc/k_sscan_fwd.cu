@@ -16,7 +16,7 @@ namespace gdn {
 namespace {
 
 constexpr int kGroup = 4;
-constexpr int kTt = 16;  // tokens staged together, double-buffered; kSscanBlock is a multiple of it
+constexpr int kTt = 16;  // tokens staged together, double-buffered; a multiple of kSscanBlock and kGroup
 
 template <int NP, bool MAP>
 struct PassSmem {
@@ -72,17 +72,14 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_pass(SscanParams p, 
     __syncthreads();
     const bool more = tb + kTt < sg.len;
     if (more) request(tb + kTt, buf ^ 1);
-    if (!MAP && p.ck && tb % kSscanBlock == 0) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (ch.live[e]) store_states<NP>(h[e], p.ck + (size_t)(sg.ck0 + tb / kSscanBlock) * p.N * p.D + ch.d[e], p.D, p.N);
-    }
     const int len = min(kTt, sg.len - tb);
     // Tokens go in groups, whose step sizes and gates (long dependent chains) are computed side by side before and after the
     // states. No branch in a token's work: past the segment's end dt = 0, which leaves the state as it is, and without
     // softplus or gate their results are not selected.
 #pragma unroll 1
     for (int t0 = 0; t0 < kTt; t0 += kGroup) {
+      if (!MAP && p.ck && t0 % kSscanBlock == 0 && t0 < len)
+        store_rows<NP>(h, p.ck + (size_t)(sg.ck0 + (tb + t0) / kSscanBlock) * p.N * p.D, p, ch);
       float dt[kGroup][2], dtu[kGroup][2], y[kGroup][2];
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
@@ -133,12 +130,12 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_pass(SscanParams p, 
       sm.u[buf].store(p.y + (sg.row0 + tb) * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
     }
   }
+  if (MAP) store_rows<NP>(h, p.seg_state + (size_t)seg * p.N * p.D, p, ch);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     if (!ch.live[e]) continue;
     const int d = ch.d[e];
     if (MAP) {
-      store_states<NP>(h[e], p.seg_state + (size_t)seg * p.N * p.D + d, p.D, p.N);
       p.seg_dt[(size_t)seg * p.D + d] = dt_sum[e];
     } else if (p.final_state && sg.j == sg.nseg - 1) {
       store_states<NP>(h[e], p.final_state + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);
