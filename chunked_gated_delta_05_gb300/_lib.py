@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -124,6 +125,16 @@ def _call(desc, args):
     return ([ctypes.POINTER(desc), ctypes.POINTER(args), c_void_p], c_int)
 
 
+def packer(cls):
+    """``pack(*fields) -> bytes`` of a structure with the C layout of ``cls`` (pointers as integers). Building the bytes
+    takes a fraction of the time of filling a ctypes structure, which is much of a small call's."""
+    codes = {c_int: "i", c_float: "f", c_size_t: "N", c_ll: "q", c_void_p: "P"}
+    fmt = struct.Struct("@" + "".join(codes.get(t, "P") for _, t in cls._fields_) + "0P")
+    if fmt.size != ctypes.sizeof(cls):
+        raise RuntimeError(f"packed layout of {cls.__name__} differs from its C layout")
+    return fmt.pack
+
+
 # Every symbol include/gdn.h declares, with its ctypes signature.
 SIGNATURES = {
     "gdn_strerror": ([c_int], ctypes.c_char_p),
@@ -172,6 +183,16 @@ SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_entries = {}
+
+
+def entry(name: str):
+    """The (desc, args, stream) entry point ``name``, taking packed structures (bytes) and the stream as an integer."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = ctypes.CFUNCTYPE(c_int, c_void_p, c_void_p, c_void_p)((name, load()))
+        _entries[name] = fn
+    return fn
 
 
 def load(build_if_missing: bool = True):

@@ -22,11 +22,27 @@ def _want(name, t, dtype, shape, dev):
 
 
 def _p(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev.index) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+
+
+_norm_desc = _lib.packer(_lib.NormDesc)
+_norm_fwd_args, _norm_bwd_args = _lib.packer(_lib.NormFwdArgs), _lib.packer(_lib.NormBwdArgs)
+_conv_step_desc, _conv_step_args = _lib.packer(_lib.ConvStepDesc), _lib.packer(_lib.ConvStepArgs)
+_step_desc, _step_args = _lib.packer(_lib.StepDesc), _lib.packer(_lib.StepArgs)
+_scan_desc, _scan_step_args = _lib.packer(_lib.SscanDesc), _lib.packer(_lib.SscanStepArgs)
+
+
+def _run(name, desc, args, dev):
+    rc = _lib.entry(name)(desc, args, _stream(dev))
+    if rc:
+        _lib.check(rc)
 
 
 def _device(name, t):
@@ -49,6 +65,10 @@ def _rows_of(name, t, dtype, shape, dev, inner):
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
     st, w, lead = t.stride(), 1, len(shape) - inner
+    if t.is_contiguous():
+        for n in shape[lead:]:
+            w *= n
+        return w
     for i in range(len(shape) - 1, lead - 1, -1):
         if shape[i] != 1 and st[i] != w:
             raise ValueError(f"{name}'s rows must be contiguous")
@@ -84,8 +104,11 @@ def _status(status, dev):
 
 # ---------------------------------------------------------------- norms
 
-def _norm_desc(rows, width, eps, scale=1.0, kind=0, act=0):
-    return _lib.NormDesc(rows, width, eps, scale, kind, act)
+def _norm_workspace(rows, width, like):
+    n = _lib.load().gdn_norm_bwd_workspace_size(_lib.NormDesc(rows=rows, width=width))
+    if n == 0:
+        _lib.check(_lib.GDN_EINVAL)
+    return like.new_empty(n, dtype=torch.uint8), n
 
 
 def _norm_shape(x):
@@ -101,7 +124,6 @@ def add_rms_norm_fwd(x, residual, weight, *, eps=1e-6, residual_scale=1.0):
     """Residual sum and RMS norm before a block: ``stream = residual + residual_scale * x`` (kept in the residual's type,
     fp32 or bf16), ``y = stream * rsqrt(mean(stream^2) + eps) * weight`` over the last dimension of ``x`` (bf16), with
     ``weight`` fp32. Without a residual (None) the stream is x itself. Returns ``(y bf16, stream)``."""
-    lib = _lib.load()
     dev, rows, width = _norm_shape(x)
     _want("weight", weight, _F32, (width,), dev)
     kind = 0
@@ -112,16 +134,14 @@ def add_rms_norm_fwd(x, residual, weight, *, eps=1e-6, residual_scale=1.0):
         kind = 2 if residual.dtype is _F32 else 1
     y = torch.empty_like(x)
     stream = x if residual is None else torch.empty_like(residual)
-    d = _norm_desc(rows, width, eps, residual_scale, kind)
-    a = _lib.NormFwdArgs(_p(x), _p(residual), _p(weight), _p(y), _p(stream) if kind else None)
-    _lib.check(lib.gdn_add_norm_fwd(d, a, _stream(dev)))
+    _run("gdn_add_norm_fwd", _norm_desc(rows, width, eps, residual_scale, kind, 0),
+         _norm_fwd_args(_p(x), _p(residual), _p(weight), _p(y), _p(stream) if kind else 0), dev)
     return y, stream
 
 
 def add_rms_norm_bwd(dy, dstream, stream, weight, *, eps=1e-6, residual_scale=1.0, has_residual=True):
     """Gradients of :func:`add_rms_norm_fwd` from ``dy`` (bf16) and ``dstream`` (the stream's type, or None), given the
     forward's ``stream``. Returns ``(dx bf16, dresidual (the stream's type) or None, dweight fp32)``."""
-    lib = _lib.load()
     dev, rows, width = _norm_shape(dy)
     if not isinstance(stream, torch.Tensor) or stream.dtype not in ((_BF16, _F32) if has_residual else (_BF16,)):
         raise ValueError("stream must be the tensor returned by the forward")
@@ -130,16 +150,12 @@ def add_rms_norm_bwd(dy, dstream, stream, weight, *, eps=1e-6, residual_scale=1.
     if dstream is not None:
         _want("dstream", dstream, stream.dtype, dy.shape, dev)
     kind = 0 if not has_residual else 2 if stream.dtype is _F32 else 1
-    d = _norm_desc(rows, width, eps, residual_scale, kind)
-    ws_bytes = lib.gdn_norm_bwd_workspace_size(d)
-    if ws_bytes == 0:
-        _lib.check(_lib.GDN_EINVAL)
+    ws, ws_bytes = _norm_workspace(rows, width, weight)
     dx = torch.empty_like(dy)
     dres = torch.empty_like(stream) if has_residual else None
     dw = torch.empty_like(weight)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    a = _lib.NormBwdArgs(_p(stream), None, _p(weight), _p(dy), _p(dstream), _p(dx), None, _p(dres), _p(dw), _p(ws), ws_bytes)
-    _lib.check(lib.gdn_add_norm_bwd(d, a, _stream(dev)))
+    _run("gdn_add_norm_bwd", _norm_desc(rows, width, eps, residual_scale, kind, 0),
+         _norm_bwd_args(_p(stream), 0, _p(weight), _p(dy), _p(dstream), _p(dx), 0, _p(dres), _p(dw), _p(ws), ws_bytes), dev)
     return dx, dres, dw
 
 
@@ -152,33 +168,26 @@ def _act(activation):
 def gated_rms_norm_fwd(x, gate, weight, *, eps=1e-6, activation="silu"):
     """Gated RMS norm after the recurrence: ``y = x * rsqrt(mean(x^2) + eps) * weight * act(gate)`` over the last dimension
     (a head, or a whole row), x and gate bf16, weight fp32, act "silu" or "sigmoid". Returns ``y`` (bf16)."""
-    lib = _lib.load()
     act = _act(activation)
     dev, rows, width = _norm_shape(x)
     _want("gate", gate, _BF16, x.shape, dev)
     _want("weight", weight, _F32, (width,), dev)
     y = torch.empty_like(x)
-    a = _lib.NormFwdArgs(_p(x), _p(gate), _p(weight), _p(y), None)
-    _lib.check(lib.gdn_gated_norm_fwd(_norm_desc(rows, width, eps, act=act), a, _stream(dev)))
+    _run("gdn_gated_norm_fwd", _norm_desc(rows, width, eps, 1.0, 0, act), _norm_fwd_args(_p(x), _p(gate), _p(weight), _p(y), 0), dev)
     return y
 
 
 def gated_rms_norm_bwd(x, gate, weight, dy, *, eps=1e-6, activation="silu"):
     """Gradients ``(dx bf16, dgate bf16, dweight fp32)`` of ``<dy, gated_rms_norm_fwd(...)>``."""
-    lib = _lib.load()
     act = _act(activation)
     dev, rows, width = _norm_shape(x)
     _want("gate", gate, _BF16, x.shape, dev)
     _want("weight", weight, _F32, (width,), dev)
     _want("dy", dy, _BF16, x.shape, dev)
-    d = _norm_desc(rows, width, eps, act=act)
-    ws_bytes = lib.gdn_norm_bwd_workspace_size(d)
-    if ws_bytes == 0:
-        _lib.check(_lib.GDN_EINVAL)
+    ws, ws_bytes = _norm_workspace(rows, width, weight)
     dx, dgate, dw = torch.empty_like(x), torch.empty_like(gate), torch.empty_like(weight)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    a = _lib.NormBwdArgs(_p(x), _p(gate), _p(weight), _p(dy), None, _p(dx), _p(dgate), None, _p(dw), _p(ws), ws_bytes)
-    _lib.check(lib.gdn_gated_norm_bwd(d, a, _stream(dev)))
+    _run("gdn_gated_norm_bwd", _norm_desc(rows, width, eps, 1.0, 0, act),
+         _norm_bwd_args(_p(x), _p(gate), _p(weight), _p(dy), 0, _p(dx), _p(dgate), 0, _p(dw), _p(ws), ws_bytes), dev)
     return dx, dgate, dw
 
 
@@ -257,7 +266,6 @@ def causal_conv1d_step(state, x, weight, bias=None, *, dilation=1, activation=Tr
     """One token of the short convolution: ``x [B,C]`` (bf16, rows may be strided) against ``state
     [slots,(W-1)*dilation,C]``, which is updated in place. ``state_indices`` (int32 [B] on the device) names each row's slot;
     a negative one marks a padding row (zero output, no state touched). Returns ``y [B,C]``."""
-    lib = _lib.load()
     dev = _device("x", x)
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must be [B,C] and weight [C,W]")
@@ -273,15 +281,13 @@ def causal_conv1d_step(state, x, weight, bias=None, *, dilation=1, activation=Tr
     _want("state", state, _BF16, (slots, (W - 1) * dilation, C), dev)
     _pool(state_indices, B, slots, dev)
     _status(status, dev)
-    y = torch.empty((B, C), dtype=_BF16, device=dev)
-    d = _lib.ConvStepDesc(B, C, W, dilation, 1 if activation else 0, slots, xs)
-    a = _lib.ConvStepArgs(_p(x), _p(weight), _p(bias), _p(state) or None, _p(state_indices), _p(y), _p(status))
-    _lib.check(lib.gdn_conv_step(d, a, _stream(dev)))
+    y = x.new_empty((B, C))
+    _run("gdn_conv_step", _conv_step_desc(B, C, W, dilation, 1 if activation else 0, slots, xs),
+         _conv_step_args(_p(x), _p(weight), _p(bias), _p(state), _p(state_indices), _p(y), _p(status)), dev)
     return y
 
 
 def _delta_step(per_channel, state, q, k, v, g, beta, state_indices, l2, sig, scale, gate, status):
-    lib = _lib.load()
     dev = _device("q", q)
     if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
         raise ValueError("q and v must have shape [B,H,128]")
@@ -301,11 +307,11 @@ def _delta_step(per_channel, state, q, k, v, g, beta, state_indices, l2, sig, sc
     A_log, dt_bias = _gate_checks(gate, H, dev)
     _pool(state_indices, B, slots, dev)
     _status(status, dev)
-    o = torch.empty((B, H, K_DIM), dtype=_BF16, device=dev)
-    d = _lib.StepDesc(B, H, Hk, slots, 0.0 if scale is None else scale, 1 if l2 else 0, 1 if sig else 0,
-                      0 if gate is None else 1, 0.0 if gate is None else gate[2], qs, ks, vs)
-    a = _lib.StepArgs(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(state), _p(state_indices), _p(o), _p(A_log), _p(dt_bias), _p(status))
-    _lib.check((lib.kda_step if per_channel else lib.gdn_step)(d, a, _stream(dev)))
+    o = v.new_empty((B, H, K_DIM))
+    _run("kda_step" if per_channel else "gdn_step",
+         _step_desc(B, H, Hk, slots, 0.0 if scale is None else scale, 1 if l2 else 0, 1 if sig else 0,
+                    0 if gate is None else 1, 0.0 if gate is None else gate[2], qs, ks, vs),
+         _step_args(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(state), _p(state_indices), _p(o), _p(A_log), _p(dt_bias), _p(status)), dev)
     return o
 
 
@@ -327,7 +333,7 @@ def kda_step(state, q, k, v, g, beta, *, state_indices=None, use_qk_l2norm=True,
 # ---------------------------------------------------------------- selective scan
 
 def _sscan_desc(u, delta, A, Bm, Cm, D, z, delta_bias, softplus, lead, offsets):
-    """Checks the inputs of a scan (lead = 2: [B,T,..]) or a step (lead = 1: [B,..])."""
+    """Checks the inputs of a scan (lead = 2: [B,T,..]) or a step (lead = 1: [B,..]); ``(device, sequences, D, N, packed description)``."""
     dev = _device("u", u)
     if u.dim() != lead + 1 or u.numel() == 0:
         raise ValueError("u must be [B,T,D]" if lead == 2 else "u must be [B,D]")
@@ -348,12 +354,15 @@ def _sscan_desc(u, delta, A, Bm, Cm, D, z, delta_bias, softplus, lead, offsets):
     if delta_bias is not None:
         _want("delta_bias", delta_bias, _F32, (Dc,), dev)
     B, T = head[0], head[1] if lead == 2 else 1
-    d = _lib.SscanDesc(B, T, Dc, N, G, None, B, 1 if softplus else 0, us, ds, zs, bs, cs)
-    if offsets is not None:
-        arr, n = offsets
-        d.cu_seqlens = ctypes.cast(arr, ctypes.POINTER(ctypes.c_int32))
-        d.num_seqs = n
-    return dev, d
+    cu, n = (0, B) if offsets is None else (ctypes.addressof(offsets[0]), offsets[1])
+    return dev, n, Dc, N, _scan_desc(B, T, Dc, N, G, cu, n, 1 if softplus else 0, us, ds, zs, bs, cs)
+
+
+def _scan_size(fn, d):
+    return fn(_lib.SscanDesc.from_buffer_copy(d))
+
+
+_scan_fwd_args, _scan_bwd_args = _lib.packer(_lib.SscanFwdArgs), _lib.packer(_lib.SscanBwdArgs)
 
 
 def selective_scan_fwd(u, delta, A, B, C, *, D=None, z=None, delta_bias=None, delta_softplus=True, initial_state=None,
@@ -366,24 +375,23 @@ def selective_scan_fwd(u, delta, A, B, C, *, D=None, z=None, delta_bias=None, de
     ``[sequences,D,N]``. Packed documents by ``cu_seqlens``. Returns ``(y bf16, final_state or None)``; with ``save=True``
     also the buffer to hand to :func:`selective_scan_bwd`."""
     lib = _lib.load()
-    offsets = _offsets(cu_seqlens, 0)
-    dev, d = _sscan_desc(u, delta, A, B, C, D, z, delta_bias, delta_softplus, 2, offsets)
-    state_shape = (d.num_seqs, d.D, d.N)
+    offsets = _offsets(cu_seqlens, 0)       # the packed description points into it
+    dev, *state_shape, d = _sscan_desc(u, delta, A, B, C, D, z, delta_bias, delta_softplus, 2, offsets)
+    state_shape = tuple(state_shape)
     if initial_state is not None:
         _want("initial_state", initial_state, _F32, state_shape, dev)
-    ws_bytes = lib.gdn_sscan_fwd_workspace_size(d)
+    ws_bytes = _scan_size(lib.gdn_sscan_fwd_workspace_size, d)
     if ws_bytes == 0:
         _lib.check(_lib.GDN_EINVAL)
-    y = torch.empty(u.shape, dtype=_BF16, device=dev)
-    final = torch.empty(state_shape, dtype=_F32, device=dev) if output_final_state else None
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    y = u.new_empty(u.shape)
+    final = A.new_empty(state_shape) if output_final_state else None
+    ws = u.new_empty(ws_bytes, dtype=torch.uint8)
     saved_bytes, saved = 0, None
     if save:
-        saved_bytes = lib.gdn_sscan_saved_size(d)
-        saved = torch.empty(saved_bytes, dtype=torch.uint8, device=dev)
-    a = _lib.SscanFwdArgs(_p(u), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(delta_bias), _p(z), _p(initial_state), _p(y),
-                          _p(final), _p(ws), ws_bytes, _p(saved), saved_bytes)
-    _lib.check(lib.gdn_sscan_fwd(d, a, _stream(dev)))
+        saved_bytes = _scan_size(lib.gdn_sscan_saved_size, d)
+        saved = u.new_empty(saved_bytes, dtype=torch.uint8)
+    _run("gdn_sscan_fwd", d, _scan_fwd_args(_p(u), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(delta_bias), _p(z), _p(initial_state),
+                                            _p(y), _p(final), _p(ws), ws_bytes, _p(saved), saved_bytes), dev)
     return (y, final, saved) if save else (y, final)
 
 
@@ -392,33 +400,32 @@ def selective_scan_bwd(u, delta, A, B, C, dy, *, D=None, z=None, delta_bias=None
     """Gradients of ``<dy, y> + <dfinal, final_state>``: ``(du, ddelta, dA, dB, dC, dD, dz, ddelta_bias, dh0)``, None where the
     input is None. ``saved`` is the buffer of a ``save=True`` forward on the same inputs (else its states are recomputed)."""
     lib = _lib.load()
-    offsets = _offsets(cu_seqlens, 0)
-    dev, d = _sscan_desc(u, delta, A, B, C, D, z, delta_bias, delta_softplus, 2, offsets)
-    state_shape = (d.num_seqs, d.D, d.N)
+    offsets = _offsets(cu_seqlens, 0)       # the packed description points into it
+    dev, *state_shape, d = _sscan_desc(u, delta, A, B, C, D, z, delta_bias, delta_softplus, 2, offsets)
+    state_shape = tuple(state_shape)
     _want("dy", dy, _BF16, u.shape, dev)
     for name, t in (("initial_state", initial_state), ("dfinal", dfinal)):
         if t is not None:
             _want(name, t, _F32, state_shape, dev)
-    ws_bytes = lib.gdn_sscan_bwd_workspace_size(d)
+    ws_bytes = _scan_size(lib.gdn_sscan_bwd_workspace_size, d)
     if ws_bytes == 0:
         _lib.check(_lib.GDN_EINVAL)
     saved_bytes = 0
     if saved is not None:
-        saved_bytes = lib.gdn_sscan_saved_size(d)
+        saved_bytes = _scan_size(lib.gdn_sscan_saved_size, d)
         if not isinstance(saved, torch.Tensor) or saved.device != dev or saved.numel() * saved.element_size() < saved_bytes:
             raise ValueError("saved must be the buffer returned by the forward with save=True")
         ws_bytes -= saved_bytes
 
     def like(t, dtype):
-        return None if t is None else torch.empty(t.shape, dtype=dtype, device=dev)
+        return None if t is None else t.new_empty(t.shape, dtype=dtype)
 
     du, ddelta, dB, dC, dz = like(u, _BF16), like(delta, _BF16), like(B, _BF16), like(C, _BF16), like(z, _BF16)
     dA, dD, dbias, dh0 = like(A, _F32), like(D, _F32), like(delta_bias, _F32), like(initial_state, _F32)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    a = _lib.SscanBwdArgs(_p(u), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(delta_bias), _p(z), _p(initial_state), _p(dy), _p(dfinal),
-                          _p(du), _p(ddelta), _p(dA), _p(dB), _p(dC), _p(dD), _p(dbias), _p(dz), _p(dh0), _p(ws), ws_bytes,
-                          _p(saved), saved_bytes)
-    _lib.check(lib.gdn_sscan_bwd(d, a, _stream(dev)))
+    ws = u.new_empty(ws_bytes, dtype=torch.uint8)
+    _run("gdn_sscan_bwd", d, _scan_bwd_args(_p(u), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(delta_bias), _p(z), _p(initial_state),
+                                            _p(dy), _p(dfinal), _p(du), _p(ddelta), _p(dA), _p(dB), _p(dC), _p(dD), _p(dbias), _p(dz),
+                                            _p(dh0), _p(ws), ws_bytes, _p(saved), saved_bytes), dev)
     return du, ddelta, dA, dB, dC, dD, dz, dbias, dh0
 
 
@@ -427,18 +434,16 @@ def selective_scan_step(state, u, delta, A, B, C, *, D=None, z=None, delta_bias=
     """One token of the selective scan per batch row: u, delta, z ``[B,D]``, B, C ``[B,G,N]`` (bf16, rows may be strided) and
     ``state [slots,D,N]`` fp32, updated in place (the final state of :func:`selective_scan_fwd` is one). ``state_indices`` as
     for :func:`causal_conv1d_step`. Returns ``y [B,D]`` bf16."""
-    lib = _lib.load()
-    dev, d = _sscan_desc(u, delta, A, B, C, D, z, delta_bias, delta_softplus, 1, None)
+    dev, rows, Dc, N, d = _sscan_desc(u, delta, A, B, C, D, z, delta_bias, delta_softplus, 1, None)
     if not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError("state must be [slots,D,N]")
     slots = state.shape[0]
-    _want("state", state, _F32, (slots, d.D, d.N), dev)
-    _pool(state_indices, d.B, slots, dev)
+    _want("state", state, _F32, (slots, Dc, N), dev)
+    _pool(state_indices, rows, slots, dev)
     _status(status, dev)
-    y = torch.empty((d.B, d.D), dtype=_BF16, device=dev)
-    a = _lib.SscanStepArgs(_p(u), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(delta_bias), _p(z), _p(state), _p(state_indices), slots,
-                           _p(y), _p(status))
-    _lib.check(lib.gdn_sscan_step(d, a, _stream(dev)))
+    y = u.new_empty((rows, Dc))
+    _run("gdn_sscan_step", d, _scan_step_args(_p(u), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(delta_bias), _p(z), _p(state),
+                                              _p(state_indices), slots, _p(y), _p(status)), dev)
     return y
 
 
