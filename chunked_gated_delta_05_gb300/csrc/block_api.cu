@@ -373,6 +373,7 @@ int gdn_conv_step(const gdn_conv_step_desc_t* d, const gdn_conv_step_args_t* a, 
   p.HW = int(HW);
   p.slots = d->num_slots;
   p.silu = d->activation;
+  p.vec_w = aligned(a->weight, 16);
   p.x_stride = xs;
   p.index = a->state_indices;
   p.x = static_cast<cbf*>(a->x);
@@ -610,7 +611,6 @@ int gdn_sscan_step(const gdn_sscan_desc_t* d, const gdn_sscan_step_args_t* a, vo
   if (rc) return rc;
   if (!a || !a->u || !a->delta || !a->A || !a->Bm || !a->Cm || !a->state || !a->y) return bad("u, delta, A, B, C, state and y must be non-NULL");
   if (a->num_slots < 1 || (!a->state_indices && a->num_slots < P.B)) return bad("num_slots must cover the batch");
-  if (P.N % 4 == 0 && (!aligned(a->state, 16) || !aligned(a->A, 16))) return bad("state and A must be 16-byte aligned when N is a multiple of 4");
   if ((long long)P.B * ((P.D * 4ll + 255) / 256) >= (1ll << 31)) return bad("problem too large");
   auto span = [&](long long stride, long long width) { return (size_t(P.B - 1) * stride + width) * 2; };
   const size_t yb = size_t(P.B) * P.D * 2, sb = size_t(a->num_slots) * P.D * P.N * 4;
@@ -619,8 +619,9 @@ int gdn_sscan_step(const gdn_sscan_desc_t* d, const gdn_sscan_step_args_t* a, vo
   for (const auto& i : in)
     if (overlap(a->y, yb, i.p, i.n) || overlap(a->state, sb, i.p, i.n)) return bad("y and state must not alias an input");
   if (overlap(a->y, yb, a->state, sb)) return bad("y must not alias state");
-  if ((rc = device_or_error(nullptr))) return rc;
   SscanStepParams p{};
+  if ((rc = device_or_error(&p.sms))) return rc;
+  p.vec = P.N % 4 == 0 && aligned(a->state, 16) && aligned(a->A, 16) && aligned(a->Bm, 8) && aligned(a->Cm, 8) && P.b_s % 4 == 0 && P.c_s % 4 == 0;
   p.B = P.B;
   p.D = P.D;
   p.N = P.N;

@@ -115,6 +115,7 @@ int norm_partial_rows();
 // and treated the same.
 struct ConvStepParams {
   int B, C, W, dil, HW, slots, silu;
+  bool vec_w;                  // weight 16-byte aligned
   long long x_stride;          // elements between batch rows
   const int* index;
   const __nv_bfloat16* x;
@@ -186,7 +187,8 @@ cudaError_t launch_sscan_fwd(const SscanParams& p, cudaStream_t s);
 cudaError_t launch_sscan_bwd(const SscanParams& p, cudaStream_t s);
 
 struct SscanStepParams {
-  int B, D, N, G, Dg, slots, softplus;
+  int B, D, N, G, Dg, slots, softplus, sms;
+  bool vec;                    // N % 4 == 0 and states, A, B and C aligned to four of their elements
   long long u_s, dt_s, z_s, b_s, c_s;  // elements between batch rows
   const int* index;
   const __nv_bfloat16 *u, *delta, *z, *Bm, *Cm;

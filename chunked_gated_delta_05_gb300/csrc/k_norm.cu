@@ -20,25 +20,36 @@ namespace {
 
 enum { kAdd = 0, kGated = 1 };
 
-template <int VEC>
-__device__ __forceinline__ void load_row(float* v, const __nv_bfloat16* src) {
-  if constexpr (VEC == 8) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
-    v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-    v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
-  } else {
-    v[0] = __bfloat162float(src[0]);
+// A vector of VEC elements as it is in memory: requested early, widened when it is used.
+template <int VEC, typename T>
+struct Raw;
+template <>
+struct Raw<8, __nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* src) { u = __ldg(reinterpret_cast<const uint4*>(src)); }
+  __device__ __forceinline__ float operator[](int e) const {
+    const uint32_t w = e < 2 ? u.x : e < 4 ? u.y : e < 6 ? u.z : u.w;
+    return e & 1 ? bf16_hi(w) : bf16_lo(w);
   }
-}
-template <int VEC>
-__device__ __forceinline__ void load_row(float* v, const float* src) {
-  if constexpr (VEC == 8) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    v[0] = src[0];
+};
+template <>
+struct Raw<8, float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* src) {
+    a = __ldg(reinterpret_cast<const float4*>(src));
+    b = __ldg(reinterpret_cast<const float4*>(src) + 1);
   }
-}
+  __device__ __forceinline__ float operator[](int e) const {
+    const float4 q = e < 4 ? a : b;
+    return e % 4 == 0 ? q.x : e % 4 == 1 ? q.y : e % 4 == 2 ? q.z : q.w;
+  }
+};
+template <typename T>
+struct Raw<1, T> {
+  T x;
+  __device__ __forceinline__ void load(const T* src) { x = src[0]; }
+  __device__ __forceinline__ float operator[](int) const { return float(x); }
+};
 template <int VEC>
 __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float* v) {
   if constexpr (VEC == 8)
@@ -58,24 +69,24 @@ __device__ __forceinline__ void store_row(float* dst, const float* v) {
 __device__ __forceinline__ float round_to(float v, const float*) { return v; }
 __device__ __forceinline__ float round_to(float v, const __nv_bfloat16*) { return __bfloat162float(__float2bfloat16_rn(v)); }
 
-// Sums of NS values over the G threads of a row; every thread of the block takes part. `red` holds NS x 32 floats.
+// Sums of NS values over the G threads of a row; every thread of the block takes part. `red` (NS x 32 floats) is another
+// one for every second call, so that one barrier a call is enough.
 template <int NS>
-__device__ __forceinline__ void row_sum(float* s, int G, float* red) {
+__device__ __forceinline__ void row_sum(float* s, int G, float (*red)[32]) {
   const int lanes = min(G, 32);
   for (int o = lanes >> 1; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < NS; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
   if (G <= 32) return;
   const int warp = threadIdx.x >> 5, per = G >> 5, first = warp / per * per;
-  __syncthreads();  // the previous row's sums have been read
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int i = 0; i < NS; ++i) red[i * 32 + warp] = s[i];
+    for (int i = 0; i < NS; ++i) red[i][warp] = s[i];
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     float t = 0.f;
-    for (int w = 0; w < per; ++w) t += red[i * 32 + first + w];
+    for (int w = 0; w < per; ++w) t += red[i][first + w];
     s[i] = t;
   }
 }
@@ -93,50 +104,58 @@ __device__ __forceinline__ float gate_act(float g, int act, float* d) {
 
 template <int KIND, int VEC, int NV, int THREADS, typename ST>
 __global__ void __launch_bounds__(THREADS) k_norm_fwd(NormParams p, int G) {
-  __shared__ float red[32];
+  using bf = __nv_bfloat16;
+  __shared__ float red[2][1][32];
   const int per_block = blockDim.x / G, lane = threadIdx.x & (G - 1);
   const int units = p.width / VEC;
   const float inv = 1.f / float(p.width);
-  for (long long r0 = (long long)blockIdx.x * per_block; r0 < p.rows; r0 += (long long)gridDim.x * per_block) {
+  int turn = 0;
+  for (long long r0 = (long long)blockIdx.x * per_block; r0 < p.rows; r0 += (long long)gridDim.x * per_block, turn ^= 1) {
     const long long r = r0 + threadIdx.x / G;
     const bool live = r < p.rows;
     const long long base = r * p.width;
+    Raw<VEC, bf> x[NV], gate[NV];
+    Raw<VEC, ST> res[NV];
+    Raw<VEC, float> w[NV];
     float v[NV][VEC], ss[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int u = lane + j * G;
       if (live && u < units) {
         const long long at = base + (long long)u * VEC;
-        load_row<VEC>(v[j], p.x + at);
-        if (KIND == kAdd && p.residual) {
-          float t[VEC];
-          load_row<VEC>(t, static_cast<const ST*>(p.residual) + at);
+        x[j].load(p.x + at);
+        if (KIND == kAdd && p.residual) res[j].load(static_cast<const ST*>(p.residual) + at);
+        if (KIND == kGated) gate[j].load(p.gate + at);
+        w[j].load(p.weight + u * VEC);
+      }
+    }
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) v[j][e] = round_to(fmaf(p.scale, v[j][e], t[e]), (const ST*)nullptr);
-          store_row<VEC>(static_cast<ST*>(p.stream) + at, v[j]);
+    for (int j = 0; j < NV; ++j) {
+      const int u = lane + j * G;
+      if (live && u < units) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[j][e] = x[j][e];
+        if (KIND == kAdd && p.residual) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[j][e] = round_to(fmaf(p.scale, v[j][e], res[j][e]), (const ST*)nullptr);
+          store_row<VEC>(static_cast<ST*>(p.stream) + base + (long long)u * VEC, v[j]);
         }
 #pragma unroll
         for (int e = 0; e < VEC; ++e) ss[0] = fmaf(v[j][e], v[j][e], ss[0]);
       }
     }
-    row_sum<1>(ss, G, red);
+    row_sum<1>(ss, G, red[turn]);
     const float rstd = rsqrtf(fmaf(ss[0], inv, p.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int u = lane + j * G;
       if (live && u < units) {
-        const long long at = base + (long long)u * VEC;
-        float w[VEC];
-        load_row<VEC>(w, p.weight + u * VEC);
-        if (KIND == kGated) {
-          float t[VEC], d;
-          load_row<VEC>(t, p.gate + at);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) w[e] *= gate_act(t[e], p.act, &d);
+        for (int e = 0; e < VEC; ++e) {
+          float d;
+          v[j][e] = v[j][e] * rstd * (KIND == kGated ? w[j][e] * gate_act(gate[j][e], p.act, &d) : w[j][e]);
         }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[j][e] = v[j][e] * rstd * w[e];
-        store_row<VEC>(p.y + at, v[j]);
+        store_row<VEC>(p.y + base + (long long)u * VEC, v[j]);
       }
     }
   }
@@ -146,8 +165,9 @@ __global__ void __launch_bounds__(THREADS) k_norm_fwd(NormParams p, int G) {
 // the block add theirs in shared memory in a fixed order, and the block writes one row of partial sums.
 template <int KIND, int VEC, int NV, int THREADS, typename ST>
 __global__ void __launch_bounds__(THREADS) k_norm_bwd(NormParams p, int G) {
+  using bf = __nv_bfloat16;
   extern __shared__ float acc_s[];
-  __shared__ float red[64];
+  __shared__ float red[2][2][32];
   const int per_block = blockDim.x / G, lane = threadIdx.x & (G - 1), grp = threadIdx.x / G;
   const int units = p.width / VEC;
   const float inv = 1.f / float(p.width);
@@ -156,67 +176,72 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(NormParams p, int G) {
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[j][e] = 0.f;
-  for (long long r0 = (long long)blockIdx.x * per_block; r0 < p.rows; r0 += (long long)gridDim.x * per_block) {
+  int turn = 0;
+  for (long long r0 = (long long)blockIdx.x * per_block; r0 < p.rows; r0 += (long long)gridDim.x * per_block, turn ^= 1) {
     const long long r = r0 + grp;
     const bool live = r < p.rows;
     const long long base = r * p.width;
-    float v[NV][VEC], d[NV][VEC], s[2] = {0.f, 0.f};
+    Raw<VEC, bf> dy[NV], gate[NV];
+    Raw<VEC, ST> x[NV], ds[NV];
+    float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int u = lane + j * G;
       if (live && u < units) {
         const long long at = base + (long long)u * VEC;
-        load_row<VEC>(v[j], KIND == kAdd ? static_cast<const ST*>(p.stream) + at : reinterpret_cast<const ST*>(p.x) + at);
-        load_row<VEC>(d[j], p.dy + at);
-        float w[VEC];
-        load_row<VEC>(w, p.weight + u * VEC);
-        if (KIND == kGated) {
-          float t[VEC], da;
-          load_row<VEC>(t, p.gate + at);
+        x[j].load(KIND == kAdd ? static_cast<const ST*>(p.stream) + at : reinterpret_cast<const ST*>(p.x) + at);
+        dy[j].load(p.dy + at);
+        if (KIND == kGated) gate[j].load(p.gate + at);
+        if (KIND == kAdd && p.dstream) ds[j].load(static_cast<const ST*>(p.dstream) + at);
+      }
+    }
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) d[j][e] *= gate_act(t[e], p.act, &da);  // dn
-        }
+    for (int j = 0; j < NV; ++j) {
+      const int u = lane + j * G;
+      if (live && u < units) {
+        Raw<VEC, float> w;
+        w.load(p.weight + u * VEC);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          s[0] = fmaf(v[j][e], v[j][e], s[0]);
-          s[1] = fmaf(d[j][e] * w[e], v[j][e], s[1]);
+          float da;
+          const float dn = KIND == kGated ? dy[j][e] * gate_act(gate[j][e], p.act, &da) : dy[j][e];
+          s[0] = fmaf(x[j][e], x[j][e], s[0]);
+          s[1] = fmaf(dn * w[e], x[j][e], s[1]);
         }
       }
     }
-    row_sum<2>(s, G, red);
+    row_sum<2>(s, G, red[turn]);
     const float rstd = rsqrtf(fmaf(s[0], inv, p.eps));
-    const float c = s[1] * inv * rstd * rstd;  // mean(dn w xh) / (rstd r) per element: xh mean(...) = r rstd^2 mean(dn w r)
+    const float c = s[1] * inv * rstd * rstd;  // xh mean(dn w xh) = x rstd c
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int u = lane + j * G;
       if (live && u < units) {
         const long long at = base + (long long)u * VEC;
-        float w[VEC], o[VEC];
-        load_row<VEC>(w, p.weight + u * VEC);
+        Raw<VEC, float> w;
+        w.load(p.weight + u * VEC);
+        float o[VEC], q[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          o[e] = rstd * fmaf(d[j][e], w[e], -v[j][e] * c);
-          dw[j][e] = fmaf(d[j][e], v[j][e] * rstd, dw[j][e]);
+          const float v = x[j][e], xh = v * rstd;
+          float da = 0.f, dn = dy[j][e];
+          if (KIND == kGated) {
+            q[e] = dn * xh * w[e];
+            dn *= gate_act(gate[j][e], p.act, &da);
+            q[e] *= da;
+          }
+          o[e] = rstd * fmaf(dn, w[e], -v * c);
+          dw[j][e] = fmaf(dn, xh, dw[j][e]);
         }
         if (KIND == kAdd) {
           if (p.dstream) {
-            float t[VEC];
-            load_row<VEC>(t, static_cast<const ST*>(p.dstream) + at);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] += t[e];
+            for (int e = 0; e < VEC; ++e) o[e] += ds[j][e];
           }
           if (p.dresidual) store_row<VEC>(static_cast<ST*>(p.dresidual) + at, o);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) o[e] *= p.scale;
         } else {
-          float t[VEC], q[VEC], da;
-          load_row<VEC>(t, p.gate + at);
-          load_row<VEC>(q, p.dy + at);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            gate_act(t[e], p.act, &da);
-            q[e] *= v[j][e] * rstd * w[e] * da;
-          }
           store_row<VEC>(p.dgate + at, q);
         }
         store_row<VEC>(p.dx + at, o);
@@ -264,17 +289,18 @@ struct Plan {
   int vec, nv, G, threads;
 };
 
-// Threads and vectors of a row: as few threads as hold it in two vectors each (16 elements; 8 on the element path), so that
-// the sums cross few threads and each has several loads in flight; four (32) where that takes over 256 threads.
+// Threads and vectors of a row: one vector a thread (8 elements; on the element path too) while 256 threads hold the row, so
+// that the loads of many rows are in flight in few registers; more vectors, then 512 threads, beyond (the element path takes
+// the threads first).
 Plan plan_rows(int width, bool vec8) {
   Plan p;
   p.vec = vec8 ? 8 : 1;
-  const int units = width / p.vec, few = vec8 ? 2 : 8, most = vec8 ? 4 : 32;
+  const int units = width / p.vec, few = vec8 ? 1 : 8, most = vec8 ? 4 : 32;
   int G = 8;
-  while (G < 256 && G * few < units) G *= 2;
+  while (G < (vec8 ? 256 : 512) && G * few < units) G *= 2;
   if (G * most < units) G = 512;
   const int nv = (units + G - 1) / G;
-  p.nv = vec8 && nv <= 1 ? 1 : nv <= few ? few : most;
+  p.nv = nv <= few ? few : vec8 && nv <= 2 ? 2 : most;
   p.G = G;
   p.threads = G > 256 ? G : 256;
   return p;
@@ -291,9 +317,9 @@ constexpr int kMaxPartialRows = 160 * kBwdBlocksPerSm;
     else if (q.nv == 2) { CALL(8, 2, 256); }                         \
     else { CALL(8, 4, 256); }                                        \
   } else {                                                           \
-    if (q.threads == 512) { CALL(1, 32, 512); }                      \
-    else if (q.nv == 8) { CALL(1, 8, 256); }                         \
-    else { CALL(1, 32, 256); }                                       \
+    if (q.threads == 256) { CALL(1, 8, 256); }                       \
+    else if (q.nv == 8) { CALL(1, 8, 512); }                         \
+    else { CALL(1, 32, 512); }                                       \
   }
 
 template <int KIND, typename ST>

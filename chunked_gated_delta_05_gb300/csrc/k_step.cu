@@ -27,44 +27,52 @@ __device__ __forceinline__ int slot_of(const int* index, int b, int slots, int* 
 
 // ------------------------------------------------------------------ short convolution
 
-// Eight channels per thread: the weights stay in registers while the block walks its batch rows.
+// Four channels per thread: the weights stay in registers while the block walks its batch rows.
 template <int W>
 __global__ void __launch_bounds__(128) k_conv_step(ConvStepParams p) {
-  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
   const bool live = c < p.C;
-  float w[8][W], bias[8];
+  float w[4][W], bias[4];
   if (live) {
+    // 4 W consecutive floats, 16-byte aligned for an aligned weight
+    if (p.vec_w) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+      for (int i = 0; i < W; ++i) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(p.w + (size_t)c * W) + i);
+        w[(4 * i) / W][(4 * i) % W] = q.x, w[(4 * i + 1) / W][(4 * i + 1) % W] = q.y;
+        w[(4 * i + 2) / W][(4 * i + 2) % W] = q.z, w[(4 * i + 3) / W][(4 * i + 3) % W] = q.w;
+      }
+    } else {
 #pragma unroll
-      for (int i = 0; i < W; ++i) w[e][i] = __ldg(p.w + (size_t)(c + e) * W + i);
-      bias[e] = p.bias ? __ldg(p.bias + c + e) : 0.f;
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[e][i] = __ldg(p.w + (size_t)(c + e) * W + i);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bias[e] = p.bias ? __ldg(p.bias + c + e) : 0.f;
   }
   for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
     const int slot = slot_of(p.index, b, p.slots, p.status);
     if (!live) continue;
-    __nv_bfloat16* y = p.y + (size_t)b * p.C + c;
+    uint2* y = reinterpret_cast<uint2*>(p.y + (size_t)b * p.C + c);
     if (slot < 0) {
-      *reinterpret_cast<uint4*>(y) = make_uint4(0, 0, 0, 0);
+      *y = make_uint2(0, 0);
       continue;
     }
-    const uint4 xu = __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)b * p.x_stride + c));
-    uint4* st = reinterpret_cast<uint4*>(p.state + (size_t)slot * p.HW * p.C + c);
-    const size_t row = size_t(p.C) / 8;
-    float z[8];
+    const uint2 xu = __ldg(reinterpret_cast<const uint2*>(p.x + (size_t)b * p.x_stride + c));
+    uint2* st = reinterpret_cast<uint2*>(p.state + (size_t)slot * p.HW * p.C + c);
+    const size_t row = size_t(p.C) / 4;
+    float z[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = bias[e];
-    auto tap = [&](const uint4& u, int i) {
-      const uint32_t q[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        z[2 * e] = fmaf(bf16_lo(q[e]), w[2 * e][i], z[2 * e]);
-        z[2 * e + 1] = fmaf(bf16_hi(q[e]), w[2 * e + 1][i], z[2 * e + 1]);
-      }
+    for (int e = 0; e < 4; ++e) z[e] = bias[e];
+    auto tap = [&](const uint2& u, int i) {
+      z[0] = fmaf(bf16_lo(u.x), w[0][i], z[0]);
+      z[1] = fmaf(bf16_hi(u.x), w[1][i], z[1]);
+      z[2] = fmaf(bf16_lo(u.y), w[2][i], z[2]);
+      z[3] = fmaf(bf16_hi(u.y), w[3][i], z[3]);
     };
     if (p.dil == 1) {
-      uint4 h[W];
+      uint2 h[W];
 #pragma unroll
       for (int i = 0; i < W - 1; ++i) h[i] = st[i * row];
       h[W - 1] = xu;
@@ -82,8 +90,8 @@ __global__ void __launch_bounds__(128) k_conv_step(ConvStepParams p) {
     }
     if (p.silu)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] *= sigmoid_fast(z[e]);
-    *reinterpret_cast<uint4*>(y) = make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
+      for (int e = 0; e < 4; ++e) z[e] *= sigmoid_fast(z[e]);
+    *y = make_uint2(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]));
   }
 }
 
@@ -218,68 +226,77 @@ __global__ void __launch_bounds__(256) k_delta_step(DeltaStepParams p) {
 
 // ------------------------------------------------------------------ selective scan
 
-// LPC lanes per channel, four states each (16-byte pieces when N is a multiple of 4).
-template <int LPC>
+// LPC lanes per channel, four states each. A block walks its channels over several batch rows: A, D and the bias are read
+// once, and the next row's slot is known before this one's state is stored. VEC: the states, A, B and C in 16- and 8-byte
+// pieces (N a multiple of 4 and everything aligned).
+template <int LPC, bool VEC>
 __global__ void __launch_bounds__(256) k_sscan_step(SscanStepParams p) {
-  const int cblocks = (p.D * LPC + 255) / 256;
-  const int b = blockIdx.x / cblocks, i = blockIdx.x % cblocks * 256 + threadIdx.x;
-  const int d = i / LPC, n0 = (i % LPC) * 4;
-  const int slot = slot_of(p.index, b, p.slots, p.status);
+  const int i = blockIdx.x * 256 + threadIdx.x, d = i / LPC, n0 = (i % LPC) * 4;
   const bool live = d < p.D;
-  float y = 0.f;
-  if (live && slot >= 0) {
-    float* hp = p.state + ((size_t)slot * p.D + d) * p.N + n0;
-    const float* ap = p.A + (size_t)d * p.N + n0;
-    const __nv_bfloat16* bp = p.Bm + (size_t)b * p.b_s + (d / p.Dg) * p.N + n0;
-    const __nv_bfloat16* cp = p.Cm + (size_t)b * p.c_s + (d / p.Dg) * p.N + n0;
-    const int ns = min(4, p.N - n0);
-    const bool vec = p.N % 4 == 0;
-    float h[4] = {0.f, 0.f, 0.f, 0.f}, a[4] = {0.f, 0.f, 0.f, 0.f};
-    if (vec) {
-      const float4 hv = *reinterpret_cast<const float4*>(hp), av = __ldg(reinterpret_cast<const float4*>(ap));
-      h[0] = hv.x, h[1] = hv.y, h[2] = hv.z, h[3] = hv.w;
-      a[0] = av.x, a[1] = av.y, a[2] = av.z, a[3] = av.w;
-    } else {
+  const int dc = live ? d : p.D - 1, ns = min(4, p.N - n0);
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+  if (VEC && ns > 0) {
+    const float4 av = __ldg(reinterpret_cast<const float4*>(p.A + (size_t)dc * p.N + n0));
+    a[0] = kLog2e * av.x, a[1] = kLog2e * av.y, a[2] = kLog2e * av.z, a[3] = kLog2e * av.w;
+  } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < ns) h[e] = hp[e], a[e] = __ldg(ap + e);
-    }
-    const float u = __bfloat162float(p.u[(size_t)b * p.u_s + d]);
-    float dt = __bfloat162float(p.delta[(size_t)b * p.dt_s + d]), slope;
-    if (p.bias) dt += __ldg(p.bias + d);
-    if (p.softplus) dt = softplus(dt, &slope);
-    const float dtu = dt * u, dtl = dt * kLog2e;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (e < ns) {
-        h[e] = fmaf(exp2_approx(dtl * a[e]), h[e], dtu * __bfloat162float(bp[e]));
-        y = fmaf(h[e], __bfloat162float(cp[e]), y);
-      }
-    }
-    if (vec) {
-      *reinterpret_cast<float4*>(hp) = make_float4(h[0], h[1], h[2], h[3]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < ns) hp[e] = h[e];
-    }
-    if (n0 == 0 && p.Dskip) y = fmaf(__ldg(p.Dskip + d), u, y);
+    for (int e = 0; e < 4; ++e)
+      if (e < ns) a[e] = kLog2e * __ldg(p.A + (size_t)dc * p.N + n0 + e);
   }
+  const float bias = p.bias ? __ldg(p.bias + dc) : 0.f, skip = p.Dskip && n0 == 0 ? __ldg(p.Dskip + dc) : 0.f;
+  const int bc = (dc / p.Dg) * p.N + n0;
+#pragma unroll 2
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
+    const int slot = slot_of(p.index, b, p.slots, p.status);
+    float y = 0.f;
+    if (slot >= 0) {
+      float* hp = p.state + ((size_t)slot * p.D + dc) * p.N + n0;
+      const __nv_bfloat16 *bp = p.Bm + (size_t)b * p.b_s + bc, *cp = p.Cm + (size_t)b * p.c_s + bc;
+      float h[4] = {0.f, 0.f, 0.f, 0.f}, B[4] = {0.f, 0.f, 0.f, 0.f}, C[4] = {0.f, 0.f, 0.f, 0.f};
+      if (VEC) {
+        if (ns > 0) {
+          const float4 hv = *reinterpret_cast<const float4*>(hp);
+          const uint2 bu = __ldg(reinterpret_cast<const uint2*>(bp)), cu = __ldg(reinterpret_cast<const uint2*>(cp));
+          h[0] = hv.x, h[1] = hv.y, h[2] = hv.z, h[3] = hv.w;
+          B[0] = bf16_lo(bu.x), B[1] = bf16_hi(bu.x), B[2] = bf16_lo(bu.y), B[3] = bf16_hi(bu.y);
+          C[0] = bf16_lo(cu.x), C[1] = bf16_hi(cu.x), C[2] = bf16_lo(cu.y), C[3] = bf16_hi(cu.y);
+        }
+      } else {
 #pragma unroll
-  for (int m = LPC / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
-  if (live && n0 == 0) {
-    if (p.z && slot >= 0) {
-      const float z = __bfloat162float(p.z[(size_t)b * p.z_s + d]);
-      y *= z * sigmoid_fast(z);
+        for (int e = 0; e < 4; ++e)
+          if (e < ns) h[e] = hp[e], B[e] = __bfloat162float(bp[e]), C[e] = __bfloat162float(cp[e]);
+      }
+      const float u = __bfloat162float(p.u[(size_t)b * p.u_s + dc]), x = __bfloat162float(p.delta[(size_t)b * p.dt_s + dc]) + bias;
+      const float z = p.z ? __bfloat162float(p.z[(size_t)b * p.z_s + dc]) : 0.f;
+      float slope;
+      const float dt = p.softplus ? softplus(x, &slope) : x, dtu = dt * u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[e] = fmaf(exp2_approx(dt * a[e]), h[e], dtu * B[e]);
+        y = fmaf(h[e], C[e], y);
+      }
+      y = fmaf(skip, u, y);
+      if (live) {
+        if (VEC) {
+          if (ns > 0) *reinterpret_cast<float4*>(hp) = make_float4(h[0], h[1], h[2], h[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e < ns) hp[e] = h[e];
+        }
+      }
+#pragma unroll
+      for (int m = LPC / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+      if (p.z) y *= z * sigmoid_fast(z);
     }
-    p.y[(size_t)b * p.D + d] = __float2bfloat16_rn(y);
+    if (live && n0 == 0) p.y[(size_t)b * p.D + d] = __float2bfloat16_rn(y);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t s) {
-  const int bx = (p.C / 8 + 127) / 128;
+  const int bx = (p.C / 4 + 127) / 128;
   // up to eight CTAs of four warps per SM; beyond that a block walks several rows on one load of its weights
   const int by = std::max(1, std::min(p.B, (p.sms * 8 + bx - 1) / bx));
   const dim3 grid(bx, std::min(by, 65535));
@@ -306,13 +323,17 @@ cudaError_t launch_delta_step(const DeltaStepParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_sscan_step(const SscanStepParams& p, cudaStream_t s) {
-  const int lpc = p.N <= 4 ? 1 : p.N <= 8 ? 2 : 4;
-  const int grid = (p.D * lpc + 255) / 256 * p.B;
-  if (lpc == 1) k_sscan_step<1><<<grid, 256, 0, s>>>(p);
-  else if (lpc == 2) k_sscan_step<2><<<grid, 256, 0, s>>>(p);
-  else k_sscan_step<4><<<grid, 256, 0, s>>>(p);
+template <bool VEC>
+static cudaError_t run_sscan_step(const SscanStepParams& p, cudaStream_t s) {
+  const int lpc = p.N <= 4 ? 1 : p.N <= 8 ? 2 : 4, bx = (p.D * lpc + 255) / 256;
+  // up to eight CTAs of eight warps per SM; beyond that a block walks several rows
+  const dim3 grid(bx, std::max(1, std::min(p.B, std::min(65535, (p.sms * 8 + bx - 1) / bx))));
+  if (lpc == 1) k_sscan_step<1, VEC><<<grid, 256, 0, s>>>(p);
+  else if (lpc == 2) k_sscan_step<2, VEC><<<grid, 256, 0, s>>>(p);
+  else k_sscan_step<4, VEC><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
+
+cudaError_t launch_sscan_step(const SscanStepParams& p, cudaStream_t s) { return p.vec ? run_sscan_step<true>(p, s) : run_sscan_step<false>(p, s); }
 
 }  // namespace gdn

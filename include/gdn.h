@@ -422,7 +422,7 @@ int gdn_sscan_fwd(const gdn_sscan_desc_t* desc, const gdn_sscan_fwd_args_t* args
 int gdn_sscan_bwd(const gdn_sscan_desc_t* desc, const gdn_sscan_bwd_args_t* args, void* stream);
 
 /* One token per batch row: u, delta, z, y [B,D], B, C [B,G,N] (row strides as above, T ignored, cu_seqlens NULL),
- * state fp32 [num_slots,D,N] updated (16-byte aligned when N % 4 == 0, like A). */
+ * state fp32 [num_slots,D,N] updated. */
 typedef struct {
   const void *u, *delta;
   const float* A;
