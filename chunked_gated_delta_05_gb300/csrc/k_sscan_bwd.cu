@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, 
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) g[e][s + k] = mul2(exp2_approx2(mul2(dt2[e], A2[e][s + k])), fma2(c[k], dy2[e], g[e][s + k]));
+            for (int e = 0; e < 2; ++e) g[e][s + k] = mul2(decay2(dt2[e], A2[e][s + k]), fma2(c[k], dy2[e], g[e][s + k]));
         }
       }
     }
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(256) k_sscan_rcompose(SscanParams p) {
     for (int i = 0; i < kAhead; ++i)
       if (s - i >= s0) {
         p.seg_state[(size_t)(s - i) * per + nd] = carry;
-        if (s - i > s0) carry = fmaf(exp2_approx(a2 * t[i]), carry, f[i]);
+        if (s - i > s0) carry = fmaf(decay(t[i], a2), carry, f[i]);
       }
   }
 }
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) k_sscan_bwd(SscanParams p, int
       F2 v[NP / 2];
       sm.B[buf].pairs(v, t);
 #pragma unroll
-      for (int s = 0; s < NP / 2; ++s) to[s] = fma2(exp2_approx2(mul2(dt2, A2[s])), from[s], mul2(dtu2, v[s]));
+      for (int s = 0; s < NP / 2; ++s) to[s] = fma2(decay2(dt2, A2[s]), from[s], mul2(dtu2, v[s]));
     };
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) {
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) k_sscan_bwd(SscanParams p, int
 #pragma unroll
         for (int s = 0; s < NP / 2; ++s) {
           sB = fma2(g[s], v[s], sB);
-          g[s] = mul2(g[s], exp2_approx2(mul2(dt2, A2[s])));
+          g[s] = mul2(g[s], decay2(dt2, A2[s]));
           const F2 x = mul2(g[s], i ? H[i ? i - 1 : 0][s] : h[s]);
           sA = fma2(x, A2[s], sA);
           dA[s] = fma2(x, dt2, dA[s]);

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_pass(SscanParams p, 
           for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              h[e][s + k] = fma2(exp2_approx2(mul2(dt2[e], A2[e][s + k])), h[e][s + k], mul2(dtu2[e], b[k]));
+              h[e][s + k] = fma2(decay2(dt2[e], A2[e][s + k]), h[e][s + k], mul2(dtu2[e], b[k]));
               if (!MAP) y2[e] = fma2(h[e][s + k], c[k], y2[e]);
             }
         }
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(256) k_sscan_compose(SscanParams p) {
     for (int i = 0; i < kAhead; ++i)
       if (s + i < s1) {
         p.seg_state[(size_t)(s + i) * per + nd] = carry;
-        if (s + i < s1 - 1) carry = fmaf(exp2_approx(a2 * t[i]), carry, f[i]);
+        if (s + i < s1 - 1) carry = fmaf(decay(t[i], a2), carry, f[i]);
       }
   }
 }

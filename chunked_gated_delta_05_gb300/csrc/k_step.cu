@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(256) k_sscan_step(SscanStepParams p) {
       const float dt = p.softplus ? softplus(x, &slope) : x, dtu = dt * u;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        h[e] = fmaf(exp2_approx(dt * a[e]), h[e], dtu * B[e]);
+        h[e] = fmaf(decay(dt, a[e]), h[e], dtu * B[e]);
         y = fmaf(h[e], C[e], y);
       }
       y = fmaf(skip, u, y);
