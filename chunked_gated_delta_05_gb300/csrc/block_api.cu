@@ -185,21 +185,20 @@ int validate_sscan(const gdn_sscan_desc_t* d, SscanProblem* P, bool step) {
 // Segments. One CTA walks kSscanChans channels of one segment token by token, so a call needs CTAs enough for every SM;
 // cutting the sequences costs the map pass, which walks all segments but the last ones again. The times compared are in
 // steps of one CTA among others on its SM: whole sequences take the longest one's steps, at `alone` each while the SM has
-// few CTAs, or one CTA after the other when there are more; cut ones take all steps and the map's, evenly spread. Measured
-// at 8192 tokens x 4096 channels (forward): segments of 96, 128, 224, 320 tokens 294, 289, 296, 299 us; backward at 4093
-// packed tokens x 2048 channels, segments of 64, 128, 256: 252, 255, 266 us.
+// few CTAs, or one CTA after the other when there are more; cut ones take all steps and the map's, evenly spread. Of the
+// lengths that fill one to `rounds` rounds of resident CTAs, the one whose rounds and fixed cost per CTA are least is taken.
 struct SscanPlan {
   int L;                 // tokens per segment, a multiple of kSscanCut
   int most;              // most segments of a sequence
   long long segs, cks;   // segments and kept states of all sequences
 };
 constexpr int kSms = 152;
-constexpr int kMinSegment = 64;
+constexpr int kMinSegment = 64, kCtaTokens = 12;
 struct SscanCost {
-  int ctas;              // CTAs of all rounds per SM that the segments are cut for
+  int ctas, first, last; // resident CTAs per SM, and the rounds of them that are tried
   double alone, map;     // a step of a CTA alone on its SM, and of the map pass
 };
-constexpr SscanCost kFwdCost = {14, 2.4, 0.7}, kBwdCost = {8, 1.5, 0.3};
+constexpr SscanCost kFwdCost = {8, 1, 3, 2.4, 0.7}, kBwdCost = {2, 4, 4, 1.5, 0.3};
 
 long long count_segments(const SscanProblem& P, long long L) {
   if (!P.cu) return (P.T + L - 1) / L * P.seqs;
@@ -210,7 +209,7 @@ long long count_segments(const SscanProblem& P, long long L) {
 
 SscanPlan plan_sscan(const SscanProblem& P, bool backward) {
   const SscanCost& c = backward ? kBwdCost : kFwdCost;
-  const long long blocks = sscan_blocks(P.G, P.D / P.G);
+  const long long blocks = sscan_blocks(P.G, P.D / P.G), slots = (long long)kSms * c.ctas;
   int longest = P.T;
   if (P.cu) {
     longest = 0;
@@ -218,15 +217,20 @@ SscanPlan plan_sscan(const SscanProblem& P, bool backward) {
   }
   const double whole = longest * std::max(c.alone, double((P.seqs * blocks + kSms - 1) / kSms));
   const double cut = (1.0 + c.map) * double(P.rows) * blocks / kSms;
-  long long L = ((long long)longest + kSscanCut - 1) / kSscanCut * kSscanCut;
+  const long long all = ((long long)longest + kSscanCut - 1) / kSscanCut * kSscanCut;
+  long long best = all, least = 0;
   if (cut < whole) {
-    const long long unit = (long long)kSms * c.ctas * kSscanCut;
-    L = std::min(L, std::max<long long>(kMinSegment, (P.rows * blocks + unit - 1) / unit * kSscanCut));
+    for (int r = c.first; r <= c.last; ++r) {
+      const long long unit = slots * r * kSscanCut;
+      const long long L = std::min(all, std::max<long long>(kMinSegment, (P.rows * blocks + unit - 1) / unit * kSscanCut));
+      const long long rounds = (count_segments(P, L) * blocks + slots - 1) / slots, cost = rounds * (L + kCtaTokens);
+      if (!least || cost < least) least = cost, best = L;
+    }
   }
   SscanPlan q{};
-  q.L = int(L);
-  q.segs = count_segments(P, L);
-  q.most = int((longest + L - 1) / L);
+  q.L = int(best);
+  q.segs = count_segments(P, best);
+  q.most = int((longest + best - 1) / best);
   q.cks = count_segments(P, kSscanBlock);
   return q;
 }
@@ -318,6 +322,7 @@ void fill(const SscanProblem& P, const SscanPlan& q, const SscanLayout& l, char*
 
 // Whether all channel blocks' rows start on 16-byte boundaries: the tensors, their strides and the groups.
 void set_vectors(const SscanProblem& P, SscanParams* p) {
+  p->vec_A = aligned(p->A, 16);
   p->pair = P.D % 2 == 0 && (P.D / P.G) % 2 == 0;
   const bool groups = P.G == 1 || (P.D / P.G) % 8 == 0;
   p->vec = groups && aligned(p->u, 16) && aligned(p->delta, 16) && aligned(p->z, 16) && aligned(p->dy, 16) && P.u_s % 8 == 0 &&

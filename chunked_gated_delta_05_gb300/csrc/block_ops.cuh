@@ -168,6 +168,7 @@ struct SscanParams {
   const int *cu, *seg_base, *ck_base;  // packed: device arrays [seqs+1] (tokens, segments, kept states), else null
   int softplus;
   bool pair;                   // neighbouring channels of a state row 8-byte aligned
+  bool vec_A;                  // A 16-byte aligned
   bool vec, vec_out;           // u, delta, z (dy): every 8 channels of a block 16-byte aligned; the same of the outputs
   long long u_s, dt_s, z_s, b_s, c_s;  // elements between tokens
   const __nv_bfloat16 *u, *delta, *z, *Bm, *Cm;

@@ -81,6 +81,12 @@ struct BcRegs {
   static constexpr int kPer = TT * NP / kSscanThreads;
   uint16_t r[kPer];
   __device__ __forceinline__ void load(const __nv_bfloat16* src, long long row, int len, int N) {
+    if (len >= TT && N == NP) {
+      const uint16_t* from = reinterpret_cast<const uint16_t*>(src + (threadIdx.x / NP) * row + threadIdx.x % NP);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) r[j] = __ldg(from + j * (kSscanThreads / NP) * row);
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int e = threadIdx.x + j * kSscanThreads, t = e / NP, n = e % NP;
@@ -102,7 +108,13 @@ struct ChTile {
   static constexpr int kPieces = kSscanChans / 8;
   // src: element (first token, first channel); row: elements between tokens; len tokens and chans channels exist.
   __device__ __forceinline__ void load(const __nv_bfloat16* src, long long row, int len, int chans, bool vec) {
-    if (vec) {
+    if (vec && len >= TT && chans == kSscanChans) {  // a whole tile
+      const __nv_bfloat16* from = src + (threadIdx.x / kPieces) * row + threadIdx.x % kPieces * 8;
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&v[0][0])) + threadIdx.x * 16;
+#pragma unroll
+      for (int j = 0; j < TT * kPieces / THREADS; ++j)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * THREADS * 16), "l"(from + j * (THREADS / kPieces) * row) : "memory");
+    } else if (vec) {
 #pragma unroll
       for (int j = 0; j < TT * kPieces / THREADS; ++j) {
         const int e = threadIdx.x + j * THREADS, t = e / kPieces, c = e % kPieces * 8;
@@ -120,7 +132,12 @@ struct ChTile {
   }
   // Writes the tile's valid part to dst; every element must have been written to the tile before a barrier.
   __device__ __forceinline__ void store(__nv_bfloat16* dst, long long row, int len, int chans, bool vec) const {
-    if (vec) {
+    if (vec && len >= TT && chans == kSscanChans) {
+      __nv_bfloat16* to = dst + (threadIdx.x / kPieces) * row + threadIdx.x % kPieces * 8;
+#pragma unroll
+      for (int j = 0; j < TT * kPieces / THREADS; ++j)
+        *reinterpret_cast<uint4*>(to + j * (THREADS / kPieces) * row) = reinterpret_cast<const uint4*>(&v[0][0])[threadIdx.x + j * THREADS];
+    } else if (vec) {
 #pragma unroll
       for (int j = 0; j < TT * kPieces / THREADS; ++j) {
         const int e = threadIdx.x + j * THREADS, t = e / kPieces, c = e % kPieces * 8;
@@ -187,7 +204,17 @@ __device__ __forceinline__ void store_rows(const F2 (*h)[NP / 2], float* row, co
 // log2(e) A of one channel (a padded state then stays 0).
 template <int NP>
 __device__ __forceinline__ void load_A2(F2* A2, const SscanParams& p, int d) {
-  load_states<NP>(A2, p.A + (size_t)d * p.N, 1, p.N);
+  if (p.vec_A && p.N == NP) {
+    const float4* a = reinterpret_cast<const float4*>(p.A + (size_t)d * NP);
+#pragma unroll
+    for (int i = 0; i < NP / 4; ++i) {
+      const float4 q = __ldg(a + i);
+      A2[2 * i] = f2(q.x, q.y);
+      A2[2 * i + 1] = f2(q.z, q.w);
+    }
+  } else {
+    load_states<NP>(A2, p.A + (size_t)d * p.N, 1, p.N);
+  }
 #pragma unroll
   for (int i = 0; i < NP / 2; ++i) A2[i] = mul2(A2[i], dup2(kLog2e));
 }

@@ -20,12 +20,13 @@ constexpr int kTt = 16;  // tokens staged together, double-buffered; a multiple 
 
 template <int NP, bool MAP>
 struct PassSmem {
-  BcTile<NP, kTt> B[2], C[MAP ? 1 : 2];
+  static constexpr int kBc = MAP ? 2 : 1;      // the pass with outputs has a barrier between tiles anyway
+  BcTile<NP, kTt> B[kBc], C[1];
   ChTile<kTt> delta[2], u[2], z[MAP ? 1 : 2];  // y replaces u token by token
 };
 
 template <int NP, bool MAP>
-__global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_pass(SscanParams p, int blocks) {
+__global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   PassSmem<NP, MAP>& sm = *reinterpret_cast<PassSmem<NP, MAP>*>(smem_raw);
   const int seg = blockIdx.x / blocks;
@@ -62,8 +63,8 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_pass(SscanParams p, 
     if (!MAP) rc.load(p.Cm + row * p.c_s + ch.g * p.N, p.c_s, len, p.N);
   };
   auto arrive = [&](int buf) {
-    rb.store(sm.B[buf]);
-    if (!MAP) rc.store(sm.C[buf]);
+    rb.store(sm.B[MAP ? buf : 0]);
+    if (!MAP) rc.store(sm.C[0]);
   };
   request(0, 0);
   arrive(0);
@@ -102,8 +103,8 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_pass(SscanParams p, 
 #pragma unroll
         for (int s = 0; s < NP / 2; s += 2) {
           F2 b[2], c[2];
-          sm.B[buf].quad(b, t0 + i, s / 2);
-          if (!MAP) sm.C[buf].quad(c, t0 + i, s / 2);
+          sm.B[MAP ? buf : 0].quad(b, t0 + i, s / 2);
+          if (!MAP) sm.C[0].quad(c, t0 + i, s / 2);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -124,11 +125,9 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_pass(SscanParams p, 
         }
       }
     }
+    if (!MAP) __syncthreads();
     if (more) arrive(buf ^ 1);
-    if (out) {
-      __syncthreads();
-      sm.u[buf].store(p.y + (sg.row0 + tb) * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
-    }
+    if (out) sm.u[buf].store(p.y + (sg.row0 + tb) * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
   }
   if (MAP) store_rows<NP>(h, p.seg_state + (size_t)seg * p.N * p.D, p, ch);
 #pragma unroll
