@@ -198,7 +198,7 @@ struct SscanCost {
   int ctas, first, last; // resident CTAs per SM, and the rounds of them that are tried
   double alone, map;     // a step of a CTA alone on its SM, and of the map pass
 };
-constexpr SscanCost kFwdCost = {8, 1, 3, 2.4, 0.7}, kBwdCost = {2, 4, 4, 1.5, 0.3};
+constexpr SscanCost kFwdCost = {8, 1, 3, 2.4, 0.7}, kBwdCost = {3, 4, 4, 1.5, 0.3};
 
 long long count_segments(const SscanProblem& P, long long L) {
   if (!P.cu) return (P.T + L - 1) / L * P.seqs;
@@ -256,7 +256,7 @@ SscanLayout layout_sscan(const SscanProblem& P, const SscanPlan& q, bool backwar
     l.seg_dt = take(size_t(q.segs) * P.D * 4);
   }
   if (backward) {
-    l.part_bc = take(size_t(sscan_blocks(P.G, P.D / P.G)) * P.rows * 2 * P.N * 4);
+    l.part_bc = take(size_t(sscan_blocks(P.G, P.D / P.G, kSscanBwdChans)) * P.rows * 2 * P.N * 4);
     l.part_par = take(size_t(q.segs) * (P.N + 2) * P.D * 4);
   }
   l.total = off;
@@ -265,28 +265,32 @@ SscanLayout layout_sscan(const SscanProblem& P, const SscanPlan& q, bool backwar
 
 int check_sscan_size(const SscanProblem& P, const SscanPlan& q) {
   const long long blocks = sscan_blocks(P.G, P.D / P.G);
-  if (blocks * q.segs >= (1ll << 31) || P.rows * P.G * 2 * P.N >= (1ll << 38) || (long long)P.seqs * P.N * P.D >= (1ll << 38))
+  if (2 * blocks * q.segs >= (1ll << 31) || P.rows * P.G * 2 * P.N >= (1ll << 38) || (long long)P.seqs * P.N * P.D >= (1ll << 38))
     return bad("problem too large");
   return GDN_OK;
 }
 
-// The offsets and the running counts of segments and kept states, uploaded through kernel parameters.
+// Offsets, then the running counts of segments, then of kept states (seqs + 1 each), uploaded through kernel parameters: as one
+// array, so that a call with up to kMaxUploadInts / 3 documents takes one launch.
 int upload_tables(const SscanProblem& P, const SscanPlan& q, int* dst, cudaStream_t s) {
+  int32_t buf[kMaxUploadInts];
+  const long long per = P.seqs + 1ll;
+  int fill = 0;
+  long long at = 0;
   for (int which = 0; which < 3; ++which) {
-    int32_t buf[1024];
     long long run = 0;
-    for (int i0 = 0; i0 <= P.seqs; i0 += 1024) {
-      const int n = std::min(1024, P.seqs + 1 - i0);
-      for (int j = 0; j < n; ++j) {
-        const int i = i0 + j;
-        buf[j] = which == 0 ? P.cu[i] : int32_t(run);
-        if (i < P.seqs) run += which == 1 ? (sequence_length(P, i) + q.L - 1) / q.L : (sequence_length(P, i) + kSscanBlock - 1) / kSscanBlock;
+    for (int i = 0; i <= P.seqs; ++i) {
+      buf[fill++] = which == 0 ? P.cu[i] : int32_t(run);
+      if (which && i < P.seqs) run += which == 1 ? (sequence_length(P, i) + q.L - 1) / q.L : (sequence_length(P, i) + kSscanBlock - 1) / kSscanBlock;
+      if (fill == kMaxUploadInts || (which == 2 && i == P.seqs)) {
+        const int rc = upload_offsets(buf, fill, dst + at, s);
+        if (rc) return rc;
+        at += fill;
+        fill = 0;
       }
-      const int rc = upload_offsets(buf, n, dst + (size_t)which * (P.seqs + 1) + i0, s);
-      if (rc) return rc;
     }
   }
-  return GDN_OK;
+  return at == 3 * per ? GDN_OK : bad("internal: table upload");
 }
 
 void fill(const SscanProblem& P, const SscanPlan& q, const SscanLayout& l, char* ws, SscanParams* p) {

@@ -159,6 +159,7 @@ constexpr int kSscanBlock = 8;     // tokens between the states a training forwa
 constexpr int kSscanCut = 32;      // segments are multiples of this
 constexpr int kSscanChans = 128;   // channels per CTA
 constexpr int kSscanThreads = kSscanChans / 2;
+constexpr int kSscanBwdChans = 64; // channels per CTA of the backward's main kernel
 
 struct SscanParams {
   int T, D, N, G, Dg, seqs;    // Dg = D / G channels per group
@@ -188,7 +189,7 @@ struct SscanParams {
   long long rows;
 };
 // Channel blocks of all groups.
-inline int sscan_blocks(int G, int Dg) { return G * ((Dg + kSscanChans - 1) / kSscanChans); }
+inline int sscan_blocks(int G, int Dg, int chans = kSscanChans) { return G * ((Dg + chans - 1) / chans); }
 cudaError_t launch_sscan_fwd(const SscanParams& p, cudaStream_t s);
 cudaError_t launch_sscan_bwd(const SscanParams& p, cudaStream_t s);
 

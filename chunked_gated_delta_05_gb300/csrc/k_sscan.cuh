@@ -48,13 +48,14 @@ struct SscanChan {
   int d[2];
   bool live[2];
 };
+template <int CH = kSscanChans>
 __device__ __forceinline__ SscanChan sscan_chan(const SscanParams& p, int cb) {
-  const int bpg = (p.Dg + kSscanChans - 1) / kSscanChans;
+  const int bpg = (p.Dg + CH - 1) / CH;
   SscanChan c;
   c.g = cb / bpg;
-  const int first = (cb - c.g * bpg) * kSscanChans;
+  const int first = (cb - c.g * bpg) * CH;
   c.d0 = c.g * p.Dg + first;
-  c.chans = min(kSscanChans, p.Dg - first);
+  c.chans = min(CH, p.Dg - first);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int i = 2 * threadIdx.x + e;
@@ -102,49 +103,49 @@ struct BcRegs {
 };
 // TT tokens x kSscanChans channels of a bf16 tensor in shared memory, as they are in memory, zero past the segment's
 // end and the group's channels. Copied in 16-byte pieces where every piece is aligned (`vec`), else by elements.
-template <int TT, int THREADS = kSscanThreads>
+template <int TT, int THREADS = kSscanThreads, int CH = kSscanChans, int PAD = 0>
 struct ChTile {
-  uint16_t v[TT][kSscanChans];
-  static constexpr int kPieces = kSscanChans / 8;
-  // src: element (first token, first channel); row: elements between tokens; len tokens and chans channels exist.
-  __device__ __forceinline__ void load(const __nv_bfloat16* src, long long row, int len, int chans, bool vec) {
-    if (vec && len >= TT && chans == kSscanChans) {  // a whole tile
-      const __nv_bfloat16* from = src + (threadIdx.x / kPieces) * row + threadIdx.x % kPieces * 8;
-      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&v[0][0])) + threadIdx.x * 16;
+  uint16_t v[TT][CH + PAD];
+  static constexpr int kPieces = CH / 8;
+  // Thread tid of THREADS. src: element (first token, first channel); row: elements between tokens; len tokens and chans channels exist.
+  __device__ __forceinline__ void load(const __nv_bfloat16* src, long long row, int len, int chans, bool vec, int tid = threadIdx.x) {
+    if (vec && len >= TT && chans == CH) {  // a whole tile
+      const __nv_bfloat16* from = src + (tid / kPieces) * row + tid % kPieces * 8;
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&v[tid / kPieces][tid % kPieces * 8]));
 #pragma unroll
       for (int j = 0; j < TT * kPieces / THREADS; ++j)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * THREADS * 16), "l"(from + j * (THREADS / kPieces) * row) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * (THREADS / kPieces) * (CH + PAD) * 2), "l"(from + j * (THREADS / kPieces) * row) : "memory");
     } else if (vec) {
 #pragma unroll
       for (int j = 0; j < TT * kPieces / THREADS; ++j) {
-        const int e = threadIdx.x + j * THREADS, t = e / kPieces, c = e % kPieces * 8;
+        const int e = tid + j * THREADS, t = e / kPieces, c = e % kPieces * 8;
         const int bytes = t < len ? max(0, min(8, chans - c)) * 2 : 0;
         const __nv_bfloat16* from = bytes ? src + t * row + c : src;
         const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&v[t][c]));
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
       }
     } else {
-      for (int c = threadIdx.x; c < kSscanChans; c += THREADS)
+      for (int c = tid; c < CH; c += THREADS)
 #pragma unroll 8
         for (int t = 0; t < TT; ++t)
           v[t][c] = t < len && c < chans ? __ldg(reinterpret_cast<const uint16_t*>(src + t * row + c)) : uint16_t(0);
     }
   }
   // Writes the tile's valid part to dst; every element must have been written to the tile before a barrier.
-  __device__ __forceinline__ void store(__nv_bfloat16* dst, long long row, int len, int chans, bool vec) const {
-    if (vec && len >= TT && chans == kSscanChans) {
-      __nv_bfloat16* to = dst + (threadIdx.x / kPieces) * row + threadIdx.x % kPieces * 8;
+  __device__ __forceinline__ void store(__nv_bfloat16* dst, long long row, int len, int chans, bool vec, int tid = threadIdx.x) const {
+    if (vec && len >= TT && chans == CH) {
+      __nv_bfloat16* to = dst + (tid / kPieces) * row + tid % kPieces * 8;
 #pragma unroll
       for (int j = 0; j < TT * kPieces / THREADS; ++j)
-        *reinterpret_cast<uint4*>(to + j * (THREADS / kPieces) * row) = reinterpret_cast<const uint4*>(&v[0][0])[threadIdx.x + j * THREADS];
+        *reinterpret_cast<uint4*>(to + j * (THREADS / kPieces) * row) = *reinterpret_cast<const uint4*>(&v[tid / kPieces + j * (THREADS / kPieces)][tid % kPieces * 8]);
     } else if (vec) {
 #pragma unroll
       for (int j = 0; j < TT * kPieces / THREADS; ++j) {
-        const int e = threadIdx.x + j * THREADS, t = e / kPieces, c = e % kPieces * 8;
+        const int e = tid + j * THREADS, t = e / kPieces, c = e % kPieces * 8;
         if (t < len && c < chans) *reinterpret_cast<uint4*>(dst + t * row + c) = *reinterpret_cast<const uint4*>(&v[t][c]);
       }
     } else {
-      for (int c = threadIdx.x; c < kSscanChans; c += THREADS)
+      for (int c = tid; c < CH; c += THREADS)
         for (int t = 0; t < TT; ++t)
           if (t < len && c < chans) reinterpret_cast<uint16_t*>(dst)[t * row + c] = v[t][c];
     }

@@ -4,12 +4,12 @@
 //   w = dh_t a_t h_{t-1},  dA = sum_t w dt,  ddt = u (B . dh) + A . w,  ddelta = ddt sigmoid(delta + bias),
 //   dz = dy (C . h + D u) silu'(z),  dD = sum_t dy0 u,  dh0 = a_1 dh_1.
 //
-// One thread walks one channel. The states it needs in reverse come from those a training forward keeps before every 8th
+// Two lanes walk one channel. The states they need in reverse come from those a training forward keeps before every 8th
 // token (8 bytes a token and channel): each tile of 8, last to first, is run forward again and then walked back. Keeping
 // fewer costs another forward walk, which this kernel, bound by its instructions at 7% of HBM's rate, cannot hide as it
 // does the reads. The adjoint chain is cut into segments like the forward's. The sums over channels in dB and dC begin as matrix products with ones: a
 // lane's four states are its share of the A operand of m16n8k8, whose products add up four lanes' channels (tf32 operands;
-// the results are bf16), and seven exchanges add up the eight groups of lanes. All other sums are fp32.
+// the results are bf16), and three exchanges add up the groups of lanes. All other sums are fp32.
 #include "k_sscan.cuh"
 
 namespace gdn {
@@ -138,47 +138,45 @@ __device__ __forceinline__ void mma_tf32(float* d, float a0, float a1, float a2,
         "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// Sums over the four channels of lanes 4 r .. 4 r + 3 of NP values a lane (pairs over states): states 4 j .. 4 j + 3 enter
-// product j as A, whose B has ones in column 2 j for k < 4 and in column 2 j + 1 for k >= 4 (sel). Lane 4 r + j then holds the
-// sums of states 4 j + {0, 2, 1, 3} of the four lanes.
-template <int NP>
-__device__ __forceinline__ void channel_sum(float* c, const F2* v, const float (*sel)[2]) {
-  const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < NP / 4; ++j) {
-    float a0, a1, a2, a3;
-    unf2(v[2 * j], &a0, &a1);
-    unf2(v[2 * j + 1], &a2, &a3);
-    mma_tf32(c, a0, a1, a2, a3, sel[j][0], sel[j][1], j ? c : zero);
-  }
-}
 // One value for two lanes: the lane with `up` keeps b, the other a, each plus the other lane's.
 __device__ __forceinline__ float exchange(float a, float b, bool up, int mask) {
   return (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, mask);
 }
 
-// ------------------------------------------------------------------ one channel a thread, states in pairs
+// ------------------------------------------------------------------ two lanes a channel, states in pairs
 
-constexpr int kBwdThreads = kSscanChans;
-constexpr int kWarps = kBwdThreads / 32;
+constexpr int kBwdChans = kSscanBwdChans, kBwdThreads = 2 * kBwdChans, kWarps = kBwdThreads / 32;
 constexpr int kTile = kSscanBlock, kHalf = kTile / 2;
+constexpr int kBwdRow = kBwdChans + 2;  // a lane's states and tokens lie 16 banks from the other half's
 
-// A tile of tokens of B or C as fp32, [token][NP]: one element a thread.
+// A tile of tokens of B or C as fp32, [token][NP], filled by kBwdChans threads.
 template <int NP>
 struct VecTile {
+  static constexpr int kPer = (kTile * NP + kBwdChans - 1) / kBwdChans;
+  struct Raw {
+    uint16_t r[kPer];
+  };
   float v[kTile][NP];
-  static_assert(kTile * NP <= kBwdThreads, "one element a thread");
-  __device__ __forceinline__ static uint16_t fetch(const __nv_bfloat16* src, long long row, int len, int N) {
-    const int t = threadIdx.x / NP, n = threadIdx.x % NP;
-    return t < len && t < kTile && n < N ? __ldg(reinterpret_cast<const uint16_t*>(src + t * row + n)) : uint16_t(0);
-  }
-  __device__ __forceinline__ void put(uint16_t r) {
-    if (threadIdx.x < kTile * NP) (&v[0][0])[threadIdx.x] = __uint_as_float(uint32_t(r) << 16);
-  }
-  __device__ __forceinline__ void pairs(F2* out, int t) const {
+  __device__ __forceinline__ static Raw fetch(const __nv_bfloat16* src, long long row, int len, int N, int tid) {
+    Raw x;
 #pragma unroll
-    for (int i = 0; i < NP / 4; ++i) {
-      const float4 q = reinterpret_cast<const float4*>(v[t])[i];
+    for (int j = 0; j < kPer; ++j) {
+      const int e = tid + j * kBwdChans, t = e / NP, n = e % NP;
+      x.r[j] = t < len && t < kTile && n < N ? __ldg(reinterpret_cast<const uint16_t*>(src + t * row + n)) : uint16_t(0);
+    }
+    return x;
+  }
+  __device__ __forceinline__ void put(const Raw& x, int tid) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (tid + j * kBwdChans < kTile * NP) (&v[0][0])[tid + j * kBwdChans] = __uint_as_float(uint32_t(x.r[j]) << 16);
+  }
+  // States n0 .. n0 + 2 PAIRS - 1 of token t.
+  template <int PAIRS>
+  __device__ __forceinline__ void pairs(F2* out, int t, int n0) const {
+#pragma unroll
+    for (int i = 0; i < PAIRS / 2; ++i) {
+      const float4 q = reinterpret_cast<const float4*>(&v[t][n0])[i];
       out[2 * i] = f2(q.x, q.y);
       out[2 * i + 1] = f2(q.z, q.w);
     }
@@ -188,210 +186,214 @@ struct VecTile {
 template <int NP>
 struct BwdSmem {
   VecTile<NP> B[2], C[2];
-  ChTile<kTile, kBwdThreads> u[2], delta[2], z[2], dy[2];  // du, ddelta and dz replace u, delta and z token by token
-  float ck[2][NP][kBwdThreads];                            // states before the tile
-  float4 H[kHalf][NP / 4][kBwdThreads];                    // states after the tokens of the tile's first half
-  float2 dts[kTile][kBwdThreads];                          // dt and d dt / d delta
-  float red[kWarps][kTile][2][16];                         // the warps' sums over their channels: dC, dB
+  ChTile<kTile, kBwdChans, kBwdChans, 8> u[2], delta[2], z[2], dy[2];  // du, ddelta and dz replace u, delta and z
+  float ck[2][NP][kBwdRow];                              // states before the tile
+  float4 tok[kTile][kBwdChans];                          // a token's dt, dt u, dy silu(z), d dt / d delta
+  float4 sums[2][kTile][kBwdChans];                      // each lane's share of C . h, B . dh and A . w
+  float red[kWarps][kTile][2][NP];                         // the warps' sums over their channels: dC, dB
 };
 
-// Tile by tile, the last first: forward over the tile's tokens, whose states stay in shared memory (first half) and
-// registers (second half), then back over them.
+// Tile by tile, the last first: forward over the tile's tokens, whose states stay in registers, then back over them. A channel
+// takes two lanes of a warp, 16 apart, each with half of the states: that leaves registers for a whole tile's states and for
+// four warps a scheduler, and each lane does the scalar work (step size, gates, their gradients) of half of the tile's tokens.
 template <int NP>
-__global__ void __launch_bounds__(kBwdThreads, 2) k_sscan_bwd(SscanParams p, int blocks) {
+__global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int blocks) {
+  constexpr int SP = NP / 2, PR = SP / 2, NQ = SP / 4;  // states, state pairs and quads of a lane
   extern __shared__ __align__(16) char smem_raw[];
   BwdSmem<NP>& sm = *reinterpret_cast<BwdSmem<NP>*>(smem_raw);
   const int seg = blockIdx.x / blocks, cb = blockIdx.x % blocks;
   const SscanSeg sg = sscan_seg(p, seg);
-  const SscanChan ch = sscan_chan(p, cb);
-  const int tid = threadIdx.x, d = ch.d0 + min(tid, ch.chans - 1), lane = tid & 31, warp = tid >> 5;
-  const bool gate = p.z != nullptr, softplus_on = p.softplus, live = tid < ch.chans;
-  float sel[NP / 4][2];
+  const SscanChan ch = sscan_chan<kBwdChans>(p, cb);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = lane >> 4, part = tid & (kBwdChans - 1);
+  const int c = warp * 16 + (lane & 15), d = ch.d0 + min(c, ch.chans - 1), n0 = half * SP, ns = p.N - n0;
+  const bool gate = p.z != nullptr, softplus_on = p.softplus, live = c < ch.chans, low = tid < kBwdChans;
+  // The products below put quad j of dC (dB) into columns 2 j and 2 j + 1 (4 + 2 j and 4 + 2 j + 1).
+  float sel[2 * NQ][2];
 #pragma unroll
-  for (int j = 0; j < NP / 4; ++j) {
-    sel[j][0] = (lane >> 2) == 2 * j ? 1.f : 0.f;
-    sel[j][1] = (lane >> 2) == 2 * j + 1 ? 1.f : 0.f;
+  for (int j = 0; j < NQ; ++j)
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sel[w * NQ + j][e] = (lane >> 2) == w * 4 + 2 * j + e ? 1.f : 0.f;
+  F2 A2[PR], g[PR], dA[PR];
+  load_states<SP>(A2, p.A + (size_t)d * p.N + n0, 1, ns);
+#pragma unroll
+  for (int i = 0; i < PR; ++i) {
+    A2[i] = mul2(A2[i], dup2(kLog2e));
+    g[i] = dA[i] = f2(0.f, 0.f);
   }
-  F2 A2[NP / 2], g[NP / 2], dA[NP / 2];
-  load_A2<NP>(A2, p, d);
-#pragma unroll
-  for (int i = 0; i < NP / 2; ++i) g[i] = dA[i] = f2(0.f, 0.f);
   if (live) {
-    if (p.seg_state) load_states<NP>(g, p.seg_state + (size_t)seg * p.N * p.D + d, p.D, p.N);
-    else if (p.dfinal) load_states<NP>(g, p.dfinal + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);
+    if (p.seg_state) load_states<SP>(g, p.seg_state + ((size_t)seg * p.N + n0) * p.D + d, p.D, ns);
+    else if (p.dfinal) load_states<SP>(g, p.dfinal + ((size_t)sg.seq * p.D + d) * p.N + n0, 1, ns);
   }
   const float bias = param(p.bias, d), skip = param(p.Dskip, d);
   float dD = 0.f, dbias = 0.f;
-  uint16_t rb, rc;
+  typename VecTile<NP>::Raw raw;
   auto request = [&](int tb, int buf) {
     const long long row = sg.row0 + tb;
     const int len = sg.len - tb;
-    sm.u[buf].load(p.u + row * p.u_s + ch.d0, p.u_s, len, ch.chans, p.vec);
-    sm.delta[buf].load(p.delta + row * p.dt_s + ch.d0, p.dt_s, len, ch.chans, p.vec);
-    sm.dy[buf].load(p.dy + row * p.D + ch.d0, p.D, len, ch.chans, p.vec);
-    if (gate) sm.z[buf].load(p.z + row * p.z_s + ch.d0, p.z_s, len, ch.chans, p.vec);
+    if (low) {
+      sm.u[buf].load(p.u + row * p.u_s + ch.d0, p.u_s, len, ch.chans, p.vec, part);
+      sm.delta[buf].load(p.delta + row * p.dt_s + ch.d0, p.dt_s, len, ch.chans, p.vec, part);
+      raw = VecTile<NP>::fetch(p.Bm + row * p.b_s + ch.g * p.N, p.b_s, len, p.N, part);
+    } else {
+      sm.dy[buf].load(p.dy + row * p.D + ch.d0, p.D, len, ch.chans, p.vec, part);
+      if (gate) sm.z[buf].load(p.z + row * p.z_s + ch.d0, p.z_s, len, ch.chans, p.vec, part);
+      raw = VecTile<NP>::fetch(p.Cm + row * p.c_s + ch.g * p.N, p.c_s, len, p.N, part);
+    }
     const float* ck = p.ck + (size_t)(sg.ck0 + tb / kTile) * p.N * p.D + d;
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&sm.ck[buf][0][tid]));
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&sm.ck[buf][n0][c]));
 #pragma unroll
-    for (int n = 0; n < NP; ++n)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + n * kBwdThreads * 4), "l"(ck + (size_t)min(n, p.N - 1) * p.D),
-                   "r"(n < p.N ? 4 : 0)
+    for (int n = 0; n < SP; ++n)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + n * kBwdRow * 4), "l"(ck + (size_t)min(n0 + n, p.N - 1) * p.D),
+                   "r"(n < ns ? 4 : 0)
                    : "memory");
     copies_commit();
-    rb = VecTile<NP>::fetch(p.Bm + row * p.b_s + ch.g * p.N, p.b_s, len, p.N);
-    rc = VecTile<NP>::fetch(p.Cm + row * p.c_s + ch.g * p.N, p.c_s, len, p.N);
   };
+  auto arrive = [&](int buf) { (low ? sm.B[buf] : sm.C[buf]).put(raw, part); };
   const int last = (sg.len - 1) / kTile * kTile;
   request(last, 0);
-  sm.B[0].put(rb);
-  sm.C[0].put(rc);
+  arrive(0);
   for (int tb = last, buf = 0; tb >= 0; tb -= kTile, buf ^= 1) {
     const int len = min(kTile, sg.len - tb);
     const long long row = sg.row0 + tb;
     copies_wait();
     __syncthreads();
     if (tb > 0) request(tb - kTile, buf ^ 1);
-    // No branch in a token's work: past the segment's end dt and d dt / d delta are 0, dy is 0, and the state stays.
-    F2 h[NP / 2], H[kHalf][NP / 2];
-#pragma unroll
-    for (int i = 0; i < NP / 2; ++i) h[i] = f2(sm.ck[buf][2 * i][tid], sm.ck[buf][2 * i + 1][tid]);
-    auto forward = [&](int t, const F2* from, F2* to) {
-      const float x = sm.delta[buf].one(t, tid) + bias, u = sm.u[buf].one(t, tid);
-      float slope, dt = softplus(x, &slope);
-      dt = t < len ? (softplus_on ? dt : x) : 0.f;
-      slope = t < len ? (softplus_on ? slope : 1.f) : 0.f;
-      sm.dts[t][tid] = make_float2(dt, slope);
-      const F2 dt2 = dup2(dt), dtu2 = dup2(dt * u);
-      F2 v[NP / 2];
-      sm.B[buf].pairs(v, t);
-#pragma unroll
-      for (int s = 0; s < NP / 2; ++s) to[s] = fma2(decay2(dt2, A2[s]), from[s], mul2(dtu2, v[s]));
-    };
+    // The lane's half of the tokens. Past the segment's end dt and d dt / d delta are 0, dy is 0, and the state stays.
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) {
-      forward(i, h, h);
+      const int t = half * kHalf + i;
+      const float x = sm.delta[buf].one(t, c) + bias, u = sm.u[buf].one(t, c), dy = sm.dy[buf].one(t, c), z = sm.z[buf].one(t, c);
+      float slope;
+      const float sp = softplus(x, &slope), dt = t < len ? (softplus_on ? sp : x) : 0.f;
+      sm.tok[t][c] = make_float4(dt, dt * u, gate ? dy * (z * sigmoid_fast(z)) : dy, t < len ? (softplus_on ? slope : 1.f) : 0.f);
+    }
+    __syncwarp();
+    F2 H[kTile][PR];
+    auto before = [&](int t, int s) { return t ? H[t ? t - 1 : 0][s] : f2(sm.ck[buf][n0 + 2 * s][c], sm.ck[buf][n0 + 2 * s + 1][c]); };
 #pragma unroll
-      for (int s = 0; s < NP / 4; ++s) {
-        float4 q;
-        unf2(h[2 * s], &q.x, &q.y);
-        unf2(h[2 * s + 1], &q.z, &q.w);
-        sm.H[i][s][tid] = q;
-      }
+    for (int t = 0; t < kTile; ++t) {
+      const float2 q = *reinterpret_cast<const float2*>(&sm.tok[t][c]);
+      const F2 dt2 = dup2(q.x), dtu2 = dup2(q.y);
+      F2 v[PR];
+      sm.B[buf].template pairs<PR>(v, t, n0);
+#pragma unroll
+      for (int s = 0; s < PR; ++s) H[t][s] = fma2(decay2(dt2, A2[s]), before(t, s), mul2(dtu2, v[s]));
     }
 #pragma unroll
-    for (int i = 0; i < kHalf; ++i) forward(kHalf + i, i ? H[i ? i - 1 : 0] : h, H[i]);
-#pragma unroll 1
-    for (int half = 1; half >= 0; --half) {
-      if (half == 0) {
+    for (int t = kTile - 1; t >= 0; --t) {
+      const float4 q = sm.tok[t][c];
+      const F2 dt2 = dup2(q.x), dtu2 = dup2(q.y), dy2 = dup2(q.z);
+      F2 v[PR], w[2][PR];
+      sm.C[buf].template pairs<PR>(v, t, n0);
+      F2 y2 = f2(0.f, 0.f), sB = f2(0.f, 0.f), sA = f2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i)
-#pragma unroll
-          for (int s = 0; s < NP / 4; ++s) {
-            const float4 q = sm.H[i][s][tid];
-            H[i][2 * s] = f2(q.x, q.y);
-            H[i][2 * s + 1] = f2(q.z, q.w);
-          }
-#pragma unroll
-        for (int i = 0; i < NP / 2; ++i) h[i] = f2(sm.ck[buf][2 * i][tid], sm.ck[buf][2 * i + 1][tid]);
+      for (int s = 0; s < PR; ++s) {
+        y2 = fma2(H[t][s], v[s], y2);
+        g[s] = fma2(v[s], dy2, g[s]);
+        w[0][s] = mul2(H[t][s], dy2);
+        w[1][s] = mul2(g[s], dtu2);
       }
+      // Sums over the four channels of each four lanes: a lane's quad of states is its share of A, ones in B pick columns.
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = kHalf - 1; i >= 0; --i) {
-        const int t = half * kHalf + i;
-        const float u = sm.u[buf].one(t, tid), dy = sm.dy[buf].one(t, tid), z = sm.z[buf].one(t, tid);
-        const float2 ds = sm.dts[t][tid];
-        const float dt = ds.x, sig = sigmoid_fast(z), dy0 = gate ? dy * (z * sig) : dy;
-        const F2 dt2 = dup2(dt), dtu2 = dup2(dt * u), dy2 = dup2(dy0);
-        float cC[4], cB[4];
-        F2 v[NP / 2], w[NP / 2];
-        sm.C[buf].pairs(v, t);
-        F2 y2 = f2(skip * u, 0.f), sB = f2(0.f, 0.f), sA = f2(0.f, 0.f);
-#pragma unroll
-        for (int s = 0; s < NP / 2; ++s) {
-          y2 = fma2(H[i][s], v[s], y2);
-          g[s] = fma2(v[s], dy2, g[s]);
-          w[s] = mul2(H[i][s], dy2);
-        }
-        channel_sum<NP>(cC, w, sel);
-#pragma unroll
-        for (int s = 0; s < NP / 2; ++s) w[s] = mul2(g[s], dtu2);
-        channel_sum<NP>(cB, w, sel);
-        sm.B[buf].pairs(v, t);
-#pragma unroll
-        for (int s = 0; s < NP / 2; ++s) {
-          sB = fma2(g[s], v[s], sB);
-          g[s] = mul2(g[s], decay2(dt2, A2[s]));
-          const F2 x = mul2(g[s], i ? H[i ? i - 1 : 0][s] : h[s]);
-          sA = fma2(x, A2[s], sA);
-          dA[s] = fma2(x, dt2, dA[s]);
-        }
-        const float dhB = sum2(sB);
-        const float ddt = fmaf(u, dhB, 0.6931471805599453f * sum2(sA)), dd = ddt * ds.y;
-        dD = fmaf(dy0, u, dD);
-        dbias += dd;
-        sm.u[buf].set_one(t, tid, fmaf(dt, dhB, skip * dy0));
-        sm.delta[buf].set_one(t, tid, dd);
-        sm.z[buf].set_one(t, tid, dy * sum2(y2) * (sig * fmaf(z, 1.f - sig, 1.f)));
-        // the eight sums of lane 4 r + j over its four lanes, added up over r, of which each lane ends with one
-        const bool r0 = lane & 4, r1 = lane & 8, r2 = lane & 16;
-        const float k0 = exchange(cC[0], cB[0], r0, 4), k1 = exchange(cC[1], cB[1], r0, 4);
-        const float k2 = exchange(cC[2], cB[2], r0, 4), k3 = exchange(cC[3], cB[3], r0, 4);
-        const float l0 = exchange(k0, k1, r1, 8), l1 = exchange(k2, k3, r1, 8);
-        // accumulator 0, 1, 2, 3 = states 4 j + 0, 2, 1, 3
-        sm.red[warp][t][r0][(lane & 3) * 4 + (r1 ? 2 : 0) + (r2 ? 1 : 0)] = exchange(l0, l1, r2, 16);
+      for (int j = 0; j < 2 * NQ; ++j) {
+        const F2* q4 = &w[j / NQ][2 * (j % NQ)];
+        float a0, a1, a2, a3;
+        unf2(q4[0], &a0, &a1);
+        unf2(q4[1], &a2, &a3);
+        mma_tf32(acc, a0, a1, a2, a3, sel[j][0], sel[j][1], acc);
       }
+      sm.B[buf].template pairs<PR>(v, t, n0);
+#pragma unroll
+      for (int s = 0; s < PR; ++s) {
+        sB = fma2(g[s], v[s], sB);
+        g[s] = mul2(g[s], decay2(dt2, A2[s]));
+        const F2 x = mul2(g[s], before(t, s));
+        sA = fma2(x, A2[s], sA);
+        dA[s] = fma2(x, dt2, dA[s]);
+      }
+      sm.sums[half][t][c] = make_float4(sum2(y2), sum2(sB), sum2(sA), 0.f);
+      // Lane 4 r + i now holds quad i % 2 of dC (i < 2) or dB, states 0, 2, 1, 3 in acc[0 .. 3], of the four lanes r: added up
+      // over the half's four r, each lane ends with one.
+      const bool r0 = lane & 4, r1 = lane & 8;
+      const float k0 = exchange(acc[0], acc[1], r0, 4), k1 = exchange(acc[2], acc[3], r0, 4), r = exchange(k0, k1, r1, 8);
+      if ((lane & 1) < NQ) sm.red[warp][t][(lane >> 1) & 1][n0 + (lane & 1) * 4 + (r0 ? 2 : 0) + (r1 ? 1 : 0)] = r;
     }
-    if (tb > 0) {
-      sm.B[buf ^ 1].put(rb);
-      sm.C[buf ^ 1].put(rc);
+    __syncwarp();
+    // Both lanes' shares together; each lane ends its half of the tokens.
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      const int t = half * kHalf + i;
+      const float4 s0 = sm.sums[0][t][c], s1 = sm.sums[1][t][c];
+      const float y = s0.x + s1.x, dhB = s0.y + s1.y, w = s0.z + s1.z;
+      const float4 q = sm.tok[t][c];
+      const float u = sm.u[buf].one(t, c), dy = sm.dy[buf].one(t, c), z = sm.z[buf].one(t, c), sig = sigmoid_fast(z);
+      const float dd = fmaf(u, dhB, 0.6931471805599453f * w) * q.w;
+      dD = fmaf(q.z, u, dD);
+      dbias += dd;
+      sm.u[buf].set_one(t, c, fmaf(q.x, dhB, skip * q.z));
+      sm.delta[buf].set_one(t, c, dd);
+      sm.z[buf].set_one(t, c, dy * fmaf(skip, u, y) * (sig * fmaf(z, 1.f - sig, 1.f)));
     }
+    if (tb > 0) arrive(buf ^ 1);
     __syncthreads();
-    sm.u[buf].store(p.du + row * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
-    sm.delta[buf].store(p.ddelta + row * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
-    if (gate) sm.z[buf].store(p.dz + row * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
+    if (low) {
+      sm.u[buf].store(p.du + row * p.D + ch.d0, p.D, len, ch.chans, p.vec_out, part);
+      sm.delta[buf].store(p.ddelta + row * p.D + ch.d0, p.D, len, ch.chans, p.vec_out, part);
+    } else if (gate) {
+      sm.z[buf].store(p.dz + row * p.D + ch.d0, p.D, len, ch.chans, p.vec_out, part);
+    }
     // partial dC and dB of the tile: [token][dC, dB][N]
-    float* part = p.part_bc + ((size_t)cb * p.rows + row) * 2 * p.N;
 #pragma unroll
-    for (int j = 0; j < kTile * 32 / kBwdThreads; ++j) {
-      const int e = tid + j * kBwdThreads, t = e / 32, which = e / 16 % 2, n = e % 16;
+    for (int e = tid; e < kTile * 32; e += kBwdThreads) {
+      const int t = e / 32, which = e / 16 % 2, n = e % 16;
       float r = 0.f;
+      if (n < NP)
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) r += sm.red[k][t][which][n];
-      if (t < len && n < p.N) part[(t * 2 + which) * p.N + n] = r;
+        for (int k = 0; k < kWarps; ++k) r += sm.red[k][t][which][n];
+      if (t < len && n < p.N) p.part_bc[((size_t)cb * p.rows + row + t) * 2 * p.N + which * p.N + n] = r;
     }
   }
+  dD += __shfl_xor_sync(0xffffffffu, dD, 16);
+  dbias += __shfl_xor_sync(0xffffffffu, dbias, 16);
   if (!live) return;
-  if (p.dh0 && sg.j == 0) store_states<NP>(g, p.dh0 + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);
+  if (p.dh0 && sg.j == 0) store_states<SP>(g, p.dh0 + ((size_t)sg.seq * p.D + d) * p.N + n0, 1, ns);
   float* par = p.part_par + (size_t)seg * (p.N + 2) * p.D + d;
-  store_states<NP>(dA, par, p.D, p.N);
-  par[(size_t)p.N * p.D] = dD;
-  par[(size_t)(p.N + 1) * p.D] = dbias;
+  store_states<SP>(dA, par + (size_t)n0 * p.D, p.D, ns);
+  if (half == 0) {
+    par[(size_t)p.N * p.D] = dD;
+    par[(size_t)(p.N + 1) * p.D] = dbias;
+  }
 }
 
-// dC and dB of one (row, group, state): the sum over the group's channel blocks, in order.
-__global__ void __launch_bounds__(256) k_sscan_sum_bc(SscanParams p, int bpg) {
-  const long long at = (long long)blockIdx.x * 256 + threadIdx.x, per = 2ll * p.N;
-  if (at >= p.rows * p.G * per) return;
-  const int w = int(at % per), which = w / p.N, n = w - which * p.N;
-  const long long rg = at / per, row = rg / p.G;
-  const int g = int(rg - row * p.G);
-  float s = 0.f;
-  for (int k = 0; k < bpg; ++k) s += p.part_bc[((size_t)(g * bpg + k) * p.rows + row) * per + w];
-  (which ? p.dB : p.dC)[(row * p.G + g) * p.N + n] = __float2bfloat16_rn(s);
-}
-
-// dA, dD and ddelta_bias of one channel: the sum over the segments, in a fixed order. 32 channels x 8 segment lanes.
-__global__ void __launch_bounds__(256) k_sscan_sum_par(SscanParams p) {
+// The last sums, in one launch. Blocks below `bc`: dC and dB of one (row, group, state) a thread, over the group's channel
+// blocks in order. The others: dA, dD and ddelta_bias of 32 channels x 8 segment lanes, over the segments in a fixed order.
+__global__ void __launch_bounds__(256) k_sscan_sums(SscanParams p, int bpg, int bc) {
   __shared__ float s[8][33];
-  const int d = blockIdx.x * 32 + threadIdx.x, k = blockIdx.y;
+  if (int(blockIdx.x) < bc) {
+    const long long at = (long long)blockIdx.x * 256 + threadIdx.x, per = 2ll * p.N;
+    if (at >= p.rows * p.G * per) return;
+    const int w = int(at % per), which = w / p.N, n = w - which * p.N;
+    const long long rg = at / per, row = rg / p.G;
+    const int g = int(rg - row * p.G);
+    float t = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < bpg; ++k) t += p.part_bc[((size_t)(g * bpg + k) * p.rows + row) * per + w];
+    (which ? p.dB : p.dC)[(row * p.G + g) * p.N + n] = __float2bfloat16_rn(t);
+    return;
+  }
+  const int b = blockIdx.x - bc, k = b % (p.N + 2), x = threadIdx.x & 31, y = threadIdx.x >> 5, d = b / (p.N + 2) * 32 + x;
   float t = 0.f;
   if (d < p.D)
-#pragma unroll 4
-    for (int i = threadIdx.y; i < p.segs; i += 8) t += p.part_par[((size_t)i * (p.N + 2) + k) * p.D + d];
-  s[threadIdx.y][threadIdx.x] = t;
+#pragma unroll 8
+    for (int i = y; i < p.segs; i += 8) t += p.part_par[((size_t)i * (p.N + 2) + k) * p.D + d];
+  s[y][x] = t;
   __syncthreads();
-  if (threadIdx.y || d >= p.D) return;
+  if (y || d >= p.D) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) t += s[i][threadIdx.x];
+  for (int i = 1; i < 8; ++i) t += s[i][x];
   if (k < p.N) p.dA[(size_t)d * p.N + k] = t;
   else if (k == p.N && p.dD) p.dD[d] = t;
   else if (k == p.N + 1 && p.dbias) p.dbias[d] = t;
@@ -408,10 +410,10 @@ cudaError_t run(const SscanParams& p, cudaStream_t s) {
   const int smem = int(sizeof(BwdSmem<NP>));
   cudaError_t e = cudaFuncSetAttribute(k_sscan_bwd<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k_sscan_bwd<NP><<<grid, kBwdThreads, smem, s>>>(p, blocks);
-  const long long n = p.rows * p.G * 2 * p.N;
-  k_sscan_sum_bc<<<int((n + 255) / 256), 256, 0, s>>>(p, blocks / p.G);
-  k_sscan_sum_par<<<dim3((p.D + 31) / 32, p.N + 2), dim3(32, 8), 0, s>>>(p);
+  const int bblocks = sscan_blocks(p.G, p.Dg, kBwdChans);
+  k_sscan_bwd<NP><<<bblocks * p.segs, kBwdThreads, smem, s>>>(p, bblocks);
+  const int bc = int((p.rows * p.G * 2 * p.N + 255) / 256);
+  k_sscan_sums<<<bc + (p.D + 31) / 32 * (p.N + 2), 256, 0, s>>>(p, bblocks / p.G, bc);
   return cudaGetLastError();
 }
 
