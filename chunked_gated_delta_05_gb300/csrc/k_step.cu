@@ -226,70 +226,97 @@ __global__ void __launch_bounds__(256) k_delta_step(DeltaStepParams p) {
 
 // ------------------------------------------------------------------ selective scan
 
-// LPC lanes per channel, four states each. A block walks its channels over several batch rows: A, D and the bias are read
-// once, and the next row's slot is known before this one's state is stored. VEC: the states, A, B and C in 16- and 8-byte
-// pieces (N a multiple of 4 and everything aligned).
-template <int LPC, bool VEC>
-__global__ void __launch_bounds__(256) k_sscan_step(SscanStepParams p) {
-  const int i = blockIdx.x * 256 + threadIdx.x, d = i / LPC, n0 = (i % LPC) * 4;
-  const bool live = d < p.D;
-  const int dc = live ? d : p.D - 1, ns = min(4, p.N - n0);
-  float a[4] = {0.f, 0.f, 0.f, 0.f};
-  if (VEC && ns > 0) {
-    const float4 av = __ldg(reinterpret_cast<const float4*>(p.A + (size_t)dc * p.N + n0));
-    a[0] = kLog2e * av.x, a[1] = kLog2e * av.y, a[2] = kLog2e * av.z, a[3] = kLog2e * av.w;
-  } else {
+// LPC lanes per channel, eight states each. A block walks its channels over several batch rows: A, D and the bias are read
+// once, a row's loads are in flight while the one before it is computed, and its slot is known a row earlier still. VEC: the
+// states, A, B and C in 16- and 8-byte pieces (N a multiple of 4 and everything aligned).
+template <bool VEC>
+struct SscanRow {
+  int slot;
+  float h[8];
+  uint2 B[2], C[2];
+  uint16_t u, dt, z;
+
+  __device__ __forceinline__ void load(const SscanStepParams& p, int b, int slot_, int d, int n0, int ns, int bc) {
+    slot = slot_;
+    if (slot < 0) return;
+    const float* hp = p.state + ((size_t)slot * p.D + d) * p.N + n0;
+    const __nv_bfloat16 *bp = p.Bm + (size_t)b * p.b_s + bc, *cp = p.Cm + (size_t)b * p.c_s + bc;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < ns) a[e] = kLog2e * __ldg(p.A + (size_t)dc * p.N + n0 + e);
-  }
-  const float bias = p.bias ? __ldg(p.bias + dc) : 0.f, skip = p.Dskip && n0 == 0 ? __ldg(p.Dskip + dc) : 0.f;
-  const int bc = (dc / p.Dg) * p.N + n0;
-#pragma unroll 2
-  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
-    const int slot = slot_of(p.index, b, p.slots, p.status);
-    float y = 0.f;
-    if (slot >= 0) {
-      float* hp = p.state + ((size_t)slot * p.D + dc) * p.N + n0;
-      const __nv_bfloat16 *bp = p.Bm + (size_t)b * p.b_s + bc, *cp = p.Cm + (size_t)b * p.c_s + bc;
-      float h[4] = {0.f, 0.f, 0.f, 0.f}, B[4] = {0.f, 0.f, 0.f, 0.f}, C[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < 2; ++j) {
       if (VEC) {
-        if (ns > 0) {
-          const float4 hv = *reinterpret_cast<const float4*>(hp);
-          const uint2 bu = __ldg(reinterpret_cast<const uint2*>(bp)), cu = __ldg(reinterpret_cast<const uint2*>(cp));
-          h[0] = hv.x, h[1] = hv.y, h[2] = hv.z, h[3] = hv.w;
-          B[0] = bf16_lo(bu.x), B[1] = bf16_hi(bu.x), B[2] = bf16_lo(bu.y), B[3] = bf16_hi(bu.y);
-          C[0] = bf16_lo(cu.x), C[1] = bf16_hi(cu.x), C[2] = bf16_lo(cu.y), C[3] = bf16_hi(cu.y);
-        }
+        const bool in = 4 * j < ns;
+        const float4 q = in ? *reinterpret_cast<const float4*>(hp + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+        h[4 * j] = q.x, h[4 * j + 1] = q.y, h[4 * j + 2] = q.z, h[4 * j + 3] = q.w;
+        B[j] = in ? __ldg(reinterpret_cast<const uint2*>(bp) + j) : make_uint2(0, 0);
+        C[j] = in ? __ldg(reinterpret_cast<const uint2*>(cp) + j) : make_uint2(0, 0);
       } else {
+        uint32_t v[2][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < ns) h[e] = hp[e], B[e] = __bfloat162float(bp[e]), C[e] = __bfloat162float(cp[e]);
+        for (int e = 0; e < 4; ++e) {
+          const int n = 4 * j + e;
+          h[n] = n < ns ? hp[n] : 0.f;
+          v[0][e] = n < ns ? __ldg(reinterpret_cast<const uint16_t*>(bp) + n) : 0;
+          v[1][e] = n < ns ? __ldg(reinterpret_cast<const uint16_t*>(cp) + n) : 0;
+        }
+        B[j] = make_uint2(v[0][0] | v[0][1] << 16, v[0][2] | v[0][3] << 16);
+        C[j] = make_uint2(v[1][0] | v[1][1] << 16, v[1][2] | v[1][3] << 16);
       }
-      const float u = __bfloat162float(p.u[(size_t)b * p.u_s + dc]), x = __bfloat162float(p.delta[(size_t)b * p.dt_s + dc]) + bias;
-      const float z = p.z ? __bfloat162float(p.z[(size_t)b * p.z_s + dc]) : 0.f;
+    }
+    u = __ldg(reinterpret_cast<const uint16_t*>(p.u + (size_t)b * p.u_s + d));
+    dt = __ldg(reinterpret_cast<const uint16_t*>(p.delta + (size_t)b * p.dt_s + d));
+    z = p.z ? __ldg(reinterpret_cast<const uint16_t*>(p.z + (size_t)b * p.z_s + d)) : uint16_t(0);
+  }
+};
+
+template <int LPC, bool VEC>
+__global__ void __launch_bounds__(128) k_sscan_step(SscanStepParams p) {
+  const int i = blockIdx.x * 128 + threadIdx.x, d = i / LPC, n0 = (i % LPC) * 8;
+  const bool live = d < p.D;
+  const int dc = live ? d : p.D - 1, ns = p.N - n0;
+  float a[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) a[e] = e < ns ? kLog2e * __ldg(p.A + (size_t)dc * p.N + n0 + e) : 0.f;
+  const float bias = p.bias ? __ldg(p.bias + dc) : 0.f, skip = p.Dskip && n0 == 0 ? __ldg(p.Dskip + dc) : 0.f;
+  const int bc = (dc / p.Dg) * p.N + n0, stride = gridDim.y;
+  auto slot_at = [&](int b) { return b < p.B ? slot_of(p.index, b, p.slots, p.status) : -1; };
+  SscanRow<VEC> row;
+  row.load(p, blockIdx.y, slot_at(blockIdx.y), dc, n0, ns, bc);
+  int slot = slot_at(blockIdx.y + stride);
+  for (int b = blockIdx.y; b < p.B; b += stride) {
+    SscanRow<VEC> next;
+    next.load(p, b + stride, slot, dc, n0, ns, bc);
+    slot = slot_at(b + 2 * stride);
+    float y = 0.f;
+    if (row.slot >= 0) {
+      const float u = bf16_lo(row.u), x = bf16_lo(row.dt) + bias, z = bf16_lo(row.z);
       float slope;
       const float dt = p.softplus ? softplus(x, &slope) : x, dtu = dt * u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        h[e] = fmaf(decay(dt, a[e]), h[e], dtu * B[e]);
-        y = fmaf(h[e], C[e], y);
+      for (int e = 0; e < 8; ++e) {
+        const uint2 bq = row.B[e / 4], cq = row.C[e / 4];
+        const uint32_t bw = e & 2 ? bq.y : bq.x, cw = e & 2 ? cq.y : cq.x;
+        row.h[e] = fmaf(decay(dt, a[e]), row.h[e], dtu * (e & 1 ? bf16_hi(bw) : bf16_lo(bw)));
+        y = fmaf(row.h[e], e & 1 ? bf16_hi(cw) : bf16_lo(cw), y);
       }
       y = fmaf(skip, u, y);
       if (live) {
-        if (VEC) {
-          if (ns > 0) *reinterpret_cast<float4*>(hp) = make_float4(h[0], h[1], h[2], h[3]);
-        } else {
+        float* hp = p.state + ((size_t)row.slot * p.D + d) * p.N + n0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (e < ns) hp[e] = h[e];
+        for (int j = 0; j < 2; ++j) {
+          if (VEC) {
+            if (4 * j < ns) reinterpret_cast<float4*>(hp)[j] = make_float4(row.h[4 * j], row.h[4 * j + 1], row.h[4 * j + 2], row.h[4 * j + 3]);
+          } else {
+#pragma unroll
+            for (int e = 4 * j; e < 4 * j + 4; ++e)
+              if (e < ns) hp[e] = row.h[e];
+          }
         }
       }
-#pragma unroll
-      for (int m = LPC / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+      if (LPC == 2) y += __shfl_xor_sync(0xffffffffu, y, 1);
       if (p.z) y *= z * sigmoid_fast(z);
     }
     if (live && n0 == 0) p.y[(size_t)b * p.D + d] = __float2bfloat16_rn(y);
+    row = next;
   }
 }
 
@@ -325,12 +352,11 @@ cudaError_t launch_delta_step(const DeltaStepParams& p, cudaStream_t s) {
 
 template <bool VEC>
 static cudaError_t run_sscan_step(const SscanStepParams& p, cudaStream_t s) {
-  const int lpc = p.N <= 4 ? 1 : p.N <= 8 ? 2 : 4, bx = (p.D * lpc + 255) / 256;
-  // up to eight CTAs of eight warps per SM; beyond that a block walks several rows
+  const int lpc = p.N <= 8 ? 1 : 2, bx = (p.D * lpc + 127) / 128;
+  // up to eight CTAs of four warps per SM; beyond that a block walks several rows
   const dim3 grid(bx, std::max(1, std::min(p.B, std::min(65535, (p.sms * 8 + bx - 1) / bx))));
-  if (lpc == 1) k_sscan_step<1, VEC><<<grid, 256, 0, s>>>(p);
-  else if (lpc == 2) k_sscan_step<2, VEC><<<grid, 256, 0, s>>>(p);
-  else k_sscan_step<4, VEC><<<grid, 256, 0, s>>>(p);
+  if (lpc == 1) k_sscan_step<1, VEC><<<grid, 128, 0, s>>>(p);
+  else k_sscan_step<2, VEC><<<grid, 128, 0, s>>>(p);
   return cudaGetLastError();
 }
 
