@@ -16,9 +16,9 @@ _ACTIVATIONS = {"silu": 1, "sigmoid": 2}
 
 
 def _want(name, t, dtype, shape, dev):
-    """_check_tensor behind one cheap test of the usual case."""
-    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
-        _check_tensor(name, t, dtype, shape, dev)
+    """_check_tensor behind one cheap test of the usual case. ``dev``: the device's index."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+        _check_tensor(name, t, dtype, shape, torch.device("cuda", dev))
 
 
 def _p(t):
@@ -29,7 +29,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(dev):
-    return _raw_stream(dev.index) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
 
 
 _norm_desc = _lib.packer(_lib.NormDesc)
@@ -48,27 +48,23 @@ def _run(name, desc, args, dev):
 def _device(name, t):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
-    if t.device.type != "cuda":
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("inputs must be CUDA tensors")
-    return t.device
+    return dev
 
 
-def _rows_of(name, t, dtype, shape, dev, inner):
-    """Elements between the rows of ``t``, whose last ``inner`` dimensions are contiguous and whose leading ones follow
-    each other at one stride (a slice of a wider projection qualifies)."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a tensor")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    st, w, lead = t.stride(), 1, len(shape) - inner
+def _rows_of(name, t, dtype, shape, dev, inner, width):
+    """Elements between the rows (of ``width`` elements) of ``t``, whose last ``inner`` dimensions are contiguous and whose
+    leading ones follow each other at one stride (a slice of a wider projection qualifies)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+        _check_tensor(name, t, dtype, shape, torch.device("cuda", dev))
     if t.is_contiguous():
-        for n in shape[lead:]:
-            w *= n
-        return w
+        return width
+    st, lead = t.stride(), len(shape) - inner
+    if lead == 1 and st[-1] == 1 and st[0] >= width and (inner == 1 or st[1] == shape[2]):    # a step's usual case
+        return st[0] if shape[0] > 1 else width
+    w = 1
     for i in range(len(shape) - 1, lead - 1, -1):
         if shape[i] != 1 and st[i] != w:
             raise ValueError(f"{name}'s rows must be contiguous")
@@ -135,7 +131,7 @@ def add_rms_norm_fwd(x, residual, weight, *, eps=1e-6, residual_scale=1.0):
     y = torch.empty_like(x)
     stream = x if residual is None else torch.empty_like(residual)
     _run("gdn_add_norm_fwd", _norm_desc(rows, width, eps, residual_scale, kind, 0),
-         _norm_fwd_args(_p(x), _p(residual), _p(weight), _p(y), _p(stream) if kind else 0), dev)
+         _norm_fwd_args(x.data_ptr(), _p(residual), weight.data_ptr(), y.data_ptr(), stream.data_ptr() if kind else 0), dev)
     return y, stream
 
 
@@ -155,7 +151,7 @@ def add_rms_norm_bwd(dy, dstream, stream, weight, *, eps=1e-6, residual_scale=1.
     dres = torch.empty_like(stream) if has_residual else None
     dw = torch.empty_like(weight)
     _run("gdn_add_norm_bwd", _norm_desc(rows, width, eps, residual_scale, kind, 0),
-         _norm_bwd_args(_p(stream), 0, _p(weight), _p(dy), _p(dstream), _p(dx), 0, _p(dres), _p(dw), _p(ws), ws_bytes), dev)
+         _norm_bwd_args(stream.data_ptr(), 0, weight.data_ptr(), dy.data_ptr(), _p(dstream), dx.data_ptr(), 0, _p(dres), dw.data_ptr(), ws.data_ptr(), ws_bytes), dev)
     return dx, dres, dw
 
 
@@ -173,7 +169,7 @@ def gated_rms_norm_fwd(x, gate, weight, *, eps=1e-6, activation="silu"):
     _want("gate", gate, _BF16, x.shape, dev)
     _want("weight", weight, _F32, (width,), dev)
     y = torch.empty_like(x)
-    _run("gdn_gated_norm_fwd", _norm_desc(rows, width, eps, 1.0, 0, act), _norm_fwd_args(_p(x), _p(gate), _p(weight), _p(y), 0), dev)
+    _run("gdn_gated_norm_fwd", _norm_desc(rows, width, eps, 1.0, 0, act), _norm_fwd_args(x.data_ptr(), gate.data_ptr(), weight.data_ptr(), y.data_ptr(), 0), dev)
     return y
 
 
@@ -187,7 +183,7 @@ def gated_rms_norm_bwd(x, gate, weight, dy, *, eps=1e-6, activation="silu"):
     ws, ws_bytes = _norm_workspace(rows, width, weight)
     dx, dgate, dw = torch.empty_like(x), torch.empty_like(gate), torch.empty_like(weight)
     _run("gdn_gated_norm_bwd", _norm_desc(rows, width, eps, 1.0, 0, act),
-         _norm_bwd_args(_p(x), _p(gate), _p(weight), _p(dy), 0, _p(dx), _p(dgate), 0, _p(dw), _p(ws), ws_bytes), dev)
+         _norm_bwd_args(x.data_ptr(), gate.data_ptr(), weight.data_ptr(), dy.data_ptr(), 0, dx.data_ptr(), dgate.data_ptr(), 0, dw.data_ptr(), ws.data_ptr(), ws_bytes), dev)
     return dx, dgate, dw
 
 
@@ -249,15 +245,16 @@ def causal_conv1d_state(x, weight, *, dilation=1, cu_seqlens: Optional[Sequence[
     offsets = _offsets(cu_seqlens, x.shape[1] if x.dim() == 3 else 0)
     desc = _conv_desc(x, weight, dilation, False, offsets)
     N, HW = desc.num_seqs, (weight.shape[1] - 1) * dilation
-    dev = _conv_checks(x, weight, None, halo, N, HW)
+    _conv_checks(x, weight, None, halo, N, HW)
+    dev = x.get_device()
     ws_bytes = lib.gdn_conv_fwd_workspace_size(desc)
     if ws_bytes == 0:
         _lib.check(_lib.GDN_EINVAL)
-    state = torch.empty((N, HW, x.shape[2]), dtype=_BF16, device=dev)
+    state = x.new_empty((N, HW, x.shape[2]))
     if HW == 0:
         return state
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    a = _lib.ConvFwdArgs(x=_p(x), halo=_p(halo), y=_p(state), workspace=_p(ws), workspace_bytes=ws_bytes)
+    ws = x.new_empty(ws_bytes, dtype=torch.uint8)
+    a = _lib.ConvFwdArgs(x=x.data_ptr(), halo=_p(halo), y=state.data_ptr(), workspace=ws.data_ptr(), workspace_bytes=ws_bytes)
     _lib.check(lib.gdn_conv_state(desc, a, _stream(dev)))
     return state
 
@@ -271,7 +268,7 @@ def causal_conv1d_step(state, x, weight, bias=None, *, dilation=1, activation=Tr
         raise ValueError("x must be [B,C] and weight [C,W]")
     B, C = x.shape
     W = weight.shape[1]
-    xs = _rows_of("x", x, _BF16, (B, C), dev, 1)
+    xs = _rows_of("x", x, _BF16, (B, C), dev, 1, C)
     _want("weight", weight, _F32, (C, W), dev)
     if bias is not None:
         _want("bias", bias, _F32, (C,), dev)
@@ -283,7 +280,7 @@ def causal_conv1d_step(state, x, weight, bias=None, *, dilation=1, activation=Tr
     _status(status, dev)
     y = x.new_empty((B, C))
     _run("gdn_conv_step", _conv_step_desc(B, C, W, dilation, 1 if activation else 0, slots, xs),
-         _conv_step_args(_p(x), _p(weight), _p(bias), _p(state), _p(state_indices), _p(y), _p(status)), dev)
+         _conv_step_args(x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(), _p(state_indices), y.data_ptr(), _p(status)), dev)
     return y
 
 
@@ -295,23 +292,24 @@ def _delta_step(per_channel, state, q, k, v, g, beta, state_indices, l2, sig, sc
     H = v.shape[1]
     if Hk < 1 or H % Hk != 0:
         raise ValueError("the value heads must be a multiple of the q/k heads")
-    qs = _rows_of("q", q, _BF16, (B, Hk, K_DIM), dev, 2)
-    ks = _rows_of("k", k, _BF16, (B, Hk, K_DIM), dev, 2)
-    vs = _rows_of("v", v, _BF16, (B, H, K_DIM), dev, 2)
+    qk = (B, Hk, K_DIM)
+    qs = _rows_of("q", q, _BF16, qk, dev, 2, Hk * K_DIM)
+    ks = _rows_of("k", k, _BF16, qk, dev, 2, Hk * K_DIM)
+    vs = _rows_of("v", v, _BF16, (B, H, K_DIM), dev, 2, H * K_DIM)
     _want("g", g, _F32, (B, H, K_DIM) if per_channel else (B, H), dev)
     _want("beta", beta, _BF16, (B, H), dev)
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be [slots,H,128,128]")
     slots = state.shape[0]
     _want("state", state, _F32, (slots, H, K_DIM, K_DIM), dev)
-    A_log, dt_bias = _gate_checks(gate, H, dev)
+    A_log, dt_bias = (None, None) if gate is None else _gate_checks(gate, H, q.device)
     _pool(state_indices, B, slots, dev)
     _status(status, dev)
     o = v.new_empty((B, H, K_DIM))
     _run("kda_step" if per_channel else "gdn_step",
          _step_desc(B, H, Hk, slots, 0.0 if scale is None else scale, 1 if l2 else 0, 1 if sig else 0,
                     0 if gate is None else 1, 0.0 if gate is None else gate[2], qs, ks, vs),
-         _step_args(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(state), _p(state_indices), _p(o), _p(A_log), _p(dt_bias), _p(status)), dev)
+         _step_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), _p(state_indices), o.data_ptr(), _p(A_log), _p(dt_bias), _p(status)), dev)
     return o
 
 
@@ -343,11 +341,12 @@ def _sscan_desc(u, delta, A, Bm, Cm, D, z, delta_bias, softplus, lead, offsets):
         raise ValueError("B must be [B,T,G,N]" if lead == 2 else "B must be [B,G,N]")
     shape, head = u.shape, u.shape[:lead]
     Dc, N, G = shape[lead], A.shape[1], Bm.shape[lead]
-    us = _rows_of("u", u, _BF16, shape, dev, 1)
-    ds = _rows_of("delta", delta, _BF16, shape, dev, 1)
-    zs = _rows_of("z", z, _BF16, shape, dev, 1) if z is not None else 0
-    bs = _rows_of("B", Bm, _BF16, (*head, G, N), dev, 2)
-    cs = _rows_of("C", Cm, _BF16, (*head, G, N), dev, 2)
+    vectors = (*head, G, N)
+    us = _rows_of("u", u, _BF16, shape, dev, 1, Dc)
+    ds = _rows_of("delta", delta, _BF16, shape, dev, 1, Dc)
+    zs = _rows_of("z", z, _BF16, shape, dev, 1, Dc) if z is not None else 0
+    bs = _rows_of("B", Bm, _BF16, vectors, dev, 2, G * N)
+    cs = _rows_of("C", Cm, _BF16, vectors, dev, 2, G * N)
     _want("A", A, _F32, (Dc, N), dev)
     if D is not None:
         _want("D", D, _F32, (Dc,), dev)
@@ -390,8 +389,8 @@ def selective_scan_fwd(u, delta, A, B, C, *, D=None, z=None, delta_bias=None, de
     if save:
         saved_bytes = _scan_size(lib.gdn_sscan_saved_size, d)
         saved = u.new_empty(saved_bytes, dtype=torch.uint8)
-    _run("gdn_sscan_fwd", d, _scan_fwd_args(_p(u), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(delta_bias), _p(z), _p(initial_state),
-                                            _p(y), _p(final), _p(ws), ws_bytes, _p(saved), saved_bytes), dev)
+    _run("gdn_sscan_fwd", d, _scan_fwd_args(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(delta_bias), _p(z), _p(initial_state),
+                                            y.data_ptr(), _p(final), ws.data_ptr(), ws_bytes, _p(saved), saved_bytes), dev)
     return (y, final, saved) if save else (y, final)
 
 
@@ -413,7 +412,7 @@ def selective_scan_bwd(u, delta, A, B, C, dy, *, D=None, z=None, delta_bias=None
     saved_bytes = 0
     if saved is not None:
         saved_bytes = _scan_size(lib.gdn_sscan_saved_size, d)
-        if not isinstance(saved, torch.Tensor) or saved.device != dev or saved.numel() * saved.element_size() < saved_bytes:
+        if not isinstance(saved, torch.Tensor) or saved.get_device() != dev or saved.numel() * saved.element_size() < saved_bytes:
             raise ValueError("saved must be the buffer returned by the forward with save=True")
         ws_bytes -= saved_bytes
 
@@ -423,9 +422,9 @@ def selective_scan_bwd(u, delta, A, B, C, dy, *, D=None, z=None, delta_bias=None
     du, ddelta, dB, dC, dz = like(u, _BF16), like(delta, _BF16), like(B, _BF16), like(C, _BF16), like(z, _BF16)
     dA, dD, dbias, dh0 = like(A, _F32), like(D, _F32), like(delta_bias, _F32), like(initial_state, _F32)
     ws = u.new_empty(ws_bytes, dtype=torch.uint8)
-    _run("gdn_sscan_bwd", d, _scan_bwd_args(_p(u), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(delta_bias), _p(z), _p(initial_state),
-                                            _p(dy), _p(dfinal), _p(du), _p(ddelta), _p(dA), _p(dB), _p(dC), _p(dD), _p(dbias), _p(dz),
-                                            _p(dh0), _p(ws), ws_bytes, _p(saved), saved_bytes), dev)
+    _run("gdn_sscan_bwd", d, _scan_bwd_args(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(delta_bias), _p(z), _p(initial_state),
+                                            dy.data_ptr(), _p(dfinal), du.data_ptr(), ddelta.data_ptr(), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _p(dD), _p(dbias), _p(dz),
+                                            _p(dh0), ws.data_ptr(), ws_bytes, _p(saved), saved_bytes), dev)
     return du, ddelta, dA, dB, dC, dD, dz, dbias, dh0
 
 
@@ -442,8 +441,8 @@ def selective_scan_step(state, u, delta, A, B, C, *, D=None, z=None, delta_bias=
     _pool(state_indices, rows, slots, dev)
     _status(status, dev)
     y = u.new_empty((rows, Dc))
-    _run("gdn_sscan_step", d, _scan_step_args(_p(u), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(delta_bias), _p(z), _p(state),
-                                              _p(state_indices), slots, _p(y), _p(status)), dev)
+    _run("gdn_sscan_step", d, _scan_step_args(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(delta_bias), _p(z), state.data_ptr(),
+                                              _p(state_indices), slots, y.data_ptr(), _p(status)), dev)
     return y
 
 

@@ -1,6 +1,7 @@
 // Host side of the operators around the recurrence (declared in include/gdn.h): contract validation, workspace layout,
 // the selective scan's segment plan, and the launches.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 
@@ -21,13 +22,20 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return a && b && x < y + nb && y < x + na;
 }
 
+// The current device is a GB300: asked of the driver once per device and process.
 int device_or_error(int* sms) {
-  int dev = 0;
+  static std::atomic<int> known[64];  // SM count of a supported device, 0 before the first question
+  int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return set_last_error(GDN_EUNSUPPORTED, "no CUDA device");
-  if (gdn_device_supported(dev) != GDN_OK)
-    return set_last_error(GDN_EUNSUPPORTED, "device is not compute capability 10.3 (GB300)");
-  if (sms && cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return set_last_error(GDN_ECUDA, "SM count query failed");
+  if (dev < 64) n = known[dev].load(std::memory_order_relaxed);
+  if (!n) {
+    if (gdn_device_supported(dev) != GDN_OK)
+      return set_last_error(GDN_EUNSUPPORTED, "device is not compute capability 10.3 (GB300)");
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return set_last_error(GDN_ECUDA, "SM count query failed");
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  if (sms) *sms = n;
   return GDN_OK;
 }
 
