@@ -98,7 +98,7 @@ int norm_fwd(const gdn_norm_desc_t* d, const gdn_norm_fwd_args_t* a, void* strea
   } else if (a->residual || a->stream) {
     return bad("residual and stream must be NULL without a residual (stream_kind 0)");
   }
-  if ((rc = device_or_error(nullptr))) return rc;
+  if ((rc = device_or_error(&p.sms))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TimedScope t(kKNormFwd, s);
   return cuda_rc(gated ? launch_gated_norm_fwd(p, s) : launch_add_norm_fwd(p, s), "norm kernel");

@@ -83,6 +83,30 @@ __device__ __forceinline__ float sum2(F2 a) {
   return lo + hi;
 }
 
+// ------------------------------------------------------------------ kernels of one call behind each other
+
+// A call's second and later kernels are launched so that they may start while the one before them runs
+// (programmatic stream serialisation): their launch and whatever they do before wait_for_previous() then costs no time of
+// its own. Every such kernel passes wait_for_previous() before it reads what the kernel before it wrote or writes
+// anything; the call's first kernel is launched plainly, behind all earlier work of the stream.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // ------------------------------------------------------------------ parameter blocks
 
 // Residual add and RMS norm before a block; gated RMS norm after it (k_norm.cu). `stream` is the

@@ -30,6 +30,8 @@ template <int NP>
 __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   RmapSmem<NP>& sm = *reinterpret_cast<RmapSmem<NP>*>(smem_raw);
+  if (p.cu) wait_for_previous();  // the tables
+  let_next_start();
   const int seg = blockIdx.x / blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   if (sg.j == 0) return;
@@ -105,11 +107,13 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, 
 
 // One thread per (sequence, state, channel): from the sequence's end, each segment's exit gradient.
 __global__ void __launch_bounds__(256) k_sscan_rcompose(SscanParams p) {
+  let_next_start();
   const long long per = (long long)p.N * p.D, at = (long long)blockIdx.x * 256 + threadIdx.x;
   if (at >= per * p.seqs) return;
   const int seq = int(at / per), nd = int(at - seq * per), n = nd / p.D, d = nd - n * p.D;
   const int s0 = p.cu ? p.seg_base[seq] : seq * p.nseg_dense, s1 = p.cu ? p.seg_base[seq + 1] : s0 + p.nseg_dense;
   const float a2 = kLog2e * p.A[(size_t)d * p.N + n];
+  wait_for_previous();
   float carry = p.dfinal ? p.dfinal[((size_t)seq * p.D + d) * p.N + n] : 0.f;
   constexpr int kAhead = 8;
   for (int s = s1 - 1; s >= s0; s -= kAhead) {
@@ -201,6 +205,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
   constexpr int SP = NP / 2, PR = SP / 2, NQ = SP / 4;  // states, state pairs and quads of a lane
   extern __shared__ __align__(16) char smem_raw[];
   BwdSmem<NP>& sm = *reinterpret_cast<BwdSmem<NP>*>(smem_raw);
+  let_next_start();
   const int seg = blockIdx.x / blocks, cb = blockIdx.x % blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   const SscanChan ch = sscan_chan<kBwdChans>(p, cb);
@@ -222,6 +227,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
     A2[i] = mul2(A2[i], dup2(kLog2e));
     g[i] = dA[i] = f2(0.f, 0.f);
   }
+  if (p.seg_state) wait_for_previous();
   if (live) {
     if (p.seg_state) load_states<SP>(g, p.seg_state + ((size_t)seg * p.N + n0) * p.D + d, p.D, ns);
     else if (p.dfinal) load_states<SP>(g, p.dfinal + ((size_t)sg.seq * p.D + d) * p.N + n0, 1, ns);
@@ -372,6 +378,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
 // blocks in order. The others: dA, dD and ddelta_bias of 32 channels x 8 segment lanes, over the segments in a fixed order.
 __global__ void __launch_bounds__(256) k_sscan_sums(SscanParams p, int bpg, int bc) {
   __shared__ float s[8][33];
+  wait_for_previous();
   if (int(blockIdx.x) < bc) {
     const long long at = (long long)blockIdx.x * 256 + threadIdx.x, per = 2ll * p.N;
     if (at >= p.rows * p.G * per) return;
@@ -402,18 +409,22 @@ __global__ void __launch_bounds__(256) k_sscan_sums(SscanParams p, int bpg, int 
 template <int NP>
 cudaError_t run(const SscanParams& p, cudaStream_t s) {
   const int blocks = sscan_blocks(p.G, p.Dg), grid = blocks * p.segs;
-  if (p.seg_state) {
-    k_sscan_rmap<NP><<<grid, kSscanThreads, sizeof(RmapSmem<NP>), s>>>(p, blocks);
-    const long long n = (long long)p.seqs * p.N * p.D;
-    k_sscan_rcompose<<<int((n + 255) / 256), 256, 0, s>>>(p);
-  }
-  const int smem = int(sizeof(BwdSmem<NP>));
+  // The first kernel is launched plainly, or, behind the upload of the tables, like the others.
+  const int smem = int(sizeof(BwdSmem<NP>)), bblocks = sscan_blocks(p.G, p.Dg, kBwdChans), bc = int((p.rows * p.G * 2 * p.N + 255) / 256);
   cudaError_t e = cudaFuncSetAttribute(k_sscan_bwd<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int bblocks = sscan_blocks(p.G, p.Dg, kBwdChans);
-  k_sscan_bwd<NP><<<bblocks * p.segs, kBwdThreads, smem, s>>>(p, bblocks);
-  const int bc = int((p.rows * p.G * 2 * p.N + 255) / 256);
-  k_sscan_sums<<<bc + (p.D + 31) / 32 * (p.N + 2), 256, 0, s>>>(p, bblocks / p.G, bc);
+  if (p.seg_state) {
+    const size_t rsmem = sizeof(RmapSmem<NP>);
+    if (p.cu) e = launch_after(k_sscan_rmap<NP>, grid, dim3(kSscanThreads), rsmem, s, p, blocks);
+    else k_sscan_rmap<NP><<<grid, kSscanThreads, rsmem, s>>>(p, blocks);
+    const long long n = (long long)p.seqs * p.N * p.D;
+    if (e == cudaSuccess) e = launch_after(k_sscan_rcompose, int((n + 255) / 256), 256, 0, s, p);
+    if (e == cudaSuccess) e = launch_after(k_sscan_bwd<NP>, bblocks * p.segs, kBwdThreads, smem, s, p, bblocks);
+  } else {
+    k_sscan_bwd<NP><<<bblocks * p.segs, kBwdThreads, smem, s>>>(p, bblocks);
+  }
+  if (e == cudaSuccess) e = launch_after(k_sscan_sums, bc + (p.D + 31) / 32 * (p.N + 2), 256, 0, s, p, bblocks / p.G, bc);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

@@ -29,6 +29,8 @@ template <int NP, bool MAP>
 __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   PassSmem<NP, MAP>& sm = *reinterpret_cast<PassSmem<NP, MAP>*>(smem_raw);
+  if (MAP && p.cu) wait_for_previous();  // the tables
+  let_next_start();
   const int seg = blockIdx.x / blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   if (MAP && sg.j == sg.nseg - 1) return;
@@ -40,12 +42,6 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
   for (int e = 0; e < 2; ++e) {
     const int d = ch.d[e];
     load_A2<NP>(A2[e], p, d);
-#pragma unroll
-    for (int i = 0; i < NP / 2; ++i) h[e][i] = f2(0.f, 0.f);
-    if (!MAP) {
-      if (p.seg_state) load_states<NP>(h[e], p.seg_state + (size_t)seg * p.N * p.D + d, p.D, p.N);
-      else if (p.h0) load_states<NP>(h[e], p.h0 + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);
-    }
     bias[e] = param(p.bias, d);
     skip[e] = param(MAP ? nullptr : p.Dskip, d);
   }
@@ -68,6 +64,17 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
   };
   request(0, 0);
   arrive(0);
+  if (!MAP && p.seg_state) wait_for_previous();  // the composed states; the rest above are the call's inputs
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int d = ch.d[e];
+#pragma unroll
+    for (int i = 0; i < NP / 2; ++i) h[e][i] = f2(0.f, 0.f);
+    if (!MAP) {
+      if (p.seg_state) load_states<NP>(h[e], p.seg_state + (size_t)seg * p.N * p.D + d, p.D, p.N);
+      else if (p.h0) load_states<NP>(h[e], p.h0 + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);
+    }
+  }
   for (int tb = 0, buf = 0; tb < sg.len; tb += kTt, buf ^= 1) {
     copies_wait();
     __syncthreads();
@@ -144,11 +151,13 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
 
 // One thread per (sequence, state, channel): walks the sequence's segments, leaving each its entry state.
 __global__ void __launch_bounds__(256) k_sscan_compose(SscanParams p) {
+  let_next_start();
   const long long per = (long long)p.N * p.D, at = (long long)blockIdx.x * 256 + threadIdx.x;
   if (at >= per * p.seqs) return;
   const int seq = int(at / per), nd = int(at - seq * per), n = nd / p.D, d = nd - n * p.D;
   const int s0 = p.cu ? p.seg_base[seq] : seq * p.nseg_dense, s1 = p.cu ? p.seg_base[seq + 1] : s0 + p.nseg_dense;
   const float a2 = kLog2e * p.A[(size_t)d * p.N + n];
+  wait_for_previous();
   float carry = p.h0 ? p.h0[((size_t)seq * p.D + d) * p.N + n] : 0.f;
   constexpr int kAhead = 8;
   for (int s = s0; s < s1; s += kAhead) {
@@ -171,12 +180,20 @@ __global__ void __launch_bounds__(256) k_sscan_compose(SscanParams p) {
 template <int NP>
 cudaError_t run(const SscanParams& p, cudaStream_t s) {
   const int blocks = sscan_blocks(p.G, p.Dg), grid = blocks * p.segs;
+  // The first kernel is launched plainly, or, behind the upload of the tables, like the others.
+  cudaError_t e = cudaSuccess;
+  const dim3 block(kSscanThreads);
   if (p.seg_state) {
-    k_sscan_pass<NP, true><<<grid, kSscanThreads, sizeof(PassSmem<NP, true>), s>>>(p, blocks);
+    const size_t smem = sizeof(PassSmem<NP, true>);
+    if (p.cu) e = launch_after(k_sscan_pass<NP, true>, grid, block, smem, s, p, blocks);
+    else k_sscan_pass<NP, true><<<grid, block, smem, s>>>(p, blocks);
     const long long n = (long long)p.seqs * p.N * p.D;
-    k_sscan_compose<<<int((n + 255) / 256), 256, 0, s>>>(p);
+    if (e == cudaSuccess) e = launch_after(k_sscan_compose, int((n + 255) / 256), 256, 0, s, p);
+    if (e == cudaSuccess) e = launch_after(k_sscan_pass<NP, false>, grid, block, sizeof(PassSmem<NP, false>), s, p, blocks);
+  } else {
+    k_sscan_pass<NP, false><<<grid, block, sizeof(PassSmem<NP, false>), s>>>(p, blocks);
   }
-  k_sscan_pass<NP, false><<<grid, kSscanThreads, sizeof(PassSmem<NP, false>), s>>>(p, blocks);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
