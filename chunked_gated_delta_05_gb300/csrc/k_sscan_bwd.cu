@@ -205,7 +205,6 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
   constexpr int SP = NP / 2, PR = SP / 2, NQ = SP / 4;  // states, state pairs and quads of a lane
   extern __shared__ __align__(16) char smem_raw[];
   BwdSmem<NP>& sm = *reinterpret_cast<BwdSmem<NP>*>(smem_raw);
-  let_next_start();
   const int seg = blockIdx.x / blocks, cb = blockIdx.x % blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   const SscanChan ch = sscan_chan<kBwdChans>(p, cb);
@@ -226,11 +225,6 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
   for (int i = 0; i < PR; ++i) {
     A2[i] = mul2(A2[i], dup2(kLog2e));
     g[i] = dA[i] = f2(0.f, 0.f);
-  }
-  if (p.seg_state) wait_for_previous();
-  if (live) {
-    if (p.seg_state) load_states<SP>(g, p.seg_state + ((size_t)seg * p.N + n0) * p.D + d, p.D, ns);
-    else if (p.dfinal) load_states<SP>(g, p.dfinal + ((size_t)sg.seq * p.D + d) * p.N + n0, 1, ns);
   }
   const float bias = param(p.bias, d), skip = param(p.Dskip, d);
   float dD = 0.f, dbias = 0.f;
@@ -260,6 +254,11 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
   const int last = (sg.len - 1) / kTile * kTile;
   request(last, 0);
   arrive(0);
+  if (p.seg_state) wait_for_previous();  // the composed gradients; the rest above are the call's inputs
+  if (live) {
+    if (p.seg_state) load_states<SP>(g, p.seg_state + ((size_t)seg * p.N + n0) * p.D + d, p.D, ns);
+    else if (p.dfinal) load_states<SP>(g, p.dfinal + ((size_t)sg.seq * p.D + d) * p.N + n0, 1, ns);
+  }
   for (int tb = last, buf = 0; tb >= 0; tb -= kTile, buf ^= 1) {
     const int len = min(kTile, sg.len - tb);
     const long long row = sg.row0 + tb;
