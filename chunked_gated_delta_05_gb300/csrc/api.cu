@@ -858,7 +858,7 @@ const char* gdn_strerror(int code) {
     case GDN_EUNSUPPORTED: return "unsupported device or feature";
     case GDN_ECUDA: return "CUDA runtime error";
     case GDN_ETIMEOUT: return "bounded device wait expired";
-    case GDN_ERANGE: return "per-channel gate outside the supported range";
+    case GDN_ERANGE: return "per-channel gate or state index outside the supported range";
     default: return "unknown error";
   }
 }

@@ -281,13 +281,7 @@ __global__ void __launch_bounds__(128) k_sscan_step(SscanStepParams p) {
   const float bias = p.bias ? __ldg(p.bias + dc) : 0.f, skip = p.Dskip && n0 == 0 ? __ldg(p.Dskip + dc) : 0.f;
   const int bc = (dc / p.Dg) * p.N + n0, stride = gridDim.y;
   auto slot_at = [&](int b) { return b < p.B ? slot_of(p.index, b, p.slots, p.status) : -1; };
-  SscanRow<VEC> row;
-  row.load(p, blockIdx.y, slot_at(blockIdx.y), dc, n0, ns, bc);
-  int slot = slot_at(blockIdx.y + stride);
-  for (int b = blockIdx.y; b < p.B; b += stride) {
-    SscanRow<VEC> next;
-    next.load(p, b + stride, slot, dc, n0, ns, bc);
-    slot = slot_at(b + 2 * stride);
+  auto compute = [&](SscanRow<VEC>& row, int b) {
     float y = 0.f;
     if (row.slot >= 0) {
       const float u = bf16_lo(row.u), x = bf16_lo(row.dt) + bias, z = bf16_lo(row.z);
@@ -318,7 +312,20 @@ __global__ void __launch_bounds__(128) k_sscan_step(SscanStepParams p) {
       if (p.z) y *= z * sigmoid_fast(z);
     }
     if (live && n0 == 0) p.y[(size_t)b * p.D + d] = __float2bfloat16_rn(y);
-    row = next;
+  };
+  // two rows in turn, so that none is copied
+  SscanRow<VEC> even, odd;
+  int b = blockIdx.y;
+  even.load(p, b, slot_at(b), dc, n0, ns, bc);
+  int slot = slot_at(b + stride);
+  for (; b < p.B; b += 2 * stride) {
+    odd.load(p, b + stride, slot, dc, n0, ns, bc);
+    slot = slot_at(b + 2 * stride);
+    compute(even, b);
+    if (b + stride >= p.B) break;
+    even.load(p, b + 2 * stride, slot, dc, n0, ns, bc);
+    slot = slot_at(b + 3 * stride);
+    compute(odd, b + stride);
   }
 }
 

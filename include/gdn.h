@@ -74,7 +74,8 @@ extern "C" {
 #define GDN_EUNSUPPORTED 2  /* not a compute-capability 10.3 device, or no device */
 #define GDN_ECUDA 3         /* a CUDA runtime call or kernel launch failed */
 #define GDN_ETIMEOUT 4      /* a bounded in-kernel wait ran out (reported via the status word) */
-#define GDN_ERANGE 5        /* a KDA gate outside the supported range (reported via the status word) */
+#define GDN_ERANGE 5        /* a KDA gate outside the supported range, or a step's state index outside the pool
+                               (reported via the status word) */
 
 /* Problem description shared by every entry point. */
 typedef struct {
