@@ -83,14 +83,19 @@ __device__ __forceinline__ float sum2(F2 a) {
   return lo + hi;
 }
 
-// ------------------------------------------------------------------ kernels of one call behind each other
+// ------------------------------------------------------------------ kernels behind each other
 
-// A call's second and later kernels are launched so that they may start while the one before them runs
-// (programmatic stream serialisation): their launch and whatever they do before wait_for_previous() then costs no time of
-// its own. Every such kernel passes wait_for_previous() before it reads what the kernel before it wrote or writes
-// anything; the call's first kernel is launched plainly, behind all earlier work of the stream.
+// The kernels of these operators are launched so that they may start while the kernel before them in the stream runs
+// (programmatic stream serialisation): their launch, and what they do before wait_for_previous(), costs no time of its own.
+// A call's first kernel waits before it reads or writes anything, and only then lets the next one start; so the call's later
+// kernels, which start behind it, may read the call's inputs at once, and wait before they touch what the kernels before them
+// wrote. A kernel that has waited has everything before it in the stream behind it: what it waited for had waited, too.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void begin_first_kernel() {
+  wait_for_previous();
+  let_next_start();
+}
 
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {

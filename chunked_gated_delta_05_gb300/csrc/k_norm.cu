@@ -123,6 +123,7 @@ template <int KIND, int VEC, int NV, int THREADS, typename ST>
 __global__ void __launch_bounds__(THREADS) k_norm_fwd(NormParams p, int G) {
   constexpr bool kAhead = NV == 1 && KIND != kAdd;
   __shared__ float red[2][1][32];
+  begin_first_kernel();
   const int per_block = blockDim.x / G, lane = threadIdx.x & (G - 1);
   const int units = p.width / VEC;
   const float inv = 1.f / float(p.width);
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(NormParams p, int G) {
   const int units = p.width / VEC;
   const float inv = 1.f / float(p.width);
   const long long step = (long long)gridDim.x * per_block;
-  let_next_start();
+  begin_first_kernel();
   float dw[NV][VEC];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -359,10 +360,9 @@ cudaError_t run_fwd(const NormParams& p, bool vec8, cudaStream_t s) {
   const long long blocks = (p.rows + per_block - 1) / per_block;
   // resident blocks that walk the rows a warp or less holds, one loaded ahead; else a block per row (or few rows)
   const int grid = int(std::min(blocks, KIND != kAdd && q.nv == 1 && q.G <= 32 ? (long long)p.sms * kFwdBlocksPerSm : 1ll << 30));
-#define GDN_CALL(VEC, NV, T) k_norm_fwd<KIND, VEC, NV, T, ST><<<grid, T, 0, s>>>(p, q.G)
+#define GDN_CALL(VEC, NV, T) return launch_after(k_norm_fwd<KIND, VEC, NV, T, ST>, grid, T, 0, s, p, q.G)
   GDN_NORM_DISPATCH(q, GDN_CALL)
 #undef GDN_CALL
-  return cudaGetLastError();
 }
 
 template <int KIND, typename ST>
@@ -373,10 +373,10 @@ cudaError_t run_bwd(const NormParams& p, bool vec8, cudaStream_t s) {
   const long long most = std::min((long long)p.sms * kBwdBlocksPerSm, (long long)kMaxPartialRows);
   const int grid = int(std::min(blocks, most));
   const size_t smem = per_block > 1 ? size_t(p.width) * 4 : 0;
-#define GDN_CALL(VEC, NV, T) k_norm_bwd<KIND, VEC, NV, T, ST><<<grid, T, smem, s>>>(p, q.G)
+  cudaError_t e = cudaSuccess;
+#define GDN_CALL(VEC, NV, T) e = launch_after(k_norm_bwd<KIND, VEC, NV, T, ST>, grid, T, smem, s, p, q.G)
   GDN_NORM_DISPATCH(q, GDN_CALL)
 #undef GDN_CALL
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_after(k_norm_reduce, (p.width + 31) / 32, dim3(32, 32), 0, s, (const float*)p.part, p.dweight, grid, p.width);
 }

@@ -30,8 +30,7 @@ template <int NP>
 __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   RmapSmem<NP>& sm = *reinterpret_cast<RmapSmem<NP>*>(smem_raw);
-  if (p.cu) wait_for_previous();  // the tables
-  let_next_start();
+  begin_first_kernel();
   const int seg = blockIdx.x / blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   if (sg.j == 0) return;
@@ -205,6 +204,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
   constexpr int SP = NP / 2, PR = SP / 2, NQ = SP / 4;  // states, state pairs and quads of a lane
   extern __shared__ __align__(16) char smem_raw[];
   BwdSmem<NP>& sm = *reinterpret_cast<BwdSmem<NP>*>(smem_raw);
+  if (!p.seg_state) wait_for_previous();
   const int seg = blockIdx.x / blocks, cb = blockIdx.x % blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   const SscanChan ch = sscan_chan<kBwdChans>(p, cb);
@@ -408,23 +408,15 @@ __global__ void __launch_bounds__(256) k_sscan_sums(SscanParams p, int bpg, int 
 template <int NP>
 cudaError_t run(const SscanParams& p, cudaStream_t s) {
   const int blocks = sscan_blocks(p.G, p.Dg), grid = blocks * p.segs;
-  // The first kernel is launched plainly, or, behind the upload of the tables, like the others.
   const int smem = int(sizeof(BwdSmem<NP>)), bblocks = sscan_blocks(p.G, p.Dg, kBwdChans), bc = int((p.rows * p.G * 2 * p.N + 255) / 256);
   cudaError_t e = cudaFuncSetAttribute(k_sscan_bwd<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  if (p.seg_state) {
-    const size_t rsmem = sizeof(RmapSmem<NP>);
-    if (p.cu) e = launch_after(k_sscan_rmap<NP>, grid, dim3(kSscanThreads), rsmem, s, p, blocks);
-    else k_sscan_rmap<NP><<<grid, kSscanThreads, rsmem, s>>>(p, blocks);
+  if (e == cudaSuccess && p.seg_state) {
     const long long n = (long long)p.seqs * p.N * p.D;
+    e = launch_after(k_sscan_rmap<NP>, grid, kSscanThreads, sizeof(RmapSmem<NP>), s, p, blocks);
     if (e == cudaSuccess) e = launch_after(k_sscan_rcompose, int((n + 255) / 256), 256, 0, s, p);
-    if (e == cudaSuccess) e = launch_after(k_sscan_bwd<NP>, bblocks * p.segs, kBwdThreads, smem, s, p, bblocks);
-  } else {
-    k_sscan_bwd<NP><<<bblocks * p.segs, kBwdThreads, smem, s>>>(p, bblocks);
   }
-  if (e == cudaSuccess) e = launch_after(k_sscan_sums, bc + (p.D + 31) / 32 * (p.N + 2), 256, 0, s, p, bblocks / p.G, bc);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  if (e == cudaSuccess) e = launch_after(k_sscan_bwd<NP>, bblocks * p.segs, kBwdThreads, smem, s, p, bblocks);
+  return e == cudaSuccess ? launch_after(k_sscan_sums, bc + (p.D + 31) / 32 * (p.N + 2), 256, 0, s, p, bblocks / p.G, bc) : e;
 }
 
 }  // namespace

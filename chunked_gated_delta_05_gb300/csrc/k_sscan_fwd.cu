@@ -29,8 +29,8 @@ template <int NP, bool MAP>
 __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   PassSmem<NP, MAP>& sm = *reinterpret_cast<PassSmem<NP, MAP>*>(smem_raw);
-  if (MAP && p.cu) wait_for_previous();  // the tables
-  let_next_start();
+  if (MAP || !p.seg_state) begin_first_kernel();
+  else let_next_start();
   const int seg = blockIdx.x / blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   if (MAP && sg.j == sg.nseg - 1) return;
@@ -180,21 +180,14 @@ __global__ void __launch_bounds__(256) k_sscan_compose(SscanParams p) {
 template <int NP>
 cudaError_t run(const SscanParams& p, cudaStream_t s) {
   const int blocks = sscan_blocks(p.G, p.Dg), grid = blocks * p.segs;
-  // The first kernel is launched plainly, or, behind the upload of the tables, like the others.
-  cudaError_t e = cudaSuccess;
   const dim3 block(kSscanThreads);
+  cudaError_t e = cudaSuccess;
   if (p.seg_state) {
-    const size_t smem = sizeof(PassSmem<NP, true>);
-    if (p.cu) e = launch_after(k_sscan_pass<NP, true>, grid, block, smem, s, p, blocks);
-    else k_sscan_pass<NP, true><<<grid, block, smem, s>>>(p, blocks);
     const long long n = (long long)p.seqs * p.N * p.D;
+    e = launch_after(k_sscan_pass<NP, true>, grid, block, sizeof(PassSmem<NP, true>), s, p, blocks);
     if (e == cudaSuccess) e = launch_after(k_sscan_compose, int((n + 255) / 256), 256, 0, s, p);
-    if (e == cudaSuccess) e = launch_after(k_sscan_pass<NP, false>, grid, block, sizeof(PassSmem<NP, false>), s, p, blocks);
-  } else {
-    k_sscan_pass<NP, false><<<grid, block, sizeof(PassSmem<NP, false>), s>>>(p, blocks);
   }
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return e == cudaSuccess ? launch_after(k_sscan_pass<NP, false>, grid, block, sizeof(PassSmem<NP, false>), s, p, blocks) : e;
 }
 
 }  // namespace

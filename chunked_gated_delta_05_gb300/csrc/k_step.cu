@@ -30,6 +30,7 @@ __device__ __forceinline__ int slot_of(const int* index, int b, int slots, int* 
 // Four channels per thread: the weights stay in registers while the block walks its batch rows.
 template <int W>
 __global__ void __launch_bounds__(128) k_conv_step(ConvStepParams p) {
+  begin_first_kernel();
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
   const bool live = c < p.C;
   float w[4][W], bias[4];
@@ -123,6 +124,7 @@ __global__ void __launch_bounds__(256) k_delta_step(DeltaStepParams p) {
   constexpr int kCols = kD / kVSplit, kLanes = kCols / 4, kRows = 8 * (32 / kLanes), kPer = kD / kRows;  // lanes a row, rows of a pass, passes
   __shared__ float qs[kD], ks[kD], dec[kD], qk_s;
   __shared__ float4 red[2][8][kLanes];
+  begin_first_kernel();
   const int vt = blockIdx.x % kVSplit, h = (blockIdx.x / kVSplit) % p.H;
   const int b = blockIdx.x / (kVSplit * p.H);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -272,6 +274,7 @@ struct SscanRow {
 
 template <int LPC, bool VEC>
 __global__ void __launch_bounds__(128) k_sscan_step(SscanStepParams p) {
+  begin_first_kernel();
   const int i = blockIdx.x * 128 + threadIdx.x, d = i / LPC, n0 = (i % LPC) * 8;
   const bool live = d < p.D;
   const int dc = live ? d : p.D - 1, ns = p.N - n0;
@@ -337,16 +340,15 @@ cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t s) {
   const int by = std::max(1, std::min(p.B, (p.sms * 8 + bx - 1) / bx));
   const dim3 grid(bx, std::min(by, 65535));
   switch (p.W) {
-    case 1: k_conv_step<1><<<grid, 128, 0, s>>>(p); break;
-    case 2: k_conv_step<2><<<grid, 128, 0, s>>>(p); break;
-    case 3: k_conv_step<3><<<grid, 128, 0, s>>>(p); break;
-    case 4: k_conv_step<4><<<grid, 128, 0, s>>>(p); break;
-    case 5: k_conv_step<5><<<grid, 128, 0, s>>>(p); break;
-    case 6: k_conv_step<6><<<grid, 128, 0, s>>>(p); break;
-    case 7: k_conv_step<7><<<grid, 128, 0, s>>>(p); break;
-    default: k_conv_step<8><<<grid, 128, 0, s>>>(p); break;
+    case 1: return launch_after(k_conv_step<1>, grid, 128, 0, s, p);
+    case 2: return launch_after(k_conv_step<2>, grid, 128, 0, s, p);
+    case 3: return launch_after(k_conv_step<3>, grid, 128, 0, s, p);
+    case 4: return launch_after(k_conv_step<4>, grid, 128, 0, s, p);
+    case 5: return launch_after(k_conv_step<5>, grid, 128, 0, s, p);
+    case 6: return launch_after(k_conv_step<6>, grid, 128, 0, s, p);
+    case 7: return launch_after(k_conv_step<7>, grid, 128, 0, s, p);
+    default: return launch_after(k_conv_step<8>, grid, 128, 0, s, p);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_conv_state(const ConvStateParams& p, cudaStream_t s) {
@@ -355,8 +357,7 @@ cudaError_t launch_conv_state(const ConvStateParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_delta_step(const DeltaStepParams& p, cudaStream_t s) {
-  k_delta_step<<<p.B * p.H * kVSplit, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(k_delta_step, p.B * p.H * kVSplit, 256, 0, s, p);
 }
 
 template <bool VEC>
@@ -364,9 +365,7 @@ static cudaError_t run_sscan_step(const SscanStepParams& p, cudaStream_t s) {
   const int lpc = p.N <= 8 ? 1 : 2, bx = (p.D * lpc + 127) / 128;
   // up to eight CTAs of four warps per SM; beyond that a block walks several rows
   const dim3 grid(bx, std::max(1, std::min(p.B, std::min(65535, (p.sms * 8 + bx - 1) / bx))));
-  if (lpc == 1) k_sscan_step<1, VEC><<<grid, 128, 0, s>>>(p);
-  else k_sscan_step<2, VEC><<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError();
+  return lpc == 1 ? launch_after(k_sscan_step<1, VEC>, grid, 128, 0, s, p) : launch_after(k_sscan_step<2, VEC>, grid, 128, 0, s, p);
 }
 
 cudaError_t launch_sscan_step(const SscanStepParams& p, cudaStream_t s) { return p.vec ? run_sscan_step<true>(p, s) : run_sscan_step<false>(p, s); }
