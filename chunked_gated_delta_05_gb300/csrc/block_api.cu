@@ -193,8 +193,8 @@ int validate_sscan(const gdn_sscan_desc_t* d, SscanProblem* P, bool step) {
 // Segments. One CTA walks kSscanChans channels of one segment token by token, so a call needs CTAs enough for every SM;
 // cutting the sequences costs the map pass, which walks all segments but the last ones again. The times compared are in
 // steps of one CTA among others on its SM: whole sequences take the longest one's steps, at `alone` each while the SM has
-// few CTAs, or one CTA after the other when there are more; cut ones take all steps and the map's, evenly spread. Of the
-// lengths that fill one to `rounds` rounds of resident CTAs, the one whose rounds and fixed cost per CTA are least is taken.
+// few CTAs, or one CTA after the other when there are more; cut ones take all steps and the map's, evenly spread but no fewer
+// than a shortest segment's, and two more kernels. Of the lengths that fill one to `rounds` rounds of resident CTAs, the one whose rounds and fixed cost per CTA are least is taken.
 struct SscanPlan {
   int L;                 // tokens per segment, a multiple of kSscanCut
   int most;              // most segments of a sequence
@@ -205,8 +205,9 @@ constexpr int kMinSegment = 64, kCtaTokens = 12;
 struct SscanCost {
   int ctas, first, last; // resident CTAs per SM, and the rounds of them that are tried
   double alone, map;     // a step of a CTA alone on its SM, and of the map pass
+  double launches;       // the map and compose kernels
 };
-constexpr SscanCost kFwdCost = {8, 1, 3, 2.4, 0.7}, kBwdCost = {3, 4, 4, 1.5, 0.3};
+constexpr SscanCost kFwdCost = {8, 1, 3, 2.4, 0.7, 120.0}, kBwdCost = {3, 4, 4, 2.0, 0.3, 60.0};
 
 long long count_segments(const SscanProblem& P, long long L) {
   if (!P.cu) return (P.T + L - 1) / L * P.seqs;
@@ -224,7 +225,7 @@ SscanPlan plan_sscan(const SscanProblem& P, bool backward) {
     for (int i = 0; i < P.seqs; ++i) longest = std::max(longest, sequence_length(P, i));
   }
   const double whole = longest * std::max(c.alone, double((P.seqs * blocks + kSms - 1) / kSms));
-  const double cut = (1.0 + c.map) * double(P.rows) * blocks / kSms;
+  const double cut = (1.0 + c.map) * std::max(double(P.rows) * blocks / kSms, c.alone * kMinSegment) + c.launches;
   const long long all = ((long long)longest + kSscanCut - 1) / kSscanCut * kSscanCut;
   long long best = all, least = 0;
   if (cut < whole) {

@@ -85,17 +85,13 @@ __device__ __forceinline__ float sum2(F2 a) {
 
 // ------------------------------------------------------------------ kernels behind each other
 
-// The kernels of these operators are launched so that they may start while the kernel before them in the stream runs
-// (programmatic stream serialisation): their launch, and what they do before wait_for_previous(), costs no time of its own.
-// A call's first kernel waits before it reads or writes anything, and only then lets the next one start; so the call's later
-// kernels, which start behind it, may read the call's inputs at once, and wait before they touch what the kernels before them
-// wrote. A kernel that has waited has everything before it in the stream behind it: what it waited for had waited, too.
+// The kernels of these operators are launched so that their launch overlaps the end of the kernel before them in the stream
+// (programmatic stream serialisation): a kernel may start when the last block of the one before it has ended, ahead of its
+// memory being flushed, and waits for that before it reads what that one wrote, or writes anything. (A call's later kernels may
+// read the call's inputs at once: its first kernel has waited for whatever wrote them.) No kernel lets the next one
+// start earlier: blocks that wait beside running ones were then packed onto few SMs, and the scan's small calls, bound by one
+// block's walk, took up to twice as long (2048 channels, 256 tokens: 59 against 32 us).
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void begin_first_kernel() {
-  wait_for_previous();
-  let_next_start();
-}
 
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {

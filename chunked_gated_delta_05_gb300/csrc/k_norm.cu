@@ -123,7 +123,7 @@ template <int KIND, int VEC, int NV, int THREADS, typename ST>
 __global__ void __launch_bounds__(THREADS) k_norm_fwd(NormParams p, int G) {
   constexpr bool kAhead = NV == 1 && KIND != kAdd;
   __shared__ float red[2][1][32];
-  begin_first_kernel();
+  wait_for_previous();
   const int per_block = blockDim.x / G, lane = threadIdx.x & (G - 1);
   const int units = p.width / VEC;
   const float inv = 1.f / float(p.width);
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(NormParams p, int G) {
   const int units = p.width / VEC;
   const float inv = 1.f / float(p.width);
   const long long step = (long long)gridDim.x * per_block;
-  begin_first_kernel();
+  wait_for_previous();
   float dw[NV][VEC];
 #pragma unroll
   for (int j = 0; j < NV; ++j)

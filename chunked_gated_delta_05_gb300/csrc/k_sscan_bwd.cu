@@ -30,7 +30,7 @@ template <int NP>
 __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   RmapSmem<NP>& sm = *reinterpret_cast<RmapSmem<NP>*>(smem_raw);
-  begin_first_kernel();
+  wait_for_previous();
   const int seg = blockIdx.x / blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   if (sg.j == 0) return;
@@ -106,7 +106,6 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, 
 
 // One thread per (sequence, state, channel): from the sequence's end, each segment's exit gradient.
 __global__ void __launch_bounds__(256) k_sscan_rcompose(SscanParams p) {
-  let_next_start();
   const long long per = (long long)p.N * p.D, at = (long long)blockIdx.x * 256 + threadIdx.x;
   if (at >= per * p.seqs) return;
   const int seq = int(at / per), nd = int(at - seq * per), n = nd / p.D, d = nd - n * p.D;

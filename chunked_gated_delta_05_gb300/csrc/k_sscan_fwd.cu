@@ -29,8 +29,7 @@ template <int NP, bool MAP>
 __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, int blocks) {
   extern __shared__ __align__(16) char smem_raw[];
   PassSmem<NP, MAP>& sm = *reinterpret_cast<PassSmem<NP, MAP>*>(smem_raw);
-  if (MAP || !p.seg_state) begin_first_kernel();
-  else let_next_start();
+  if (MAP || !p.seg_state) wait_for_previous();
   const int seg = blockIdx.x / blocks;
   const SscanSeg sg = sscan_seg(p, seg);
   if (MAP && sg.j == sg.nseg - 1) return;
@@ -151,7 +150,6 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
 
 // One thread per (sequence, state, channel): walks the sequence's segments, leaving each its entry state.
 __global__ void __launch_bounds__(256) k_sscan_compose(SscanParams p) {
-  let_next_start();
   const long long per = (long long)p.N * p.D, at = (long long)blockIdx.x * 256 + threadIdx.x;
   if (at >= per * p.seqs) return;
   const int seq = int(at / per), nd = int(at - seq * per), n = nd / p.D, d = nd - n * p.D;

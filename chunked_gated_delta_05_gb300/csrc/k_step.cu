@@ -30,7 +30,7 @@ __device__ __forceinline__ int slot_of(const int* index, int b, int slots, int* 
 // Four channels per thread: the weights stay in registers while the block walks its batch rows.
 template <int W>
 __global__ void __launch_bounds__(128) k_conv_step(ConvStepParams p) {
-  begin_first_kernel();
+  wait_for_previous();
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
   const bool live = c < p.C;
   float w[4][W], bias[4];
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(256) k_delta_step(DeltaStepParams p) {
   constexpr int kCols = kD / kVSplit, kLanes = kCols / 4, kRows = 8 * (32 / kLanes), kPer = kD / kRows;  // lanes a row, rows of a pass, passes
   __shared__ float qs[kD], ks[kD], dec[kD], qk_s;
   __shared__ float4 red[2][8][kLanes];
-  begin_first_kernel();
+  wait_for_previous();
   const int vt = blockIdx.x % kVSplit, h = (blockIdx.x / kVSplit) % p.H;
   const int b = blockIdx.x / (kVSplit * p.H);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -274,7 +274,7 @@ struct SscanRow {
 
 template <int LPC, bool VEC>
 __global__ void __launch_bounds__(128) k_sscan_step(SscanStepParams p) {
-  begin_first_kernel();
+  wait_for_previous();
   const int i = blockIdx.x * 128 + threadIdx.x, d = i / LPC, n0 = (i % LPC) * 8;
   const bool live = d < p.D;
   const int dc = live ? d : p.D - 1, ns = p.N - n0;
