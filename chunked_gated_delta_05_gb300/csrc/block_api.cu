@@ -201,7 +201,7 @@ struct SscanPlan {
   long long segs, cks;   // segments and kept states of all sequences
 };
 constexpr int kSms = 152;
-constexpr int kMinSegment = 64, kCtaTokens = 12;
+constexpr int kMinSegment = 32, kCtaTokens = 12;
 struct SscanCost {
   int ctas, first, last; // resident CTAs per SM, and the rounds of them that are tried
   double alone, map;     // a step of a CTA alone on its SM, and of the map pass
