@@ -195,6 +195,17 @@ def entry(name: str):
     return fn
 
 
+def size(name: str, desc: bytes) -> int:
+    """What the size query ``name`` says of a packed description; raises where it is invalid (0)."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = ctypes.CFUNCTYPE(c_size_t, c_void_p)((name, load()))
+    n = fn(desc)
+    if n == 0:
+        check(GDN_EINVAL)
+    return n
+
+
 def load(build_if_missing: bool = True):
     """Load libgdn.so (building it first when missing or stale). Raises if it cannot."""
     global _lib

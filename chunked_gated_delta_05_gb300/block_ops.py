@@ -86,6 +86,11 @@ def _rows_of(name, t, dtype, shape, dev, inner, width):
     return row
 
 
+def _like(t):
+    """An empty contiguous tensor of t's shape (None of None)."""
+    return None if t is None else torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _pool(state_indices, B, slots, dev):
     if state_indices is not None:
         _want("state_indices", state_indices, _I32, (B,), dev)
@@ -101,9 +106,7 @@ def _status(status, dev):
 # ---------------------------------------------------------------- norms
 
 def _norm_workspace(rows, width, like):
-    n = _lib.load().gdn_norm_bwd_workspace_size(_lib.NormDesc(rows=rows, width=width))
-    if n == 0:
-        _lib.check(_lib.GDN_EINVAL)
+    n = _lib.size("gdn_norm_bwd_workspace_size", _norm_desc(rows, width, 0.0, 1.0, 0, 0))
     return like.new_empty(n, dtype=torch.uint8), n
 
 
@@ -278,7 +281,7 @@ def causal_conv1d_step(state, x, weight, bias=None, *, dilation=1, activation=Tr
     _want("state", state, _BF16, (slots, (W - 1) * dilation, C), dev)
     _pool(state_indices, B, slots, dev)
     _status(status, dev)
-    y = x.new_empty((B, C))
+    y = _like(x)
     _run("gdn_conv_step", _conv_step_desc(B, C, W, dilation, 1 if activation else 0, slots, xs),
          _conv_step_args(x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(), _p(state_indices), y.data_ptr(), _p(status)), dev)
     return y
@@ -305,7 +308,7 @@ def _delta_step(per_channel, state, q, k, v, g, beta, state_indices, l2, sig, sc
     A_log, dt_bias = (None, None) if gate is None else _gate_checks(gate, H, q.device)
     _pool(state_indices, B, slots, dev)
     _status(status, dev)
-    o = v.new_empty((B, H, K_DIM))
+    o = _like(v)
     _run("kda_step" if per_channel else "gdn_step",
          _step_desc(B, H, Hk, slots, 0.0 if scale is None else scale, 1 if l2 else 0, 1 if sig else 0,
                     0 if gate is None else 1, 0.0 if gate is None else gate[2], qs, ks, vs),
@@ -357,10 +360,6 @@ def _sscan_desc(u, delta, A, Bm, Cm, D, z, delta_bias, softplus, lead, offsets):
     return dev, n, Dc, N, _scan_desc(B, T, Dc, N, G, cu, n, 1 if softplus else 0, us, ds, zs, bs, cs)
 
 
-def _scan_size(fn, d):
-    return fn(_lib.SscanDesc.from_buffer_copy(d))
-
-
 _scan_fwd_args, _scan_bwd_args = _lib.packer(_lib.SscanFwdArgs), _lib.packer(_lib.SscanBwdArgs)
 
 
@@ -373,21 +372,18 @@ def selective_scan_fwd(u, delta, A, B, C, *, D=None, z=None, delta_bias=None, de
     strided slices of wider projections); A fp32 ``[D,N]`` (negative); D, delta_bias fp32 ``[D]``; states fp32
     ``[sequences,D,N]``. Packed documents by ``cu_seqlens``. Returns ``(y bf16, final_state or None)``; with ``save=True``
     also the buffer to hand to :func:`selective_scan_bwd`."""
-    lib = _lib.load()
     offsets = _offsets(cu_seqlens, 0)       # the packed description points into it
     dev, *state_shape, d = _sscan_desc(u, delta, A, B, C, D, z, delta_bias, delta_softplus, 2, offsets)
     state_shape = tuple(state_shape)
     if initial_state is not None:
         _want("initial_state", initial_state, _F32, state_shape, dev)
-    ws_bytes = _scan_size(lib.gdn_sscan_fwd_workspace_size, d)
-    if ws_bytes == 0:
-        _lib.check(_lib.GDN_EINVAL)
-    y = u.new_empty(u.shape)
+    ws_bytes = _lib.size("gdn_sscan_fwd_workspace_size", d)
+    y = _like(u)
     final = A.new_empty(state_shape) if output_final_state else None
     ws = u.new_empty(ws_bytes, dtype=torch.uint8)
     saved_bytes, saved = 0, None
     if save:
-        saved_bytes = _scan_size(lib.gdn_sscan_saved_size, d)
+        saved_bytes = _lib.size("gdn_sscan_saved_size", d)
         saved = u.new_empty(saved_bytes, dtype=torch.uint8)
     _run("gdn_sscan_fwd", d, _scan_fwd_args(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(delta_bias), _p(z), _p(initial_state),
                                             y.data_ptr(), _p(final), ws.data_ptr(), ws_bytes, _p(saved), saved_bytes), dev)
@@ -398,7 +394,6 @@ def selective_scan_bwd(u, delta, A, B, C, dy, *, D=None, z=None, delta_bias=None
                        dfinal=None, cu_seqlens=None, saved=None):
     """Gradients of ``<dy, y> + <dfinal, final_state>``: ``(du, ddelta, dA, dB, dC, dD, dz, ddelta_bias, dh0)``, None where the
     input is None. ``saved`` is the buffer of a ``save=True`` forward on the same inputs (else its states are recomputed)."""
-    lib = _lib.load()
     offsets = _offsets(cu_seqlens, 0)       # the packed description points into it
     dev, *state_shape, d = _sscan_desc(u, delta, A, B, C, D, z, delta_bias, delta_softplus, 2, offsets)
     state_shape = tuple(state_shape)
@@ -406,21 +401,16 @@ def selective_scan_bwd(u, delta, A, B, C, dy, *, D=None, z=None, delta_bias=None
     for name, t in (("initial_state", initial_state), ("dfinal", dfinal)):
         if t is not None:
             _want(name, t, _F32, state_shape, dev)
-    ws_bytes = _scan_size(lib.gdn_sscan_bwd_workspace_size, d)
-    if ws_bytes == 0:
-        _lib.check(_lib.GDN_EINVAL)
+    ws_bytes = _lib.size("gdn_sscan_bwd_workspace_size", d)
     saved_bytes = 0
     if saved is not None:
-        saved_bytes = _scan_size(lib.gdn_sscan_saved_size, d)
+        saved_bytes = _lib.size("gdn_sscan_saved_size", d)
         if not isinstance(saved, torch.Tensor) or saved.get_device() != dev or saved.numel() * saved.element_size() < saved_bytes:
             raise ValueError("saved must be the buffer returned by the forward with save=True")
         ws_bytes -= saved_bytes
 
-    def like(t, dtype):
-        return None if t is None else t.new_empty(t.shape, dtype=dtype)
-
-    du, ddelta, dB, dC, dz = like(u, _BF16), like(delta, _BF16), like(B, _BF16), like(C, _BF16), like(z, _BF16)
-    dA, dD, dbias, dh0 = like(A, _F32), like(D, _F32), like(delta_bias, _F32), like(initial_state, _F32)
+    du, ddelta, dz = torch.empty_like(dy), torch.empty_like(dy), None if z is None else torch.empty_like(dy)
+    dA, dB, dC, dD, dbias, dh0 = torch.empty_like(A), _like(B), _like(C), _like(D), _like(delta_bias), _like(initial_state)
     ws = u.new_empty(ws_bytes, dtype=torch.uint8)
     _run("gdn_sscan_bwd", d, _scan_bwd_args(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(delta_bias), _p(z), _p(initial_state),
                                             dy.data_ptr(), _p(dfinal), du.data_ptr(), ddelta.data_ptr(), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _p(dD), _p(dbias), _p(dz),
@@ -440,7 +430,7 @@ def selective_scan_step(state, u, delta, A, B, C, *, D=None, z=None, delta_bias=
     _want("state", state, _F32, (slots, Dc, N), dev)
     _pool(state_indices, rows, slots, dev)
     _status(status, dev)
-    y = u.new_empty((rows, Dc))
+    y = _like(u)
     _run("gdn_sscan_step", d, _scan_step_args(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(delta_bias), _p(z), state.data_ptr(),
                                               _p(state_indices), slots, y.data_ptr(), _p(status)), dev)
     return y

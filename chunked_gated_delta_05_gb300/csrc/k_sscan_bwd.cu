@@ -10,6 +10,8 @@
 // does the reads. The adjoint chain is cut into segments like the forward's. The sums over channels in dB and dC begin as matrix products with ones: a
 // lane's four states are its share of the A operand of m16n8k8, whose products add up four lanes' channels (tf32 operands;
 // the results are bf16), and three exchanges add up the groups of lanes. All other sums are fp32.
+#include <atomic>
+
 #include "k_sscan.cuh"
 
 namespace gdn {
@@ -408,7 +410,14 @@ template <int NP>
 cudaError_t run(const SscanParams& p, cudaStream_t s) {
   const int blocks = sscan_blocks(p.G, p.Dg), grid = blocks * p.segs;
   const int smem = int(sizeof(BwdSmem<NP>)), bblocks = sscan_blocks(p.G, p.Dg, kBwdChans), bc = int((p.rows * p.G * 2 * p.N + 255) / 256);
-  cudaError_t e = cudaFuncSetAttribute(k_sscan_bwd<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (e == cudaSuccess && !(allowed.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(k_sscan_bwd<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
   if (e == cudaSuccess && p.seg_state) {
     const long long n = (long long)p.seqs * p.N * p.D;
     e = launch_after(k_sscan_rmap<NP>, grid, kSscanThreads, sizeof(RmapSmem<NP>), s, p, blocks);
