@@ -265,7 +265,9 @@ def causal_conv1d_state(x, weight, *, dilation=1, cu_seqlens: Optional[Sequence[
 def causal_conv1d_step(state, x, weight, bias=None, *, dilation=1, activation=True, state_indices=None, status=None):
     """One token of the short convolution: ``x [B,C]`` (bf16, rows may be strided) against ``state
     [slots,(W-1)*dilation,C]``, which is updated in place. ``state_indices`` (int32 [B] on the device) names each row's slot;
-    a negative one marks a padding row (zero output, no state touched). Returns ``y [B,C]``."""
+    a negative one marks a padding row (zero output, no state touched), and no slot may be named twice. A row whose slot lies
+    outside the state is treated as padding and recorded as GDN_ERANGE in ``status`` (int32 [1] on the device). Returns
+    ``y [B,C]``."""
     dev = _device("x", x)
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must be [B,C] and weight [C,W]")
@@ -463,4 +465,7 @@ class SelectiveScan(torch.autograd.Function):
 def selective_scan(u, delta, A, B, C, *, D=None, z=None, delta_bias=None, delta_softplus=True, initial_state=None,
                    output_final_state=False, cu_seqlens=None):
     """Differentiable selective scan (see :func:`selective_scan_fwd`): ``(y, final_state or None)``."""
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (u, delta, A, B, C, D, z, delta_bias, initial_state))):
+        return selective_scan_fwd(u, delta, A, B, C, D=D, z=z, delta_bias=delta_bias, delta_softplus=delta_softplus,
+                                  initial_state=initial_state, output_final_state=output_final_state, cu_seqlens=cu_seqlens)
     return SelectiveScan.apply(u, delta, A, B, C, D, z, delta_bias, initial_state, delta_softplus, output_final_state, cu_seqlens)
