@@ -157,12 +157,14 @@ struct ChTile {
     const uint32_t u = *reinterpret_cast<const uint32_t*>(&v[t][2 * threadIdx.x]);
     return make_float2(bf16_lo(u), bf16_hi(u));
   }
+  __device__ __forceinline__ F2 pair(int t) const {
+    const float2 x = at(t);
+    return f2(x.x, x.y);
+  }
   __device__ __forceinline__ void set(int t, float a, float b) { *reinterpret_cast<uint32_t*>(&v[t][2 * threadIdx.x]) = pack_bf16(a, b); }
 };
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-
-__device__ __forceinline__ F2 dup2(float x) { return f2(x, x); }
 
 // The state pairs of one channel, `apart` elements between states: the channels' own layout ([..][N][D], segment and kept
 // states) or a caller's ([..][D][N]). Zero past N.

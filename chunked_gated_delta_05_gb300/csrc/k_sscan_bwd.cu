@@ -38,13 +38,13 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, 
   if (sg.j == 0) return;
   const SscanChan ch = sscan_chan(p, blockIdx.x % blocks);
   F2 A2[2][NP / 2], g[2][NP / 2];
-  float bias[2], dt_sum[2] = {0.f, 0.f};
+  const F2 bias = f2(param(p.bias, ch.d[0]), param(p.bias, ch.d[1]));
+  F2 dt_sum = f2(0.f, 0.f);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     load_A2<NP>(A2[e], p, ch.d[e]);
 #pragma unroll
     for (int i = 0; i < NP / 2; ++i) g[e][i] = f2(0.f, 0.f);
-    bias[e] = param(p.bias, ch.d[e]);
   }
   const bool gate = p.z != nullptr, softplus_on = p.softplus;
   BcRegs<NP, kRt> rc;
@@ -71,16 +71,14 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, 
       float dt[kRGroup][2], dy0[kRGroup][2];
 #pragma unroll
       for (int i = 0; i < kRGroup; ++i) {
-        const float2 dr = sm.delta[buf].at(t0 + i), yr = sm.dy[buf].at(t0 + i), zr = sm.z[buf].at(t0 + i);
+        const F2 x = add2(sm.delta[buf].pair(t0 + i), bias), sp = softplus2(x), dy = sm.dy[buf].pair(t0 + i);
+        const F2 gated = mul2(dy, silu2(sm.z[buf].pair(t0 + i)));
+        const bool in = t0 + i < len;
+        unf2(softplus_on ? sp : x, &dt[i][0], &dt[i][1]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = (e ? dr.y : dr.x) + bias[e], dy = e ? yr.y : yr.x, z = e ? zr.y : zr.x;
-          float slope;
-          const float sp = softplus(x, &slope);
-          dt[i][e] = t0 + i < len ? (softplus_on ? sp : x) : 0.f;
-          dt_sum[e] += dt[i][e];
-          dy0[i][e] = gate ? dy * (z * sigmoid_fast(z)) : dy;
-        }
+        for (int e = 0; e < 2; ++e) dt[i][e] = in ? dt[i][e] : 0.f;
+        dt_sum = add2(dt_sum, f2(dt[i][0], dt[i][1]));
+        unf2(gate ? gated : dy, &dy0[i][0], &dy0[i][1]);
       }
 #pragma unroll
       for (int i = kRGroup - 1; i >= 0; --i) {
@@ -99,10 +97,12 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, 
     if (tb > 0) rc.store(sm.C[buf ^ 1]);
   }
   store_rows<NP>(g, p.seg_state + (size_t)seg * p.N * p.D, p, ch);
+  float dts[2];
+  unf2(dt_sum, &dts[0], &dts[1]);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     if (!ch.live[e]) continue;
-    p.seg_dt[(size_t)seg * p.D + ch.d[e]] = dt_sum[e];
+    p.seg_dt[(size_t)seg * p.D + ch.d[e]] = dts[e];
   }
 }
 
@@ -199,7 +199,7 @@ struct BwdSmem {
 
 // Tile by tile, the last first: forward over the tile's tokens, whose states stay in registers, then back over them. A channel
 // takes two lanes of a warp, 16 apart, each with half of the states: that leaves registers for a whole tile's states and for
-// four warps a scheduler, and each lane does the scalar work (step size, gates, their gradients) of half of the tile's tokens.
+// three warps a scheduler, and each lane does the scalar work (step size, gates, their gradients) of half of the tile's tokens.
 template <int NP>
 __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int blocks) {
   constexpr int SP = NP / 2, PR = SP / 2, NQ = SP / 4;  // states, state pairs and quads of a lane

@@ -36,14 +36,11 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
   const SscanChan ch = sscan_chan(p, blockIdx.x % blocks);
 
   F2 A2[2][NP / 2], h[2][NP / 2];
-  float bias[2], skip[2], dt_sum[2] = {0.f, 0.f};
+  const F2 bias = f2(param(p.bias, ch.d[0]), param(p.bias, ch.d[1]));
+  const F2 skip = f2(param(MAP ? nullptr : p.Dskip, ch.d[0]), param(MAP ? nullptr : p.Dskip, ch.d[1]));
+  F2 dt_sum = f2(0.f, 0.f);
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int d = ch.d[e];
-    load_A2<NP>(A2[e], p, d);
-    bias[e] = param(p.bias, d);
-    skip[e] = param(MAP ? nullptr : p.Dskip, d);
-  }
+  for (int e = 0; e < 2; ++e) load_A2<NP>(A2[e], p, ch.d[e]);
   const bool out = !MAP && p.y, gate = out && p.z, softplus_on = p.softplus;
 
   BcRegs<NP, kTt> rb, rc;
@@ -87,24 +84,23 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
     for (int t0 = 0; t0 < kTt; t0 += kGroup) {
       if (!MAP && p.ck && t0 % kSscanBlock == 0 && t0 < len)
         store_rows<NP>(h, p.ck + (size_t)(sg.ck0 + (tb + t0) / kSscanBlock) * p.N * p.D, p, ch);
-      float dt[kGroup][2], dtu[kGroup][2], y[kGroup][2];
+      float dt[kGroup][2], dtu[kGroup][2];
+      F2 y[kGroup];
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
-        const float2 dr = sm.delta[buf].at(t0 + i), ur = sm.u[buf].at(t0 + i);
+        const F2 u = sm.u[buf].pair(t0 + i), x = add2(sm.delta[buf].pair(t0 + i), bias), sp = softplus2(x);
+        const bool in = t0 + i < len;
+        unf2(softplus_on ? sp : x, &dt[i][0], &dt[i][1]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = (e ? dr.y : dr.x) + bias[e], u = e ? ur.y : ur.x;
-          float slope;
-          const float sp = softplus(x, &slope);
-          dt[i][e] = t0 + i < len ? (softplus_on ? sp : x) : 0.f;
-          dtu[i][e] = dt[i][e] * u;
-          if (MAP) dt_sum[e] += dt[i][e];
-          else y[i][e] = skip[e] * u;
-        }
+        for (int e = 0; e < 2; ++e) dt[i][e] = in ? dt[i][e] : 0.f;
+        const F2 both = f2(dt[i][0], dt[i][1]);
+        unf2(mul2(both, u), &dtu[i][0], &dtu[i][1]);
+        if (MAP) dt_sum = add2(dt_sum, both);
+        else y[i] = mul2(skip, u);
       }
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
-        F2 y2[2] = {f2(y[i][0], 0.f), f2(y[i][1], 0.f)};
+        F2 y2[2];
         const F2 dt2[2] = {dup2(dt[i][0]), dup2(dt[i][1])}, dtu2[2] = {dup2(dtu[i][0]), dup2(dtu[i][1])};
 #pragma unroll
         for (int s = 0; s < NP / 2; s += 2) {
@@ -116,18 +112,18 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               h[e][s + k] = fma2(decay2(dt2[e], A2[e][s + k]), h[e][s + k], mul2(dtu2[e], b[k]));
-              if (!MAP) y2[e] = fma2(h[e][s + k], c[k], y2[e]);
+              if (!MAP) y2[e] = s + k ? fma2(h[e][s + k], c[k], y2[e]) : mul2(h[e][0], c[0]);
             }
         }
-        y[i][0] = sum2(y2[0]);
-        y[i][1] = sum2(y2[1]);
+        if (!MAP) y[i] = add2(y[i], f2(sum2(y2[0]), sum2(y2[1])));
       }
       if (!MAP) {
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
-          const float2 z = sm.z[MAP ? 0 : buf].at(t0 + i);
-          const float a = y[i][0] * (z.x * sigmoid_fast(z.x)), b = y[i][1] * (z.y * sigmoid_fast(z.y));
-          sm.u[buf].set(t0 + i, gate ? a : y[i][0], gate ? b : y[i][1]);
+          const F2 a = mul2(y[i], silu2(sm.z[MAP ? 0 : buf].pair(t0 + i)));
+          float lo, hi;
+          unf2(gate ? a : y[i], &lo, &hi);
+          sm.u[buf].set(t0 + i, lo, hi);
         }
       }
     }
@@ -136,12 +132,14 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
     if (out) sm.u[buf].store(p.y + (sg.row0 + tb) * p.D + ch.d0, p.D, len, ch.chans, p.vec_out);
   }
   if (MAP) store_rows<NP>(h, p.seg_state + (size_t)seg * p.N * p.D, p, ch);
+  float dts[2];
+  unf2(dt_sum, &dts[0], &dts[1]);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     if (!ch.live[e]) continue;
     const int d = ch.d[e];
     if (MAP) {
-      p.seg_dt[(size_t)seg * p.D + d] = dt_sum[e];
+      p.seg_dt[(size_t)seg * p.D + d] = dts[e];
     } else if (p.final_state && sg.j == sg.nseg - 1) {
       store_states<NP>(h[e], p.final_state + ((size_t)sg.seq * p.D + d) * p.N, 1, p.N);
     }

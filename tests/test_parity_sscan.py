@@ -249,3 +249,15 @@ def test_refusals():
             call(**kw)
     with pytest.raises(ValueError):
         m.selective_scan_bwd(c["u"], c["delta"], c["A"], c["B"], c["C"], c["dy"], saved=torch.zeros(8, dtype=torch.uint8, device="cuda"), **kwargs(c))
+
+
+def test_without_gradients_is_the_forward():
+    u, delta, A, B, C = (t.cuda() for t in (torch.randn(1, 21, 40).bfloat16(), torch.randn(1, 21, 40).bfloat16(), -torch.rand(40, 8) - 0.1,
+                                             torch.randn(1, 21, 1, 8).bfloat16(), torch.randn(1, 21, 1, 8).bfloat16()))
+    want, final = lib().selective_scan_fwd(u, delta, A, B, C, output_final_state=True)
+    A.requires_grad_(True)
+    with torch.no_grad():
+        y, h = lib().selective_scan(u, delta, A, B, C, output_final_state=True)
+    assert y.grad_fn is None and torch.equal(y, want) and torch.equal(h, final)
+    y, h = lib().selective_scan(u, delta, A, B, C, output_final_state=True)
+    assert y.grad_fn is not None and torch.equal(y, want) and torch.equal(h, final)
