@@ -337,6 +337,7 @@ void fill(const SscanProblem& P, const SscanPlan& q, const SscanLayout& l, char*
 void set_vectors(const SscanProblem& P, SscanParams* p) {
   p->vec_A = aligned(p->A, 16);
   p->pair = P.D % 2 == 0 && (P.D / P.G) % 2 == 0;
+  p->quad = P.D % 4 == 0 && (P.D / P.G) % 4 == 0;
   const bool groups = P.G == 1 || (P.D / P.G) % 8 == 0;
   p->vec = groups && aligned(p->u, 16) && aligned(p->delta, 16) && aligned(p->z, 16) && aligned(p->dy, 16) && P.u_s % 8 == 0 &&
            P.dt_s % 8 == 0 && (!p->z || P.z_s % 8 == 0) && (!p->dy || P.D % 8 == 0);

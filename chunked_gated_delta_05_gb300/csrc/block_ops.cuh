@@ -32,14 +32,11 @@ __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_approx(1.f +
 constexpr int kLog1p = 9;
 __device__ constexpr float kLog1pTerm[kLog1p + 1] = {1.f,           -0.4999990242f, 0.3332996235f,   -0.2495413302f, 0.1967593617f,
                                                      -0.1530558414f, 0.1060364124f, -0.05695940459f, 0.01985139552f, -0.003244010752f};
-// *slope = d softplus / dx = sigmoid(x).
-__device__ __forceinline__ float softplus(float x, float* slope) {
+__device__ __forceinline__ float softplus(float x) {
   const float e = exp2_approx(-kLog2e * fabsf(x));
   float p = kLog1pTerm[kLog1p];
 #pragma unroll
   for (int i = kLog1p - 1; i >= 0; --i) p = fmaf(p, e, kLog1pTerm[i]);
-  const float r = rcp_approx(1.f + e);
-  *slope = x >= 0.f ? r : e * r;
   return fmaf(e, p, fmaxf(x, 0.f));
 }
 
@@ -82,22 +79,33 @@ __device__ __forceinline__ F2 decay2(F2 dt, F2 a2) {
   return f2(exp2_approx(lo), exp2_approx(hi));
 }
 __device__ __forceinline__ F2 dup2(float x) { return f2(x, x); }
-// softplus of both.
-__device__ __forceinline__ F2 softplus2(F2 x) {
+// 1 / x, sigmoid, silu and softplus (*slope = d softplus / dx = sigmoid(x)) of both.
+__device__ __forceinline__ F2 rcp2(F2 x) {
+  float lo, hi;
+  unf2(x, &lo, &hi);
+  return f2(rcp_approx(lo), rcp_approx(hi));
+}
+__device__ __forceinline__ F2 sigmoid2(F2 z) {
+  float lo, hi;
+  unf2(mul2(z, dup2(-kLog2e)), &lo, &hi);
+  return rcp2(add2(f2(exp2_approx(lo), exp2_approx(hi)), dup2(1.f)));
+}
+__device__ __forceinline__ F2 silu2(F2 z) { return mul2(z, sigmoid2(z)); }
+__device__ __forceinline__ F2 softplus2(F2 x, F2* slope = nullptr) {
   float lo, hi;
   unf2(x, &lo, &hi);
   const F2 e = f2(exp2_approx(-kLog2e * fabsf(lo)), exp2_approx(-kLog2e * fabsf(hi)));
   F2 p = dup2(kLog1pTerm[kLog1p]);
 #pragma unroll
   for (int i = kLog1p - 1; i >= 0; --i) p = fma2(p, e, dup2(kLog1pTerm[i]));
+  if (slope) {
+    const F2 r = rcp2(add2(e, dup2(1.f)));
+    float r0, r1, s0, s1;
+    unf2(r, &r0, &r1);
+    unf2(mul2(e, r), &s0, &s1);
+    *slope = f2(lo >= 0.f ? r0 : s0, hi >= 0.f ? r1 : s1);
+  }
   return fma2(e, p, f2(fmaxf(lo, 0.f), fmaxf(hi, 0.f)));
-}
-// z sigmoid(z) of both.
-__device__ __forceinline__ F2 silu2(F2 z) {
-  float lo, hi;
-  unf2(mul2(z, dup2(-kLog2e)), &lo, &hi);
-  unf2(add2(f2(exp2_approx(lo), exp2_approx(hi)), dup2(1.f)), &lo, &hi);
-  return mul2(z, f2(rcp_approx(lo), rcp_approx(hi)));
 }
 __device__ __forceinline__ float sum2(F2 a) {
   float lo, hi;
@@ -216,6 +224,7 @@ struct SscanParams {
   const int *cu, *seg_base, *ck_base;  // packed: device arrays [seqs+1] (tokens, segments, kept states), else null
   int softplus;
   bool pair;                   // neighbouring channels of a state row 8-byte aligned
+  bool quad;                   // and four of them 16-byte aligned
   bool vec_A;                  // A 16-byte aligned
   bool vec, vec_out;           // u, delta, z (dy): every 8 channels of a block 16-byte aligned; the same of the outputs
   long long u_s, dt_s, z_s, b_s, c_s;  // elements between tokens

@@ -152,7 +152,14 @@ struct ChTile {
   }
   // One channel of token t, and the thread's pair.
   __device__ __forceinline__ float one(int t, int c) const { return __uint_as_float(uint32_t(v[t][c]) << 16); }
-  __device__ __forceinline__ void set_one(int t, int c, float x) { v[t][c] = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+  __device__ __forceinline__ F2 next(int t, int c) const { return f2(one(t, c), one(t + 1, c)); }  // and of the token after it
+  __device__ __forceinline__ void set_next(int t, int c, F2 x) {
+    float lo, hi;
+    unf2(x, &lo, &hi);
+    const uint32_t u = pack_bf16(lo, hi);
+    v[t][c] = uint16_t(u);
+    v[t + 1][c] = uint16_t(u >> 16);
+  }
   __device__ __forceinline__ float2 at(int t) const {
     const uint32_t u = *reinterpret_cast<const uint32_t*>(&v[t][2 * threadIdx.x]);
     return make_float2(bf16_lo(u), bf16_hi(u));

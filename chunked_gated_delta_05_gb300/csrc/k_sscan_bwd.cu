@@ -151,7 +151,6 @@ __device__ __forceinline__ float exchange(float a, float b, bool up, int mask) {
 
 constexpr int kBwdChans = kSscanBwdChans, kBwdThreads = 2 * kBwdChans, kWarps = kBwdThreads / 32;
 constexpr int kTile = kSscanBlock, kHalf = kTile / 2;
-constexpr int kBwdRow = kBwdChans + 2;  // a lane's states and tokens lie 16 banks from the other half's
 
 // A tile of tokens of B or C as fp32, [token][NP], filled by kBwdChans threads.
 template <int NP>
@@ -191,7 +190,7 @@ template <int NP>
 struct BwdSmem {
   VecTile<NP> B[2], C[2];
   ChTile<kTile, kBwdChans, kBwdChans, 8> u[2], delta[2], z[2], dy[2];  // du, ddelta and dz replace u, delta and z
-  float ck[2][NP][kBwdRow];                              // states before the tile
+  float ck[2][2][NP / 2 * kBwdChans + 16];               // states before the tile, each half's [state][channel] 16 banks from the other's
   float4 tok[kTile][kBwdChans];                          // a token's dt, dt u, dy silu(z), d dt / d delta
   float4 sums[2][kTile][kBwdChans];                      // each lane's share of C . h, B . dh and A . w
   float red[kWarps][kTile][2][NP];                         // the warps' sums over their channels: dC, dB
@@ -228,7 +227,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
     g[i] = dA[i] = f2(0.f, 0.f);
   }
   const float bias = param(p.bias, d), skip = param(p.Dskip, d);
-  float dD = 0.f, dbias = 0.f;
+  F2 dD = f2(0.f, 0.f), dbias = f2(0.f, 0.f);
   typename VecTile<NP>::Raw raw;
   auto request = [&](int tb, int buf) {
     const long long row = sg.row0 + tb;
@@ -242,13 +241,27 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
       if (gate) sm.z[buf].load(p.z + row * p.z_s + ch.d0, p.z_s, len, ch.chans, p.vec, part);
       raw = VecTile<NP>::fetch(p.Cm + row * p.c_s + ch.g * p.N, p.c_s, len, p.N, part);
     }
-    const float* ck = p.ck + (size_t)(sg.ck0 + tb / kTile) * p.N * p.D + d;
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&sm.ck[buf][n0][c]));
+    const float* ck = p.ck + (size_t)(sg.ck0 + tb / kTile) * p.N * p.D;
+    if (p.quad) {  // four channels a copy; channels and states that the group lacks read as 0
+      constexpr int kRow = kBwdChans / 4, kStep = kBwdThreads / kRow;
+      const int c4 = tid % kRow * 4, n = tid / kRow;
+      const bool in = c4 < ch.chans;
+      const float* from = ck + (in ? ch.d0 + c4 : 0);
 #pragma unroll
-    for (int n = 0; n < SP; ++n)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + n * kBwdRow * 4), "l"(ck + (size_t)min(n0 + n, p.N - 1) * p.D),
-                   "r"(n < ns ? 4 : 0)
-                   : "memory");
+      for (int j = 0; j < NP / kStep; ++j) {
+        const int s = n + j * kStep;
+        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&sm.ck[buf][s / SP][s % SP * kBwdChans + c4]));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from + (size_t)min(s, p.N - 1) * p.D), "r"(in && s < p.N ? 16 : 0)
+                     : "memory");
+      }
+    } else {
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&sm.ck[buf][half][c]));
+#pragma unroll
+      for (int n = 0; n < SP; ++n)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + n * kBwdChans * 4), "l"(ck + (size_t)min(n0 + n, p.N - 1) * p.D + d),
+                     "r"(n < ns ? 4 : 0)
+                     : "memory");
+    }
     copies_commit();
   };
   auto arrive = [&](int buf) { (low ? sm.B[buf] : sm.C[buf]).put(raw, part); };
@@ -268,16 +281,27 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
     if (tb > 0) request(tb - kTile, buf ^ 1);
     // The lane's half of the tokens. Past the segment's end dt and d dt / d delta are 0, dy is 0, and the state stays.
 #pragma unroll
-    for (int i = 0; i < kHalf; ++i) {
+    for (int i = 0; i < kHalf; i += 2) {
       const int t = half * kHalf + i;
-      const float x = sm.delta[buf].one(t, c) + bias, u = sm.u[buf].one(t, c), dy = sm.dy[buf].one(t, c), z = sm.z[buf].one(t, c);
-      float slope;
-      const float sp = softplus(x, &slope), dt = t < len ? (softplus_on ? sp : x) : 0.f;
-      sm.tok[t][c] = make_float4(dt, dt * u, gate ? dy * (z * sigmoid_fast(z)) : dy, t < len ? (softplus_on ? slope : 1.f) : 0.f);
+      const F2 x = add2(sm.delta[buf].next(t, c), dup2(bias)), u = sm.u[buf].next(t, c), dy = sm.dy[buf].next(t, c);
+      F2 slope;
+      const F2 sp = softplus2(x, &slope), gated = mul2(dy, silu2(sm.z[buf].next(t, c)));
+      float dt[2], dtu[2], dy0[2], dd[2];
+      unf2(softplus_on ? sp : x, &dt[0], &dt[1]);
+      unf2(softplus_on ? slope : dup2(1.f), &dd[0], &dd[1]);
+      unf2(gate ? gated : dy, &dy0[0], &dy0[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        dt[e] = t + e < len ? dt[e] : 0.f;
+        dd[e] = t + e < len ? dd[e] : 0.f;
+      }
+      unf2(mul2(f2(dt[0], dt[1]), u), &dtu[0], &dtu[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sm.tok[t + e][c] = make_float4(dt[e], dtu[e], dy0[e], dd[e]);
     }
     __syncwarp();
     F2 H[kTile][PR];
-    auto before = [&](int t, int s) { return t ? H[t ? t - 1 : 0][s] : f2(sm.ck[buf][n0 + 2 * s][c], sm.ck[buf][n0 + 2 * s + 1][c]); };
+    auto before = [&](int t, int s) { return t ? H[t ? t - 1 : 0][s] : f2(sm.ck[buf][half][2 * s * kBwdChans + c], sm.ck[buf][half][(2 * s + 1) * kBwdChans + c]); };
 #pragma unroll
     for (int t = 0; t < kTile; ++t) {
       const float2 q = *reinterpret_cast<const float2*>(&sm.tok[t][c]);
@@ -330,18 +354,26 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
     __syncwarp();
     // Both lanes' shares together; each lane ends its half of the tokens.
 #pragma unroll
-    for (int i = 0; i < kHalf; ++i) {
+    for (int i = 0; i < kHalf; i += 2) {
       const int t = half * kHalf + i;
-      const float4 s0 = sm.sums[0][t][c], s1 = sm.sums[1][t][c];
-      const float y = s0.x + s1.x, dhB = s0.y + s1.y, w = s0.z + s1.z;
-      const float4 q = sm.tok[t][c];
-      const float u = sm.u[buf].one(t, c), dy = sm.dy[buf].one(t, c), z = sm.z[buf].one(t, c), sig = sigmoid_fast(z);
-      const float dd = fmaf(u, dhB, 0.6931471805599453f * w) * q.w;
-      dD = fmaf(q.z, u, dD);
-      dbias += dd;
-      sm.u[buf].set_one(t, c, fmaf(q.x, dhB, skip * q.z));
-      sm.delta[buf].set_one(t, c, dd);
-      sm.z[buf].set_one(t, c, dy * fmaf(skip, u, y) * (sig * fmaf(z, 1.f - sig, 1.f)));
+      float y[2], dhB[2], w[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 s0 = sm.sums[0][t + e][c], s1 = sm.sums[1][t + e][c];
+        y[e] = s0.x + s1.x;
+        dhB[e] = s0.y + s1.y;
+        w[e] = s0.z + s1.z;
+      }
+      const float4 q0 = sm.tok[t][c], q1 = sm.tok[t + 1][c];
+      const F2 u = sm.u[buf].next(t, c), z = sm.z[buf].next(t, c), dy0 = f2(q0.z, q1.z), B2 = f2(dhB[0], dhB[1]);
+      const F2 dd = mul2(fma2(u, B2, mul2(dup2(0.6931471805599453f), f2(w[0], w[1]))), f2(q0.w, q1.w)), sig = sigmoid2(z);
+      dD = fma2(dy0, u, dD);
+      dbias = add2(dbias, dd);
+      const F2 slope = mul2(sig, fma2(z, fma2(sig, dup2(-1.f), dup2(1.f)), dup2(1.f)));
+      const F2 dz = mul2(mul2(sm.dy[buf].next(t, c), fma2(dup2(skip), u, f2(y[0], y[1]))), slope);
+      sm.u[buf].set_next(t, c, fma2(f2(q0.x, q1.x), B2, mul2(dup2(skip), dy0)));
+      sm.delta[buf].set_next(t, c, dd);
+      sm.z[buf].set_next(t, c, dz);
     }
     if (tb > 0) arrive(buf ^ 1);
     __syncthreads();
@@ -362,15 +394,15 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
       if (t < len && n < p.N) p.part_bc[((size_t)cb * p.rows + row + t) * 2 * p.N + which * p.N + n] = r;
     }
   }
-  dD += __shfl_xor_sync(0xffffffffu, dD, 16);
-  dbias += __shfl_xor_sync(0xffffffffu, dbias, 16);
+  const float dD_half = sum2(dD), dbias_half = sum2(dbias);
+  const float dD_sum = dD_half + __shfl_xor_sync(0xffffffffu, dD_half, 16), dbias_sum = dbias_half + __shfl_xor_sync(0xffffffffu, dbias_half, 16);
   if (!live) return;
   if (p.dh0 && sg.j == 0) store_states<SP>(g, p.dh0 + ((size_t)sg.seq * p.D + d) * p.N + n0, 1, ns);
   float* par = p.part_par + (size_t)seg * (p.N + 2) * p.D + d;
   store_states<SP>(dA, par + (size_t)n0 * p.D, p.D, ns);
   if (half == 0) {
-    par[(size_t)p.N * p.D] = dD;
-    par[(size_t)(p.N + 1) * p.D] = dbias;
+    par[(size_t)p.N * p.D] = dD_sum;
+    par[(size_t)(p.N + 1) * p.D] = dbias_sum;
   }
 }
 

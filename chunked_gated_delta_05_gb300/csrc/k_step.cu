@@ -294,8 +294,7 @@ __global__ void __launch_bounds__(128) k_sscan_step(SscanStepParams p) {
     float y = 0.f;
     if (row.slot >= 0) {
       const float u = bf16_lo(row.u), x = bf16_lo(row.dt) + bias, z = bf16_lo(row.z);
-      float slope;
-      const float dt = p.softplus ? softplus(x, &slope) : x, dtu = dt * u;
+      const float dt = p.softplus ? softplus(x) : x, dtu = dt * u;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint2 bq = row.B[e / 4], cq = row.C[e / 4];
