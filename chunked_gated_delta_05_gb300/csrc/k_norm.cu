@@ -55,6 +55,32 @@ struct Raw<1, T> {
   __device__ __forceinline__ void load(const T* src) { x = src[0]; }
   __device__ __forceinline__ float operator[](int) const { return float(x); }
 };
+
+// The arithmetic of the backward is written once for pairs of elements and for single ones.
+template <int VEC>
+struct Elems {  // 8: pairs
+  using T = F2;
+  static constexpr int kCount = VEC / 2;
+  template <typename R>
+  __device__ __forceinline__ static T of(const R& raw, int i) { return f2(raw[2 * i], raw[2 * i + 1]); }
+  __device__ __forceinline__ static T dup(float x) { return dup2(x); }
+  __device__ __forceinline__ static void put(float* v, int i, T x) { unf2(x, v + 2 * i, v + 2 * i + 1); }
+};
+template <>
+struct Elems<1> {
+  using T = float;
+  static constexpr int kCount = 1;
+  template <typename R>
+  __device__ __forceinline__ static T of(const R& raw, int i) { return raw[i]; }
+  __device__ __forceinline__ static T dup(float x) { return x; }
+  __device__ __forceinline__ static void put(float* v, int i, T x) { v[i] = x; }
+};
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float sum2(float a) { return a; }
+__device__ __forceinline__ float sigmoid2(float z) { return sigmoid_fast(z); }
+
 template <int VEC>
 __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float* v) {
   if constexpr (VEC == 8)
@@ -197,10 +223,15 @@ struct BwdRow {
   }
 };
 
+// Blocks an SM that the registers must allow: four where a thread holds one vector (SiLU's gate then takes 64 instead of 79
+// registers: 87 -> 63 us at 262144 x 128, 107 -> 79 us at 16384 x 2048); else the compiler's choice, which was the fastest.
+template <int VEC, int NV>
+constexpr int kBwdBlocks = VEC == 8 && NV == 1 ? 4 : 0;
+
 // One pass per row; each thread keeps its columns' weight gradients in registers over all rows of its group, the groups of
 // the block add theirs in shared memory in a fixed order, and the block writes one row of partial sums.
 template <int KIND, int VEC, int NV, int THREADS, typename ST>
-__global__ void __launch_bounds__(THREADS) k_norm_bwd(NormParams p, int G) {
+__global__ void __launch_bounds__(THREADS, kBwdBlocks<VEC, NV>) k_norm_bwd(NormParams p, int G) {
   constexpr bool kAhead = NV == 1 && KIND != kAdd;
   extern __shared__ float acc_s[];
   __shared__ float red[2][2][32];
@@ -209,11 +240,13 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(NormParams p, int G) {
   const float inv = 1.f / float(p.width);
   const long long step = (long long)gridDim.x * per_block;
   wait_for_previous();
-  float dw[NV][VEC];
+  using E = Elems<VEC>;
+  using T = typename E::T;
+  T dw[NV][E::kCount];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[j][e] = 0.f;
+    for (int e = 0; e < E::kCount; ++e) dw[j][e] = E::dup(0.f);
   int turn = 0;
   BwdRow<KIND, VEC, NV, ST> row, next;
   Raw<VEC, float> w[NV];
@@ -225,25 +258,27 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(NormParams p, int G) {
     const long long base = r * p.width;
     if (kAhead) next.load(p, r + step, lane, G, units);
     else row.load(p, r, lane, G, units);
-    float s[2] = {0.f, 0.f}, sg[NV][VEC];  // sigmoid(gate), used again below
+    T s2[2] = {E::dup(0.f), E::dup(0.f)}, sg[NV][E::kCount];  // sigmoid(gate), used again below
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int u = lane + j * G;
       if (live && u < units) {
         if (!kAhead) w[j].load(p.weight + u * VEC);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float v = row.x[j][e];
-          float dn = row.dy[j][e] * w[j][e];
+        for (int e = 0; e < E::kCount; ++e) {
+          const T v = E::of(row.x[j], e);
+          T dn = mul2(E::of(row.dy[j], e), E::of(w[j], e));
           if (KIND != kAdd) {
-            sg[j][e] = sigmoid_fast(row.gate[j][e]);
-            dn *= act_of<KIND>(row.gate[j][e], sg[j][e]);
+            const T g = E::of(row.gate[j], e);
+            sg[j][e] = sigmoid2(g);
+            dn = mul2(dn, KIND == kSilu ? mul2(g, sg[j][e]) : sg[j][e]);
           }
-          s[0] = fmaf(v, v, s[0]);
-          s[1] = fmaf(dn, v, s[1]);
+          s2[0] = fma2(v, v, s2[0]);
+          s2[1] = fma2(dn, v, s2[1]);
         }
       }
     }
+    float s[2] = {sum2(s2[0]), sum2(s2[1])};
     row_sum<2>(s, G, red[turn]);
     const float rstd = rsqrtf(fmaf(s[0], inv, p.eps));
     const float c = -s[1] * inv * rstd * rstd * rstd;  // xh mean(dn w xh) rstd = -x c
@@ -255,17 +290,18 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(NormParams p, int G) {
         if (!kAhead) w[j].load(p.weight + u * VEC);
         float o[VEC], q[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float v = row.x[j][e], xh = v * rstd, dyw = row.dy[j][e] * w[j][e];
-          float dn = row.dy[j][e], dnw = dyw;
+        for (int e = 0; e < E::kCount; ++e) {
+          const T one = E::dup(1.f), v = E::of(row.x[j], e), xh = mul2(v, E::dup(rstd)), dy = E::of(row.dy[j], e), dyw = mul2(dy, E::of(w[j], e));
+          T dn = dy, dnw = dyw;
           if (KIND != kAdd) {
-            const float a = sg[j][e], act = act_of<KIND>(row.gate[j][e], a);
-            q[e] = dyw * xh * (KIND == kSilu ? fmaf(act, 1.f - a, a) : a * (1.f - a));  // act' = sg + act (1 - sg), or sg (1 - sg)
-            dn *= act;
-            dnw *= act;
+            const T a = sg[j][e], act = KIND == kSilu ? mul2(E::of(row.gate[j], e), a) : a, not_a = fma2(a, E::dup(-1.f), one);
+            // act' = sg + act (1 - sg), or sg (1 - sg)
+            E::put(q, e, mul2(mul2(dyw, xh), KIND == kSilu ? fma2(act, not_a, a) : mul2(a, not_a)));
+            dn = mul2(dn, act);
+            dnw = mul2(dnw, act);
           }
-          o[e] = fmaf(dnw, rstd, v * c);
-          dw[j][e] = fmaf(dn, xh, dw[j][e]);
+          E::put(o, e, fma2(dnw, E::dup(rstd), mul2(v, E::dup(c))));
+          dw[j][e] = fma2(dn, xh, dw[j][e]);
         }
         if (KIND == kAdd) {
           if (p.dstream) {
@@ -286,39 +322,50 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(NormParams p, int G) {
   for (int g = 0; g < per_block; ++g) {
     if (grp == g) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        float mine[VEC];
+#pragma unroll
+        for (int e = 0; e < E::kCount; ++e) E::put(mine, e, dw[j][e]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const int u = lane + j * G;
           if (u >= units) continue;
           const int at = u * VEC + e;
-          const float t = g == 0 ? dw[j][e] : acc_s[at] + dw[j][e];
+          const float t = g == 0 ? mine[e] : acc_s[at] + mine[e];
           if (g == per_block - 1)
             p.part[(long long)blockIdx.x * p.width + at] = t;
           else
             acc_s[at] = t;
         }
+      }
     }
     if (per_block > 1) __syncthreads();
   }
 }
 
-// dweight[c] = sum over the blocks' partial rows, in a fixed order: 32 columns x 32 row lanes per block.
+// dweight[c] = sum over the blocks' partial rows, in a fixed order: COLS columns x 1024 / COLS row lanes per block. 8 columns
+// (a sector) give few columns more blocks and a thread fewer loads in turn: 1.2 us less at 128 and 2048 columns; 32 (a
+// line) read wide rows faster: 5 us less at 8192.
+template <int COLS>
 __global__ void __launch_bounds__(1024) k_norm_reduce(const float* part, float* dw, int rows, int width) {
-  __shared__ float s[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  constexpr int kLanes = 1024 / COLS;
+  __shared__ float s[COLS][kLanes + 4];
+  const int x = threadIdx.x % COLS, y = threadIdx.x / COLS, c = blockIdx.x * COLS + x;
   wait_for_previous();
   float t = 0.f;
   if (c < width)
 #pragma unroll 10
-    for (int r = threadIdx.y; r < rows; r += 32) t += part[(long long)r * width + c];
-  s[threadIdx.y][threadIdx.x] = t;
+    for (int r = y; r < rows; r += kLanes) t += part[(long long)r * width + c];
+  s[x][y] = t;
   __syncthreads();
-  float v = s[threadIdx.x][threadIdx.y];  // lane: row group, warp: column
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cc = blockIdx.x * COLS + warp;
+  if (warp >= COLS || cc >= width) return;
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kLanes / 32; ++i) v += s[warp][lane + 32 * i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int cc = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && cc < width) dw[cc] = v;
+  if (lane == 0) dw[cc] = v;
 }
 
 struct Plan {
@@ -383,7 +430,9 @@ cudaError_t run_bwd(const NormParams& p, bool vec8, cudaStream_t s) {
   GDN_NORM_DISPATCH(q, GDN_CALL)
 #undef GDN_CALL
   if (e != cudaSuccess) return e;
-  return launch_after(k_norm_reduce, (p.width + 31) / 32, dim3(32, 32), 0, s, (const float*)p.part, p.dweight, grid, p.width);
+  if (p.width <= 8 * 2 * p.sms)  // 8-column blocks, two of which fit an SM, are all resident
+    return launch_after(k_norm_reduce<8>, (p.width + 7) / 8, 1024, 0, s, (const float*)p.part, p.dweight, grid, p.width);
+  return launch_after(k_norm_reduce<32>, (p.width + 31) / 32, 1024, 0, s, (const float*)p.part, p.dweight, grid, p.width);
 }
 
 bool all16(std::initializer_list<const void*> ps) {
