@@ -203,10 +203,10 @@ __global__ void __launch_bounds__(THREADS) k_norm_fwd(NormParams p, int G) {
   }
 }
 
-template <int KIND, int VEC, int NV, typename ST>
+template <int KIND, int VEC, int NV, typename ST, bool DS>
 struct BwdRow {
   Raw<VEC, __nv_bfloat16> dy[NV], gate[NV];
-  Raw<VEC, ST> x[NV], ds[NV];
+  Raw<VEC, ST> x[NV], ds[DS ? NV : 1];
   __device__ __forceinline__ void load(const NormParams& p, long long r, int lane, int G, int units) {
     if (r >= p.rows) return;
 #pragma unroll
@@ -217,23 +217,29 @@ struct BwdRow {
         x[j].load(KIND == kAdd ? static_cast<const ST*>(p.stream) + at : reinterpret_cast<const ST*>(p.x) + at);
         dy[j].load(p.dy + at);
         if (KIND != kAdd) gate[j].load(p.gate + at);
-        if (KIND == kAdd && p.dstream) ds[j].load(static_cast<const ST*>(p.dstream) + at);
+        if (DS && KIND == kAdd && p.dstream) ds[j].load(static_cast<const ST*>(p.dstream) + at);
       }
     }
   }
 };
 
-// Blocks an SM that the registers must allow: four where a thread holds one vector (SiLU's gate then takes 64 instead of 79
-// registers: 87 -> 63 us at 262144 x 128, 107 -> 79 us at 16384 x 2048); else the compiler's choice, which was the fastest.
-template <int VEC, int NV>
-constexpr int kBwdBlocks = VEC == 8 && NV == 1 ? 4 : 0;
+// Rows of more than one vector a thread keep their weight gradients in shared memory instead of registers (and load dstream
+// only when it is added), where that leaves room for another block: with an fp32 stream (8192 wide, 4096 wide: 71 -> 64, 58 ->
+// 49 us for 268 MB) and with a gate (109 -> 76, 84 -> 79 us for 336 MB); with a bf16 stream it costs (8192 wide 48.8 -> 51.9).
+template <int KIND, int VEC, int NV, int THREADS, typename ST>
+constexpr bool kLean = VEC == 8 && NV > 1 && THREADS == 256 && (KIND != kAdd || sizeof(ST) == 4);
+// Blocks an SM that the registers must allow, where the compiler's own choice was slower: four for one vector a thread (SiLU's
+// gate then takes 64 instead of 79 registers: 87 -> 63 us at 262144 x 128, 107 -> 79 us at 16384 x 2048), and for gates
+// four for two vectors (86 -> 79 us at 8192 x 4096) and two for four (107 -> 76 us at 4096 x 8192).
+template <int KIND, int VEC, int NV, int THREADS>
+constexpr int kBwdBlocks = VEC != 8 || THREADS != 256 ? 0 : NV == 1 ? 4 : KIND == kAdd ? 0 : NV == 2 ? 4 : 2;
 
 // One pass per row; each thread keeps its columns' weight gradients in registers over all rows of its group, the groups of
 // the block add theirs in shared memory in a fixed order, and the block writes one row of partial sums.
 template <int KIND, int VEC, int NV, int THREADS, typename ST>
-__global__ void __launch_bounds__(THREADS, kBwdBlocks<VEC, NV>) k_norm_bwd(NormParams p, int G) {
-  constexpr bool kAhead = NV == 1 && KIND != kAdd;
-  extern __shared__ float acc_s[];
+__global__ void __launch_bounds__(THREADS, kBwdBlocks<KIND, VEC, NV, THREADS>) k_norm_bwd(NormParams p, int G) {
+  constexpr bool kAhead = NV == 1 && KIND != kAdd, kShared = kLean<KIND, VEC, NV, THREADS, ST>;
+  extern __shared__ __align__(16) float acc_s[];
   __shared__ float red[2][2][32];
   const int per_block = blockDim.x / G, lane = threadIdx.x & (G - 1), grp = threadIdx.x / G;
   const int units = p.width / VEC;
@@ -243,12 +249,17 @@ __global__ void __launch_bounds__(THREADS, kBwdBlocks<VEC, NV>) k_norm_bwd(NormP
   using E = Elems<VEC>;
   using T = typename E::T;
   T dw[NV][E::kCount];
+  // a unit's eight sums in shared memory, four and four
+  auto lean = [&](int u, int half) { return reinterpret_cast<float4*>(acc_s) + half * units + u; };
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
 #pragma unroll
     for (int e = 0; e < E::kCount; ++e) dw[j][e] = E::dup(0.f);
+    const int u = lane + j * G;
+    if (kShared && u < units) *lean(u, 0) = *lean(u, 1) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   int turn = 0;
-  BwdRow<KIND, VEC, NV, ST> row, next;
+  BwdRow<KIND, VEC, NV, ST, !kShared> row, next;
   Raw<VEC, float> w[NV];
   if (kAhead && lane < units) w[0].load(p.weight + lane * VEC);
   if (kAhead) row.load(p, (long long)blockIdx.x * per_block + grp, lane, G, units);
@@ -288,6 +299,13 @@ __global__ void __launch_bounds__(THREADS, kBwdBlocks<VEC, NV>) k_norm_bwd(NormP
       if (live && u < units) {
         const long long at = base + (long long)u * VEC;
         if (!kAhead) w[j].load(p.weight + u * VEC);
+        if (kShared && KIND == kAdd && p.dstream) row.ds[0].load(static_cast<const ST*>(p.dstream) + at);
+        if (kShared) {
+          const float4 a = *lean(u, 0), b = *lean(u, 1);
+          const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int e = 0; e < E::kCount; ++e) dw[j][e] = E::of(v, e);
+        }
         float o[VEC], q[VEC];
 #pragma unroll
         for (int e = 0; e < E::kCount; ++e) {
@@ -303,10 +321,17 @@ __global__ void __launch_bounds__(THREADS, kBwdBlocks<VEC, NV>) k_norm_bwd(NormP
           E::put(o, e, fma2(dnw, E::dup(rstd), mul2(v, E::dup(c))));
           dw[j][e] = fma2(dn, xh, dw[j][e]);
         }
+        if (kShared) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < E::kCount; ++e) E::put(v, e, dw[j][e]);
+          *lean(u, 0) = make_float4(v[0], v[1], v[2], v[3]);
+          *lean(u, 1) = make_float4(v[4], v[5], v[6], v[7]);
+        }
         if (KIND == kAdd) {
           if (p.dstream) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] += row.ds[j][e];
+            for (int e = 0; e < VEC; ++e) o[e] += row.ds[kShared ? 0 : j][e];
           }
           if (p.dresidual) store_row<VEC>(static_cast<ST*>(p.dresidual) + at, o);
 #pragma unroll
@@ -318,6 +343,16 @@ __global__ void __launch_bounds__(THREADS, kBwdBlocks<VEC, NV>) k_norm_bwd(NormP
       }
     }
     if (kAhead) row = next;
+  }
+  if (kShared) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int u = lane + j * G;
+      if (u < units)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) *reinterpret_cast<float4*>(p.part + (long long)blockIdx.x * p.width + u * 8 + half * 4) = *lean(u, half);
+    }
+    return;
   }
   for (int g = 0; g < per_block; ++g) {
     if (grp == g) {
@@ -424,9 +459,9 @@ cudaError_t run_bwd(const NormParams& p, bool vec8, cudaStream_t s) {
   const long long blocks = (p.rows + per_block - 1) / per_block;
   const long long most = std::min((long long)p.sms * kBwdBlocksPerSm, (long long)kMaxPartialRows);
   const int grid = int(std::min(blocks, most));
-  const size_t smem = per_block > 1 ? size_t(p.width) * 4 : 0;
   cudaError_t e = cudaSuccess;
-#define GDN_CALL(VEC, NV, T) e = launch_after(k_norm_bwd<KIND, VEC, NV, T, ST>, grid, T, smem, s, p, q.G)
+#define GDN_CALL(VEC, NV, T) \
+  e = launch_after(k_norm_bwd<KIND, VEC, NV, T, ST>, grid, T, per_block > 1 || kLean<KIND, VEC, NV, T, ST> ? size_t(p.width) * 4 : 0, s, p, q.G)
   GDN_NORM_DISPATCH(q, GDN_CALL)
 #undef GDN_CALL
   if (e != cudaSuccess) return e;

@@ -210,3 +210,22 @@ def test_refusals():
                 lambda: m.add_rms_norm_bwd(x, x.float(), x, w), lambda: m.add_rms_norm_bwd(x, None, x.float(), w, has_residual=False)):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("rows,width", [(1300, 2568), (1300, 4096), (1300, 5000), (700, 8192), (700, 8200)])
+def test_many_wide_rows(rows, width):
+    """More rows than blocks, of more than one vector a thread: the weight gradients gather over a block's rows."""
+    g = gen(rows + width)
+    x, gate, w, dy, ds = rn(g, rows, width), rn(g, rows, width), 1 + rn(g, width, dtype=torch.float32, std=0.1), rn(g, rows, width), rn(g, rows, width, dtype=torch.float32)
+    for act in ("silu", "sigmoid"):
+        got = lib().gated_rms_norm_bwd(x, gate, w, dy, eps=1e-5, activation=act)
+        want = block.gated_norm_bwd(f64(x), f64(gate), f64(w), f64(dy), 1e-5, act)
+        close_bf16("dx", got[0], want[0])
+        close_bf16("dgate", got[1], want[1])
+        close_f32("dweight", got[2], want[2])
+    for stream, d in ((ds, ds.flip(0).contiguous()), (ds, None), (x, gate)):
+        dx, dres, dw = lib().add_rms_norm_bwd(dy, d, stream, w, eps=1e-5, residual_scale=0.7)
+        rx, rr, rw = block.add_norm_bwd(f64(dy), None if d is None else f64(d), f64(stream), f64(w), 1e-5, 0.7)
+        close_bf16("dx", dx, rx)
+        close_stream(dres, rr, stream.dtype)
+        close_f32("dweight", dw, rw)
