@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(THREADS) k_norm_fwd(NormParams p, int G) {
   constexpr bool kAhead = NV == 1 && KIND != kAdd;
   __shared__ float red[2][1][32];
   wait_for_previous();
-  const int per_block = blockDim.x / G, lane = threadIdx.x & (G - 1);
+  const bool whole = G == blockDim.x;  // else G is a power of two
+  const int log = 31 - __clz(G), per_block = whole ? 1 : blockDim.x >> log, grp = whole ? 0 : threadIdx.x >> log, lane = threadIdx.x - (grp << log);
   const int units = p.width / VEC;
   const float inv = 1.f / float(p.width);
   const long long step = (long long)gridDim.x * per_block;
@@ -165,9 +166,9 @@ __global__ void __launch_bounds__(THREADS) k_norm_fwd(NormParams p, int G) {
 #pragma unroll
   for (int j = 0; j < NV; ++j)
     if (lane + j * G < units) w[j].load(p.weight + (lane + j * G) * VEC);
-  if (kAhead) row.load(p, (long long)blockIdx.x * per_block + threadIdx.x / G, lane, G, units);
+  if (kAhead) row.load(p, (long long)blockIdx.x * per_block + grp, lane, G, units);
   for (long long r0 = (long long)blockIdx.x * per_block; r0 < p.rows; r0 += step, turn ^= 1) {
-    const long long r = r0 + threadIdx.x / G;
+    const long long r = r0 + grp;
     const bool live = r < p.rows;
     const long long base = r * p.width;
     if (kAhead) next.load(p, r + step, lane, G, units);
@@ -234,7 +235,7 @@ constexpr bool kLean = VEC == 8 && NV > 1 && THREADS == 256 && (KIND != kAdd || 
 template <int KIND, int VEC, int NV, int THREADS>
 constexpr int kBwdBlocks = VEC != 8 || THREADS != 256 ? 0 : NV == 1 ? 4 : KIND == kAdd ? 0 : NV == 2 ? 4 : 2;
 
-// One pass per row; each thread keeps its columns' weight gradients in registers over all rows of its group, the groups of
+// One pass per row; each thread keeps its columns' weight gradients (in registers, or kLean) over all rows of its group, the groups of
 // the block add theirs in shared memory in a fixed order, and the block writes one row of partial sums.
 template <int KIND, int VEC, int NV, int THREADS, typename ST>
 __global__ void __launch_bounds__(THREADS, kBwdBlocks<KIND, VEC, NV, THREADS>) k_norm_bwd(NormParams p, int G) {
@@ -442,12 +443,15 @@ constexpr int kMaxPartialRows = 160 * kBwdBlocksPerSm;
 
 template <int KIND, typename ST>
 cudaError_t run_fwd(const NormParams& p, bool vec8, cudaStream_t s) {
-  const Plan q = plan_rows(p.width, vec8);
-  const int per_block = q.threads / q.G;
+  Plan q = plan_rows(p.width, vec8);
+  int block = q.threads;
+  // No warp of a wide row without work: 53 -> 36 us at 5120 columns. (The backward was slower so: 62 -> 67 us at 6144.)
+  if (vec8 && q.nv > 1) block = q.G = ((p.width / 8 + q.nv - 1) / q.nv + 31) / 32 * 32;
+  const int per_block = block / q.G;
   const long long blocks = (p.rows + per_block - 1) / per_block;
   // resident blocks that walk the rows a warp or less holds, one loaded ahead; else a block per row (or few rows)
   const int grid = int(std::min(blocks, KIND != kAdd && q.nv == 1 && q.G <= 32 ? (long long)p.sms * kFwdBlocksPerSm : 1ll << 30));
-#define GDN_CALL(VEC, NV, T) return launch_after(k_norm_fwd<KIND, VEC, NV, T, ST>, grid, T, 0, s, p, q.G)
+#define GDN_CALL(VEC, NV, T) return launch_after(k_norm_fwd<KIND, VEC, NV, T, ST>, grid, block, 0, s, p, q.G)
   GDN_NORM_DISPATCH(q, GDN_CALL)
 #undef GDN_CALL
 }
