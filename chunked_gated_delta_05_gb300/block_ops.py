@@ -88,7 +88,7 @@ def _rows_of(name, t, dtype, shape, dev, inner, width):
 
 def _like(t):
     """An empty contiguous tensor of t's shape (None of None)."""
-    return None if t is None else torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+    return None if t is None else torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _pool(state_indices, B, slots, dev):
@@ -107,7 +107,7 @@ def _status(status, dev):
 
 def _norm_workspace(rows, width, like):
     n = _lib.size("gdn_norm_bwd_workspace_size", _norm_desc(rows, width, 0.0, 1.0, 0, 0))
-    return like.new_empty(n, dtype=torch.uint8), n
+    return torch.empty(n, dtype=torch.uint8, device=like.device), n
 
 
 def _norm_shape(x):
@@ -253,10 +253,10 @@ def causal_conv1d_state(x, weight, *, dilation=1, cu_seqlens: Optional[Sequence[
     ws_bytes = lib.gdn_conv_fwd_workspace_size(desc)
     if ws_bytes == 0:
         _lib.check(_lib.GDN_EINVAL)
-    state = x.new_empty((N, HW, x.shape[2]))
+    state = torch.empty((N, HW, x.shape[2]), dtype=_BF16, device=x.device)
     if HW == 0:
         return state
-    ws = x.new_empty(ws_bytes, dtype=torch.uint8)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
     a = _lib.ConvFwdArgs(x=x.data_ptr(), halo=_p(halo), y=state.data_ptr(), workspace=ws.data_ptr(), workspace_bytes=ws_bytes)
     _lib.check(lib.gdn_conv_state(desc, a, _stream(dev)))
     return state
@@ -381,12 +381,12 @@ def selective_scan_fwd(u, delta, A, B, C, *, D=None, z=None, delta_bias=None, de
         _want("initial_state", initial_state, _F32, state_shape, dev)
     ws_bytes = _lib.size("gdn_sscan_fwd_workspace_size", d)
     y = _like(u)
-    final = A.new_empty(state_shape) if output_final_state else None
-    ws = u.new_empty(ws_bytes, dtype=torch.uint8)
+    final = torch.empty(state_shape, dtype=_F32, device=A.device) if output_final_state else None
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=u.device)
     saved_bytes, saved = 0, None
     if save:
         saved_bytes = _lib.size("gdn_sscan_saved_size", d)
-        saved = u.new_empty(saved_bytes, dtype=torch.uint8)
+        saved = torch.empty(saved_bytes, dtype=torch.uint8, device=u.device)
     _run("gdn_sscan_fwd", d, _scan_fwd_args(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(delta_bias), _p(z), _p(initial_state),
                                             y.data_ptr(), _p(final), ws.data_ptr(), ws_bytes, _p(saved), saved_bytes), dev)
     return (y, final, saved) if save else (y, final)
@@ -413,7 +413,7 @@ def selective_scan_bwd(u, delta, A, B, C, dy, *, D=None, z=None, delta_bias=None
 
     du, ddelta, dz = torch.empty_like(dy), torch.empty_like(dy), None if z is None else torch.empty_like(dy)
     dA, dB, dC, dD, dbias, dh0 = torch.empty_like(A), _like(B), _like(C), _like(D), _like(delta_bias), _like(initial_state)
-    ws = u.new_empty(ws_bytes, dtype=torch.uint8)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=u.device)
     _run("gdn_sscan_bwd", d, _scan_bwd_args(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(delta_bias), _p(z), _p(initial_state),
                                             dy.data_ptr(), _p(dfinal), du.data_ptr(), ddelta.data_ptr(), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _p(dD), _p(dbias), _p(dz),
                                             _p(dh0), ws.data_ptr(), ws_bytes, _p(saved), saved_bytes), dev)
