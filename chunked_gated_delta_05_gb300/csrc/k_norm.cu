@@ -11,10 +11,9 @@
 // of every tensor. All sums are fp32. Rows of widths that are no multiple of 8, or unaligned tensors, take the element
 // path (VEC = 1).
 //
-// Bound: HBM, a few operations a byte. On GB300: residual norm of 8192 x 2048 with an fp32 stream, forward and backward, 80 us
-// for 470 MB (5.9 TB/s, 87% of the copy rate: 31 + 44 + 5 us for the partial sums); gated norm of 262144 x 128, both, 95 us
-// for 537 MB (5.7 TB/s; the sigmoids and the backward's sums keep the schedulers two thirds busy); its forward alone at
-// 131072 x 128, 15.8 us for 101 MB (6.4 TB/s).
+// Bound: HBM, a few operations a byte. On GB300: residual norm of 8192 x 2048 with an fp32 stream, forward and backward, 78.5 us
+// for 470 MB (6.0 TB/s, 88% of the copy rate: 31.3 + 47.2 us, the sums of the weight gradients included); gated norm of 262144 x
+// 128, both, 91.8 us for 537 MB (5.9 TB/s); its forward alone at 131072 x 128, 15.7 us for 101 MB (6.4 TB/s).
 #include <algorithm>
 #include <initializer_list>
 

@@ -6,10 +6,15 @@
 //
 // Two lanes walk one channel. The states they need in reverse come from those a training forward keeps before every 8th
 // token (8 bytes a token and channel): each tile of 8, last to first, is run forward again and then walked back. Keeping
-// fewer costs another forward walk, which this kernel, bound by its instructions at 7% of HBM's rate, cannot hide as it
-// does the reads. The adjoint chain is cut into segments like the forward's. The sums over channels in dB and dC begin as matrix products with ones: a
-// lane's four states are its share of the A operand of m16n8k8, whose products add up four lanes' channels (tf32 operands;
-// the results are bf16), and three exchanges add up the groups of lanes. All other sums are fp32.
+// fewer costs another forward walk, which this kernel, bound by its instructions at 15% of HBM's rate, cannot hide as it
+// does the reads. The adjoint chain is cut into segments like the forward's. The sums over channels in dB and dC begin as
+// matrix products with ones: a lane's four states are its share of the A operand of m16n8k8, whose products add up four
+// lanes' channels (tf32 operands; the results are bf16), and three exchanges add up the groups of lanes. All other sums are fp32.
+//
+// On GB300, 4093 tokens in 7 documents x 2048 channels x 16 states: 205 us (adjoint maps 38, composition 8, this walk
+// 160, last sums 8 warm); 168 registers leave three warps a scheduler, which issue 55% of the time. Exchanges between the two
+// lanes in place of their sums' trip through shared memory: 212 -> 226 us for the backward. Adding up the lane groups at the
+// tile's end in place of the exchanges: 212 -> 222 us.
 #include <atomic>
 
 #include "k_sscan.cuh"
@@ -300,7 +305,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
       for (int e = 0; e < 2; ++e) sm.tok[t + e][c] = make_float4(dt[e], dtu[e], dy0[e], dd[e]);
     }
     __syncwarp();
-    F2 H[kTile][PR];
+    F2 H[kTile][PR] = {};
     auto before = [&](int t, int s) { return t ? H[t ? t - 1 : 0][s] : f2(sm.ck[buf][half][2 * s * kBwdChans + c], sm.ck[buf][half][(2 * s + 1) * kBwdChans + c]); };
 #pragma unroll
     for (int t = 0; t < kTile; ++t) {

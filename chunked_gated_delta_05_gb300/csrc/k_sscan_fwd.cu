@@ -6,6 +6,10 @@
 // exponential and four multiply-adds (packed in state pairs), which the exponential unit and the fp32 pipe bound
 // alike: about 4 cycles per warp and state on each.
 //
+// On GB300, 8192 tokens x 4096 channels x 16 states: 245 us (maps 98, composition 9, outputs 140; 2.2e12 state updates a
+// second in two passes, 1.1 TB/s of algorithmic bytes), with both units 45 to 60% busy. In isolation a pass's
+// loop takes 290 cycles per warp-token (64 channels) and scheduler, where either unit alone would take 130 to 150.
+//
 // Few channels leave the GPU empty, so the tokens are cut into segments of L. The map of a segment,
 // h_out = exp(A sum dt) h_in + F, is diagonal: a first pass runs every segment but the last from zero for F and sum dt,
 // a small kernel composes them into entry states, and a second pass runs every segment from its entry state.

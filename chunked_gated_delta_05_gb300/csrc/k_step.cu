@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(256) k_delta_step(DeltaStepParams p) {
 // LPC lanes per channel, eight states each. A block walks its channels over several batch rows: A, D and the bias are read
 // once, a row's loads are in flight while the one before it is computed, and its slot is known a row earlier still. VEC: the
 // states, A, B and C in 16- and 8-byte pieces (N a multiple of 4 and everything aligned). 120 of 160 rows x 4096 channels x 16
-// states: 15.1 us for 59 MB (3.9 TB/s). The states (42 MB) come from L2, whose latency bounds it: 88 registers leave five
+// states: 14.9 us for 59 MB (4.0 TB/s). The states (42 MB) come from L2, whose latency bounds it: 80 registers leave six
 // blocks of four warps an SM, each thread with one row in flight and one in hand.
 template <bool VEC>
 struct SscanRow {
