@@ -29,7 +29,7 @@ __device__ __forceinline__ int slot_of(const int* index, int b, int slots, int* 
 
 // Four channels per thread: the weights stay in registers while the block walks its batch rows. Latency bounds it: the state
 // of a serving batch (250 of 320 rows x 6144 channels x 3: 12 MB) stays in L2, and a thread has one row's loads in flight.
-// 4.4 us for those 22 MB of reads and writes (4.9 TB/s), 1.5 us for one row.
+// 4.3 us for those 22 MB of reads and writes (5.1 TB/s), 1.4 us for one row.
 template <int W>
 __global__ void __launch_bounds__(128) k_conv_step(ConvStepParams p) {
   wait_for_previous();
@@ -234,39 +234,43 @@ __global__ void __launch_bounds__(256) k_delta_step(DeltaStepParams p) {
 
 // ------------------------------------------------------------------ selective scan
 
-// LPC lanes per channel, eight states each. A block walks its channels over several batch rows: A, D and the bias are read
-// once, a row's loads are in flight while the one before it is computed, and its slot is known a row earlier still. VEC: the
-// states, A, B and C in 16- and 8-byte pieces (N a multiple of 4 and everything aligned). 120 of 160 rows x 4096 channels x 16
-// states: 14.9 us for 59 MB (4.0 TB/s). The states (42 MB) come from L2, whose latency bounds it: 80 registers leave six
-// blocks of four warps an SM, each thread with one row in flight and one in hand.
-template <bool VEC>
+// Two lanes per channel, whose quads of states take turns: a load or store instruction of a warp covers whole sectors. A block
+// walks its channels over several batch rows: A, D and the bias are read once, a row's loads are in flight while the one
+// before it is computed, and its slot is known a row earlier still. VEC: the states, A, B and C in 16- and 8-byte pieces (N a
+// multiple of 4 and everything aligned). 120 of 160 rows x 4096 channels x 16
+// states: 12.4 us for 59 MB (4.7 TB/s). The states (42 MB) come from L2, whose latency bounds it: 80 registers leave six blocks
+// of four warps an SM, each thread with one row in flight and one in hand. (Eight consecutive states a lane, and a grid of
+// more blocks than fit: 14.9 us.)
+template <int NQ, bool VEC>
 struct SscanRow {
   int slot;
-  float h[8];
-  uint2 B[2], C[2];
+  float h[NQ][4];
+  uint2 B[NQ], C[NQ];
   uint16_t u, dt, z;
 
-  __device__ __forceinline__ void load(const SscanStepParams& p, int b, int slot_, int d, int n0, int ns, int bc) {
+  // half: the lane's turn; bc: the group's place in a row of B and C
+  __device__ __forceinline__ void load(const SscanStepParams& p, int b, int slot_, int d, int half, int bc) {
     slot = slot_;
     if (slot < 0) return;
-    const float* hp = p.state + ((size_t)slot * p.D + d) * p.N + n0;
+    const float* hp = p.state + ((size_t)slot * p.D + d) * p.N;
     const __nv_bfloat16 *bp = p.Bm + (size_t)b * p.b_s + bc, *cp = p.Cm + (size_t)b * p.c_s + bc;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < NQ; ++j) {
+      const int n0 = (2 * j + half) * 4;
       if (VEC) {
-        const bool in = 4 * j < ns;
-        const float4 q = in ? *reinterpret_cast<const float4*>(hp + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
-        h[4 * j] = q.x, h[4 * j + 1] = q.y, h[4 * j + 2] = q.z, h[4 * j + 3] = q.w;
-        B[j] = in ? __ldg(reinterpret_cast<const uint2*>(bp) + j) : make_uint2(0, 0);
-        C[j] = in ? __ldg(reinterpret_cast<const uint2*>(cp) + j) : make_uint2(0, 0);
+        const bool in = n0 < p.N;
+        const float4 q = in ? *reinterpret_cast<const float4*>(hp + n0) : make_float4(0.f, 0.f, 0.f, 0.f);
+        h[j][0] = q.x, h[j][1] = q.y, h[j][2] = q.z, h[j][3] = q.w;
+        B[j] = in ? __ldg(reinterpret_cast<const uint2*>(bp + n0)) : make_uint2(0, 0);
+        C[j] = in ? __ldg(reinterpret_cast<const uint2*>(cp + n0)) : make_uint2(0, 0);
       } else {
         uint32_t v[2][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int n = 4 * j + e;
-          h[n] = n < ns ? hp[n] : 0.f;
-          v[0][e] = n < ns ? __ldg(reinterpret_cast<const uint16_t*>(bp) + n) : 0;
-          v[1][e] = n < ns ? __ldg(reinterpret_cast<const uint16_t*>(cp) + n) : 0;
+          const int n = n0 + e;
+          h[j][e] = n < p.N ? hp[n] : 0.f;
+          v[0][e] = n < p.N ? __ldg(reinterpret_cast<const uint16_t*>(bp) + n) : 0;
+          v[1][e] = n < p.N ? __ldg(reinterpret_cast<const uint16_t*>(cp) + n) : 0;
         }
         B[j] = make_uint2(v[0][0] | v[0][1] << 16, v[0][2] | v[0][3] << 16);
         C[j] = make_uint2(v[1][0] | v[1][1] << 16, v[1][2] | v[1][3] << 16);
@@ -278,60 +282,67 @@ struct SscanRow {
   }
 };
 
-template <int LPC, bool VEC>
+template <int NQ, bool VEC>
 __global__ void __launch_bounds__(128) k_sscan_step(SscanStepParams p) {
   wait_for_previous();
-  const int i = blockIdx.x * 128 + threadIdx.x, d = i / LPC, n0 = (i % LPC) * 8;
+  const int i = blockIdx.x * 128 + threadIdx.x, d = i >> 1, half = i & 1;
   const bool live = d < p.D;
-  const int dc = live ? d : p.D - 1, ns = p.N - n0;
-  float a[8];
+  const int dc = live ? d : p.D - 1;
+  float a[NQ][4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) a[e] = e < ns ? kLog2e * __ldg(p.A + (size_t)dc * p.N + n0 + e) : 0.f;
-  const float bias = p.bias ? __ldg(p.bias + dc) : 0.f, skip = p.Dskip && n0 == 0 ? __ldg(p.Dskip + dc) : 0.f;
-  const int bc = (dc / p.Dg) * p.N + n0, stride = gridDim.y;
+  for (int j = 0; j < NQ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = (2 * j + half) * 4 + e;
+      a[j][e] = n < p.N ? kLog2e * __ldg(p.A + (size_t)dc * p.N + n) : 0.f;
+    }
+  const float bias = p.bias ? __ldg(p.bias + dc) : 0.f, skip = p.Dskip && half == 0 ? __ldg(p.Dskip + dc) : 0.f;
+  const int bc = (dc / p.Dg) * p.N, stride = gridDim.y;
   auto slot_at = [&](int b) { return b < p.B ? slot_of(p.index, b, p.slots, p.status) : -1; };
-  auto compute = [&](SscanRow<VEC>& row, int b) {
+  auto compute = [&](SscanRow<NQ, VEC>& row, int b) {
     float y = 0.f;
     if (row.slot >= 0) {
       const float u = bf16_lo(row.u), x = bf16_lo(row.dt) + bias, z = bf16_lo(row.z);
       const float dt = p.softplus ? softplus(x) : x, dtu = dt * u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint2 bq = row.B[e / 4], cq = row.C[e / 4];
-        const uint32_t bw = e & 2 ? bq.y : bq.x, cw = e & 2 ? cq.y : cq.x;
-        row.h[e] = fmaf(decay(dt, a[e]), row.h[e], dtu * (e & 1 ? bf16_hi(bw) : bf16_lo(bw)));
-        y = fmaf(row.h[e], e & 1 ? bf16_hi(cw) : bf16_lo(cw), y);
-      }
+      for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t bw = e & 2 ? row.B[j].y : row.B[j].x, cw = e & 2 ? row.C[j].y : row.C[j].x;
+          row.h[j][e] = fmaf(decay(dt, a[j][e]), row.h[j][e], dtu * (e & 1 ? bf16_hi(bw) : bf16_lo(bw)));
+          y = fmaf(row.h[j][e], e & 1 ? bf16_hi(cw) : bf16_lo(cw), y);
+        }
       y = fmaf(skip, u, y);
       if (live) {
-        float* hp = p.state + ((size_t)row.slot * p.D + d) * p.N + n0;
+        float* hp = p.state + ((size_t)row.slot * p.D + d) * p.N;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < NQ; ++j) {
+          const int n0 = (2 * j + half) * 4;
           if (VEC) {
-            if (4 * j < ns) reinterpret_cast<float4*>(hp)[j] = make_float4(row.h[4 * j], row.h[4 * j + 1], row.h[4 * j + 2], row.h[4 * j + 3]);
+            if (n0 < p.N) *reinterpret_cast<float4*>(hp + n0) = make_float4(row.h[j][0], row.h[j][1], row.h[j][2], row.h[j][3]);
           } else {
 #pragma unroll
-            for (int e = 4 * j; e < 4 * j + 4; ++e)
-              if (e < ns) hp[e] = row.h[e];
+            for (int e = 0; e < 4; ++e)
+              if (n0 + e < p.N) hp[n0 + e] = row.h[j][e];
           }
         }
       }
-      if (LPC == 2) y += __shfl_xor_sync(0xffffffffu, y, 1);
+      y += __shfl_xor_sync(0xffffffffu, y, 1);
       if (p.z) y *= z * sigmoid_fast(z);
     }
-    if (live && n0 == 0) p.y[(size_t)b * p.D + d] = __float2bfloat16_rn(y);
+    if (live && half == 0) p.y[(size_t)b * p.D + d] = __float2bfloat16_rn(y);
   };
   // two rows in turn, so that none is copied
-  SscanRow<VEC> even, odd;
+  SscanRow<NQ, VEC> even, odd;
   int b = blockIdx.y;
-  even.load(p, b, slot_at(b), dc, n0, ns, bc);
+  even.load(p, b, slot_at(b), dc, half, bc);
   int slot = slot_at(b + stride);
   for (; b < p.B; b += 2 * stride) {
-    odd.load(p, b + stride, slot, dc, n0, ns, bc);
+    odd.load(p, b + stride, slot, dc, half, bc);
     slot = slot_at(b + 2 * stride);
     compute(even, b);
     if (b + stride >= p.B) break;
-    even.load(p, b + 2 * stride, slot, dc, n0, ns, bc);
+    even.load(p, b + 2 * stride, slot, dc, half, bc);
     slot = slot_at(b + 3 * stride);
     compute(odd, b + stride);
   }
@@ -341,8 +352,8 @@ __global__ void __launch_bounds__(128) k_sscan_step(SscanStepParams p) {
 
 cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t s) {
   const int bx = (p.C / 4 + 127) / 128;
-  // up to eight CTAs of four warps per SM; beyond that a block walks several rows on one load of its weights
-  const int by = std::max(1, std::min(p.B, (p.sms * 8 + bx - 1) / bx));
+  // up to eight CTAs of four warps per SM, all resident; beyond that a block walks several rows on one load of its weights
+  const int by = std::max(1, std::min(p.B, p.sms * 8 / bx));
   const dim3 grid(bx, std::min(by, 65535));
   switch (p.W) {
     case 1: return launch_after(k_conv_step<1>, grid, 128, 0, s, p);
@@ -367,10 +378,10 @@ cudaError_t launch_delta_step(const DeltaStepParams& p, cudaStream_t s) {
 
 template <bool VEC>
 static cudaError_t run_sscan_step(const SscanStepParams& p, cudaStream_t s) {
-  const int lpc = p.N <= 8 ? 1 : 2, bx = (p.D * lpc + 127) / 128;
-  // up to eight CTAs of four warps per SM; beyond that a block walks several rows
-  const dim3 grid(bx, std::max(1, std::min(p.B, std::min(65535, (p.sms * 8 + bx - 1) / bx))));
-  return lpc == 1 ? launch_after(k_sscan_step<1, VEC>, grid, 128, 0, s, p) : launch_after(k_sscan_step<2, VEC>, grid, 128, 0, s, p);
+  const int bx = (2 * p.D + 127) / 128, resident = p.sms * (p.N <= 8 ? 8 : 6);
+  // No more blocks than are resident, but several rows a block: 14 of them for the 120 rows above 12.5 us, 15 (a second wave) 16.6, 10 15.0.
+  const dim3 grid(bx, std::max(1, std::min(p.B, std::min(65535, resident / bx))));
+  return p.N <= 8 ? launch_after(k_sscan_step<1, VEC>, grid, 128, 0, s, p) : launch_after(k_sscan_step<2, VEC>, grid, 128, 0, s, p);
 }
 
 cudaError_t launch_sscan_step(const SscanStepParams& p, cudaStream_t s) { return p.vec ? run_sscan_step<true>(p, s) : run_sscan_step<false>(p, s); }
