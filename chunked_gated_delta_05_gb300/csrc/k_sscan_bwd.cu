@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kSscanThreads, 7) k_sscan_rmap(SscanParams p, 
     const int len = min(kRt, sg.len - tb);
     // as in the forward: tokens in groups, no branch in a token's work; past the segment's end dt and dy are 0
 #pragma unroll 1
-    for (int t0 = kRt - kRGroup; t0 >= 0; t0 -= kRGroup) {
+    for (int t0 = (len - 1) / kRGroup * kRGroup; t0 >= 0; t0 -= kRGroup) {
       float dt[kRGroup][2], dy0[kRGroup][2];
 #pragma unroll
       for (int i = 0; i < kRGroup; ++i) {

@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(kSscanThreads, 8) k_sscan_pass(SscanParams p, 
     // states. No branch in a token's work: past the segment's end dt = 0, which leaves the state as it is, and without
     // softplus or gate their results are not selected.
 #pragma unroll 1
-    for (int t0 = 0; t0 < kTt; t0 += kGroup) {
-      if (!MAP && p.ck && t0 % kSscanBlock == 0 && t0 < len)
+    for (int t0 = 0; t0 < len; t0 += kGroup) {
+      if (!MAP && p.ck && t0 % kSscanBlock == 0)
         store_rows<NP>(h, p.ck + (size_t)(sg.ck0 + (tb + t0) / kSscanBlock) * p.N * p.D, p, ch);
       float dt[kGroup][2], dtu[kGroup][2];
       F2 y[kGroup];
