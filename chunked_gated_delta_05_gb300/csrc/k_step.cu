@@ -350,11 +350,23 @@ __global__ void __launch_bounds__(128) k_sscan_step(SscanStepParams p) {
 
 }  // namespace
 
+// How many blocks share the B rows of a step, where bx blocks cover a row and `resident` run at once: whole rounds of resident
+// blocks, several rows a block. Of one to four rounds the one with the fewest rows in turn, a round's start counted as
+// one. (120 rows of the scan step, bx = 64, resident = 912: 14 blocks 12.5 us; 15, a second round for a few, 16.6; 10 15.0.)
+static int row_blocks(int B, int bx, int resident) {
+  int best = 1;
+  long long least = -1;
+  for (int r = 1; r <= 4; ++r) {
+    const int by = std::min({B, 65535, std::max(1, int((long long)r * resident / bx))});
+    const long long rounds = ((long long)bx * by + resident - 1) / resident, cost = rounds * ((B + by - 1) / by + 1);
+    if (least < 0 || cost < least) least = cost, best = by;
+  }
+  return best;
+}
+
 cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t s) {
   const int bx = (p.C / 4 + 127) / 128;
-  // up to eight CTAs of four warps per SM, all resident; beyond that a block walks several rows on one load of its weights
-  const int by = std::max(1, std::min(p.B, p.sms * 8 / bx));
-  const dim3 grid(bx, std::min(by, 65535));
+  const dim3 grid(bx, row_blocks(p.B, bx, p.sms * 8));
   switch (p.W) {
     case 1: return launch_after(k_conv_step<1>, grid, 128, 0, s, p);
     case 2: return launch_after(k_conv_step<2>, grid, 128, 0, s, p);
@@ -378,9 +390,8 @@ cudaError_t launch_delta_step(const DeltaStepParams& p, cudaStream_t s) {
 
 template <bool VEC>
 static cudaError_t run_sscan_step(const SscanStepParams& p, cudaStream_t s) {
-  const int bx = (2 * p.D + 127) / 128, resident = p.sms * (p.N <= 8 ? 8 : 6);
-  // No more blocks than are resident, but several rows a block: 14 of them for the 120 rows above 12.5 us, 15 (a second wave) 16.6, 10 15.0.
-  const dim3 grid(bx, std::max(1, std::min(p.B, std::min(65535, resident / bx))));
+  const int bx = (2 * p.D + 127) / 128;
+  const dim3 grid(bx, row_blocks(p.B, bx, p.sms * (p.N <= 8 ? 8 : 6)));
   return p.N <= 8 ? launch_after(k_sscan_step<1, VEC>, grid, 128, 0, s, p) : launch_after(k_sscan_step<2, VEC>, grid, 128, 0, s, p);
 }
 
