@@ -9,12 +9,15 @@
 // fewer costs another forward walk, which this kernel, bound by its instructions at 15% of HBM's rate, cannot hide as it
 // does the reads. The adjoint chain is cut into segments like the forward's. The sums over channels in dB and dC begin as
 // matrix products with ones: a lane's four states are its share of the A operand of m16n8k8, whose products add up four
-// lanes' channels (tf32 operands; the results are bf16), and three exchanges add up the groups of lanes. All other sums are fp32.
+// lanes' channels (each term as two tf32 operands, 22 bits of it), and three exchanges add up the groups of lanes. All sums are
+// fp32; dB and dC are rounded to bf16 once.
 //
-// On GB300, 4093 tokens in 7 documents x 2048 channels x 16 states: 205 us (adjoint maps 38, composition 8, this walk
-// 160, last sums 8 warm); 168 registers leave three warps a scheduler, which issue 55% of the time. Exchanges between the two
-// lanes in place of their sums' trip through shared memory: 212 -> 226 us for the backward. Adding up the lane groups at the
-// tile's end in place of the exchanges: 212 -> 222 us.
+// On GB300, 4093 tokens in 7 documents x 2048 channels x 16 states: 241 us (adjoint maps 37, composition 8, this walk
+// 190, last sums 8 warm), of which the second operand of every term takes 29 (14% of the backward; without it dB and dC shrink by
+// 3.5e-4, and by 5% of their value where channels cancel to 1%). 168 registers leave three warps a scheduler. Tried before that
+// operand, when the backward took 212 us: exchanges between the two lanes in place of their sums' trip through shared memory, 226;
+// adding up the lane groups at the tile's end in place of the exchanges, 222. The rest of the terms as bf16, two to a register
+// (six products a token in place of eight): 241 as well; selectors of their own for dC and dB: 256.
 #include <atomic>
 
 #include "k_sscan.cuh"
@@ -147,6 +150,9 @@ __device__ __forceinline__ void mma_tf32(float* d, float a0, float a1, float a2,
         "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
+// The upper 11 significant bits of x, which tf32 holds exactly: the operands above are to be tf32 values.
+__device__ __forceinline__ float tf32_part(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
+
 // One value for two lanes: the lane with `up` keeps b, the other a, each plus the other lane's.
 __device__ __forceinline__ float exchange(float a, float b, bool up, int mask) {
   return (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, mask);
@@ -216,14 +222,12 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = lane >> 4, part = tid & (kBwdChans - 1);
   const int c = warp * 16 + (lane & 15), d = ch.d0 + min(c, ch.chans - 1), n0 = half * SP, ns = p.N - n0;
   const bool gate = p.z != nullptr, softplus_on = p.softplus, live = c < ch.chans, low = tid < kBwdChans;
-  // The products below put quad j of dC (dB) into columns 2 j and 2 j + 1 (4 + 2 j and 4 + 2 j + 1).
-  float sel[2 * NQ][2];
+  // The products below put quad j into columns 2 j and 2 j + 1, and once more into 4 + 2 j and 5 + 2 j.
+  float sel[NQ][2];
 #pragma unroll
   for (int j = 0; j < NQ; ++j)
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) sel[w * NQ + j][e] = (lane >> 2) == w * 4 + 2 * j + e ? 1.f : 0.f;
+    for (int e = 0; e < 2; ++e) sel[j][e] = (lane >> 2 & 3) == 2 * j + e ? 1.f : 0.f;
   F2 A2[PR], g[PR], dA[PR];
   load_states<SP>(A2, p.A + (size_t)d * p.N + n0, 1, ns);
 #pragma unroll
@@ -320,25 +324,39 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
     for (int t = kTile - 1; t >= 0; --t) {
       const float4 q = sm.tok[t][c];
       const F2 dt2 = dup2(q.x), dtu2 = dup2(q.y), dy2 = dup2(q.z);
-      F2 v[PR], w[2][PR];
+      F2 v[PR];
       sm.C[buf].template pairs<PR>(v, t, n0);
       F2 y2 = f2(0.f, 0.f), sB = f2(0.f, 0.f), sA = f2(0.f, 0.f);
+      // Sums over the four channels of each four lanes: a lane's quad of states is its share of A, ones in B pick columns. A term
+      // goes in as its upper 11 bits and the 11 bits after those (the rest of it is below 2^-21 of it), so the sums are as good as
+      // fp32's; the upper part alone would take 2^-11 off every term. dC and dB have accumulators of their own: fewer selectors,
+      // and what is not finite in one does not reach the other. (Within one, a term that is infinite or NaN makes NaN of the token's
+      // sums over all states.)
+      float acc[2][4] = {};
 #pragma unroll
-      for (int s = 0; s < PR; ++s) {
-        y2 = fma2(H[t][s], v[s], y2);
-        g[s] = fma2(v[s], dy2, g[s]);
-        w[0][s] = mul2(H[t][s], dy2);
-        w[1][s] = mul2(g[s], dtu2);
-      }
-      // Sums over the four channels of each four lanes: a lane's quad of states is its share of A, ones in B pick columns.
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < NQ; ++j) {
+        F2 w[2][2];
 #pragma unroll
-      for (int j = 0; j < 2 * NQ; ++j) {
-        const F2* q4 = &w[j / NQ][2 * (j % NQ)];
-        float a0, a1, a2, a3;
-        unf2(q4[0], &a0, &a1);
-        unf2(q4[1], &a2, &a3);
-        mma_tf32(acc, a0, a1, a2, a3, sel[j][0], sel[j][1], acc);
+        for (int i = 0; i < 2; ++i) {
+          const int s = 2 * j + i;
+          y2 = fma2(H[t][s], v[s], y2);
+          g[s] = fma2(v[s], dy2, g[s]);
+          w[0][i] = mul2(H[t][s], dy2);
+          w[1][i] = mul2(g[s], dtu2);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float high[4], low[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            unf2(w[k][i], &high[2 * i], &high[2 * i + 1]);
+            high[2 * i] = tf32_part(high[2 * i]), high[2 * i + 1] = tf32_part(high[2 * i + 1]);
+            unf2(fma2(f2(high[2 * i], high[2 * i + 1]), dup2(-1.f), w[k][i]), &low[2 * i], &low[2 * i + 1]);
+            low[2 * i] = tf32_part(low[2 * i]), low[2 * i + 1] = tf32_part(low[2 * i + 1]);
+          }
+          mma_tf32(acc[k], high[0], high[1], high[2], high[3], sel[j][0], sel[j][1], acc[k]);
+          mma_tf32(acc[k], low[0], low[1], low[2], low[3], sel[j][0], sel[j][1], acc[k]);
+        }
       }
       sm.B[buf].template pairs<PR>(v, t, n0);
 #pragma unroll
@@ -350,10 +368,13 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_sscan_bwd(SscanParams p, int
         dA[s] = fma2(x, dt2, dA[s]);
       }
       sm.sums[half][t][c] = make_float4(sum2(y2), sum2(sB), sum2(sA), 0.f);
-      // Lane 4 r + i now holds quad i % 2 of dC (i < 2) or dB, states 0, 2, 1, 3 in acc[0 .. 3], of the four lanes r: added up
-      // over the half's four r, each lane ends with one.
-      const bool r0 = lane & 4, r1 = lane & 8;
-      const float k0 = exchange(acc[0], acc[1], r0, 4), k1 = exchange(acc[2], acc[3], r0, 4), r = exchange(k0, k1, r1, 8);
+      // Lane 4 r + i now holds quad i % 2 of both, of the four lanes r; it goes on with dC's (i < 2) or dB's states 0, 2, 1, 3 in
+      // k[0 .. 3]: added up over the half's four r, each lane ends with one.
+      const bool is_dB = lane & 2, r0 = lane & 4, r1 = lane & 8;
+      float k[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = is_dB ? acc[1][e] : acc[0][e];
+      const float k0 = exchange(k[0], k[1], r0, 4), k1 = exchange(k[2], k[3], r0, 4), r = exchange(k0, k1, r1, 8);
       if ((lane & 1) < NQ) sm.red[warp][t][(lane >> 1) & 1][n0 + (lane & 1) * 4 + (r0 ? 2 : 0) + (r1 ? 1 : 0)] = r;
     }
     __syncwarp();
