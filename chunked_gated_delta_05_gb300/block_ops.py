@@ -69,21 +69,19 @@ def _rows_of(name, t, dtype, shape, dev, inner, width):
         if shape[i] != 1 and st[i] != w:
             raise ValueError(f"{name}'s rows must be contiguous")
         w *= shape[i]
-    row = 0
+    row = None
     for i in range(lead - 1, -1, -1):       # from the innermost leading dimension of more than one row
         if shape[i] == 1:
             continue
-        if row == 0:
+        if row is None:
             row, n = st[i], shape[i]
+            if row < w:
+                raise ValueError(f"{name}'s rows must not overlap (an expanded tensor must be made contiguous)")
         elif st[i] != n * row:
             raise ValueError(f"{name}'s rows must follow each other at one stride")
         else:
             n *= shape[i]
-    if row == 0:
-        return w
-    if row < w:
-        raise ValueError(f"{name}'s rows must not overlap")
-    return row
+    return w if row is None else row
 
 
 def _like(t):
