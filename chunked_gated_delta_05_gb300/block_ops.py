@@ -9,7 +9,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from .ops import K_DIM, _check_tensor, _conv_checks, _conv_desc, _gate_checks, _offsets
+from .ops import K_DIM, _check_tensor, _conv_checks, _conv_desc, _gate_checks, _launch, _offsets
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _ACTIVATIONS = {"silu": 1, "sigmoid": 2}
@@ -25,13 +25,6 @@ def _p(t):
     return 0 if t is None else t.data_ptr()
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream(dev):
-    return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
-
-
 _norm_desc = _lib.packer(_lib.NormDesc)
 _norm_fwd_args, _norm_bwd_args = _lib.packer(_lib.NormFwdArgs), _lib.packer(_lib.NormBwdArgs)
 _conv_step_desc, _conv_step_args = _lib.packer(_lib.ConvStepDesc), _lib.packer(_lib.ConvStepArgs)
@@ -40,9 +33,7 @@ _scan_desc, _scan_step_args = _lib.packer(_lib.SscanDesc), _lib.packer(_lib.Ssca
 
 
 def _run(name, desc, args, dev):
-    rc = _lib.entry(name)(desc, args, _stream(dev))
-    if rc:
-        _lib.check(rc)
+    _launch(_lib.entry(name), desc, args, dev)
 
 
 def _device(name, t):
@@ -256,7 +247,7 @@ def causal_conv1d_state(x, weight, *, dilation=1, cu_seqlens: Optional[Sequence[
         return state
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
     a = _lib.ConvFwdArgs(x=x.data_ptr(), halo=_p(halo), y=state.data_ptr(), workspace=ws.data_ptr(), workspace_bytes=ws_bytes)
-    _lib.check(lib.gdn_conv_state(desc, a, _stream(dev)))
+    _launch(lib.gdn_conv_state, desc, a, dev)
     return state
 
 

@@ -18,6 +18,25 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(dev):
+    return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _launch(fn, desc, args, dev):
+    """Calls the entry point ``fn`` on the current stream of the tensors' device (its index), as the current device: the library
+    launches there, whatever the stream's handle."""
+    if torch.cuda.current_device() == dev:
+        rc = fn(desc, args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(desc, args, _stream(dev))
+    if rc:
+        _lib.check(rc)
+
+
 def _check_tensor(name, t, dtype, shape, device):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
@@ -129,9 +148,8 @@ def _fwd(per_channel, q, k, v, g, beta, initial_state, output_final_state, use_q
                      workspace=None if save else _ptr(buf), workspace_bytes=0 if save else ws_bytes,
                      status=_ptr(status), saved=_ptr(buf) if save else None, saved_bytes=ws_bytes if save else 0,
                      A_log=_ptr(A_log), dt_bias=_ptr(dt_bias))
-    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
     fn = lib.kda_fwd if per_channel else lib.gdn_fwd
-    _lib.check(fn(ctypes.byref(desc), ctypes.byref(a), stream))
+    _launch(fn, ctypes.byref(desc), ctypes.byref(a), dev.index)
     if save:
         return o, final, buf
     return o, final
@@ -176,9 +194,8 @@ def _bwd(per_channel, q, k, v, g, beta, dO, dht, initial_state, use_qk_l2norm, u
                      workspace=_ptr(ws), workspace_bytes=ws_bytes, status=_ptr(status),
                      saved=_ptr(saved), saved_bytes=saved_bytes, A_log=_ptr(A_log), dt_bias=_ptr(dt_bias),
                      dA_log=_ptr(dA_log), ddt_bias=_ptr(ddt_bias))
-    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
     fn = lib.kda_bwd if per_channel else lib.gdn_bwd
-    _lib.check(fn(ctypes.byref(desc), ctypes.byref(a), stream))
+    _launch(fn, ctypes.byref(desc), ctypes.byref(a), dev.index)
     if gate is not None:
         return dq, dk, dv, dbeta, dg, dh0, dA_log, ddt_bias
     return dq, dk, dv, dbeta, dg, dh0
@@ -333,8 +350,7 @@ def causal_conv1d_fwd(x, weight, bias=None, *, dilation=1, activation=True, cu_s
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     a = _lib.ConvFwdArgs(x=_ptr(x), weight=_ptr(weight), bias=_ptr(bias), halo=_ptr(halo), y=_ptr(y),
                          workspace=_ptr(ws), workspace_bytes=ws_bytes)
-    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-    _lib.check(lib.gdn_conv_fwd(ctypes.byref(desc), ctypes.byref(a), stream))
+    _launch(lib.gdn_conv_fwd, ctypes.byref(desc), ctypes.byref(a), dev.index)
     return y
 
 
@@ -359,8 +375,7 @@ def causal_conv1d_bwd(x, weight, bias, dy, *, dilation=1, activation=True, cu_se
     a = _lib.ConvBwdArgs(x=_ptr(x), weight=_ptr(weight), bias=_ptr(bias), halo=_ptr(halo), dy=_ptr(dy),
                          dx=_ptr(dx), dweight=_ptr(dw), dbias=_ptr(db), dhalo=_ptr(dh), workspace=_ptr(ws),
                          workspace_bytes=ws_bytes)
-    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-    _lib.check(lib.gdn_conv_bwd(ctypes.byref(desc), ctypes.byref(a), stream))
+    _launch(lib.gdn_conv_bwd, ctypes.byref(desc), ctypes.byref(a), dev.index)
     return dx, dw, db, dh
 
 
