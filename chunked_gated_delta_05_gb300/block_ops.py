@@ -7,6 +7,7 @@ import ctypes
 from typing import Optional, Sequence
 
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 from . import _lib
 from .ops import K_DIM, _check_tensor, _conv_checks, _conv_desc, _gate_checks, _launch, _offsets
@@ -451,10 +452,18 @@ class SelectiveScan(torch.autograd.Function):
         return du, ddelta, dA, dB, dC, dD, dz, dbias, dh0, None, None, None
 
 
+def _differentiated(tensors):
+    """Whether one of the tensors asks for gradients or carries a forward-mode tangent (which the autograd function refuses)."""
+    tensors = [t for t in tensors if t is not None]
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        return True
+    return getattr(forward_ad, "_current_level", 0) >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def selective_scan(u, delta, A, B, C, *, D=None, z=None, delta_bias=None, delta_softplus=True, initial_state=None,
                    output_final_state=False, cu_seqlens=None):
-    """Differentiable selective scan (see :func:`selective_scan_fwd`): ``(y, final_state or None)``."""
-    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (u, delta, A, B, C, D, z, delta_bias, initial_state))):
+    """Differentiable selective scan (see :func:`selective_scan_fwd`): ``(y, final_state or None)``. Reverse mode only."""
+    if not _differentiated((u, delta, A, B, C, D, z, delta_bias, initial_state)):
         return selective_scan_fwd(u, delta, A, B, C, D=D, z=z, delta_bias=delta_bias, delta_softplus=delta_softplus,
                                   initial_state=initial_state, output_final_state=output_final_state, cu_seqlens=cu_seqlens)
     return SelectiveScan.apply(u, delta, A, B, C, D, z, delta_bias, initial_state, delta_softplus, output_final_state, cu_seqlens)
