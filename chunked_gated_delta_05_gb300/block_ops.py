@@ -231,6 +231,12 @@ def gated_rms_norm(x, gate, weight, *, eps=1e-6, activation="silu"):
 
 # ---------------------------------------------------------------- single-token steps
 
+def _changed(state):
+    """Tells autograd that a kernel wrote to the state, so that a backward that had saved it raises."""
+    if not state.is_inference():
+        torch.autograd.graph.increment_version(state)
+
+
 def causal_conv1d_state(x, weight, *, dilation=1, cu_seqlens: Optional[Sequence[int]] = None, halo=None):
     """The state that a prompt ``x [B,T,C]`` leaves for :func:`causal_conv1d_step`: the last ``(W-1)*dilation`` inputs of
     every sequence (from its halo, or zeros, where it is shorter), bf16 ``[N,(W-1)*dilation,C]``."""
@@ -256,8 +262,8 @@ def causal_conv1d_step(state, x, weight, bias=None, *, dilation=1, activation=Tr
     """One token of the short convolution: ``x [B,C]`` (bf16, rows may be strided) against ``state
     [slots,(W-1)*dilation,C]``, which is updated in place. ``state_indices`` (int32 [B] on the device) names each row's slot;
     a negative one marks a padding row (zero output, no state touched), and no slot may be named twice. A row whose slot lies
-    outside the state is treated as padding and recorded as GDN_ERANGE in ``status`` (int32 [1] on the device). Returns
-    ``y [B,C]``."""
+    outside the state is treated as padding and recorded as GDN_ERANGE in ``status`` (int32 [1] on the device). Steps have no
+    gradients; a backward that saved ``state`` before it changed raises. Returns ``y [B,C]``."""
     dev = _device("x", x)
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must be [B,C] and weight [C,W]")
@@ -276,6 +282,7 @@ def causal_conv1d_step(state, x, weight, bias=None, *, dilation=1, activation=Tr
     y = _like(x)
     _run("gdn_conv_step", _conv_step_desc(B, C, W, dilation, 1 if activation else 0, slots, xs),
          _conv_step_args(x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(), _p(state_indices), y.data_ptr(), _p(status)), dev)
+    _changed(state)
     return y
 
 
@@ -305,6 +312,7 @@ def _delta_step(per_channel, state, q, k, v, g, beta, state_indices, l2, sig, sc
          _step_desc(B, H, Hk, slots, 0.0 if scale is None else scale, 1 if l2 else 0, 1 if sig else 0,
                     0 if gate is None else 1, 0.0 if gate is None else gate[2], qs, ks, vs),
          _step_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), _p(state_indices), o.data_ptr(), _p(A_log), _p(dt_bias), _p(status)), dev)
+    _changed(state)
     return o
 
 
@@ -425,6 +433,7 @@ def selective_scan_step(state, u, delta, A, B, C, *, D=None, z=None, delta_bias=
     y = _like(u)
     _run("gdn_sscan_step", d, _scan_step_args(u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _p(D), _p(delta_bias), _p(z), state.data_ptr(),
                                               _p(state_indices), slots, y.data_ptr(), _p(status)), dev)
+    _changed(state)
     return y
 
 
