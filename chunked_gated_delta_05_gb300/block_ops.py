@@ -10,7 +10,7 @@ import torch
 import torch.autograd.forward_ad as forward_ad
 
 from . import _lib
-from .ops import K_DIM, _check_tensor, _conv_checks, _conv_desc, _gate_checks, _launch, _offsets
+from .ops import K_DIM, _check_tensor, _conv_checks, _conv_desc, _first_order, _gate_checks, _launch, _offsets
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _ACTIVATIONS = {"silu": 1, "sigmoid": 2}
@@ -192,6 +192,7 @@ class AddRmsNorm(torch.autograd.Function):
         return (y, stream) if residual is not None else y
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy, dstream=None):
         stream, weight = ctx.saved_tensors
         eps, scale, has_residual = ctx.cfg
@@ -211,6 +212,7 @@ class GatedRmsNorm(torch.autograd.Function):
         return gated_rms_norm_fwd(x, gate, weight, eps=eps, activation=activation)
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy):
         x, gate, weight = ctx.saved_tensors
         eps, activation = ctx.cfg
@@ -451,6 +453,7 @@ class SelectiveScan(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy, dfinal):
         u, delta, A, B, C, D, z, delta_bias, h0, saved = ctx.saved_tensors
         softplus, cu = ctx.cfg

@@ -4,6 +4,7 @@ There is no fallback path: without the built library or a GB300 these functions 
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence
 
 import torch
@@ -35,6 +36,36 @@ def _launch(fn, desc, args, dev):
             rc = fn(desc, args, _stream(dev))
     if rc:
         _lib.check(rc)
+
+
+class _NoSecondOrder(torch.autograd.Function):
+    """Passes gradients on, attached to a graph that refuses to be walked."""
+
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return tuple(g.detach() for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("this operator's gradients cannot be differentiated again")
+
+
+def _first_order(backward):
+    """Decorates a ``backward`` that has no derivative of its own. With ``create_graph=True`` its gradients are usable as values
+    and an error to differentiate. (torch's once_differentiable lets them pass for constants where the incoming gradient asks for
+    none, although they depend on the saved inputs.)"""
+
+    @functools.wraps(backward)
+    def wrapped(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        real = [g for g in out if g is not None]
+        attached = iter(_NoSecondOrder.apply(torch.zeros((), requires_grad=True), *real))
+        return tuple(None if g is None else next(attached) for g in out)
+
+    return wrapped
 
 
 def _check_tensor(name, t, dtype, shape, device):
@@ -277,6 +308,7 @@ class ChunkGatedDeltaRule(torch.autograd.Function):
         return o, final
 
     @staticmethod
+    @_first_order
     def backward(ctx, dO, dfinal):
         q, k, v, g, beta, h0, A_log, dt_bias, saved = ctx.saved_tensors
         per_channel, l2, sig, cu, scale, lower_bound = ctx.cfg
@@ -390,6 +422,7 @@ class CausalConv1d(torch.autograd.Function):
                                  cu_seqlens=cu_seqlens, halo=halo)
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy):
         x, weight, bias, halo = ctx.saved_tensors
         dilation, activation, cu = ctx.cfg

@@ -4,7 +4,7 @@ import torch
 import torch.autograd.forward_ad as fwad
 
 import chunked_gated_delta_05_gb300 as lib
-from chunked_gated_delta_05_gb300 import block_ops
+from chunked_gated_delta_05_gb300 import block_ops, ops
 
 
 @pytest.fixture
@@ -127,3 +127,50 @@ def test_a_step_on_a_saved_halo_is_noticed():
     lib.causal_conv1d_step(state, x[:, 0].contiguous(), w.detach())
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+def ones(*shape, dtype=torch.float32):
+    return torch.ones(*shape, dtype=dtype)
+
+
+@pytest.mark.parametrize("name", ["add_rms_norm", "add_rms_norm alone", "gated_rms_norm", "selective_scan", "gdn", "causal_conv1d"])
+def test_second_derivatives_are_refused(monkeypatch, name):
+    """A gradient taken with create_graph=True has no derivative of its own: it must not pass for a constant."""
+    bf = torch.bfloat16
+    monkeypatch.setattr(block_ops, "add_rms_norm_fwd", lambda x, r, w, **kw: (x * 2, x if r is None else r + x))
+    monkeypatch.setattr(block_ops, "add_rms_norm_bwd", lambda dy, ds, s, w, **kw: (dy * 2, None if not kw["has_residual"] else dy.to(s.dtype), torch.zeros_like(w)))
+    monkeypatch.setattr(block_ops, "gated_rms_norm_fwd", lambda x, g, w, **kw: x * 2)
+    monkeypatch.setattr(block_ops, "gated_rms_norm_bwd", lambda x, g, w, dy, **kw: (dy * 2, dy * 2, torch.zeros_like(w)))
+    monkeypatch.setattr(block_ops, "selective_scan_fwd", lambda u, *a, **kw: (u * 2, None, torch.zeros(1)))
+    monkeypatch.setattr(block_ops, "selective_scan_bwd", lambda u, delta, A, B, C, dy, **kw: (dy * 2, dy * 2, torch.zeros_like(A), torch.zeros_like(B), torch.zeros_like(C),
+                                                                                               None, None, None, None))
+    monkeypatch.setattr(ops, "_fwd", lambda kda, q, k, v, *a, **kw: (v * 2, None, torch.zeros(1)))
+    monkeypatch.setattr(ops, "_bwd", lambda kda, q, k, v, g, beta, dO, *a: tuple(t * 2 for t in (q, k, v, beta, g)) + (None,))
+    monkeypatch.setattr(ops, "causal_conv1d_fwd", lambda x, w, *a, **kw: x * 2)
+    monkeypatch.setattr(ops, "causal_conv1d_bwd", lambda x, w, b, dy, **kw: (dy * 2, torch.zeros_like(w), None, None))
+    x = ones(1, 4, 8, dtype=bf).requires_grad_()
+    q = ones(1, 4, 1, 128, dtype=bf).requires_grad_()
+    leaf, y = {
+        "add_rms_norm": lambda: (x, lib.add_rms_norm(x, ones(1, 4, 8), ones(8))[0]),
+        "add_rms_norm alone": lambda: (x, lib.add_rms_norm(x, None, ones(8))[0]),
+        "gated_rms_norm": lambda: (x, lib.gated_rms_norm(x, ones(1, 4, 8, dtype=bf), ones(8))),
+        "selective_scan": lambda: (x, lib.selective_scan(x, ones(1, 4, 8, dtype=bf), ones(8, 2), ones(1, 4, 1, 2), ones(1, 4, 1, 2))[0]),
+        "gdn": lambda: (q, lib.chunk_gated_delta_rule(q, q.detach(), q.detach(), ones(1, 4, 1), ones(1, 4, 1, dtype=bf))[0]),
+        "causal_conv1d": lambda: (x, lib.causal_conv1d(x, ones(8, 4))),
+    }[name]()
+    for loss in (y.float().sum(), (y.float() ** 2).sum()):     # the incoming gradient depends on nothing, or on the leaf
+        grad, = torch.autograd.grad(loss, leaf, create_graph=True)
+        with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+            (grad.float() * leaf.float()).sum().backward(retain_graph=True)
+
+
+@pytest.mark.gpu
+def test_first_derivatives_with_create_graph():
+    """They are the same with create_graph=True, and used alone they still give an error, not zeros."""
+    x, w = torch.randn(4, 64, device="cuda").bfloat16().requires_grad_(), torch.ones(64, device="cuda")
+    y = lib.gated_rms_norm(x, x.detach(), w)
+    plain, = torch.autograd.grad(y.float().sum(), x, retain_graph=True)
+    graph, = torch.autograd.grad(y.float().sum(), x, create_graph=True)
+    assert torch.equal(plain, graph.detach())
+    with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+        graph.float().sum().backward()
