@@ -407,7 +407,7 @@ def selective_scan_bwd(u, delta, A, B, C, dy, *, D=None, z=None, delta_bias=None
     saved_bytes = 0
     if saved is not None:
         saved_bytes = _lib.size("gdn_sscan_saved_size", d)
-        if not isinstance(saved, torch.Tensor) or saved.get_device() != dev or saved.numel() * saved.element_size() < saved_bytes:
+        if not isinstance(saved, torch.Tensor) or saved.get_device() != dev or not saved.is_contiguous() or saved.numel() * saved.element_size() < saved_bytes:
             raise ValueError("saved must be the buffer returned by the forward with save=True")
         ws_bytes -= saved_bytes
 

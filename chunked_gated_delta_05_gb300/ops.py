@@ -205,7 +205,7 @@ def _bwd(per_channel, q, k, v, g, beta, dO, dht, initial_state, use_qk_l2norm, u
     saved_bytes = 0
     if saved is not None:
         saved_bytes = (lib.kda_saved_size if per_channel else lib.gdn_saved_size)(ctypes.byref(desc))
-        if not isinstance(saved, torch.Tensor) or saved.device != dev or saved.numel() < saved_bytes:
+        if not isinstance(saved, torch.Tensor) or saved.device != dev or not saved.is_contiguous() or saved.numel() < saved_bytes:
             raise ValueError("saved must be the buffer returned by the forward with save=True")
         ws_bytes -= saved_bytes
     dq = torch.empty_like(q)
