@@ -640,7 +640,7 @@ int gdn_sscan_step(const gdn_sscan_desc_t* d, const gdn_sscan_step_args_t* a, vo
   if (overlap(a->y, yb, a->state, sb)) return bad("y must not alias state");
   SscanStepParams p{};
   if ((rc = device_or_error(&p.sms))) return rc;
-  p.vec = P.N % 4 == 0 && aligned(a->state, 16) && aligned(a->A, 16) && aligned(a->Bm, 8) && aligned(a->Cm, 8) && P.b_s % 4 == 0 && P.c_s % 4 == 0;
+  p.vec = P.N % 4 == 0 && aligned(a->state, 16) && aligned(a->Bm, 8) && aligned(a->Cm, 8) && P.b_s % 4 == 0 && P.c_s % 4 == 0;
   p.B = P.B;
   p.D = P.D;
   p.N = P.N;

@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(256) k_delta_step(DeltaStepParams p) {
 
 // Two lanes per channel, whose quads of states take turns: a load or store instruction of a warp covers whole sectors. A block
 // walks its channels over several batch rows: A, D and the bias are read once, a row's loads are in flight while the one
-// before it is computed, and its slot is known a row earlier still. VEC: the states, A, B and C in 16- and 8-byte pieces (N a
-// multiple of 4 and everything aligned). 120 of 160 rows x 4096 channels x 16
+// before it is computed, and its slot is known a row earlier still. VEC: the states, B and C in 16- and 8-byte pieces (N a
+// multiple of 4 and these aligned; A, read once a block, comes by elements either way). 120 of 160 rows x 4096 channels x 16
 // states: 12.4 us for 59 MB (4.7 TB/s). The states (42 MB) come from L2, whose latency bounds it: 80 registers leave six blocks
 // of four warps an SM, each thread with one row in flight and one in hand. (Eight consecutive states a lane, and a grid of
 // more blocks than fit: 14.9 us.)
