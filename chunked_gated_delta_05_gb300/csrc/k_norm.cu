@@ -7,9 +7,9 @@
 // The backward kernels recompute rstd: sum r^2 and sum dy w r come out of the same pass over the row, so nothing but
 // the stream is kept by the forward.
 //
-// A row is held in registers by G threads (a power of two) of NV vectors of VEC elements each: one read and one write
-// of every tensor. All sums are fp32. Rows of widths that are no multiple of 8, or unaligned tensors, take the element
-// path (VEC = 1).
+// A row is held in registers by G threads (a power of two; in the forward of wide rows, a multiple of 32) of NV vectors of VEC
+// elements each: one read and one write of every tensor. All sums are fp32. Rows of widths that are no multiple of 8, or unaligned
+// tensors, take the element path (VEC = 1).
 //
 // Bound: HBM, a few operations a byte. On GB300: residual norm of 8192 x 2048 with an fp32 stream, forward and backward, 78.5 us
 // for 470 MB (6.0 TB/s, 88% of the copy rate: 31.3 + 47.2 us, the sums of the weight gradients included); gated norm of 262144 x
