@@ -16,6 +16,7 @@
 #include <string>
 #include <vector>
 
+#include "block_ops.cuh"
 #include "common.cuh"
 #include "gdn.h"
 
@@ -295,14 +296,14 @@ int check_cuda(cudaError_t e, const char* what) {
 
 // Optional per-kernel timing (CUDA events recorded on the launching stream around every
 // launch while enabled). Process-global and not thread-safe: a profiling aid.
-const char* const kKindNames[kKinds] = {"tables", "prepare", "chain_fwd", "chain_bwd", "bwd_feat", "bwd_tok",
+const char* const kKindNames[kKAllKinds] = {"tables", "prepare", "chain_fwd", "chain_bwd", "bwd_feat", "bwd_tok",
                                         "compose", "group_sum", "conv_fwd", "conv_bwd", "gate_grad",
                                         "norm_fwd", "norm_bwd", "conv_step", "delta_step", "sscan_fwd", "sscan_bwd",
                                         "sscan_step"};
 struct Timing {
   bool on = false;
-  std::vector<std::pair<cudaEvent_t, cudaEvent_t>> ev[kKinds];
-  size_t used[kKinds] = {};
+  std::vector<std::pair<cudaEvent_t, cudaEvent_t>> ev[kKAllKinds];
+  size_t used[kKAllKinds] = {};
 } g_tim;
 
 struct TimedLaunch {
@@ -930,16 +931,16 @@ int gdn_chain_plan(const gdn_desc_t* desc, int* chunks_per_segment, int* max_seg
 
 int gdn_timing_enable(int enable) {
   g_tim.on = enable != 0;
-  for (int k = 0; k < kKinds; ++k) g_tim.used[k] = 0;
+  for (int k = 0; k < kKAllKinds; ++k) g_tim.used[k] = 0;
   return GDN_OK;
 }
 
-int gdn_timing_kinds(void) { return kKinds; }
+int gdn_timing_kinds(void) { return kKAllKinds; }
 
-const char* gdn_timing_name(int kind) { return (kind >= 0 && kind < kKinds) ? kKindNames[kind] : ""; }
+const char* gdn_timing_name(int kind) { return (kind >= 0 && kind < kKAllKinds) ? kKindNames[kind] : ""; }
 
 int gdn_timing_read(int kind, double* total_ms, int* launches) {
-  if (kind < 0 || kind >= kKinds || !total_ms || !launches) return fail(GDN_EINVAL, "bad timing query");
+  if (kind < 0 || kind >= kKAllKinds || !total_ms || !launches) return fail(GDN_EINVAL, "bad timing query");
   double tot = 0.0;
   for (size_t i = 0; i < g_tim.used[kind]; ++i) {
     float ms = 0.f;

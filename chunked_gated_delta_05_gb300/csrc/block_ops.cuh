@@ -138,6 +138,11 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// Kernel kinds of the per-launch timing hook, after the recurrence's (names in api.cu).
+enum BlockKernelKind {
+  kKNormFwd = kKinds, kKNormBwd, kKConvStep, kKDeltaStep, kKSscanFwd, kKSscanBwd, kKSscanStep, kKAllKinds
+};
+
 // ------------------------------------------------------------------ parameter blocks
 
 // Residual add and RMS norm before a block; gated RMS norm after it (k_norm.cu). `stream` is the

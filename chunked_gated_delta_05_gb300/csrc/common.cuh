@@ -247,7 +247,7 @@ struct BwdTokParams {
 // Kernel kinds of the per-launch timing hook (names in api.cu).
 enum KernelKind {
   kKTables = 0, kKPrep, kKChainFwd, kKChainBwd, kKBwdFeat, kKBwdTok, kKCompose, kKGroupSum, kKConvFwd, kKConvBwd,
-  kKGateGrad, kKNormFwd, kKNormBwd, kKConvStep, kKDeltaStep, kKSscanFwd, kKSscanBwd, kKSscanStep, kKinds
+  kKGateGrad, kKinds
 };
 
 // Host helpers shared by the entry points of several files (api.cu).
