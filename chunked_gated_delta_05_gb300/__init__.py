@@ -1,5 +1,5 @@
 """Chunkwise gated delta rule (Gated DeltaNet and Kimi Delta Attention) on one GB300, with the operators
-around it: the short convolution, the block norms, the selective scan and the single-token steps.
+around it: the short convolution, the block norms, the selective scan, the attention blocks and the single-token steps.
 
 The computation lives in ``libgdn.so`` (hand-written sm_103a CUDA behind the C ABI of
 ``include/gdn.h``); this package builds and loads it and marshals PyTorch tensors into it.
@@ -13,6 +13,8 @@ from .block_ops import (AddRmsNorm, GatedRmsNorm, SelectiveScan, add_rms_norm, a
                         causal_conv1d_state, causal_conv1d_step, gated_rms_norm, gated_rms_norm_bwd,
                         gated_rms_norm_fwd, gdn_step, kda_step, selective_scan, selective_scan_bwd,
                         selective_scan_fwd, selective_scan_step)
+from .attention_ops import (Attention, QkNormRope, attention, attention_bwd, attention_fwd, attention_step, qk_norm_rope,
+                            qk_norm_rope_bwd, qk_norm_rope_fwd, qk_norm_rope_store)
 from ._lib import GDN_EINVAL, GDN_ERANGE, GDN_ETIMEOUT, GdnError, load as load_library
 
 __all__ = ["gdn_fwd", "gdn_bwd", "kda_fwd", "kda_bwd", "chunk_gated_delta_rule",
@@ -21,4 +23,6 @@ __all__ = ["gdn_fwd", "gdn_bwd", "kda_fwd", "kda_bwd", "chunk_gated_delta_rule",
            "add_rms_norm", "add_rms_norm_fwd", "add_rms_norm_bwd", "AddRmsNorm",
            "gated_rms_norm", "gated_rms_norm_fwd", "gated_rms_norm_bwd", "GatedRmsNorm",
            "selective_scan", "selective_scan_fwd", "selective_scan_bwd", "selective_scan_step", "SelectiveScan",
-           "causal_conv1d_state", "causal_conv1d_step", "gdn_step", "kda_step"]
+           "causal_conv1d_state", "causal_conv1d_step", "gdn_step", "kda_step",
+           "qk_norm_rope", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_store", "QkNormRope",
+           "attention", "attention_fwd", "attention_bwd", "attention_step", "Attention"]

@@ -121,6 +121,55 @@ class SscanStepArgs(ctypes.Structure):
                 ("state_indices", c_void_p), ("num_slots", c_int), ("y", c_void_p), ("status", c_void_p)]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("B", c_int), ("T", c_int), ("cu_seqlens", ctypes.POINTER(ctypes.c_int32)), ("num_seqs", c_int),
+                ("H", c_int), ("num_k_heads", c_int), ("head_dim", c_int), ("rotary_dim", c_int), ("interleaved", c_int),
+                ("eps", c_float), ("q_stride", c_ll), ("k_stride", c_ll), ("v_stride", c_ll), ("num_pages", c_int),
+                ("page_size", c_int), ("table_width", c_int)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("q_weight", c_void_p), ("k_weight", c_void_p),
+                ("inv_freq", c_void_p), ("positions", c_void_p), ("q_out", c_void_p), ("k_out", c_void_p),
+                ("k_cache", c_void_p), ("v_cache", c_void_p), ("page_table", c_void_p), ("lengths", c_void_p),
+                ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("status", c_void_p)]
+
+
+class RopeBwdArgs(ctypes.Structure):
+    _fields_ = [("dq_out", c_void_p), ("dk_out", c_void_p), ("q", c_void_p), ("k", c_void_p), ("q_weight", c_void_p),
+                ("k_weight", c_void_p), ("inv_freq", c_void_p), ("positions", c_void_p), ("dq", c_void_p),
+                ("dk", c_void_p), ("dq_weight", c_void_p), ("dk_weight", c_void_p), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t)]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("B", c_int), ("T", c_int), ("cu_seqlens", ctypes.POINTER(ctypes.c_int32)), ("num_seqs", c_int),
+                ("H", c_int), ("num_k_heads", c_int), ("head_dim", c_int), ("causal", c_int), ("scale", c_float),
+                ("q_stride", c_ll), ("k_stride", c_ll), ("v_stride", c_ll)]
+
+
+class AttnFwdArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("o", c_void_p), ("lse", c_void_p),
+                ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("status", c_void_p)]
+
+
+class AttnBwdArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("o", c_void_p), ("lse", c_void_p), ("dO", c_void_p),
+                ("dq", c_void_p), ("dk", c_void_p), ("dv", c_void_p), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t), ("status", c_void_p)]
+
+
+class AttnStepDesc(ctypes.Structure):
+    _fields_ = [("B", c_int), ("H", c_int), ("num_k_heads", c_int), ("head_dim", c_int), ("scale", c_float),
+                ("num_pages", c_int), ("page_size", c_int), ("table_width", c_int), ("q_stride", c_ll)]
+
+
+class AttnStepArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k_cache", c_void_p), ("v_cache", c_void_p), ("page_table", c_void_p),
+                ("lengths", c_void_p), ("o", c_void_p), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+                ("status", c_void_p)]
+
+
 def _call(desc, args):
     return ([ctypes.POINTER(desc), ctypes.POINTER(args), c_void_p], c_int)
 
@@ -174,6 +223,16 @@ SIGNATURES = {
     "gdn_sscan_fwd": _call(SscanDesc, SscanFwdArgs),
     "gdn_sscan_bwd": _call(SscanDesc, SscanBwdArgs),
     "gdn_sscan_step": _call(SscanDesc, SscanStepArgs),
+    "gdn_qk_norm_rope_workspace_size": ([ctypes.POINTER(RopeDesc)], c_size_t),
+    "gdn_qk_norm_rope_fwd": _call(RopeDesc, RopeArgs),
+    "gdn_qk_norm_rope_store": _call(RopeDesc, RopeArgs),
+    "gdn_qk_norm_rope_bwd": _call(RopeDesc, RopeBwdArgs),
+    "gdn_attn_fwd_workspace_size": ([ctypes.POINTER(AttnDesc)], c_size_t),
+    "gdn_attn_bwd_workspace_size": ([ctypes.POINTER(AttnDesc)], c_size_t),
+    "gdn_attn_fwd": _call(AttnDesc, AttnFwdArgs),
+    "gdn_attn_bwd": _call(AttnDesc, AttnBwdArgs),
+    "gdn_attn_step_workspace_size": ([ctypes.POINTER(AttnStepDesc)], c_size_t),
+    "gdn_attn_step": _call(AttnStepDesc, AttnStepArgs),
     "gdn_timing_enable": ([c_int], c_int),
     "gdn_timing_kinds": ([], c_int),
     "gdn_timing_name": ([c_int], ctypes.c_char_p),

@@ -16,6 +16,7 @@
 #include <string>
 #include <vector>
 
+#include "attn.cuh"
 #include "block_ops.cuh"
 #include "common.cuh"
 #include "gdn.h"
@@ -296,14 +297,14 @@ int check_cuda(cudaError_t e, const char* what) {
 
 // Optional per-kernel timing (CUDA events recorded on the launching stream around every
 // launch while enabled). Process-global and not thread-safe: a profiling aid.
-const char* const kKindNames[kKAllKinds] = {"tables", "prepare", "chain_fwd", "chain_bwd", "bwd_feat", "bwd_tok",
+const char* const kKindNames[kKEveryKind] = {"tables", "prepare", "chain_fwd", "chain_bwd", "bwd_feat", "bwd_tok",
                                         "compose", "group_sum", "conv_fwd", "conv_bwd", "gate_grad",
                                         "norm_fwd", "norm_bwd", "conv_step", "delta_step", "sscan_fwd", "sscan_bwd",
-                                        "sscan_step"};
+                                        "sscan_step", "rope_fwd", "rope_bwd", "attn_fwd", "attn_bwd", "attn_step"};
 struct Timing {
   bool on = false;
-  std::vector<std::pair<cudaEvent_t, cudaEvent_t>> ev[kKAllKinds];
-  size_t used[kKAllKinds] = {};
+  std::vector<std::pair<cudaEvent_t, cudaEvent_t>> ev[kKEveryKind];
+  size_t used[kKEveryKind] = {};
 } g_tim;
 
 struct TimedLaunch {
@@ -846,6 +847,10 @@ int upload_offsets(const int32_t* host, int count, int* dst, cudaStream_t s) {
   return GDN_OK;
 }
 
+bool attn_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t stride, uint32_t box_rows) {
+  return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cols, rows, stride * 2, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 }  // namespace gdn
 
 using namespace gdn;
@@ -931,16 +936,16 @@ int gdn_chain_plan(const gdn_desc_t* desc, int* chunks_per_segment, int* max_seg
 
 int gdn_timing_enable(int enable) {
   g_tim.on = enable != 0;
-  for (int k = 0; k < kKAllKinds; ++k) g_tim.used[k] = 0;
+  for (int k = 0; k < kKEveryKind; ++k) g_tim.used[k] = 0;
   return GDN_OK;
 }
 
-int gdn_timing_kinds(void) { return kKAllKinds; }
+int gdn_timing_kinds(void) { return kKEveryKind; }
 
-const char* gdn_timing_name(int kind) { return (kind >= 0 && kind < kKAllKinds) ? kKindNames[kind] : ""; }
+const char* gdn_timing_name(int kind) { return (kind >= 0 && kind < kKEveryKind) ? kKindNames[kind] : ""; }
 
 int gdn_timing_read(int kind, double* total_ms, int* launches) {
-  if (kind < 0 || kind >= kKAllKinds || !total_ms || !launches) return fail(GDN_EINVAL, "bad timing query");
+  if (kind < 0 || kind >= kKEveryKind || !total_ms || !launches) return fail(GDN_EINVAL, "bad timing query");
   double tot = 0.0;
   for (size_t i = 0; i < g_tim.used[kind]; ++i) {
     float ms = 0.f;

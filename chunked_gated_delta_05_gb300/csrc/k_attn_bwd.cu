@@ -1,0 +1,491 @@
+// Attention over whole sequences, backward. With p_ij = e^(s_ij - lse_i) recomputed from q, k and the forward's lse:
+//   dP = dO v^T,  D_i = sum_c dO_ic o_ic (= sum_j p_ij dP_ij),  dS = p (dP - D)
+//   dv_j = sum_i p_ij dO_i,   dk_j = scale sum_i dS_ij q_i,   dq_i = scale sum_j dS_ij k_j
+// summed over the query heads of a key head for dk and dv.
+//
+// Three kernels. k_attn_delta leaves D and lse log2(e) by head. k_attn_dkv owns 128 keys of a key head and walks the query tiles
+// (and the group's heads) that see them; k_attn_dq owns 128 queries and walks the key tiles they see. Each output is
+// summed in registers of one CTA's tensor core in a fixed order, so nothing is added atomically and results do not depend on
+// the order of blocks; the price is that both recompute s and dP: seven products of 128 x 128 x D a tile pair, where adding dq up in
+// memory would need five.
+//
+// k_attn_dkv works on transposed scores, keys on the TMEM lanes, so that P^T and dS^T are TMEM-resident A operands:
+//   S^T = K Q^T, dP^T = V dO^T  (shared-memory operands, K-major)
+//   dV += P^T dO, dK += dS^T Q  (the same Q and dO tiles read MN-major)
+// TMEM: S^T (P^T over it), dP^T (dS^T over it), dV, dK. The products run in the order dV(i), S(i+1), dK(i), dP(i+1): while a pair of
+// them runs, the softmax warps turn the scores (or dP) of the other pair's into the next operand.
+// k_attn_dq: S = Q K^T, dP = dO V^T, dQ += dS K (dS over S in TMEM; S double-buffered, a tile ahead).
+//
+// Eight softmax warps, two threads a TMEM lane, each on half of a tile's columns. The bf16 operand halves lie over the columns
+// that their own writers have read. p and dS are rounded to bf16 (as the products' operands); all sums are fp32.
+#include "attn.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 384;                        // 8 softmax warps, the MMA warp, the TMA warp, two that only give registers
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 8 x 208 + 4 x 88 = 12 x 168, the launch's
+constexpr int kSoftmax = 256;
+
+template <int D>
+struct Cfg {
+  static constexpr int kTile = kAttnTile * D * 2;
+  static constexpr int kSmem = 7 * kTile + 2 * 1024 + 512;  // 2 fixed tiles, rings of 3 and 2, two stages of vectors, barriers
+};
+
+// Column of k-step s of a bf16 operand that lies in two halves over 128 columns.
+__device__ __forceinline__ uint32_t half_col(int s) { return uint32_t(s < 4 ? s * 8 : 64 + (s - 4) * 8); }
+
+// 64 columns of x, rounded to bf16, to 32 columns of TMEM.
+__device__ __forceinline__ void store_operand(uint32_t t, const float* x) {
+  float w[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) w[e] = __uint_as_float(pack_bf16(x[2 * e], x[2 * e + 1]));
+  tmem_st32(t, w);
+}
+
+// 32 columns of an accumulator row times f, as bf16.
+__device__ __forceinline__ void store_row(__nv_bfloat16* dst, uint32_t t, float f, bool mine) {
+  float o[32];
+  tmem_ld32(t, o);
+  tmem_wait_ld_regs(o);
+  if (!mine) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float* x = o + 8 * e;
+    *reinterpret_cast<uint4*>(dst + 8 * e) =
+        make_uint4(pack_bf16(x[0] * f, x[1] * f), pack_bf16(x[2] * f, x[3] * f), pack_bf16(x[4] * f, x[5] * f), pack_bf16(x[6] * f, x[7] * f));
+  }
+}
+
+// Ring position and phase of use i.
+__device__ __forceinline__ int slot(int i, int n) { return i % n; }
+__device__ __forceinline__ uint32_t phase(int i, int n) { return uint32_t(i / n) & 1u; }
+
+}  // namespace
+
+// D_i and lse_i log2(e) of 32 rows of a head a warp.
+template <int D>
+__global__ void __launch_bounds__(256) k_attn_delta(const AttnParams p) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, which = lane / kLanes;
+  const long long chunks = (p.rows + 31) / 32, item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  wait_for_previous();
+  if (item >= chunks * p.H) return;
+  const int h = int(item % p.H);
+  const long long row0 = item / p.H * 32;
+  float mine = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < kLanes; ++i) {
+    const long long row = row0 + i * kRows + which;
+    float x = 0.f;
+    if (row < p.rows) {
+      const long long at = (row * p.H + h) * D + sub * 8;
+      const uint4 a = *reinterpret_cast<const uint4*>(p.dO + at), b = *reinterpret_cast<const uint4*>(p.o_in + at);
+      const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x = fmaf(bf16_lo(u[e]), bf16_lo(v[e]), fmaf(bf16_hi(u[e]), bf16_hi(v[e]), x));
+    }
+#pragma unroll
+    for (int d = kLanes / 2; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    // row i kRows + w of the 32 was summed by the lanes of part w
+    const float got = __shfl_sync(0xffffffffu, x, (lane % kRows) * kLanes);
+    if (lane / kRows == i) mine = got;
+  }
+  const long long row = row0 + lane;
+  if (row < p.rows) {
+    p.delta[h * p.rows + row] = mine;
+    p.lse2[h * p.rows + row] = p.lse_in[row * p.H + h] * kLog2e;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_dkv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+               const __grid_constant__ CUtensorMap mdo, const AttnParams p) {
+  constexpr int kTile = Cfg<D>::kTile, kQ = 3, kO = 2;  // stages of Q and of dO (a Q tile is needed longer)
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint8_t *sK = sm, *sV = sK + kTile, *sQ = sV + kTile, *sO = sQ + kQ * kTile;
+  float* vec = reinterpret_cast<float*>(sO + kO * kTile);  // [2][lse2 | delta][128]
+  uint64_t* bar = reinterpret_cast<uint64_t*>(vec + 2 * 256);
+  uint64_t *kv_full = bar, *q_full = bar + 1, *q_empty = bar + 4, *o_full = bar + 7, *o_empty = bar + 9, *ready = bar + 11, *vec_free = bar + 13, *s_full = bar + 15,
+           *dp_full = bar + 16, *p_ready = bar + 17, *ds_ready = bar + 18, *done = bar + 19;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 20);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 21);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hk = blockIdx.x % p.Hk;
+  wait_for_previous();
+  const AttnTile tl = attn_tile(p, blockIdx.x / p.Hk, kAttnTile, p.causal != 0);
+  const int all = (tl.len + kAttnTile - 1) / kAttnTile, i0 = p.causal ? tl.first / kAttnTile : 0, per = all - i0, n = per * p.group;
+  const bool ragged = all * kAttnTile > tl.len;
+
+  if (warp == 8) tmem_alloc(tslot, 512);
+  if (tid == 0) {
+    *abort_flag = 0;
+    mbar_init(kv_full, 1);
+    for (int i = 0; i < kQ; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1);
+    for (int i = 0; i < kO; ++i) mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 1), mbar_init(&ready[i], 32), mbar_init(&vec_free[i], kSoftmax);
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_ready, kSoftmax);
+    mbar_init(ds_ready, kSoftmax);
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = *tslot, tS = tb, tP = tb + 128, tV = tb + 256, tK = tb + 256 + D;
+
+  if (warp >= 8) {
+    regs_dec<kOtherRegs>();
+    if (warp == 9) {
+      // ---------------- producer ----------------
+      if (lane == 0) {
+        mbar_expect_tx(kv_full, 2 * kTile);
+        load_attn_tile<D>(sK, &mk, hk * D, tl.row0 + tl.first, kv_full);
+        load_attn_tile<D>(sV, &mv, hk * D, tl.row0 + tl.first, kv_full);
+      }
+      int it = 0;
+      bool ok = true;
+      for (; it < n; ++it) {
+        const int h = hk * p.group + it / per, q0 = (i0 + it % per) * kAttnTile, y = tl.row0 + q0, qs = slot(it, kQ), os = slot(it, kO);
+        if (it >= kQ) ok = mbar_wait(&q_empty[qs], phase(it - kQ, kQ), abort_flag, p.status, kDevTimeoutMma);
+        if (ok && lane == 0) {
+          mbar_expect_tx(&q_full[qs], kTile);
+          load_attn_tile<D>(sQ + qs * kTile, &mq, h * D, y, &q_full[qs]);
+        }
+        if (ok && it >= kO)
+          ok = mbar_wait(&o_empty[os], phase(it - kO, kO), abort_flag, p.status, kDevTimeoutMma) &&
+               mbar_wait(&vec_free[os], phase(it - kO, kO), abort_flag, p.status, kDevTimeoutSync);
+        if (ok && lane == 0) {
+          mbar_expect_tx(&o_full[os], kTile);
+          load_attn_tile<D>(sO + os * kTile, &mdo, h * D, y, &o_full[os]);
+        }
+        if (!__all_sync(0xffffffffu, ok)) break;
+        float* v = vec + os * 256;
+        const long long at = (long long)h * p.rows + y;
+#pragma unroll
+        for (int e = lane; e < kAttnTile; e += 32) {
+          const bool in = q0 + e < tl.len;
+          v[e] = in ? p.lse2[at + e] : INFINITY;
+          v[128 + e] = in ? p.delta[at + e] : 0.f;
+        }
+        if (ragged && q0 + kAttnTile > tl.len) {
+          ok = mbar_wait(&q_full[qs], phase(it, kQ), abort_flag, p.status, kDevTimeoutTma) &&
+               mbar_wait(&o_full[os], phase(it, kO), abort_flag, p.status, kDevTimeoutTma);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          zero_attn_rows<D>(sQ + qs * kTile, tl.len - q0, lane);
+          zero_attn_rows<D>(sO + os * kTile, tl.len - q0, lane);
+          fence_async_smem();
+        }
+        mbar_arrive(&ready[os]);
+      }
+      if (it < n && lane == 0) {  // the copies in flight land before their destination is given up
+        mbar_drain(kv_full, 0);
+        for (int k = max(0, it - kQ + 1); k < it; ++k) mbar_drain(&q_full[slot(k, kQ)], phase(k, kQ));
+        for (int k = max(0, it - kO + 1); k < it; ++k) mbar_drain(&o_full[slot(k, kO)], phase(k, kO));
+        // the last ones, if they were requested
+        mbar_drain(&q_full[slot(it, kQ)], phase(it, kQ), 1000000ull);
+        mbar_drain(&o_full[slot(it, kO)], phase(it, kO), 1000000ull);
+      }
+    } else if (warp == 8 && lane == 0) {
+      // ---------------- MMA issuer ----------------
+      constexpr uint32_t idS = idesc_bf16(128, 128), idO = idesc_bf16(128, D, false, true);
+      const uint32_t aK = smem_u32(sK), aV = smem_u32(sV), bQ = smem_u32(sQ), bO = smem_u32(sO);
+      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return mbar_wait(b, ph, abort_flag, p.status, code); };
+      auto scores = [&](int it) {
+        if (!wait(&q_full[slot(it, kQ)], phase(it, kQ), kDevTimeoutTma) || !wait(&ready[slot(it, kO)], phase(it, kO), kDevTimeoutSync)) return false;
+        tc_fence_after();
+        const uint32_t b = bQ + slot(it, kQ) * kTile;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) mma_bf16_ss(tS, desc_kmajor(aK, kAttnPanel, s), desc_kmajor(b, kAttnPanel, s), idS, s > 0);
+        mma_commit(s_full);
+        return true;
+      };
+      auto dprobs = [&](int it) {
+        if (!wait(&o_full[slot(it, kO)], phase(it, kO), kDevTimeoutTma)) return false;
+        tc_fence_after();
+        const uint32_t b = bO + slot(it, kO) * kTile;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) mma_bf16_ss(tP, desc_kmajor(aV, kAttnPanel, s), desc_kmajor(b, kAttnPanel, s), idS, s > 0);
+        mma_commit(dp_full);
+        return true;
+      };
+      bool ok = wait(kv_full, 0, kDevTimeoutTma) && scores(0) && dprobs(0);
+      for (int it = 0; it < n && ok; ++it) {
+        ok = wait(p_ready, it & 1, kDevTimeoutSync);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t o = bO + slot(it, kO) * kTile, q = bQ + slot(it, kQ) * kTile;
+#pragma unroll
+        for (int s = 0; s < kAttnTile / 16; ++s) mma_bf16_ts(tV, tS + half_col(s), desc_mnmajor_bf16(o, kAttnPanel, s), idO, it > 0 || s > 0);
+        mma_commit(&o_empty[slot(it, kO)]);
+        if (it + 1 < n && !(ok = scores(it + 1))) break;
+        ok = wait(ds_ready, it & 1, kDevTimeoutSync);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int s = 0; s < kAttnTile / 16; ++s) mma_bf16_ts(tK, tP + half_col(s), desc_mnmajor_bf16(q, kAttnPanel, s), idO, it > 0 || s > 0);
+        mma_commit(&q_empty[slot(it, kQ)]);
+        if (it + 1 < n) ok = dprobs(it + 1);
+      }
+      mma_commit(done);  // the softmax warps wait for it, or, after an error:
+      if (!ok) mbar_drain(done, 0);
+    }
+  } else {
+    // ---------------- softmax: key row, half of the queries ----------------
+    regs_inc<kSoftmaxRegs>();
+    const int half = warp >> 2, row = tid & 127, key = tl.first + row;
+    const uint32_t lb = tmem_lane_base(warp) + uint32_t(half) * 64;
+    const F2 c2 = dup2(p.scale * kLog2e), minus = dup2(-1.f);
+    bool ok = true;
+    for (int it = 0; it < n && ok; ++it) {
+      const int q0 = (i0 + it % per) * kAttnTile + half * 64, os = slot(it, kO);
+      const float4 *lse = reinterpret_cast<const float4*>(vec + os * 256 + half * 64), *delta = lse + 32;
+      ok = mbar_wait(&ready[os], phase(it, kO), abort_flag, p.status, kDevTimeoutSync) &&
+           mbar_wait(s_full, it & 1, abort_flag, p.status, kDevTimeoutMma);
+      if (!ok) break;
+      tc_fence_after();
+      float w[64];
+      tmem_ld64(tS + lb, w);
+      tmem_wait_ld_regs(w);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float4 l = lse[e];
+        float* x = w + 4 * e;
+        unf2(fma2(f2(x[0], x[1]), c2, mul2(f2(l.x, l.y), minus)), &x[0], &x[1]);
+        unf2(fma2(f2(x[2], x[3]), c2, mul2(f2(l.z, l.w), minus)), &x[2], &x[3]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = exp2_approx(x[u]);
+      }
+      const int from = p.causal ? key - q0 : 0, to = tl.len - q0;  // of the half's queries, those that see the key
+      if (to < 64 || (p.causal && tl.first + kAttnTile > q0)) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e < from || e >= to) w[e] = 0.f;
+      }
+      store_operand(tS + lb, w);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(p_ready);
+      ok = mbar_wait(dp_full, it & 1, abort_flag, p.status, kDevTimeoutMma);
+      if (!ok) break;
+      tc_fence_after();
+      float d[64];
+      tmem_ld64(tP + lb, d);
+      tmem_wait_ld_regs(d);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float4 l = delta[e];
+        float *x = d + 4 * e, *y = w + 4 * e;
+        unf2(mul2(f2(y[0], y[1]), fma2(f2(l.x, l.y), minus, f2(x[0], x[1]))), &x[0], &x[1]);
+        unf2(mul2(f2(y[2], y[3]), fma2(f2(l.z, l.w), minus, f2(x[2], x[3]))), &x[2], &x[3]);
+      }
+      mbar_arrive(&vec_free[os]);
+      store_operand(tP + lb, d);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(ds_ready);
+    }
+    if (ok && mbar_wait(done, 0, abort_flag, p.status, kDevTimeoutMma)) {
+      tc_fence_after();
+      __nv_bfloat16* dst = (half ? p.dk : p.dv) + ((size_t(tl.row0) + key) * p.Hk + hk) * D;
+      const uint32_t acc = (half ? tK : tV) + tmem_lane_base(warp);
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) store_row(dst + q * 32, acc + q * 32, half ? p.scale : 1.f, key < tl.len);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tb, 512);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+              const __grid_constant__ CUtensorMap mdo, const AttnParams p) {
+  constexpr int kTile = Cfg<D>::kTile, kK = 3, kV = 2;  // stages of K (needed longer) and V
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint8_t *sQ = sm, *sO = sQ + kTile, *sK = sO + kTile, *sV = sK + kK * kTile;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sV + kV * kTile);
+  uint64_t *q_full = bar, *k_full = bar + 1, *k_empty = bar + 4, *v_full = bar + 7, *v_empty = bar + 9, *s_full = bar + 11, *dp_full = bar + 13, *ds_ready = bar + 14,
+           *tail_ready = bar + 15, *done = bar + 16;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 17);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 18);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.x % p.H, hk = h / p.group;
+  wait_for_previous();
+  const AttnTile tl = attn_tile(p, blockIdx.x / p.H, kAttnTile, false);
+  const int all = (tl.len + kAttnTile - 1) / kAttnTile, n = p.causal ? tl.first / kAttnTile + 1 : all;
+  const bool tail = n * kAttnTile > tl.len;
+
+  if (warp == 8) tmem_alloc(tslot, 512);
+  if (tid == 0) {
+    *abort_flag = 0;
+    mbar_init(q_full, 1);
+    for (int i = 0; i < kK; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
+    for (int i = 0; i < kV; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 1), mbar_init(&s_full[i], 1);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_ready, kSoftmax);
+    mbar_init(tail_ready, 32);
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = *tslot, tP = tb + 256, tQ = tb + 384;
+  auto tS = [&](int i) { return tb + uint32_t(i & 1) * 128; };
+
+  if (warp >= 8) {
+    regs_dec<kOtherRegs>();
+    if (warp == 9) {
+      // ---------------- producer ----------------
+      int it = 0;
+      if (lane == 0) {
+        mbar_expect_tx(q_full, 2 * kTile);
+        load_attn_tile<D>(sQ, &mq, h * D, tl.row0 + tl.first, q_full);
+        load_attn_tile<D>(sO, &mdo, h * D, tl.row0 + tl.first, q_full);
+        for (; it < n; ++it) {
+          const int ks = slot(it, kK), vs = slot(it, kV), y = tl.row0 + it * kAttnTile;
+          if (it >= kK && !mbar_wait(&k_empty[ks], phase(it - kK, kK), abort_flag, p.status, kDevTimeoutMma)) break;
+          mbar_expect_tx(&k_full[ks], kTile);
+          load_attn_tile<D>(sK + ks * kTile, &mk, hk * D, y, &k_full[ks]);
+          if (it >= kV && !mbar_wait(&v_empty[vs], phase(it - kV, kV), abort_flag, p.status, kDevTimeoutMma)) {
+            mbar_drain(&k_full[ks], phase(it, kK));
+            break;
+          }
+          mbar_expect_tx(&v_full[vs], kTile);
+          load_attn_tile<D>(sV + vs * kTile, &mv, hk * D, y, &v_full[vs]);
+        }
+        if (it < n) {  // the copies in flight land before their destination is given up
+          mbar_drain(q_full, 0);
+          for (int k = max(0, it - kK); k < it; ++k) mbar_drain(&k_full[slot(k, kK)], phase(k, kK));
+          for (int k = max(0, it - kV); k < it; ++k) mbar_drain(&v_full[slot(k, kV)], phase(k, kV));
+        }
+      }
+      it = __shfl_sync(0xffffffffu, it, 0);
+      if (tail && it == n && mbar_wait(&k_full[slot(n - 1, kK)], phase(n - 1, kK), abort_flag, p.status, kDevTimeoutTma)) {
+        zero_attn_rows<D>(sK + slot(n - 1, kK) * kTile, tl.len - (n - 1) * kAttnTile, lane);
+        fence_async_smem();
+        mbar_arrive(tail_ready);
+      }
+    } else if (warp == 8 && lane == 0) {
+      // ---------------- MMA issuer ----------------
+      constexpr uint32_t idS = idesc_bf16(128, 128), idO = idesc_bf16(128, D, false, true);
+      const uint32_t aQ = smem_u32(sQ), aO = smem_u32(sO), bK = smem_u32(sK), bV = smem_u32(sV);
+      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return mbar_wait(b, ph, abort_flag, p.status, code); };
+      auto scores = [&](int i) {
+        if (!wait(&k_full[slot(i, kK)], phase(i, kK), kDevTimeoutTma)) return false;
+        if (tail && i + 1 == n && !wait(tail_ready, 0, kDevTimeoutSync)) return false;
+        tc_fence_after();
+        const uint32_t b = bK + slot(i, kK) * kTile;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) mma_bf16_ss(tS(i), desc_kmajor(aQ, kAttnPanel, s), desc_kmajor(b, kAttnPanel, s), idS, s > 0);
+        mma_commit(&s_full[i & 1]);
+        return true;
+      };
+      auto dprobs = [&](int i) {
+        if (!wait(&v_full[slot(i, kV)], phase(i, kV), kDevTimeoutTma)) return false;
+        tc_fence_after();
+        const uint32_t b = bV + slot(i, kV) * kTile;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) mma_bf16_ss(tP, desc_kmajor(aO, kAttnPanel, s), desc_kmajor(b, kAttnPanel, s), idS, s > 0);
+        mma_commit(dp_full);
+        mma_commit(&v_empty[slot(i, kV)]);
+        return true;
+      };
+      bool ok = wait(q_full, 0, kDevTimeoutTma) && scores(0) && dprobs(0) && (n == 1 || scores(1));
+      for (int i = 0; i < n && ok; ++i) {
+        ok = wait(ds_ready, i & 1, kDevTimeoutSync);
+        if (!ok) break;
+        tc_fence_after();
+        if (i + 1 < n && !(ok = dprobs(i + 1))) break;
+        const uint32_t b = bK + slot(i, kK) * kTile;
+#pragma unroll
+        for (int s = 0; s < kAttnTile / 16; ++s) mma_bf16_ts(tQ, tS(i) + half_col(s), desc_mnmajor_bf16(b, kAttnPanel, s), idO, i > 0 || s > 0);
+        mma_commit(&k_empty[slot(i, kK)]);
+        if (i + 2 < n) ok = scores(i + 2);
+      }
+      mma_commit(done);  // the softmax warps wait for it, or, after an error:
+      if (!ok) mbar_drain(done, 0);
+    }
+  } else {
+    // ---------------- softmax: query row, half of the keys ----------------
+    regs_inc<kSoftmaxRegs>();
+    const int half = warp >> 2, row = tid & 127, qi = tl.first + row;
+    const uint32_t lane0 = tmem_lane_base(warp), lb = lane0 + uint32_t(half) * 64;
+    const bool mine = qi < tl.len;
+    const long long at = (long long)h * p.rows + tl.row0 + qi;
+    const F2 c2 = dup2(p.scale * kLog2e), lse = dup2(mine ? -p.lse2[at] : 0.f), delta = dup2(mine ? -p.delta[at] : 0.f);
+    bool ok = true;
+    for (int i = 0; i < n && ok; ++i) {
+      ok = mbar_wait(&s_full[i & 1], (i >> 1) & 1, abort_flag, p.status, kDevTimeoutMma);
+      if (!ok) break;
+      tc_fence_after();
+      float w[64], d[64];
+      tmem_ld64(tS(i) + lb, w);
+      tmem_wait_ld_regs(w);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        float a, b;
+        unf2(fma2(f2(w[2 * e], w[2 * e + 1]), c2, lse), &a, &b);
+        w[2 * e] = exp2_approx(a);
+        w[2 * e + 1] = exp2_approx(b);
+      }
+      ok = mbar_wait(dp_full, i & 1, abort_flag, p.status, kDevTimeoutMma);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld64(tP + lb, d);
+      tmem_wait_ld_regs(d);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) unf2(mul2(f2(w[2 * e], w[2 * e + 1]), add2(f2(d[2 * e], d[2 * e + 1]), delta)), &d[2 * e], &d[2 * e + 1]);
+      const int k0 = i * kAttnTile;
+      if (i + 1 == n && (p.causal || tail)) {
+        const int seen = (p.causal ? min(qi + 1, tl.len) : tl.len) - k0 - half * 64;
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e >= seen) d[e] = 0.f;
+      }
+      store_operand(tS(i) + lb, d);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(ds_ready);
+    }
+    if (ok && mbar_wait(done, 0, abort_flag, p.status, kDevTimeoutMma)) {
+      tc_fence_after();
+      __nv_bfloat16* dst = p.dq + ((size_t(tl.row0) + qi) * p.H + h) * D + half * (D / 2);
+#pragma unroll
+      for (int q = 0; q < D / 64; ++q) store_row(dst + q * 32, tQ + lane0 + half * (D / 2) + q * 32, p.scale, mine);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tb, 512);
+}
+
+template <int D>
+static cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, const AttnParams& p, const int* keys, cudaStream_t s) {
+  constexpr int kSmem = Cfg<D>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(k_attn_dkv<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_attn_dq<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const long long items = (p.rows + 31) / 32 * p.H;
+  e = launch_after(k_attn_delta<D>, dim3(unsigned((items + 7) / 8)), dim3(256), 0, s, p);
+  if (e != cudaSuccess) return e;
+  AttnParams pk = p;
+  pk.table = keys;
+  e = launch_after(k_attn_dkv<D>, dim3(unsigned(p.tiles * p.Hk)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, pk);
+  if (e != cudaSuccess) return e;
+  return launch_after(k_attn_dq<D>, dim3(unsigned(p.tiles * p.H)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, p);
+}
+
+cudaError_t launch_attn_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, int D, const AttnParams& p, const int* keys,
+                            cudaStream_t s) {
+  return D == 128 ? launch<128>(mq, mk, mv, mdo, p, keys, s) : launch<64>(mq, mk, mv, mdo, p, keys, s);
+}
+
+}  // namespace gdn

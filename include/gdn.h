@@ -439,6 +439,130 @@ typedef struct {
 
 int gdn_sscan_step(const gdn_sscan_desc_t* desc, const gdn_sscan_step_args_t* args, void* stream);
 
+/* ---- Attention blocks between recurrent ones (no counterpart in the pages). head_dim is 64 or 128; the H query heads read
+ * num_k_heads key heads (0: H), head h the key head h / (H / num_k_heads). Token rows of q, k and v lie `*_stride` elements apart
+ * (0: contiguous; batches follow each other at T rows), their heads are contiguous. Tensors are 16-byte aligned, strides multiples of 8.
+ * Packed documents as for gdn_fwd.
+ *
+ * Norm and rotation of every query and key head: n = x rsqrt(mean(x^2) + eps) weight (no norm where both weights are NULL), then
+ * the first rotary_dim channels of n in pairs (a, b), the i-th turned by the angle position * inv_freq[i]:
+ *   a' = a cos - b sin, b' = b cos + a sin.   Pairs are (i, i + rotary_dim/2), or (2i, 2i + 1) when `interleaved`.
+ * The angle is taken modulo a turn in 64-bit integers: it is as good at far positions as at near ones. Positions count from
+ * the sequence's first token, or are given. */
+typedef struct {
+  int B, T;
+  const int32_t* cu_seqlens; /* HOST, num_seqs + 1 offsets, or NULL for dense */
+  int num_seqs;
+  int H, num_k_heads, head_dim;
+  int rotary_dim;            /* a multiple of 16, 0 .. head_dim */
+  int interleaved;
+  float eps;                 /* >= 0 */
+  long long q_stride, k_stride, v_stride;
+  int num_pages, page_size;  /* gdn_qk_norm_rope_store: the cache's */
+  int table_width;           /* pages a sequence can name */
+} gdn_rope_desc_t;
+
+typedef struct {
+  const void *q, *k;         /* bf16 [B,T,H,D], [B,T,Hk,D] */
+  const void* v;             /* store: bf16 [B,T,Hk,D] */
+  const float *q_weight, *k_weight; /* fp32 [D], both or neither */
+  const float* inv_freq;     /* fp32 [rotary_dim/2], or NULL when rotary_dim is 0 */
+  const int32_t* positions;  /* device [B,T], or NULL; NULL with a store */
+  void *q_out, *k_out;       /* bf16 [B,T,H,D], [B,T,Hk,D] contiguous, written */
+  void *k_cache, *v_cache;   /* store: bf16 [num_pages,page_size,Hk,D], written in the new tokens' rows */
+  const int32_t* page_table; /* store: device [num_seqs,table_width]: the sequence's pages in order */
+  const int32_t* lengths;    /* store: device [num_seqs]: tokens of the sequence, the new ones among them */
+  void* workspace;           /* >= gdn_qk_norm_rope_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int* status;               /* or NULL */
+} gdn_rope_args_t;
+
+typedef struct {
+  const void *dq_out, *dk_out;  /* bf16, contiguous: gradients of q_out and k_out */
+  const void *q, *k;         /* the forward's inputs */
+  const float *q_weight, *k_weight, *inv_freq;
+  const int32_t* positions;
+  void *dq, *dk;             /* bf16, contiguous, written */
+  float *dq_weight, *dk_weight; /* fp32 [D], written (needed with the weights): summed over tokens and heads in a fixed order */
+  void* workspace;
+  size_t workspace_bytes;
+} gdn_rope_bwd_args_t;
+
+size_t gdn_qk_norm_rope_workspace_size(const gdn_rope_desc_t* desc);  /* of all three calls */
+int gdn_qk_norm_rope_fwd(const gdn_rope_desc_t* desc, const gdn_rope_args_t* args, void* stream);
+int gdn_qk_norm_rope_bwd(const gdn_rope_desc_t* desc, const gdn_rope_bwd_args_t* args, void* stream);
+
+/* The same for tokens that enter a paged cache: sequence n's T (or document's) tokens are the last of its lengths[n], their
+ * positions count accordingly, and token p of it goes to row p % page_size of page page_table[n][p / page_size]. lengths[n] <= 0
+ * marks padding: its outputs are zero and nothing is written to the cache; so do tokens whose length is shorter than the new tokens,
+ * or whose page lies outside the table or the cache, which also record GDN_ERANGE in the status word (not reset by the call).
+ * No cache row may be written twice in a call. */
+int gdn_qk_norm_rope_store(const gdn_rope_desc_t* desc, const gdn_rope_args_t* args, void* stream);
+
+/* Attention over whole sequences: o = softmax(scale q k^T) v per head, every query seeing its whole sequence or, when
+ * causal, the tokens up to itself. lse is the logarithm of the softmax's denominator. bf16 operands of the tensor core (the softmax's
+ * weights and their gradients are rounded to it), fp32 scores, sums and accumulators; results do not depend on the order
+ * in which blocks run. */
+typedef struct {
+  int B, T;
+  const int32_t* cu_seqlens;
+  int num_seqs;
+  int H, num_k_heads, head_dim;
+  int causal;
+  float scale;               /* <= 0 selects 1/sqrt(head_dim) */
+  long long q_stride, k_stride, v_stride;
+} gdn_attn_desc_t;
+
+typedef struct {
+  const void *q, *k, *v;     /* bf16 [B,T,H,D], [B,T,Hk,D], [B,T,Hk,D] */
+  void* o;                   /* bf16 [B,T,H,D] contiguous, written */
+  float* lse;                /* fp32 [B,T,H], written */
+  void* workspace;           /* >= gdn_attn_fwd_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int* status;               /* or NULL; records a wait that ran out (GDN_ETIMEOUT), not reset by the call */
+} gdn_attn_fwd_args_t;
+
+typedef struct {
+  const void *q, *k, *v;     /* the forward's inputs */
+  const void* o;             /* and its results */
+  const float* lse;
+  const void* dO;            /* bf16 [B,T,H,D] contiguous */
+  void *dq, *dk, *dv;        /* bf16 contiguous, written */
+  void* workspace;           /* >= gdn_attn_bwd_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int* status;
+} gdn_attn_bwd_args_t;
+
+size_t gdn_attn_fwd_workspace_size(const gdn_attn_desc_t* desc);
+size_t gdn_attn_bwd_workspace_size(const gdn_attn_desc_t* desc);
+int gdn_attn_fwd(const gdn_attn_desc_t* desc, const gdn_attn_fwd_args_t* args, void* stream);
+int gdn_attn_bwd(const gdn_attn_desc_t* desc, const gdn_attn_bwd_args_t* args, void* stream);
+
+/* One token per sequence over a paged cache (gdn_qk_norm_rope_store's): row b attends to the first lengths[b] keys of its pages.
+ * lengths[b] <= 0: its output is zero. A length beyond the table gives a zero row, a page outside the cache counts as absent keys;
+ * both record GDN_ERANGE in the status word. */
+typedef struct {
+  int B;
+  int H, num_k_heads, head_dim;
+  float scale;               /* <= 0 selects 1/sqrt(head_dim) */
+  int num_pages, page_size, table_width;
+  long long q_stride;        /* elements between rows of q (0: contiguous), a multiple of 8 */
+} gdn_attn_step_desc_t;
+
+typedef struct {
+  const void* q;             /* bf16 [B,H,D], 16-byte aligned */
+  const void *k_cache, *v_cache; /* bf16 [num_pages,page_size,Hk,D], 16-byte aligned */
+  const int32_t* page_table; /* device [B,table_width] */
+  const int32_t* lengths;    /* device [B] */
+  void* o;                   /* bf16 [B,H,D], written */
+  void* workspace;           /* >= gdn_attn_step_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int* status;
+} gdn_attn_step_args_t;
+
+size_t gdn_attn_step_workspace_size(const gdn_attn_step_desc_t* desc);
+int gdn_attn_step(const gdn_attn_step_desc_t* desc, const gdn_attn_step_args_t* args, void* stream);
+
 /* Profiling hooks (not part of the computation). While enabled, every kernel launch of the
  * calls above is bracketed by CUDA events on its stream. gdn_timing_read() synchronizes the
  * recorded events of one kernel kind (0 .. gdn_timing_kinds()-1, named by gdn_timing_name()),
