@@ -9,12 +9,64 @@ namespace gdn {
 // Kernel kinds of the per-launch timing hook, after the block operators' (names in api.cu).
 enum AttnKernelKind { kKRopeFwd = kKAllKinds, kKRopeBwd, kKAttnFwd, kKAttnBwd, kKAttnStep, kKEveryKind };
 
-// A operand read from TMEM, bf16: M lanes, two neighbouring K entries per 32-bit column.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool acc) {
+// One thread issues the products, and what it takes to form an instruction's operands sets their pace: with the descriptors of
+// umma.cuh built anew for every step it took 90 cycles an instruction, where the tensor core needs 64 (measured, products of
+// 128 x 128 x 128). So the descriptors' low words are kept and a step is one addition; the high word is a constant.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart, version, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_low_k(uint32_t base) { return (base >> 4) | (1u << 16); }                                     // K-major
+__device__ __forceinline__ uint32_t desc_low_mn(uint32_t base, uint32_t panel) { return (base >> 4) | ((panel >> 4) << 16); }          // MN-major
+//
+// The whole issuing warp walks the code, and `lead` (one lane) issues: control flow that the compiler knows to be the same for all
+// lanes keeps descriptors and addresses in uniform registers, where the instruction wants them.
+template <bool kAcc>
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(uint32_t(acc))
+      "{\n .reg .pred p, q;\n .reg .b64 x, y;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHigh), "n"(int(kAcc)), "r"(lead)
       : "memory");
+}
+// A operand in TMEM, bf16: M lanes, two neighbouring K entries per 32-bit column.
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 y;\n mov.b64 y, {%2, %4};\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHigh), "r"(uint32_t(acc)), "r"(lead)
+      : "memory");
+}
+// Arrive on `bar` once every product that the leading lane has issued so far is complete.
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_lead() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+
+// mbar_wait (bounded, umma.cuh) behind tries that let the hardware suspend the thread for up to a millisecond: it wakes with the
+// phase, and neither spins nor reads a clock meanwhile.
+__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int code) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return mbar_wait(bar, parity, abort, status, code);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // A warpgroup's share of the block's registers.
@@ -41,6 +93,7 @@ struct AttnParams {
   int H, Hk, group;            // group = H / Hk query heads read one key head
   int T, N;                    // dense: tokens per sequence and sequences
   int tiles;                   // tiles of all sequences
+  int sms;
   const int* table;            // packed: 3 ints per tile, most work first; else null (dense, computed)
   int causal;
   float scale;
@@ -70,6 +123,44 @@ __device__ __forceinline__ void load_attn_tile(uint8_t* dst, const CUtensorMap* 
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) tma_load_2d(dst + i * kAttnPanel, m, x + i * 64, y, bar);
 }
+// d = A B^T of two such tiles (inner dimension D), from their descriptors' low words.
+template <int D>
+__device__ __forceinline__ void product_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t id = idesc_bf16(kAttnTile, kAttnTile);
+  mma_ss<false>(lead, d, a, b, id);
+#pragma unroll
+  for (int s = 1; s < D / 16; ++s) {
+    const uint32_t o = ((s >> 2) * kAttnPanel + (s & 3) * 32) >> 4;
+    mma_ss<true>(lead, d, a + o, b + o, id);
+  }
+}
+// d (+)= A B for half of the inner dimension, 64: A [128,64] in TMEM, B those 64 rows of a tile read MN-major.
+template <int D>
+__device__ __forceinline__ void product_ts_half(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, bool acc) {
+  constexpr uint32_t id = idesc_bf16(kAttnTile, D, false, true);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) mma_ts(lead, d, a + s * 8, b + s * 128, id, acc || s > 0);
+}
+// Both halves, A's `half` columns apart.
+template <int D>
+__device__ __forceinline__ void product_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t half, uint32_t b, bool acc) {
+  product_ts_half<D>(lead, d, a, b, acc);
+  product_ts_half<D>(lead, d, a + half, b + 4 * 128, true);
+}
+// A ring of kN stages walked kStep uses at a time: this use's stage and phase.
+template <int kN, int kStep>
+struct Ring {
+  int at;
+  uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int first) : at(first) {}
+  __device__ __forceinline__ void next() {
+    at += kStep;
+    if (at >= kN) {
+      at -= kN;
+      phase ^= 1u;
+    }
+  }
+};
 // Rows `from` .. 127 of a tile zeroed by a warp. They belong to the next sequence, and 0 x NaN would carry its NaN over.
 template <int D>
 __device__ __forceinline__ void zero_attn_rows(uint8_t* tile, int from, int lane) {

@@ -281,8 +281,8 @@ int attn_fwd(const gdn_attn_desc_t* d, const gdn_attn_fwd_args_t* a, void* strea
   const Span out[] = {{a->o, size_t(P.S.rows) * P.S.H * P.S.D * 2}, {a->lse, size_t(P.S.rows) * P.S.H * 4}};
   if (alias(in, out)) return bad("o and lse must not alias the inputs or each other");
   if (!workspace_ok(a->workspace, a->workspace_bytes, attn_fwd_ws(P))) return bad("workspace missing, too small or not 256-byte aligned");
-  if ((rc = device_or_error(nullptr)) || (rc = bind_context())) return rc;
   AttnParams p = attn_params(d, P);
+  if ((rc = device_or_error(&p.sms)) || (rc = bind_context())) return rc;
   p.tiles = int(P.pairs);
   p.o = static_cast<bf*>(a->o);
   p.lse = a->lse;
@@ -327,9 +327,9 @@ int attn_bwd(const gdn_attn_desc_t* d, const gdn_attn_bwd_args_t* a, void* strea
   if (alias(in, out)) return bad("the gradients must not alias the inputs or each other");
   const AttnBwdLayout l = layout_attn_bwd(P);
   if (!workspace_ok(a->workspace, a->workspace_bytes, l.total)) return bad("workspace missing, too small or not 256-byte aligned");
-  if ((rc = device_or_error(nullptr)) || (rc = bind_context())) return rc;
-  char* ws = static_cast<char*>(a->workspace);
   AttnParams p = attn_params(d, P);
+  if ((rc = device_or_error(&p.sms)) || (rc = bind_context())) return rc;
+  char* ws = static_cast<char*>(a->workspace);
   p.tiles = int(P.tiles);
   p.dO = static_cast<cbf*>(a->dO);
   p.o_in = static_cast<cbf*>(a->o);

@@ -33,9 +33,6 @@ struct Cfg {
   static constexpr int kSmem = 7 * kTile + 2 * 1024 + 512;  // 2 fixed tiles, rings of 3 and 2, two stages of vectors, barriers
 };
 
-// Column of k-step s of a bf16 operand that lies in two halves over 128 columns.
-__device__ __forceinline__ uint32_t half_col(int s) { return uint32_t(s < 4 ? s * 8 : 64 + (s - 4) * 8); }
-
 // 64 columns of x, rounded to bf16, to 32 columns of TMEM.
 __device__ __forceinline__ void store_operand(uint32_t t, const float* x) {
   float w[32];
@@ -151,14 +148,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (; it < n; ++it) {
         const int h = hk * p.group + it / per, q0 = (i0 + it % per) * kAttnTile, y = tl.row0 + q0, qs = slot(it, kQ), os = slot(it, kO);
-        if (it >= kQ) ok = mbar_wait(&q_empty[qs], phase(it - kQ, kQ), abort_flag, p.status, kDevTimeoutMma);
+        if (it >= kQ) ok = attn_wait(&q_empty[qs], phase(it - kQ, kQ), abort_flag, p.status, kDevTimeoutMma);
         if (ok && lane == 0) {
           mbar_expect_tx(&q_full[qs], kTile);
           load_attn_tile<D>(sQ + qs * kTile, &mq, h * D, y, &q_full[qs]);
         }
         if (ok && it >= kO)
-          ok = mbar_wait(&o_empty[os], phase(it - kO, kO), abort_flag, p.status, kDevTimeoutMma) &&
-               mbar_wait(&vec_free[os], phase(it - kO, kO), abort_flag, p.status, kDevTimeoutSync);
+          ok = attn_wait(&o_empty[os], phase(it - kO, kO), abort_flag, p.status, kDevTimeoutMma) &&
+               attn_wait(&vec_free[os], phase(it - kO, kO), abort_flag, p.status, kDevTimeoutSync);
         if (ok && lane == 0) {
           mbar_expect_tx(&o_full[os], kTile);
           load_attn_tile<D>(sO + os * kTile, &mdo, h * D, y, &o_full[os]);
@@ -173,8 +170,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           v[128 + e] = in ? p.delta[at + e] : 0.f;
         }
         if (ragged && q0 + kAttnTile > tl.len) {
-          ok = mbar_wait(&q_full[qs], phase(it, kQ), abort_flag, p.status, kDevTimeoutTma) &&
-               mbar_wait(&o_full[os], phase(it, kO), abort_flag, p.status, kDevTimeoutTma);
+          ok = attn_wait(&q_full[qs], phase(it, kQ), abort_flag, p.status, kDevTimeoutTma) &&
+               attn_wait(&o_full[os], phase(it, kO), abort_flag, p.status, kDevTimeoutTma);
           if (!__all_sync(0xffffffffu, ok)) break;
           zero_attn_rows<D>(sQ + qs * kTile, tl.len - q0, lane);
           zero_attn_rows<D>(sO + os * kTile, tl.len - q0, lane);
@@ -192,24 +189,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 8 && lane == 0) {
       // ---------------- MMA issuer ----------------
-      constexpr uint32_t idS = idesc_bf16(128, 128), idO = idesc_bf16(128, D, false, true);
-      const uint32_t aK = smem_u32(sK), aV = smem_u32(sV), bQ = smem_u32(sQ), bO = smem_u32(sO);
-      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return mbar_wait(b, ph, abort_flag, p.status, code); };
+      const uint32_t aK = desc_low_k(smem_u32(sK)), aV = desc_low_k(smem_u32(sV)), bQ = desc_low_k(smem_u32(sQ)), bO = desc_low_k(smem_u32(sO)),
+                     nQ = desc_low_mn(smem_u32(sQ), kAttnPanel), nO = desc_low_mn(smem_u32(sO), kAttnPanel);
+      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
       auto scores = [&](int it) {
         if (!wait(&q_full[slot(it, kQ)], phase(it, kQ), kDevTimeoutTma) || !wait(&ready[slot(it, kO)], phase(it, kO), kDevTimeoutSync)) return false;
         tc_fence_after();
-        const uint32_t b = bQ + slot(it, kQ) * kTile;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) mma_bf16_ss(tS, desc_kmajor(aK, kAttnPanel, s), desc_kmajor(b, kAttnPanel, s), idS, s > 0);
+        product_ss<D>(1u, tS, aK, bQ + slot(it, kQ) * (kTile >> 4));
         mma_commit(s_full);
         return true;
       };
       auto dprobs = [&](int it) {
         if (!wait(&o_full[slot(it, kO)], phase(it, kO), kDevTimeoutTma)) return false;
         tc_fence_after();
-        const uint32_t b = bO + slot(it, kO) * kTile;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) mma_bf16_ss(tP, desc_kmajor(aV, kAttnPanel, s), desc_kmajor(b, kAttnPanel, s), idS, s > 0);
+        product_ss<D>(1u, tP, aV, bO + slot(it, kO) * (kTile >> 4));
         mma_commit(dp_full);
         return true;
       };
@@ -218,16 +211,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(p_ready, it & 1, kDevTimeoutSync);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t o = bO + slot(it, kO) * kTile, q = bQ + slot(it, kQ) * kTile;
-#pragma unroll
-        for (int s = 0; s < kAttnTile / 16; ++s) mma_bf16_ts(tV, tS + half_col(s), desc_mnmajor_bf16(o, kAttnPanel, s), idO, it > 0 || s > 0);
+        product_ts<D>(1u, tV, tS, 64, nO + slot(it, kO) * (kTile >> 4), it > 0);
         mma_commit(&o_empty[slot(it, kO)]);
         if (it + 1 < n && !(ok = scores(it + 1))) break;
         ok = wait(ds_ready, it & 1, kDevTimeoutSync);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
-        for (int s = 0; s < kAttnTile / 16; ++s) mma_bf16_ts(tK, tP + half_col(s), desc_mnmajor_bf16(q, kAttnPanel, s), idO, it > 0 || s > 0);
+        product_ts<D>(1u, tK, tP, 64, nQ + slot(it, kQ) * (kTile >> 4), it > 0);
         mma_commit(&q_empty[slot(it, kQ)]);
         if (it + 1 < n) ok = dprobs(it + 1);
       }
@@ -244,8 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = 0; it < n && ok; ++it) {
       const int q0 = (i0 + it % per) * kAttnTile + half * 64, os = slot(it, kO);
       const float4 *lse = reinterpret_cast<const float4*>(vec + os * 256 + half * 64), *delta = lse + 32;
-      ok = mbar_wait(&ready[os], phase(it, kO), abort_flag, p.status, kDevTimeoutSync) &&
-           mbar_wait(s_full, it & 1, abort_flag, p.status, kDevTimeoutMma);
+      ok = attn_wait(&ready[os], phase(it, kO), abort_flag, p.status, kDevTimeoutSync) &&
+           attn_wait(s_full, it & 1, abort_flag, p.status, kDevTimeoutMma);
       if (!ok) break;
       tc_fence_after();
       float w[64];
@@ -270,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(p_ready);
-      ok = mbar_wait(dp_full, it & 1, abort_flag, p.status, kDevTimeoutMma);
+      ok = attn_wait(dp_full, it & 1, abort_flag, p.status, kDevTimeoutMma);
       if (!ok) break;
       tc_fence_after();
       float d[64];
@@ -289,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(ds_ready);
     }
-    if (ok && mbar_wait(done, 0, abort_flag, p.status, kDevTimeoutMma)) {
+    if (ok && attn_wait(done, 0, abort_flag, p.status, kDevTimeoutMma)) {
       tc_fence_after();
       __nv_bfloat16* dst = (half ? p.dk : p.dv) + ((size_t(tl.row0) + key) * p.Hk + hk) * D;
       const uint32_t acc = (half ? tK : tV) + tmem_lane_base(warp);
@@ -351,10 +341,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_attn_tile<D>(sO, &mdo, h * D, tl.row0 + tl.first, q_full);
         for (; it < n; ++it) {
           const int ks = slot(it, kK), vs = slot(it, kV), y = tl.row0 + it * kAttnTile;
-          if (it >= kK && !mbar_wait(&k_empty[ks], phase(it - kK, kK), abort_flag, p.status, kDevTimeoutMma)) break;
+          if (it >= kK && !attn_wait(&k_empty[ks], phase(it - kK, kK), abort_flag, p.status, kDevTimeoutMma)) break;
           mbar_expect_tx(&k_full[ks], kTile);
           load_attn_tile<D>(sK + ks * kTile, &mk, hk * D, y, &k_full[ks]);
-          if (it >= kV && !mbar_wait(&v_empty[vs], phase(it - kV, kV), abort_flag, p.status, kDevTimeoutMma)) {
+          if (it >= kV && !attn_wait(&v_empty[vs], phase(it - kV, kV), abort_flag, p.status, kDevTimeoutMma)) {
             mbar_drain(&k_full[ks], phase(it, kK));
             break;
           }
@@ -368,32 +358,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       it = __shfl_sync(0xffffffffu, it, 0);
-      if (tail && it == n && mbar_wait(&k_full[slot(n - 1, kK)], phase(n - 1, kK), abort_flag, p.status, kDevTimeoutTma)) {
+      if (tail && it == n && attn_wait(&k_full[slot(n - 1, kK)], phase(n - 1, kK), abort_flag, p.status, kDevTimeoutTma)) {
         zero_attn_rows<D>(sK + slot(n - 1, kK) * kTile, tl.len - (n - 1) * kAttnTile, lane);
         fence_async_smem();
         mbar_arrive(tail_ready);
       }
     } else if (warp == 8 && lane == 0) {
       // ---------------- MMA issuer ----------------
-      constexpr uint32_t idS = idesc_bf16(128, 128), idO = idesc_bf16(128, D, false, true);
-      const uint32_t aQ = smem_u32(sQ), aO = smem_u32(sO), bK = smem_u32(sK), bV = smem_u32(sV);
-      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return mbar_wait(b, ph, abort_flag, p.status, code); };
+      const uint32_t aQ = desc_low_k(smem_u32(sQ)), aO = desc_low_k(smem_u32(sO)), bK = desc_low_k(smem_u32(sK)), bV = desc_low_k(smem_u32(sV)),
+                     nK = desc_low_mn(smem_u32(sK), kAttnPanel);
+      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
       auto scores = [&](int i) {
         if (!wait(&k_full[slot(i, kK)], phase(i, kK), kDevTimeoutTma)) return false;
         if (tail && i + 1 == n && !wait(tail_ready, 0, kDevTimeoutSync)) return false;
         tc_fence_after();
-        const uint32_t b = bK + slot(i, kK) * kTile;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) mma_bf16_ss(tS(i), desc_kmajor(aQ, kAttnPanel, s), desc_kmajor(b, kAttnPanel, s), idS, s > 0);
+        product_ss<D>(1u, tS(i), aQ, bK + slot(i, kK) * (kTile >> 4));
         mma_commit(&s_full[i & 1]);
         return true;
       };
       auto dprobs = [&](int i) {
         if (!wait(&v_full[slot(i, kV)], phase(i, kV), kDevTimeoutTma)) return false;
         tc_fence_after();
-        const uint32_t b = bV + slot(i, kV) * kTile;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) mma_bf16_ss(tP, desc_kmajor(aO, kAttnPanel, s), desc_kmajor(b, kAttnPanel, s), idS, s > 0);
+        product_ss<D>(1u, tP, aO, bV + slot(i, kV) * (kTile >> 4));
         mma_commit(dp_full);
         mma_commit(&v_empty[slot(i, kV)]);
         return true;
@@ -404,9 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (i + 1 < n && !(ok = dprobs(i + 1))) break;
-        const uint32_t b = bK + slot(i, kK) * kTile;
-#pragma unroll
-        for (int s = 0; s < kAttnTile / 16; ++s) mma_bf16_ts(tQ, tS(i) + half_col(s), desc_mnmajor_bf16(b, kAttnPanel, s), idO, i > 0 || s > 0);
+        product_ts<D>(1u, tQ, tS(i), 64, nK + slot(i, kK) * (kTile >> 4), i > 0);
         mma_commit(&k_empty[slot(i, kK)]);
         if (i + 2 < n) ok = scores(i + 2);
       }
@@ -423,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const F2 c2 = dup2(p.scale * kLog2e), lse = dup2(mine ? -p.lse2[at] : 0.f), delta = dup2(mine ? -p.delta[at] : 0.f);
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
-      ok = mbar_wait(&s_full[i & 1], (i >> 1) & 1, abort_flag, p.status, kDevTimeoutMma);
+      ok = attn_wait(&s_full[i & 1], (i >> 1) & 1, abort_flag, p.status, kDevTimeoutMma);
       if (!ok) break;
       tc_fence_after();
       float w[64], d[64];
@@ -436,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w[2 * e] = exp2_approx(a);
         w[2 * e + 1] = exp2_approx(b);
       }
-      ok = mbar_wait(dp_full, i & 1, abort_flag, p.status, kDevTimeoutMma);
+      ok = attn_wait(dp_full, i & 1, abort_flag, p.status, kDevTimeoutMma);
       if (!ok) break;
       tc_fence_after();
       tmem_ld64(tP + lb, d);
@@ -455,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(ds_ready);
     }
-    if (ok && mbar_wait(done, 0, abort_flag, p.status, kDevTimeoutMma)) {
+    if (ok && attn_wait(done, 0, abort_flag, p.status, kDevTimeoutMma)) {
       tc_fence_after();
       __nv_bfloat16* dst = p.dq + ((size_t(tl.row0) + qi) * p.H + h) * D + half * (D / 2);
 #pragma unroll

@@ -5,17 +5,23 @@
 // in one pass over the keys: with a running reference m (log2 units below), weights p = 2^(c s - m), their sum l and the
 // weighted sum of v are kept, and o = sum / l at the end.
 //
-// One CTA takes 256 queries of one head as two tiles of 128. A tile's row of scores belongs to one thread (TMEM lane = row), so
-// the softmax needs no shuffles. The two tiles alternate on the tensor core: while one tile's 128 threads turn scores into
-// weights, the other's products run.
+// A CTA takes 256 queries of one head at a time, as two tiles of 128, and goes through such items in turn. A tile's row of scores
+// belongs to one thread (TMEM lane = row), so the softmax needs no shuffles. The two tiles alternate on the tensor core: while
+// one tile's 128 threads turn scores into weights, the other's products run.
 //   S_t = Q_t K_j^T        128 x 128 x D, operands in shared memory (128-byte swizzle, by TMA)
 //   O_t += P_t V_j         128 x D x 128, P_t bf16 in TMEM over S_t's columns (the A operand), V_j read MN-major
-// TMEM: S_0, S_1, O_0, O_1. Keys and values come through one ring of stages. Weights are rounded to bf16 (2^-9 relative, the
+// TMEM: S_0, S_1, O_0, O_1. Keys and values come through one ring of stages. Weights are rounded to bf16 (2^-8 relative at most, the
 // type of v and o); scores, sums and the accumulators are fp32.
 //
-// The reference m is the first tile's row maximum and moves only when a later one lies more than 2^8 above it (then the
-// accumulator and l are rescaled): weights up to 256 cost no precision in bf16 or fp32, and almost no tile needs the rescaling.
-// It needs no wait: the commit that announces S_t(j) also covers the product O_t(j - 1) issued before it.
+// What bounds it: the tensor core, and the time its issuing thread spends on anything else. An instruction is taken only when the
+// one before it is nearly done, and every wait, even for a phase long past, costs about 130 cycles in which the core soon
+// idles (measured; a tile's two products take 1024). So the issuing thread waits once per tile and iteration, on a barrier on which both the
+// tile's 128 softmax threads and a gate thread arrive, the latter when the K and V tiles needed next have landed.
+//
+// The reference m moves only when a row's maximum lies more than 2^8 above it (then l and the accumulator are rescaled):
+// weights up to 256 cost no precision in bf16 or fp32, almost no tile needs it, and the weights can be taken against the reference at
+// hand while the maximum is still being looked for. It needs no wait: the commit that announces S_t(j) also covers the
+// product O_t(j - 1) issued before it.
 //
 // Keys past the sequence's end are masked in the scores, and the last tile's values past it are zeroed in shared memory: they
 // belong to the next sequence, and 0 x NaN would carry a neighbour's NaN over.
@@ -24,7 +30,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 384;  // 8 softmax warps, the MMA warp, the TMA warp and two that only give their registers
+constexpr int kThreads = 384;  // 8 softmax warps, the MMA warp, the TMA warp and a gate warp for either tile
 // The launch's 168 registers a thread (12 warps x 168 x 32 = 64512) are shared out anew: 208 for the softmax's rows of 128 scores,
 // 88 for the rest (8 x 208 + 4 x 88 = 12 x 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -37,10 +43,28 @@ struct Cfg {
   static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes;
 };
 
-template <int D>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* m, int x, int y, uint64_t* bar) {
-  mbar_expect_tx(bar, Cfg<D>::kTileBytes);
-  load_attn_tile<D>(dst, m, x, y, bar);
+// The CTA's item of a round, most work first: every other round the other way round, so that the CTAs' sums of work come out
+// alike. False where the last round has none for it.
+struct Item {
+  int h, hk, n[2], most;  // head and key head; key tiles of either query tile (the second sees no fewer, or has no rows)
+  bool tail;              // the last key tile reaches past the sequence
+  AttnTile tl;
+};
+__device__ __forceinline__ bool item_of(const AttnParams& p, long long round, long long total, Item* it) {
+  const long long i = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  if (i >= total) return false;
+  it->h = int(i % p.H);
+  it->hk = it->h / p.group;
+  it->tl = attn_tile(p, int(i / p.H), kAttnPair, false);
+  const int all = (it->tl.len + kAttnTile - 1) / kAttnTile;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int q0 = it->tl.first + t * kAttnTile;
+    it->n[t] = q0 >= it->tl.len ? 0 : p.causal ? q0 / kAttnTile + 1 : all;
+  }
+  it->most = max(it->n[0], it->n[1]);
+  it->tail = it->most * kAttnTile > it->tl.len;
+  return true;
 }
 
 }  // namespace
@@ -49,131 +73,166 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnParams p) {
   using C = Cfg<D>;
+  constexpr int kS = C::kStages, kTile = C::kTileBytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sKV = sm + 2 * C::kTileBytes;
-  __shared__ uint64_t q_full[2], kv_full[C::kStages], kv_empty[C::kStages], s_full[2], p_full[2], o_full[2], tail_ready, drained;
+  uint8_t* sKV = sm + 2 * kTile;
+  __shared__ uint64_t q_full[2], q_empty[2], kv_full[kS], kv_empty[kS], zeroed[kS], s_full[2], p_full[2], o_full[2], drained;
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x % p.H, hk = h / p.group;
-  wait_for_previous();
-  const AttnTile tl = attn_tile(p, blockIdx.x / p.H, kAttnPair, false);
-  const int all = (tl.len + kAttnTile - 1) / kAttnTile;
-  int n[2];  // key tiles of either query tile; the second sees no fewer, or has no rows
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int q0 = tl.first + t * kAttnTile;
-    n[t] = q0 >= tl.len ? 0 : p.causal ? q0 / kAttnTile + 1 : all;
-  }
-  const int most = max(n[0], n[1]), last_tile = n[1] > 0 ? 1 : 0;
-  const bool tail = most * kAttnTile > tl.len;
-
+  const long long total = (long long)p.tiles * p.H, rounds = (total + gridDim.x - 1) / gridDim.x;
   if (warp == 8) tmem_alloc(&tslot, 512);
   if (tid == 0) {
     abort_flag = 0;
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
+      mbar_init(&q_empty[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], kAttnTile);
+      mbar_init(&p_full[t], kAttnTile + 1);
       mbar_init(&o_full[t], 1);
     }
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < kS; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
+      mbar_init(&zeroed[i], 32);
     }
-    mbar_init(&tail_ready, 32);
     mbar_init(&drained, 1);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tb = tslot;
-  // S_t at 128 t, O_t at 256 + D t
-  auto tS = [&](int t) { return tb + uint32_t(t) * 128; };
-  auto tO = [&](int t) { return tb + 256 + uint32_t(t) * D; };
+  wait_for_previous();
+  // All of TMEM, so it starts at column 0: S_t at 128 t, O_t at 256 + D t.
+  auto tS = [&](int t) { return uint32_t(t) * 128; };
+  auto tO = [&](int t) { return 256 + uint32_t(t) * D; };
+  auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, &abort_flag, p.status, code); };
+  Item it;
 
   if (warp >= 8) {
     regs_dec<kOtherRegs>();
     if (warp == 9) {
       // ---------------- producer: Q, then K and V tile by tile through the ring ----------------
+      Ring<kS, 1> r(0);
+      int use = 0;                   // tiles requested through the ring
+      uint32_t q_use[2] = {0, 0};    // items whose tile t has rows
       bool ok = true;
-      if (lane == 0) {
-        load_tile<D>(sm, &mq, h * D, tl.row0 + tl.first, &q_full[0]);
-        if (n[1]) load_tile<D>(sm + C::kTileBytes, &mq, h * D, tl.row0 + tl.first + kAttnTile, &q_full[1]);
-        for (int i = 0; i < 2 * most; ++i) {
-          const int st = i % C::kStages, use = i / C::kStages;
-          if (use > 0 && !mbar_wait(&kv_empty[st], (use - 1) & 1, &abort_flag, p.status, kDevTimeoutMma)) {
-            // the copies in flight land before their destination is given up
-            for (int k = max(0, i - C::kStages); k < i; ++k) mbar_drain(&kv_full[k % C::kStages], (k / C::kStages) & 1);
-            for (int t = 0; t < 1 + last_tile; ++t) mbar_drain(&q_full[t], 0);
-            ok = false;
-            break;
+      for (long long rd = 0; rd < rounds && ok; ++rd) {
+        if (!item_of(p, rd, total, &it)) break;
+        for (int i = 0; i < 2 * it.most && ok; ++i, ++use, r.next()) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (i != t || !it.n[t]) continue;  // Q_0 ahead of the first K, Q_1 behind it
+            ok = q_use[t] == 0 || wait(&q_empty[t], (q_use[t] - 1) & 1, kDevTimeoutMma);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) {
+              mbar_expect_tx(&q_full[t], kTile);
+              load_attn_tile<D>(sm + t * kTile, &mq, it.h * D, it.tl.row0 + it.tl.first + t * kAttnTile, &q_full[t]);
+            }
+            ++q_use[t];
           }
-          load_tile<D>(sKV + st * C::kTileBytes, i & 1 ? &mv : &mk, hk * D, tl.row0 + (i >> 1) * kAttnTile, &kv_full[st]);
+          ok = ok && (use < kS || wait(&kv_empty[r.at], r.phase ^ 1u, kDevTimeoutMma));
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          uint8_t* dst = sKV + r.at * kTile;
+          if (lane == 0) {
+            mbar_expect_tx(&kv_full[r.at], kTile);
+            load_attn_tile<D>(dst, i & 1 ? &mv : &mk, it.hk * D, it.tl.row0 + (i >> 1) * kAttnTile, &kv_full[r.at]);
+          }
+          if (it.tail && i == 2 * it.most - 1) {
+            ok = __all_sync(0xffffffffu, wait(&kv_full[r.at], r.phase, kDevTimeoutTma));
+            if (!ok) break;
+            zero_attn_rows<D>(dst, it.tl.len - (it.most - 1) * kAttnTile, lane);
+            fence_async_smem();
+            mbar_arrive(&zeroed[r.at]);
+          }
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (tail && ok) {
-        const int i = 2 * most - 1, st = i % C::kStages;
-        if (mbar_wait(&kv_full[st], (i / C::kStages) & 1, &abort_flag, p.status, kDevTimeoutTma)) {
-          zero_attn_rows<D>(sKV + st * C::kTileBytes, tl.len - (most - 1) * kAttnTile, lane);
-          fence_async_smem();
-          mbar_arrive(&tail_ready);
-        }
+      if (!ok && lane == 0) {  // the copies in flight land before their destination is given up
+        for (int k = max(0, use - kS + 1); k < use; ++k) mbar_drain(&kv_full[k % kS], (k / kS) & 1);
+        mbar_drain(&kv_full[r.at], r.phase, 1000000ull);  // this one if it was requested
+        for (int t = 0; t < 2; ++t)
+          if (q_use[t]) mbar_drain(&q_full[t], (q_use[t] - 1) & 1);
       }
     } else if (warp == 8) {
       // ---------------- MMA issuer ----------------
-      if (lane == 0) {
-        constexpr uint32_t idS = idesc_bf16(128, 128), idO = idesc_bf16(128, D, false, true);
-        const uint32_t sQ = smem_u32(sm), kv = smem_u32(sKV);
-        auto full = [&](int i) { return mbar_wait(&kv_full[i % C::kStages], (i / C::kStages) & 1, &abort_flag, p.status, kDevTimeoutTma); };
-        auto tile = [&](int i) { return kv + uint32_t(i % C::kStages) * C::kTileBytes; };
-        auto scores = [&](int t, int j) {
-          const uint32_t a = sQ + t * C::kTileBytes, b = tile(2 * j);
+      const uint32_t lead = elect_lead();
+      const uint32_t q = desc_low_k(smem_u32(sm)), kk = desc_low_k(smem_u32(sKV)), vv = desc_low_mn(smem_u32(sKV), kAttnPanel);
+      Ring<kS, 2> rk(0), rv(1);
+      uint32_t cnt[2] = {0, 0}, q_use[2] = {0, 0};  // iterations and items of either tile so far
+      bool ok = true;
+      auto all_wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, wait(b, ph, code))); };
+      auto scores = [&](int t, bool last) {
+        product_ss<D>(lead, uint32_t(t) * 128, q + t * (kTile >> 4), kk + rk.at * (kTile >> 4));
+        commit(lead, &s_full[t]);
+        if (last) commit(lead, &q_empty[t]);
+      };
+      auto outputs = [&](int t, int j) {
+        if (!all_wait(&p_full[t], cnt[t] & 1, kDevTimeoutSync)) return false;
+        ++cnt[t];
+        tc_fence_after();
+        product_ts<D>(lead, 256 + uint32_t(t) * D, uint32_t(t) * 128, 32, vv + rv.at * (kTile >> 4), j > 0);
+        return true;
+      };
+      for (long long rd = 0; rd < rounds && ok; ++rd) {
+        if (!item_of(p, rd, total, &it)) break;
+        // A tile's first scores overwrite the weights of the item before it, which the products issued so far have read; its first
+        // output product waits for weights from threads that have taken the item's output out before.
+        ok = all_wait(&kv_full[rk.at], rk.phase, kDevTimeoutTma);
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s) mma_bf16_ss(tS(t), desc_kmajor(a, kAttnPanel, s), desc_kmajor(b, kAttnPanel, s), idS, s > 0);
-          mma_commit(&s_full[t]);
-          if (t == last_tile) mma_commit(&kv_empty[(2 * j) % C::kStages]);
-        };
-        auto outputs = [&](int t, int j) {
-          const uint32_t b = tile(2 * j + 1);
-#pragma unroll
-          for (int s = 0; s < kAttnTile / 16; ++s) mma_bf16_ts(tO(t), tS(t) + s * 8, desc_mnmajor_bf16(b, kAttnPanel, s), idO, j > 0 || s > 0);
-          if (t == last_tile) mma_commit(&kv_empty[(2 * j + 1) % C::kStages]);
-          if (j + 1 == n[t]) mma_commit(&o_full[t]);
-        };
-        bool ok = full(0);
-        for (int t = 0; t < 2 && ok; ++t)
-          if (n[t]) {
-            ok = mbar_wait(&q_full[t], 0, &abort_flag, p.status, kDevTimeoutTma);
-            if (ok) scores(t, 0);
-          }
-        for (int j = 0; j < most && ok; ++j) {
-          ok = full(2 * j + 1);
-          if (ok && tail && j + 1 == most) ok = mbar_wait(&tail_ready, 0, &abort_flag, p.status, kDevTimeoutSync);
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (j >= n[t]) continue;
-            if (!mbar_wait(&p_full[t], j & 1, &abort_flag, p.status, kDevTimeoutSync)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            outputs(t, j);
-            if (j + 1 < n[t]) {
-              if (!full(2 * j + 2)) {
-                ok = false;
-                break;
-              }
-              scores(t, j + 1);
-            }
-          }
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || !it.n[t]) continue;
+          ok = all_wait(&q_full[t], q_use[t]++ & 1, kDevTimeoutTma);
+          if (ok) scores(t, it.n[t] == 1);
         }
-        if (!ok) {  // the products in flight end before their accumulators are given up
-          mma_commit(&drained);
-          mbar_drain(&drained, 0);
+        for (int j = 0; j < it.most && ok; ++j) {
+          rk.next();
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || j >= it.n[t]) continue;
+            if (!(ok = outputs(t, j))) break;
+            if (j + 1 < it.n[t]) scores(t, j + 2 == it.n[t]);
+            else commit(lead, &o_full[t]);
+          }
+          rv.next();
+        }
+      }
+      if (!ok) {  // the products in flight end before their accumulators are given up
+        commit(lead, &drained);
+        mbar_drain(&drained, 0);
+      }
+    } else if (warp >= 10 && lane == 0) {
+      // ---------------- gate of a tile: the tiles that the products behind its weights read have landed ----------------
+      const int t = warp - 10;
+      Ring<kS, 2> rk(0), rv(1);
+      uint32_t cnt = 0, outs = 0, zeros = 0;  // iterations and items so far; a bit per stage, the phase of its next zeroing
+      bool ok = true;
+      for (long long rd = 0; rd < rounds && ok; ++rd) {
+        if (!item_of(p, rd, total, &it)) break;
+        const bool frees = t == 1 || !it.n[1];  // this tile's products are the last to read a stage
+        for (int j = 0; j < it.most && ok; ++j) {
+          const int k = rk.at, v = rv.at;
+          const uint32_t v_phase = rv.phase;
+          rk.next();
+          rv.next();
+          if (it.tail && j + 1 == it.most) zeros ^= 1u << v;
+          if (j >= it.n[t]) continue;
+          ok = wait(&kv_full[v], v_phase, kDevTimeoutTma) && (j + 1 == it.n[t] || wait(&kv_full[rk.at], rk.phase, kDevTimeoutTma)) &&
+               (!it.tail || j + 1 < it.most || wait(&zeroed[v], ~zeros >> v & 1u, kDevTimeoutSync));
+          if (!ok) break;
+          mbar_arrive(&p_full[t]);
+          // weights j are there: their scores are done, and the output product of the weights before them
+          ok = wait(&p_full[t], cnt++ & 1, kDevTimeoutSync);
+          if (!ok) break;
+          if (frees) {
+            mbar_arrive(&kv_empty[k]);
+            if (j > 0) mbar_arrive(&kv_empty[v >= 2 ? v - 2 : v - 2 + kS]);
+          }
+          if (j + 1 == it.n[t]) {
+            ok = wait(&o_full[t], outs++ & 1, kDevTimeoutMma);
+            if (ok && frees) mbar_arrive(&kv_empty[v]);
+          }
         }
       }
     }
@@ -182,82 +241,87 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_inc<kSoftmaxRegs>();
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lb = tmem_lane_base(warp);
-    const int qi = tl.first + t * kAttnTile + row;  // in the sequence
-    const float c = p.scale * kLog2e, far = kRescale / c;
+    const float c = p.scale * kLog2e, far = fminf(kRescale / c, 3e38f);
     const F2 c2 = dup2(c);
-    float m = -INFINITY;
-    F2 l2 = dup2(0.f);
+    uint32_t cnt = 0, outs = 0;
     bool ok = true;
-    for (int j = 0; j < n[t]; ++j) {
-      if (!mbar_wait(&s_full[t], j & 1, &abort_flag, p.status, kDevTimeoutMma)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      float s[128];
-      tmem_ld64(tS(t) + lb, s);
-      tmem_ld64(tS(t) + lb + 64, s + 64);
-      tmem_wait_ld_regs(s);
-      const int k0 = j * kAttnTile;
-      if (k0 + kAttnTile > tl.len || (p.causal && k0 + kAttnTile > tl.first + t * kAttnTile)) {
-        const int seen = (p.causal ? min(qi + 1, tl.len) : tl.len) - k0;
+    for (long long rd = 0; rd < rounds && ok; ++rd) {
+      if (!item_of(p, rd, total, &it)) break;
+      const int mine = it.n[t], len = it.tl.len, qi = it.tl.first + t * kAttnTile + row;  // in the sequence
+      if (mine == 0) continue;
+      float m = -INFINITY;
+      F2 l2 = dup2(0.f);
+      for (int j = 0; j < mine; ++j) {
+        if (!(ok = wait(&s_full[t], cnt++ & 1, kDevTimeoutMma))) break;
+        tc_fence_after();
+        // Weights against the reference at hand, and the row's maximum beside them (the two run on different units): only where
+        // that lies too far above the reference does it move, and the weights are taken again from the scores in TMEM.
+        const F2 before = l2;
+        float w[64];
+#pragma unroll 1
+        while (true) {
+          float s[128];
+          tmem_ld64(tS(t) + lb, s);
+          tmem_ld64(tS(t) + lb + 64, s + 64);
+          tmem_wait_ld_regs(s);
+          if (j + 1 == mine && (p.causal || it.tail)) {
+            const int seen = (p.causal ? min(qi + 1, len) : len) - j * kAttnTile;
 #pragma unroll
-        for (int e = 0; e < 128; ++e)
-          if (e >= seen) s[e] = -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+            for (int e = 0; e < 128; ++e)
+              if (e >= seen) s[e] = -INFINITY;
+          }
+          if (j == 0) {
+            float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int e = 4; e < 128; e += 8)
+            for (int e = 4; e < 124; e += 8)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = e + 4 + u < 128 ? fmaxf(fmaxf(mx[u], s[e + u]), s[e + 4 + u]) : fmaxf(mx[u], s[e + u]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (j == 0) {
-        m = top;
-      } else if (__any_sync(0xffffffffu, top > m + far)) {
-        const float next = fmaxf(m, top), f = next == -INFINITY ? 1.f : exp2_approx((m - next) * c);
-        m = next;
-        l2 = mul2(l2, dup2(f));
+              for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[e + u], s[e + 4 + u]);
+            m = max3(max3(mx[0], mx[1], s[124]), max3(mx[2], mx[3], s[125]), fmaxf(s[126], s[127]));
+          }
+          const F2 mc = dup2(-m * c);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          float o[32];
-          tmem_ld32(tO(t) + lb + q * 32, o);
-          tmem_wait_ld_regs(o);
+          for (int e = 0; e < 64; ++e) {
+            float a, b;
+            mx[e & 3] = max3(mx[e & 3], s[2 * e], s[2 * e + 1]);
+            unf2(fma2(f2(s[2 * e], s[2 * e + 1]), c2, mc), &a, &b);
+            a = exp2_approx(a);
+            b = exp2_approx(b);
+            l2 = add2(l2, f2(a, b));
+            w[e] = __uint_as_float(pack_bf16(a, b));
+          }
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          if (!__any_sync(0xffffffffu, top > m + far)) break;
+          const float next = fmaxf(m, top), f = next == -INFINITY ? 1.f : exp2_approx((m - next) * c);
+          m = next;
+          l2 = mul2(before, dup2(f));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= f;
-          tmem_st32(tO(t) + lb + q * 32, o);
+          for (int q = 0; q < D / 32; ++q) {  // not in the first tile, whose reference is its maximum
+            float o[32];
+            tmem_ld32(tO(t) + lb + q * 32, o);
+            tmem_wait_ld_regs(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            tmem_st32(tO(t) + lb + q * 32, o);
+          }
         }
+        tmem_st32(tS(t) + lb, w);
+        tmem_st32(tS(t) + lb + 32, w + 32);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[t]);
       }
-      const F2 mc = dup2(-m * c);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float a, b;
-          unf2(fma2(f2(s[q * 32 + 2 * e], s[q * 32 + 2 * e + 1]), c2, mc), &a, &b);
-          a = exp2_approx(a);
-          b = exp2_approx(b);
-          l2 = add2(l2, f2(a, b));
-          w[e] = __uint_as_float(pack_bf16(a, b));
-        }
-        tmem_st16(tS(t) + lb + q * 16, w);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&p_full[t]);
-    }
-    if (ok && n[t] && mbar_wait(&o_full[t], 0, &abort_flag, p.status, kDevTimeoutMma)) {
+      if (!ok || !(ok = wait(&o_full[t], outs++ & 1, kDevTimeoutMma))) break;
       tc_fence_after();
       const float l = sum2(l2), r = 1.f / l;
-      const bool mine = qi < tl.len;
-      const size_t at = (size_t(tl.row0) + qi) * p.H + h;
-      if (mine) p.lse[at] = m * p.scale + logf(l);
+      const size_t at = (size_t(it.tl.row0) + qi) * p.H + it.h;
+      if (qi < len) p.lse[at] = m * p.scale + logf(l);
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         float o[32];
         tmem_ld32(tO(t) + lb + q * 32, o);
         tmem_wait_ld_regs(o);
-        if (mine)
+        if (qi < len)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float* x = o + 8 * e;
@@ -265,18 +329,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(pack_bf16(x[0] * r, x[1] * r), pack_bf16(x[2] * r, x[3] * r), pack_bf16(x[4] * r, x[5] * r), pack_bf16(x[6] * r, x[7] * r));
           }
       }
+      tc_fence_before();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tb, 512);
+  if (warp == 8) tmem_dealloc(tslot, 512);
 }
 
 template <int D>
 static cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(k_attn_fwd<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_after(k_attn_fwd<D>, dim3(p.tiles * p.H), dim3(kThreads), Cfg<D>::kSmem, s, mq, mk, mv, p);
+  const long long items = (long long)p.tiles * p.H;
+  return launch_after(k_attn_fwd<D>, dim3(unsigned(items < p.sms ? items : p.sms)), dim3(kThreads), Cfg<D>::kSmem, s, mq, mk, mv, p);
 }
 
 cudaError_t launch_attn_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, int D, const AttnParams& p, cudaStream_t s) {

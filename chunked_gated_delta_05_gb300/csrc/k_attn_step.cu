@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_step(const AttnStepParams 
       q[r][j] = make_uint4(0, 0, 0, 0);
       if (g + 8 * r < heads) q[r][j] = *reinterpret_cast<const uint4*>(p.q + b * p.q_stride + (head0 + g + 8 * r) * D + (c + 4 * j) * 8);
     }
-  const float cs = p.scale * kLog2e, far = kRescale / cs;
+  const float cs = p.scale * kLog2e, far = fminf(kRescale / cs, 3e38f);
   float m[kRows], l[kRows], o[kHalves][8][2 * kRows > 2 ? 4 : 2];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) m[r] = -INFINITY, l[r] = 0.f;
