@@ -23,7 +23,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 384;                        // 8 softmax warps, the MMA warp, the TMA warp, two that only give registers
+constexpr int kThreads = 384;                        // 8 softmax warps, the MMA warp, the TMA warp, two gate warps
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 8 x 208 + 4 x 88 = 12 x 168, the launch's
 constexpr int kSoftmax = 256;
 
@@ -125,15 +125,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kO; ++i) mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 1), mbar_init(&ready[i], 32), mbar_init(&vec_free[i], kSoftmax);
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    mbar_init(p_ready, kSoftmax);
-    mbar_init(ds_ready, kSoftmax);
+    mbar_init(p_ready, kSoftmax + 1);
+    mbar_init(ds_ready, kSoftmax + 1);
     mbar_init(done, 1);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tb = *tslot, tS = tb, tP = tb + 128, tV = tb + 256, tK = tb + 256 + D;
+  constexpr uint32_t tS = 0, tP = 128, tV = 256, tK = 256 + D;  // all of TMEM, so it starts at column 0
 
   if (warp >= 8) {
     regs_dec<kOtherRegs>();
@@ -187,42 +187,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_drain(&q_full[slot(it, kQ)], phase(it, kQ), 1000000ull);
         mbar_drain(&o_full[slot(it, kO)], phase(it, kO), 1000000ull);
       }
-    } else if (warp == 8 && lane == 0) {
+    } else if (warp == 8) {
       // ---------------- MMA issuer ----------------
+      const uint32_t lead = elect_lead();
       const uint32_t aK = desc_low_k(smem_u32(sK)), aV = desc_low_k(smem_u32(sV)), bQ = desc_low_k(smem_u32(sQ)), bO = desc_low_k(smem_u32(sO)),
                      nQ = desc_low_mn(smem_u32(sQ), kAttnPanel), nO = desc_low_mn(smem_u32(sO), kAttnPanel);
-      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
-      auto scores = [&](int it) {
-        if (!wait(&q_full[slot(it, kQ)], phase(it, kQ), kDevTimeoutTma) || !wait(&ready[slot(it, kO)], phase(it, kO), kDevTimeoutSync)) return false;
-        tc_fence_after();
-        product_ss<D>(1u, tS, aK, bQ + slot(it, kQ) * (kTile >> 4));
-        mma_commit(s_full);
-        return true;
+      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, attn_wait(b, ph, abort_flag, p.status, code))); };
+      auto scores = [&](int at) {
+        product_ss<D>(lead, tS, aK, bQ + at * (kTile >> 4));
+        commit(lead, s_full);
       };
-      auto dprobs = [&](int it) {
-        if (!wait(&o_full[slot(it, kO)], phase(it, kO), kDevTimeoutTma)) return false;
-        tc_fence_after();
-        product_ss<D>(1u, tP, aV, bO + slot(it, kO) * (kTile >> 4));
-        mma_commit(dp_full);
-        return true;
+      auto dprobs = [&](int at) {
+        product_ss<D>(lead, tP, aV, bO + at * (kTile >> 4));
+        commit(lead, dp_full);
       };
-      bool ok = wait(kv_full, 0, kDevTimeoutTma) && scores(0) && dprobs(0);
+      Ring<kQ, 1> rq(0);
+      bool ok = wait(kv_full, 0, kDevTimeoutTma) && wait(&q_full[0], 0, kDevTimeoutTma) && wait(&ready[0], 0, kDevTimeoutSync);
+      if (ok) scores(0);
+      ok = ok && wait(&o_full[0], 0, kDevTimeoutTma);
+      if (ok) dprobs(0);
       for (int it = 0; it < n && ok; ++it) {
-        ok = wait(p_ready, it & 1, kDevTimeoutSync);
-        if (!ok) break;
+        // the gates answer for the tiles of the products that follow either operand
+        if (!(ok = wait(p_ready, it & 1, kDevTimeoutSync))) break;
         tc_fence_after();
-        product_ts<D>(1u, tV, tS, 64, nO + slot(it, kO) * (kTile >> 4), it > 0);
-        mma_commit(&o_empty[slot(it, kO)]);
-        if (it + 1 < n && !(ok = scores(it + 1))) break;
-        ok = wait(ds_ready, it & 1, kDevTimeoutSync);
-        if (!ok) break;
+        const int qs = rq.at, os = it & 1;
+        rq.next();
+        product_ts<D>(lead, tV, tS, 64, nO + os * (kTile >> 4), it > 0);
+        commit(lead, &o_empty[os]);
+        if (it + 1 < n) scores(rq.at);
+        if (!(ok = wait(ds_ready, it & 1, kDevTimeoutSync))) break;
         tc_fence_after();
-        product_ts<D>(1u, tK, tP, 64, nQ + slot(it, kQ) * (kTile >> 4), it > 0);
-        mma_commit(&q_empty[slot(it, kQ)]);
-        if (it + 1 < n) ok = dprobs(it + 1);
+        product_ts<D>(lead, tK, tP, 64, nQ + qs * (kTile >> 4), it > 0);
+        commit(lead, &q_empty[qs]);
+        if (it + 1 < n) dprobs(os ^ 1);
       }
-      mma_commit(done);  // the softmax warps wait for it, or, after an error:
+      commit(lead, done);  // the softmax warps wait for it, or, after an error:
       if (!ok) mbar_drain(done, 0);
+    } else if (warp >= 10 && lane == 0) {
+      // ---------------- gates: warp 10 for S(it + 1) behind dV(it), warp 11 for dP(it + 1) behind dK(it) ----------------
+      uint64_t* bar = warp == 10 ? p_ready : ds_ready;
+      Ring<kQ, 1> rq(0);
+      bool ok = true;
+      for (int it = 0; it < n && ok; ++it) {
+        rq.next();
+        if (it + 1 < n) {
+          const int os = (it + 1) & 1;
+          const uint32_t ph = phase(it + 1, kO);
+          ok = warp == 10 ? attn_wait(&q_full[rq.at], rq.phase, abort_flag, p.status, kDevTimeoutTma) && attn_wait(&ready[os], ph, abort_flag, p.status, kDevTimeoutSync)
+                          : attn_wait(&o_full[os], ph, abort_flag, p.status, kDevTimeoutTma);
+          if (!ok) break;
+        }
+        mbar_arrive(bar);
+        ok = attn_wait(bar, it & 1, abort_flag, p.status, kDevTimeoutSync);  // the next arrival belongs to the next phase
+      }
     }
   } else {
     // ---------------- softmax: key row, half of the queries ----------------
@@ -289,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tb, 512);
+  if (warp == 8) tmem_dealloc(*tslot, 512);
 }
 
 template <int D>
@@ -319,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kK; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
     for (int i = 0; i < kV; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 1), mbar_init(&s_full[i], 1);
     mbar_init(dp_full, 1);
-    mbar_init(ds_ready, kSoftmax);
+    mbar_init(ds_ready, kSoftmax + 1);
     mbar_init(tail_ready, 32);
     mbar_init(done, 1);
     fence_mbar_init();
@@ -327,8 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tb = *tslot, tP = tb + 256, tQ = tb + 384;
-  auto tS = [&](int i) { return tb + uint32_t(i & 1) * 128; };
+  constexpr uint32_t tP = 256, tQ = 384;  // all of TMEM, so it starts at column 0
+  auto tS = [&](int i) { return uint32_t(i & 1) * 128; };
 
   if (warp >= 8) {
     regs_dec<kOtherRegs>();
@@ -363,39 +380,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async_smem();
         mbar_arrive(tail_ready);
       }
-    } else if (warp == 8 && lane == 0) {
+    } else if (warp == 8) {
       // ---------------- MMA issuer ----------------
+      const uint32_t lead = elect_lead();
       const uint32_t aQ = desc_low_k(smem_u32(sQ)), aO = desc_low_k(smem_u32(sO)), bK = desc_low_k(smem_u32(sK)), bV = desc_low_k(smem_u32(sV)),
                      nK = desc_low_mn(smem_u32(sK), kAttnPanel);
-      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
+      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, attn_wait(b, ph, abort_flag, p.status, code))); };
+      Ring<kK, 1> rs(0), rk(0);  // K of the scores, and of dq
       auto scores = [&](int i) {
-        if (!wait(&k_full[slot(i, kK)], phase(i, kK), kDevTimeoutTma)) return false;
-        if (tail && i + 1 == n && !wait(tail_ready, 0, kDevTimeoutSync)) return false;
-        tc_fence_after();
-        product_ss<D>(1u, tS(i), aQ, bK + slot(i, kK) * (kTile >> 4));
-        mma_commit(&s_full[i & 1]);
-        return true;
+        product_ss<D>(lead, tS(i), aQ, bK + rs.at * (kTile >> 4));
+        commit(lead, &s_full[i & 1]);
+        rs.next();
       };
       auto dprobs = [&](int i) {
-        if (!wait(&v_full[slot(i, kV)], phase(i, kV), kDevTimeoutTma)) return false;
-        tc_fence_after();
-        product_ss<D>(1u, tP, aO, bV + slot(i, kV) * (kTile >> 4));
-        mma_commit(dp_full);
-        mma_commit(&v_empty[slot(i, kV)]);
-        return true;
+        product_ss<D>(lead, tP, aO, bV + (i & 1) * (kTile >> 4));
+        commit(lead, dp_full);
+        commit(lead, &v_empty[i & 1]);
       };
-      bool ok = wait(q_full, 0, kDevTimeoutTma) && scores(0) && dprobs(0) && (n == 1 || scores(1));
+      auto k_there = [&](int i) {
+        return wait(&k_full[slot(i, kK)], phase(i, kK), kDevTimeoutTma) && (!tail || i + 1 < n || wait(tail_ready, 0, kDevTimeoutSync));
+      };
+      bool ok = wait(q_full, 0, kDevTimeoutTma) && k_there(0);
+      if (ok) scores(0);
+      ok = ok && wait(&v_full[0], 0, kDevTimeoutTma);
+      if (ok) dprobs(0);
+      if (n > 1 && ok && (ok = k_there(1))) scores(1);
       for (int i = 0; i < n && ok; ++i) {
-        ok = wait(ds_ready, i & 1, kDevTimeoutSync);
-        if (!ok) break;
+        // the gate answers for V of the next tile and K of the one behind it
+        if (!(ok = wait(ds_ready, i & 1, kDevTimeoutSync))) break;
         tc_fence_after();
-        if (i + 1 < n && !(ok = dprobs(i + 1))) break;
-        product_ts<D>(1u, tQ, tS(i), 64, nK + slot(i, kK) * (kTile >> 4), i > 0);
-        mma_commit(&k_empty[slot(i, kK)]);
-        if (i + 2 < n) ok = scores(i + 2);
+        if (i + 1 < n) dprobs(i + 1);
+        product_ts<D>(lead, tQ, tS(i), 64, nK + rk.at * (kTile >> 4), i > 0);
+        commit(lead, &k_empty[rk.at]);
+        rk.next();
+        if (i + 2 < n) scores(i + 2);
       }
-      mma_commit(done);  // the softmax warps wait for it, or, after an error:
+      commit(lead, done);  // the softmax warps wait for it, or, after an error:
       if (!ok) mbar_drain(done, 0);
+    } else if (warp == 10 && lane == 0) {
+      // ---------------- gate: the tiles of the products that follow dS(i) have landed ----------------
+      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i) {
+        ok = (i + 1 >= n || wait(&v_full[(i + 1) & 1], phase(i + 1, kV), kDevTimeoutTma)) &&
+             (i + 2 >= n || wait(&k_full[slot(i + 2, kK)], phase(i + 2, kK), kDevTimeoutTma)) && (!tail || i + 3 != n || wait(tail_ready, 0, kDevTimeoutSync));
+        if (!ok) break;
+        mbar_arrive(ds_ready);
+        ok = wait(ds_ready, i & 1, kDevTimeoutSync);  // the next arrival belongs to the next phase
+      }
     }
   } else {
     // ---------------- softmax: query row, half of the keys ----------------
@@ -448,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tb, 512);
+  if (warp == 8) tmem_dealloc(*tslot, 512);
 }
 
 template <int D>
