@@ -406,25 +406,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) dprobs(0);
       if (n > 1 && ok && (ok = k_there(1))) scores(1);
       for (int i = 0; i < n && ok; ++i) {
-        // the gate answers for V of the next tile and K of the one behind it
+        // the gate answers for V of the next tile
         if (!(ok = wait(ds_ready, i & 1, kDevTimeoutSync))) break;
         tc_fence_after();
         if (i + 1 < n) dprobs(i + 1);
         product_ts<D>(lead, tQ, tS(i), 64, nK + rk.at * (kTile >> 4), i > 0);
         commit(lead, &k_empty[rk.at]);
         rk.next();
-        if (i + 2 < n) scores(i + 2);
+        // K of the tile after next is requested when the product before this one has let go of its stage
+        if (i + 2 < n && (ok = k_there(i + 2))) scores(i + 2);
       }
       commit(lead, done);  // the softmax warps wait for it, or, after an error:
       if (!ok) mbar_drain(done, 0);
     } else if (warp == 10 && lane == 0) {
-      // ---------------- gate: the tiles of the products that follow dS(i) have landed ----------------
+      // ---------------- gate: V of the product that follows dS(i) has landed ----------------
       auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
       bool ok = true;
       for (int i = 0; i < n && ok; ++i) {
-        ok = (i + 1 >= n || wait(&v_full[(i + 1) & 1], phase(i + 1, kV), kDevTimeoutTma)) &&
-             (i + 2 >= n || wait(&k_full[slot(i + 2, kK)], phase(i + 2, kK), kDevTimeoutTma)) && (!tail || i + 3 != n || wait(tail_ready, 0, kDevTimeoutSync));
-        if (!ok) break;
+        if (i + 1 < n && !(ok = wait(&v_full[(i + 1) & 1], phase(i + 1, kV), kDevTimeoutTma))) break;
         mbar_arrive(ds_ready);
         ok = wait(ds_ready, i & 1, kDevTimeoutSync);  // the next arrival belongs to the next phase
       }
