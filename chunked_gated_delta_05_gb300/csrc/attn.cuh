@@ -214,7 +214,7 @@ struct AttnStepParams {
   const __nv_bfloat16 *q, *kc, *vc;
   const int *table, *lengths;
   __nv_bfloat16* o;            // [B,H,D]
-  float* part;                 // splits > 1: [B,H,splits][D + 2]: weighted sum, reference, sum of weights
+  float* part;                 // splits > 1: weighted sums [B,H,splits][D], then {reference, sum of weights} [B,H,splits]
   int* status;
 };
 cudaError_t launch_attn_step(const AttnStepParams& p, int D, cudaStream_t s);

@@ -364,9 +364,10 @@ struct AttnStepProblem {
   int splits;
 };
 
-// Pieces of a row's keys: blocks enough for kStepBlocks on every SM, of at least kStepKeys keys at the table's capacity (the lengths are
-// known on the device only).
-constexpr int kSms = 152, kStepBlocks = 8, kStepKeys = 128, kMaxSplits = 64;
+// Pieces of a row's keys, each a block: as many as the SMs hold at once where rows are few, and pieces of no more than kStepKeys
+// keys (at the table's capacity: the lengths are known on the device only) where they are many, so that rows of different lengths
+// spread evenly.
+constexpr int kSms = 152, kStepBlocks = 2, kStepKeys = 2048, kLeastKeys = 64, kMaxSplits = 128;
 
 int validate_step(const gdn_attn_step_desc_t* d, AttnStepProblem* P) {
   if (!d) return bad("desc is NULL");
@@ -383,7 +384,7 @@ int validate_step(const gdn_attn_step_desc_t* d, AttnStepProblem* P) {
   if (P->q_s < 0) return bad("q_stride must be a multiple of 8, at least a row");
   const int group = P->S.H / P->S.Hk, rows = group > 8 ? 16 : 8;
   const long long blocks = (long long)d->B * P->S.Hk * ((group + rows - 1) / rows);
-  const long long want = (kSms * kStepBlocks + blocks - 1) / blocks, most = (room + kStepKeys - 1) / kStepKeys;
+  const long long want = std::max(kSms * kStepBlocks / blocks, (room + kStepKeys - 1) / kStepKeys), most = (room + kLeastKeys - 1) / kLeastKeys;
   P->splits = int(std::max(1ll, std::min({want, most, (long long)kMaxSplits})));
   if (blocks * P->splits >= (1ll << 31)) return bad("problem too large");
   return GDN_OK;

@@ -2,9 +2,9 @@
 // sequence's first `length` keys, which lie in the pages its row of the table names.
 //
 // Memory bound: every key and value is read once (4 D bytes a key and key head) for the group's query heads together, two
-// products of 4 D group flops. A warp takes 16 keys at a time, K and V straight into registers in 16-byte pieces; the products run
-// on the tensor core with the query heads as the 16 rows (m16n8k16: for so few rows the larger tcgen05 shapes would be idle
-// rows, and their operands would have to pass through shared memory).
+// products of 4 D group flops. A warp takes 16 keys at a time, K and V in 16-byte pieces by asynchronous copies two groups of keys
+// ahead; each lane copies what it reads itself, so that no lane waits for another. The products run on the tensor core with the
+// query heads as the 16 rows (m16n8k16: for so few rows the larger tcgen05 shapes would be idle rows).
 //
 // No shuffles between the products: in q k^T a lane's 16-byte piece of a key stands for whichever products' inner indices it falls
 // on (the same channels are taken from q), so it needs no rearranging; the weights come out where the second product
@@ -19,7 +19,14 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 4, kKeys = 16;
+constexpr int kWarps = 4, kKeys = 16, kStages = 3;
+// A warp's stage of 16 keys: pieces of 16 bytes by lane.
+template <int D>
+struct Stage {
+  static constexpr int kPieces = D / 32, kHalves = D / 64;  // of a key, of half a value row, to a lane
+  static constexpr int kCount = 2 * kPieces + 4 * kHalves, kBytes = kCount * 512;
+  static constexpr int kSmem = kWarps * kStages * kBytes;
+};
 constexpr float kRescale = 8.f;
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -35,9 +42,13 @@ __device__ __forceinline__ void mma16816_low(float* c, uint32_t a0, uint32_t a2,
                : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-__device__ __forceinline__ uint4 ldg16(const __nv_bfloat16* p) {
+// 16 bytes to shared memory, zeros where `there` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const __nv_bfloat16* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
   return r;
 }
 __device__ __forceinline__ uint32_t part(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -47,8 +58,11 @@ __device__ __forceinline__ uint32_t part(const uint4& v, int i) { return i == 0 
 // kRows: 1 for up to 8 query heads of a key head in a block, 2 for up to 16.
 template <int D, int kRows>
 __global__ void __launch_bounds__(kWarps * 32) k_attn_step(const AttnStepParams p, int row_blocks) {
-  constexpr int kPieces = D / 32, kHalves = D / 64;
-  __shared__ float acc_s[kWarps][8 * kRows][D], ml_s[kWarps][8 * kRows][2];
+  using St = Stage<D>;
+  constexpr int kPieces = St::kPieces, kHalves = St::kHalves;
+  extern __shared__ __align__(16) uint8_t smem[];  // the warps' stages, then their sums
+  __shared__ float ml_s[kWarps][8 * kRows][2];
+  float(*acc_s)[8 * kRows][D] = reinterpret_cast<float(*)[8 * kRows][D]>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   int i = blockIdx.x;
   const int split = i % p.splits;
@@ -102,26 +116,60 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_step(const AttnStepParams 
     }
     return (long long)page * p.page + k % p.page;
   };
-  long long mine = cache_row(from + warp * kKeys + (lane & 15));
   const long long token = (long long)p.Hk * D;
   const __nv_bfloat16 *kc = p.kc + hk * D, *vc = p.vc + hk * D;
-  for (int k0 = from + warp * kKeys; k0 < to; k0 += kWarps * kKeys) {
+  const uint32_t mem = smem_u32(smem) + warp * (kStages * St::kBytes) + lane * 16;
+  // Requests the pieces of 16 keys whose cache rows the lanes hold; bit x: this lane's x-th value row is there.
+  auto request = [&](uint32_t at, long long mine) -> uint32_t {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {  // key g of either eight
+      const long long r = __shfl_sync(0xffffffffu, mine, u * 8 + g);
+      const __nv_bfloat16* src = kc + (r < 0 ? 0 : r) * token + c * 8;
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) copy16(at + (u * kPieces + j) * 512, src + j * 32, r >= 0);
+    }
+    uint32_t bits = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {  // values of keys 2c, 2c + 1, 2c + 8, 2c + 9
+      const long long r = __shfl_sync(0xffffffffu, mine, (x >> 1) * 8 + 2 * c + (x & 1));
+      const __nv_bfloat16* src = vc + (r < 0 ? 0 : r) * token + g * 8;
+      bits |= uint32_t(r >= 0) << x;
+#pragma unroll
+      for (int h2 = 0; h2 < kHalves; ++h2) copy16(at + (2 * kPieces + x * kHalves + h2) * 512, src + h2 * 64, r >= 0);
+    }
+    return bits;
+  };
+  constexpr int kStride = kWarps * kKeys;
+  const int first = from + warp * kKeys;
+  uint32_t bits[kStages] = {};
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    bits[i] = request(mem + i * St::kBytes, cache_row(first + i * kStride + (lane & 15)));
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  long long mine = cache_row(first + (kStages - 1) * kStride + (lane & 15));
+  int stage = 0;
+  for (int k0 = first; k0 < to; k0 += kStride) {
+    bits[kStages - 1] = request(mem + (stage == 0 ? kStages - 1 : stage - 1) * St::kBytes, mine);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    mine = cache_row(k0 + kStages * kStride + (lane & 15));
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    const uint32_t at = mem + stage * St::kBytes;
     uint4 kk[2][kPieces], vv[4][kHalves];
     bool there[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const long long r = __shfl_sync(0xffffffffu, mine, u * 8 + g);
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) kk[u][j] = r >= 0 ? ldg16(kc + r * token + (c + 4 * j) * 8) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < kPieces; ++j) kk[u][j] = lds16(at + (u * kPieces + j) * 512);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      there[x] = bits[0] >> x & 1u;
+#pragma unroll
+      for (int h2 = 0; h2 < kHalves; ++h2) vv[x][h2] = lds16(at + (2 * kPieces + x * kHalves + h2) * 512);
     }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {  // keys 2c, 2c + 1, 2c + 8, 2c + 9
-      const long long r = __shfl_sync(0xffffffffu, mine, (x >> 1) * 8 + 2 * c + (x & 1));
-      there[x] = r >= 0;
-#pragma unroll
-      for (int h2 = 0; h2 < kHalves; ++h2) vv[x][h2] = r >= 0 ? ldg16(vc + r * token + h2 * 64 + g * 8) : make_uint4(0, 0, 0, 0);
-    }
-    mine = cache_row(k0 + kWarps * kKeys + (lane & 15));
+    for (int i = 0; i + 1 < kStages; ++i) bits[i] = bits[i + 1];
+    stage = stage + 1 == kStages ? 0 : stage + 1;
     float s[2][4] = {};
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -179,7 +227,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_step(const AttnStepParams 
       }
   }
 
-  // the block's warps joined
+  // the block's warps joined, their sums where the stages were
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -214,57 +264,84 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_step(const AttnStepParams 
     if (p.splits == 1) {
       p.o[at * D + d] = __float2bfloat16(total == 0.f ? 0.f : sum / total);
     } else {
-      float* dst = p.part + (at * p.splits + split) * (D + 2);
-      dst[d] = sum;
-      if (d == 0) {
-        dst[D] = top;
-        dst[D + 1] = total;
-      }
+      const long long i = at * p.splits + split;
+      p.part[i * D + d] = sum;
+      if (d == 0) *reinterpret_cast<float2*>(p.part + (long long)p.B * p.H * p.splits * D + 2 * i) = make_float2(top, total);
     }
   }
 }
 
-// Joins the pieces of a (row, head): one warp each.
-template <int D>
-__global__ void __launch_bounds__(128) k_attn_join(const AttnStepParams p) {
+// Joins the pieces of a (row, head): a block each, its kJoin warps taking pieces in turn, four requested together.
+template <int D, int kJoin>
+__global__ void __launch_bounds__(kJoin * 32) k_attn_join(const AttnStepParams p) {
   constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long at = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  __shared__ float acc[kJoin][D], tot[kJoin];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long at = blockIdx.x;
   wait_for_previous();
-  if (at >= (long long)p.B * p.H) return;
   int len = p.lengths[at / p.H];
   if (len > 0 && (len - 1) / p.page >= p.width) len = 0;
   float sum[kPer] = {}, total = 0.f;
   if (len > 0) {
     const int piece = ((len + p.splits - 1) / p.splits + kKeys - 1) / kKeys * kKeys, n = (len + piece - 1) / piece;
-    const float* src = p.part + at * p.splits * (D + 2);
+    const float* src = p.part + at * p.splits * D + lane * kPer;
+    const float2* ml = reinterpret_cast<const float2*>(p.part + (long long)p.B * p.H * p.splits * D) + at * p.splits;
     const float cs = p.scale * kLog2e;
     float top = -INFINITY;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, src[i * (D + 2) + D]);
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[i].x);
+    for (int i0 = warp; i0 < n; i0 += 4 * kJoin) {
+      float x[4][kPer];
+      float2 y[4];
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float* x = src + i * (D + 2);
-      const float mi = x[D], f = mi == top ? 1.f : exp2_approx((mi - top) * cs);
-      total = fmaf(x[D + 1], f, total);
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kJoin;
+        y[u] = i < n ? ml[i] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) sum[e] = fmaf(x[lane + 32 * e], f, sum[e]);
+        for (int e = 0; e < kPer; ++e) x[u][e] = i < n ? src[(long long)i * D + e] : 0.f;
+      }
+      if (i0 == warp)
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = y[u].x == top ? 1.f : exp2_approx((y[u].x - top) * cs);
+        total = fmaf(y[u].y, f, total);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) sum[e] = fmaf(x[u][e], f, sum[e]);
+      }
     }
   }
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) p.o[at * D + lane + 32 * e] = __float2bfloat16(total == 0.f ? 0.f : sum[e] / total);
+  for (int e = 0; e < kPer; ++e) acc[warp][lane * kPer + e] = sum[e];
+  if (lane == 0) tot[warp] = total;
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += kJoin * 32) {
+    float v = 0.f, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+      v += acc[i][d];
+      l += tot[i];
+    }
+    p.o[at * D + d] = __float2bfloat16(l == 0.f ? 0.f : v / l);
+  }
 }
 
-template <int D>
+template <int D, int kRows>
 static cudaError_t launch(const AttnStepParams& p, cudaStream_t s) {
-  const int rows = p.group > 8 ? 16 : 8, rb = (p.group + rows - 1) / rows;
+  constexpr int kSmem = Stage<D>::kSmem;
+  static_assert(kSmem >= kWarps * 8 * kRows * D * 4, "the warps' sums lie where the stages were");
+  const int rb = (p.group + 8 * kRows - 1) / (8 * kRows);
   const dim3 grid(unsigned((long long)p.B * p.Hk * rb * p.splits)), block(kWarps * 32);
-  cudaError_t e = rows == 8 ? launch_after(k_attn_step<D, 1>, grid, block, 0, s, p, rb) : launch_after(k_attn_step<D, 2>, grid, block, 0, s, p, rb);
-  if (e == cudaSuccess && p.splits > 1) e = launch_after(k_attn_join<D>, dim3(unsigned(((long long)p.B * p.H + 3) / 4)), dim3(128), 0, s, p);
+  cudaError_t e = cudaFuncSetAttribute(k_attn_step<D, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) e = launch_after(k_attn_step<D, kRows>, grid, block, kSmem, s, p, rb);
+  if (e == cudaSuccess && p.splits > 1) e = p.splits > 16 ? launch_after(k_attn_join<D, 16>, dim3(unsigned((long long)p.B * p.H)), dim3(512), 0, s, p)
+                                                      : launch_after(k_attn_join<D, 4>, dim3(unsigned((long long)p.B * p.H)), dim3(128), 0, s, p);
   return e;
 }
 
-cudaError_t launch_attn_step(const AttnStepParams& p, int D, cudaStream_t s) { return D == 128 ? launch<128>(p, s) : launch<64>(p, s); }
+cudaError_t launch_attn_step(const AttnStepParams& p, int D, cudaStream_t s) {
+  if (D == 128) return p.group > 8 ? launch<128, 2>(p, s) : launch<128, 1>(p, s);
+  return p.group > 8 ? launch<64, 2>(p, s) : launch<64, 1>(p, s);
+}
 
 }  // namespace gdn
