@@ -208,16 +208,21 @@ int rope_bwd_blocks();
 struct AttnStepParams {
   int B, H, Hk, group;
   int pages, page, width;      // cache pages, keys in a page, entries of a row of the table
-  int splits;                  // pieces a row's keys are cut into
+  int shares;                  // the rows' keys are cut into
   float scale;
   long long q_stride;
   const __nv_bfloat16 *q, *kc, *vc;
   const int *table, *lengths;
   __nv_bfloat16* o;            // [B,H,D]
-  float* part;                 // splits > 1: weighted sums [B,H,splits][D], then {reference, sum of weights} [B,H,splits]
+  // pieces of rows that several shares hold, by row + share and part (key head, block of query heads): weighted sums [..][8 or 16][D]
+  // and {reference, sum of weights}; and every row's and part's first and last share
+  float* part;
+  float2* ml;
+  int2* span;
   int* status;
 };
 cudaError_t launch_attn_step(const AttnStepParams& p, int D, cudaStream_t s);
+inline int attn_step_rows(int group) { return group > 8 ? 16 : 8; }  // query heads of a block
 
 // Host: a 2-D bf16 tensor map (api.cu): rows of `cols` elements, `stride` elements apart, boxes of 64 x `box_rows`, 128-byte swizzle.
 bool attn_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t stride, uint32_t box_rows);

@@ -361,13 +361,10 @@ struct AttnStepProblem {
   Shape S;
   long long q_s;
   float scale;
-  int splits;
+  int parts, shares;
 };
 
-// Pieces of a row's keys, each a block: as many as the SMs hold at once where rows are few, and pieces of no more than kStepKeys
-// keys (at the table's capacity: the lengths are known on the device only) where they are many, so that rows of different lengths
-// spread evenly.
-constexpr int kSms = 152, kStepBlocks = 2, kStepKeys = 2048, kLeastKeys = 64, kMaxSplits = 128;
+constexpr int kStepBlocks = 304;  // the SMs hold two each
 
 int validate_step(const gdn_attn_step_desc_t* d, AttnStepProblem* P) {
   if (!d) return bad("desc is NULL");
@@ -382,16 +379,23 @@ int validate_step(const gdn_attn_step_desc_t* d, AttnStepProblem* P) {
   P->scale = d->scale > 0.f ? d->scale : 1.f / std::sqrt(float(P->S.D));
   P->q_s = stride_of(d->q_stride, P->S.H, P->S.D);
   if (P->q_s < 0) return bad("q_stride must be a multiple of 8, at least a row");
-  const int group = P->S.H / P->S.Hk, rows = group > 8 ? 16 : 8;
-  const long long blocks = (long long)d->B * P->S.Hk * ((group + rows - 1) / rows);
-  const long long want = std::max(kSms * kStepBlocks / blocks, (room + kStepKeys - 1) / kStepKeys), most = (room + kLeastKeys - 1) / kLeastKeys;
-  P->splits = int(std::max(1ll, std::min({want, most, (long long)kMaxSplits})));
-  if (blocks * P->splits >= (1ll << 31)) return bad("problem too large");
+  const int group = P->S.H / P->S.Hk, rows = attn_step_rows(group);
+  P->parts = P->S.Hk * ((group + rows - 1) / rows);
+  if ((long long)d->B * P->S.H >= (1ll << 31)) return bad("problem too large");
+  P->shares = int(std::min((long long)std::max(1, kStepBlocks / P->parts), d->B * ((room + 63) / 64)));
   return GDN_OK;
 }
 
-size_t step_ws(const AttnStepProblem& P) {
-  return P.splits == 1 ? 256 : align256(size_t(P.S.B) * P.S.H * P.splits * (P.S.D + 2) * 4);
+struct StepLayout {
+  size_t ml, span, total;
+};
+StepLayout layout_step(const AttnStepProblem& P) {
+  StepLayout l{};
+  const size_t rows = (size_t(P.S.B) + P.shares) * P.parts * attn_step_rows(P.S.H / P.S.Hk);
+  l.ml = align256(rows * P.S.D * 4);
+  l.span = l.ml + align256(rows * 8);
+  l.total = l.span + align256(size_t(P.S.B) * P.parts * 8);
+  return l;
 }
 
 int attn_step(const gdn_attn_step_desc_t* d, const gdn_attn_step_args_t* a, void* stream) {
@@ -404,7 +408,7 @@ int attn_step(const gdn_attn_step_desc_t* d, const gdn_attn_step_args_t* a, void
   const size_t cache = size_t(d->num_pages) * d->page_size * P.S.Hk * P.S.D * 2;
   const Span in[] = {{a->q, extent(d->B, P.q_s, P.S.H, P.S.D)}, {a->k_cache, cache}, {a->v_cache, cache}}, out[] = {{a->o, size_t(d->B) * P.S.H * P.S.D * 2}};
   if (alias(in, out)) return bad("o must not alias the inputs");
-  if (!workspace_ok(a->workspace, a->workspace_bytes, step_ws(P))) return bad("workspace missing, too small or not 256-byte aligned");
+  if (!workspace_ok(a->workspace, a->workspace_bytes, layout_step(P).total)) return bad("workspace missing, too small or not 256-byte aligned");
   if ((rc = device_or_error(nullptr))) return rc;
   AttnStepParams p{};
   p.B = d->B;
@@ -414,7 +418,7 @@ int attn_step(const gdn_attn_step_desc_t* d, const gdn_attn_step_args_t* a, void
   p.pages = d->num_pages;
   p.page = d->page_size;
   p.width = d->table_width;
-  p.splits = P.splits;
+  p.shares = P.shares;
   p.scale = P.scale;
   p.q_stride = P.q_s;
   p.q = static_cast<cbf*>(a->q);
@@ -423,7 +427,11 @@ int attn_step(const gdn_attn_step_desc_t* d, const gdn_attn_step_args_t* a, void
   p.table = a->page_table;
   p.lengths = a->lengths;
   p.o = static_cast<bf*>(a->o);
-  p.part = static_cast<float*>(a->workspace);
+  const StepLayout l = layout_step(P);
+  char* ws = static_cast<char*>(a->workspace);
+  p.part = reinterpret_cast<float*>(ws);
+  p.ml = reinterpret_cast<float2*>(ws + l.ml);
+  p.span = reinterpret_cast<int2*>(ws + l.span);
   p.status = a->status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TimedScope t(kKAttnStep, s);
@@ -509,7 +517,7 @@ int gdn_attn_bwd(const gdn_attn_desc_t* d, const gdn_attn_bwd_args_t* a, void* s
 
 size_t gdn_attn_step_workspace_size(const gdn_attn_step_desc_t* d) {
   AttnStepProblem P{};
-  return validate_step(d, &P) ? 0 : step_ws(P);
+  return validate_step(d, &P) ? 0 : layout_step(P).total;
 }
 int gdn_attn_step(const gdn_attn_step_desc_t* d, const gdn_attn_step_args_t* a, void* s) { return attn_step(d, a, s); }
 
