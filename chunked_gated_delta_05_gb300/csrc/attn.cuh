@@ -223,6 +223,8 @@ struct AttnStepParams {
 };
 cudaError_t launch_attn_step(const AttnStepParams& p, int D, cudaStream_t s);
 inline int attn_step_rows(int group) { return group > 8 ? 16 : 8; }  // query heads of a block
+// Blocks that 152 SMs hold at once, by shared memory and registers: 3 each, or 6 (4 with 16 heads) of the narrower heads.
+inline int attn_step_blocks(int D, int rows) { return 152 * (D == 128 ? 3 : rows == 8 ? 6 : 4); }
 
 // Host: a 2-D bf16 tensor map (api.cu): rows of `cols` elements, `stride` elements apart, boxes of 64 x `box_rows`, 128-byte swizzle.
 bool attn_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t stride, uint32_t box_rows);

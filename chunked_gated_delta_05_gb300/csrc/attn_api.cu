@@ -364,8 +364,6 @@ struct AttnStepProblem {
   int parts, shares;
 };
 
-constexpr int kStepBlocks = 304;  // the SMs hold two each
-
 int validate_step(const gdn_attn_step_desc_t* d, AttnStepProblem* P) {
   if (!d) return bad("desc is NULL");
   const int rc = check_heads(d->H, d->num_k_heads, d->head_dim, &P->S);
@@ -382,7 +380,7 @@ int validate_step(const gdn_attn_step_desc_t* d, AttnStepProblem* P) {
   const int group = P->S.H / P->S.Hk, rows = attn_step_rows(group);
   P->parts = P->S.Hk * ((group + rows - 1) / rows);
   if ((long long)d->B * P->S.H >= (1ll << 31)) return bad("problem too large");
-  P->shares = int(std::min((long long)std::max(1, kStepBlocks / P->parts), d->B * ((room + 63) / 64)));
+  P->shares = int(std::min((long long)std::max(1, attn_step_blocks(P->S.D, rows) / P->parts), d->B * ((room + 63) / 64)));
   return GDN_OK;
 }
 

@@ -2,9 +2,10 @@
 // sequence's first `length` keys, which lie in the pages its row of the table names.
 //
 // Memory bound: every key and value is read once (4 D bytes a key and key head) for the group's query heads together, two
-// products of 4 D group flops. A warp takes 16 keys at a time, whole K and V rows by asynchronous bulk copies (a lane each) two groups
-// of keys ahead. The products run on the tensor core, the keys (then the channels) as the 16 rows of m16n8k16 and the query heads as
-// its 8 columns (for so few heads the larger tcgen05 shapes would be idle columns):
+// products of 4 D group flops. A warp takes 16 keys at a time, whole K and V rows by asynchronous bulk copies (a lane each) a group
+// of keys ahead: twelve warps an SM with two stages each read faster than eight with three (120 rows, 1.14 GB: 173 us, 6.6 TB/s,
+// against 196). The products run on the tensor core, the keys (then the channels) as the 16 rows of m16n8k16 and the query heads
+// as its 8 columns (for so few heads the larger tcgen05 shapes would be idle columns):
 //   S^T [16 keys, 8 heads] = K q^T,   O^T [16 channels, 8 heads] += V^T P^T
 // K comes by ldmatrix, V^T by its transposing form, and the weights' 8 x 8 blocks are transposed in registers between the two.
 // A warp iteration is about 150 instructions for 8 KB; with the heads as rows it was over 500, which held the call to 5.0 TB/s.
@@ -20,7 +21,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 4, kKeys = 16, kUnit = kWarps * kKeys, kStages = 3;
+constexpr int kWarps = 4, kKeys = 16, kUnit = kWarps * kKeys, kStages = 2;
 // A warp's stage of 16 keys: their K rows, then their V rows, 16 bytes further apart than they are long (ldmatrix's eight rows then
 // lie in different banks).
 template <int D>
