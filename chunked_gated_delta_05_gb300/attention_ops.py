@@ -17,23 +17,27 @@ _attn_desc, _attn_fwd_args, _attn_bwd_args = _lib.packer(_lib.AttnDesc), _lib.pa
 _step_desc, _step_args = _lib.packer(_lib.AttnStepDesc), _lib.packer(_lib.AttnStepArgs)
 
 
-def _heads(q, others, names):
-    """Shapes and strides of q ``[..,H,D]`` and the key-side tensors ``[..,Hk,D]``: ``(device, lead, H, Hk, D, strides)``."""
+def _rows(name, t, shape, dev, width):
+    """Elements between tokens of ``t [..,heads,D]`` (0: contiguous)."""
+    if type(t) is torch.Tensor and t.dtype is _BF16 and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return 0
+    return _rows_of(name, t, _BF16, shape, dev, 2, width)
+
+
+def _heads(q, k, v):
+    """Shapes and strides of q ``[..,H,D]`` and of k, v ``[..,Hk,D]`` (v or None): ``(device, lead, H, Hk, D, strides)``."""
     dev = _device("q", q)
-    if q.dim() not in (3, 4) or q.numel() == 0:
+    shape = q.shape
+    if len(shape) not in (3, 4) or q.numel() == 0:
         raise ValueError("q must be [B,T,H,D] (or [B,H,D] for single tokens)")
-    k = others[0]
-    if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
-        raise ValueError(f"{names[0]} must have q's dimensions")
-    lead, H, D, Hk = q.shape[:-2], q.shape[-2], q.shape[-1], k.shape[-2]
+    if not isinstance(k, torch.Tensor) or k.dim() != len(shape):
+        raise ValueError("k must have q's dimensions")
+    *lead, H, D = shape
+    Hk = k.shape[-2]
     if Hk < 1 or H % Hk != 0:
         raise ValueError("the query heads must be a multiple of the key heads")
-    n = q.dim()
-    if n == 4:
-        lead = tuple(lead)
-    st = [_rows_of("q", q, _BF16, q.shape, dev, 2, H * D)]
-    st += [_rows_of(name, t, _BF16, (*lead, Hk, D), dev, 2, Hk * D) for name, t in zip(names, others)]
-    return dev, tuple(lead), H, Hk, D, st
+    keys = (*lead, Hk, D)
+    return dev, lead, H, Hk, D, (_rows("q", q, shape, dev, H * D), _rows("k", k, keys, dev, Hk * D), 0 if v is None else _rows("v", v, keys, dev, Hk * D))
 
 
 def _packed(offsets, n):
@@ -42,7 +46,7 @@ def _packed(offsets, n):
 
 def _rope_inputs(q, k, v, q_weight, k_weight, inv_freq, positions, interleaved, eps, offsets, cache):
     """Checks a call's inputs; ``(device, sequences, packed description)``. ``cache``: (pages, page size, table width) or zeros."""
-    dev, lead, H, Hk, D, st = _heads(q, (k,) if v is None else (k, v), ("k", "v"))
+    dev, lead, H, Hk, D, st = _heads(q, k, v)
     B, T = (lead[0], 1) if len(lead) == 1 else lead
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight must both be given or both be None")
@@ -56,18 +60,23 @@ def _rope_inputs(q, k, v, q_weight, k_weight, inv_freq, positions, interleaved, 
         _want("inv_freq", inv_freq, _F32, inv_freq.shape, dev)
         rotary = 2 * inv_freq.shape[0]
     if positions is not None:
-        _want("positions", positions, _I32, lead, dev)
+        _want("positions", positions, _I32, tuple(lead), dev)
     cu, n = _packed(offsets, B)
-    return dev, n, _rope_desc(B, T, cu, n, H, Hk, D, rotary, 1 if interleaved else 0, eps, st[0], st[1], st[2] if v is not None else 0, *cache)
+    return dev, n, _rope_desc(B, T, cu, n, H, Hk, D, rotary, 1 if interleaved else 0, eps, *st, *cache)
 
 
 def _workspace(name, desc, like):
+    """``(buffer, its address, its bytes)``."""
     n = _lib.size(name, desc)
-    return torch.empty(n, dtype=torch.uint8, device=like.device), n
+    ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+    return ws, ws.data_ptr(), n
+
+
+_NONE = (None, 0, 0)    # calls on dense batches that need no workspace
 
 
 def _new(t):
-    return torch.empty(t.shape, dtype=_BF16, device=t.device)
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=_BF16, device=t.device)
 
 
 def qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, *, positions=None, cu_seqlens: Optional[Sequence[int]] = None, eps=1e-6, interleaved=False):
@@ -81,10 +90,10 @@ def qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, *, positions=None, cu_s
     position. Returns ``(q, k)``, contiguous."""
     offsets = _offsets(cu_seqlens, 0)       # the packed description points into it
     dev, _, d = _rope_inputs(q, k, None, q_weight, k_weight, inv_freq, positions, interleaved, eps, offsets, (0, 0, 0))
-    ws, ws_bytes = _workspace("gdn_qk_norm_rope_workspace_size", d, q)
+    ws, *space = _NONE if offsets is None else _workspace("gdn_qk_norm_rope_workspace_size", d, q)
     qo, ko = _new(q), _new(k)
     _run("gdn_qk_norm_rope_fwd", d, _rope_args(q.data_ptr(), k.data_ptr(), 0, _p(q_weight), _p(k_weight), _p(inv_freq), _p(positions), qo.data_ptr(), ko.data_ptr(),
-                                               0, 0, 0, 0, ws.data_ptr(), ws_bytes, 0), dev)
+                                               0, 0, 0, 0, *space, 0), dev)
     return qo, ko
 
 
@@ -95,11 +104,11 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, *, posi
     dev, _, d = _rope_inputs(q, k, None, q_weight, k_weight, inv_freq, positions, interleaved, eps, offsets, (0, 0, 0))
     _want("dq_out", dq_out, _BF16, q.shape, dev)
     _want("dk_out", dk_out, _BF16, k.shape, dev)
-    ws, ws_bytes = _workspace("gdn_qk_norm_rope_workspace_size", d, q)
+    ws, *space = _workspace("gdn_qk_norm_rope_workspace_size", d, q)
     dq, dk = _new(q), _new(k)
     dqw, dkw = (None, None) if q_weight is None else (torch.empty_like(q_weight), torch.empty_like(k_weight))
     _run("gdn_qk_norm_rope_bwd", d, _rope_bwd_args(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight), _p(inv_freq), _p(positions),
-                                                   dq.data_ptr(), dk.data_ptr(), _p(dqw), _p(dkw), ws.data_ptr(), ws_bytes), dev)
+                                                   dq.data_ptr(), dk.data_ptr(), _p(dqw), _p(dkw), *space), dev)
     return dq, dk, dqw, dkw
 
 
@@ -135,10 +144,10 @@ def qk_norm_rope_store(q, k, v, q_weight, k_weight, inv_freq, k_cache, v_cache, 
     cache = _cache(k_cache, v_cache, page_table, lengths, n, k.shape[-2], k.shape[-1], dev)
     _, _, d = _rope_inputs(q, k, v, q_weight, k_weight, inv_freq, None, interleaved, eps, offsets, cache)
     _status(status, dev)
-    ws, ws_bytes = _workspace("gdn_qk_norm_rope_workspace_size", d, q)
+    ws, *space = _NONE if offsets is None else _workspace("gdn_qk_norm_rope_workspace_size", d, q)
     qo, ko = _new(q), _new(k)
     _run("gdn_qk_norm_rope_store", d, _rope_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), _p(q_weight), _p(k_weight), _p(inv_freq), 0, qo.data_ptr(), ko.data_ptr(),
-                                                 k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), ws.data_ptr(), ws_bytes, _p(status)), dev)
+                                                 k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), *space, _p(status)), dev)
     _changed(k_cache)
     _changed(v_cache)
     return qo, ko
@@ -147,7 +156,7 @@ def qk_norm_rope_store(q, k, v, q_weight, k_weight, inv_freq, k_cache, v_cache, 
 def _attn_inputs(q, k, v, causal, scale, offsets):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be [B,T,H,D]")
-    dev, lead, H, Hk, D, st = _heads(q, (k, v), ("k", "v"))
+    dev, lead, H, Hk, D, st = _heads(q, k, v)
     cu, n = _packed(offsets, lead[0])
     if scale is not None and not scale > 0:
         raise ValueError("scale must be positive")
@@ -162,9 +171,9 @@ def attention_fwd(q, k, v, *, causal=True, scale=None, cu_seqlens: Optional[Sequ
     offsets = _offsets(cu_seqlens, 0)       # the packed description points into it
     dev, shape, d = _attn_inputs(q, k, v, causal, scale, offsets)
     _status(status, dev)
-    ws, ws_bytes = _workspace("gdn_attn_fwd_workspace_size", d, q)
+    ws, *space = _NONE if offsets is None else _workspace("gdn_attn_fwd_workspace_size", d, q)
     o, lse = _new(q), torch.empty(shape, dtype=_F32, device=q.device)
-    _run("gdn_attn_fwd", d, _attn_fwd_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws_bytes, _p(status)), dev)
+    _run("gdn_attn_fwd", d, _attn_fwd_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), *space, _p(status)), dev)
     return o, lse
 
 
@@ -176,10 +185,10 @@ def attention_bwd(dO, q, k, v, o, lse, *, causal=True, scale=None, cu_seqlens=No
     _want("o", o, _BF16, q.shape, dev)
     _want("lse", lse, _F32, shape, dev)
     _status(status, dev)
-    ws, ws_bytes = _workspace("gdn_attn_bwd_workspace_size", d, q)
+    ws, *space = _workspace("gdn_attn_bwd_workspace_size", d, q)
     dq, dk, dv = _new(q), _new(k), _new(v)
     _run("gdn_attn_bwd", d, _attn_bwd_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                           ws.data_ptr(), ws_bytes, _p(status)), dev)
+                                           *space, _p(status)), dev)
     return dq, dk, dv
 
 
@@ -203,9 +212,9 @@ def attention_step(q, k_cache, v_cache, page_table, lengths, *, scale=None, stat
         raise ValueError("scale must be positive")
     _status(status, dev)
     d = _step_desc(B, H, Hk, D, 0.0 if scale is None else scale, pages, page, width, qs)
-    ws, ws_bytes = _workspace("gdn_attn_step_workspace_size", d, q)
+    ws, *space = _workspace("gdn_attn_step_workspace_size", d, q)
     o = _new(q)
-    _run("gdn_attn_step", d, _step_args(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), o.data_ptr(), ws.data_ptr(), ws_bytes, _p(status)), dev)
+    _run("gdn_attn_step", d, _step_args(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), o.data_ptr(), *space, _p(status)), dev)
     return o
 
 

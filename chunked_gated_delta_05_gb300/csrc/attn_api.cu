@@ -163,7 +163,7 @@ int rope_fwd(const gdn_rope_desc_t* d, const gdn_rope_args_t* a, void* stream, b
   const Span out[] = {{a->q_out, qb}, {a->k_out, kb}, {store ? a->k_cache : nullptr, cache}, {store ? a->v_cache : nullptr, cache}};
   if (alias(in, out)) return bad("outputs and caches must not alias the inputs or each other");
   const RopeLayout l = layout_rope(P);
-  if (!workspace_ok(a->workspace, a->workspace_bytes, l.total)) return bad("workspace missing, too small or not 256-byte aligned");
+  if (P.S.cu && !workspace_ok(a->workspace, a->workspace_bytes, l.total)) return bad("workspace missing, too small or not 256-byte aligned");
   RopeParams p = rope_params(d, P);
   if ((rc = device_or_error(&p.sms))) return rc;
   p.q = static_cast<cbf*>(a->q);
@@ -280,7 +280,7 @@ int attn_fwd(const gdn_attn_desc_t* d, const gdn_attn_fwd_args_t* a, void* strea
   const Span in[] = {{a->q, extent(P.S.rows, P.q_s, P.S.H, P.S.D)}, {a->k, extent(P.S.rows, P.k_s, P.S.Hk, P.S.D)}, {a->v, extent(P.S.rows, P.v_s, P.S.Hk, P.S.D)}};
   const Span out[] = {{a->o, size_t(P.S.rows) * P.S.H * P.S.D * 2}, {a->lse, size_t(P.S.rows) * P.S.H * 4}};
   if (alias(in, out)) return bad("o and lse must not alias the inputs or each other");
-  if (!workspace_ok(a->workspace, a->workspace_bytes, attn_fwd_ws(P))) return bad("workspace missing, too small or not 256-byte aligned");
+  if (P.S.cu && !workspace_ok(a->workspace, a->workspace_bytes, attn_fwd_ws(P))) return bad("workspace missing, too small or not 256-byte aligned");
   AttnParams p = attn_params(d, P);
   if ((rc = device_or_error(&p.sms)) || (rc = bind_context())) return rc;
   p.tiles = int(P.pairs);

@@ -11,14 +11,15 @@
 // is, and the remainder, in half a turn to either side, is what the sine unit is exact for (its error, 2^-20.9, is far below
 // a bf16 rounding). A token's angles serve all of its heads.
 //
-// Memory bound: a head's row is one 16-byte piece a lane (two heads of 128 channels a warp), four of them requested together.
-// A warp takes a token; calls of few tokens share a token's heads among several warps.
+// Memory bound: a head's row is 16 (or 8) lanes of eight channels, in two pieces of four whose channels are each other's partners, so
+// that a turn needs no shuffles; a warp has two (or four) heads at a time, kAhead such rows of heads requested together.
+// A warp takes a token; calls of few tokens share a token's heads among several warps. Arithmetic in packed pairs.
 #include "attn.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8, kAhead = 4;
+constexpr int kWarps = 8, kAhead = 4, kFwdBlocks = 3, kBwdPerSm = 2;  // blocks an SM holds
 
 // f / 2 pi modulo 1, in units of 2^-64: the 24-bit significand times 2^66 / 2 pi, shifted to its place.
 __device__ __forceinline__ unsigned long long turns_per_position(float f) {
@@ -49,69 +50,122 @@ __device__ __forceinline__ void cos_sin(unsigned long long f, int p, float* c, f
   *s = __sinf(a);
 }
 
-__device__ __forceinline__ void unpack8(uint4 u, float* x) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(w[i]);
-    x[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-}
+// A lane's share of a head's row: four channels and their four partners (channel i of `a` turns with channel i of `b`), as packed
+// pairs. Pieces of four channels lie at `ca` and `cb`.
+struct Share {
+  F2 a[2], b[2];
+};
 
-// A lane's share of a head: channels 8 sub .. 8 sub + 7.
 template <int D, bool kPairs>
-struct Turn {
-  static constexpr int kN = kPairs ? 4 : 8;  // angles of a lane
-  unsigned long long f[kN];
-  float c[kN], s[kN];
-  bool rot;
-  int partner;  // lane that holds the other halves of the pairs
-  __device__ __forceinline__ Turn(const RopeParams& p, int lane) {
-    const int sub = lane % (D / 8), half = p.rotary / 2;
-    rot = sub * 8 < p.rotary;
-    const bool first = sub * 8 < half;
-    partner = kPairs || !rot ? lane : lane + (first ? half / 8 : -half / 8);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int at = kPairs ? sub * 4 + i : sub * 8 + i - (first ? 0 : half);
-      f[i] = rot ? turns_per_position(p.inv_freq[at]) : 0;
-      if (!kPairs && first) f[i] = 0 - f[i];  // a' = a cos + b sin(-angle)
+struct Lane {
+  int ca, cb;
+  bool rot;                  // false: channels behind the turned ones, which stay
+  unsigned long long f[4];   // turns per position
+  F2 c[2], s[2];             // cosines and sines at the token's position
+  __device__ __forceinline__ Lane(const RopeParams& p, int lane) {
+    const int l = lane % (D / 8), half = p.rotary / 8;  // lanes that hold pairs, when those lie half the rotary width apart
+    if (kPairs) {
+      ca = 8 * l;
+      cb = 8 * l + 4;
+      rot = 8 * l < p.rotary;
+    } else {
+      rot = l < half;
+      ca = rot ? 4 * l : p.rotary + 8 * (l - half);
+      cb = rot ? 4 * (l + half) : ca + 4;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = rot ? turns_per_position(p.inv_freq[4 * l + i]) : 0;
   }
   __device__ __forceinline__ void at(int pos) {
+    float x[4], y[4];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) cos_sin(f[i], pos, &c[i], &s[i]);
+    for (int i = 0; i < 4; ++i) cos_sin(f[i], pos, &x[i], &y[i]);
+    c[0] = f2(x[0], x[1]), c[1] = f2(x[2], x[3]);
+    s[0] = f2(y[0], y[1]), s[1] = f2(y[2], y[3]);
+  }
+  // Eight channels as loaded (pieces at ca and cb) to a share and back.
+  static __device__ __forceinline__ Share split(const float* x) {
+    if (kPairs) return {{f2(x[0], x[2]), f2(x[4], x[6])}, {f2(x[1], x[3]), f2(x[5], x[7])}};
+    return {{f2(x[0], x[1]), f2(x[2], x[3])}, {f2(x[4], x[5]), f2(x[6], x[7])}};
+  }
+  static __device__ __forceinline__ void join(const Share& v, float* x) {
+    float a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      unf2(v.a[i], &a[2 * i], &a[2 * i + 1]);
+      unf2(v.b[i], &b[2 * i], &b[2 * i + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[kPairs ? 2 * i : i] = a[i];
+      x[kPairs ? 2 * i + 1 : 4 + i] = b[i];
+    }
+  }
+  __device__ __forceinline__ Share weights(const float* w) const {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = w ? w[ca + i] : 1.f;
+      x[4 + i] = w ? w[cb + i] : 1.f;
+    }
+    return split(x);
+  }
+  __device__ __forceinline__ void load(uint2* in, const __nv_bfloat16* row) const {
+    in[0] = *reinterpret_cast<const uint2*>(row + ca);
+    in[1] = *reinterpret_cast<const uint2*>(row + cb);
+  }
+  static __device__ __forceinline__ Share unpack(const uint2* in) {
+    const uint32_t w[4] = {in[0].x, in[0].y, in[1].x, in[1].y};
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16_lo(w[i]);
+      x[2 * i + 1] = bf16_hi(w[i]);
+    }
+    return split(x);
+  }
+  static __device__ __forceinline__ void pack(const Share& v, uint2* out) {
+    float x[8];
+    join(v, x);
+    out[0] = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    out[1] = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  }
+  __device__ __forceinline__ void store(const uint2* out, __nv_bfloat16* row) const {
+    *reinterpret_cast<uint2*>(row + ca) = out[0];
+    *reinterpret_cast<uint2*>(row + cb) = out[1];
   }
   // In place; kBack: the inverse turn.
   template <bool kBack>
-  __device__ __forceinline__ void apply(float* x) const {
-    if (kPairs) {
-      if (!rot) return;
+  __device__ __forceinline__ void turn(Share* v) const {
+    if (!rot) return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1], sn = kBack ? -s[i] : s[i];
-        x[2 * i] = a * c[i] - b * sn;
-        x[2 * i + 1] = b * c[i] + a * sn;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_sync(0xffffffffu, x[i], partner), sn = kBack ? -s[i % kN] : s[i % kN];
-        if (rot) x[i] = x[i] * c[i % kN] + other * sn;
-      }
+    for (int i = 0; i < 2; ++i) {
+      const F2 a = v->a[i], b = v->b[i], minus = mul2(s[i], dup2(-1.f));
+      v->a[i] = fma2(b, kBack ? s[i] : minus, mul2(a, c[i]));
+      v->b[i] = fma2(a, kBack ? minus : s[i], mul2(b, c[i]));
     }
   }
 };
 
-// Sum over the lanes of a head.
+// Sum over the lanes of a head of x y.
 template <int D>
-__device__ __forceinline__ float head_sum(float x) {
+__device__ __forceinline__ float head_dot(const Share& x, const Share& y) {
+  F2 t = mul2(x.a[0], y.a[0]);
+  t = fma2(x.a[1], y.a[1], t);
+  t = fma2(x.b[0], y.b[0], t);
+  t = fma2(x.b[1], y.b[1], t);
+  float v = sum2(t);
 #pragma unroll
-  for (int d = D / 16; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-  return x;
+  for (int d = D / 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+__device__ __forceinline__ void scale(Share* x, F2 f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) x->a[i] = mul2(x->a[i], f), x->b[i] = mul2(x->b[i], f);
+}
+__device__ __forceinline__ void times(Share* x, const Share& w) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) x->a[i] = mul2(x->a[i], w.a[i]), x->b[i] = mul2(x->b[i], w.b[i]);
 }
 
 struct Token {
@@ -121,7 +175,7 @@ struct Token {
 };
 
 // Sequence of `row`, then its position and place in the cache.
-__device__ __forceinline__ Token token_of(const RopeParams& p, long long row, bool report) {
+__device__ __forceinline__ Token token_of(const RopeParams& p, int row, bool report) {
   int n, t, len;
   if (p.cu) {
     int lo = 0, hi = p.N;
@@ -130,11 +184,11 @@ __device__ __forceinline__ Token token_of(const RopeParams& p, long long row, bo
       if (p.cu[mid] <= row) lo = mid; else hi = mid;
     }
     n = lo;
-    t = int(row) - p.cu[n];
+    t = row - p.cu[n];
     len = p.cu[n + 1] - p.cu[n];
   } else {
-    n = int(row / p.T);
-    t = int(row - (long long)n * p.T);
+    n = int(unsigned(row) / unsigned(p.T));
+    t = row - n * p.T;
     len = p.T;
   }
   Token k{p.positions ? p.positions[row] : t, -1, true};
@@ -158,144 +212,147 @@ __device__ __forceinline__ Token token_of(const RopeParams& p, long long row, bo
 
 }  // namespace
 
-// Items are (token, chunk of its passes): a pass is as many heads of q, then k, then (store) v as a warp holds.
-template <int D, bool kPairs>
-__global__ void __launch_bounds__(kWarps * 32) k_rope_fwd(const RopeParams p, int chunks, int per) {
-  wait_for_previous();
-  constexpr int kHeads = 256 / D;
-  const int lane = threadIdx.x & 31, sub = lane % (D / 8), which = lane / (D / 8);
-  const bool norm = p.qw != nullptr;
-  float wq[8], wk[8];
+// Heads of one kind (kKind 0: queries, 1: keys, 2: values, which are only copied) of a token, passes from .. to - 1 of as many heads
+// as a warp holds.
+template <int D, bool kPairs, int kKind>
+__device__ __forceinline__ void rope_heads(const RopeParams& p, const Lane<D, kPairs>& ln, const Share& w, bool norm, const Token& tk, int row, int which, int from, int to) {
+  constexpr int kHeads = 256 / D, kStep = kHeads * D;
+  const int heads = kKind ? p.Hk : p.H;
+  const __nv_bfloat16* src = (kKind == 0 ? p.q + row * p.q_s : kKind == 1 ? p.k + row * p.k_s : p.v + row * p.v_s) + which * D;
+  __nv_bfloat16* dst = (kKind == 0 ? p.qo : p.ko) + (long long)row * heads * D + which * D;
+  __nv_bfloat16* cache = kKind ? (kKind == 1 ? p.kc : p.vc) + tk.cache_row * heads * D + which * D : nullptr;
+  const bool cached = kKind && tk.cache_row >= 0;
+  for (int p0 = from; p0 < to; p0 += kAhead) {
+    uint2 in[kAhead][2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    wq[i] = norm ? p.qw[sub * 8 + i] : 1.f;
-    wk[i] = norm ? p.kw[sub * 8 + i] : 1.f;
-  }
-  Turn<D, kPairs> turn(p, lane);
-  const int pq = (p.H + kHeads - 1) / kHeads, pk = (p.Hk + kHeads - 1) / kHeads, passes = pq + pk * (p.lengths ? 2 : 1);
-  const long long items = p.rows * chunks, step = (long long)gridDim.x * kWarps;
-  for (long long it = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); it < items; it += step) {
-    const long long row = it / chunks;
-    const int from = int(it - row * chunks) * per, to = min(passes, from + per);
-    const Token tk = token_of(p, row, lane == 0);
-    turn.at(tk.pos);
-    for (int p0 = from; p0 < to; p0 += kAhead) {
-      uint4 in[kAhead];
+    for (int a = 0; a < kAhead; ++a) {
+      in[a][0] = in[a][1] = make_uint2(0, 0);
+      if (p0 + a < to && (p0 + a) * kHeads + which < heads) ln.load(in[a], src + (p0 + a) * kStep);
+    }
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int ps = p0 + a;
-        const int kind = ps < pq ? 0 : ps < pq + pk ? 1 : 2, hh = (ps - (kind == 0 ? 0 : kind == 1 ? pq : pq + pk)) * kHeads + which;
-        const __nv_bfloat16* src = kind == 0 ? p.q + row * p.q_s : kind == 1 ? p.k + row * p.k_s : p.v + row * p.v_s;
-        in[a] = make_uint4(0, 0, 0, 0);
-        if (ps < to && hh < (kind ? p.Hk : p.H)) in[a] = *reinterpret_cast<const uint4*>(src + hh * D + sub * 8);
+    for (int a = 0; a < kAhead; ++a) {
+      if (p0 + a >= to) break;
+      const int at = (p0 + a) * kStep;
+      const bool there = (p0 + a) * kHeads + which < heads;
+      if (kKind == 2) {
+        if (there && cached) ln.store(in[a], cache + at);
+        continue;
       }
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int ps = p0 + a;
-        if (ps >= to) break;
-        const int kind = ps < pq ? 0 : ps < pq + pk ? 1 : 2, hh = (ps - (kind == 0 ? 0 : kind == 1 ? pq : pq + pk)) * kHeads + which;
-        const bool there = hh < (kind ? p.Hk : p.H);
-        const long long cached = tk.cache_row < 0 ? -1 : (tk.cache_row * p.Hk + hh) * D + sub * 8;
-        if (kind == 2) {
-          if (there && cached >= 0) *reinterpret_cast<uint4*>(p.vc + cached) = in[a];
-          continue;
-        }
-        float x[8];
-        unpack8(in[a], x);
-        if (norm) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-          const float rstd = rsqrtf(fmaf(head_sum<D>(ss), 1.f / D, p.eps));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * rstd * (kind ? wk[i] : wq[i]);
-        }
-        turn.template apply<false>(x);
-        const uint4 y = tk.live ? pack8(x) : make_uint4(0, 0, 0, 0);
-        if (!there) continue;
-        if (kind == 0) {
-          *reinterpret_cast<uint4*>(p.qo + (row * p.H + hh) * D + sub * 8) = y;
-        } else {
-          *reinterpret_cast<uint4*>(p.ko + (row * p.Hk + hh) * D + sub * 8) = y;
-          if (cached >= 0) *reinterpret_cast<uint4*>(p.kc + cached) = y;
-        }
+      Share x = ln.unpack(in[a]);
+      if (norm) {
+        const float rstd = rsqrtf(fmaf(head_dot<D>(x, x), 1.f / D, p.eps));
+        scale(&x, dup2(rstd));
+        times(&x, w);
       }
+      ln.template turn<false>(&x);
+      uint2 y[2];
+      ln.pack(x, y);
+      if (!tk.live) y[0] = y[1] = make_uint2(0, 0);
+      if (!there) continue;
+      ln.store(y, dst + at);
+      if (cached) ln.store(y, cache + at);
     }
   }
 }
 
-template <int D, bool kPairs>
-__global__ void __launch_bounds__(kWarps * 32) k_rope_bwd(const RopeParams p) {
+// blockIdx.y: the chunk of `per` of a token's passes (q's, then k's, then (store) v's).
+template <int D, bool kPairs, bool kStore>
+__global__ void __launch_bounds__(kWarps * 32, kFwdBlocks) k_rope_fwd(const RopeParams p, int per) {
+  constexpr int kHeads = 256 / D;
   wait_for_previous();
-  constexpr int kHeads = 256 / D, kTwo = 2;
-  __shared__ float part[kWarps][2][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % (D / 8), which = lane / (D / 8);
+  const int lane = threadIdx.x & 31, which = lane / (D / 8);
   const bool norm = p.qw != nullptr;
-  Turn<D, kPairs> turn(p, lane);
-  float dw[2][8] = {};
-  float w[2][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    w[0][i] = norm ? p.qw[sub * 8 + i] : 1.f;
-    w[1][i] = norm ? p.kw[sub * 8 + i] : 1.f;
+  Lane<D, kPairs> ln(p, lane);
+  const Share wq = ln.weights(p.qw), wk = ln.weights(p.kw);
+  const int pq = (p.H + kHeads - 1) / kHeads, pk = (p.Hk + kHeads - 1) / kHeads, from = blockIdx.y * per, to = from + per;
+  const int step = gridDim.x * kWarps;
+  for (int row = blockIdx.x * kWarps + (threadIdx.x >> 5); row < p.rows; row += step) {
+    const Token tk = token_of(p, row, lane == 0);
+    ln.at(tk.pos);
+    rope_heads<D, kPairs, 0>(p, ln, wq, norm, tk, row, which, from, min(to, pq));
+    rope_heads<D, kPairs, 1>(p, ln, wk, norm, tk, row, which, max(from - pq, 0), min(to - pq, pk));
+    if (kStore) rope_heads<D, kPairs, 2>(p, ln, wk, norm, tk, row, which, max(from - pq - pk, 0), min(to - pq - pk, pk));
   }
-  const long long step = (long long)gridDim.x * kWarps;
-  for (long long row = (long long)blockIdx.x * kWarps + warp; row < p.rows; row += step) {
-    turn.at(token_of(p, row, false).pos);
+}
+
+template <int D, bool kPairs>
+__global__ void __launch_bounds__(kWarps * 32, kBwdPerSm) k_rope_bwd(const RopeParams p) {
+  wait_for_previous();
+  constexpr int kHeads = 256 / D, kTogether = 4;
+  __shared__ float part[kWarps][2][D];
+  wait_for_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = lane / (D / 8);
+  const bool norm = p.qw != nullptr;
+  Lane<D, kPairs> ln(p, lane);
+  const Share w[2] = {ln.weights(p.qw), ln.weights(p.kw)};
+  Share dw[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) dw[k].a[i] = dw[k].b[i] = dup2(0.f);
+  const int step = gridDim.x * kWarps;
+  for (int row = blockIdx.x * kWarps + warp; row < p.rows; row += step) {
+    ln.at(token_of(p, row, false).pos);
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
       const int heads = kind ? p.Hk : p.H;
-      const __nv_bfloat16 *x_ = (kind ? p.k + row * p.k_s : p.q + row * p.q_s) + sub * 8, *dy_ = (kind ? p.dko : p.dqo) + row * heads * D + sub * 8;
-      __nv_bfloat16* dx_ = (kind ? p.dk : p.dq) + row * heads * D + sub * 8;
-      for (int h0 = 0; h0 < heads; h0 += kHeads * kTwo) {
-        uint4 xin[kTwo], din[kTwo];
+      const long long at = (long long)row * heads * D + which * D;
+      const __nv_bfloat16 *x_ = (kind ? p.k + row * p.k_s : p.q + row * p.q_s) + which * D, *dy_ = (kind ? p.dko : p.dqo) + at;
+      __nv_bfloat16* dx_ = (kind ? p.dk : p.dq) + at;
+      for (int h0 = 0; h0 < heads; h0 += kHeads * kTogether) {
+        uint2 xin[kTogether][2], din[kTogether][2];
 #pragma unroll
-        for (int a = 0; a < kTwo; ++a) {
+        for (int a = 0; a < kTogether; ++a) {
           const int hh = h0 + a * kHeads + which;
-          xin[a] = din[a] = make_uint4(0, 0, 0, 0);
+          xin[a][0] = xin[a][1] = din[a][0] = din[a][1] = make_uint2(0, 0);
           if (hh < heads) {
-            din[a] = *reinterpret_cast<const uint4*>(dy_ + hh * D);
-            if (norm) xin[a] = *reinterpret_cast<const uint4*>(x_ + hh * D);
+            ln.load(din[a], dy_ + (h0 + a * kHeads) * D);
+            if (norm) ln.load(xin[a], x_ + (h0 + a * kHeads) * D);
           }
         }
 #pragma unroll
-        for (int a = 0; a < kTwo; ++a) {
+        for (int a = 0; a < kTogether; ++a) {
           const int hh = h0 + a * kHeads + which;
-          float x[8], d[8];
-          unpack8(din[a], d);
-          turn.template apply<true>(d);
+          if (h0 + a * kHeads >= heads) break;
+          Share d = ln.unpack(din[a]);
+          ln.template turn<true>(&d);
           if (norm) {
-            unpack8(xin[a], x);
-            float ss = 0.f, dot = 0.f;
+            Share x = ln.unpack(xin[a]);
+            const float rstd = rsqrtf(fmaf(head_dot<D>(x, x), 1.f / D, p.eps));
+            scale(&x, dup2(rstd));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-            const float rstd = rsqrtf(fmaf(head_sum<D>(ss), 1.f / D, p.eps));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              x[i] *= rstd;
-              dw[kind][i] = fmaf(d[i], x[i], dw[kind][i]);  // zero where the head does not exist
-              d[i] *= w[kind][i];
-              dot = fmaf(d[i], x[i], dot);
+            for (int i = 0; i < 2; ++i) {  // zero where the head does not exist
+              dw[kind].a[i] = fma2(d.a[i], x.a[i], dw[kind].a[i]);
+              dw[kind].b[i] = fma2(d.b[i], x.b[i], dw[kind].b[i]);
             }
-            const float mean = head_sum<D>(dot) * (1.f / D);
+            times(&d, w[kind]);
+            const F2 mean = dup2(head_dot<D>(d, x) * (-1.f / D));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] = rstd * (d[i] - x[i] * mean);
+            for (int i = 0; i < 2; ++i) {
+              d.a[i] = fma2(x.a[i], mean, d.a[i]);
+              d.b[i] = fma2(x.b[i], mean, d.b[i]);
+            }
+            scale(&d, dup2(rstd));
           }
-          if (hh < heads) *reinterpret_cast<uint4*>(dx_ + hh * D) = pack8(d);
+          uint2 out[2];
+          ln.pack(d, out);
+          if (hh < heads) ln.store(out, dx_ + (h0 + a * kHeads) * D);
         }
       }
     }
   }
   if (!norm) return;
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind)
+  for (int kind = 0; kind < 2; ++kind) {
+    float x[8];
+    ln.join(dw[kind], x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float v = dw[kind][i];
 #pragma unroll
-      for (int d = D / 8; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-      if (which == 0) part[warp][kind][sub * 8 + i] = v;
+      for (int d = D / 8; d < 32; d <<= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], d);
+      if (which == 0) part[warp][kind][(i < 4 ? ln.ca : ln.cb - 4) + i] = x[i];
     }
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
     float v = 0.f;
@@ -324,20 +381,22 @@ __global__ void __launch_bounds__(1024) k_rope_dw(const RopeParams p, int blocks
 }
 
 namespace {
-constexpr int kBwdBlocks = 152 * 3;
+constexpr int kBwdBlocks = 152 * kBwdPerSm;
 
 template <int D, bool kPairs>
 cudaError_t fwd(const RopeParams& p, cudaStream_t s) {
   constexpr int kHeads = 256 / D;
   const int passes = (p.H + kHeads - 1) / kHeads + (p.Hk + kHeads - 1) / kHeads * (p.lengths ? 2 : 1);
   // a token to a warp, its passes shared among more while there are fewer warps than the SMs hold
-  const long long room = (long long)p.sms * 16;
+  const long long room = (long long)p.sms * kWarps * kFwdBlocks;
   int chunks = 1;
   if (p.rows < room) chunks = int(room / p.rows < passes ? room / p.rows : passes);
   const int per = (passes + chunks - 1) / chunks;
   chunks = (passes + per - 1) / per;
-  const long long want = (p.rows * chunks + kWarps - 1) / kWarps, most = (long long)p.sms * 8;
-  return launch_after(k_rope_fwd<D, kPairs>, dim3(unsigned(want < most ? want : most)), dim3(kWarps * 32), 0, s, p, chunks, per);
+  const long long want = (p.rows + kWarps - 1) / kWarps, most = (long long)p.sms * kFwdBlocks;
+  const dim3 grid(unsigned(want < most ? want : most), chunks);
+  return p.lengths ? launch_after(k_rope_fwd<D, kPairs, true>, grid, dim3(kWarps * 32), 0, s, p, per)
+                   : launch_after(k_rope_fwd<D, kPairs, false>, grid, dim3(kWarps * 32), 0, s, p, per);
 }
 
 template <int D, bool kPairs>

@@ -472,7 +472,7 @@ typedef struct {
   void *k_cache, *v_cache;   /* store: bf16 [num_pages,page_size,Hk,D], written in the new tokens' rows */
   const int32_t* page_table; /* store: device [num_seqs,table_width]: the sequence's pages in order */
   const int32_t* lengths;    /* store: device [num_seqs]: tokens of the sequence, the new ones among them */
-  void* workspace;           /* >= gdn_qk_norm_rope_workspace_size() bytes, 256-byte aligned */
+  void* workspace;           /* >= gdn_qk_norm_rope_workspace_size() bytes, 256-byte aligned; without cu_seqlens it may be NULL */
   size_t workspace_bytes;
   int* status;               /* or NULL */
 } gdn_rope_args_t;
@@ -517,7 +517,7 @@ typedef struct {
   const void *q, *k, *v;     /* bf16 [B,T,H,D], [B,T,Hk,D], [B,T,Hk,D] */
   void* o;                   /* bf16 [B,T,H,D] contiguous, written */
   float* lse;                /* fp32 [B,T,H], written */
-  void* workspace;           /* >= gdn_attn_fwd_workspace_size() bytes, 256-byte aligned */
+  void* workspace;           /* >= gdn_attn_fwd_workspace_size() bytes, 256-byte aligned; without cu_seqlens it may be NULL */
   size_t workspace_bytes;
   int* status;               /* or NULL; records a wait that ran out (GDN_ETIMEOUT), not reset by the call */
 } gdn_attn_fwd_args_t;

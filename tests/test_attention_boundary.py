@@ -65,7 +65,7 @@ def step_args(**kw):
     ("gdn_qk_norm_rope_fwd", rope_desc(rotary_dim=0), rope_args(inv_freq=None, q_weight=None, k_weight=None, positions=13 * MB)),
     ("gdn_qk_norm_rope_store", rope_desc(cu=[0, 7, 40]), rope_args()), ("gdn_qk_norm_rope_bwd", rope_desc(), rope_bwd()),
     ("gdn_qk_norm_rope_bwd", rope_desc(), rope_bwd(q_weight=None, k_weight=None, dq_weight=None, dk_weight=None)),
-    ("gdn_attn_fwd", attn_desc(), attn_fwd()), ("gdn_attn_bwd", attn_desc(), attn_bwd()), ("gdn_attn_step", step_desc(), step_args())])
+    ("gdn_attn_fwd", attn_desc(), attn_fwd(workspace=None, workspace_bytes=0)), ("gdn_attn_fwd", attn_desc(cu=[0, 40]), attn_fwd()), ("gdn_attn_bwd", attn_desc(), attn_bwd()), ("gdn_attn_step", step_desc(), step_args())])
 def test_complete_calls_pass_the_checks(name, desc, args):
     """They stop at the missing device."""
     assert getattr(_lib.load(), name)(ctypes.byref(desc), ctypes.byref(args), None) == _lib.GDN_EUNSUPPORTED
@@ -86,9 +86,17 @@ def test_rope_descriptions(kw, why):
 
 
 @pytest.mark.parametrize("kw,why", [(dict(q=None), "non-NULL"), (dict(q_weight=None), "both"), (dict(inv_freq=None), "inv_freq"), (dict(k=2 * MB + 8), "aligned"),
-                                    (dict(q_out=MB), "alias"), (dict(k_out=7 * MB + 16), "alias"), (dict(workspace_bytes=8), "workspace"), (dict(workspace=64 * MB + 8), "workspace")])
+                                    (dict(q_out=MB), "alias"), (dict(k_out=7 * MB + 16), "alias")])
 def test_rope_arguments(kw, why):
     refused("gdn_qk_norm_rope_fwd", rope_desc(), rope_args(**kw), why)
+
+
+@pytest.mark.parametrize("kw", [dict(workspace=None), dict(workspace_bytes=8), dict(workspace=64 * MB + 8)])
+def test_packed_calls_need_a_workspace(kw):
+    """For the documents' offsets or tiles; dense ones need none."""
+    refused("gdn_qk_norm_rope_fwd", rope_desc(cu=[0, 40]), rope_args(**kw), "workspace")
+    refused("gdn_qk_norm_rope_store", rope_desc(cu=[0, 40]), rope_args(**kw), "workspace")
+    refused("gdn_attn_fwd", attn_desc(cu=[0, 40]), attn_fwd(**kw), "workspace")
 
 
 @pytest.mark.parametrize("dkw,kw,why", [({}, dict(v=None), "non-NULL"), ({}, dict(lengths=None), "non-NULL"), ({}, dict(positions=20 * MB), "positions"), (dict(page_size=0), {}, "page"),
@@ -112,7 +120,7 @@ def test_attention_descriptions(kw, why):
     assert _lib.load().gdn_attn_bwd_workspace_size(ctypes.byref(attn_desc(**kw))) == 0
 
 
-@pytest.mark.parametrize("kw,why", [(dict(lse=None), "non-NULL"), (dict(v=3 * MB + 2), "aligned"), (dict(o=MB), "alias"), (dict(lse=4 * MB), "alias"), (dict(workspace_bytes=0), "workspace")])
+@pytest.mark.parametrize("kw,why", [(dict(lse=None), "non-NULL"), (dict(v=3 * MB + 2), "aligned"), (dict(o=MB), "alias"), (dict(lse=4 * MB), "alias")])
 def test_attention_forward_arguments(kw, why):
     refused("gdn_attn_fwd", attn_desc(), attn_fwd(**kw), why)
 
