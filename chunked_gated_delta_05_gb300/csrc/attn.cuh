@@ -63,6 +63,27 @@ __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volati
   return mbar_wait(bar, parity, abort, status, code);
 }
 
+// 16 lanes x 64 columns: registers 4 i .. 4 i + 3 hold columns 8 i + 2 (t % 4), + 1 of lane t / 4, then of lane t / 4 + 8 (t: the thread).
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
+        "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
+        "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr));
+}
+// 16 lanes x 32 columns: registers 2 i, 2 i + 1 go to column 4 i + t % 4 of lanes t / 4 and t / 4 + 8.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t* u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+        "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+      : "memory");
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -103,7 +124,7 @@ struct AttnParams {
   // backward
   const __nv_bfloat16 *dO, *o_in;  // [rows,H,D]
   const float* lse_in;
-  float *lse2, *delta;         // [H][rows]: lse log2(e), and the rows' sums of dO o
+  float *lse2, *delta;         // [H][rows]: -lse log2(e), and minus the rows' sums of dO o
   __nv_bfloat16 *dq, *dk, *dv;
   int* status;
 };
@@ -134,18 +155,13 @@ __device__ __forceinline__ void product_ss(uint32_t lead, uint32_t d, uint32_t a
     mma_ss<true>(lead, d, a + o, b + o, id);
   }
 }
-// d (+)= A B for half of the inner dimension, 64: A [128,64] in TMEM, B those 64 rows of a tile read MN-major.
-template <int D>
-__device__ __forceinline__ void product_ts_half(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, bool acc) {
+// d (+)= A B, A [128,128] in TMEM in parts of 2 kSteps columns, which lie at the first kSteps of their columns; B a tile read MN-major.
+template <int D, int kSteps>
+__device__ __forceinline__ void product_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, bool acc) {
   constexpr uint32_t id = idesc_bf16(kAttnTile, D, false, true);
+  constexpr int kPer = kSteps / 8;  // products of 16 inner entries in a part
 #pragma unroll
-  for (int s = 0; s < 4; ++s) mma_ts(lead, d, a + s * 8, b + s * 128, id, acc || s > 0);
-}
-// Both halves, A's `half` columns apart.
-template <int D>
-__device__ __forceinline__ void product_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t half, uint32_t b, bool acc) {
-  product_ts_half<D>(lead, d, a, b, acc);
-  product_ts_half<D>(lead, d, a + half, b + 4 * 128, true);
+  for (int s = 0; s < kAttnTile / 16; ++s) mma_ts(lead, d, a + (s / kPer) * 2 * kSteps + (s % kPer) * 8, b + s * 128, id, acc || s > 0);
 }
 // A ring of kN stages walked kStep uses at a time: this use's stage and phase.
 template <int kN, int kStep>

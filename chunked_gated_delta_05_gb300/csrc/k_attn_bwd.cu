@@ -16,16 +16,18 @@
 // them runs, the softmax warps turn the scores (or dP) of the other pair's into the next operand.
 // k_attn_dq: S = Q K^T, dP = dO V^T, dQ += dS K (dS over S in TMEM; S double-buffered, a tile ahead).
 //
-// Eight softmax warps, two threads a TMEM lane, each on half of a tile's columns. The bf16 operand halves lie over the columns
-// that their own writers have read. p and dS are rounded to bf16 (as the products' operands); all sums are fp32.
+// Eight softmax warps, two to a quarter of the TMEM lanes, each on half of a tile's columns. The bf16 operand's halves lie over the
+// columns that their own writers have read. p and dS are rounded to bf16 (as the products' operands); all sums are fp32.
 #include "attn.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kThreads = 384;                        // 8 softmax warps, the MMA warp, the TMA warp, two gate warps
+constexpr int kMma = 8, kTma = 9, kGate = 10;        // the latter four
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 8 x 208 + 4 x 88 = 12 x 168, the launch's
 constexpr int kSoftmax = 256;
+constexpr int kCols = 64;                            // columns of a tile to a softmax warp
 
 template <int D>
 struct Cfg {
@@ -61,7 +63,7 @@ __device__ __forceinline__ uint32_t phase(int i, int n) { return uint32_t(i / n)
 
 }  // namespace
 
-// D_i and lse_i log2(e) of 32 rows of a head a warp.
+// -D_i and -lse_i log2(e) of 32 rows of a head a warp.
 template <int D>
 __global__ void __launch_bounds__(256) k_attn_delta(const AttnParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
@@ -91,8 +93,8 @@ __global__ void __launch_bounds__(256) k_attn_delta(const AttnParams p) {
   }
   const long long row = row0 + lane;
   if (row < p.rows) {
-    p.delta[h * p.rows + row] = mine;
-    p.lse2[h * p.rows + row] = p.lse_in[row * p.H + h] * kLog2e;
+    p.delta[h * p.rows + row] = -mine;
+    p.lse2[h * p.rows + row] = p.lse_in[row * p.H + h] * -kLog2e;
   }
 }
 
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int all = (tl.len + kAttnTile - 1) / kAttnTile, i0 = p.causal ? tl.first / kAttnTile : 0, per = all - i0, n = per * p.group;
   const bool ragged = all * kAttnTile > tl.len;
 
-  if (warp == 8) tmem_alloc(tslot, 512);
+  if (warp == kMma) tmem_alloc(tslot, 512);
   if (tid == 0) {
     *abort_flag = 0;
     mbar_init(kv_full, 1);
@@ -135,9 +137,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   constexpr uint32_t tS = 0, tP = 128, tV = 256, tK = 256 + D;  // all of TMEM, so it starts at column 0
 
-  if (warp >= 8) {
+  if (warp >= kMma) {
     regs_dec<kOtherRegs>();
-    if (warp == 9) {
+    if (warp == kTma) {
       // ---------------- producer ----------------
       if (lane == 0) {
         mbar_expect_tx(kv_full, 2 * kTile);
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = lane; e < kAttnTile; e += 32) {
           const bool in = q0 + e < tl.len;
-          v[e] = in ? p.lse2[at + e] : INFINITY;
+          v[e] = in ? p.lse2[at + e] : -INFINITY;
           v[128 + e] = in ? p.delta[at + e] : 0.f;
         }
         if (ragged && q0 + kAttnTile > tl.len) {
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_drain(&q_full[slot(it, kQ)], phase(it, kQ), 1000000ull);
         mbar_drain(&o_full[slot(it, kO)], phase(it, kO), 1000000ull);
       }
-    } else if (warp == 8) {
+    } else if (warp == kMma) {
       // ---------------- MMA issuer ----------------
       const uint32_t lead = elect_lead();
       const uint32_t aK = desc_low_k(smem_u32(sK)), aV = desc_low_k(smem_u32(sV)), bQ = desc_low_k(smem_u32(sQ)), bO = desc_low_k(smem_u32(sO)),
@@ -212,20 +214,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int qs = rq.at, os = it & 1;
         rq.next();
-        product_ts<D>(lead, tV, tS, 64, nO + os * (kTile >> 4), it > 0);
+        product_ts<D, kCols / 2>(lead, tV, tS, nO + os * (kTile >> 4), it > 0);
         commit(lead, &o_empty[os]);
         if (it + 1 < n) scores(rq.at);
         if (!(ok = wait(ds_ready, it & 1, kDevTimeoutSync))) break;
         tc_fence_after();
-        product_ts<D>(lead, tK, tP, 64, nQ + qs * (kTile >> 4), it > 0);
+        product_ts<D, kCols / 2>(lead, tK, tP, nQ + qs * (kTile >> 4), it > 0);
         commit(lead, &q_empty[qs]);
         if (it + 1 < n) dprobs(os ^ 1);
       }
       commit(lead, done);  // the softmax warps wait for it, or, after an error:
       if (!ok) mbar_drain(done, 0);
-    } else if (warp >= 10 && lane == 0) {
-      // ---------------- gates: warp 10 for S(it + 1) behind dV(it), warp 11 for dP(it + 1) behind dK(it) ----------------
-      uint64_t* bar = warp == 10 ? p_ready : ds_ready;
+    } else if (warp >= kGate && lane == 0) {
+      // ---------------- gates: one warp for S(it + 1) behind dV(it), the other for dP(it + 1) behind dK(it) ----------------
+      uint64_t* bar = warp == kGate ? p_ready : ds_ready;
       Ring<kQ, 1> rq(0);
       bool ok = true;
       for (int it = 0; it < n && ok; ++it) {
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it + 1 < n) {
           const int os = (it + 1) & 1;
           const uint32_t ph = phase(it + 1, kO);
-          ok = warp == 10 ? attn_wait(&q_full[rq.at], rq.phase, abort_flag, p.status, kDevTimeoutTma) && attn_wait(&ready[os], ph, abort_flag, p.status, kDevTimeoutSync)
+          ok = warp == kGate ? attn_wait(&q_full[rq.at], rq.phase, abort_flag, p.status, kDevTimeoutTma) && attn_wait(&ready[os], ph, abort_flag, p.status, kDevTimeoutSync)
                           : attn_wait(&o_full[os], ph, abort_flag, p.status, kDevTimeoutTma);
           if (!ok) break;
         }
@@ -242,38 +244,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---------------- softmax: key row, half of the queries ----------------
+    // ---------------- softmax: 32 key rows a warp, half of the queries ----------------
+    // The rows' values come as the products' fragments (four rows and every fourth pair of columns a thread), so that a query's
+    // lse and D, which differ by column, are read from shared memory once for four rows: with a row a thread those reads took 128
+    // KB of shared memory's bandwidth an iteration, beside 192 KB of the products' and 64 KB of the copies'.
     regs_inc<kSoftmaxRegs>();
-    const int half = warp >> 2, row = tid & 127, key = tl.first + row;
-    const uint32_t lb = tmem_lane_base(warp) + uint32_t(half) * 64;
-    const F2 c2 = dup2(p.scale * kLog2e), minus = dup2(-1.f);
+    const int half = warp >> 2, g = lane >> 2, col = (lane & 3) * 2, key0 = (warp & 3) * 32 + g;  // rows key0 + 8 r
+    const uint32_t lane0 = tmem_lane_base(warp), lb = lane0 + uint32_t(half) * kCols;
+    const F2 c2 = dup2(p.scale * kLog2e);
     bool ok = true;
     for (int it = 0; it < n && ok; ++it) {
-      const int q0 = (i0 + it % per) * kAttnTile + half * 64, os = slot(it, kO);
-      const float4 *lse = reinterpret_cast<const float4*>(vec + os * 256 + half * 64), *delta = lse + 32;
-      ok = attn_wait(&ready[os], phase(it, kO), abort_flag, p.status, kDevTimeoutSync) &&
-           attn_wait(s_full, it & 1, abort_flag, p.status, kDevTimeoutMma);
+      const int q0 = (i0 + it % per) * kAttnTile + half * kCols, os = it & 1;
+      const float2 *lse = reinterpret_cast<const float2*>(vec + os * 256 + half * kCols + col), *delta = lse + 64;
+      ok = attn_wait(&ready[os], phase(it, kO), abort_flag, p.status, kDevTimeoutSync) && attn_wait(s_full, it & 1, abort_flag, p.status, kDevTimeoutMma);
       if (!ok) break;
       tc_fence_after();
+      // w[32 h + 4 b + 2 r + y]: row key0 + 16 h + 8 r, column 8 b + col + y
       float w[64];
-      tmem_ld64(tS + lb, w);
+      tmem_ld_16x64(tS + lb, w);
+      tmem_ld_16x64(tS + lb + (16u << 16), w + 32);
       tmem_wait_ld_regs(w);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float4 l = lse[e];
-        float* x = w + 4 * e;
-        unf2(fma2(f2(x[0], x[1]), c2, mul2(f2(l.x, l.y), minus)), &x[0], &x[1]);
-        unf2(fma2(f2(x[2], x[3]), c2, mul2(f2(l.z, l.w), minus)), &x[2], &x[3]);
+      for (int b = 0; b < 8; ++b) {
+        const float2 l = lse[4 * b];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = exp2_approx(x[u]);
+        for (int r = 0; r < 4; ++r) {
+          float* x = w + (r >> 1) * 32 + 4 * b + (r & 1) * 2;
+          unf2(fma2(f2(x[0], x[1]), c2, f2(l.x, l.y)), &x[0], &x[1]);
+          x[0] = exp2_approx(x[0]);
+          x[1] = exp2_approx(x[1]);
+        }
       }
-      const int from = p.causal ? key - q0 : 0, to = tl.len - q0;  // of the half's queries, those that see the key
-      if (to < 64 || (p.causal && tl.first + kAttnTile > q0)) {
+      const int to = tl.len - q0 - col;  // columns (from this thread's first) of queries that exist
+      if (tl.len - q0 < kCols || (p.causal && tl.first + kAttnTile > q0)) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (e < from || e >= to) w[e] = 0.f;
+        for (int r = 0; r < 4; ++r) {
+          const int from = p.causal ? tl.first + key0 + 8 * r - q0 - col : 0;  // and of those that see the row's key
+#pragma unroll
+          for (int b = 0; b < 8; ++b)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              if (8 * b + y < from || 8 * b + y >= to) w[(r >> 1) * 32 + 4 * b + (r & 1) * 2 + y] = 0.f;
+        }
       }
-      store_operand(tS + lb, w);
+      uint32_t out[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) out[e] = pack_bf16(w[2 * e], w[2 * e + 1]);
+      tmem_st_16x32(tS + lb, out);
+      tmem_st_16x32(tS + lb + (16u << 16), out + 16);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(p_ready);
@@ -281,32 +299,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       float d[64];
-      tmem_ld64(tP + lb, d);
+      tmem_ld_16x64(tP + lb, d);
+      tmem_ld_16x64(tP + lb + (16u << 16), d + 32);
       tmem_wait_ld_regs(d);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float4 l = delta[e];
-        float *x = d + 4 * e, *y = w + 4 * e;
-        unf2(mul2(f2(y[0], y[1]), fma2(f2(l.x, l.y), minus, f2(x[0], x[1]))), &x[0], &x[1]);
-        unf2(mul2(f2(y[2], y[3]), fma2(f2(l.z, l.w), minus, f2(x[2], x[3]))), &x[2], &x[3]);
+      for (int b = 0; b < 8; ++b) {
+        const float2 l = delta[4 * b];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int at = (r >> 1) * 32 + 4 * b + (r & 1) * 2;
+          unf2(mul2(f2(w[at], w[at + 1]), add2(f2(d[at], d[at + 1]), f2(l.x, l.y))), &d[at], &d[at + 1]);
+        }
       }
       mbar_arrive(&vec_free[os]);
-      store_operand(tP + lb, d);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) out[e] = pack_bf16(d[2 * e], d[2 * e + 1]);
+      tmem_st_16x32(tP + lb, out);
+      tmem_st_16x32(tP + lb + (16u << 16), out + 16);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(ds_ready);
     }
     if (ok && attn_wait(done, 0, abort_flag, p.status, kDevTimeoutMma)) {
       tc_fence_after();
+      const int key = tl.first + (tid & 127);
       __nv_bfloat16* dst = (half ? p.dk : p.dv) + ((size_t(tl.row0) + key) * p.Hk + hk) * D;
-      const uint32_t acc = (half ? tK : tV) + tmem_lane_base(warp);
+      const uint32_t acc = (half ? tK : tV) + lane0;
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) store_row(dst + q * 32, acc + q * 32, half ? p.scale : 1.f, key < tl.len);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(*tslot, 512);
+  if (warp == kMma) tmem_dealloc(*tslot, 512);
 }
 
 template <int D>
@@ -329,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int all = (tl.len + kAttnTile - 1) / kAttnTile, n = p.causal ? tl.first / kAttnTile + 1 : all;
   const bool tail = n * kAttnTile > tl.len;
 
-  if (warp == 8) tmem_alloc(tslot, 512);
+  if (warp == kMma) tmem_alloc(tslot, 512);
   if (tid == 0) {
     *abort_flag = 0;
     mbar_init(q_full, 1);
@@ -347,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t tP = 256, tQ = 384;  // all of TMEM, so it starts at column 0
   auto tS = [&](int i) { return uint32_t(i & 1) * 128; };
 
-  if (warp >= 8) {
+  if (warp >= kMma) {
     regs_dec<kOtherRegs>();
-    if (warp == 9) {
+    if (warp == kTma) {
       // ---------------- producer ----------------
       int it = 0;
       if (lane == 0) {
@@ -380,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async_smem();
         mbar_arrive(tail_ready);
       }
-    } else if (warp == 8) {
+    } else if (warp == kMma) {
       // ---------------- MMA issuer ----------------
       const uint32_t lead = elect_lead();
       const uint32_t aQ = desc_low_k(smem_u32(sQ)), aO = desc_low_k(smem_u32(sO)), bK = desc_low_k(smem_u32(sK)), bV = desc_low_k(smem_u32(sV)),
@@ -410,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait(ds_ready, i & 1, kDevTimeoutSync))) break;
         tc_fence_after();
         if (i + 1 < n) dprobs(i + 1);
-        product_ts<D>(lead, tQ, tS(i), 64, nK + rk.at * (kTile >> 4), i > 0);
+        product_ts<D, kCols / 2>(lead, tQ, tS(i), nK + rk.at * (kTile >> 4), i > 0);
         commit(lead, &k_empty[rk.at]);
         rk.next();
         // K of the tile after next is requested when the product before this one has let go of its stage
@@ -418,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       commit(lead, done);  // the softmax warps wait for it, or, after an error:
       if (!ok) mbar_drain(done, 0);
-    } else if (warp == 10 && lane == 0) {
+    } else if (warp == kGate && lane == 0) {
       // ---------------- gate: V of the product that follows dS(i) has landed ----------------
       auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
       bool ok = true;
@@ -432,20 +457,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- softmax: query row, half of the keys ----------------
     regs_inc<kSoftmaxRegs>();
     const int half = warp >> 2, row = tid & 127, qi = tl.first + row;
-    const uint32_t lane0 = tmem_lane_base(warp), lb = lane0 + uint32_t(half) * 64;
+    const uint32_t lane0 = tmem_lane_base(warp), lb = lane0 + uint32_t(half) * kCols;
     const bool mine = qi < tl.len;
     const long long at = (long long)h * p.rows + tl.row0 + qi;
-    const F2 c2 = dup2(p.scale * kLog2e), lse = dup2(mine ? -p.lse2[at] : 0.f), delta = dup2(mine ? -p.delta[at] : 0.f);
+    const F2 c2 = dup2(p.scale * kLog2e), lse = dup2(mine ? p.lse2[at] : 0.f), delta = dup2(mine ? p.delta[at] : 0.f);
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
       ok = attn_wait(&s_full[i & 1], (i >> 1) & 1, abort_flag, p.status, kDevTimeoutMma);
       if (!ok) break;
       tc_fence_after();
-      float w[64], d[64];
+      float w[kCols], d[kCols];
       tmem_ld64(tS(i) + lb, w);
       tmem_wait_ld_regs(w);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
+      for (int e = 0; e < kCols / 2; ++e) {
         float a, b;
         unf2(fma2(f2(w[2 * e], w[2 * e + 1]), c2, lse), &a, &b);
         w[2 * e] = exp2_approx(a);
@@ -457,12 +482,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld64(tP + lb, d);
       tmem_wait_ld_regs(d);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) unf2(mul2(f2(w[2 * e], w[2 * e + 1]), add2(f2(d[2 * e], d[2 * e + 1]), delta)), &d[2 * e], &d[2 * e + 1]);
-      const int k0 = i * kAttnTile;
+      for (int e = 0; e < kCols / 2; ++e) unf2(mul2(f2(w[2 * e], w[2 * e + 1]), add2(f2(d[2 * e], d[2 * e + 1]), delta)), &d[2 * e], &d[2 * e + 1]);
       if (i + 1 == n && (p.causal || tail)) {
-        const int seen = (p.causal ? min(qi + 1, tl.len) : tl.len) - k0 - half * 64;
+        const int seen = (p.causal ? min(qi + 1, tl.len) : tl.len) - i * kAttnTile - half * kCols;
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
+        for (int e = 0; e < kCols; ++e)
           if (e >= seen) d[e] = 0.f;
       }
       store_operand(tS(i) + lb, d);
@@ -479,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(*tslot, 512);
+  if (warp == kMma) tmem_dealloc(*tslot, 512);
 }
 
 template <int D>

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!all_wait(&p_full[t], cnt[t] & 1, kDevTimeoutSync)) return false;
         ++cnt[t];
         tc_fence_after();
-        product_ts<D>(lead, 256 + uint32_t(t) * D, uint32_t(t) * 128, 32, vv + rv.at * (kTile >> 4), j > 0);
+        product_ts<D, 64>(lead, 256 + uint32_t(t) * D, uint32_t(t) * 128, vv + rv.at * (kTile >> 4), j > 0);
         return true;
       };
       for (long long rd = 0; rd < rounds && ok; ++rd) {
