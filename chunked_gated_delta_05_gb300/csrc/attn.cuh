@@ -155,13 +155,30 @@ __device__ __forceinline__ void product_ss(uint32_t lead, uint32_t d, uint32_t a
     mma_ss<true>(lead, d, a + o, b + o, id);
   }
 }
-// d (+)= A B, A [128,128] in TMEM in parts of 2 kSteps columns, which lie at the first kSteps of their columns; B a tile read MN-major.
-template <int D, int kSteps>
+// d (+)= A B for steps kFrom .. kTo - 1 of 16 inner entries, A [128,128] in TMEM in parts of 2 kPart columns of which the first kPart
+// hold it; B a tile read MN-major.
+template <int D, int kPart, int kFrom, int kTo>
 __device__ __forceinline__ void product_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, bool acc) {
   constexpr uint32_t id = idesc_bf16(kAttnTile, D, false, true);
-  constexpr int kPer = kSteps / 8;  // products of 16 inner entries in a part
+  constexpr int kPer = kPart / 8;  // steps in a part
 #pragma unroll
-  for (int s = 0; s < kAttnTile / 16; ++s) mma_ts(lead, d, a + (s / kPer) * 2 * kSteps + (s % kPer) * 8, b + s * 128, id, acc || s > 0);
+  for (int s = kFrom; s < kTo; ++s) mma_ts(lead, d, a + (s / kPer) * 2 * kPart + (s % kPer) * 8, b + s * 128, id, acc || s > kFrom);
+}
+// 32 bf16 of a row times f from 32 fp32 columns, to 16-byte aligned memory (32-byte aligned: whole sectors a store).
+__device__ __forceinline__ void store_bf16x32(__nv_bfloat16* dst, const float* x, float f, bool wide) {
+  uint32_t u[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) u[e] = pack_bf16(x[2 * e] * f, x[2 * e + 1] * f);
+  if (wide) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 2 * e), "r"(u[e]), "r"(u[e + 1]), "r"(u[e + 2]), "r"(u[e + 3]), "r"(u[e + 4]), "r"(u[e + 5]),
+                   "r"(u[e + 6]), "r"(u[e + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(dst + 2 * e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+  }
 }
 // A ring of kN stages walked kStep uses at a time: this use's stage and phase.
 template <int kN, int kStep>

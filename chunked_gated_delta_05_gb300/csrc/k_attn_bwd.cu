@@ -44,17 +44,11 @@ __device__ __forceinline__ void store_operand(uint32_t t, const float* x) {
 }
 
 // 32 columns of an accumulator row times f, as bf16.
-__device__ __forceinline__ void store_row(__nv_bfloat16* dst, uint32_t t, float f, bool mine) {
+__device__ __forceinline__ void store_row(__nv_bfloat16* dst, uint32_t t, float f, bool mine, bool wide) {
   float o[32];
   tmem_ld32(t, o);
   tmem_wait_ld_regs(o);
-  if (!mine) return;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float* x = o + 8 * e;
-    *reinterpret_cast<uint4*>(dst + 8 * e) =
-        make_uint4(pack_bf16(x[0] * f, x[1] * f), pack_bf16(x[2] * f, x[3] * f), pack_bf16(x[4] * f, x[5] * f), pack_bf16(x[6] * f, x[7] * f));
-  }
+  if (mine) store_bf16x32(dst, o, f, wide);
 }
 
 // Ring position and phase of use i.
@@ -214,12 +208,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int qs = rq.at, os = it & 1;
         rq.next();
-        product_ts<D, kCols / 2>(lead, tV, tS, nO + os * (kTile >> 4), it > 0);
+        product_ts<D, kCols / 2, 0, kAttnTile / 16>(lead, tV, tS, nO + os * (kTile >> 4), it > 0);
         commit(lead, &o_empty[os]);
         if (it + 1 < n) scores(rq.at);
         if (!(ok = wait(ds_ready, it & 1, kDevTimeoutSync))) break;
         tc_fence_after();
-        product_ts<D, kCols / 2>(lead, tK, tP, nQ + qs * (kTile >> 4), it > 0);
+        product_ts<D, kCols / 2, 0, kAttnTile / 16>(lead, tK, tP, nQ + qs * (kTile >> 4), it > 0);
         commit(lead, &q_empty[qs]);
         if (it + 1 < n) dprobs(os ^ 1);
       }
@@ -323,10 +317,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && attn_wait(done, 0, abort_flag, p.status, kDevTimeoutMma)) {
       tc_fence_after();
       const int key = tl.first + (tid & 127);
+      const bool wide = (reinterpret_cast<uintptr_t>(half ? p.dk : p.dv) & 31) == 0;
       __nv_bfloat16* dst = (half ? p.dk : p.dv) + ((size_t(tl.row0) + key) * p.Hk + hk) * D;
       const uint32_t acc = (half ? tK : tV) + lane0;
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) store_row(dst + q * 32, acc + q * 32, half ? p.scale : 1.f, key < tl.len);
+      for (int q = 0; q < D / 32; ++q) store_row(dst + q * 32, acc + q * 32, half ? p.scale : 1.f, key < tl.len, wide);
     }
   }
   tc_fence_before();
@@ -435,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait(ds_ready, i & 1, kDevTimeoutSync))) break;
         tc_fence_after();
         if (i + 1 < n) dprobs(i + 1);
-        product_ts<D, kCols / 2>(lead, tQ, tS(i), nK + rk.at * (kTile >> 4), i > 0);
+        product_ts<D, kCols / 2, 0, kAttnTile / 16>(lead, tQ, tS(i), nK + rk.at * (kTile >> 4), i > 0);
         commit(lead, &k_empty[rk.at]);
         rk.next();
         // K of the tile after next is requested when the product before this one has let go of its stage
@@ -496,9 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && attn_wait(done, 0, abort_flag, p.status, kDevTimeoutMma)) {
       tc_fence_after();
+      const bool wide = (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
       __nv_bfloat16* dst = p.dq + ((size_t(tl.row0) + qi) * p.H + h) * D + half * (D / 2);
 #pragma unroll
-      for (int q = 0; q < D / 64; ++q) store_row(dst + q * 32, tQ + lane0 + half * (D / 2) + q * 32, p.scale, mine);
+      for (int q = 0; q < D / 64; ++q) store_row(dst + q * 32, tQ + lane0 + half * (D / 2) + q * 32, p.scale, mine, wide);
     }
   }
   tc_fence_before();

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = sm + 2 * kTile;
-  __shared__ uint64_t q_full[2], q_empty[2], kv_full[kS], kv_empty[kS], zeroed[kS], s_full[2], p_full[2], o_full[2], drained;
+  __shared__ uint64_t q_full[2], q_empty[2], kv_full[kS], kv_empty[kS], zeroed[kS], s_full[2], p_full[2][2], o_full[2], drained;
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
 
@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[t], 1);
       mbar_init(&q_empty[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], kAttnTile + 1);
+      mbar_init(&p_full[t][0], kAttnTile + 1);
+      mbar_init(&p_full[t][1], kAttnTile + 1);
       mbar_init(&o_full[t], 1);
     }
     for (int i = 0; i < kS; ++i) {
@@ -161,42 +162,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q = desc_low_k(smem_u32(sm)), kk = desc_low_k(smem_u32(sKV)), vv = desc_low_mn(smem_u32(sKV), kAttnPanel);
       Ring<kS, 2> rk(0), rv(1);
       uint32_t cnt[2] = {0, 0}, q_use[2] = {0, 0};  // iterations and items of either tile so far
-      bool ok = true;
+      bool ok = true, begun[2];
       auto all_wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, wait(b, ph, code))); };
-      auto scores = [&](int t, bool last) {
-        product_ss<D>(lead, uint32_t(t) * 128, q + t * (kTile >> 4), kk + rk.at * (kTile >> 4));
+      auto scores = [&](int t, int at, bool last) {
+        product_ss<D>(lead, uint32_t(t) * 128, q + t * (kTile >> 4), kk + at * (kTile >> 4));
         commit(lead, &s_full[t]);
         if (last) commit(lead, &q_empty[t]);
       };
       auto outputs = [&](int t, int j) {
-        if (!all_wait(&p_full[t], cnt[t] & 1, kDevTimeoutSync)) return false;
-        ++cnt[t];
+        const uint32_t v = vv + rv.at * (kTile >> 4), d = 256 + uint32_t(t) * D;
+        if (!all_wait(&p_full[t][0], cnt[t] & 1, kDevTimeoutSync)) return false;
         tc_fence_after();
-        product_ts<D, 64>(lead, 256 + uint32_t(t) * D, uint32_t(t) * 128, vv + rv.at * (kTile >> 4), j > 0);
+        product_ts<D, 64, 0, 4>(lead, d, uint32_t(t) * 128, v, j > 0);
+        if (!all_wait(&p_full[t][1], cnt[t]++ & 1, kDevTimeoutSync)) return false;
+        tc_fence_after();
+        product_ts<D, 64, 4, 8>(lead, d, uint32_t(t) * 128, v, true);
         return true;
       };
-      for (long long rd = 0; rd < rounds && ok; ++rd) {
-        if (!item_of(p, rd, total, &it)) break;
-        // A tile's first scores overwrite the weights of the item before it, which the products issued so far have read; its first
-        // output product waits for weights from threads that have taken the item's output out before.
-        ok = all_wait(&kv_full[rk.at], rk.phase, kDevTimeoutTma);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || !it.n[t]) continue;
-          ok = all_wait(&q_full[t], q_use[t]++ & 1, kDevTimeoutTma);
-          if (ok) scores(t, it.n[t] == 1);
-        }
+      // A tile's first scores of an item overwrite the weights of the item before it, which the products issued so far have read; its
+      // first output product waits for weights from threads that have taken the former item's output out before.
+      auto begin = [&](int t, const Item& x, int use) {  // use: of the item's first K tile
+        begun[t] = true;
+        if (!x.n[t]) return true;
+        if (!all_wait(&kv_full[use % kS], use / kS & 1, kDevTimeoutTma) || !all_wait(&q_full[t], q_use[t]++ & 1, kDevTimeoutTma)) return false;
+        scores(t, use % kS, x.n[t] == 1);
+        return true;
+      };
+      Item next;
+      int use = 0;
+      bool more = item_of(p, 0, total, &it);
+      if (more) ok = begin(0, it, 0) && begin(1, it, 0);
+      for (long long rd = 0; more && ok; ++rd) {
+        more = item_of(p, rd + 1, total, &next);
+        use += 2 * it.most;
+        begun[0] = begun[1] = false;
         for (int j = 0; j < it.most && ok; ++j) {
           rk.next();
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (!ok || j >= it.n[t]) continue;
+            if (!ok) continue;
+            if (j >= it.n[t]) {  // ahead of the other tile: the next item's scores meanwhile
+              if (t == 0 && more && !begun[0]) ok = begin(0, next, use);
+              continue;
+            }
             if (!(ok = outputs(t, j))) break;
-            if (j + 1 < it.n[t]) scores(t, j + 2 == it.n[t]);
+            if (j + 1 < it.n[t]) scores(t, rk.at, j + 2 == it.n[t]);
             else commit(lead, &o_full[t]);
           }
           rv.next();
         }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && more && !begun[t]) ok = begin(t, next, use);
+        it = next;
       }
       if (!ok) {  // the products in flight end before their accumulators are given up
         commit(lead, &drained);
@@ -218,12 +236,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           rv.next();
           if (it.tail && j + 1 == it.most) zeros ^= 1u << v;
           if (j >= it.n[t]) continue;
-          ok = wait(&kv_full[v], v_phase, kDevTimeoutTma) && (j + 1 == it.n[t] || wait(&kv_full[rk.at], rk.phase, kDevTimeoutTma)) &&
-               (!it.tail || j + 1 < it.most || wait(&zeroed[v], ~zeros >> v & 1u, kDevTimeoutSync));
+          ok = wait(&kv_full[v], v_phase, kDevTimeoutTma) && (!it.tail || j + 1 < it.most || wait(&zeroed[v], ~zeros >> v & 1u, kDevTimeoutSync));
           if (!ok) break;
-          mbar_arrive(&p_full[t]);
+          mbar_arrive(&p_full[t][0]);
+          if (j + 1 < it.n[t] && !(ok = wait(&kv_full[rk.at], rk.phase, kDevTimeoutTma))) break;
+          mbar_arrive(&p_full[t][1]);
           // weights j are there: their scores are done, and the output product of the weights before them
-          ok = wait(&p_full[t], cnt++ & 1, kDevTimeoutSync);
+          ok = wait(&p_full[t][1], cnt++ & 1, kDevTimeoutSync);
           if (!ok) break;
           if (frees) {
             mbar_arrive(&kv_empty[k]);
@@ -257,10 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Weights against the reference at hand, and the row's maximum beside them (the two run on different units): only where
         // that lies too far above the reference does it move, and the weights are taken again from the scores in TMEM.
         const F2 before = l2;
-        float w[64];
+        F2 mc;
+        float s[128], w[32];
 #pragma unroll 1
         while (true) {
-          float s[128];
           tmem_ld64(tS(t) + lb, s);
           tmem_ld64(tS(t) + lb + 64, s + 64);
           tmem_wait_ld_regs(s);
@@ -278,12 +297,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[e + u], s[e + 4 + u]);
             m = max3(max3(mx[0], mx[1], s[124]), max3(mx[2], mx[3], s[125]), fmaxf(s[126], s[127]));
           }
-          const F2 mc = dup2(-m * c);
+          mc = dup2(-m * c);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {
+          for (int e = 0; e < 32; ++e) {
             float a, b;
             mx[e & 3] = max3(mx[e & 3], s[2 * e], s[2 * e + 1]);
+            mx[(e + 2) & 3] = max3(mx[(e + 2) & 3], s[64 + 2 * e], s[65 + 2 * e]);
             unf2(fma2(f2(s[2 * e], s[2 * e + 1]), c2, mc), &a, &b);
             a = exp2_approx(a);
             b = exp2_approx(b);
@@ -306,14 +326,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tmem_st32(tS(t) + lb, w);
-        tmem_st32(tS(t) + lb + 32, w + 32);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_full[t]);
+        mbar_arrive(&p_full[t][0]);  // the product of the first half may start
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          float a, b;
+          unf2(fma2(f2(s[64 + 2 * e], s[65 + 2 * e]), c2, mc), &a, &b);
+          a = exp2_approx(a);
+          b = exp2_approx(b);
+          l2 = add2(l2, f2(a, b));
+          w[e] = __uint_as_float(pack_bf16(a, b));
+        }
+        tmem_st32(tS(t) + lb + 32, w);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[t][1]);
       }
       if (!ok || !(ok = wait(&o_full[t], outs++ & 1, kDevTimeoutMma))) break;
       tc_fence_after();
       const float l = sum2(l2), r = 1.f / l;
+      const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
       const size_t at = (size_t(it.tl.row0) + qi) * p.H + it.h;
       if (qi < len) p.lse[at] = m * p.scale + logf(l);
 #pragma unroll
@@ -321,13 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float o[32];
         tmem_ld32(tO(t) + lb + q * 32, o);
         tmem_wait_ld_regs(o);
-        if (qi < len)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float* x = o + 8 * e;
-            *reinterpret_cast<uint4*>(p.o + at * D + q * 32 + 8 * e) =
-                make_uint4(pack_bf16(x[0] * r, x[1] * r), pack_bf16(x[2] * r, x[3] * r), pack_bf16(x[4] * r, x[5] * r), pack_bf16(x[6] * r, x[7] * r));
-          }
+        if (qi < len) store_bf16x32(p.o + at * D + q * 32, o, r, wide);
       }
       tc_fence_before();
     }
