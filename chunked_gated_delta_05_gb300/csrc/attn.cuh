@@ -155,14 +155,13 @@ __device__ __forceinline__ void product_ss(uint32_t lead, uint32_t d, uint32_t a
     mma_ss<true>(lead, d, a + o, b + o, id);
   }
 }
-// d (+)= A B for steps kFrom .. kTo - 1 of 16 inner entries, A [128,128] in TMEM in parts of 2 kPart columns of which the first kPart
-// hold it; B a tile read MN-major.
-template <int D, int kPart, int kFrom, int kTo>
+// d (+)= A B, A [128,128] in TMEM in parts of 2 kPart columns of which the first kPart hold it; B a tile read MN-major.
+template <int D, int kPart>
 __device__ __forceinline__ void product_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, bool acc) {
   constexpr uint32_t id = idesc_bf16(kAttnTile, D, false, true);
-  constexpr int kPer = kPart / 8;  // steps in a part
+  constexpr int kPer = kPart / 8;  // steps of 16 inner entries in a part
 #pragma unroll
-  for (int s = kFrom; s < kTo; ++s) mma_ts(lead, d, a + (s / kPer) * 2 * kPart + (s % kPer) * 8, b + s * 128, id, acc || s > kFrom);
+  for (int s = 0; s < kAttnTile / 16; ++s) mma_ts(lead, d, a + (s / kPer) * 2 * kPart + (s % kPer) * 8, b + s * 128, id, acc || s > 0);
 }
 // 32 bf16 of a row times f from 32 fp32 columns, to 16-byte aligned memory (32-byte aligned: whole sectors a store).
 __device__ __forceinline__ void store_bf16x32(__nv_bfloat16* dst, const float* x, float f, bool wide) {

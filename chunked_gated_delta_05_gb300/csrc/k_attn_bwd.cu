@@ -15,6 +15,8 @@
 // TMEM: S^T (P^T over it), dP^T (dS^T over it), dV, dK. The products run in the order dV(i), S(i+1), dK(i), dP(i+1): while a pair of
 // them runs, the softmax warps turn the scores (or dP) of the other pair's into the next operand.
 // k_attn_dq: S = Q K^T, dP = dO V^T, dQ += dS K (dS over S in TMEM; S double-buffered, a tile ahead).
+// Both go through their output tiles in turn, one CTA an SM: an output leaves while the next tile's operands arrive and its first
+// products run (2 x 4096 tokens x 16 heads: a CTA per tile spent 40 of 203 us, and 22 of 152, on starting and ending).
 //
 // Eight softmax warps, two to a quarter of the TMEM lanes, each on half of a tile's columns. The bf16 operand's halves lie over the
 // columns that their own writers have read. p and dS are rounded to bf16 (as the products' operands); all sums are fp32.
@@ -51,9 +53,12 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, uint32_t t, float 
   if (mine) store_bf16x32(dst, o, f, wide);
 }
 
-// Ring position and phase of use i.
-__device__ __forceinline__ int slot(int i, int n) { return i % n; }
-__device__ __forceinline__ uint32_t phase(int i, int n) { return uint32_t(i / n) & 1u; }
+// The CTA's tile of a round, most work first: every other round the other way round, so that the CTAs' sums of work come out
+// alike. False where the last round has none for it. `i`: the tile's index, times the heads, plus the head.
+__device__ __forceinline__ bool round_item(long long round, long long total, long long* i) {
+  *i = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  return *i < total;
+}
 
 }  // namespace
 
@@ -101,22 +106,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *sK = sm, *sV = sK + kTile, *sQ = sV + kTile, *sO = sQ + kQ * kTile;
   float* vec = reinterpret_cast<float*>(sO + kO * kTile);  // [2][lse2 | delta][128]
   uint64_t* bar = reinterpret_cast<uint64_t*>(vec + 2 * 256);
-  uint64_t *kv_full = bar, *q_full = bar + 1, *q_empty = bar + 4, *o_full = bar + 7, *o_empty = bar + 9, *ready = bar + 11, *vec_free = bar + 13, *s_full = bar + 15,
-           *dp_full = bar + 16, *p_ready = bar + 17, *ds_ready = bar + 18, *done = bar + 19;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 20);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 21);
+  uint64_t *kv_full = bar, *kv_empty = bar + 1, *q_full = bar + 2, *q_empty = bar + 5, *o_full = bar + 8, *o_empty = bar + 10, *ready = bar + 12, *vec_free = bar + 14,
+           *s_full = bar + 16, *dp_full = bar + 17, *p_ready = bar + 18, *ds_ready = bar + 19, *done = bar + 20, *drained = bar + 21;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 22);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 23);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hk = blockIdx.x % p.Hk;
-  wait_for_previous();
-  const AttnTile tl = attn_tile(p, blockIdx.x / p.Hk, kAttnTile, p.causal != 0);
-  const int all = (tl.len + kAttnTile - 1) / kAttnTile, i0 = p.causal ? tl.first / kAttnTile : 0, per = all - i0, n = per * p.group;
-  const bool ragged = all * kAttnTile > tl.len;
-
+  const long long total = (long long)p.tiles * p.Hk;
   if (warp == kMma) tmem_alloc(tslot, 512);
   if (tid == 0) {
     *abort_flag = 0;
     mbar_init(kv_full, 1);
+    mbar_init(kv_empty, 1);
     for (int i = 0; i < kQ; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1);
     for (int i = 0; i < kO; ++i) mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 1), mbar_init(&ready[i], 32), mbar_init(&vec_free[i], kSoftmax);
     mbar_init(s_full, 1);
@@ -124,118 +125,171 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(p_ready, kSoftmax + 1);
     mbar_init(ds_ready, kSoftmax + 1);
     mbar_init(done, 1);
+    mbar_init(drained, 1);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  wait_for_previous();
   constexpr uint32_t tS = 0, tP = 128, tV = 256, tK = 256 + D;  // all of TMEM, so it starts at column 0
+  auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
+
+  // A tile: its key head, keys, first query tile, query tiles a head, and all it walks.
+  struct Item {
+    int hk, i0, per, n;
+    AttnTile tl;
+    bool ragged;
+  };
+  auto item_of = [&](long long round, Item* x) {
+    long long i;
+    if (!round_item(round, total, &i)) return false;
+    x->hk = int(i % p.Hk);
+    x->tl = attn_tile(p, int(i / p.Hk), kAttnTile, p.causal != 0);
+    const int all = (x->tl.len + kAttnTile - 1) / kAttnTile;
+    x->i0 = p.causal ? x->tl.first / kAttnTile : 0;
+    x->per = all - x->i0;
+    x->n = x->per * p.group;
+    x->ragged = all * kAttnTile > x->tl.len;
+    return true;
+  };
+  Item x;
 
   if (warp >= kMma) {
     regs_dec<kOtherRegs>();
     if (warp == kTma) {
       // ---------------- producer ----------------
-      if (lane == 0) {
-        mbar_expect_tx(kv_full, 2 * kTile);
-        load_attn_tile<D>(sK, &mk, hk * D, tl.row0 + tl.first, kv_full);
-        load_attn_tile<D>(sV, &mv, hk * D, tl.row0 + tl.first, kv_full);
-      }
-      int it = 0;
+      Ring<kQ, 1> rq(0);
+      Ring<kO, 1> ro(0);
+      int use = 0;        // query tiles requested
+      uint32_t tiles = 0;  // key tiles
       bool ok = true;
-      for (; it < n; ++it) {
-        const int h = hk * p.group + it / per, q0 = (i0 + it % per) * kAttnTile, y = tl.row0 + q0, qs = slot(it, kQ), os = slot(it, kO);
-        if (it >= kQ) ok = attn_wait(&q_empty[qs], phase(it - kQ, kQ), abort_flag, p.status, kDevTimeoutMma);
-        if (ok && lane == 0) {
-          mbar_expect_tx(&q_full[qs], kTile);
-          load_attn_tile<D>(sQ + qs * kTile, &mq, h * D, y, &q_full[qs]);
+      for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+        if (tiles > 0) ok = __all_sync(0xffffffffu, wait(kv_empty, (tiles - 1) & 1, kDevTimeoutMma));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_expect_tx(kv_full, 2 * kTile);
+          load_attn_tile<D>(sK, &mk, x.hk * D, x.tl.row0 + x.tl.first, kv_full);
+          load_attn_tile<D>(sV, &mv, x.hk * D, x.tl.row0 + x.tl.first, kv_full);
         }
-        if (ok && it >= kO)
-          ok = attn_wait(&o_empty[os], phase(it - kO, kO), abort_flag, p.status, kDevTimeoutMma) &&
-               attn_wait(&vec_free[os], phase(it - kO, kO), abort_flag, p.status, kDevTimeoutSync);
-        if (ok && lane == 0) {
-          mbar_expect_tx(&o_full[os], kTile);
-          load_attn_tile<D>(sO + os * kTile, &mdo, h * D, y, &o_full[os]);
-        }
-        if (!__all_sync(0xffffffffu, ok)) break;
-        float* v = vec + os * 256;
-        const long long at = (long long)h * p.rows + y;
+        ++tiles;
+        int h = x.hk * p.group, q0 = x.i0 * kAttnTile;
+        for (int it = 0; it < x.n && ok; ++it) {
+          const int y = x.tl.row0 + q0;
+          ok = use < kQ || wait(&q_empty[rq.at], rq.phase ^ 1u, kDevTimeoutMma);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (lane == 0) {
+            mbar_expect_tx(&q_full[rq.at], kTile);
+            load_attn_tile<D>(sQ + rq.at * kTile, &mq, h * D, y, &q_full[rq.at]);
+          }
+          ok = use < kO || (wait(&o_empty[ro.at], ro.phase ^ 1u, kDevTimeoutMma) && wait(&vec_free[ro.at], ro.phase ^ 1u, kDevTimeoutSync));
+          if (!(ok = __all_sync(0xffffffffu, ok))) {
+            if (lane == 0) mbar_drain(&q_full[rq.at], rq.phase);
+            break;
+          }
+          if (lane == 0) {
+            mbar_expect_tx(&o_full[ro.at], kTile);
+            load_attn_tile<D>(sO + ro.at * kTile, &mdo, h * D, y, &o_full[ro.at]);
+          }
+          float* v = vec + ro.at * 256;
+          const long long at = (long long)h * p.rows + y;
 #pragma unroll
-        for (int e = lane; e < kAttnTile; e += 32) {
-          const bool in = q0 + e < tl.len;
-          v[e] = in ? p.lse2[at + e] : -INFINITY;
-          v[128 + e] = in ? p.delta[at + e] : 0.f;
+          for (int e = lane; e < kAttnTile; e += 32) {
+            const bool in = q0 + e < x.tl.len;
+            v[e] = in ? p.lse2[at + e] : -INFINITY;
+            v[128 + e] = in ? p.delta[at + e] : 0.f;
+          }
+          if (x.ragged && q0 + kAttnTile > x.tl.len) {
+            ok = wait(&q_full[rq.at], rq.phase, kDevTimeoutTma) && wait(&o_full[ro.at], ro.phase, kDevTimeoutTma);
+            if (!(ok = __all_sync(0xffffffffu, ok))) {
+              if (lane == 0) mbar_drain(&q_full[rq.at], rq.phase), mbar_drain(&o_full[ro.at], ro.phase);
+              break;
+            }
+            zero_attn_rows<D>(sQ + rq.at * kTile, x.tl.len - q0, lane);
+            zero_attn_rows<D>(sO + ro.at * kTile, x.tl.len - q0, lane);
+            fence_async_smem();
+          }
+          mbar_arrive(&ready[ro.at]);
+          ++use;
+          rq.next();
+          ro.next();
+          q0 += kAttnTile;
+          if (q0 >= x.tl.len) {  // the next head of the group
+            q0 = x.i0 * kAttnTile;
+            ++h;
+          }
         }
-        if (ragged && q0 + kAttnTile > tl.len) {
-          ok = attn_wait(&q_full[qs], phase(it, kQ), abort_flag, p.status, kDevTimeoutTma) &&
-               attn_wait(&o_full[os], phase(it, kO), abort_flag, p.status, kDevTimeoutTma);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          zero_attn_rows<D>(sQ + qs * kTile, tl.len - q0, lane);
-          zero_attn_rows<D>(sO + os * kTile, tl.len - q0, lane);
-          fence_async_smem();
-        }
-        mbar_arrive(&ready[os]);
       }
-      if (it < n && lane == 0) {  // the copies in flight land before their destination is given up
-        mbar_drain(kv_full, 0);
-        for (int k = max(0, it - kQ + 1); k < it; ++k) mbar_drain(&q_full[slot(k, kQ)], phase(k, kQ));
-        for (int k = max(0, it - kO + 1); k < it; ++k) mbar_drain(&o_full[slot(k, kO)], phase(k, kO));
-        // the last ones, if they were requested
-        mbar_drain(&q_full[slot(it, kQ)], phase(it, kQ), 1000000ull);
-        mbar_drain(&o_full[slot(it, kO)], phase(it, kO), 1000000ull);
+      if (!ok && lane == 0) {  // the copies in flight land before their destination is given up
+        if (tiles) mbar_drain(kv_full, (tiles - 1) & 1);
+        for (int k = max(0, use - kQ); k < use; ++k) mbar_drain(&q_full[k % kQ], k / kQ & 1);
+        for (int k = max(0, use - kO); k < use; ++k) mbar_drain(&o_full[k % kO], k / kO & 1);
       }
     } else if (warp == kMma) {
       // ---------------- MMA issuer ----------------
       const uint32_t lead = elect_lead();
       const uint32_t aK = desc_low_k(smem_u32(sK)), aV = desc_low_k(smem_u32(sV)), bQ = desc_low_k(smem_u32(sQ)), bO = desc_low_k(smem_u32(sO)),
                      nQ = desc_low_mn(smem_u32(sQ), kAttnPanel), nO = desc_low_mn(smem_u32(sO), kAttnPanel);
-      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, attn_wait(b, ph, abort_flag, p.status, code))); };
+      auto all_wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, wait(b, ph, code))); };
+      Ring<kQ, 1> rq(0);   // the products' Q, S's one tile ahead of dK's
+      uint32_t u = 0;      // query tiles so far
       auto scores = [&](int at) {
         product_ss<D>(lead, tS, aK, bQ + at * (kTile >> 4));
         commit(lead, s_full);
       };
-      auto dprobs = [&](int at) {
-        product_ss<D>(lead, tP, aV, bO + at * (kTile >> 4));
+      auto dprobs = [&](uint32_t os, bool last) {
+        product_ss<D>(lead, tP, aV, bO + os * (kTile >> 4));
         commit(lead, dp_full);
+        if (last) commit(lead, kv_empty);
       };
-      Ring<kQ, 1> rq(0);
-      bool ok = wait(kv_full, 0, kDevTimeoutTma) && wait(&q_full[0], 0, kDevTimeoutTma) && wait(&ready[0], 0, kDevTimeoutSync);
-      if (ok) scores(0);
-      ok = ok && wait(&o_full[0], 0, kDevTimeoutTma);
-      if (ok) dprobs(0);
-      for (int it = 0; it < n && ok; ++it) {
-        // the gates answer for the tiles of the products that follow either operand
-        if (!(ok = wait(p_ready, it & 1, kDevTimeoutSync))) break;
+      bool ok = true;
+      for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+        // the first products overwrite operands that the products issued so far have read
+        ok = all_wait(kv_full, rd & 1, kDevTimeoutTma) && all_wait(&q_full[rq.at], rq.phase, kDevTimeoutTma) && all_wait(&ready[u & 1], u >> 1 & 1, kDevTimeoutSync);
+        if (!ok) break;
         tc_fence_after();
-        const int qs = rq.at, os = it & 1;
-        rq.next();
-        product_ts<D, kCols / 2, 0, kAttnTile / 16>(lead, tV, tS, nO + os * (kTile >> 4), it > 0);
-        commit(lead, &o_empty[os]);
-        if (it + 1 < n) scores(rq.at);
-        if (!(ok = wait(ds_ready, it & 1, kDevTimeoutSync))) break;
-        tc_fence_after();
-        product_ts<D, kCols / 2, 0, kAttnTile / 16>(lead, tK, tP, nQ + qs * (kTile >> 4), it > 0);
-        commit(lead, &q_empty[qs]);
-        if (it + 1 < n) dprobs(os ^ 1);
+        scores(rq.at);
+        if (!(ok = all_wait(&o_full[u & 1], u >> 1 & 1, kDevTimeoutTma))) break;
+        dprobs(u & 1, x.n == 1);
+        for (int it = 0; it < x.n; ++it, ++u) {
+          // the gates answer for the tiles of the products that follow either operand
+          if (!(ok = all_wait(p_ready, u & 1, kDevTimeoutSync))) break;
+          tc_fence_after();
+          const int qs = rq.at;
+          const uint32_t os = u & 1;
+          rq.next();
+          product_ts<D, kCols / 2>(lead, tV, tS, nO + os * (kTile >> 4), it > 0);
+          commit(lead, &o_empty[os]);
+          if (it + 1 < x.n) scores(rq.at);
+          if (!(ok = all_wait(ds_ready, u & 1, kDevTimeoutSync))) break;
+          tc_fence_after();
+          product_ts<D, kCols / 2>(lead, tK, tP, nQ + qs * (kTile >> 4), it > 0);
+          commit(lead, &q_empty[qs]);
+          if (it + 1 < x.n) dprobs(os ^ 1u, it + 2 == x.n);
+        }
+        if (ok) commit(lead, done);
       }
-      commit(lead, done);  // the softmax warps wait for it, or, after an error:
-      if (!ok) mbar_drain(done, 0);
+      if (!ok) {  // the products in flight end before their accumulators are given up
+        commit(lead, drained);
+        mbar_drain(drained, 0);
+      }
     } else if (warp >= kGate && lane == 0) {
       // ---------------- gates: one warp for S(it + 1) behind dV(it), the other for dP(it + 1) behind dK(it) ----------------
-      uint64_t* bar = warp == kGate ? p_ready : ds_ready;
+      uint64_t* b = warp == kGate ? p_ready : ds_ready;
       Ring<kQ, 1> rq(0);
+      uint32_t u = 0;
       bool ok = true;
-      for (int it = 0; it < n && ok; ++it) {
-        rq.next();
-        if (it + 1 < n) {
-          const int os = (it + 1) & 1;
-          const uint32_t ph = phase(it + 1, kO);
-          ok = warp == kGate ? attn_wait(&q_full[rq.at], rq.phase, abort_flag, p.status, kDevTimeoutTma) && attn_wait(&ready[os], ph, abort_flag, p.status, kDevTimeoutSync)
-                          : attn_wait(&o_full[os], ph, abort_flag, p.status, kDevTimeoutTma);
-          if (!ok) break;
+      for (long long rd = 0; ok && item_of(rd, &x); ++rd)
+        for (int it = 0; it < x.n && ok; ++it, ++u) {
+          rq.next();
+          if (it + 1 < x.n) {
+            const uint32_t os = (u + 1) & 1, ph = (u + 1) >> 1 & 1;
+            ok = warp == kGate ? wait(&q_full[rq.at], rq.phase, kDevTimeoutTma) && wait(&ready[os], ph, kDevTimeoutSync) : wait(&o_full[os], ph, kDevTimeoutTma);
+            if (!ok) break;
+          }
+          mbar_arrive(b);
+          ok = wait(b, u & 1, kDevTimeoutSync);  // the next arrival belongs to the next phase
         }
-        mbar_arrive(bar);
-        ok = attn_wait(bar, it & 1, abort_flag, p.status, kDevTimeoutSync);  // the next arrival belongs to the next phase
-      }
     }
   } else {
     // ---------------- softmax: 32 key rows a warp, half of the queries ----------------
@@ -246,11 +300,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp >> 2, g = lane >> 2, col = (lane & 3) * 2, key0 = (warp & 3) * 32 + g;  // rows key0 + 8 r
     const uint32_t lane0 = tmem_lane_base(warp), lb = lane0 + uint32_t(half) * kCols;
     const F2 c2 = dup2(p.scale * kLog2e);
+    const bool wide = (reinterpret_cast<uintptr_t>(half ? p.dk : p.dv) & 31) == 0;
     bool ok = true;
-    for (int it = 0; it < n && ok; ++it) {
-      const int q0 = (i0 + it % per) * kAttnTile + half * kCols, os = it & 1;
+    uint32_t u = 0;
+    for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+    const AttnTile& tl = x.tl;
+    int q0 = x.i0 * kAttnTile + half * kCols;
+    for (int it = 0; it < x.n && ok; ++it, ++u) {
+      const uint32_t os = u & 1;
       const float2 *lse = reinterpret_cast<const float2*>(vec + os * 256 + half * kCols + col), *delta = lse + 64;
-      ok = attn_wait(&ready[os], phase(it, kO), abort_flag, p.status, kDevTimeoutSync) && attn_wait(s_full, it & 1, abort_flag, p.status, kDevTimeoutMma);
+      ok = wait(&ready[os], u >> 1 & 1, kDevTimeoutSync) && wait(s_full, u & 1, kDevTimeoutMma);
       if (!ok) break;
       tc_fence_after();
       // w[32 h + 4 b + 2 r + y]: row key0 + 16 h + 8 r, column 8 b + col + y
@@ -289,8 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(p_ready);
-      ok = attn_wait(dp_full, it & 1, abort_flag, p.status, kDevTimeoutMma);
-      if (!ok) break;
+      if (!(ok = wait(dp_full, u & 1, kDevTimeoutMma))) break;
       tc_fence_after();
       float d[64];
       tmem_ld_16x64(tP + lb, d);
@@ -313,15 +371,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(ds_ready);
+      q0 += kAttnTile;
+      if (q0 - half * kCols >= tl.len) q0 = x.i0 * kAttnTile + half * kCols;  // the next head of the group
     }
-    if (ok && attn_wait(done, 0, abort_flag, p.status, kDevTimeoutMma)) {
-      tc_fence_after();
-      const int key = tl.first + (tid & 127);
-      const bool wide = (reinterpret_cast<uintptr_t>(half ? p.dk : p.dv) & 31) == 0;
-      __nv_bfloat16* dst = (half ? p.dk : p.dv) + ((size_t(tl.row0) + key) * p.Hk + hk) * D;
-      const uint32_t acc = (half ? tK : tV) + lane0;
+    if (!ok || !(ok = wait(done, rd & 1, kDevTimeoutMma))) break;
+    tc_fence_after();
+    const int key = tl.first + (tid & 127);
+    __nv_bfloat16* dst = (half ? p.dk : p.dv) + ((size_t(tl.row0) + key) * p.Hk + x.hk) * D;
+    const uint32_t acc = (half ? tK : tV) + lane0;
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) store_row(dst + q * 32, acc + q * 32, half ? p.scale : 1.f, key < tl.len, wide);
+    for (int q = 0; q < D / 32; ++q) store_row(dst + q * 32, acc + q * 32, half ? p.scale : 1.f, key < tl.len, wide);
+    tc_fence_before();
     }
   }
   tc_fence_before();
@@ -337,164 +397,222 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t *sQ = sm, *sO = sQ + kTile, *sK = sO + kTile, *sV = sK + kK * kTile;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sV + kV * kTile);
-  uint64_t *q_full = bar, *k_full = bar + 1, *k_empty = bar + 4, *v_full = bar + 7, *v_empty = bar + 9, *s_full = bar + 11, *dp_full = bar + 13, *ds_ready = bar + 14,
-           *tail_ready = bar + 15, *done = bar + 16;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 17);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 18);
+  uint64_t *q_full = bar, *q_empty = bar + 1, *k_full = bar + 2, *k_empty = bar + 5, *zeroed = bar + 8, *v_full = bar + 11, *v_empty = bar + 13, *s_full = bar + 15,
+           *dp_full = bar + 17, *ds_ready = bar + 18, *done = bar + 19, *drained = bar + 20;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 21);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 22);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x % p.H, hk = h / p.group;
-  wait_for_previous();
-  const AttnTile tl = attn_tile(p, blockIdx.x / p.H, kAttnTile, false);
-  const int all = (tl.len + kAttnTile - 1) / kAttnTile, n = p.causal ? tl.first / kAttnTile + 1 : all;
-  const bool tail = n * kAttnTile > tl.len;
-
+  const long long total = (long long)p.tiles * p.H;
   if (warp == kMma) tmem_alloc(tslot, 512);
   if (tid == 0) {
     *abort_flag = 0;
     mbar_init(q_full, 1);
-    for (int i = 0; i < kK; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < kK; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1), mbar_init(&zeroed[i], 32);
     for (int i = 0; i < kV; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 1), mbar_init(&s_full[i], 1);
     mbar_init(dp_full, 1);
     mbar_init(ds_ready, kSoftmax + 1);
-    mbar_init(tail_ready, 32);
     mbar_init(done, 1);
+    mbar_init(drained, 1);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  wait_for_previous();
   constexpr uint32_t tP = 256, tQ = 384;  // all of TMEM, so it starts at column 0
-  auto tS = [&](int i) { return uint32_t(i & 1) * 128; };
+  auto tS = [&](uint32_t u) { return (u & 1) * 128; };
+  auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
+
+  // A tile: its head and key head, queries, key tiles, and whether the last of those reaches past the sequence.
+  struct Item {
+    int h, hk, n;
+    bool tail;
+    AttnTile tl;
+  };
+  auto item_of = [&](long long round, Item* x) {
+    long long i;
+    if (!round_item(round, total, &i)) return false;
+    x->h = int(i % p.H);
+    x->hk = x->h / p.group;
+    x->tl = attn_tile(p, int(i / p.H), kAttnTile, false);
+    x->n = p.causal ? x->tl.first / kAttnTile + 1 : (x->tl.len + kAttnTile - 1) / kAttnTile;
+    x->tail = x->n * kAttnTile > x->tl.len;
+    return true;
+  };
+  Item x;
 
   if (warp >= kMma) {
     regs_dec<kOtherRegs>();
     if (warp == kTma) {
       // ---------------- producer ----------------
-      int it = 0;
-      if (lane == 0) {
-        mbar_expect_tx(q_full, 2 * kTile);
-        load_attn_tile<D>(sQ, &mq, h * D, tl.row0 + tl.first, q_full);
-        load_attn_tile<D>(sO, &mdo, h * D, tl.row0 + tl.first, q_full);
-        for (; it < n; ++it) {
-          const int ks = slot(it, kK), vs = slot(it, kV), y = tl.row0 + it * kAttnTile;
-          if (it >= kK && !attn_wait(&k_empty[ks], phase(it - kK, kK), abort_flag, p.status, kDevTimeoutMma)) break;
-          mbar_expect_tx(&k_full[ks], kTile);
-          load_attn_tile<D>(sK + ks * kTile, &mk, hk * D, y, &k_full[ks]);
-          if (it >= kV && !attn_wait(&v_empty[vs], phase(it - kV, kV), abort_flag, p.status, kDevTimeoutMma)) {
-            mbar_drain(&k_full[ks], phase(it, kK));
+      Ring<kK, 1> rk(0);
+      Ring<kV, 1> rv(0);
+      int use = 0;         // key tiles requested
+      uint32_t tiles = 0;  // query tiles
+      bool ok = true;
+      for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+        if (tiles > 0) ok = __all_sync(0xffffffffu, wait(q_empty, (tiles - 1) & 1, kDevTimeoutMma));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_expect_tx(q_full, 2 * kTile);
+          load_attn_tile<D>(sQ, &mq, x.h * D, x.tl.row0 + x.tl.first, q_full);
+          load_attn_tile<D>(sO, &mdo, x.h * D, x.tl.row0 + x.tl.first, q_full);
+        }
+        ++tiles;
+        for (int i = 0; i < x.n && ok; ++i) {
+          const int y = x.tl.row0 + i * kAttnTile;
+          ok = use < kK || wait(&k_empty[rk.at], rk.phase ^ 1u, kDevTimeoutMma);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (lane == 0) {
+            mbar_expect_tx(&k_full[rk.at], kTile);
+            load_attn_tile<D>(sK + rk.at * kTile, &mk, x.hk * D, y, &k_full[rk.at]);
+          }
+          ok = use < kV || wait(&v_empty[rv.at], rv.phase ^ 1u, kDevTimeoutMma);
+          if (!(ok = __all_sync(0xffffffffu, ok))) {
+            if (lane == 0) mbar_drain(&k_full[rk.at], rk.phase);
             break;
           }
-          mbar_expect_tx(&v_full[vs], kTile);
-          load_attn_tile<D>(sV + vs * kTile, &mv, hk * D, y, &v_full[vs]);
-        }
-        if (it < n) {  // the copies in flight land before their destination is given up
-          mbar_drain(q_full, 0);
-          for (int k = max(0, it - kK); k < it; ++k) mbar_drain(&k_full[slot(k, kK)], phase(k, kK));
-          for (int k = max(0, it - kV); k < it; ++k) mbar_drain(&v_full[slot(k, kV)], phase(k, kV));
+          if (lane == 0) {
+            mbar_expect_tx(&v_full[rv.at], kTile);
+            load_attn_tile<D>(sV + rv.at * kTile, &mv, x.hk * D, y, &v_full[rv.at]);
+          }
+          if (x.tail && i + 1 == x.n) {
+            ok = __all_sync(0xffffffffu, wait(&k_full[rk.at], rk.phase, kDevTimeoutTma));
+            if (!ok) {
+              if (lane == 0) mbar_drain(&k_full[rk.at], rk.phase), mbar_drain(&v_full[rv.at], rv.phase);
+              break;
+            }
+            zero_attn_rows<D>(sK + rk.at * kTile, x.tl.len - i * kAttnTile, lane);
+            fence_async_smem();
+            mbar_arrive(&zeroed[rk.at]);
+          }
+          ++use;
+          rk.next();
+          rv.next();
         }
       }
-      it = __shfl_sync(0xffffffffu, it, 0);
-      if (tail && it == n && attn_wait(&k_full[slot(n - 1, kK)], phase(n - 1, kK), abort_flag, p.status, kDevTimeoutTma)) {
-        zero_attn_rows<D>(sK + slot(n - 1, kK) * kTile, tl.len - (n - 1) * kAttnTile, lane);
-        fence_async_smem();
-        mbar_arrive(tail_ready);
+      if (!ok && lane == 0) {  // the copies in flight land before their destination is given up
+        if (tiles) mbar_drain(q_full, (tiles - 1) & 1);
+        for (int k = max(0, use - kK); k < use; ++k) mbar_drain(&k_full[k % kK], k / kK & 1);
+        for (int k = max(0, use - kV); k < use; ++k) mbar_drain(&v_full[k % kV], k / kV & 1);
       }
     } else if (warp == kMma) {
       // ---------------- MMA issuer ----------------
       const uint32_t lead = elect_lead();
       const uint32_t aQ = desc_low_k(smem_u32(sQ)), aO = desc_low_k(smem_u32(sO)), bK = desc_low_k(smem_u32(sK)), bV = desc_low_k(smem_u32(sV)),
                      nK = desc_low_mn(smem_u32(sK), kAttnPanel);
-      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, attn_wait(b, ph, abort_flag, p.status, code))); };
+      auto all_wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, wait(b, ph, code))); };
       Ring<kK, 1> rs(0), rk(0);  // K of the scores, and of dq
-      auto scores = [&](int i) {
-        product_ss<D>(lead, tS(i), aQ, bK + rs.at * (kTile >> 4));
-        commit(lead, &s_full[i & 1]);
-        rs.next();
-      };
-      auto dprobs = [&](int i) {
-        product_ss<D>(lead, tP, aO, bV + (i & 1) * (kTile >> 4));
-        commit(lead, dp_full);
-        commit(lead, &v_empty[i & 1]);
-      };
-      auto k_there = [&](int i) {
-        return wait(&k_full[slot(i, kK)], phase(i, kK), kDevTimeoutTma) && (!tail || i + 1 < n || wait(tail_ready, 0, kDevTimeoutSync));
-      };
-      bool ok = wait(q_full, 0, kDevTimeoutTma) && k_there(0);
-      if (ok) scores(0);
-      ok = ok && wait(&v_full[0], 0, kDevTimeoutTma);
-      if (ok) dprobs(0);
-      if (n > 1 && ok && (ok = k_there(1))) scores(1);
-      for (int i = 0; i < n && ok; ++i) {
-        // the gate answers for V of the next tile
-        if (!(ok = wait(ds_ready, i & 1, kDevTimeoutSync))) break;
+      uint32_t u = 0, zeros = 0;  // key tiles so far; a bit per stage, the phase of its next zeroing
+      auto scores = [&](uint32_t at, bool last) {  // S of key tile u = at, once its K has landed
+        bool there = all_wait(&k_full[rs.at], rs.phase, kDevTimeoutTma);
+        if (there && last && x.tail) {
+          there = all_wait(&zeroed[rs.at], zeros >> rs.at & 1u, kDevTimeoutSync);
+          zeros ^= 1u << rs.at;
+        }
+        if (!there) return false;
         tc_fence_after();
-        if (i + 1 < n) dprobs(i + 1);
-        product_ts<D, kCols / 2, 0, kAttnTile / 16>(lead, tQ, tS(i), nK + rk.at * (kTile >> 4), i > 0);
-        commit(lead, &k_empty[rk.at]);
-        rk.next();
-        // K of the tile after next is requested when the product before this one has let go of its stage
-        if (i + 2 < n && (ok = k_there(i + 2))) scores(i + 2);
+        product_ss<D>(lead, tS(at), aQ, bK + rs.at * (kTile >> 4));
+        commit(lead, &s_full[at & 1]);
+        rs.next();
+        return true;
+      };
+      auto dprobs = [&](uint32_t at, bool last) {
+        product_ss<D>(lead, tP, aO, bV + (at & 1) * (kTile >> 4));
+        commit(lead, dp_full);
+        commit(lead, &v_empty[at & 1]);
+        if (last) commit(lead, q_empty);  // and the scores, issued before, have read Q
+      };
+      bool ok = true;
+      for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+        // the first products overwrite operands that the products issued so far have read
+        if (!(ok = all_wait(q_full, rd & 1, kDevTimeoutTma) && scores(u, x.n == 1) && all_wait(&v_full[u & 1], u >> 1 & 1, kDevTimeoutTma))) break;
+        if (x.n > 1) {
+          dprobs(u, false);
+          if (!(ok = scores(u + 1, x.n == 2))) break;
+        } else {
+          dprobs(u, true);
+        }
+        for (int i = 0; i < x.n; ++i, ++u) {
+          // the gate answers for V of the next tile
+          if (!(ok = all_wait(ds_ready, u & 1, kDevTimeoutSync))) break;
+          tc_fence_after();
+          if (i + 1 < x.n) dprobs(u + 1, i + 2 == x.n);
+          product_ts<D, kCols / 2>(lead, tQ, tS(u), nK + rk.at * (kTile >> 4), i > 0);
+          commit(lead, &k_empty[rk.at]);
+          rk.next();
+          // K of the tile after next is requested when the product before this one has let go of its stage
+          if (i + 2 < x.n && !(ok = scores(u + 2, i + 3 == x.n))) break;
+        }
+        if (ok) commit(lead, done);
       }
-      commit(lead, done);  // the softmax warps wait for it, or, after an error:
-      if (!ok) mbar_drain(done, 0);
+      if (!ok) {  // the products in flight end before their accumulators are given up
+        commit(lead, drained);
+        mbar_drain(drained, 0);
+      }
     } else if (warp == kGate && lane == 0) {
       // ---------------- gate: V of the product that follows dS(i) has landed ----------------
-      auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
+      uint32_t u = 0;
       bool ok = true;
-      for (int i = 0; i < n && ok; ++i) {
-        if (i + 1 < n && !(ok = wait(&v_full[(i + 1) & 1], phase(i + 1, kV), kDevTimeoutTma))) break;
-        mbar_arrive(ds_ready);
-        ok = wait(ds_ready, i & 1, kDevTimeoutSync);  // the next arrival belongs to the next phase
-      }
+      for (long long rd = 0; ok && item_of(rd, &x); ++rd)
+        for (int i = 0; i < x.n && ok; ++i, ++u) {
+          if (i + 1 < x.n && !(ok = wait(&v_full[(u + 1) & 1], (u + 1) >> 1 & 1, kDevTimeoutTma))) break;
+          mbar_arrive(ds_ready);
+          ok = wait(ds_ready, u & 1, kDevTimeoutSync);  // the next arrival belongs to the next phase
+        }
     }
   } else {
     // ---------------- softmax: query row, half of the keys ----------------
     regs_inc<kSoftmaxRegs>();
-    const int half = warp >> 2, row = tid & 127, qi = tl.first + row;
+    const int half = warp >> 2, row = tid & 127;
     const uint32_t lane0 = tmem_lane_base(warp), lb = lane0 + uint32_t(half) * kCols;
-    const bool mine = qi < tl.len;
-    const long long at = (long long)h * p.rows + tl.row0 + qi;
-    const F2 c2 = dup2(p.scale * kLog2e), lse = dup2(mine ? p.lse2[at] : 0.f), delta = dup2(mine ? p.delta[at] : 0.f);
+    const F2 c2 = dup2(p.scale * kLog2e);
+    const bool wide = (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
     bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      ok = attn_wait(&s_full[i & 1], (i >> 1) & 1, abort_flag, p.status, kDevTimeoutMma);
-      if (!ok) break;
-      tc_fence_after();
-      float w[kCols], d[kCols];
-      tmem_ld64(tS(i) + lb, w);
-      tmem_wait_ld_regs(w);
+    uint32_t u = 0;
+    for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+      const int qi = x.tl.first + row;
+      const bool mine = qi < x.tl.len;
+      const long long at = (long long)x.h * p.rows + x.tl.row0 + qi;
+      const F2 lse = dup2(mine ? p.lse2[at] : 0.f), delta = dup2(mine ? p.delta[at] : 0.f);
+      for (int i = 0; i < x.n && ok; ++i, ++u) {
+        if (!(ok = wait(&s_full[u & 1], u >> 1 & 1, kDevTimeoutMma))) break;
+        tc_fence_after();
+        float w[kCols], d[kCols];
+        tmem_ld64(tS(u) + lb, w);
+        tmem_wait_ld_regs(w);
 #pragma unroll
-      for (int e = 0; e < kCols / 2; ++e) {
-        float a, b;
-        unf2(fma2(f2(w[2 * e], w[2 * e + 1]), c2, lse), &a, &b);
-        w[2 * e] = exp2_approx(a);
-        w[2 * e + 1] = exp2_approx(b);
+        for (int e = 0; e < kCols / 2; ++e) {
+          float a, b;
+          unf2(fma2(f2(w[2 * e], w[2 * e + 1]), c2, lse), &a, &b);
+          w[2 * e] = exp2_approx(a);
+          w[2 * e + 1] = exp2_approx(b);
+        }
+        if (!(ok = wait(dp_full, u & 1, kDevTimeoutMma))) break;
+        tc_fence_after();
+        tmem_ld64(tP + lb, d);
+        tmem_wait_ld_regs(d);
+#pragma unroll
+        for (int e = 0; e < kCols / 2; ++e) unf2(mul2(f2(w[2 * e], w[2 * e + 1]), add2(f2(d[2 * e], d[2 * e + 1]), delta)), &d[2 * e], &d[2 * e + 1]);
+        if (i + 1 == x.n && (p.causal || x.tail)) {
+          const int seen = (p.causal ? min(qi + 1, x.tl.len) : x.tl.len) - i * kAttnTile - half * kCols;
+#pragma unroll
+          for (int e = 0; e < kCols; ++e)
+            if (e >= seen) d[e] = 0.f;
+        }
+        store_operand(tS(u) + lb, d);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(ds_ready);
       }
-      ok = attn_wait(dp_full, i & 1, abort_flag, p.status, kDevTimeoutMma);
-      if (!ok) break;
+      if (!ok || !(ok = wait(done, rd & 1, kDevTimeoutMma))) break;
       tc_fence_after();
-      tmem_ld64(tP + lb, d);
-      tmem_wait_ld_regs(d);
-#pragma unroll
-      for (int e = 0; e < kCols / 2; ++e) unf2(mul2(f2(w[2 * e], w[2 * e + 1]), add2(f2(d[2 * e], d[2 * e + 1]), delta)), &d[2 * e], &d[2 * e + 1]);
-      if (i + 1 == n && (p.causal || tail)) {
-        const int seen = (p.causal ? min(qi + 1, tl.len) : tl.len) - i * kAttnTile - half * kCols;
-#pragma unroll
-        for (int e = 0; e < kCols; ++e)
-          if (e >= seen) d[e] = 0.f;
-      }
-      store_operand(tS(i) + lb, d);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(ds_ready);
-    }
-    if (ok && attn_wait(done, 0, abort_flag, p.status, kDevTimeoutMma)) {
-      tc_fence_after();
-      const bool wide = (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
-      __nv_bfloat16* dst = p.dq + ((size_t(tl.row0) + qi) * p.H + h) * D + half * (D / 2);
+      __nv_bfloat16* dst = p.dq + ((size_t(x.tl.row0) + qi) * p.H + x.h) * D + half * (D / 2);
 #pragma unroll
       for (int q = 0; q < D / 64; ++q) store_row(dst + q * 32, tQ + lane0 + half * (D / 2) + q * 32, p.scale, mine, wide);
+      tc_fence_before();
     }
   }
   tc_fence_before();
@@ -513,9 +631,10 @@ static cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CU
   if (e != cudaSuccess) return e;
   AttnParams pk = p;
   pk.table = keys;
-  e = launch_after(k_attn_dkv<D>, dim3(unsigned(p.tiles * p.Hk)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, pk);
+  const long long nk = (long long)p.tiles * p.Hk, nq = (long long)p.tiles * p.H;
+  e = launch_after(k_attn_dkv<D>, dim3(unsigned(nk < p.sms ? nk : p.sms)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, pk);
   if (e != cudaSuccess) return e;
-  return launch_after(k_attn_dq<D>, dim3(unsigned(p.tiles * p.H)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, p);
+  return launch_after(k_attn_dq<D>, dim3(unsigned(nq < p.sms ? nq : p.sms)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, p);
 }
 
 cudaError_t launch_attn_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, int D, const AttnParams& p, const int* keys,

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = sm + 2 * kTile;
-  __shared__ uint64_t q_full[2], q_empty[2], kv_full[kS], kv_empty[kS], zeroed[kS], s_full[2], p_full[2][2], o_full[2], drained;
+  __shared__ uint64_t q_full[2], q_empty[2], kv_full[kS], kv_empty[kS], zeroed[kS], s_full[2], p_full[2], o_full[2], drained;
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
 
@@ -90,8 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[t], 1);
       mbar_init(&q_empty[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t][0], kAttnTile + 1);
-      mbar_init(&p_full[t][1], kAttnTile + 1);
+      mbar_init(&p_full[t], kAttnTile + 1);
       mbar_init(&o_full[t], 1);
     }
     for (int i = 0; i < kS; ++i) {
@@ -171,12 +170,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto outputs = [&](int t, int j) {
         const uint32_t v = vv + rv.at * (kTile >> 4), d = 256 + uint32_t(t) * D;
-        if (!all_wait(&p_full[t][0], cnt[t] & 1, kDevTimeoutSync)) return false;
+        if (!all_wait(&p_full[t], cnt[t]++ & 1, kDevTimeoutSync)) return false;
         tc_fence_after();
-        product_ts<D, 64, 0, 4>(lead, d, uint32_t(t) * 128, v, j > 0);
-        if (!all_wait(&p_full[t][1], cnt[t]++ & 1, kDevTimeoutSync)) return false;
-        tc_fence_after();
-        product_ts<D, 64, 4, 8>(lead, d, uint32_t(t) * 128, v, true);
+        product_ts<D, 64>(lead, d, uint32_t(t) * 128, v, j > 0);
         return true;
       };
       // A tile's first scores of an item overwrite the weights of the item before it, which the products issued so far have read; its
@@ -184,7 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto begin = [&](int t, const Item& x, int use) {  // use: of the item's first K tile
         begun[t] = true;
         if (!x.n[t]) return true;
-        if (!all_wait(&kv_full[use % kS], use / kS & 1, kDevTimeoutTma) || !all_wait(&q_full[t], q_use[t]++ & 1, kDevTimeoutTma)) return false;
+        if (t == 0 && !all_wait(&kv_full[use % kS], use / kS & 1, kDevTimeoutTma)) return false;  // the first tile begins first
+        if (!all_wait(&q_full[t], q_use[t]++ & 1, kDevTimeoutTma)) return false;
         scores(t, use % kS, x.n[t] == 1);
         return true;
       };
@@ -236,13 +233,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           rv.next();
           if (it.tail && j + 1 == it.most) zeros ^= 1u << v;
           if (j >= it.n[t]) continue;
-          ok = wait(&kv_full[v], v_phase, kDevTimeoutTma) && (!it.tail || j + 1 < it.most || wait(&zeroed[v], ~zeros >> v & 1u, kDevTimeoutSync));
+          ok = wait(&kv_full[v], v_phase, kDevTimeoutTma) && (j + 1 == it.n[t] || wait(&kv_full[rk.at], rk.phase, kDevTimeoutTma)) &&
+               (!it.tail || j + 1 < it.most || wait(&zeroed[v], ~zeros >> v & 1u, kDevTimeoutSync));
           if (!ok) break;
-          mbar_arrive(&p_full[t][0]);
-          if (j + 1 < it.n[t] && !(ok = wait(&kv_full[rk.at], rk.phase, kDevTimeoutTma))) break;
-          mbar_arrive(&p_full[t][1]);
+          mbar_arrive(&p_full[t]);
           // weights j are there: their scores are done, and the output product of the weights before them
-          ok = wait(&p_full[t][1], cnt++ & 1, kDevTimeoutSync);
+          ok = wait(&p_full[t], cnt++ & 1, kDevTimeoutSync);
           if (!ok) break;
           if (frees) {
             mbar_arrive(&kv_empty[k]);
@@ -276,10 +272,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Weights against the reference at hand, and the row's maximum beside them (the two run on different units): only where
         // that lies too far above the reference does it move, and the weights are taken again from the scores in TMEM.
         const F2 before = l2;
-        F2 mc;
-        float s[128], w[32];
+        float w[64];
 #pragma unroll 1
         while (true) {
+          float s[128];
           tmem_ld64(tS(t) + lb, s);
           tmem_ld64(tS(t) + lb + 64, s + 64);
           tmem_wait_ld_regs(s);
@@ -297,13 +293,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[e + u], s[e + 4 + u]);
             m = max3(max3(mx[0], mx[1], s[124]), max3(mx[2], mx[3], s[125]), fmaxf(s[126], s[127]));
           }
-          mc = dup2(-m * c);
+          const F2 mc = dup2(-m * c);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < 64; ++e) {
             float a, b;
             mx[e & 3] = max3(mx[e & 3], s[2 * e], s[2 * e + 1]);
-            mx[(e + 2) & 3] = max3(mx[(e + 2) & 3], s[64 + 2 * e], s[65 + 2 * e]);
             unf2(fma2(f2(s[2 * e], s[2 * e + 1]), c2, mc), &a, &b);
             a = exp2_approx(a);
             b = exp2_approx(b);
@@ -326,22 +321,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tmem_st32(tS(t) + lb, w);
+        tmem_st32(tS(t) + lb + 32, w + 32);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_full[t][0]);  // the product of the first half may start
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          float a, b;
-          unf2(fma2(f2(s[64 + 2 * e], s[65 + 2 * e]), c2, mc), &a, &b);
-          a = exp2_approx(a);
-          b = exp2_approx(b);
-          l2 = add2(l2, f2(a, b));
-          w[e] = __uint_as_float(pack_bf16(a, b));
-        }
-        tmem_st32(tS(t) + lb + 32, w);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_full[t][1]);
+        mbar_arrive(&p_full[t]);
       }
       if (!ok || !(ok = wait(&o_full[t], outs++ & 1, kDevTimeoutMma))) break;
       tc_fence_after();
