@@ -126,6 +126,7 @@ struct AttnParams {
   const float* lse_in;
   float *lse2, *delta;         // [H][rows]: -lse log2(e), and minus the rows' sums of dO o
   __nv_bfloat16 *dq, *dk, *dv;
+  unsigned* counters;          // [2]: tiles handed out
   int* status;
 };
 

@@ -300,7 +300,7 @@ int attn_fwd(const gdn_attn_desc_t* d, const gdn_attn_fwd_args_t* a, void* strea
 }
 
 struct AttnBwdLayout {
-  size_t order, keys, lse2, delta, total;
+  size_t order, keys, lse2, delta, counters, total;
 };
 AttnBwdLayout layout_attn_bwd(const AttnProblem& P) {
   AttnBwdLayout l{};
@@ -308,7 +308,8 @@ AttnBwdLayout layout_attn_bwd(const AttnProblem& P) {
   l.lse2 = 2 * l.keys;
   const size_t n = align256(size_t(P.S.rows) * P.S.H * 4);
   l.delta = l.lse2 + n;
-  l.total = l.delta + n;
+  l.counters = l.delta + n;
+  l.total = l.counters + 256;
   return l;
 }
 
@@ -336,6 +337,7 @@ int attn_bwd(const gdn_attn_desc_t* d, const gdn_attn_bwd_args_t* a, void* strea
   p.lse_in = a->lse;
   p.lse2 = reinterpret_cast<float*>(ws + l.lse2);
   p.delta = reinterpret_cast<float*>(ws + l.delta);
+  p.counters = reinterpret_cast<unsigned*>(ws + l.counters);
   p.dq = static_cast<bf*>(a->dq);
   p.dk = static_cast<bf*>(a->dk);
   p.dv = static_cast<bf*>(a->dv);

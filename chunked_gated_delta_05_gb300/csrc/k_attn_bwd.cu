@@ -53,12 +53,45 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, uint32_t t, float 
   if (mine) store_bf16x32(dst, o, f, wide);
 }
 
-// The CTA's tile of a round, most work first: every other round the other way round, so that the CTAs' sums of work come out
-// alike. False where the last round has none for it. `i`: the tile's index, times the heads, plus the head.
-__device__ __forceinline__ bool round_item(long long round, long long total, long long* i) {
-  *i = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-  return *i < total;
-}
+// Output tiles are handed out as CTAs get free, the ones with the most work first (a fixed assignment left some CTAs 20% more work
+// on documents with grouped heads; a tile's result does not depend on who computes it). The producer warp takes the next one and
+// passes it to the CTA's other threads through two places in shared memory.
+struct Handout {
+  long long* tile;             // [2]
+  uint64_t *full, *empty;      // [2]
+  unsigned* counter;           // tiles taken beyond every CTA's first, zeroed by k_attn_delta
+  long long total;
+  __device__ __forceinline__ void init(int readers) const {
+    for (int i = 0; i < 2; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], readers);
+  }
+  // The producer warp's round: true with the tile, false at the end (`*ok`) or after an error.
+  template <class W>
+  __device__ __forceinline__ bool take(long long round, long long* i, bool* ok, W wait) const {
+    const int at = int(round & 1);
+    if (round >= 2) *ok = __all_sync(0xffffffffu, wait(&empty[at], (round >> 1) - 1 & 1, kDevTimeoutSync));
+    if (!*ok) return false;
+    long long mine = blockIdx.x;
+    if ((threadIdx.x & 31) == 0) {
+      if (round > 0) mine = (long long)gridDim.x + atomicAdd(counter, 1u);
+      tile[at] = mine;
+      mbar_arrive(&full[at]);
+    }
+    *i = __shfl_sync(0xffffffffu, mine, 0);
+    return *i < total;
+  }
+  // Another thread's round, the same. kWarp: a warp's, known to be the same for its lanes (the MMA warp's control flow).
+  template <bool kWarp, class W>
+  __device__ __forceinline__ bool get(long long round, long long* i, bool* ok, W wait) const {
+    const int at = int(round & 1);
+    *ok = wait(&full[at], round >> 1 & 1, kDevTimeoutSync);
+    if (kWarp) *ok = __all_sync(0xffffffffu, *ok);
+    if (!*ok) return false;
+    const unsigned got = unsigned(tile[at]);
+    *i = kWarp ? __reduce_max_sync(0xffffffffu, got) : got;
+    mbar_arrive(&empty[at]);
+    return *i < total;
+  }
+};
 
 }  // namespace
 
@@ -69,6 +102,7 @@ __global__ void __launch_bounds__(256) k_attn_delta(const AttnParams p) {
   const int lane = threadIdx.x & 31, sub = lane % kLanes, which = lane / kLanes;
   const long long chunks = (p.rows + 31) / 32, item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   wait_for_previous();
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0;
   if (item >= chunks * p.H) return;
   const int h = int(item % p.H);
   const long long row0 = item / p.H * 32;
@@ -108,11 +142,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(vec + 2 * 256);
   uint64_t *kv_full = bar, *kv_empty = bar + 1, *q_full = bar + 2, *q_empty = bar + 5, *o_full = bar + 8, *o_empty = bar + 10, *ready = bar + 12, *vec_free = bar + 14,
            *s_full = bar + 16, *dp_full = bar + 17, *p_ready = bar + 18, *ds_ready = bar + 19, *done = bar + 20, *drained = bar + 21;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 22);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 23);
+  const Handout hand{reinterpret_cast<long long*>(bar + 22), bar + 24, bar + 26, p.counters, (long long)p.tiles * p.Hk};
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 28);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 29);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long total = (long long)p.tiles * p.Hk;
   if (warp == kMma) tmem_alloc(tslot, 512);
   if (tid == 0) {
     *abort_flag = 0;
@@ -126,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(ds_ready, kSoftmax + 1);
     mbar_init(done, 1);
     mbar_init(drained, 1);
+    hand.init(kSoftmax + 32 + 2);  // the softmax warps, the MMA warp and the gates
     fence_mbar_init();
   }
   tc_fence_before();
@@ -141,9 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     AttnTile tl;
     bool ragged;
   };
-  auto item_of = [&](long long round, Item* x) {
-    long long i;
-    if (!round_item(round, total, &i)) return false;
+  auto describe = [&](long long i, Item* x) {
     x->hk = int(i % p.Hk);
     x->tl = attn_tile(p, int(i / p.Hk), kAttnTile, p.causal != 0);
     const int all = (x->tl.len + kAttnTile - 1) / kAttnTile;
@@ -151,9 +184,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     x->per = all - x->i0;
     x->n = x->per * p.group;
     x->ragged = all * kAttnTile > x->tl.len;
-    return true;
   };
   Item x;
+  // The round's tile, as the producer and the others learn of it; false at the end, and after an error (*ok false).
+  auto take = [&](long long round, bool* ok) {
+    long long i;
+    if (!hand.take(round, &i, ok, wait)) return false;
+    describe(i, &x);
+    return true;
+  };
+  auto get = [&](long long round, bool* ok) {
+    long long i;
+    if (!hand.get<false>(round, &i, ok, wait)) return false;
+    describe(i, &x);
+    return true;
+  };
+  auto get_warp = [&](long long round, bool* ok) {
+    long long i;
+    if (!hand.get<true>(round, &i, ok, wait)) return false;
+    describe(i, &x);
+    return true;
+  };
 
   if (warp >= kMma) {
     regs_dec<kOtherRegs>();
@@ -164,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int use = 0;        // query tiles requested
       uint32_t tiles = 0;  // key tiles
       bool ok = true;
-      for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+      for (long long rd = 0; ok && take(rd, &ok); ++rd) {
         if (tiles > 0) ok = __all_sync(0xffffffffu, wait(kv_empty, (tiles - 1) & 1, kDevTimeoutMma));
         if (!ok) break;
         if (lane == 0) {
@@ -243,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) commit(lead, kv_empty);
       };
       bool ok = true;
-      for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+      for (long long rd = 0; ok && get_warp(rd, &ok); ++rd) {
         // the first products overwrite operands that the products issued so far have read
         ok = all_wait(kv_full, rd & 1, kDevTimeoutTma) && all_wait(&q_full[rq.at], rq.phase, kDevTimeoutTma) && all_wait(&ready[u & 1], u >> 1 & 1, kDevTimeoutSync);
         if (!ok) break;
@@ -279,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<kQ, 1> rq(0);
       uint32_t u = 0;
       bool ok = true;
-      for (long long rd = 0; ok && item_of(rd, &x); ++rd)
+      for (long long rd = 0; ok && get(rd, &ok); ++rd)
         for (int it = 0; it < x.n && ok; ++it, ++u) {
           rq.next();
           if (it + 1 < x.n) {
@@ -303,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool wide = (reinterpret_cast<uintptr_t>(half ? p.dk : p.dv) & 31) == 0;
     bool ok = true;
     uint32_t u = 0;
-    for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+    for (long long rd = 0; ok && get(rd, &ok); ++rd) {
     const AttnTile& tl = x.tl;
     int q0 = x.i0 * kAttnTile + half * kCols;
     for (int it = 0; it < x.n && ok; ++it, ++u) {
@@ -399,11 +450,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(sV + kV * kTile);
   uint64_t *q_full = bar, *q_empty = bar + 1, *k_full = bar + 2, *k_empty = bar + 5, *zeroed = bar + 8, *v_full = bar + 11, *v_empty = bar + 13, *s_full = bar + 15,
            *dp_full = bar + 17, *ds_ready = bar + 18, *done = bar + 19, *drained = bar + 20;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 21);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 22);
+  const Handout hand{reinterpret_cast<long long*>(bar + 21), bar + 23, bar + 25, p.counters + 1, (long long)p.tiles * p.H};
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 27);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 28);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long total = (long long)p.tiles * p.H;
   if (warp == kMma) tmem_alloc(tslot, 512);
   if (tid == 0) {
     *abort_flag = 0;
@@ -415,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(ds_ready, kSoftmax + 1);
     mbar_init(done, 1);
     mbar_init(drained, 1);
+    hand.init(kSoftmax + 32 + 1);
     fence_mbar_init();
   }
   tc_fence_before();
@@ -431,17 +483,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool tail;
     AttnTile tl;
   };
-  auto item_of = [&](long long round, Item* x) {
-    long long i;
-    if (!round_item(round, total, &i)) return false;
+  auto describe = [&](long long i, Item* x) {
     x->h = int(i % p.H);
     x->hk = x->h / p.group;
     x->tl = attn_tile(p, int(i / p.H), kAttnTile, false);
     x->n = p.causal ? x->tl.first / kAttnTile + 1 : (x->tl.len + kAttnTile - 1) / kAttnTile;
     x->tail = x->n * kAttnTile > x->tl.len;
-    return true;
   };
   Item x;
+  // The round's tile, as the producer and the others learn of it; false at the end, and after an error (*ok false).
+  auto take = [&](long long round, bool* ok) {
+    long long i;
+    if (!hand.take(round, &i, ok, wait)) return false;
+    describe(i, &x);
+    return true;
+  };
+  auto get = [&](long long round, bool* ok) {
+    long long i;
+    if (!hand.get<false>(round, &i, ok, wait)) return false;
+    describe(i, &x);
+    return true;
+  };
+  auto get_warp = [&](long long round, bool* ok) {
+    long long i;
+    if (!hand.get<true>(round, &i, ok, wait)) return false;
+    describe(i, &x);
+    return true;
+  };
 
   if (warp >= kMma) {
     regs_dec<kOtherRegs>();
@@ -452,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int use = 0;         // key tiles requested
       uint32_t tiles = 0;  // query tiles
       bool ok = true;
-      for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+      for (long long rd = 0; ok && take(rd, &ok); ++rd) {
         if (tiles > 0) ok = __all_sync(0xffffffffu, wait(q_empty, (tiles - 1) & 1, kDevTimeoutMma));
         if (!ok) break;
         if (lane == 0) {
@@ -526,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) commit(lead, q_empty);  // and the scores, issued before, have read Q
       };
       bool ok = true;
-      for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+      for (long long rd = 0; ok && get_warp(rd, &ok); ++rd) {
         // the first products overwrite operands that the products issued so far have read
         if (!(ok = all_wait(q_full, rd & 1, kDevTimeoutTma) && scores(u, x.n == 1) && all_wait(&v_full[u & 1], u >> 1 & 1, kDevTimeoutTma))) break;
         if (x.n > 1) {
@@ -556,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- gate: V of the product that follows dS(i) has landed ----------------
       uint32_t u = 0;
       bool ok = true;
-      for (long long rd = 0; ok && item_of(rd, &x); ++rd)
+      for (long long rd = 0; ok && get(rd, &ok); ++rd)
         for (int i = 0; i < x.n && ok; ++i, ++u) {
           if (i + 1 < x.n && !(ok = wait(&v_full[(u + 1) & 1], (u + 1) >> 1 & 1, kDevTimeoutTma))) break;
           mbar_arrive(ds_ready);
@@ -572,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool wide = (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
     bool ok = true;
     uint32_t u = 0;
-    for (long long rd = 0; ok && item_of(rd, &x); ++rd) {
+    for (long long rd = 0; ok && get(rd, &ok); ++rd) {
       const int qi = x.tl.first + row;
       const bool mine = qi < x.tl.len;
       const long long at = (long long)x.h * p.rows + x.tl.row0 + qi;
