@@ -1,13 +1,15 @@
-"""A small language model of two kinds of recurrent blocks, trained, prompted and decoded token by token with this library.
+"""A small language model of recurrent and attention blocks, trained, prompted and decoded token by token with this library.
 
 Each block adds its predecessor's output to the residual stream and normalises it (``add_rms_norm``), mixes tokens with a
 short convolution and a recurrence, and ends in an output projection:
 
 * ``DeltaBlock``: convolution -> gated delta rule -> gated norm per head (``gated_rms_norm``);
-* ``ScanBlock``: convolution -> selective scan, whose own gate and skip close it.
+* ``ScanBlock``: convolution -> selective scan, whose own gate and skip close it;
+* ``AttentionBlock`` (``attention=True``): norm and rotation of every query and key head (``qk_norm_rope``) -> causal attention.
 
-A prompt leaves each block's states (``causal_conv1d_state`` and the recurrence's final state); decoding carries them on with
-``causal_conv1d_step``, ``gdn_step`` and ``selective_scan_step``. Run on a GB300: ``python examples/hybrid_blocks.py``.
+A prompt leaves each block's states (``causal_conv1d_state`` and the recurrence's final state; an attention block's keys and values
+in the pages of a cache, ``qk_norm_rope_store``); decoding carries them on with ``causal_conv1d_step``, ``gdn_step``,
+``selective_scan_step`` and ``attention_step``. Run on a GB300: ``python examples/hybrid_blocks.py``.
 """
 import os
 import sys
@@ -98,13 +100,57 @@ class ScanBlock:
         return lib.selective_scan_step(h, u, delta, A, B, C, D=self.p["D"], z=z, delta_bias=self.p["dt_bias"]) @ self.p["w_out"], stream
 
 
-class Model:
-    def __init__(self, vocab=512, heads=2, qk_heads=1, channels=384, states=16, rank=16, pairs=2):
+class AttentionBlock:
+    def __init__(self, heads, kv_heads, scale, page=64, pages=8, theta=1e4):
+        self.H, self.Hk, self.scale, self.page, self.pages = heads, kv_heads, scale, page, pages
         width = heads * 128
-        scale = (2 * pairs) ** -0.5
+        self.inv_freq = theta ** (-torch.arange(0, 128, 2, device="cuda", dtype=torch.float64) / 128).to(F32)
+        self.p = {
+            "norm": parameter(width, std=0, mean=1, dtype=F32), "w_in": parameter(width, width + 2 * kv_heads * 128, std=width ** -0.5),
+            "q_norm": parameter(128, std=0, mean=1, dtype=F32), "k_norm": parameter(128, std=0, mean=1, dtype=F32),
+            "w_out": parameter(width, width, std=width ** -0.5),
+        }
+
+    def heads(self, y):
+        q, k, v = (y @ self.p["w_in"]).split([self.H * 128, self.Hk * 128, self.Hk * 128], -1)     # they stay strided slices
+        return (t.unflatten(-1, (-1, 128)) for t in (q, k, v))
+
+    def cache(self, sequences, tokens):
+        """Empty pages for ``sequences``, and the lengths after ``tokens`` tokens."""
+        k = torch.zeros(sequences * self.pages, self.page, self.Hk, 128, dtype=BF16, device="cuda")
+        table = torch.arange(sequences * self.pages, dtype=torch.int32, device="cuda").view(sequences, self.pages)
+        return k, torch.zeros_like(k), table, torch.full((sequences,), tokens, dtype=torch.int32, device="cuda")
+
+    def prompt(self, x, stream, keep):
+        y, stream = lib.add_rms_norm(x, stream, self.p["norm"], residual_scale=self.scale)
+        q, k, v = self.heads(y)
+        cache = self.cache(*x.shape[:2]) if keep else None
+        if keep:
+            q, k = lib.qk_norm_rope_store(q, k, v, self.p["q_norm"], self.p["k_norm"], self.inv_freq, *cache)
+        else:
+            q, k = lib.qk_norm_rope(q, k, self.p["q_norm"], self.p["k_norm"], self.inv_freq)
+        return lib.attention(q, k, v).flatten(-2) @ self.p["w_out"], stream, cache
+
+    def step(self, x, stream, cache):
+        k_cache, v_cache, table, lengths = cache
+        y, stream = lib.add_rms_norm_fwd(x, stream, self.p["norm"], residual_scale=self.scale)
+        lengths += 1
+        q, k, v = self.heads(y)
+        q, _ = lib.qk_norm_rope_store(q, k, v, self.p["q_norm"], self.p["k_norm"], self.inv_freq, k_cache, v_cache, table, lengths)
+        return lib.attention_step(q, k_cache, v_cache, table, lengths).flatten(-2) @ self.p["w_out"], stream
+
+
+class Model:
+    def __init__(self, vocab=512, heads=2, qk_heads=1, channels=384, states=16, rank=16, pairs=2, attention=False):
+        width = heads * 128
+        scale = ((3 if attention else 2) * pairs) ** -0.5
         self.embed = parameter(vocab, width, std=1.0)
         self.norm = parameter(width, std=0, mean=1, dtype=F32)
-        self.blocks = [b for _ in range(pairs) for b in (DeltaBlock(heads, qk_heads, scale), ScanBlock(width, channels, states, rank, scale))]
+        self.blocks = []
+        for _ in range(pairs):
+            self.blocks += [DeltaBlock(heads, qk_heads, scale), ScanBlock(width, channels, states, rank, scale)]
+            if attention:
+                self.blocks.append(AttentionBlock(heads, qk_heads, scale))
 
     def parameters(self):
         return [self.embed, self.norm, *(t for b in self.blocks for t in b.p.values())]
@@ -154,7 +200,7 @@ def decode(model, tokens, cut):
 
 def main():
     torch.manual_seed(0)
-    model = Model()
+    model = Model(attention=True)
     tokens = torch.randint(0, 512, (4, 257), device="cuda")
     losses = train(model, tokens, 30)
     print(f"training: loss {losses[0]:.3f} -> {losses[-1]:.3f} in {len(losses)} steps")
