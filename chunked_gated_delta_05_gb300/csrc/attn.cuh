@@ -1,6 +1,8 @@
 // Parameters and device helpers of the attention block: norm and rotation of query and key heads (k_rope.cu), attention over
 // whole sequences (k_attn_fwd.cu, k_attn_bwd.cu) and of single tokens over a paged cache (k_attn_step.cu).
 #pragma once
+#include <atomic>
+
 #include "block_ops.cuh"
 #include "umma.cuh"
 
@@ -110,12 +112,16 @@ struct AttnTile {
   int row0, len, first;
 };
 
+constexpr int kAttnInline = 170;     // tiles whose table goes along with the parameters (packed calls of up to some 20000 tokens)
+
 struct AttnParams {
   int H, Hk, group;            // group = H / Hk query heads read one key head
   int T, N;                    // dense: tokens per sequence and sequences
   int tiles;                   // tiles of all sequences
   int sms;
-  const int* table;            // packed: 3 ints per tile, most work first; else null (dense, computed)
+  bool packed;                 // else the tiles are computed
+  const int* table;            // packed: 3 ints per tile, most work first, or null: `few`
+  int few[3 * kAttnInline];
   int causal;
   float scale;
   long long rows;
@@ -133,7 +139,10 @@ struct AttnParams {
 // Tile `i` of `step` tokens. Of a dense batch's sequences the last tiles come first (causal: the longest rows), or the first ones
 // (`ascending`: causal keys, which the most queries see).
 __device__ __forceinline__ AttnTile attn_tile(const AttnParams& p, int i, int step, bool ascending) {
-  if (p.table) return {p.table[3 * i], p.table[3 * i + 1], p.table[3 * i + 2]};
+  if (p.packed) {
+    if (p.table) return {p.table[3 * i], p.table[3 * i + 1], p.table[3 * i + 2]};
+    return {p.few[3 * i], p.few[3 * i + 1], p.few[3 * i + 2]};
+  }
   const int level = i / p.N, n = i - level * p.N, per = (p.T + step - 1) / step;
   return {n * p.T, p.T, (ascending ? level : per - 1 - level) * step};
 }
@@ -203,16 +212,32 @@ __device__ __forceinline__ void zero_attn_rows(uint8_t* tile, int from, int lane
 }
 
 cudaError_t launch_attn_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, int D, const AttnParams& p, cudaStream_t s);
-// Backward: `order` holds the dq kernel's tiles (128 queries, most work first) and `keys` the dk / dv kernel's.
-cudaError_t launch_attn_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, int D, const AttnParams& p, const int* keys,
+// Backward: `p` holds the dq kernel's tiles (128 queries, most work first) and `pk` the dk / dv kernel's.
+cudaError_t launch_attn_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, int D, const AttnParams& p, const AttnParams& pk,
                             cudaStream_t s);
+// Sets a kernel's shared memory limit, once per kernel (`done`: a bit per device) and device.
+template <typename K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<unsigned long long>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done->load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // ------------------------------------------------------------------ norm and rotation of query and key heads
+
+constexpr int kRopeInline = 64;      // offsets that go along with the parameters
 
 struct RopeParams {
   long long rows;              // tokens of all sequences
   int T, N;                    // dense: tokens per sequence; sequences
-  const int* cu;               // packed: device offsets [N+1], else null
+  bool packed;
+  const int* cu;               // packed: device offsets [N+1], or null: `few`
+  int few[kRopeInline];
   int H, Hk, rotary, interleaved;
   float eps;
   long long q_s, k_s, v_s;     // elements between tokens

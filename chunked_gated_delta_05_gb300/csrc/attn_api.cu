@@ -137,9 +137,14 @@ RopeParams rope_params(const gdn_rope_desc_t* d, const RopeProblem& P) {
   return p;
 }
 
-// The device copy of packed offsets, which the kernels search for a token's document.
+// Packed offsets, which the kernels search for a token's document: few go along with the parameters, more to the device first.
 int rope_offsets(const RopeProblem& P, const RopeLayout& l, void* ws, RopeParams* p, cudaStream_t s) {
   if (!P.S.cu) return GDN_OK;
+  p->packed = true;
+  if (P.S.N + 1 <= kRopeInline) {
+    std::copy(P.S.cu, P.S.cu + P.S.N + 1, p->few);
+    return GDN_OK;
+  }
   int* cu = reinterpret_cast<int*>(static_cast<char*>(ws) + l.cu);
   p->cu = cu;
   return upload_offsets(P.S.cu, P.S.N + 1, cu, s);
@@ -227,8 +232,9 @@ int validate_attn(const gdn_attn_desc_t* d, AttnProblem* P) {
 size_t table_bytes(const AttnProblem& P, long long tiles) { return P.S.cu ? align256(size_t(tiles) * 12) : 0; }
 
 // Packed documents: {first row, length, first token} of every tile of `step` tokens, a sequence's last tiles first (or its first
-// ones, `ascending`), level by level through the sequences, longest first: the tiles with the most work start first.
-int upload_tiles(const AttnProblem& P, int step, bool ascending, int* dst, cudaStream_t s) {
+// ones, `ascending`), level by level through the sequences, longest first: the tiles with the most work start first. Few go along
+// with the parameters, more to the device first.
+int pack_tiles(const AttnProblem& P, int step, bool ascending, AttnParams* p, int* dst, cudaStream_t s) {
   const int32_t* cu = P.S.cu;
   std::vector<int> order(P.S.N);
   for (int i = 0; i < P.S.N; ++i) order[i] = i;
@@ -247,6 +253,12 @@ int upload_tiles(const AttnProblem& P, int step, bool ascending, int* dst, cudaS
       table.push_back(level * step);
     }
   }
+  p->packed = true;
+  if (table.size() <= 3 * kAttnInline) {
+    std::copy(table.begin(), table.end(), p->few);
+    return GDN_OK;
+  }
+  p->table = dst;
   return upload_offsets(table.data(), int(table.size()), dst, s);
 }
 
@@ -291,11 +303,7 @@ int attn_fwd(const gdn_attn_desc_t* d, const gdn_attn_fwd_args_t* a, void* strea
   if (!input_maps(P, a->q, a->k, a->v, &mq, &mk, &mv)) return set_last_error(GDN_ECUDA, "cuTensorMapEncodeTiled failed");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TimedScope t(kKAttnFwd, s);
-  if (P.S.cu) {
-    int* table = static_cast<int*>(a->workspace);
-    p.table = table;
-    if ((rc = upload_tiles(P, kAttnPair, false, table, s))) return rc;
-  }
+  if (P.S.cu && (rc = pack_tiles(P, kAttnPair, false, &p, static_cast<int*>(a->workspace), s))) return rc;
   return cuda_rc(launch_attn_fwd(mq, mk, mv, P.S.D, p, s), "attention kernel");
 }
 
@@ -347,14 +355,11 @@ int attn_bwd(const gdn_attn_desc_t* d, const gdn_attn_bwd_args_t* a, void* strea
     return set_last_error(GDN_ECUDA, "cuTensorMapEncodeTiled failed");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TimedScope t(kKAttnBwd, s);
-  int* keys = nullptr;
-  if (P.S.cu) {
-    int* order = reinterpret_cast<int*>(ws + l.order);
-    keys = reinterpret_cast<int*>(ws + l.keys);
-    p.table = order;
-    if ((rc = upload_tiles(P, kAttnTile, false, order, s)) || (rc = upload_tiles(P, kAttnTile, true, keys, s))) return rc;
-  }
-  return cuda_rc(launch_attn_bwd(mq, mk, mv, mdo, P.S.D, p, keys, s), "attention backward kernels");
+  AttnParams pk = p;
+  if (P.S.cu && ((rc = pack_tiles(P, kAttnTile, false, &p, reinterpret_cast<int*>(ws + l.order), s)) ||
+                 (rc = pack_tiles(P, kAttnTile, true, &pk, reinterpret_cast<int*>(ws + l.keys), s))))
+    return rc;
+  return cuda_rc(launch_attn_bwd(mq, mk, mv, mdo, P.S.D, p, pk, s), "attention backward kernels");
 }
 
 // ------------------------------------------------------------------ single tokens

@@ -97,7 +97,7 @@ struct Handout {
 
 // -D_i and -lse_i log2(e) of 32 rows of a head a warp.
 template <int D>
-__global__ void __launch_bounds__(256) k_attn_delta(const AttnParams p) {
+__global__ void __launch_bounds__(256) k_attn_delta(const __grid_constant__ AttnParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
   const int lane = threadIdx.x & 31, sub = lane % kLanes, which = lane / kLanes;
   const long long chunks = (p.rows + 31) / 32, item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(256) k_attn_delta(const AttnParams p) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_dkv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-               const __grid_constant__ CUtensorMap mdo, const AttnParams p) {
+               const __grid_constant__ CUtensorMap mdo, const __grid_constant__ AttnParams p) {
   constexpr int kTile = Cfg<D>::kTile, kQ = 3, kO = 2;  // stages of Q and of dO (a Q tile is needed longer)
   extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t *sK = sm, *sV = sK + kTile, *sQ = sV + kTile, *sO = sQ + kQ * kTile;
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-              const __grid_constant__ CUtensorMap mdo, const AttnParams p) {
+              const __grid_constant__ CUtensorMap mdo, const __grid_constant__ AttnParams p) {
   constexpr int kTile = Cfg<D>::kTile, kK = 3, kV = 2;  // stages of K (needed longer) and V
   extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t *sQ = sm, *sO = sQ + kTile, *sK = sO + kTile, *sV = sK + kK * kTile;
@@ -689,25 +689,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-static cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, const AttnParams& p, const int* keys, cudaStream_t s) {
+static cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, const AttnParams& p, const AttnParams& pk, cudaStream_t s) {
   constexpr int kSmem = Cfg<D>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(k_attn_dkv<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_attn_dq<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<unsigned long long> done_dkv{0}, done_dq{0};
+  cudaError_t e = allow_smem(k_attn_dkv<D>, kSmem, &done_dkv);
+  if (e == cudaSuccess) e = allow_smem(k_attn_dq<D>, kSmem, &done_dq);
   if (e != cudaSuccess) return e;
   const long long items = (p.rows + 31) / 32 * p.H;
   e = launch_after(k_attn_delta<D>, dim3(unsigned((items + 7) / 8)), dim3(256), 0, s, p);
   if (e != cudaSuccess) return e;
-  AttnParams pk = p;
-  pk.table = keys;
   const long long nk = (long long)p.tiles * p.Hk, nq = (long long)p.tiles * p.H;
   e = launch_after(k_attn_dkv<D>, dim3(unsigned(nk < p.sms ? nk : p.sms)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, pk);
   if (e != cudaSuccess) return e;
   return launch_after(k_attn_dq<D>, dim3(unsigned(nq < p.sms ? nq : p.sms)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, p);
 }
 
-cudaError_t launch_attn_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, int D, const AttnParams& p, const int* keys,
+cudaError_t launch_attn_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, int D, const AttnParams& p, const AttnParams& pk,
                             cudaStream_t s) {
-  return D == 128 ? launch<128>(mq, mk, mv, mdo, p, keys, s) : launch<64>(mq, mk, mv, mdo, p, keys, s);
+  return D == 128 ? launch<128>(mq, mk, mv, mdo, p, pk, s) : launch<64>(mq, mk, mv, mdo, p, pk, s);
 }
 
 }  // namespace gdn

@@ -71,7 +71,7 @@ __device__ __forceinline__ bool item_of(const AttnParams& p, long long round, lo
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attn_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnParams p) {
+    k_attn_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnParams p) {
   using C = Cfg<D>;
   constexpr int kS = C::kStages, kTile = C::kTileBytes;
   extern __shared__ uint8_t smem_raw[];
@@ -349,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 static cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(k_attn_fwd<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(k_attn_fwd<D>, Cfg<D>::kSmem, &done);
   if (e != cudaSuccess) return e;
   const long long items = (long long)p.tiles * p.H;
   return launch_after(k_attn_fwd<D>, dim3(unsigned(items < p.sms ? items : p.sms)), dim3(kThreads), Cfg<D>::kSmem, s, mq, mk, mv, p);

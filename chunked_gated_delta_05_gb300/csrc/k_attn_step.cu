@@ -373,7 +373,8 @@ static cudaError_t launch(const AttnStepParams& p, cudaStream_t s) {
   static_assert(kSmem >= kWarps * 8 * kRows * D * 4, "the warps' sums lie where the stages were");
   const int rb = (p.group + 8 * kRows - 1) / (8 * kRows);
   const dim3 block(kWarps * 32), rows(unsigned((long long)p.B * p.H));
-  cudaError_t e = cudaFuncSetAttribute(k_attn_step<D, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(k_attn_step<D, kRows>, kSmem, &done);
   if (e == cudaSuccess) e = launch_after(k_attn_step<D, kRows>, dim3(unsigned(p.shares * p.Hk * rb)), block, kSmem, s, p, rb);
   if (e != cudaSuccess) return e;
   return p.shares > 16 * p.B ?  // pieces of a row: about the shares over the rows

@@ -177,15 +177,16 @@ struct Token {
 // Sequence of `row`, then its position and place in the cache.
 __device__ __forceinline__ Token token_of(const RopeParams& p, int row, bool report) {
   int n, t, len;
-  if (p.cu) {
+  if (p.packed) {
+    auto cu = [&](int i) { return p.cu ? p.cu[i] : p.few[i]; };
     int lo = 0, hi = p.N;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (p.cu[mid] <= row) lo = mid; else hi = mid;
+      if (cu(mid) <= row) lo = mid; else hi = mid;
     }
     n = lo;
-    t = row - p.cu[n];
-    len = p.cu[n + 1] - p.cu[n];
+    t = row - cu(n);
+    len = cu(n + 1) - cu(n);
   } else {
     n = int(unsigned(row) / unsigned(p.T));
     t = row - n * p.T;
@@ -257,7 +258,7 @@ __device__ __forceinline__ void rope_heads(const RopeParams& p, const Lane<D, kP
 
 // blockIdx.y: the chunk of `per` of a token's passes (q's, then k's, then (store) v's).
 template <int D, bool kPairs, bool kStore>
-__global__ void __launch_bounds__(kWarps * 32, kFwdBlocks) k_rope_fwd(const RopeParams p, int per) {
+__global__ void __launch_bounds__(kWarps * 32, kFwdBlocks) k_rope_fwd(const __grid_constant__ RopeParams p, int per) {
   constexpr int kHeads = 256 / D;
   wait_for_previous();
   const int lane = threadIdx.x & 31, which = lane / (D / 8);
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kWarps * 32, kFwdBlocks) k_rope_fwd(const Rope
 }
 
 template <int D, bool kPairs>
-__global__ void __launch_bounds__(kWarps * 32, kBwdPerSm) k_rope_bwd(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kBwdPerSm) k_rope_bwd(const __grid_constant__ RopeParams p) {
   wait_for_previous();
   constexpr int kHeads = 256 / D, kTogether = 4;
   __shared__ float part[kWarps][2][D];
