@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(256) k_attn_delta(const __grid_constant__ Attn
   const int h = int(item % p.H);
   const long long row0 = item / p.H * 32;
   float mine = 0.f;
-#pragma unroll 4
+#pragma unroll
   for (int i = 0; i < kLanes; ++i) {
     const long long row = row0 + i * kRows + which;
     float x = 0.f;

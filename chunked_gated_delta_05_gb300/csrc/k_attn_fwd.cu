@@ -18,10 +18,10 @@
 // idles (measured; a tile's two products take 1024). So the issuing thread waits once per tile and iteration, on a barrier on which both the
 // tile's 128 softmax threads and a gate thread arrive, the latter when the K and V tiles needed next have landed.
 //
-// The reference m moves only when a row's maximum lies more than 2^8 above it (then l and the accumulator are rescaled):
-// weights up to 256 cost no precision in bf16 or fp32, almost no tile needs it, and the weights can be taken against the reference at
-// hand while the maximum is still being looked for. It needs no wait: the commit that announces S_t(j) also covers the
-// product O_t(j - 1) issued before it.
+// The reference m is the row's maximum in its first tile and moves only when a later tile's weights sum to more than 2^16 (then l and
+// the accumulator are rescaled and the tile's weights taken again): weights up to that cost no precision in bf16 or fp32, almost no
+// tile needs it, and no maximum is taken in the others (64 instructions of 380 a row, and nearly a third of the time). It
+// needs no wait: the commit that announces S_t(j) also covers the product O_t(j - 1) issued before it.
 //
 // Keys past the sequence's end are masked in the scores, and the last tile's values past it are zeroed in shared memory: they
 // belong to the next sequence, and 0 x NaN would carry a neighbour's NaN over.
@@ -34,7 +34,7 @@ constexpr int kThreads = 384;  // 8 softmax warps, the MMA warp, the TMA warp an
 // The launch's 168 registers a thread (12 warps x 168 x 32 = 64512) are shared out anew: 208 for the softmax's rows of 128 scores,
 // 88 for the rest (8 x 208 + 4 x 88 = 12 x 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-constexpr float kRescale = 8.f;
+constexpr float kHigh = 65536.f;  // sum of a tile's weights that moves the reference
 
 template <int D>
 struct Cfg {
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_inc<kSoftmaxRegs>();
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lb = tmem_lane_base(warp);
-    const float c = p.scale * kLog2e, far = fminf(kRescale / c, 3e38f);
+    const float c = p.scale * kLog2e;
     const F2 c2 = dup2(c);
     uint32_t cnt = 0, outs = 0;
     bool ok = true;
@@ -269,10 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < mine; ++j) {
         if (!(ok = wait(&s_full[t], cnt++ & 1, kDevTimeoutMma))) break;
         tc_fence_after();
-        // Weights against the reference at hand, and the row's maximum beside them (the two run on different units): only where
-        // that lies too far above the reference does it move, and the weights are taken again from the scores in TMEM.
-        const F2 before = l2;
         float w[64];
+        bool fresh = j == 0;  // the reference is taken from this tile
 #pragma unroll 1
         while (true) {
           float s[128];
@@ -285,40 +283,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 128; ++e)
               if (e >= seen) s[e] = -INFINITY;
           }
-          if (j == 0) {
+          if (fresh) {
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
             for (int e = 4; e < 124; e += 8)
 #pragma unroll
               for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[e + u], s[e + 4 + u]);
-            m = max3(max3(mx[0], mx[1], s[124]), max3(mx[2], mx[3], s[125]), fmaxf(s[126], s[127]));
+            const float top = max3(max3(mx[0], mx[1], s[124]), max3(mx[2], mx[3], s[125]), fmaxf(s[126], s[127]));
+            const float next = fmaxf(m, top), f = next == m ? 1.f : exp2_approx((m - next) * c);
+            m = next;
+            l2 = mul2(l2, dup2(f));
+            if (j > 0) {
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                float o[32];
+                tmem_ld32(tO(t) + lb + q * 32, o);
+                tmem_wait_ld_regs(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= f;
+                tmem_st32(tO(t) + lb + q * 32, o);
+              }
+            }
           }
           const F2 mc = dup2(-m * c);
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          F2 sum[2] = {dup2(0.f), dup2(0.f)};
 #pragma unroll
           for (int e = 0; e < 64; ++e) {
             float a, b;
-            mx[e & 3] = max3(mx[e & 3], s[2 * e], s[2 * e + 1]);
             unf2(fma2(f2(s[2 * e], s[2 * e + 1]), c2, mc), &a, &b);
             a = exp2_approx(a);
             b = exp2_approx(b);
-            l2 = add2(l2, f2(a, b));
+            sum[e & 1] = add2(sum[e & 1], f2(a, b));
             w[e] = __uint_as_float(pack_bf16(a, b));
           }
-          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-          if (!__any_sync(0xffffffffu, top > m + far)) break;
-          const float next = fmaxf(m, top), f = next == -INFINITY ? 1.f : exp2_approx((m - next) * c);
-          m = next;
-          l2 = mul2(before, dup2(f));
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {  // not in the first tile, whose reference is its maximum
-            float o[32];
-            tmem_ld32(tO(t) + lb + q * 32, o);
-            tmem_wait_ld_regs(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st32(tO(t) + lb + q * 32, o);
+          sum[0] = add2(sum[0], sum[1]);
+          if (fresh || !__any_sync(0xffffffffu, sum2(sum[0]) > kHigh)) {
+            l2 = add2(l2, sum[0]);
+            break;
           }
+          fresh = true;
         }
         tmem_st32(tS(t) + lb, w);
         tmem_st32(tS(t) + lb + 32, w + 32);
