@@ -40,6 +40,14 @@ def _heads(q, k, v):
     return dev, lead, H, Hk, D, (_rows("q", q, shape, dev, H * D), _rows("k", k, keys, dev, Hk * D), 0 if v is None else _rows("v", v, keys, dev, Hk * D))
 
 
+def _vectors(n, dev, *vectors):
+    """Whether all are contiguous fp32 vectors of n on the device: one cheap test of the usual case ahead of _want's messages."""
+    for t in vectors:
+        if not (isinstance(t, torch.Tensor) and t.dtype is _F32 and t.numel() == n and t.dim() == 1 and t.get_device() == dev and t.is_contiguous()):
+            return False
+    return True
+
+
 def _packed(offsets, n):
     return (0, n) if offsets is None else (ctypes.addressof(offsets[0]), offsets[1])
 
@@ -50,15 +58,16 @@ def _rope_inputs(q, k, v, q_weight, k_weight, inv_freq, positions, interleaved, 
     B, T = (lead[0], 1) if len(lead) == 1 else lead
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight must both be given or both be None")
-    if q_weight is not None:
+    if q_weight is not None and not _vectors(D, dev, q_weight, k_weight):
         _want("q_weight", q_weight, _F32, (D,), dev)
         _want("k_weight", k_weight, _F32, (D,), dev)
     rotary = 0
     if inv_freq is not None:
         if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be [rotary/2]")
-        _want("inv_freq", inv_freq, _F32, inv_freq.shape, dev)
-        rotary = 2 * inv_freq.shape[0]
+        rotary = 2 * len(inv_freq)
+        if not _vectors(rotary // 2, dev, inv_freq):
+            _want("inv_freq", inv_freq, _F32, inv_freq.shape, dev)
     if positions is not None:
         _want("positions", positions, _I32, tuple(lead), dev)
     cu, n = _packed(offsets, B)
@@ -116,14 +125,20 @@ def _cache(k_cache, v_cache, page_table, lengths, n, Hk, D, dev):
     """Checks a paged cache ``[pages,page size,Hk,D]`` and its tables; ``(pages, page size, table width)``."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages,page_size,Hk,D]")
-    pages, page = k_cache.shape[:2]
-    _want("k_cache", k_cache, _BF16, (pages, page, Hk, D), dev)
-    _want("v_cache", v_cache, _BF16, (pages, page, Hk, D), dev)
+    shape = k_cache.shape
+    pages, page, heads, width = shape
+    if not (heads == Hk and width == D and isinstance(v_cache, torch.Tensor) and v_cache.shape == shape and k_cache.dtype is v_cache.dtype is _BF16 and
+            k_cache.get_device() == v_cache.get_device() == dev and k_cache.is_contiguous() and v_cache.is_contiguous()):     # which of these it is
+        _want("k_cache", k_cache, _BF16, (pages, page, Hk, D), dev)
+        _want("v_cache", v_cache, _BF16, (pages, page, Hk, D), dev)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [sequences,pages of a sequence]")
-    _want("page_table", page_table, _I32, (n, page_table.shape[1]), dev)
-    _want("lengths", lengths, _I32, (n,), dev)
-    return pages, page, page_table.shape[1]
+    rows, columns = page_table.shape
+    if not (rows == n and isinstance(lengths, torch.Tensor) and lengths.dim() == 1 and lengths.numel() == n and page_table.dtype is lengths.dtype is _I32 and
+            page_table.get_device() == lengths.get_device() == dev and page_table.is_contiguous() and lengths.is_contiguous()):
+        _want("page_table", page_table, _I32, (n, columns), dev)
+        _want("lengths", lengths, _I32, (n,), dev)
+    return pages, page, columns
 
 
 def qk_norm_rope_store(q, k, v, q_weight, k_weight, inv_freq, k_cache, v_cache, page_table, lengths, *, cu_seqlens: Optional[Sequence[int]] = None, eps=1e-6,
