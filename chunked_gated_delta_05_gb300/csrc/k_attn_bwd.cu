@@ -45,12 +45,16 @@ __device__ __forceinline__ void store_operand(uint32_t t, const float* x) {
   tmem_st32(t, w);
 }
 
-// 32 columns of an accumulator row times f, as bf16.
+// kN columns of an accumulator row times f, as bf16.
+template <int kN>
 __device__ __forceinline__ void store_row(__nv_bfloat16* dst, uint32_t t, float f, bool mine, bool wide) {
-  float o[32];
-  tmem_ld32(t, o);
+  float o[kN];
+#pragma unroll
+  for (int q = 0; q < kN / 32; ++q) tmem_ld32(t + q * 32, o + q * 32);
   tmem_wait_ld_regs(o);
-  if (mine) store_bf16x32(dst, o, f, wide);
+  if (mine)
+#pragma unroll
+    for (int q = 0; q < kN / 32; ++q) store_bf16x32(dst + q * 32, o + q * 32, f, wide);
 }
 
 // Output tiles are handed out as CTAs get free, the ones with the most work first (a fixed assignment left some CTAs 20% more work
@@ -430,8 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key = tl.first + (tid & 127);
     __nv_bfloat16* dst = (half ? p.dk : p.dv) + ((size_t(tl.row0) + key) * p.Hk + x.hk) * D;
     const uint32_t acc = (half ? tK : tV) + lane0;
-#pragma unroll
-    for (int q = 0; q < D / 32; ++q) store_row(dst + q * 32, acc + q * 32, half ? p.scale : 1.f, key < tl.len, wide);
+    store_row<D>(dst, acc, half ? p.scale : 1.f, key < tl.len, wide);
     tc_fence_before();
     }
   }
@@ -678,8 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || !(ok = wait(done, rd & 1, kDevTimeoutMma))) break;
       tc_fence_after();
       __nv_bfloat16* dst = p.dq + ((size_t(x.tl.row0) + qi) * p.H + x.h) * D + half * (D / 2);
-#pragma unroll
-      for (int q = 0; q < D / 64; ++q) store_row(dst + q * 32, tQ + lane0 + half * (D / 2) + q * 32, p.scale, mine, wide);
+      store_row<D / 2>(dst, tQ + lane0 + half * (D / 2), p.scale, mine, wide);
       tc_fence_before();
     }
   }

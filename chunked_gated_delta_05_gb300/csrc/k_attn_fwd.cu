@@ -335,13 +335,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
       const size_t at = (size_t(it.tl.row0) + qi) * p.H + it.h;
       if (qi < len) p.lse[at] = m * p.scale + logf(l);
+      float o[D];
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        float o[32];
-        tmem_ld32(tO(t) + lb + q * 32, o);
-        tmem_wait_ld_regs(o);
-        if (qi < len) store_bf16x32(p.o + at * D + q * 32, o, r, wide);
-      }
+      for (int q = 0; q < D / 64; ++q) tmem_ld64(tO(t) + lb + q * 64, o + q * 64);
+      tmem_wait_ld_regs(o);
+      if (qi < len)
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) store_bf16x32(p.o + at * D + q * 32, o + q * 32, r, wide);
       tc_fence_before();
     }
   }
