@@ -3,8 +3,8 @@
 //   dv_j = sum_i p_ij dO_i,   dk_j = scale sum_i dS_ij q_i,   dq_i = scale sum_j dS_ij k_j
 // summed over the query heads of a key head for dk and dv.
 //
-// Three kernels. k_attn_delta leaves D and lse log2(e) by head. k_attn_dkv owns 128 keys of a key head and walks the query tiles
-// (and the group's heads) that see them; k_attn_dq owns 128 queries and walks the key tiles they see. Each output is
+// Three kernels. k_attn_delta leaves D and lse log2(e) by head. k_attn_dq owns 128 queries and walks the key tiles they see;
+// k_attn_dkv owns 128 keys of a key head and walks the query tiles (and the group's heads) that see them. Each output is
 // summed in registers of one CTA's tensor core in a fixed order, so nothing is added atomically and results do not depend on
 // the order of blocks; the price is that both recompute s and dP: seven products of 128 x 128 x D a tile pair, where adding dq up in
 // memory would need five.
@@ -20,6 +20,12 @@
 //
 // Eight softmax warps, two to a quarter of the TMEM lanes, each on half of a tile's columns. The bf16 operand's halves lie over the
 // columns that their own writers have read. p and dS are rounded to bf16 (as the products' operands); all sums are fp32.
+//
+// D from o carries o's rounding to bf16, which a query of few keys feels (dP - D is small there, and 0 for a single key). So the
+// query tiles that see one key tile, the first 128 queries of a causal sequence and all of a shorter one, have it from the scores
+// themselves: sum_j p_ij dP_ij / sum_j p_ij. k_attn_dq, which has a query's whole row there, leaves it to k_attn_dkv, and a query
+// of a single key has dS = 0 in both. (Sequences of 3 to 20 tokens: dq and dk off by 0.0027
+// to 0.0033 of their size with o's D, 0.0024 so, what the operands' and outputs' roundings make.)
 #include "attn.cuh"
 
 namespace gdn {
@@ -419,6 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mbar_arrive(&vec_free[os]);
+      if (q0 + col == 0 && (p.causal || tl.len == 1))  // the sequence's first query sees a single key
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d[(r >> 1) * 32 + (r & 1) * 2] = 0.f;
 #pragma unroll
       for (int e = 0; e < 32; ++e) out[e] = pack_bf16(d[2 * e], d[2 * e + 1]);
       tmem_st_16x32(tP + lb, out);
@@ -454,8 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *q_full = bar, *q_empty = bar + 1, *k_full = bar + 2, *k_empty = bar + 5, *zeroed = bar + 8, *v_full = bar + 11, *v_empty = bar + 13, *s_full = bar + 15,
            *dp_full = bar + 17, *ds_ready = bar + 18, *done = bar + 19, *drained = bar + 20;
   const Handout hand{reinterpret_cast<long long*>(bar + 21), bar + 23, bar + 25, p.counters + 1, (long long)p.tiles * p.H};
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 27);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 28);
+  uint64_t* summed = bar + 27;  // [4]: both halves of 32 queries' rows
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 31);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 32);
+  float2* sums = reinterpret_cast<float2*>(bar + 64);  // [256]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == kMma) tmem_alloc(tslot, 512);
@@ -469,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(ds_ready, kSoftmax + 1);
     mbar_init(done, 1);
     mbar_init(drained, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&summed[i], 64);
     hand.init(kSoftmax + 32 + 1);
     fence_mbar_init();
   }
@@ -642,12 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const F2 c2 = dup2(p.scale * kLog2e);
     const bool wide = (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
     bool ok = true;
-    uint32_t u = 0;
+    uint32_t u = 0, short_rows = 0;
     for (long long rd = 0; ok && get(rd, &ok); ++rd) {
       const int qi = x.tl.first + row;
       const bool mine = qi < x.tl.len;
       const long long at = (long long)x.h * p.rows + x.tl.row0 + qi;
-      const F2 lse = dup2(mine ? p.lse2[at] : 0.f), delta = dup2(mine ? p.delta[at] : 0.f);
+      const F2 lse = dup2(mine ? p.lse2[at] : 0.f);
+      F2 delta = dup2(mine && x.n > 1 ? p.delta[at] : 0.f);
       for (int i = 0; i < x.n && ok; ++i, ++u) {
         if (!(ok = wait(&s_full[u & 1], u >> 1 & 1, kDevTimeoutMma))) break;
         tc_fence_after();
@@ -665,14 +678,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_ld64(tP + lb, d);
         tmem_wait_ld_regs(d);
-#pragma unroll
-        for (int e = 0; e < kCols / 2; ++e) unf2(mul2(f2(w[2 * e], w[2 * e + 1]), add2(f2(d[2 * e], d[2 * e + 1]), delta)), &d[2 * e], &d[2 * e + 1]);
+        const int seen = p.causal ? min(qi + 1, x.tl.len) : x.tl.len;
         if (i + 1 == x.n && (p.causal || x.tail)) {
-          const int seen = (p.causal ? min(qi + 1, x.tl.len) : x.tl.len) - i * kAttnTile - half * kCols;
+          const int left = seen - i * kAttnTile - half * kCols;
 #pragma unroll
           for (int e = 0; e < kCols; ++e)
-            if (e >= seen) d[e] = 0.f;
+            if (e >= left) w[e] = d[e] = 0.f;
         }
+        if (x.n == 1) {
+          // the row's D from its two halves' sums; a half's slot is written again only after the other's dS of this tile
+          F2 a = dup2(0.f), b = a;
+#pragma unroll
+          for (int e = 0; e < kCols / 2; ++e) {
+            a = fma2(f2(w[2 * e], w[2 * e + 1]), f2(d[2 * e], d[2 * e + 1]), a);
+            b = add2(b, f2(w[2 * e], w[2 * e + 1]));
+          }
+          float a0, a1, b0, b1;
+          unf2(a, &a0, &a1);
+          unf2(b, &b0, &b1);
+          sums[tid] = make_float2(a0 + a1, b0 + b1);
+          mbar_arrive(&summed[warp & 3]);
+          if (!(ok = wait(&summed[warp & 3], short_rows++ & 1, kDevTimeoutSync))) break;
+          const float2 lo = sums[row], hi = sums[row + 128];
+          const float own = -(lo.x + hi.x) / (lo.y + hi.y);
+          delta = dup2(own);
+          if (mine && half == 0) p.delta[at] = own;
+        }
+#pragma unroll
+        for (int e = 0; e < kCols / 2; ++e) unf2(mul2(f2(w[2 * e], w[2 * e + 1]), add2(f2(d[2 * e], d[2 * e + 1]), delta)), &d[2 * e], &d[2 * e + 1]);
+        if (x.n == 1 && seen == 1 && half == 0) d[0] = 0.f;
         store_operand(tS(u) + lb, d);
         tmem_wait_st();
         tc_fence_before();
@@ -701,9 +735,9 @@ static cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CU
   e = launch_after(k_attn_delta<D>, dim3(unsigned((items + 7) / 8)), dim3(256), 0, s, p);
   if (e != cudaSuccess) return e;
   const long long nk = (long long)p.tiles * p.Hk, nq = (long long)p.tiles * p.H;
-  e = launch_after(k_attn_dkv<D>, dim3(unsigned(nk < p.sms ? nk : p.sms)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, pk);
+  e = launch_after(k_attn_dq<D>, dim3(unsigned(nq < p.sms ? nq : p.sms)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, p);
   if (e != cudaSuccess) return e;
-  return launch_after(k_attn_dq<D>, dim3(unsigned(nq < p.sms ? nq : p.sms)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, p);
+  return launch_after(k_attn_dkv<D>, dim3(unsigned(nk < p.sms ? nk : p.sms)), dim3(kThreads), kSmem, s, mq, mk, mv, mdo, pk);
 }
 
 cudaError_t launch_attn_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, int D, const AttnParams& p, const AttnParams& pk,

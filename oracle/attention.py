@@ -71,10 +71,13 @@ def attention_bwd(dO, q, k, v, starts, scale, causal):
     return dq, dk, dv
 
 
-def bounds(dO, q, k, v, starts, scale, causal, half=2.0 ** -8):
+def bounds(dO, q, k, v, starts, scale, causal, half=2.0 ** -8, tile=0):
     """How far results may lie from the exact ones when the weights and their gradients are rounded once to a type whose half step is
     ``half`` relative, outputs once more, and scores and products are fp32 sums of D terms in any order (each of at most D 2^-23 of
-    the sum of their magnitudes): a dict of elementwise bounds for o, lse, dq, dk, dv. First-order in the roundings, plus 1% for the rest."""
+    the sum of their magnitudes): a dict of elementwise bounds for o, lse, dq, dk, dv. First-order in the roundings, plus 1% for the rest.
+
+    The sum D of a row's weights times their gradients is taken from the rounded o, but from the weights themselves for the queries that
+    see only the sequence's first ``tile`` keys by their place (its first ``tile`` queries if causal, all of it if it is no longer)."""
     D, H, G = q.shape[2], q.shape[1], q.shape[1] // k.shape[1]
     out = {"o": np.zeros_like(q), "lse": np.zeros(q.shape[:2]), "dq": np.zeros_like(q), "dk": np.zeros_like(k), "dv": np.zeros_like(v)}
     exact = dict(zip(("o", "lse"), attention(q, k, v, starts, scale, causal)))
@@ -97,6 +100,10 @@ def bounds(dO, q, k, v, starts, scale, causal, half=2.0 ** -8):
             dP = O @ V.T
             delta = (P * dP).sum(-1, keepdims=True)
             edelta = (np.abs(O) * eo).sum(-1, keepdims=True) + D * fp * (np.abs(O) * np.abs(exact["o"][a:b, h])).sum(-1, keepdims=True)
+            own = np.arange(b - a) < (tile if causal or b - a <= tile else 0)
+            # sum p dP / sum p: the weights' relative errors on dP - D, the products' errors, and at most `tile` + 8 roundings of the sums
+            edelta[own] = ((P * rel * np.abs(dP - delta)).sum(-1, keepdims=True) + D * fp * (P * (np.abs(O) @ np.abs(V).T)).sum(-1, keepdims=True)
+                           + (tile + 8) * fp * (P * np.abs(dP)).sum(-1, keepdims=True))[own]
             dS = np.abs(P * (dP - delta))
             edS = (half + rel) * dS + P * (D * fp * np.abs(O) @ np.abs(V).T + edelta + 2 * fp * (np.abs(dP) + np.abs(delta)))
             out["dq"][a:b, h] = scale * edS @ np.abs(K)
