@@ -4,6 +4,7 @@ marshalling only; without the built library or a GB300 these functions raise."""
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional, Sequence
 
 import torch
@@ -168,14 +169,27 @@ def qk_norm_rope_store(q, k, v, q_weight, k_weight, inv_freq, k_cache, v_cache, 
     return qo, ko
 
 
+def _scale(scale):
+    """The description's scale: 0 for the default. One that fp32 holds as zero or infinite is refused."""
+    if scale is None:
+        return 0.0
+    scale = ctypes.c_float(scale).value
+    if not 0 < scale < math.inf:
+        raise ValueError("scale must be positive and finite in fp32")
+    return scale
+
+
+def _kept(cu_seqlens):
+    """Offsets as a backward keeps them: a copy, whatever becomes of the caller's."""
+    return None if cu_seqlens is None else tuple(cu_seqlens.tolist() if isinstance(cu_seqlens, torch.Tensor) else cu_seqlens)
+
+
 def _attn_inputs(q, k, v, causal, scale, offsets):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be [B,T,H,D]")
     dev, lead, H, Hk, D, st = _heads(q, k, v)
     cu, n = _packed(offsets, lead[0])
-    if scale is not None and not scale > 0:
-        raise ValueError("scale must be positive")
-    return dev, (*lead, H), _attn_desc(lead[0], lead[1], cu, n, H, Hk, D, 1 if causal else 0, 0.0 if scale is None else scale, *st)
+    return dev, (*lead, H), _attn_desc(lead[0], lead[1], cu, n, H, Hk, D, 1 if causal else 0, _scale(scale), *st)
 
 
 def attention_fwd(q, k, v, *, causal=True, scale=None, cu_seqlens: Optional[Sequence[int]] = None, status=None):
@@ -223,10 +237,8 @@ def attention_step(q, k_cache, v_cache, page_table, lengths, *, scale=None, stat
         raise ValueError("the query heads must be a multiple of the key heads")
     qs = _rows_of("q", q, _BF16, (B, H, D), dev, 2, H * D)
     pages, page, width = _cache(k_cache, v_cache, page_table, lengths, B, Hk, D, dev)
-    if scale is not None and not scale > 0:
-        raise ValueError("scale must be positive")
     _status(status, dev)
-    d = _step_desc(B, H, Hk, D, 0.0 if scale is None else scale, pages, page, width, qs)
+    d = _step_desc(B, H, Hk, D, _scale(scale), pages, page, width, qs)
     ws, *space = _workspace("gdn_attn_step_workspace_size", d, q)
     o = _new(q)
     _run("gdn_attn_step", d, _step_args(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), o.data_ptr(), *space, _p(status)), dev)
@@ -239,7 +251,7 @@ class QkNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, inv_freq, positions, cu_seqlens, eps, interleaved):
         ctx.save_for_backward(q, k, q_weight, k_weight, inv_freq, positions)
-        ctx.cfg = dict(cu_seqlens=cu_seqlens, eps=eps, interleaved=interleaved)
+        ctx.cfg = dict(cu_seqlens=_kept(cu_seqlens), eps=eps, interleaved=interleaved)
         ctx.set_materialize_grads(False)
         return qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions=positions, **ctx.cfg)
 
@@ -258,7 +270,7 @@ class Attention(torch.autograd.Function):
     def forward(ctx, q, k, v, causal, scale, cu_seqlens):
         o, lse = attention_fwd(q, k, v, causal=causal, scale=scale, cu_seqlens=cu_seqlens)
         ctx.save_for_backward(q, k, v, o, lse)
-        ctx.cfg = dict(causal=causal, scale=scale, cu_seqlens=cu_seqlens)
+        ctx.cfg = dict(causal=causal, scale=scale, cu_seqlens=_kept(cu_seqlens))
         return o
 
     @staticmethod

@@ -365,86 +365,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t u = 0;
     for (long long rd = 0; ok && get(rd, &ok); ++rd) {
-    const AttnTile& tl = x.tl;
-    int q0 = x.i0 * kAttnTile + half * kCols;
-    for (int it = 0; it < x.n && ok; ++it, ++u) {
-      const uint32_t os = u & 1;
-      const float2 *lse = reinterpret_cast<const float2*>(vec + os * 256 + half * kCols + col), *delta = lse + 64;
-      ok = wait(&ready[os], u >> 1 & 1, kDevTimeoutSync) && wait(s_full, u & 1, kDevTimeoutMma);
-      if (!ok) break;
+      const AttnTile& tl = x.tl;
+      int q0 = x.i0 * kAttnTile + half * kCols;
+      for (int it = 0; it < x.n && ok; ++it, ++u) {
+        const uint32_t os = u & 1;
+        const float2 *lse = reinterpret_cast<const float2*>(vec + os * 256 + half * kCols + col), *delta = lse + 64;
+        ok = wait(&ready[os], u >> 1 & 1, kDevTimeoutSync) && wait(s_full, u & 1, kDevTimeoutMma);
+        if (!ok) break;
+        tc_fence_after();
+        // w[32 h + 4 b + 2 r + y]: row key0 + 16 h + 8 r, column 8 b + col + y
+        float w[64];
+        tmem_ld_16x64(tS + lb, w);
+        tmem_ld_16x64(tS + lb + (16u << 16), w + 32);
+        tmem_wait_ld_regs(w);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const float2 l = lse[4 * b];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float* x = w + (r >> 1) * 32 + 4 * b + (r & 1) * 2;
+            unf2(fma2(f2(x[0], x[1]), c2, f2(l.x, l.y)), &x[0], &x[1]);
+            x[0] = exp2_approx(x[0]);
+            x[1] = exp2_approx(x[1]);
+          }
+        }
+        const int to = tl.len - q0 - col;  // columns (from this thread's first) of queries that exist
+        if (tl.len - q0 < kCols || (p.causal && tl.first + kAttnTile > q0)) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int from = p.causal ? tl.first + key0 + 8 * r - q0 - col : 0;  // and of those that see the row's key
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (8 * b + y < from || 8 * b + y >= to) w[(r >> 1) * 32 + 4 * b + (r & 1) * 2 + y] = 0.f;
+          }
+        }
+        uint32_t out[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) out[e] = pack_bf16(w[2 * e], w[2 * e + 1]);
+        tmem_st_16x32(tS + lb, out);
+        tmem_st_16x32(tS + lb + (16u << 16), out + 16);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_ready);
+        if (!(ok = wait(dp_full, u & 1, kDevTimeoutMma))) break;
+        tc_fence_after();
+        float d[64];
+        tmem_ld_16x64(tP + lb, d);
+        tmem_ld_16x64(tP + lb + (16u << 16), d + 32);
+        tmem_wait_ld_regs(d);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const float2 l = delta[4 * b];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int at = (r >> 1) * 32 + 4 * b + (r & 1) * 2;
+            unf2(mul2(f2(w[at], w[at + 1]), add2(f2(d[at], d[at + 1]), f2(l.x, l.y))), &d[at], &d[at + 1]);
+          }
+        }
+        mbar_arrive(&vec_free[os]);
+        if (q0 + col == 0 && (p.causal || tl.len == 1))  // the sequence's first query sees a single key
+#pragma unroll
+          for (int r = 0; r < 4; ++r) d[(r >> 1) * 32 + (r & 1) * 2] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) out[e] = pack_bf16(d[2 * e], d[2 * e + 1]);
+        tmem_st_16x32(tP + lb, out);
+        tmem_st_16x32(tP + lb + (16u << 16), out + 16);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(ds_ready);
+        q0 += kAttnTile;
+        if (q0 - half * kCols >= tl.len) q0 = x.i0 * kAttnTile + half * kCols;  // the next head of the group
+      }
+      if (!ok || !(ok = wait(done, rd & 1, kDevTimeoutMma))) break;
       tc_fence_after();
-      // w[32 h + 4 b + 2 r + y]: row key0 + 16 h + 8 r, column 8 b + col + y
-      float w[64];
-      tmem_ld_16x64(tS + lb, w);
-      tmem_ld_16x64(tS + lb + (16u << 16), w + 32);
-      tmem_wait_ld_regs(w);
-#pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        const float2 l = lse[4 * b];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float* x = w + (r >> 1) * 32 + 4 * b + (r & 1) * 2;
-          unf2(fma2(f2(x[0], x[1]), c2, f2(l.x, l.y)), &x[0], &x[1]);
-          x[0] = exp2_approx(x[0]);
-          x[1] = exp2_approx(x[1]);
-        }
-      }
-      const int to = tl.len - q0 - col;  // columns (from this thread's first) of queries that exist
-      if (tl.len - q0 < kCols || (p.causal && tl.first + kAttnTile > q0)) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int from = p.causal ? tl.first + key0 + 8 * r - q0 - col : 0;  // and of those that see the row's key
-#pragma unroll
-          for (int b = 0; b < 8; ++b)
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-              if (8 * b + y < from || 8 * b + y >= to) w[(r >> 1) * 32 + 4 * b + (r & 1) * 2 + y] = 0.f;
-        }
-      }
-      uint32_t out[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) out[e] = pack_bf16(w[2 * e], w[2 * e + 1]);
-      tmem_st_16x32(tS + lb, out);
-      tmem_st_16x32(tS + lb + (16u << 16), out + 16);
-      tmem_wait_st();
+      const int key = tl.first + (tid & 127);
+      __nv_bfloat16* dst = (half ? p.dk : p.dv) + ((size_t(tl.row0) + key) * p.Hk + x.hk) * D;
+      const uint32_t acc = (half ? tK : tV) + lane0;
+      store_row<D>(dst, acc, half ? p.scale : 1.f, key < tl.len, wide);
       tc_fence_before();
-      mbar_arrive(p_ready);
-      if (!(ok = wait(dp_full, u & 1, kDevTimeoutMma))) break;
-      tc_fence_after();
-      float d[64];
-      tmem_ld_16x64(tP + lb, d);
-      tmem_ld_16x64(tP + lb + (16u << 16), d + 32);
-      tmem_wait_ld_regs(d);
-#pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        const float2 l = delta[4 * b];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int at = (r >> 1) * 32 + 4 * b + (r & 1) * 2;
-          unf2(mul2(f2(w[at], w[at + 1]), add2(f2(d[at], d[at + 1]), f2(l.x, l.y))), &d[at], &d[at + 1]);
-        }
-      }
-      mbar_arrive(&vec_free[os]);
-      if (q0 + col == 0 && (p.causal || tl.len == 1))  // the sequence's first query sees a single key
-#pragma unroll
-        for (int r = 0; r < 4; ++r) d[(r >> 1) * 32 + (r & 1) * 2] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 32; ++e) out[e] = pack_bf16(d[2 * e], d[2 * e + 1]);
-      tmem_st_16x32(tP + lb, out);
-      tmem_st_16x32(tP + lb + (16u << 16), out + 16);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(ds_ready);
-      q0 += kAttnTile;
-      if (q0 - half * kCols >= tl.len) q0 = x.i0 * kAttnTile + half * kCols;  // the next head of the group
-    }
-    if (!ok || !(ok = wait(done, rd & 1, kDevTimeoutMma))) break;
-    tc_fence_after();
-    const int key = tl.first + (tid & 127);
-    __nv_bfloat16* dst = (half ? p.dk : p.dv) + ((size_t(tl.row0) + key) * p.Hk + x.hk) * D;
-    const uint32_t acc = (half ? tK : tV) + lane0;
-    store_row<D>(dst, acc, half ? p.scale : 1.f, key < tl.len, wide);
-    tc_fence_before();
     }
   }
   tc_fence_before();

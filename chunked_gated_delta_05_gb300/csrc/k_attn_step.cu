@@ -125,185 +125,185 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_step(const AttnStepParams 
     }
     const int len = p.lengths[b], take = int(min(end - u, (long long)(n_units - k_unit)));
     const int from = k_unit * kUnit, to = min(len, from + take * kUnit);
-  // queries as the products' columns: of head g (and g + 8), channels 16 j + 2 c, + 1 and + 8, + 9
-  uint32_t q[kRows][D / 16][2];
+    // queries as the products' columns: of head g (and g + 8), channels 16 j + 2 c, + 1 and + 8, + 9
+    uint32_t q[kRows][D / 16][2];
 #pragma unroll
-  for (int r = 0; r < kRows; ++r)
+    for (int r = 0; r < kRows; ++r)
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j)
+      for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
-        q[r][j][y] = g + 8 * r < heads ? *reinterpret_cast<const uint32_t*>(p.q + b * p.q_stride + (head0 + g + 8 * r) * D + 16 * j + 2 * c + 8 * y) : 0u;
-  // reference and partial sum of weights of heads 2 c + y (+ 8 r); sums over values: o[r][j] channels 16 j + g, + 8 of those heads
-  float m[kRows][2], l[kRows][2], o[kRows][D / 16][4];
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-#pragma unroll
-    for (int y = 0; y < 2; ++y) m[r][y] = -INFINITY, l[r][y] = 0.f;
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[r][j][x] = 0.f;
-  }
-
-  // Row of the cache (pages one after the other) of key k, -1 past the piece's end, and for a page that does not exist.
-  const int* table = p.table + (long long)b * p.width;
-  auto cache_row = [&](int k) -> long long {
-    if (k >= to) return -1;
-    const int page = table[k / p.page];
-    if (page < 0 || page >= p.pages) {
-      if (p.status) atomicCAS(p.status, 0, kDevGateRange);
-      return -1;
-    }
-    return (long long)page * p.page + k % p.page;
-  };
-  const long long token = (long long)p.Hk * D;
-  const __nv_bfloat16 *kc = p.kc + hk * D, *vc = p.vc + hk * D;
-  uint8_t* mem = smem + warp * (kStages * St::kBytes);
-  // Requests the rows of 16 keys into stage st: lanes 0 .. 15 hold the keys' cache rows and copy K, the others copy V.
-  auto request = [&](int st, long long mine) {
-    uint8_t* dst = mem + st * St::kBytes + lane * St::kPitch;
-    if (mine >= 0) {
-      mbar_expect_tx(&full[warp][st], St::kRow);
-      bulk_load(dst, (lane < 16 ? kc : vc) + mine * token, St::kRow, &full[warp][st]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < St::kRow / 16; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
-      fence_async_smem();  // before a copy to the same place
-      mbar_arrive(&full[warp][st]);
-    }
-  };
-  constexpr int kStride = kWarps * kKeys;
-  const int first = from + warp * kKeys;
-  uint32_t valid[kStages] = {};  // of the stages ahead, the keys that are there
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    const long long row = cache_row(first + i * kStride + (lane & 15));
-    valid[i] = __ballot_sync(0xffffffffu, row >= 0);
-    request((stage + i) % kStages, row);
-  }
-  long long mine = cache_row(first + (kStages - 1) * kStride + (lane & 15));
-  for (int k0 = first; k0 < to; k0 += kStride) {
-    valid[kStages - 1] = __ballot_sync(0xffffffffu, mine >= 0);
-    __syncwarp();  // every lane has read the stage before this one
-    request(stage == 0 ? kStages - 1 : stage - 1, mine);
-    mine = cache_row(k0 + kStages * kStride + (lane & 15));
-    ok = __all_sync(0xffffffffu, attn_wait(&full[warp][stage], phases >> stage & 1u, &abort_flag, p.status, kDevTimeoutTma));
-    if (!ok) break;
-    phases ^= 1u << stage;
-    const uint32_t at = smem_u32(mem + stage * St::kBytes);
-    float sc[kRows][4] = {};
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-      uint32_t a[4];
-      ldmatrix4<false>(a, at + (lane & 15) * St::kPitch + (2 * j + (lane >> 4)) * 16);
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) mma16816(sc[r], a, q[r][j][0], q[r][j][1]);
-    }
-    const bool there[2] = {bool(valid[0] >> g & 1u), bool(valid[0] >> (g + 8) & 1u)};
-    uint32_t w[kRows][2];
+        for (int y = 0; y < 2; ++y)
+          q[r][j][y] = g + 8 * r < heads ? *reinterpret_cast<const uint32_t*>(p.q + b * p.q_stride + (head0 + g + 8 * r) * D + 16 * j + 2 * c + 8 * y) : 0u;
+    // reference and partial sum of weights of heads 2 c + y (+ 8 r); sums over values: o[r][j] channels 16 j + g, + 8 of those heads
+    float m[kRows][2], l[kRows][2], o[kRows][D / 16][4];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      bool high = false;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (!there[x >> 1]) sc[r][x] = -INFINITY;
-        high |= sc[r][x] > m[r][x & 1] + far;
+      for (int y = 0; y < 2; ++y) m[r][y] = -INFINITY, l[r][y] = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[r][j][x] = 0.f;
+    }
+
+    // Row of the cache (pages one after the other) of key k, -1 past the piece's end, and for a page that does not exist.
+    const int* table = p.table + (long long)b * p.width;
+    auto cache_row = [&](int k) -> long long {
+      if (k >= to) return -1;
+      const int page = table[k / p.page];
+      if (page < 0 || page >= p.pages) {
+        if (p.status) atomicCAS(p.status, 0, kDevGateRange);
+        return -1;
       }
-      if (__any_sync(0xffffffffu, high)) {  // the first keys too: their reference is -inf
+      return (long long)page * p.page + k % p.page;
+    };
+    const long long token = (long long)p.Hk * D;
+    const __nv_bfloat16 *kc = p.kc + hk * D, *vc = p.vc + hk * D;
+    uint8_t* mem = smem + warp * (kStages * St::kBytes);
+    // Requests the rows of 16 keys into stage st: lanes 0 .. 15 hold the keys' cache rows and copy K, the others copy V.
+    auto request = [&](int st, long long mine) {
+      uint8_t* dst = mem + st * St::kBytes + lane * St::kPitch;
+      if (mine >= 0) {
+        mbar_expect_tx(&full[warp][st], St::kRow);
+        bulk_load(dst, (lane < 16 ? kc : vc) + mine * token, St::kRow, &full[warp][st]);
+      } else {
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float top = fmaxf(sc[r][y], sc[r][2 + y]);
+        for (int i = 0; i < St::kRow / 16; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+        fence_async_smem();  // before a copy to the same place
+        mbar_arrive(&full[warp][st]);
+      }
+    };
+    constexpr int kStride = kWarps * kKeys;
+    const int first = from + warp * kKeys;
+    uint32_t valid[kStages] = {};  // of the stages ahead, the keys that are there
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          const float next = fmaxf(m[r][y], top), f = next == m[r][y] ? 1.f : exp2_approx((m[r][y] - next) * cs);
-          m[r][y] = next;
-          l[r][y] *= f;
+    for (int i = 0; i < kStages - 1; ++i) {
+      const long long row = cache_row(first + i * kStride + (lane & 15));
+      valid[i] = __ballot_sync(0xffffffffu, row >= 0);
+      request((stage + i) % kStages, row);
+    }
+    long long mine = cache_row(first + (kStages - 1) * kStride + (lane & 15));
+    for (int k0 = first; k0 < to; k0 += kStride) {
+      valid[kStages - 1] = __ballot_sync(0xffffffffu, mine >= 0);
+      __syncwarp();  // every lane has read the stage before this one
+      request(stage == 0 ? kStages - 1 : stage - 1, mine);
+      mine = cache_row(k0 + kStages * kStride + (lane & 15));
+      ok = __all_sync(0xffffffffu, attn_wait(&full[warp][stage], phases >> stage & 1u, &abort_flag, p.status, kDevTimeoutTma));
+      if (!ok) break;
+      phases ^= 1u << stage;
+      const uint32_t at = smem_u32(mem + stage * St::kBytes);
+      float sc[kRows][4] = {};
 #pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            o[r][j][y] *= f;
-            o[r][j][2 + y] *= f;
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t a[4];
+        ldmatrix4<false>(a, at + (lane & 15) * St::kPitch + (2 * j + (lane >> 4)) * 16);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) mma16816(sc[r], a, q[r][j][0], q[r][j][1]);
+      }
+      const bool there[2] = {bool(valid[0] >> g & 1u), bool(valid[0] >> (g + 8) & 1u)};
+      uint32_t w[kRows][2];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        bool high = false;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (!there[x >> 1]) sc[r][x] = -INFINITY;
+          high |= sc[r][x] > m[r][x & 1] + far;
+        }
+        if (__any_sync(0xffffffffu, high)) {  // the first keys too: their reference is -inf
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float top = fmaxf(sc[r][y], sc[r][2 + y]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float next = fmaxf(m[r][y], top), f = next == m[r][y] ? 1.f : exp2_approx((m[r][y] - next) * cs);
+            m[r][y] = next;
+            l[r][y] *= f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              o[r][j][y] *= f;
+              o[r][j][2 + y] *= f;
+            }
           }
         }
-      }
-      float x[4];
+        float x[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float ref = m[r][e & 1] == -INFINITY ? 0.f : m[r][e & 1];
-        x[e] = there[e >> 1] ? exp2_approx((sc[r][e] - ref) * cs) : 0.f;
-        l[r][e & 1] += x[e];
-      }
-      w[r][0] = transpose8(pack_bf16(x[0], x[1]));
-      w[r][1] = transpose8(pack_bf16(x[2], x[3]));
-    }
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-      uint32_t a[4];
-      ldmatrix4<true>(a, at + (kKeys + ((lane >> 4) << 3) + (lane & 7)) * St::kPitch + (2 * j + ((lane >> 3) & 1)) * 16);
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) mma16816(o[r][j], a, w[r][0], w[r][1]);
-    }
-#pragma unroll
-    for (int i = 0; i + 1 < kStages; ++i) valid[i] = valid[i + 1];
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-  }
-
-  // Rows before this one and shares before this one together number the pieces of a part's rows.
-  const bool whole = k_unit == 0 && take == n_units;
-  const long long slot = (long long)(b + which) * parts + part;
-  // the block's warps joined, their sums where the stages were
-  for (int i = 0; i < (ok ? kStages - 1 : kStages); ++i) {  // the stages ahead, which hold no key of the row (after an error: what is in flight)
-    const int st = stage + i >= kStages ? stage + i - kStages : stage + i;
-    mbar_drain(&full[warp][st], phases >> st & 1u);
-    phases ^= 1u << st;
-  }
-  __syncthreads();
-  if (abort_flag) return;
-#pragma unroll
-  for (int r = 0; r < kRows; ++r)
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) l[r][y] += __shfl_xor_sync(0xffffffffu, l[r][y], d);
-      const int head = 8 * r + 2 * c + y;
-      if (g == 0) {
-        ml_s[warp][head][0] = m[r][y];
-        ml_s[warp][head][1] = l[r][y];
+        for (int e = 0; e < 4; ++e) {
+          const float ref = m[r][e & 1] == -INFINITY ? 0.f : m[r][e & 1];
+          x[e] = there[e >> 1] ? exp2_approx((sc[r][e] - ref) * cs) : 0.f;
+          l[r][e & 1] += x[e];
+        }
+        w[r][0] = transpose8(pack_bf16(x[0], x[1]));
+        w[r][1] = transpose8(pack_bf16(x[2], x[3]));
       }
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
-        acc_s[warp][head][16 * j + g] = o[r][j][y];
-        acc_s[warp][head][16 * j + g + 8] = o[r][j][2 + y];
+        uint32_t a[4];
+        ldmatrix4<true>(a, at + (kKeys + ((lane >> 4) << 3) + (lane & 7)) * St::kPitch + (2 * j + ((lane >> 3) & 1)) * 16);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) mma16816(o[r][j], a, w[r][0], w[r][1]);
+      }
+#pragma unroll
+      for (int i = 0; i + 1 < kStages; ++i) valid[i] = valid[i + 1];
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+
+    // Rows before this one and shares before this one together number the pieces of a part's rows.
+    const bool whole = k_unit == 0 && take == n_units;
+    const long long slot = (long long)(b + which) * parts + part;
+    // the block's warps joined, their sums where the stages were
+    for (int i = 0; i < (ok ? kStages - 1 : kStages); ++i) {  // the stages ahead, which hold no key of the row (after an error: what is in flight)
+      const int st = stage + i >= kStages ? stage + i - kStages : stage + i;
+      mbar_drain(&full[warp][st], phases >> st & 1u);
+      phases ^= 1u << st;
+    }
+    __syncthreads();
+    if (abort_flag) return;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[r][y] += __shfl_xor_sync(0xffffffffu, l[r][y], d);
+        const int head = 8 * r + 2 * c + y;
+        if (g == 0) {
+          ml_s[warp][head][0] = m[r][y];
+          ml_s[warp][head][1] = l[r][y];
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          acc_s[warp][head][16 * j + g] = o[r][j][y];
+          acc_s[warp][head][16 * j + g + 8] = o[r][j][2 + y];
+        }
+      }
+    __syncthreads();
+    for (int x = threadIdx.x; x < heads * D; x += kWarps * 32) {
+      const int r = x / D, d = x % D;
+      float top = -INFINITY;
+#pragma unroll
+      for (int y = 0; y < kWarps; ++y) top = fmaxf(top, ml_s[y][r][0]);
+      float sum = 0.f, total = 0.f;  // of the warps
+#pragma unroll
+      for (int y = 0; y < kWarps; ++y) {
+        const float mw = ml_s[y][r][0], f = mw == top ? 1.f : exp2_approx((mw - top) * cs);
+        sum = fmaf(acc_s[y][r][d], f, sum);
+        total = fmaf(ml_s[y][r][1], f, total);
+      }
+      const long long at = (long long)b * p.H + head0 + r;
+      if (whole) {
+        p.o[at * D + d] = __float2bfloat16(total == 0.f ? 0.f : sum / total);
+      } else {
+        const long long i = (slot * 8 * kRows + r);
+        p.part[i * D + d] = sum;
+        if (d == 0) p.ml[i] = make_float2(top, total);
       }
     }
-  __syncthreads();
-  for (int x = threadIdx.x; x < heads * D; x += kWarps * 32) {
-    const int r = x / D, d = x % D;
-    float top = -INFINITY;
-#pragma unroll
-    for (int y = 0; y < kWarps; ++y) top = fmaxf(top, ml_s[y][r][0]);
-    float sum = 0.f, total = 0.f;  // of the warps
-#pragma unroll
-    for (int y = 0; y < kWarps; ++y) {
-      const float mw = ml_s[y][r][0], f = mw == top ? 1.f : exp2_approx((mw - top) * cs);
-      sum = fmaf(acc_s[y][r][d], f, sum);
-      total = fmaf(ml_s[y][r][1], f, total);
-    }
-    const long long at = (long long)b * p.H + head0 + r;
-    if (whole) {
-      p.o[at * D + d] = __float2bfloat16(total == 0.f ? 0.f : sum / total);
-    } else {
-      const long long i = (slot * 8 * kRows + r);
-      p.part[i * D + d] = sum;
-      if (d == 0) p.ml[i] = make_float2(top, total);
-    }
-  }
-  if (threadIdx.x == 0 && k_unit == 0) p.span[(long long)b * parts + part] = make_int2(which, int((u + n_units - 1) / share));
-  __syncthreads();  // the sums are read before the stages are written again
-  fence_async_smem();
-  u += take;
-  k_unit = 0;
-  ++b;
+    if (threadIdx.x == 0 && k_unit == 0) p.span[(long long)b * parts + part] = make_int2(which, int((u + n_units - 1) / share));
+    __syncthreads();  // the sums are read before the stages are written again
+    fence_async_smem();
+    u += take;
+    k_unit = 0;
+    ++b;
   }
 }
 

@@ -278,7 +278,6 @@ __global__ void __launch_bounds__(kWarps * 32, kFwdBlocks) k_rope_fwd(const __gr
 
 template <int D, bool kPairs>
 __global__ void __launch_bounds__(kWarps * 32, kBwdPerSm) k_rope_bwd(const __grid_constant__ RopeParams p) {
-  wait_for_previous();
   constexpr int kHeads = 256 / D, kTogether = 4;
   __shared__ float part[kWarps][2][D];
   wait_for_previous();

@@ -206,6 +206,61 @@ def test_captured_training_step():
             assert torch.equal(x, y)
 
 
+def test_captured_step_of_many_documents():
+    """Tables too long for the launches' parameters are captured with the call, and copied again by every replay."""
+    g = torch.Generator().manual_seed(10)
+    cu = list(range(0, 1201, 3))
+    q, k, v, dO = (rn(g, 1, 1200, h, 64) for h in (4, 2, 2, 4))
+    w, f = 1 + rn(g, 64, dtype=F32, std=0.1), freqs(64)
+
+    def step(cu):
+        a, b = lib().qk_norm_rope_fwd(q, k, w, w, f, cu_seqlens=cu)
+        o, lse = lib().attention_fwd(a, b, v, cu_seqlens=cu)
+        return (a, b, o, *lib().attention_bwd(dO, a, b, v, o, lse, cu_seqlens=cu))
+
+    want = step(cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(cu)
+    step(list(range(0, 1201, 4)))       # other tables in between
+    for _ in range(2):
+        for x in out:
+            x.zero_()
+        graph.replay()
+        for x, y in zip(out, want):
+            assert torch.equal(x, y)
+
+
+def test_offsets_changed_after_the_forward():
+    g = torch.Generator().manual_seed(11)
+    dO, w, f = rn(g, 1, 90, 4, 64), 1 + rn(g, 64, dtype=F32, std=0.1), freqs(64)
+
+    def grads(change):
+        h = torch.Generator().manual_seed(12)
+        leaves = [rn(h, 1, 90, n, 64).requires_grad_() for n in (4, 2, 2)]
+        cu = torch.tensor([0, 30, 90], dtype=torch.int32)
+        a, b = lib().qk_norm_rope(*leaves[:2], w, w, f, cu_seqlens=cu)
+        o = lib().attention(a, b, leaves[2], cu_seqlens=cu)
+        if change:
+            cu[1] = 60
+        return torch.autograd.grad(o, leaves, dO)
+
+    for x, y in zip(grads(False), grads(True)):
+        assert torch.equal(x, y)
+
+
+def test_rows_may_share_pages():
+    """Rows with a common beginning name the same pages, and a row may name one twice."""
+    g = torch.Generator().manual_seed(13)
+    kc, vc, q = rn(g, 6, 16, 2, 64), rn(g, 6, 16, 2, 64), rn(g, 3, 4, 64)
+    table = torch.tensor([[0, 1, 2], [0, 1, 3], [4, 4, 0]], dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([48, 40, 37], dtype=torch.int32, device="cuda")
+    apart = torch.arange(9, dtype=torch.int32, device="cuda").view(3, 3)
+    copies = [c[table.long().flatten()].contiguous() for c in (kc, vc)]
+    assert torch.equal(lib().attention_step(q, kc, vc, table, lengths), lib().attention_step(q, *copies, apart, lengths))
+
+
 def test_two_streams_at_once():
     g = torch.Generator().manual_seed(9)
     sets = [[rn(g, 1, 700 + 100 * i, 8, 128) for _ in range(4)] for i in range(2)]
@@ -256,7 +311,7 @@ def test_a_cache_that_changed_is_noticed():
         y.backward()
 
 
-@pytest.mark.parametrize("what", ["dtype", "heads", "expanded", "rows", "head gap", "misaligned", "scale", "table", "lengths", "cache", "positions", "rotary"])
+@pytest.mark.parametrize("what", ["dtype", "heads", "expanded", "rows", "head gap", "misaligned", "scale", "tiny scale", "huge scale", "table", "lengths", "cache", "positions", "rotary"])
 def test_refused(what):
     m = lib()
     q, k, kc = (torch.zeros(*s, dtype=BF16, device="cuda") for s in ((2, 8, 4, 64), (2, 8, 2, 64), (4, 16, 2, 64)))
@@ -269,6 +324,8 @@ def test_refused(what):
         "head gap": lambda: m.attention_fwd(torch.zeros(2, 8, 4, 128, dtype=BF16, device="cuda")[..., :64], k, k),
         "misaligned": lambda: m.attention_fwd(torch.zeros(2 * 8 * 4 * 64 + 4, dtype=BF16, device="cuda")[4:].view(2, 8, 4, 64), k, k),
         "scale": lambda: m.attention_fwd(q, k, k, scale=-1.0),
+        "tiny scale": lambda: m.attention_fwd(q, k, k, scale=1e-60),
+        "huge scale": lambda: m.attention_fwd(q, k, k, scale=1e60),
         "table": lambda: m.attention_step(q[:, 0], kc, kc, table.long(), n),
         "lengths": lambda: m.attention_step(q[:, 0], kc, kc, table, n[:1]),
         "cache": lambda: m.qk_norm_rope_store(q[:, 0], k[:, 0], k[:, 0], w, w, f, kc, kc, table, n),
