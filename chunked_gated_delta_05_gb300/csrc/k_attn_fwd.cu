@@ -6,22 +6,26 @@
 // weighted sum of v are kept, and o = sum / l at the end.
 //
 // A CTA takes 256 queries of one head at a time, as two tiles of 128, and goes through such items in turn. A tile's row of scores
-// belongs to one thread (TMEM lane = row), so the softmax needs no shuffles. The two tiles alternate on the tensor core: while
-// one tile's 128 threads turn scores into weights, the other's products run.
+// belongs to two threads, one for either half of its keys (TMEM lane = row), so the softmax needs no shuffles. The two tiles
+// alternate on the tensor core: while one tile's 256 threads turn scores into weights, the other's products run.
 //   S_t = Q_t K_j^T        128 x 128 x D, operands in shared memory (128-byte swizzle, by TMA)
 //   O_t += P_t V_j         128 x D x 128, P_t bf16 in TMEM over S_t's columns (the A operand), V_j read MN-major
 // TMEM: S_0, S_1, O_0, O_1. Keys and values come through one ring of stages. Weights are rounded to bf16 (2^-8 relative at most, the
 // type of v and o); scores, sums and the accumulators are fp32.
 //
-// What bounds it: the tensor core, and the time its issuing thread spends on anything else. An instruction is taken only when the
-// one before it is nearly done, and every wait, even for a phase long past, costs about 130 cycles in which the core soon
-// idles (measured; a tile's two products take 1024). So the issuing thread waits once per tile and iteration, on a barrier on which both the
-// tile's 128 softmax threads and a gate thread arrive, the latter when the K and V tiles needed next have landed.
+// What bounds it: with heads of 128 the tensor core. A tile's two products take 1312 cycles (its 128 x 128 x 16 steps 64, or 100 where both
+// operands come from shared memory), so two tiles 2624 of the 2870 that an iteration takes: 16 heads x 8192 causal
+// queries in 183 us, 1500 TFLOP/s. With heads of 64 it is the chain of a tile, softmax (1400 cycles), products and the signals between
+// them (1200): 8 x 1001 queries x 16 heads, every key, 54 us. One thread a row, with 8 softmax warps for 16, took 188 and 57 us: a warp
+// alone on its scheduler has 1060 cycles for a row's 128 weights, two with 64 each have 800.
+// An instruction is taken only when the one before it is nearly done, and every wait, even for a phase long past, costs some 75 cycles
+// in which the core may idle. So the issuing thread waits once per tile and iteration, on a barrier on which both the tile's
+// 256 softmax threads and a gate thread arrive, the latter when the K and V tiles needed next have landed.
 //
-// The reference m is the row's maximum in its first tile and moves only when a later tile's weights sum to more than 2^16 (then l and
-// the accumulator are rescaled and the tile's weights taken again): weights up to that cost no precision in bf16 or fp32, almost no
-// tile needs it, and no maximum is taken in the others (64 instructions of 380 a row, and nearly a third of the time). It
-// needs no wait: the commit that announces S_t(j) also covers the product O_t(j - 1) issued before it.
+// The reference m is the row's maximum in its first tile and moves only when half of a later tile has weights that sum to more than
+// 2^16 (then l and the accumulator are rescaled and the tile's weights taken again): weights up to that cost no precision in bf16 or
+// fp32, almost no tile needs it, and no maximum is taken in the others. The two warps of a row agree on it at a barrier of their own,
+// in every tile. It needs no wait: the commit that announces S_t(j) also covers the product O_t(j - 1) issued before it.
 //
 // Keys past the sequence's end are masked in the scores, and the last tile's values past it are zeroed in shared memory: they
 // belong to the next sequence, and 0 x NaN would carry a neighbour's NaN over.
@@ -30,18 +34,29 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 384;  // 8 softmax warps, the MMA warp, the TMA warp and a gate warp for either tile
-// The launch's 168 registers a thread (12 warps x 168 x 32 = 64512) are shared out anew: 208 for the softmax's rows of 128 scores,
-// 88 for the rest (8 x 208 + 4 x 88 = 12 x 168).
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-constexpr float kHigh = 65536.f;  // sum of a tile's weights that moves the reference
+constexpr int kThreads = 640;                      // 16 softmax warps, the MMA warp, the TMA warp and a gate warp for either tile
+constexpr int kMma = 16, kTma = 17, kGate = 18;
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 16 x 104 + 4 x 64 = 20 x 96, the launch's
+constexpr int kCols = 64;                          // columns of a tile to a softmax warp
+constexpr float kHigh = 65536.f;  // sum of half a tile's weights that moves the reference
 
 template <int D>
 struct Cfg {
   static constexpr int kTileBytes = kAttnTile * D * 2;
   static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes;
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + 512 + 2048;  // tiles, barriers, sums of the rows' halves
 };
+
+// Whether any of the two warps that share a tile's 32 rows says so. Both take part in every one, whatever befell either.
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(uint32_t(x))
+      : "memory");
+  return r != 0;
+}
 
 // The CTA's item of a round, most work first: every other round the other way round, so that the CTAs' sums of work come out
 // alike. False where the last round has none for it.
@@ -74,23 +89,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_attn_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnParams p) {
   using C = Cfg<D>;
   constexpr int kS = C::kStages, kTile = C::kTileBytes;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* sKV = sm + 2 * kTile;
-  __shared__ uint64_t q_full[2], q_empty[2], kv_full[kS], kv_empty[kS], zeroed[kS], s_full[2], p_full[2], o_full[2], drained;
-  __shared__ uint32_t tslot;
-  __shared__ int abort_flag;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sKV + kS * kTile);
+  uint64_t *q_full = bar, *q_empty = bar + 2, *s_full = bar + 4, *p_full = bar + 6, *o_full = bar + 8, *kv_full = bar + 10, *kv_empty = kv_full + kS, *zeroed = kv_empty + kS,
+           *drained = zeroed + kS;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(drained + 2);
+  float* halves = reinterpret_cast<float*>(bar + 64);  // [2][2][128], by tile, half and row: the half's sum of weights
+  static_assert(10 + 3 * kS + 3 <= 64, "barriers");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long total = (long long)p.tiles * p.H, rounds = (total + gridDim.x - 1) / gridDim.x;
-  if (warp == 8) tmem_alloc(&tslot, 512);
+  if (warp == kMma) tmem_alloc(tslot, 512);
   if (tid == 0) {
-    abort_flag = 0;
+    *abort_flag = 0;
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
       mbar_init(&q_empty[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], kAttnTile + 1);
+      mbar_init(&p_full[t], 2 * kAttnTile + 1);
       mbar_init(&o_full[t], 1);
     }
     for (int i = 0; i < kS; ++i) {
@@ -98,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&kv_empty[i], 1);
       mbar_init(&zeroed[i], 32);
     }
-    mbar_init(&drained, 1);
+    mbar_init(drained, 1);
     fence_mbar_init();
   }
   tc_fence_before();
@@ -108,12 +126,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // All of TMEM, so it starts at column 0: S_t at 128 t, O_t at 256 + D t.
   auto tS = [&](int t) { return uint32_t(t) * 128; };
   auto tO = [&](int t) { return 256 + uint32_t(t) * D; };
-  auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, &abort_flag, p.status, code); };
+  auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
   Item it;
 
-  if (warp >= 8) {
+  if (warp >= kMma) {
     regs_dec<kOtherRegs>();
-    if (warp == 9) {
+    if (warp == kTma) {
       // ---------------- producer: Q, then K and V tile by tile through the ring ----------------
       Ring<kS, 1> r(0);
       int use = 0;                   // tiles requested through the ring
@@ -155,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t)
           if (q_use[t]) mbar_drain(&q_full[t], (q_use[t] - 1) & 1);
       }
-    } else if (warp == 8) {
+    } else if (warp == kMma) {
       // ---------------- MMA issuer ----------------
       const uint32_t lead = elect_lead();
       const uint32_t q = desc_low_k(smem_u32(sm)), kk = desc_low_k(smem_u32(sKV)), vv = desc_low_mn(smem_u32(sKV), kAttnPanel);
@@ -172,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t v = vv + rv.at * (kTile >> 4), d = 256 + uint32_t(t) * D;
         if (!all_wait(&p_full[t], cnt[t]++ & 1, kDevTimeoutSync)) return false;
         tc_fence_after();
-        product_ts<D, 64>(lead, d, uint32_t(t) * 128, v, j > 0);
+        product_ts<D, kCols / 2>(lead, d, uint32_t(t) * 128, v, j > 0);
         return true;
       };
       // A tile's first scores of an item overwrite the weights of the item before it, which the products issued so far have read; its
@@ -214,12 +232,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         it = next;
       }
       if (!ok) {  // the products in flight end before their accumulators are given up
-        commit(lead, &drained);
-        mbar_drain(&drained, 0);
+        commit(lead, drained);
+        mbar_drain(drained, 0);
       }
-    } else if (warp >= 10 && lane == 0) {
+    } else if (warp >= kGate && lane == 0) {
       // ---------------- gate of a tile: the tiles that the products behind its weights read have landed ----------------
-      const int t = warp - 10;
+      const int t = warp - kGate;
       Ring<kS, 2> rk(0), rv(1);
       uint32_t cnt = 0, outs = 0, zeros = 0;  // iterations and items so far; a bit per stage, the phase of its next zeroing
       bool ok = true;
@@ -252,14 +270,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---------------- softmax: one query row a thread ----------------
+    // ---------------- softmax: a query row and half of its keys a thread ----------------
     regs_inc<kSoftmaxRegs>();
-    const int t = warp >> 2, row = tid & 127;
-    const uint32_t lb = tmem_lane_base(warp);
+    const int t = warp >> 3, half = warp >> 2 & 1, row = tid & 127, pair = 1 + t * 4 + (warp & 3);
+    const uint32_t lb = tmem_lane_base(warp), lS = tS(t) + lb + uint32_t(half) * kCols, lO = tO(t) + lb + uint32_t(half) * (D / 2);
+    float *own = halves + (2 * t + half) * kAttnTile + row, *his = halves + (2 * t + (half ^ 1)) * kAttnTile + row;
     const float c = p.scale * kLog2e;
     const F2 c2 = dup2(c);
+    const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
     uint32_t cnt = 0, outs = 0;
     bool ok = true;
+    auto warp_wait = [&](uint64_t* b, uint32_t ph) { return bool(__all_sync(0xffffffffu, wait(b, ph, kDevTimeoutMma))); };
     for (long long rd = 0; rd < rounds && ok; ++rd) {
       if (!item_of(p, rd, total, &it)) break;
       const int mine = it.n[t], len = it.tl.len, qi = it.tl.first + t * kAttnTile + row;  // in the sequence
@@ -267,48 +288,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY;
       F2 l2 = dup2(0.f);
       for (int j = 0; j < mine; ++j) {
-        if (!(ok = wait(&s_full[t], cnt++ & 1, kDevTimeoutMma))) break;
+        ok = warp_wait(&s_full[t], cnt++ & 1);
         tc_fence_after();
-        float w[64];
+        const bool cut = j + 1 == mine && (p.causal || it.tail);
+        const int seen = (p.causal ? min(qi + 1, len) : len) - j * kAttnTile - half * kCols;
+        float w[kCols / 2];
         bool fresh = j == 0;  // the reference is taken from this tile
 #pragma unroll 1
         while (true) {
-          float s[128];
-          tmem_ld64(tS(t) + lb, s);
-          tmem_ld64(tS(t) + lb + 64, s + 64);
-          tmem_wait_ld_regs(s);
-          if (j + 1 == mine && (p.causal || it.tail)) {
-            const int seen = (p.causal ? min(qi + 1, len) : len) - j * kAttnTile;
-#pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (e >= seen) s[e] = -INFINITY;
-          }
           if (fresh) {
-            float mx[4] = {s[0], s[1], s[2], s[3]};
+            // the maximum over both halves, before either is overwritten with its weights
+            float next = m;
+#pragma unroll 1
+            for (int y = 0; y < 2; ++y) {
+              float s[kCols];
+              tmem_ld64(tS(t) + lb + y * kCols, s);
+              tmem_wait_ld_regs(s);
+              if (cut)
 #pragma unroll
-            for (int e = 4; e < 124; e += 8)
+                for (int e = 0; e < kCols; ++e)
+                  if (e + (y - half) * kCols >= seen) s[e] = -INFINITY;
+              float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-              for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[e + u], s[e + 4 + u]);
-            const float top = max3(max3(mx[0], mx[1], s[124]), max3(mx[2], mx[3], s[125]), fmaxf(s[126], s[127]));
-            const float next = fmaxf(m, top), f = next == m ? 1.f : exp2_approx((m - next) * c);
+              for (int e = 4; e < 60; e += 8)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[e + u], s[e + 4 + u]);
+              next = max3(next, max3(mx[0], mx[1], s[60]), max3(mx[2], mx[3], fmaxf(s[61], fmaxf(s[62], s[63]))));
+            }
+            if (pair_any(pair, !ok)) {
+              ok = false;
+              break;
+            }
+            const float f = next == m ? 1.f : exp2_approx((m - next) * c);
             m = next;
             l2 = mul2(l2, dup2(f));
             if (j > 0) {
 #pragma unroll
-              for (int q = 0; q < D / 32; ++q) {
+              for (int q = 0; q < D / 64; ++q) {
                 float o[32];
-                tmem_ld32(tO(t) + lb + q * 32, o);
+                tmem_ld32(lO + q * 32, o);
                 tmem_wait_ld_regs(o);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] *= f;
-                tmem_st32(tO(t) + lb + q * 32, o);
+                tmem_st32(lO + q * 32, o);
               }
             }
           }
           const F2 mc = dup2(-m * c);
           F2 sum[2] = {dup2(0.f), dup2(0.f)};
+          float s[kCols];
+          tmem_ld64(lS, s);
+          tmem_wait_ld_regs(s);
+          if (cut)
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {
+            for (int e = 0; e < kCols; ++e)
+              if (e >= seen) s[e] = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kCols / 2; ++e) {
             float a, b;
             unf2(fma2(f2(s[2 * e], s[2 * e + 1]), c2, mc), &a, &b);
             a = exp2_approx(a);
@@ -317,37 +353,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[e] = __uint_as_float(pack_bf16(a, b));
           }
           sum[0] = add2(sum[0], sum[1]);
-          if (fresh || !__any_sync(0xffffffffu, sum2(sum[0]) > kHigh)) {
+          if (fresh || !pair_any(pair, !ok || sum2(sum[0]) > kHigh)) {
             l2 = add2(l2, sum[0]);
+            break;
+          }
+          if (pair_any(pair, !ok)) {
+            ok = false;
             break;
           }
           fresh = true;
         }
-        tmem_st32(tS(t) + lb, w);
-        tmem_st32(tS(t) + lb + 32, w + 32);
+        if (!ok) break;
+        tmem_st32(lS, w);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[t]);
       }
-      if (!ok || !(ok = wait(&o_full[t], outs++ & 1, kDevTimeoutMma))) break;
+      if (!ok) break;
+      *own = sum2(l2);  // the other thread has read the last item's before this item's first barrier
+      ok = warp_wait(&o_full[t], outs++ & 1);
+      if (pair_any(pair, !ok)) break;
       tc_fence_after();
-      const float l = sum2(l2), r = 1.f / l;
-      const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
+      const float l = *own + *his, r = 1.f / l;
       const size_t at = (size_t(it.tl.row0) + qi) * p.H + it.h;
-      if (qi < len) p.lse[at] = m * p.scale + logf(l);
-      float o[D];
+      if (half == 0 && qi < len) p.lse[at] = m * p.scale + logf(l);
+      float o[D / 2];
 #pragma unroll
-      for (int q = 0; q < D / 64; ++q) tmem_ld64(tO(t) + lb + q * 64, o + q * 64);
+      for (int q = 0; q < D / 64; ++q) tmem_ld32(lO + q * 32, o + q * 32);
       tmem_wait_ld_regs(o);
       if (qi < len)
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) store_bf16x32(p.o + at * D + q * 32, o + q * 32, r, wide);
+        for (int q = 0; q < D / 64; ++q) store_bf16x32(p.o + at * D + half * (D / 2) + q * 32, o + q * 32, r, wide);
       tc_fence_before();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tslot, 512);
+  if (warp == kMma) tmem_dealloc(*tslot, 512);
 }
 
 template <int D>
