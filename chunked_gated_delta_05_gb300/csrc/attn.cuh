@@ -253,7 +253,7 @@ struct RopeParams {
   // backward
   const __nv_bfloat16 *dqo, *dko;   // [rows,H,D], [rows,Hk,D]
   __nv_bfloat16 *dq, *dk;
-  float *part, *dqw, *dkw;     // part: [rope_bwd_blocks()][2][D]
+  float *part, *dqw, *dkw;     // part: [rope_bwd_blocks()][D]
   int sms;
 };
 cudaError_t launch_rope_fwd(const RopeParams& p, int D, cudaStream_t s);

@@ -117,7 +117,7 @@ struct RopeLayout {
 RopeLayout layout_rope(const RopeProblem& P) {
   RopeLayout l{};
   l.part = align256(P.S.cu ? size_t(P.S.N + 1) * 4 : 4);
-  l.total = l.part + align256(size_t(rope_bwd_blocks()) * 2 * P.S.D * 4);
+  l.total = l.part + align256(size_t(rope_bwd_blocks()) * P.S.D * 4);
   return l;
 }
 
