@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwdPerSm) k_rope_bwd(const __gri
         ln.template turn<true>(&d);
         if (norm) {
           Share x = ln.unpack(xin[a]);
-          const float rstd = rsqrtf(fmaf(head_dot<D>(x, x), 1.f / D, p.eps));
+          const float norm2 = fmaf(head_dot<D>(x, x), 1.f / D, p.eps), rstd = hh < heads ? rsqrtf(norm2) : 0.f;
           scale(&x, dup2(rstd));
 #pragma unroll
           for (int i = 0; i < 2; ++i) {  // zero where the head does not exist

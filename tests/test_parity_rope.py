@@ -95,6 +95,12 @@ def test_large_eps():
     check(1, 20, 2, 1, 64, 64, eps=0.5)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_no_eps(D):
+    """Heads that do not fill a warp leave lanes without one, whose zeros have no finite norm."""
+    check(1, 20, 7, 1, D, 64, eps=0.0)
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_positions_far_away(inter):
     """The same precision at any position, negative ones among them."""
