@@ -24,7 +24,7 @@
 // D from o carries o's rounding to bf16, which a query of few keys feels (dP - D is small there, and 0 for a single key). So the
 // query tiles that see one key tile, the first 128 queries of a causal sequence and all of a shorter one, have it from the scores
 // themselves: sum_j p_ij dP_ij / sum_j p_ij. k_attn_dq, which has a query's whole row there, leaves it to k_attn_dkv, and a query
-// of a single key has dS = 0 in both. (Sequences of 3 to 20 tokens: dq and dk off by 0.0027
+// of a single key has dS = 0 in both, at 1% of the time of the larger calls. (Sequences of 3 to 20 tokens: dq and dk off by 0.0027
 // to 0.0033 of their size with o's D, 0.0024 so, what the operands' and outputs' roundings make.)
 #include "attn.cuh"
 
@@ -679,14 +679,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld64(tP + lb, d);
         tmem_wait_ld_regs(d);
         const int seen = p.causal ? min(qi + 1, x.tl.len) : x.tl.len;
-        if (i + 1 == x.n && (p.causal || x.tail)) {
-          const int left = seen - i * kAttnTile - half * kCols;
+        const int left = seen - i * kAttnTile - half * kCols;
+        if (x.n == 1) {
+          // the row's D from its two halves' sums; a half's slot is written again only after the other's dS of this tile
 #pragma unroll
           for (int e = 0; e < kCols; ++e)
             if (e >= left) w[e] = d[e] = 0.f;
-        }
-        if (x.n == 1) {
-          // the row's D from its two halves' sums; a half's slot is written again only after the other's dS of this tile
           F2 a = dup2(0.f), b = a;
 #pragma unroll
           for (int e = 0; e < kCols / 2; ++e) {
@@ -706,7 +704,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int e = 0; e < kCols / 2; ++e) unf2(mul2(f2(w[2 * e], w[2 * e + 1]), add2(f2(d[2 * e], d[2 * e + 1]), delta)), &d[2 * e], &d[2 * e + 1]);
-        if (x.n == 1 && seen == 1 && half == 0) d[0] = 0.f;
+        if (i + 1 == x.n && (p.causal || x.tail)) {
+#pragma unroll
+          for (int e = 0; e < kCols; ++e)
+            if (e >= left) d[e] = 0.f;
+        }
+        if (seen == 1 && half == 0) d[0] = 0.f;
         store_operand(tS(u) + lb, d);
         tmem_wait_st();
         tc_fence_before();
