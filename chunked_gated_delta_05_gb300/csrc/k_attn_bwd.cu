@@ -5,7 +5,7 @@
 //
 // Three kernels. k_attn_delta leaves D and lse log2(e) by head. k_attn_dq owns 128 queries and walks the key tiles they see;
 // k_attn_dkv owns 128 keys of a key head and walks the query tiles (and the group's heads) that see them. Each output is
-// summed in registers of one CTA's tensor core in a fixed order, so nothing is added atomically and results do not depend on
+// summed in the accumulators of one CTA's tensor core in a fixed order, so nothing is added atomically and results do not depend on
 // the order of blocks; the price is that both recompute s and dP: seven products of 128 x 128 x D a tile pair, where adding dq up in
 // memory would need five.
 //
@@ -19,7 +19,9 @@
 // products run (2 x 4096 tokens x 16 heads: a CTA per tile spent 40 of 203 us, and 22 of 152, on starting and ending).
 //
 // Eight softmax warps, two to a quarter of the TMEM lanes, each on half of a tile's columns. The bf16 operand's halves lie over the
-// columns that their own writers have read. p and dS are rounded to bf16 (as the products' operands); all sums are fp32.
+// columns that their own writers have read. 2 x 4096 causal tokens x 16 heads of 128: 18 us for D, 141 for dq, 181 for dk and dv, 1400 TFLOP/s
+// of the seven products; the tensor core is busy 63 to 67% of it, the rest is the chain from a score to the operand made of it, for which
+// TMEM (all 512 columns in use) leaves no second buffer. p and dS are rounded to bf16 (as the products' operands); all sums are fp32.
 //
 // D from o carries o's rounding to bf16, which a query of few keys feels (dP - D is small there, and 0 for a single key). So the
 // query tiles that see one key tile, the first 128 queries of a causal sequence and all of a shorter one, have it from the scores

@@ -15,8 +15,8 @@
 //
 // What bounds it: with heads of 128 the tensor core. A tile's two products take 1312 cycles (its 128 x 128 x 16 steps 64, or 100 where both
 // operands come from shared memory), so two tiles 2624 of the 2870 that an iteration takes: 16 heads x 8192 causal
-// queries in 183 us, 1500 TFLOP/s. With heads of 64 it is the chain of a tile, softmax (1400 cycles), products and the signals between
-// them (1200): 8 x 1001 queries x 16 heads, every key, 54 us. One thread a row, with 8 softmax warps for 16, took 188 and 57 us: a warp
+// queries in 188 us, 1460 TFLOP/s. With heads of 64 it is the chain of a tile, softmax (1400 cycles), products and the signals between
+// them (1200): 8 x 1001 queries x 16 heads, every key, 53 us. One thread a row, with 8 softmax warps for 16, took 193 and 57 us: a warp
 // alone on its scheduler has 1060 cycles for a row's 128 weights, two with 64 each have 800.
 // An instruction is taken only when the one before it is nearly done, and every wait, even for a phase long past, costs some 75 cycles
 // in which the core may idle. So the issuing thread waits once per tile and iteration, on a barrier on which both the tile's
