@@ -118,6 +118,23 @@ def test_references_move_up_and_down():
         assert (np.abs(f64(t).reshape(exact[n].shape) - exact[n]) <= bound[n]).all(), n
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("far", [4, 16])
+@pytest.mark.parametrize("at", [0, 100, 130, 200, 255, 256, 383, 399])
+def test_a_key_far_above_the_others(at, far, D):
+    """Some queries meet one key whose score moves their reference, in either half of any tile, the others do not."""
+    g = torch.Generator().manual_seed(at + D)
+    T, H = 400, 2
+    q, k, v = rn(g, 1, T, H, D), rn(g, 1, T, 1, D), rn(g, 1, T, 1, D)
+    k[0, at, 0] = q[0, T - 1, 0] * far      # a score of far sqrt(D) for that query (16: 2 to its power overflows fp32), less for the others
+    q[0, ::7, 1] = q[0, T - 1, 0]
+    for causal in (True, False):
+        o, lse = lib().attention_fwd(q, k, v, causal=causal)
+        exact, bound = A.bounds(np.zeros((T, H, D)), rows(q), rows(k), rows(v), [0, T], D ** -0.5, causal)
+        for n, t in (("o", o), ("lse", lse)):
+            assert (np.abs(f64(t).reshape(exact[n].shape) - exact[n]) <= bound[n]).all(), n
+
+
 def test_strided_inputs():
     """q, k and v as slices of one projection give the bits of contiguous ones."""
     g = torch.Generator().manual_seed(5)
