@@ -289,7 +289,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, *, positions=None, cu_seqle
 
 
 def attention(q, k, v, *, causal=True, scale=None, cu_seqlens=None):
-    """Differentiable attention over whole sequences (see :func:`attention_fwd`): ``o``. Reverse mode only."""
+    """Differentiable attention over whole sequences (see :func:`attention_fwd`): ``o``. Reverse mode only. As for any differentiable
+    call, a step is captured into a graph while no eager graph of the same leaves lives (the autograd engine would join the stream
+    that made that one, which a capture does not allow)."""
     if not _differentiated((q, k, v)):
         return attention_fwd(q, k, v, causal=causal, scale=scale, cu_seqlens=cu_seqlens)[0]
     return Attention.apply(q, k, v, causal, scale, cu_seqlens)

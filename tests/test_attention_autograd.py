@@ -206,6 +206,34 @@ def test_captured_training_step():
             assert torch.equal(x, y)
 
 
+def test_captured_through_autograd():
+    """The differentiable calls and their backward captured as one, after a warm-up whose graph is gone, and replayed on new inputs."""
+    g = torch.Generator().manual_seed(14)
+    leaves = [rn(g, 2, 150, h, 64).requires_grad_() for h in (4, 2, 2)]
+    w, f, dO = (1 + rn(g, 64, dtype=F32, std=0.1)).requires_grad_(), freqs(64), rn(g, 2, 150, 4, 64)
+
+    def step(leaves, w):
+        q, k = lib().qk_norm_rope(*leaves[:2], w, w, f)
+        return torch.autograd.grad(lib().attention(q, k, leaves[2]), [*leaves, w], dO)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(leaves, w)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(leaves, w)
+    for _ in range(2):
+        with torch.no_grad():
+            for x in (*leaves, dO):
+                x.copy_(rn(g, *x.shape))
+        graph.replay()
+        want = step([x.detach().clone().requires_grad_() for x in leaves], w.detach().clone().requires_grad_())
+        for x, y in zip(out, want):
+            assert torch.equal(x, y)
+
+
 def test_captured_step_of_many_documents():
     """Tables too long for the launches' parameters are captured with the call, and copied again by every replay."""
     g = torch.Generator().manual_seed(10)
