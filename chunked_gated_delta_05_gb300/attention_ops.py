@@ -20,8 +20,17 @@ _step_desc, _step_args = _lib.packer(_lib.AttnStepDesc), _lib.packer(_lib.AttnSt
 
 def _rows(name, t, shape, dev, width):
     """Elements between tokens of ``t [..,heads,D]`` (0: contiguous)."""
-    if type(t) is torch.Tensor and t.dtype is _BF16 and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return 0
+    if type(t) is torch.Tensor and t.dtype is _BF16 and t.shape == shape and t.get_device() == dev:
+        if t.is_contiguous():
+            return 0
+        if len(shape) == 4:     # the usual cases: a prompt's rows, a step's
+            b, row, head, one = t.stride()
+            if one == 1 and head == shape[3] and row >= width and shape[1] > 1 and (shape[0] == 1 or b == shape[1] * row):
+                return row
+        else:
+            row, head, one = t.stride()
+            if one == 1 and head == shape[2] and row >= width and shape[0] > 1:
+                return row
     return _rows_of(name, t, _BF16, shape, dev, 2, width)
 
 
@@ -86,7 +95,7 @@ _NONE = (None, 0, 0)    # calls on dense batches that need no workspace
 
 
 def _new(t):
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=_BF16, device=t.device)
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, *, positions=None, cu_seqlens: Optional[Sequence[int]] = None, eps=1e-6, interleaved=False):
