@@ -181,6 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_for_previous();
   constexpr uint32_t tS = 0, tP = 128, tV = 256, tK = 256 + D;  // all of TMEM, so it starts at column 0
   auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
+  // A warp's: its lanes come out of it together and of one mind, as the instructions on TMEM behind it need (tcgen05 `.sync.aligned`).
+  auto warp_wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, wait(b, ph, code))); };
 
   // A tile: its key head, keys, first query tile, query tiles a head, and all it walks.
   struct Item {
@@ -293,7 +295,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lead = elect_lead();
       const uint32_t aK = desc_low_k(smem_u32(sK)), aV = desc_low_k(smem_u32(sV)), bQ = desc_low_k(smem_u32(sQ)), bO = desc_low_k(smem_u32(sO)),
                      nQ = desc_low_mn(smem_u32(sQ), kAttnPanel), nO = desc_low_mn(smem_u32(sO), kAttnPanel);
-      auto all_wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, wait(b, ph, code))); };
       Ring<kQ, 1> rq(0);   // the products' Q, S's one tile ahead of dK's
       uint32_t u = 0;      // query tiles so far
       auto scores = [&](int at) {
@@ -308,15 +309,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (long long rd = 0; ok && get_warp(rd, &ok); ++rd) {
         // the first products overwrite operands that the products issued so far have read
-        ok = all_wait(kv_full, rd & 1, kDevTimeoutTma) && all_wait(&q_full[rq.at], rq.phase, kDevTimeoutTma) && all_wait(&ready[u & 1], u >> 1 & 1, kDevTimeoutSync);
+        ok = warp_wait(kv_full, rd & 1, kDevTimeoutTma) && warp_wait(&q_full[rq.at], rq.phase, kDevTimeoutTma) && warp_wait(&ready[u & 1], u >> 1 & 1, kDevTimeoutSync);
         if (!ok) break;
         tc_fence_after();
         scores(rq.at);
-        if (!(ok = all_wait(&o_full[u & 1], u >> 1 & 1, kDevTimeoutTma))) break;
+        if (!(ok = warp_wait(&o_full[u & 1], u >> 1 & 1, kDevTimeoutTma))) break;
         dprobs(u & 1, x.n == 1);
         for (int it = 0; it < x.n; ++it, ++u) {
           // the gates answer for the tiles of the products that follow either operand
-          if (!(ok = all_wait(p_ready, u & 1, kDevTimeoutSync))) break;
+          if (!(ok = warp_wait(p_ready, u & 1, kDevTimeoutSync))) break;
           tc_fence_after();
           const int qs = rq.at;
           const uint32_t os = u & 1;
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           product_ts<D, kCols / 2>(lead, tV, tS, nO + os * (kTile >> 4), it > 0);
           commit(lead, &o_empty[os]);
           if (it + 1 < x.n) scores(rq.at);
-          if (!(ok = all_wait(ds_ready, u & 1, kDevTimeoutSync))) break;
+          if (!(ok = warp_wait(ds_ready, u & 1, kDevTimeoutSync))) break;
           tc_fence_after();
           product_ts<D, kCols / 2>(lead, tK, tP, nQ + qs * (kTile >> 4), it > 0);
           commit(lead, &q_empty[qs]);
@@ -366,13 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool wide = (reinterpret_cast<uintptr_t>(half ? p.dk : p.dv) & 31) == 0;
     bool ok = true;
     uint32_t u = 0;
-    for (long long rd = 0; ok && get(rd, &ok); ++rd) {
+    for (long long rd = 0; ok && get_warp(rd, &ok); ++rd) {
       const AttnTile& tl = x.tl;
       int q0 = x.i0 * kAttnTile + half * kCols;
       for (int it = 0; it < x.n && ok; ++it, ++u) {
         const uint32_t os = u & 1;
         const float2 *lse = reinterpret_cast<const float2*>(vec + os * 256 + half * kCols + col), *delta = lse + 64;
-        ok = wait(&ready[os], u >> 1 & 1, kDevTimeoutSync) && wait(s_full, u & 1, kDevTimeoutMma);
+        ok = warp_wait(&ready[os], u >> 1 & 1, kDevTimeoutSync) && warp_wait(s_full, u & 1, kDevTimeoutMma);
         if (!ok) break;
         tc_fence_after();
         // w[32 h + 4 b + 2 r + y]: row key0 + 16 h + 8 r, column 8 b + col + y
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_ready);
-        if (!(ok = wait(dp_full, u & 1, kDevTimeoutMma))) break;
+        if (!(ok = warp_wait(dp_full, u & 1, kDevTimeoutMma))) break;
         tc_fence_after();
         float d[64];
         tmem_ld_16x64(tP + lb, d);
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         q0 += kAttnTile;
         if (q0 - half * kCols >= tl.len) q0 = x.i0 * kAttnTile + half * kCols;  // the next head of the group
       }
-      if (!ok || !(ok = wait(done, rd & 1, kDevTimeoutMma))) break;
+      if (!ok || !(ok = warp_wait(done, rd & 1, kDevTimeoutMma))) break;
       tc_fence_after();
       const int key = tl.first + (tid & 127);
       __nv_bfloat16* dst = (half ? p.dk : p.dv) + ((size_t(tl.row0) + key) * p.Hk + x.hk) * D;
@@ -493,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t tP = 256, tQ = 384;  // all of TMEM, so it starts at column 0
   auto tS = [&](uint32_t u) { return (u & 1) * 128; };
   auto wait = [&](uint64_t* b, uint32_t ph, int code) { return attn_wait(b, ph, abort_flag, p.status, code); };
+  auto warp_wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, wait(b, ph, code))); };
 
   // A tile: its head and key head, queries, key tiles, and whether the last of those reaches past the sequence.
   struct Item {
@@ -588,13 +590,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lead = elect_lead();
       const uint32_t aQ = desc_low_k(smem_u32(sQ)), aO = desc_low_k(smem_u32(sO)), bK = desc_low_k(smem_u32(sK)), bV = desc_low_k(smem_u32(sV)),
                      nK = desc_low_mn(smem_u32(sK), kAttnPanel);
-      auto all_wait = [&](uint64_t* b, uint32_t ph, int code) { return bool(__all_sync(0xffffffffu, wait(b, ph, code))); };
       Ring<kK, 1> rs(0), rk(0);  // K of the scores, and of dq
       uint32_t u = 0, zeros = 0;  // key tiles so far; a bit per stage, the phase of its next zeroing
       auto scores = [&](uint32_t at, bool last) {  // S of key tile u = at, once its K has landed
-        bool there = all_wait(&k_full[rs.at], rs.phase, kDevTimeoutTma);
+        bool there = warp_wait(&k_full[rs.at], rs.phase, kDevTimeoutTma);
         if (there && last && x.tail) {
-          there = all_wait(&zeroed[rs.at], zeros >> rs.at & 1u, kDevTimeoutSync);
+          there = warp_wait(&zeroed[rs.at], zeros >> rs.at & 1u, kDevTimeoutSync);
           zeros ^= 1u << rs.at;
         }
         if (!there) return false;
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (long long rd = 0; ok && get_warp(rd, &ok); ++rd) {
         // the first products overwrite operands that the products issued so far have read
-        if (!(ok = all_wait(q_full, rd & 1, kDevTimeoutTma) && scores(u, x.n == 1) && all_wait(&v_full[u & 1], u >> 1 & 1, kDevTimeoutTma))) break;
+        if (!(ok = warp_wait(q_full, rd & 1, kDevTimeoutTma) && scores(u, x.n == 1) && warp_wait(&v_full[u & 1], u >> 1 & 1, kDevTimeoutTma))) break;
         if (x.n > 1) {
           dprobs(u, false);
           if (!(ok = scores(u + 1, x.n == 2))) break;
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < x.n; ++i, ++u) {
           // the gate answers for V of the next tile
-          if (!(ok = all_wait(ds_ready, u & 1, kDevTimeoutSync))) break;
+          if (!(ok = warp_wait(ds_ready, u & 1, kDevTimeoutSync))) break;
           tc_fence_after();
           if (i + 1 < x.n) dprobs(u + 1, i + 2 == x.n);
           product_ts<D, kCols / 2>(lead, tQ, tS(u), nK + rk.at * (kTile >> 4), i > 0);
@@ -657,14 +658,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool wide = (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
     bool ok = true;
     uint32_t u = 0, short_rows = 0;
-    for (long long rd = 0; ok && get(rd, &ok); ++rd) {
+    for (long long rd = 0; ok && get_warp(rd, &ok); ++rd) {
       const int qi = x.tl.first + row;
       const bool mine = qi < x.tl.len;
       const long long at = (long long)x.h * p.rows + x.tl.row0 + qi;
       const F2 lse = dup2(mine ? p.lse2[at] : 0.f);
       F2 delta = dup2(mine && x.n > 1 ? p.delta[at] : 0.f);
       for (int i = 0; i < x.n && ok; ++i, ++u) {
-        if (!(ok = wait(&s_full[u & 1], u >> 1 & 1, kDevTimeoutMma))) break;
+        if (!(ok = warp_wait(&s_full[u & 1], u >> 1 & 1, kDevTimeoutMma))) break;
         tc_fence_after();
         float w[kCols], d[kCols];
         tmem_ld64(tS(u) + lb, w);
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           w[2 * e] = exp2_approx(a);
           w[2 * e + 1] = exp2_approx(b);
         }
-        if (!(ok = wait(dp_full, u & 1, kDevTimeoutMma))) break;
+        if (!(ok = warp_wait(dp_full, u & 1, kDevTimeoutMma))) break;
         tc_fence_after();
         tmem_ld64(tP + lb, d);
         tmem_wait_ld_regs(d);
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           unf2(b, &b0, &b1);
           sums[tid] = make_float2(a0 + a1, b0 + b1);
           mbar_arrive(&summed[warp & 3]);
-          if (!(ok = wait(&summed[warp & 3], short_rows++ & 1, kDevTimeoutSync))) break;
+          if (!(ok = warp_wait(&summed[warp & 3], short_rows++ & 1, kDevTimeoutSync))) break;
           const float2 lo = sums[row], hi = sums[row + 128];
           const float own = -(lo.x + hi.x) / (lo.y + hi.y);
           delta = dup2(own);
@@ -717,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(ds_ready);
       }
-      if (!ok || !(ok = wait(done, rd & 1, kDevTimeoutMma))) break;
+      if (!ok || !(ok = warp_wait(done, rd & 1, kDevTimeoutMma))) break;
       tc_fence_after();
       __nv_bfloat16* dst = p.dq + ((size_t(x.tl.row0) + qi) * p.H + x.h) * D + half * (D / 2);
       store_row<D / 2>(dst, tQ + lane0 + half * (D / 2), p.scale, mine, wide);

@@ -1,0 +1,32 @@
+"""Rules of the attention kernels that no run can show without letting a wait run out on the GPU: their source is read instead (CPU)."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "chunked_gated_delta_05_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+@pytest.mark.parametrize("name,roles", [("k_attn_fwd.cu", 2), ("k_attn_bwd.cu", 4)])
+def test_warps_that_use_tensor_memory_vote_on_their_waits(name, roles):
+    """Reads and writes of tensor memory, and the products, are instructions of a whole warp: its lanes come to them together, and where a wait
+    ran out for one of them none goes on. So these roles wait by functions in which all lanes vote."""
+    seen = 0
+    for section in source(name).split("// ---------------- ")[1:]:
+        if not re.search(r"\b(tmem_(ld|st)\w*|product_\w+)[<(]", section):
+            continue
+        seen += 1
+        section = re.sub(r"__all_sync\(0xffffffffu, wait\(", "", section.split("\ntemplate <int D>")[0])
+        alone = re.findall(r"^.*(?<!\w)(?:wait|attn_wait|mbar_wait|get)\(.*$", section, re.M)
+        assert not alone, alone
+    assert seen == roles
+
+
+def test_step_warps_vote_on_their_waits():
+    lines = [x for x in source("k_attn_step.cu").splitlines() if re.search(r"\b(attn|mbar)_wait\(", x)]
+    assert lines and all("__all_sync(0xffffffffu, attn_wait(" in x for x in lines), lines
