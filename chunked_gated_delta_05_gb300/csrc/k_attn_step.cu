@@ -14,7 +14,7 @@
 // each key head (or 16 query heads of one): rows differ in length, and their lengths are known on the device only. The key
 // heads' blocks of a share run side by side, so that a token's row of the cache is read at one time. A block's four warps take 16
 // keys of a unit each. Where a row's units lie in several shares, the blocks leave a weighted sum, its reference and the sum of
-// weights, which a second kernel joins. The reference moves only when a score lies 2^8 above it, so no maximum is taken otherwise.
+// weights, which a second kernel joins. The reference moves only for a score whose weight would exceed 2^8, so no maximum is taken otherwise.
 // Weights are rounded to bf16 for the product (the values' type), sums are fp32.
 #include "attn.cuh"
 
@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(kJoin * 32) k_attn_join(const AttnStepParams p
   }
   const int parts = p.Hk * row_blocks, part = hk * row_blocks + rb;
   const int2 span = p.span[(long long)b * parts + part];
-  if (span.x == span.y) return;  // written by its only block
+  // Written by its only block; or by none, where a wait of the step ran out, and then what stands there names no pieces.
+  if (span.x < 0 || span.x >= span.y || span.y >= p.shares) return;
   const int n = span.y - span.x + 1;
   const long long first = (long long)(b + span.x) * parts + part, step = (long long)parts * 8 * kRows;  // rows from one piece to the next
   const float* src = p.part + (first * 8 * kRows + r) * D + lane * kPer;

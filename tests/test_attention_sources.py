@@ -30,3 +30,13 @@ def test_warps_that_use_tensor_memory_vote_on_their_waits(name, roles):
 def test_step_warps_vote_on_their_waits():
     lines = [x for x in source("k_attn_step.cu").splitlines() if re.search(r"\b(attn|mbar)_wait\(", x)]
     assert lines and all("__all_sync(0xffffffffu, attn_wait(" in x for x in lines), lines
+
+
+def test_the_join_trusts_no_piece_that_was_not_written():
+    """A step whose wait ran out leaves its rows' places in the workspace as they were. The join's addresses come from those, so it holds them
+    against the number of shares first."""
+    join = source("k_attn_step.cu").split("k_attn_join(", 1)[1].split("template <int D, int kRows>", 1)[0]
+    read, first = join.index("p.span["), join.index("p.part +")
+    between = join[read:first]
+    for condition in (r"span\.x < 0", r"span\.x >= span\.y", r"span\.y >= p\.shares"):
+        assert re.search(condition + r".*return;", between), condition
