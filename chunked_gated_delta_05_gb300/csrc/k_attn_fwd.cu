@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!item_of(p, rd, total, &it)) break;
       const int mine = it.n[t], len = it.tl.len, qi = it.tl.first + t * kAttnTile + row;  // in the sequence
       if (mine == 0) continue;
+      const float high = qi < len ? kHigh : INFINITY;  // rows behind the sequence hold its neighbour's queries: they move no reference
       float m = -INFINITY;
       F2 l2 = dup2(0.f);
       for (int j = 0; j < mine; ++j) {
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[e] = __uint_as_float(pack_bf16(a, b));
           }
           sum[0] = add2(sum[0], sum[1]);
-          if (fresh || !pair_any(pair, !ok || sum2(sum[0]) > kHigh)) {
+          if (fresh || !pair_any(pair, !ok || sum2(sum[0]) > high)) {
             l2 = add2(l2, sum[0]);
             break;
           }
