@@ -39,6 +39,8 @@ constexpr int kMma = 16, kTma = 17, kGate = 18;
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 16 x 104 + 4 x 64 = 20 x 96, the launch's
 constexpr int kCols = 64;                          // columns of a tile to a softmax warp
 constexpr float kHigh = 65536.f;  // sum of half a tile's weights that moves the reference
+// The reference of a row whose scores so far are all minus infinity: their weights come out as zero, and any other score moves it.
+constexpr float kNone = -1e30f;
 
 template <int D>
 struct Cfg {
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             const float f = next == m ? 1.f : exp2_approx((m - next) * c);
-            m = next;
+            m = next == -INFINITY ? kNone : next;
             l2 = mul2(l2, dup2(f));
             if (j > 0) {
 #pragma unroll
