@@ -189,7 +189,7 @@ def _scale(scale):
 
 
 def _kept(cu_seqlens):
-    """Offsets as a backward keeps them: a copy, whatever becomes of the caller's."""
+    """Offsets that a forward has accepted, as its backward keeps them: a copy, whatever becomes of the caller's."""
     return None if cu_seqlens is None else tuple(cu_seqlens.tolist() if isinstance(cu_seqlens, torch.Tensor) else cu_seqlens)
 
 
@@ -259,10 +259,11 @@ class QkNormRope(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, inv_freq, positions, cu_seqlens, eps, interleaved):
+        out = qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions=positions, cu_seqlens=cu_seqlens, eps=eps, interleaved=interleaved)
         ctx.save_for_backward(q, k, q_weight, k_weight, inv_freq, positions)
         ctx.cfg = dict(cu_seqlens=_kept(cu_seqlens), eps=eps, interleaved=interleaved)
         ctx.set_materialize_grads(False)
-        return qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions=positions, **ctx.cfg)
+        return out
 
     @staticmethod
     @_first_order
