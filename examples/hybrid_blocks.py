@@ -100,6 +100,33 @@ class ScanBlock:
         return lib.selective_scan_step(h, u, delta, A, B, C, D=self.p["D"], z=z, delta_bias=self.p["dt_bias"]) @ self.p["w_out"], stream
 
 
+class Pages:
+    """Keys and values of sequences in pages of ``page`` tokens, ``more`` pages a sequence at a time as they grow."""
+
+    def __init__(self, sequences, page, more, heads):
+        self.page, self.more, self.tokens = page, more, 0      # tokens: of the longest sequence, known without asking the device
+        self.k = torch.zeros(0, page, heads, 128, dtype=BF16, device="cuda")
+        self.v = torch.zeros_like(self.k)
+        self.table = torch.zeros(sequences, 0, dtype=torch.int32, device="cuda")
+        self.lengths = torch.zeros(sequences, dtype=torch.int32, device="cuda")
+
+    def extend(self, tokens):
+        """Counts ``tokens`` more of every sequence and sees that there are pages for them."""
+        self.tokens += tokens
+        self.lengths += tokens
+        sequences, have = self.table.shape
+        need = -(-self.tokens // self.page) - have
+        if need > 0:
+            need = -(-need // self.more) * self.more
+            pages = torch.arange(len(self.k), len(self.k) + sequences * need, dtype=torch.int32, device="cuda")
+            self.table = torch.cat([self.table, pages.view(sequences, need)], 1)
+            empty = self.k.new_zeros(sequences * need, *self.k.shape[1:])
+            self.k, self.v = torch.cat([self.k, empty]), torch.cat([self.v, empty])
+
+    def tensors(self):
+        return self.k, self.v, self.table, self.lengths
+
+
 class AttentionBlock:
     def __init__(self, heads, kv_heads, scale, page=64, pages=8, theta=1e4):
         self.H, self.Hk, self.scale, self.page, self.pages = heads, kv_heads, scale, page, pages
@@ -115,29 +142,23 @@ class AttentionBlock:
         q, k, v = (y @ self.p["w_in"]).split([self.H * 128, self.Hk * 128, self.Hk * 128], -1)     # they stay strided slices
         return (t.unflatten(-1, (-1, 128)) for t in (q, k, v))
 
-    def cache(self, sequences, tokens):
-        """Empty pages for ``sequences``, and the lengths after ``tokens`` tokens."""
-        k = torch.zeros(sequences * self.pages, self.page, self.Hk, 128, dtype=BF16, device="cuda")
-        table = torch.arange(sequences * self.pages, dtype=torch.int32, device="cuda").view(sequences, self.pages)
-        return k, torch.zeros_like(k), table, torch.full((sequences,), tokens, dtype=torch.int32, device="cuda")
-
     def prompt(self, x, stream, keep):
         y, stream = lib.add_rms_norm(x, stream, self.p["norm"], residual_scale=self.scale)
         q, k, v = self.heads(y)
-        cache = self.cache(*x.shape[:2]) if keep else None
+        cache = Pages(x.shape[0], self.page, self.pages, self.Hk) if keep else None
         if keep:
-            q, k = lib.qk_norm_rope_store(q, k, v, self.p["q_norm"], self.p["k_norm"], self.inv_freq, *cache)
+            cache.extend(x.shape[1])
+            q, k = lib.qk_norm_rope_store(q, k, v, self.p["q_norm"], self.p["k_norm"], self.inv_freq, *cache.tensors())
         else:
             q, k = lib.qk_norm_rope(q, k, self.p["q_norm"], self.p["k_norm"], self.inv_freq)
         return lib.attention(q, k, v).flatten(-2) @ self.p["w_out"], stream, cache
 
     def step(self, x, stream, cache):
-        k_cache, v_cache, table, lengths = cache
         y, stream = lib.add_rms_norm_fwd(x, stream, self.p["norm"], residual_scale=self.scale)
-        lengths += 1
+        cache.extend(1)
         q, k, v = self.heads(y)
-        q, _ = lib.qk_norm_rope_store(q, k, v, self.p["q_norm"], self.p["k_norm"], self.inv_freq, k_cache, v_cache, table, lengths)
-        return lib.attention_step(q, k_cache, v_cache, table, lengths).flatten(-2) @ self.p["w_out"], stream
+        q, _ = lib.qk_norm_rope_store(q, k, v, self.p["q_norm"], self.p["k_norm"], self.inv_freq, *cache.tensors())
+        return lib.attention_step(q, *cache.tensors()).flatten(-2) @ self.p["w_out"], stream
 
 
 class Model:
