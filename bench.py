@@ -68,16 +68,16 @@ KERNEL_SOURCES_KDA = {**KERNEL_SOURCES, "prepare": "k_prep_kda.cu", "bwd_tok": "
 # each, all heads in one group). The chunk kernels' traffic is per chunk-head, so the
 # B=1 T=32768 H=16 entries are those bytes x 4 (8192 chunk-heads) and the B=1 T=8192 H=32 KDA
 # entries x 2 (4096); the chains' traffic depends on the segment plan and is not scaled.
-_GDN_T4096 = {"prepare": 611_470_336, "chain_fwd": 545_798_400, "compose": 29_376_000,
-              "chain_bwd": 532_253_440, "bwd_feat": 526_161_920, "bwd_tok": 623_438_592}
-_KDA_T4096 = {"prepare": 748_809_984, "chain_fwd": 548_044_800, "compose": 29_377_024,
-              "chain_bwd": 533_810_176, "bwd_feat": 526_905_344, "bwd_tok": 749_082_368}
-_HASHES = {("prepare", False): "9f4bd99a328245fe", ("prepare", True): "ef796d48524c2ad1",
-           ("chain_fwd", False): "ede9cdea014a4770", ("chain_fwd", True): "ede9cdea014a4770",
-           ("compose", False): "aee154a000cfde9f", ("compose", True): "aee154a000cfde9f",
-           ("chain_bwd", False): "9a792f73725d839b", ("chain_bwd", True): "9a792f73725d839b",
-           ("bwd_feat", False): "ca6dc5d5b6a21f11", ("bwd_feat", True): "ca6dc5d5b6a21f11",
-           ("bwd_tok", False): "e3d84be8a81a7d84", ("bwd_tok", True): "674c8996578b69be"}
+_GDN_T4096 = {"prepare": 611_373_824, "chain_fwd": 545_132_032, "compose": 29_376_512,
+              "chain_bwd": 531_595_264, "bwd_feat": 526_462_720, "bwd_tok": 623_537_152}
+_KDA_T4096 = {"prepare": 749_130_496, "chain_fwd": 546_676_736, "compose": 29_376_256,
+              "chain_bwd": 533_862_912, "bwd_feat": 527_277_056, "bwd_tok": 749_122_560}
+_HASHES = {("prepare", False): "b97e2878a51cc63e", ("prepare", True): "5d00a0922f6fa8b0",
+           ("chain_fwd", False): "e2f59192c69ec219", ("chain_fwd", True): "e2f59192c69ec219",
+           ("compose", False): "98ce04849995afc5", ("compose", True): "98ce04849995afc5",
+           ("chain_bwd", False): "5e53803270f7c929", ("chain_bwd", True): "5e53803270f7c929",
+           ("bwd_feat", False): "44964a9cf178deeb", ("bwd_feat", True): "44964a9cf178deeb",
+           ("bwd_tok", False): "2dd763347c1bd1bf", ("bwd_tok", True): "0017f5e4b44a32b1"}
 NCU_TRAFFIC_BYTES = {}
 for _k, _v in _GDN_T4096.items():
     NCU_TRAFFIC_BYTES[(_k, "gdn_b2_t4096_h16")] = (_v, _HASHES[(_k, False)])

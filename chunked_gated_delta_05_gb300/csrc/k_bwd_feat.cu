@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tl = tb + tmem_lane_base(warp);
   // Half hf of the h and dh' rows f (panel hf of each: shared memory -> TMEM as tf32 A
   // operands, widened exactly from bf16); dgam partial sums in fp32.
-  const bool tma_ok = mbar_wait(&bar_tma, 0, &abort_flag, p.status, kDevTimeoutTma);
+  const bool tma_ok = warp_all(mbar_wait(&bar_tma, 0, &abort_flag, p.status, kDevTimeoutTma));
   float dg = 0.f;
   if (tma_ok) {
     const uint8_t* hrow = sm + kOffHS + hf * 16384;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_async_smem();
   __syncwarp();
-  const bool ok = mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma);
+  const bool ok = warp_all(mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   if (ok) {
     // this thread's tokens t = t0 + e of the 64-token columns
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   // dKt = P3, token-major rows, while the second group runs
-  const bool ok3 = ok && mbar_wait(&bar_mma3, 0, &abort_flag, p.status, kDevTimeoutMma);
+  const bool ok3 = warp_all(ok && mbar_wait(&bar_mma3, 0, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   if (ok3) {
     const int t0 = 32 * hf;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_wait_ld_regs(r);
     store_col_bf16<32>(p.dKt + tile * kTileW + size_t(t0) * kD, r, f);
   }
-  const bool ok2 = ok3 && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma);
+  const bool ok2 = warp_all(ok3 && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   if (ok2) {
     const int t0 = 32 * hf;

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tb = tslot;
   const uint32_t tl = tb + tmem_lane_base(warp);
   const float Glast = s_G[len - 1];
-  const bool tma_ok = mbar_wait(&bar_tma, 0, &abort_flag, p.status, kDevTimeoutTma);
+  const bool tma_ok = warp_all(mbar_wait(&bar_tma, 0, &abort_flag, p.status, kDevTimeoutTma));
   // A full chunk has no rows to clear, so its exact Gram products K K^T and Q K^T (raw bf16
   // tiles) go out now and run under the dO conversion; a ragged chunk issues them with dAqk.
   const bool early_gram = len == kC;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit(&bar_mma);  // covers the early Gram products too (same issuing thread)
   }
   __syncwarp();
-  bool ok = tma_ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma);
+  bool ok = warp_all(tma_ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   // ---- K1 = diag(beta exp(G) r_k) k and V1 = diag(beta) v as 64-row operands [j][d]
   // (a warp converts one row per step: lane l takes columns 4l..4l+3, one 16-byte chunk)
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int e = 0; e < 16; ++e) abuf[e] = a[size_t(i0 + e) * kC];
   }
-  ok = ok && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma);
+  ok = warp_all(ok && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   // ---- dL = -A^T dA A^T: X = A^T dA, then X A^T.
   // Operands (64x64 tf32, 16 KB each): AT [j][i] (A op), dAT [m][i] (B op), A [l][m] (B op), X.
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit(&bar_mma);
   }
   __syncwarp();
-  ok = ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma);
+  ok = warp_all(ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   {
     float r[16];
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit(&bar_mma);
   }
   __syncwarp();
-  ok = ok && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma);
+  ok = warp_all(ok && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
 
   // ---- elementwise on token pairs: row owner i holds row i of dL', dAqk, KK, QK.
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_dG[tid] -= col;
   }
   __syncwarp();
-  ok = ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma);
+  ok = warp_all(ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
 
   // ---- per-token assembly. Owner threads stage their rows of the two last products from

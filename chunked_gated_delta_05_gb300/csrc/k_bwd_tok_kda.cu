@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // G (scaled to log2 units) and dO as a 64-row tf32 operand; rows past the chunk are zero.
   // Both arrived with the other copies (G in R1, dO in the G area): each thread reads its
   // values into registers and, once every thread has, writes them to their places.
-  const bool tma_ok = mbar_wait(&bar_tma, 0, &abort_flag, p.status, kDevTimeoutTma);
+  const bool tma_ok = warp_all(mbar_wait(&bar_tma, 0, &abort_flag, p.status, kDevTimeoutTma));
   {
     const int t0 = 32 * half;
     const float* gt = reinterpret_cast<const float*>(sm + kR1);
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit(&bar_mma);
   }
   __syncwarp();
-  bool ok = tma_ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma);
+  bool ok = warp_all(tma_ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   // ---- K1 = beta r_k exp(G) (.) k and V1 = beta v as 64-row operands [j][c]: each warp takes
   // whole rows, lane l channels 4l .. 4l+3 (one 16-byte chunk of each swizzled row)
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int e = 0; e < 16; ++e) abuf[e] = a[size_t(i0 + e) * kC];
   }
-  ok = ok && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma);
+  ok = warp_all(ok && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   // ---- dL = -A^T dA A^T
   uint8_t* sAT = sm + kR3;
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit(&bar_mma);
   }
   __syncwarp();
-  ok = ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma);
+  ok = warp_all(ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   {
     float r[32];
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit(&bar_mma);
   }
   __syncwarp();
-  ok = ok && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma);
+  ok = warp_all(ok && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   // ---- decayed pair sums on the tensor cores. For i in the 16-row block I (reference row
   // r_I = 16 I) and j <= 16 I + 15, exp(G_ic - G_jc) = P_ic E_I[j][c] with
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit(&bar_mma);
   }
   __syncwarp();
-  ok = ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma);
+  ok = warp_all(ok && mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   __syncthreads();  // MT and XP^T are free: EK^T takes their place
   {
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit(&bar_mma);
   }
   __syncwarp();
-  ok = ok && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma);
+  ok = warp_all(ok && mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   __syncthreads();  // the EK^T operands are free: the accumulators take their places
   // Per (token, channel) results into the dk^ / dq^ / dG accumulators and k^ (.) X1 (dbeta's

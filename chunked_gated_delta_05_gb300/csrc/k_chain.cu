@@ -308,14 +308,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&vready);
         g_cur = g_next;
-        if (!mbar_wait(&mma2, par, &abort_flag, p.status, kDevTimeoutMma)) { alive = false; break; }
+        if (!warp_all(mbar_wait(&mma2, par, &abort_flag, p.status, kDevTimeoutMma))) { alive = false; break; }
         tc_fence_after();
         continue;
       }
-      if (use_u && !mbar_wait(&full2, par, &abort_flag, p.status, kDevTimeoutTma)) { alive = false; break; }
-      if (!mbar_wait(&mma1, par, &abort_flag, p.status, kDevTimeoutMma)) { alive = false; break; }
+      if (use_u && !warp_all(mbar_wait(&full2, par, &abort_flag, p.status, kDevTimeoutTma))) { alive = false; break; }
+      if (!warp_all(mbar_wait(&mma1, par, &abort_flag, p.status, kDevTimeoutMma))) { alive = false; break; }
       // the previous chunk's intra-chunk output product was issued before this product
-      if (o && j > 0 && !mbar_wait(&mma3, par ^ 1u, &abort_flag, p.status, kDevTimeoutMma)) { alive = false; break; }
+      if (o && j > 0 && !warp_all(mbar_wait(&mma3, par ^ 1u, &abort_flag, p.status, kDevTimeoutMma))) { alive = false; break; }
       tc_fence_after();
       {
         float r[32];
@@ -339,11 +339,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the previous chunk's output, while this chunk's state update runs
       if (o && j > 0) out_epilogue(j - 1, true);
       g_cur = g_next;
-      if (!mbar_wait(&mma2, par, &abort_flag, p.status, kDevTimeoutMma)) { alive = false; break; }
+      if (!warp_all(mbar_wait(&mma2, par, &abort_flag, p.status, kDevTimeoutMma))) { alive = false; break; }
       tc_fence_after();
     }
     if (o && alive) {
-      if (mbar_wait(&mma3, (nc - 1) & 1, &abort_flag, p.status, kDevTimeoutMma)) {
+      if (warp_all(mbar_wait(&mma3, (nc - 1) & 1, &abort_flag, p.status, kDevTimeoutMma))) {
         tc_fence_after();
         out_epilogue(nc - 1, false);
       } else {

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&mready);
-      if (!mbar_wait(&mma1, par, &abort_flag, p.status, kDevTimeoutMma)) { alive = false; break; }
+      if (!warp_all(mbar_wait(&mma1, par, &abort_flag, p.status, kDevTimeoutMma))) { alive = false; break; }
       tc_fence_after();
       if (dvn_save) {
         // dv_new for the feature-major kernel (rounded to tf32); its buffer is rewritten two
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&doready);
         if (j + 2 < nc) load_dO(p, c - 2, h, v, t0, dnext);
       }
-      if (!mbar_wait(&mma2, par, &abort_flag, p.status, kDevTimeoutMma)) { alive = false; break; }
+      if (!warp_all(mbar_wait(&mma2, par, &abort_flag, p.status, kDevTimeoutMma))) { alive = false; break; }
       tc_fence_after();
     }
     // exit gradient: dh0, the next segment's seed (pass 0), or the segment's map

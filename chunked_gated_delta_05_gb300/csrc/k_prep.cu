@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tma_store_commit();
   }
-  const bool ok1 = mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma);
+  const bool ok1 = warp_all(mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   if (tid == 0) tma_store_wait_read();  // L and A1 are rewritten next
   __syncthreads();
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_bf16_ss(tb + 128, desc_kmajor(a2, kPanel, s), desc_mnmajor_bf16(v0, kPanel, s), id, s > 0);
     mma_commit(&bar_mma);
   }
-  const bool ok2 = mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma);
+  const bool ok2 = warp_all(mbar_wait(&bar_mma, 1, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   // Warps 0-3 finish W (staged in L for chunk 0, S0 for chunk 1), warps 4-7 finish U (staged
   // in A1 / A2, free once the MMAs are done).

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.beff) p.beff[tile * kC + tid] = s_b[tid];
     }
   }
-  bool ok = mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma);
+  bool ok = warp_all(mbar_wait(&bar_mma, 0, &abort_flag, p.status, kDevTimeoutMma));
   uint32_t mma_phase = 1;
   tc_fence_after();
   if (tid == 0 && ok) {
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // WY operands: A1 = (A - I) diag(beta r_k) (tf32), A2 = (A - I) diag(beta) (bf16), both
   // K-major [i][j]; four threads per column j, 16 rows each. The value tile has landed by now;
   // its rows past the chunk are cleared first.
-  ok = ok && mbar_wait(&bar_v, 0, &abort_flag, p.status, kDevTimeoutTma);
+  ok = warp_all(ok && mbar_wait(&bar_v, 0, &abort_flag, p.status, kDevTimeoutTma));
   if (ok && tid >= len && tid < kC) {
     for (int c16 = 0; c16 < 16; ++c16)
       *reinterpret_cast<uint4*>(sV + sw128_offset(tid, c16 * 8, kC, 2)) = make_uint4(0, 0, 0, 0);
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
-  ok = ok && mbar_wait(&bar_mma, mma_phase, &abort_flag, p.status, kDevTimeoutMma);
+  ok = warp_all(ok && mbar_wait(&bar_mma, mma_phase, &abort_flag, p.status, kDevTimeoutMma));
   tc_fence_after();
   // W and U rows: thread (c, hf) takes channel c of the 32 tokens from 32 hf, with the unit
   // diagonal of A added in fp32: W = A1 K1 + beta r_k exp(G) k and U = A2 v + beta v. W and U

@@ -81,6 +81,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
   }
 }
+// Whether x holds for all lanes of the warp, all of which take part. Around a wait: the lanes come out of it together and of one
+// mind, as the warp's instructions on TMEM behind it need (tcgen05 `.sync.aligned`).
+__device__ __forceinline__ bool warp_all(bool x) { return __all_sync(0xffffffffu, x); }
 // Bounded wait that ignores the abort flag: an aborting CTA uses it to let its own copies and
 // MMAs that are already in flight finish before it frees their destinations. False after
 // `limit_ns` without completion.

@@ -1,4 +1,4 @@
-"""Rules of the attention kernels that no run can show without letting a wait run out on the GPU: their source is read instead (CPU)."""
+"""Rules of the kernels that no run can show without letting a wait run out on the GPU: their source is read instead (CPU)."""
 import os
 import re
 
@@ -40,3 +40,20 @@ def test_the_join_trusts_no_piece_that_was_not_written():
     between = join[read:first]
     for condition in (r"span\.x < 0", r"span\.x >= span\.y", r"span\.y >= p\.shares"):
         assert re.search(condition + r".*return;", between), condition
+
+
+@pytest.mark.parametrize("name", ["k_prep.cu", "k_prep_kda.cu", "k_chain.cu", "k_chain_bwd.cu", "k_bwd_feat.cu", "k_bwd_tok.cu", "k_bwd_tok_kda.cu"])
+def test_the_recurrences_warps_vote_on_their_waits(name):
+    """In these kernels a wait of whole warps is one whose result goes on to all of their threads: a named result, or a chain warp's loop. Waits of a
+    single thread (issuing and copying) and those whose result is not used stay as they are."""
+    voted = 0
+    chain = name.startswith("k_chain")
+    text = source(name)
+    if chain:       # behind the single threads' branches
+        text = text[text.index("} else if (warp < kChainThreads / 32) {"):]
+    for line in text.splitlines():
+        if "mbar_wait(" not in line or (not chain and not re.search(r"\bok\d?\b|\btma_ok\b", line)) or "tid == 0" in line:
+            continue
+        assert "warp_all(" in line, line
+        voted += 1
+    assert voted
