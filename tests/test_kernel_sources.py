@@ -57,3 +57,10 @@ def test_the_recurrences_warps_vote_on_their_waits(name):
         assert "warp_all(" in line, line
         voted += 1
     assert voted
+
+
+def test_the_shared_header_lists_no_attention_kinds():
+    """bench.py's traffic figures hold while a kernel's file and the shared header are those of their capture: other operators' kinds stay out of it."""
+    shared = set(re.findall(r"\bkK[A-Z]\w*", source("common.cuh")))
+    used = set(re.findall(r"TimedScope \w+\((kK\w+)", source("attn_api.cu")))
+    assert used and not used & shared, used & shared
