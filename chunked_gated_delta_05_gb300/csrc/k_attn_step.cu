@@ -378,9 +378,11 @@ static cudaError_t launch(const AttnStepParams& p, cudaStream_t s) {
   cudaError_t e = allow_smem(k_attn_step<D, kRows>, kSmem, &done);
   if (e == cudaSuccess) e = launch_after(k_attn_step<D, kRows>, dim3(unsigned(p.shares * p.Hk * rb)), block, kSmem, s, p, rb);
   if (e != cudaSuccess) return e;
-  return p.shares > 16 * p.B ?  // pieces of a row: about the shares over the rows
-       launch_after(k_attn_join<D, kRows, 16>, rows, dim3(512), 0, s, p, rb)
-                                         : launch_after(k_attn_join<D, kRows, 4>, rows, dim3(128), 0, s, p, rb);
+  // A row's pieces are about the shares over the rows: 16 warps take them where there are many, else 4. Both kernels, rows of 8192 keys with 4 and with
+  // 16 warps: 16 heads of 128 over 4 (114 shares), 1 row 12.6 and 11.9 us, 6 rows 21.9 and 21.8, 8 rows 30.6 and 30.8, 48 rows 126 and 131;
+  // 8 heads over one (456 shares), 4 rows 13.3 and 12.6, 16 rows 19.6 and 19.4, 24 rows 23.8 and 24.3.
+  if (p.shares > 16 * p.B) return launch_after(k_attn_join<D, kRows, 16>, rows, dim3(512), 0, s, p, rb);
+  return launch_after(k_attn_join<D, kRows, 4>, rows, dim3(128), 0, s, p, rb);
 }
 
 cudaError_t launch_attn_step(const AttnStepParams& p, int D, cudaStream_t s) {

@@ -502,7 +502,10 @@ int gdn_qk_norm_rope_store(const gdn_rope_desc_t* desc, const gdn_rope_args_t* a
 /* Attention over whole sequences: o = softmax(scale q k^T) v per head, every query seeing its whole sequence or, when
  * causal, the tokens up to itself. lse is the logarithm of the softmax's denominator. bf16 operands of the tensor core (the softmax's
  * weights and their gradients are rounded to it), fp32 scores, sums and accumulators; results do not depend on the order
- * in which blocks run. */
+ * in which blocks run. The backward takes the sum over p dP of a query from dO and the rounded o, but for the queries that see a
+ * sequence's first 128 keys only: where nearly all of a later query's weight lies on one key, its small gradient has o's rounding error.
+ * Outputs of a sequence do not depend on what stands beside it. Within a causal sequence a value (for the gradients: a row of any input) that is not
+ * finite also reaches queries before it, in the same 128 tokens, as 0 times it. */
 typedef struct {
   int B, T;
   const int32_t* cu_seqlens;
