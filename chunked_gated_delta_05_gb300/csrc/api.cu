@@ -270,6 +270,10 @@ int device_check() {
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
   if (major != 10 || minor != 3) return fail(GDN_EUNSUPPORTED, "device is not compute capability 10.3 (GB300)");
+  // Makes the device's context current to this thread: encoding a tensor map (a driver call) needs it, and in a thread that has just
+  // started, as autograd's, it comes before the runtime call that would.
+  const cudaError_t e = cudaSetDevice(dev);
+  if (e != cudaSuccess) return fail(GDN_ECUDA, std::string("device context: ") + cudaGetErrorString(e));
   return GDN_OK;
 }
 
