@@ -11,7 +11,7 @@ import torch
 
 from . import _lib
 from .block_ops import _BF16, _F32, _I32, _changed, _device, _differentiated, _p, _rows_of, _run, _status, _want
-from .ops import _first_order, _offsets
+from .ops import _first_order, _kept, _offsets
 
 _rope_desc, _rope_args, _rope_bwd_args = _lib.packer(_lib.RopeDesc), _lib.packer(_lib.RopeArgs), _lib.packer(_lib.RopeBwdArgs)
 _attn_desc, _attn_fwd_args, _attn_bwd_args = _lib.packer(_lib.AttnDesc), _lib.packer(_lib.AttnFwdArgs), _lib.packer(_lib.AttnBwdArgs)
@@ -186,11 +186,6 @@ def _scale(scale):
     if not 0 < scale < math.inf:
         raise ValueError("scale must be positive and finite in fp32")
     return scale
-
-
-def _kept(cu_seqlens):
-    """Offsets that a forward has accepted, as its backward keeps them: a copy, whatever becomes of the caller's."""
-    return None if cu_seqlens is None else tuple(cu_seqlens.tolist() if isinstance(cu_seqlens, torch.Tensor) else cu_seqlens)
 
 
 def _attn_inputs(q, k, v, causal, scale, offsets):

@@ -10,7 +10,7 @@ import torch
 import torch.autograd.forward_ad as forward_ad
 
 from . import _lib
-from .ops import K_DIM, _check_tensor, _conv_checks, _conv_desc, _first_order, _gate_checks, _launch, _offsets
+from .ops import K_DIM, _check_tensor, _conv_checks, _conv_desc, _first_order, _gate_checks, _kept, _launch, _offsets
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _ACTIVATIONS = {"silu": 1, "sigmoid": 2}
@@ -448,7 +448,7 @@ class SelectiveScan(torch.autograd.Function):
                                              initial_state=initial_state, output_final_state=output_final_state,
                                              cu_seqlens=cu_seqlens, save=True)
         ctx.save_for_backward(u, delta, A, B, C, D, z, delta_bias, initial_state, saved)
-        ctx.cfg = (delta_softplus, cu_seqlens)
+        ctx.cfg = (delta_softplus, _kept(cu_seqlens))
         ctx.set_materialize_grads(False)
         return y, final
 

@@ -99,6 +99,11 @@ def _offsets(cu_seqlens, T):
     return (ctypes.c_int32 * len(vals))(*vals), len(vals) - 1
 
 
+def _kept(cu_seqlens):
+    """Offsets that a forward has accepted, as its backward keeps them: a copy, whatever becomes of the caller's."""
+    return None if cu_seqlens is None else tuple(cu_seqlens.tolist() if isinstance(cu_seqlens, torch.Tensor) else cu_seqlens)
+
+
 def _desc(B, T, H, scale, l2, sig, final, offsets, Hk=None, gate=None):
     d = _lib.Desc()
     d.B, d.T, d.H, d.K, d.V, d.chunk_size = B, T, H, K_DIM, K_DIM, CHUNK
@@ -304,7 +309,7 @@ class ChunkGatedDeltaRule(torch.autograd.Function):
         o, final, saved = _fwd(per_channel, q, k, v, g, beta, initial_state, output_final_state,
                                use_qk_l2norm, use_beta_sigmoid, cu_seqlens, scale, None, save=True, gate=gate)
         ctx.save_for_backward(q, k, v, g, beta, initial_state, A_log, dt_bias, saved)
-        ctx.cfg = (per_channel, use_qk_l2norm, use_beta_sigmoid, cu_seqlens, scale, lower_bound)
+        ctx.cfg = (per_channel, use_qk_l2norm, use_beta_sigmoid, _kept(cu_seqlens), scale, lower_bound)
         return o, final
 
     @staticmethod
@@ -416,10 +421,11 @@ class CausalConv1d(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, bias, halo, dilation, activation, cu_seqlens):
+        y = causal_conv1d_fwd(x, weight, bias, dilation=dilation, activation=activation,
+                              cu_seqlens=cu_seqlens, halo=halo)
         ctx.save_for_backward(x, weight, bias, halo)
-        ctx.cfg = (dilation, activation, cu_seqlens)
-        return causal_conv1d_fwd(x, weight, bias, dilation=dilation, activation=activation,
-                                 cu_seqlens=cu_seqlens, halo=halo)
+        ctx.cfg = (dilation, activation, _kept(cu_seqlens))
+        return y
 
     @staticmethod
     @_first_order
