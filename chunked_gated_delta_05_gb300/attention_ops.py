@@ -104,7 +104,7 @@ def qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, *, positions=None, cu_s
     ``(i, i + len(inv_freq))``, or ``(2i, 2i + 1)`` when ``interleaved``.
 
     q ``[B,T,H,D]``, k ``[B,T,Hk,D]`` bf16 (D 64 or 128; tokens may be strided slices of a wider projection), weights fp32 ``[D]`` (None,
-    None: no norm), inv_freq fp32 (None: no rotation; its rotary width must be a multiple of 16). Positions count from the start
+    None: no norm), inv_freq fp32 and finite (None: no rotation; its rotary width must be a multiple of 16). Positions count from the start
     of the sequence (or document, by ``cu_seqlens``) or are given as int32 ``[B,T]``; angles keep their precision at any
     position. Returns ``(q, k)``, contiguous."""
     offsets = _offsets(cu_seqlens, 0)       # the packed description points into it
@@ -229,7 +229,7 @@ def attention_step(q, k_cache, v_cache, page_table, lengths, *, scale=None, stat
     """One token's attention per sequence over a paged cache (see :func:`qk_norm_rope_store`): row b of q ``[B,H,D]`` (bf16, rows may
     be strided) attends to the first ``lengths[b]`` keys of its pages. A length of 0 or less gives a zero row; so does one
     beyond the table, and a page outside the cache counts as absent keys, both recorded as GDN_ERANGE in ``status``. A cache of
-    one slot a sequence is one page each. Returns ``o [B,H,D]`` bf16."""
+    one slot a sequence is one page each. Steps have no gradients. Returns ``o [B,H,D]`` bf16."""
     dev = _device("q", q)
     if q.dim() != 3 or q.numel() == 0:
         raise ValueError("q must be [B,H,D]")

@@ -466,7 +466,7 @@ typedef struct {
   const void *q, *k;         /* bf16 [B,T,H,D], [B,T,Hk,D] */
   const void* v;             /* store: bf16 [B,T,Hk,D] */
   const float *q_weight, *k_weight; /* fp32 [D], both or neither */
-  const float* inv_freq;     /* fp32 [rotary_dim/2], or NULL when rotary_dim is 0 */
+  const float* inv_freq;     /* fp32 [rotary_dim/2], finite, or NULL when rotary_dim is 0 */
   const int32_t* positions;  /* device [B,T], or NULL; NULL with a store */
   void *q_out, *k_out;       /* bf16 [B,T,H,D], [B,T,Hk,D] contiguous, written */
   void *k_cache, *v_cache;   /* store: bf16 [num_pages,page_size,Hk,D], written in the new tokens' rows */
