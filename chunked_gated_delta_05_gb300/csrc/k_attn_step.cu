@@ -15,7 +15,7 @@
 // heads' blocks of a share run side by side, so that a token's row of the cache is read at one time. A block's four warps take 16
 // keys of a unit each. Where a row's units lie in several shares, the blocks leave a weighted sum, its reference and the sum of
 // weights, which a second kernel joins. The reference moves only for a score whose weight would exceed 2^8, so no maximum is taken otherwise.
-// Weights are rounded to bf16 for the product (the values' type), sums are fp32.
+// Weights are rounded to bf16 for the product (the values' type), sums are fp32. (Heads of 64, up to 8 of a key head: 12 bytes a thread are spilled.)
 #include "attn.cuh"
 
 namespace gdn {

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kWarps * 32, kFwdBlocks) k_rope_fwd(const __gr
 
 // The first `q_blocks` blocks take the queries' heads, the others the keys': a token of one kind to a warp, the next group of heads
 // requested before one is computed. (2 x 4096 tokens of 16 + 16 heads, forward and backward: 75 us with a warp for both kinds of
-// a token, 73 without requests ahead, 69 so.)
+// a token, 73 without requests ahead, 69 so; 128 registers a thread, of which the compiler spills 8 to 24 bytes.)
 template <int D, bool kPairs>
 __global__ void __launch_bounds__(kWarps * 32, kBwdPerSm) k_rope_bwd(const __grid_constant__ RopeParams p, int q_blocks) {
   constexpr int kHeads = 256 / D, kTogether = 4;
